@@ -263,6 +263,105 @@ dl_status dl_slot_release(dl_state *s, int slot, void *stream);
  * a released slot), -1 for a bad handle or slot. */
 int dl_slot_log_len(const dl_state *s, int slot);
 
+/* ------------------------------------------------------------------------
+ * Sequence operators: what stands before, behind and beside the decode step.
+ * dl_scan runs the same recurrence over whole sequences (a prompt's prefill,
+ * which leaves the state that decoding starts from, or a training step);
+ * dl_gated_norm and dl_residual_norm are the norms behind and before a
+ * recurrent block.  Each has a backward pass.  None allocates device memory;
+ * all are asynchronous on `stream` and capturable into HIP graphs; errors are
+ * reported as above, before any HIP call.  The calling thread's current
+ * device must be the one that holds the buffers and the stream.  Workspace
+ * contents need no initialisation and mean nothing between calls; calls that
+ * may overlap in time need workspaces of their own.
+ * ------------------------------------------------------------------------ */
+
+/* The sequences of one scan: `tokens` rows of all sequences, packed one after
+ * the other.  cu_seqlens (device, [seqs + 1] int32, non-decreasing, first 0,
+ * last <= tokens): sequence n is the rows cu_seqlens[n] .. cu_seqlens[n+1]-1,
+ * possibly none; rows behind the last sequence belong to none, and no output
+ * is written for them.  NULL: `seqs` sequences of tokens / seqs rows each.
+ * (Offsets out of order give meaningless results, but no access out of
+ * range.)  q (r for RWKV6), k [tokens,H,d_k] and v [tokens,H,d_v] in in_dtype
+ * may have rows further apart than H*d elements, e.g. as slices of one
+ * projection: q_stride, k_stride, v_stride are the elements from one token to
+ * the next (0: H*d).  beta [tokens,H], log_decay [tokens,H] (GDN) or
+ * [tokens,H,d_k], u [H,d_k] as for dl_decode_step. */
+typedef struct {
+    dl_op op;
+    dl_dtype in_dtype;
+    int tokens, seqs, H, d_k, d_v;
+    long long q_stride, k_stride, v_stride;
+    const int *cu_seqlens;
+    const void *q, *k, *v;
+    const float *beta, *log_decay, *u;
+} dl_scan_desc;
+
+/* Device bytes of dl_scan's workspace, of the `saved` buffer that carries the
+ * forward pass's intermediate results to the backward pass, and of
+ * dl_scan_backward's workspace (each 256-byte aligned).  Only the sizes, op
+ * and in_dtype of `d` are read.  0 if they are invalid. */
+size_t dl_scan_workspace_bytes(const dl_scan_desc *d);
+size_t dl_scan_saved_bytes(const dl_scan_desc *d);
+size_t dl_scan_backward_workspace_bytes(const dl_scan_desc *d);
+
+/* Forward: o [tokens,H,d_v] in in_dtype (the decode step's o is fp32; here it
+ * is as large as v, and is rounded once), and each sequence's end state.
+ * `initial` (NULL: zero) and `final_state` (NULL: not wanted) are fp32 state
+ * tensors [rows,H,d_k,d_v], 16-byte aligned; final_state may be `initial`
+ * itself, else they must not overlap.  With state_rows NULL sequence n has
+ * row n; else (device, [seqs] int32) row state_rows[n] of n_state_rows, no
+ * row twice; a row out of range is not read (zero) nor written.  `saved`
+ * (NULL: no backward pass will follow) keeps what dl_scan_backward needs. */
+dl_status dl_scan(const dl_scan_desc *d, const float *initial, float *final_state, const int *state_rows,
+                  int n_state_rows, void *o, void *saved, void *workspace, void *stream);
+
+/* Backward of dl_scan over the same `d` and the `saved` of that call (with
+ * state_rows NULL): from d_o [tokens,H,d_v] (in_dtype; NULL: zero) and d_final
+ * [seqs,H,d_k,d_v] fp32 (NULL: zero) the gradients dq, dk [tokens,H,d_k], dv
+ * [tokens,H,d_v] (in_dtype, contiguous), dbeta [tokens,H] fp32 (NULL for
+ * RWKV6), dlog_decay (fp32, shaped as log_decay; 0 where log_decay < -112,
+ * which acts as -112), du [H,d_k] fp32 (RWKV6, else NULL) and, unless NULL,
+ * d_initial [seqs,H,d_k,d_v] fp32. */
+dl_status dl_scan_backward(const dl_scan_desc *d, const void *saved, const void *d_o, const float *d_final,
+                           void *dq, void *dk, void *dv, float *dbeta, float *dlog_decay, float *du,
+                           float *d_initial, void *workspace, void *stream);
+
+/* y = rms(o) w silu(gate) per head, rms(a) = a / sqrt(mean(a^2) + eps): the
+ * norm behind the recurrence with its output gate.  o [rows,H,d] in o_dtype
+ * (fp32 from dl_decode_step, in_dtype from dl_scan), gate and y [rows,H,d] in
+ * dtype, gate rows gate_stride elements apart (0: H*d); weight [d] fp32 or
+ * NULL (1).  d in {16, 32, 64, 128}.  y may be o or gate itself where type
+ * and layout agree. */
+dl_status dl_gated_norm(int rows, int H, int d, dl_dtype o_dtype, dl_dtype dtype, const void *o,
+                        const void *gate, long long gate_stride, const float *weight, float eps, void *y,
+                        void *stream);
+/* Its gradients: d_o (o_dtype), d_gate (dtype, contiguous), d_weight [d] fp32
+ * (NULL: not wanted; else workspace of dl_gated_norm_workspace_bytes). */
+size_t dl_gated_norm_workspace_bytes(int rows, int H, int d);
+dl_status dl_gated_norm_backward(int rows, int H, int d, dl_dtype o_dtype, dl_dtype dtype, const void *o,
+                                 const void *gate, long long gate_stride, const float *weight, float eps,
+                                 const void *dy, void *d_o, void *d_gate, float *d_weight, void *workspace,
+                                 void *stream);
+
+/* x_out = x + scale y;  h = rms(x_out) weight: the residual add behind one
+ * block, with its per-channel scale, and the norm before the next.  x, x_out
+ * [rows,D] fp32 (x_out may be x), y, h [rows,D] in dtype; scale, weight [D]
+ * fp32 or NULL (1).  y NULL: h = rms(x) weight alone (x_out, scale NULL).
+ * 1 <= D <= 16384. */
+dl_status dl_residual_norm(int rows, int D, dl_dtype dtype, const float *x, const void *y, const float *scale,
+                           const float *weight, float eps, float *x_out, void *h, void *stream);
+/* Its gradients from d_x_out (fp32; NULL: zero) and d_h (dtype; NULL: zero):
+ * d_x [rows,D] fp32, d_y [rows,D] (NULL if the forward had no y), d_scale and
+ * d_weight [D] fp32 (NULL: not wanted; else the workspace is needed; d_scale
+ * needs y, scale and d_y).  y is read only where scale is given.  d_x may be
+ * d_x_out itself. */
+size_t dl_residual_norm_workspace_bytes(int rows, int D);
+dl_status dl_residual_norm_backward(int rows, int D, dl_dtype dtype, const float *x_out, const void *y,
+                                    const float *scale, const float *weight, float eps,
+                                    const float *d_x_out, const void *d_h, float *d_x, void *d_y,
+                                    float *d_scale, float *d_weight, void *workspace, void *stream);
+
 /* Static description of a status code (never NULL; owned by the library). */
 const char *dl_status_string(dl_status st);
 

@@ -31,7 +31,11 @@ EXPORTS = ("dl_workspace_bytes", "dl_state_create", "dl_decode_step", "dl_replay
            "dl_append_decode", "dl_merge", "dl_state_reset", "dl_log_len", "dl_set_log_len",
            "dl_state_destroy", "dl_eager_step", "dl_status_string", "dl_suggest_merge_interval",
            "dl_state_enable_slots", "dl_slot_admit", "dl_slot_merge", "dl_slot_log_len",
-           "dl_slot_release", "dl_decode_step_staged_noalloc", "dl_choose_merge_interval")
+           "dl_slot_release", "dl_decode_step_staged_noalloc", "dl_choose_merge_interval",
+           "dl_scan_workspace_bytes", "dl_scan_saved_bytes", "dl_scan_backward_workspace_bytes",
+           "dl_scan", "dl_scan_backward", "dl_gated_norm_workspace_bytes", "dl_gated_norm",
+           "dl_gated_norm_backward", "dl_residual_norm_workspace_bytes", "dl_residual_norm",
+           "dl_residual_norm_backward")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built; run `python recurrent_state_update_amd/_build.py` "
@@ -39,7 +43,17 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 _i, _p, _sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
+_l, _fl = ctypes.c_longlong, ctypes.c_float
 
+
+class dl_scan_desc(ctypes.Structure):
+    """The sequences of one scan (include/deltalog.h); device addresses as ints."""
+    _fields_ = [("op", _i), ("in_dtype", _i), ("tokens", _i), ("seqs", _i), ("H", _i), ("d_k", _i),
+                ("d_v", _i), ("q_stride", _l), ("k_stride", _l), ("v_stride", _l), ("cu_seqlens", _p),
+                ("q", _p), ("k", _p), ("v", _p), ("beta", _p), ("log_decay", _p), ("u", _p)]
+
+
+_desc = ctypes.POINTER(dl_scan_desc)
 
 _SIG = {
     "dl_workspace_bytes": ([_i] * 7, _sz),
@@ -62,6 +76,17 @@ _SIG = {
     "dl_slot_release": ([_p, _i, _p], _i),
     "dl_decode_step_staged_noalloc": ([_p] * 8, _i),
     "dl_choose_merge_interval": ([ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double), _i], _i),
+    "dl_scan_workspace_bytes": ([_desc], _sz),
+    "dl_scan_saved_bytes": ([_desc], _sz),
+    "dl_scan_backward_workspace_bytes": ([_desc], _sz),
+    "dl_scan": ([_desc, _p, _p, _p, _i, _p, _p, _p, _p], _i),
+    "dl_scan_backward": ([_desc] + [_p] * 12, _i),
+    "dl_gated_norm_workspace_bytes": ([_i] * 3, _sz),
+    "dl_gated_norm": ([_i] * 5 + [_p, _p, _l, _p, _fl, _p, _p], _i),
+    "dl_gated_norm_backward": ([_i] * 5 + [_p, _p, _l, _p, _fl] + [_p] * 6, _i),
+    "dl_residual_norm_workspace_bytes": ([_i] * 2, _sz),
+    "dl_residual_norm": ([_i] * 3 + [_p] * 4 + [_fl] + [_p] * 3, _i),
+    "dl_residual_norm_backward": ([_i] * 3 + [_p] * 4 + [_fl] + [_p] * 8, _i),
 }
 for _name, (_args, _res) in _SIG.items():
     _f = getattr(_lib, _name)
@@ -193,6 +218,62 @@ def dl_slot_release(s, slot, stream=None):
     return _lib.dl_slot_release(s, slot, _stream(stream))
 
 
+def dl_scan_workspace_bytes(desc) -> int:
+    return int(_lib.dl_scan_workspace_bytes(ctypes.byref(desc)))
+
+
+def dl_scan_saved_bytes(desc) -> int:
+    return int(_lib.dl_scan_saved_bytes(ctypes.byref(desc)))
+
+
+def dl_scan_backward_workspace_bytes(desc) -> int:
+    return int(_lib.dl_scan_backward_workspace_bytes(ctypes.byref(desc)))
+
+
+def dl_scan(desc, initial, final_state, state_rows, n_state_rows, o, saved, workspace, stream=None):
+    return _lib.dl_scan(ctypes.byref(desc), _ptr(initial), _ptr(final_state), _ptr(state_rows), n_state_rows,
+                        _ptr(o), _ptr(saved), _ptr(workspace), _stream(stream))
+
+
+def dl_scan_backward(desc, saved, d_o, d_final, dq, dk, dv, dbeta, dlog_decay, du, d_initial, workspace,
+                     stream=None):
+    return _lib.dl_scan_backward(ctypes.byref(desc), _ptr(saved), _ptr(d_o), _ptr(d_final), _ptr(dq), _ptr(dk),
+                                 _ptr(dv), _ptr(dbeta), _ptr(dlog_decay), _ptr(du), _ptr(d_initial),
+                                 _ptr(workspace), _stream(stream))
+
+
+def dl_gated_norm_workspace_bytes(rows, H, d) -> int:
+    return int(_lib.dl_gated_norm_workspace_bytes(rows, H, d))
+
+
+def dl_gated_norm(rows, H, d, o_dtype, dtype, o, gate, gate_stride, weight, eps, y, stream=None):
+    return _lib.dl_gated_norm(rows, H, d, o_dtype, dtype, _ptr(o), _ptr(gate), gate_stride, _ptr(weight), eps,
+                              _ptr(y), _stream(stream))
+
+
+def dl_gated_norm_backward(rows, H, d, o_dtype, dtype, o, gate, gate_stride, weight, eps, dy, d_o, d_gate,
+                           d_weight, workspace, stream=None):
+    return _lib.dl_gated_norm_backward(rows, H, d, o_dtype, dtype, _ptr(o), _ptr(gate), gate_stride,
+                                       _ptr(weight), eps, _ptr(dy), _ptr(d_o), _ptr(d_gate), _ptr(d_weight),
+                                       _ptr(workspace), _stream(stream))
+
+
+def dl_residual_norm_workspace_bytes(rows, D) -> int:
+    return int(_lib.dl_residual_norm_workspace_bytes(rows, D))
+
+
+def dl_residual_norm(rows, D, dtype, x, y, scale, weight, eps, x_out, h, stream=None):
+    return _lib.dl_residual_norm(rows, D, dtype, _ptr(x), _ptr(y), _ptr(scale), _ptr(weight), eps, _ptr(x_out),
+                                 _ptr(h), _stream(stream))
+
+
+def dl_residual_norm_backward(rows, D, dtype, x_out, y, scale, weight, eps, d_x_out, d_h, d_x, d_y, d_scale,
+                              d_weight, workspace, stream=None):
+    return _lib.dl_residual_norm_backward(rows, D, dtype, _ptr(x_out), _ptr(y), _ptr(scale), _ptr(weight), eps,
+                                          _ptr(d_x_out), _ptr(d_h), _ptr(d_x), _ptr(d_y), _ptr(d_scale),
+                                          _ptr(d_weight), _ptr(workspace), _stream(stream))
+
+
 def dl_status_string(st) -> str:
     return _lib.dl_status_string(st).decode()
 
@@ -303,6 +384,20 @@ class DeltaLogState:
     def log_len(self) -> int:
         return dl_log_len(self._h)
 
+    def prefill(self, q, k, v, beta, log_decay, cu_seqlens=None, slots=None, stream=None):
+        """Run whole prompts through the recurrence, from the states that
+        ``base`` holds, and leave their end states there: what `step` then
+        continues from.  q, k [T,H,d_k], v [T,H,d_v], beta [T,H], log_decay
+        [T,H(,d_k)] hold the prompts one after the other, cu_seqlens (GPU,
+        int32) the offsets where they start and the last ends (or [n,T,H,..]
+        tensors hold n of equal length; see `scan`).  ``slots``: the slot of
+        each prompt, a sequence of distinct ints (default: prompt n is slot n
+        of all B).  The logs of these slots must be empty (a fresh state or
+        slot, or after a merge).  A new prompt starts from zero: zero
+        ``base[slot]`` first.  Returns o in the input dtype, shaped as v."""
+        from .sequence import _prefill
+        return _prefill(self, q, k, v, beta, log_decay, cu_seqlens, slots, stream)
+
     # per-slot logs (continuous batching)
     def enable_slots(self, stream=None):
         _check(dl_state_enable_slots(self._h, stream), "dl_state_enable_slots")
@@ -362,3 +457,6 @@ def eager_step(op: str, S, q, k, v, beta, log_decay, u=None, o=None, stream=None
     _check(dl_eager_step(opi, B, H, dk, dv, dti, S, q, k, v, beta, log_decay, u, o,
                          stream), "dl_eager_step")
     return o
+
+
+from .sequence import gated_norm, residual_norm, scan  # noqa: E402,F401

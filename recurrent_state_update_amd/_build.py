@@ -25,7 +25,8 @@ LIB = os.path.join(PKG, "libdeltalog.so")
 # the benchmark's pattern-ceiling helper, a library of its own (not part of
 # the decode path)
 CEILING_LIB = os.path.join(PKG, "libdlceiling.so")
-SOURCES = ["dl_api.hip", "dl_device.hip", "dl_gdn.hip", "dl_kda.hip", "dl_rwkv6.hip"]
+SOURCES = ["dl_api.hip", "dl_device.hip", "dl_gdn.hip", "dl_kda.hip", "dl_rwkv6.hip",
+           "dl_sequence_api.hip", "dl_scan_gdn.hip", "dl_scan_kda.hip", "dl_scan_rwkv6.hip", "dl_norm.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -43,7 +44,7 @@ def _compile(src: str, obj: str, defines: list[str]) -> None:
 
 
 def build(defines: list[str] | None = None, out: str = LIB, build_dir: str | None = None,
-          jobs: int = 4) -> str:
+          jobs: int = 8) -> str:
     """Compile every source (in parallel) and link the shared library."""
     defines = defines or []
     build_dir = build_dir or os.path.join(ROOT, "_build")

@@ -80,4 +80,80 @@ hipError_t launch_step_gdn(int dtype, int dk, int dv, int mode, const StepArgs &
 hipError_t launch_step_kda(int dtype, int dk, int dv, int mode, const StepArgs &a, hipStream_t st);
 hipError_t launch_step_rwkv6(int dtype, int dk, int dv, int mode, const StepArgs &a, hipStream_t st);
 
+// ---- sequence operators (dl_sequence_api.hip; kernels in dl_scan.h, dl_norm.hip)
+
+constexpr int kScanChunk = 64; // tokens per chunk of the scan
+
+// Chunk slots of a scan: every sequence has enough of them (dl_scan.h).
+constexpr long scan_slots(long tokens, long seqs) { return tokens / kScanChunk + seqs; }
+// Keys as the kernels take them (d_k = 16 runs as 32, the rest zero).
+constexpr int scan_keys(int dk) { return dk < 32 ? 32 : dk; }
+// Bytes of one chunk and head's operands: three bf16 planes of three
+// chunk x keys and three chunk x chunk matrices, and a decay per key.
+constexpr size_t scan_op_bytes(int keys)
+{
+    return size_t(2) * 3 * (3 * kScanChunk * keys + 3 * kScanChunk * kScanChunk) + 4 * keys;
+}
+
+// One scan, forward or backward.  Token strides in elements.
+struct ScanArgs {
+    int T, N, H, dk, dv; // tokens in all, sequences, heads
+    int slots;           // scan_slots(T, N)
+    const int *cu;       // [N + 1] token offsets, or NULL: N equal lengths
+    const void *q, *k, *v;
+    long qs, ks, vs;
+    const float *beta, *ld, *u;
+    const float *init; // state rows, or NULL (zero)
+    float *fin;        // state rows, or NULL
+    const int *rows;   // [N] state row of each sequence, or NULL: row n
+    int nrows;         // state rows there are
+    void *o;
+    char *ops;     // [slots][H] operands
+    float *save_s; // [slots][H][dk][dv] start state of every chunk, or NULL
+    float *save_e; // [slots][H][chunk][dv] E (delta rule)
+    // backward
+    const void *d_o;   // [T][H][dv], or NULL (zero)
+    const float *dfin; // [N][H][dk][dv], or NULL (zero)
+    void *d_q, *d_k, *d_v;
+    float *d_beta, *d_ld, *d_u, *dinit;
+    float *w_ds; // [slots][H][dk][dv] gradient of every chunk's end state
+    float *w_z;  // [slots][H][chunk][dv] (delta rule)
+    float *w_db; // [slots][H][dv / 16][chunk] partial sums of dbeta
+    float *w_du; // [slots][H][dk] partial sums of du
+};
+hipError_t launch_scan_gdn(int dtype, bool backward, const ScanArgs &a, hipStream_t st);
+hipError_t launch_scan_kda(int dtype, bool backward, const ScanArgs &a, hipStream_t st);
+hipError_t launch_scan_rwkv6(int dtype, bool backward, const ScanArgs &a, hipStream_t st);
+
+struct GatedNormArgs {
+    long units; // rows x H
+    int H, d;
+    const void *o, *gate, *dy;
+    long gate_stride; // elements between rows
+    const float *weight;
+    float eps;
+    void *y, *d_o, *d_gate;
+    float *d_weight, *partial; // [blocks][d]
+    int blocks;
+};
+hipError_t launch_gated_norm(int o_dtype, int dtype, bool backward, const GatedNormArgs &a, hipStream_t st);
+
+struct ResidualNormArgs {
+    long rows;
+    int D;
+    const float *x; // forward: the stream; backward: its new value
+    const void *y;
+    const float *scale, *weight;
+    float eps;
+    float *x_out;
+    void *h;
+    const float *d_x_out;
+    const void *d_h;
+    float *d_x;
+    void *d_y;
+    float *d_scale, *d_weight, *partial; // [blocks][D] each
+    int blocks;
+};
+hipError_t launch_residual_norm(int dtype, bool backward, const ResidualNormArgs &a, hipStream_t st);
+
 } // namespace dl

@@ -1,0 +1,434 @@
+// dl_norm.hip -- the norms around a recurrent block, forward and backward:
+//   gated norm     y = rms(o) w silu(g) per head (behind the recurrence)
+//   residual norm  x' = x + s y,  h = rms(x') w  (before the next block)
+// with rms(a) = a / sqrt(mean(a^2) + eps).  Both are a few operations per
+// byte and bound by HBM: one pass over the data, each row held in registers
+// between its sum and its use, sums in fp32.  The gradients of the per-column
+// weights are summed over rows in registers, per workgroup, then over the
+// workgroups in their order: the result does not depend on timing.
+#include <hip/hip_runtime.h>
+
+#include "dl_internal.h"
+
+namespace dl {
+
+namespace {
+
+template <typename T> __device__ __forceinline__ float to_f(T x) { return static_cast<float>(x); }
+
+// N consecutive elements from p, as floats (and back).  ALIGNED: p is aligned
+// to 16 bytes, or to the N elements where they are fewer.
+template <int N, bool ALIGNED, typename T> __device__ __forceinline__ void load(float (&x)[N], const T *p)
+{
+    using V = T __attribute__((ext_vector_type(N)));
+    if constexpr (ALIGNED && N > 1) {
+        const V v = *reinterpret_cast<const V *>(p);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            x[i] = to_f(v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            x[i] = to_f(p[i]);
+    }
+}
+template <int N, bool ALIGNED, typename T> __device__ __forceinline__ void store(T *p, const float (&x)[N])
+{
+    using V = T __attribute__((ext_vector_type(N)));
+    if constexpr (ALIGNED && N > 1) {
+        V v;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = static_cast<T>(x[i]);
+        *reinterpret_cast<V *>(p) = v;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            p[i] = static_cast<T>(x[i]);
+    }
+}
+
+template <int CTRL> __device__ __forceinline__ float add_dpp(float x)
+{
+    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, false));
+}
+// Sum over groups of G consecutive lanes (2 <= G <= 64), in every lane of the
+// group: swaps within four lanes, mirrors of 8 and of 16, then across rows.
+template <int G> __device__ __forceinline__ float group_sum(float x)
+{
+    x = add_dpp<0xB1>(x);                        // quad_perm 1 0 3 2
+    if constexpr (G >= 4) x = add_dpp<0x4E>(x);  // quad_perm 2 3 0 1
+    if constexpr (G >= 8) x = add_dpp<0x141>(x); // row_half_mirror
+    if constexpr (G >= 16) x = add_dpp<0x140>(x); // row_mirror
+    if constexpr (G >= 32) x += __shfl_xor(x, 16);
+    if constexpr (G >= 64) x += __shfl_xor(x, 32);
+    return x;
+}
+
+// --------------------------------------------------------------- gated norm --
+
+// A unit is one head of one row; G = d / 8 lanes hold it, eight columns each.
+template <typename TO, typename T, int D, bool ALIGNED>
+__global__ __launch_bounds__(256) void gated_norm_kernel(GatedNormArgs a)
+{
+    constexpr int G = D / 8;
+    const long u = (static_cast<long>(blockIdx.x) * 256 + threadIdx.x) / G;
+    const int c = threadIdx.x % G * 8;
+    if (u >= a.units) // whole groups
+        return;
+    float o[8], g[8], w[8];
+    load<8, ALIGNED>(o, static_cast<const TO *>(a.o) + u * D + c);
+    load<8, ALIGNED>(g, static_cast<const T *>(a.gate) + u / a.H * a.gate_stride + u % a.H * D + c);
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        w[i] = a.weight ? a.weight[c + i] : 1.f;
+        ss = fmaf(o[i], o[i], ss);
+    }
+    const float r = 1.f / sqrtf(group_sum<G>(ss) / D + a.eps);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        o[i] = o[i] * r * w[i] * (g[i] / (1.f + expf(-g[i])));
+    store<8, ALIGNED>(static_cast<T *>(a.y) + u * D + c, o);
+}
+
+// With n = rms(o), sig = sigmoid(g): dn = dy w g sig,
+// do = r (dn - n mean(dn n)), dgate = dy n w sig (1 + g (1 - sig)),
+// dw = sum dy n g sig.
+template <typename TO, typename T, int D, bool ALIGNED>
+__global__ __launch_bounds__(256) void gated_norm_bwd_kernel(GatedNormArgs a)
+{
+    constexpr int G = D / 8;
+    __shared__ float part[256 * 8];
+    const int c = threadIdx.x % G * 8;
+    float w[8], dw[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        w[i] = a.weight ? a.weight[c + i] : 1.f;
+        dw[i] = 0.f;
+    }
+    for (long u = (static_cast<long>(blockIdx.x) * 256 + threadIdx.x) / G; u < a.units;
+         u += static_cast<long>(a.blocks) * (256 / G)) {
+        float o[8], g[8], dy[8], dn[8];
+        load<8, ALIGNED>(o, static_cast<const TO *>(a.o) + u * D + c);
+        load<8, ALIGNED>(g, static_cast<const T *>(a.gate) + u / a.H * a.gate_stride + u % a.H * D + c);
+        load<8, ALIGNED>(dy, static_cast<const T *>(a.dy) + u * D + c);
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            ss = fmaf(o[i], o[i], ss);
+        const float r = 1.f / sqrtf(group_sum<G>(ss) / D + a.eps);
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float n = o[i] * r, sig = 1.f / (1.f + expf(-g[i]));
+            const float t = dy[i] * sig;
+            o[i] = n;
+            dn[i] = t * g[i];
+            dw[i] = fmaf(dn[i], n, dw[i]);
+            dn[i] *= w[i];
+            dot = fmaf(dn[i], n, dot);
+            g[i] = t * n * w[i] * (1.f + g[i] * (1.f - sig));
+        }
+        dot = group_sum<G>(dot) / D;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            o[i] = r * (dn[i] - o[i] * dot);
+        store<8, ALIGNED>(static_cast<TO *>(a.d_o) + u * D + c, o);
+        store<8, ALIGNED>(static_cast<T *>(a.d_gate) + u * D + c, g);
+    }
+    if (!a.d_weight)
+        return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        part[threadIdx.x * 8 + i] = dw[i];
+    __syncthreads();
+    for (int j = threadIdx.x; j < D; j += 256) {
+        float x = 0.f;
+        for (int t = 0; t < 256 / G; ++t)
+            x += part[t * D + j];
+        a.partial[static_cast<long>(blockIdx.x) * D + j] = x;
+    }
+}
+
+// out[j] = the sum over the blocks' rows of partial [blocks][n].  A workgroup
+// takes 32 columns; eight threads per column take every eighth row.
+__global__ __launch_bounds__(256) void column_sum_kernel(const float *partial, int blocks, int n, float *out)
+{
+    __shared__ float part[8][33];
+    const int c = threadIdx.x % 32, s = threadIdx.x / 32, j = blockIdx.x * 32 + c;
+    float x = 0.f;
+    if (j < n)
+        for (int b = s; b < blocks; b += 8)
+            x += partial[static_cast<long>(b) * n + j];
+    part[s][c] = x;
+    __syncthreads();
+    if (s == 0 && j < n) {
+        for (int t = 1; t < 8; ++t)
+            x += part[t][c];
+        out[j] = x;
+    }
+}
+
+hipError_t column_sum(const float *partial, int blocks, int n, float *out, hipStream_t st)
+{
+    hipLaunchKernelGGL(column_sum_kernel, dim3((n + 31) / 32), dim3(256), 0, st, partial, blocks, n, out);
+    return hipGetLastError();
+}
+
+template <typename TO, typename T, int D>
+hipError_t gated_norm_t(bool aligned, bool backward, const GatedNormArgs &a, hipStream_t st)
+{
+    if (!backward) {
+        const long blocks = (a.units * (D / 8) + 255) / 256;
+        if (blocks == 0)
+            return hipSuccess;
+        if (aligned)
+            hipLaunchKernelGGL((gated_norm_kernel<TO, T, D, true>), dim3(blocks), dim3(256), 0, st, a);
+        else
+            hipLaunchKernelGGL((gated_norm_kernel<TO, T, D, false>), dim3(blocks), dim3(256), 0, st, a);
+        return hipGetLastError();
+    }
+    if (aligned)
+        hipLaunchKernelGGL((gated_norm_bwd_kernel<TO, T, D, true>), dim3(a.blocks), dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((gated_norm_bwd_kernel<TO, T, D, false>), dim3(a.blocks), dim3(256), 0, st, a);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess || !a.d_weight)
+        return e;
+    return column_sum(a.partial, a.blocks, D, a.d_weight, st);
+}
+
+template <typename TO, typename T>
+hipError_t gated_norm_d(bool aligned, bool backward, const GatedNormArgs &a, hipStream_t st)
+{
+    switch (a.d) {
+    case 16: return gated_norm_t<TO, T, 16>(aligned, backward, a, st);
+    case 32: return gated_norm_t<TO, T, 32>(aligned, backward, a, st);
+    case 64: return gated_norm_t<TO, T, 64>(aligned, backward, a, st);
+    default: return gated_norm_t<TO, T, 128>(aligned, backward, a, st);
+    }
+}
+
+bool at16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// ------------------------------------------------------------ residual norm --
+
+// NT threads per row, E x 8 columns each: VEC = 8 consecutive ones at a time
+// where every row starts on a 16-byte boundary, else single ones.
+template <int NT, int VEC, int E> struct Cols {
+    static constexpr int K = E * 8 / VEC;
+    static __device__ __forceinline__ int col(int k) { return (k * NT + static_cast<int>(threadIdx.x)) * VEC; }
+};
+
+template <int NT> __device__ __forceinline__ float row_sum(float x, float *part)
+{
+    x = group_sum<64>(x);
+    if constexpr (NT > 64) {
+        __syncthreads(); // part's last use
+        if (threadIdx.x % 64 == 0)
+            part[threadIdx.x / 64] = x;
+        __syncthreads();
+        x = 0.f;
+#pragma unroll
+        for (int w = 0; w < NT / 64; ++w)
+            x += part[w];
+    }
+    return x;
+}
+
+template <typename T, int NT, int VEC, int E>
+__global__ __launch_bounds__(NT) void residual_norm_kernel(ResidualNormArgs a)
+{
+    using L = Cols<NT, VEC, E>;
+    __shared__ float part[NT / 64];
+    const long at = static_cast<long>(blockIdx.x) * a.D;
+    float x[L::K][VEC], ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < L::K; ++k) {
+        const int c = L::col(k);
+        if (c < a.D)
+            load<VEC, true>(x[k], a.x + at + c);
+    }
+    if (a.y) {
+#pragma unroll
+        for (int k = 0; k < L::K; ++k) {
+            const int c = L::col(k);
+            if (c >= a.D)
+                continue;
+            float y[VEC];
+            load<VEC, true>(y, static_cast<const T *>(a.y) + at + c);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                x[k][i] += a.scale ? y[i] * a.scale[c + i] : y[i];
+            store<VEC, true>(a.x_out + at + c, x[k]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < L::K; ++k)
+        if (L::col(k) < a.D)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                ss = fmaf(x[k][i], x[k][i], ss);
+    const float r = 1.f / sqrtf(row_sum<NT>(ss, part) / a.D + a.eps);
+#pragma unroll
+    for (int k = 0; k < L::K; ++k) {
+        const int c = L::col(k);
+        if (c >= a.D)
+            continue;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            x[k][i] *= a.weight ? r * a.weight[c + i] : r;
+        store<VEC, true>(static_cast<T *>(a.h) + at + c, x[k]);
+    }
+}
+
+// With n = x' r: dn = dh w, d = dx' + r (dn - n mean(dn n)), dx = d,
+// dy = d s, ds = sum d y, dw = sum dh n.  A workgroup takes every
+// gridDim.x-th row and keeps its sums of ds and dw in registers.
+template <typename T, int NT, int VEC, int E>
+__global__ __launch_bounds__(NT) void residual_norm_bwd_kernel(ResidualNormArgs a)
+{
+    using L = Cols<NT, VEC, E>;
+    __shared__ float part[NT / 64];
+    float ds[L::K][VEC], dw[L::K][VEC];
+#pragma unroll
+    for (int k = 0; k < L::K; ++k)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            ds[k][i] = dw[k][i] = 0.f;
+    for (long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const long at = row * a.D;
+        float x[L::K][VEC], dn[L::K][VEC], ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int k = 0; k < L::K; ++k) {
+            const int c = L::col(k);
+            if (c >= a.D)
+                continue;
+            load<VEC, true>(x[k], a.x + at + c);
+            if (a.d_h) {
+                load<VEC, true>(dn[k], static_cast<const T *>(a.d_h) + at + c);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    dn[k][i] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                ss = fmaf(x[k][i], x[k][i], ss);
+        }
+        const float r = 1.f / sqrtf(row_sum<NT>(ss, part) / a.D + a.eps);
+#pragma unroll
+        for (int k = 0; k < L::K; ++k) {
+            const int c = L::col(k);
+            if (c >= a.D)
+                continue;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                x[k][i] *= r;
+                dw[k][i] = fmaf(dn[k][i], x[k][i], dw[k][i]);
+                if (a.weight)
+                    dn[k][i] *= a.weight[c + i];
+                dot = fmaf(dn[k][i], x[k][i], dot);
+            }
+        }
+        dot = row_sum<NT>(dot, part) / a.D;
+#pragma unroll
+        for (int k = 0; k < L::K; ++k) {
+            const int c = L::col(k);
+            if (c >= a.D)
+                continue;
+            float d[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                d[i] = 0.f;
+            if (a.d_x_out)
+                load<VEC, true>(d, a.d_x_out + at + c);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                d[i] += r * (dn[k][i] - x[k][i] * dot);
+            store<VEC, true>(a.d_x + at + c, d);
+            if (a.d_y) {
+                if (a.scale) {
+                    float y[VEC];
+                    load<VEC, true>(y, static_cast<const T *>(a.y) + at + c);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        ds[k][i] = fmaf(d[i], y[i], ds[k][i]);
+                        d[i] *= a.scale[c + i];
+                    }
+                }
+                store<VEC, true>(static_cast<T *>(a.d_y) + at + c, d);
+            }
+        }
+    }
+    const long at = static_cast<long>(blockIdx.x) * a.D;
+    float *pw = a.partial + (a.d_scale ? static_cast<long>(a.blocks) * a.D : 0);
+#pragma unroll
+    for (int k = 0; k < L::K; ++k) {
+        const int c = L::col(k);
+        if (c >= a.D)
+            continue;
+        if (a.d_scale)
+            store<VEC, true>(a.partial + at + c, ds[k]);
+        if (a.d_weight)
+            store<VEC, true>(pw + at + c, dw[k]);
+    }
+}
+
+template <typename T, int NT, int VEC, int E>
+hipError_t residual_norm_t(bool backward, const ResidualNormArgs &a, hipStream_t st)
+{
+    if (!backward) {
+        if (a.rows == 0)
+            return hipSuccess;
+        hipLaunchKernelGGL((residual_norm_kernel<T, NT, VEC, E>), dim3(a.rows), dim3(NT), 0, st, a);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL((residual_norm_bwd_kernel<T, NT, VEC, E>), dim3(a.blocks), dim3(NT), 0, st, a);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && a.d_scale)
+        e = column_sum(a.partial, a.blocks, a.D, a.d_scale, st);
+    if (e == hipSuccess && a.d_weight)
+        e = column_sum(a.partial + (a.d_scale ? static_cast<long>(a.blocks) * a.D : 0), a.blocks, a.D, a.d_weight, st);
+    return e;
+}
+
+template <typename T, int VEC> hipError_t residual_norm_e(bool backward, const ResidualNormArgs &a, hipStream_t st)
+{
+    // one wave per row up to 512 columns, else four, with up to 64 columns
+    // per thread in registers
+    if (a.D <= 512)
+        return residual_norm_t<T, 64, VEC, 1>(backward, a, st);
+    if (a.D <= 2048)
+        return residual_norm_t<T, 256, VEC, 1>(backward, a, st);
+    if (a.D <= 4096)
+        return residual_norm_t<T, 256, VEC, 2>(backward, a, st);
+    if (a.D <= 8192)
+        return residual_norm_t<T, 256, VEC, 4>(backward, a, st);
+    return residual_norm_t<T, 256, VEC, 8>(backward, a, st);
+}
+
+} // namespace
+
+hipError_t launch_gated_norm(int o_dtype, int dtype, bool backward, const GatedNormArgs &a, hipStream_t st)
+{
+    // sixteen-byte accesses where every row allows them
+    const bool aligned = at16(a.o) && at16(a.gate) && a.gate_stride % 8 == 0 &&
+                         (backward ? at16(a.dy) && at16(a.d_o) && at16(a.d_gate) : at16(a.y));
+    if (o_dtype == F32)
+        return dtype == F32 ? gated_norm_d<float, float>(aligned, backward, a, st)
+                            : gated_norm_d<float, __bf16>(aligned, backward, a, st);
+    return dtype == F32 ? gated_norm_d<__bf16, float>(aligned, backward, a, st)
+                        : gated_norm_d<__bf16, __bf16>(aligned, backward, a, st);
+}
+
+hipError_t launch_residual_norm(int dtype, bool backward, const ResidualNormArgs &a, hipStream_t st)
+{
+    const bool aligned = a.D % 8 == 0 && at16(a.x) && at16(a.y) && at16(a.x_out) && at16(a.h) && at16(a.d_x_out) &&
+                         at16(a.d_h) && at16(a.d_x) && at16(a.d_y) && at16(a.partial); // NULL is aligned
+    if (dtype == F32)
+        return aligned ? residual_norm_e<float, 8>(backward, a, st) : residual_norm_e<float, 1>(backward, a, st);
+    return aligned ? residual_norm_e<__bf16, 8>(backward, a, st) : residual_norm_e<__bf16, 1>(backward, a, st);
+}
+
+} // namespace dl

@@ -1,0 +1,11 @@
+// dl_scan_gdn.hip -- GDN instantiations of the sequence-scan kernels (dl_scan.h).
+#include "dl_scan.h"
+
+namespace dl {
+
+hipError_t launch_scan_gdn(int dtype, bool backward, const ScanArgs &a, hipStream_t st)
+{
+    return scan_launch<GDN>(dtype, backward, a, st);
+}
+
+} // namespace dl

@@ -1,0 +1,370 @@
+"""The sequence operators beside the decode step, on torch tensors: `scan` (the
+recurrence over whole sequences: prefill and training), `gated_norm` and
+`residual_norm` (the norms behind and before a recurrent block).
+
+Argument checks, output and workspace allocation and autograd nodes only: the
+arithmetic is in libdeltalog (dl_scan, dl_gated_norm, dl_residual_norm and
+their backward passes).  All three are differentiable once, asynchronous on
+the current stream (or ``stream``, on which their outputs are then allocated
+too) and capturable into HIP graphs.  Tensors may be on any one GPU.
+"""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+from . import (DTYPES, OPS, _check, _dtype_id, _op_id, dl_gated_norm, dl_gated_norm_backward,
+               dl_gated_norm_workspace_bytes, dl_residual_norm, dl_residual_norm_backward,
+               dl_residual_norm_workspace_bytes, dl_scan, dl_scan_backward,
+               dl_scan_backward_workspace_bytes, dl_scan_desc, dl_scan_saved_bytes,
+               dl_scan_workspace_bytes)
+
+
+def _on(device, stream):
+    """The context of a call: its device current, and `stream` (a torch stream
+    or a raw handle) in place of the current one, so that what is allocated
+    belongs to it."""
+    ctx = contextlib.ExitStack()
+    ctx.enter_context(torch.cuda.device(device))
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        ctx.enter_context(torch.cuda.stream(stream))
+    return ctx
+
+
+def _bytes(n, device):
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+
+
+def _tensor(t, name, dtype, shape, device):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} is required")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: want {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} is on {t.device}, want {device}")
+
+
+def _none(t, name, why):
+    if t is not None:
+        raise ValueError(f"{name}: {why} takes none")
+
+
+def _rows(t, lead):
+    """t [*lead, H, d] as rows of H*d elements a fixed distance apart: the
+    tensor (copied only if it is not laid out so) and that distance."""
+    H, d = t.shape[-2:]
+    n = t.numel() // (H * d) if t.numel() else 0
+    if n <= 1:
+        return t.contiguous(), H * d
+    inner = (d == 1 or t.stride(-1) == 1) and (H == 1 or t.stride(-2) == d)
+    step = next((t.stride(i) for i in reversed(range(lead)) if t.shape[i] > 1), H * d)
+    outer, span = True, step
+    for i in reversed(range(lead)):
+        if t.shape[i] > 1 and t.stride(i) != span:
+            outer = False
+        span *= t.shape[i]
+    if inner and outer and step >= H * d:
+        return t, step
+    return t.contiguous(), H * d
+
+
+# --------------------------------------------------------------------- scan --
+
+class _Scan:
+    """The checked arguments of one scan, and its descriptor for the library."""
+
+    def __init__(self, op, q, k, v, beta, log_decay, u, cu_seqlens):
+        opi = _op_id(op)
+        if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() not in (3, 4):
+            raise ValueError("q: want a GPU tensor [T,H,d_k] or [N,T,H,d_k]")
+        dev, lead = q.device, tuple(q.shape[:-2])
+        H, dk = q.shape[-2:]
+        dti = _dtype_id(q.dtype)
+        if not isinstance(v, torch.Tensor) or v.dim() != q.dim():
+            raise ValueError("v: want as many dimensions as q")
+        dv = v.shape[-1]
+        _tensor(k, "k", q.dtype, (*lead, H, dk), dev)
+        _tensor(v, "v", q.dtype, (*lead, H, dv), dev)
+        if op == "rwkv6":
+            _none(beta, "beta", op)
+            _tensor(u, "u", torch.float32, (H, dk), dev)
+        else:
+            _none(u, "u", op)
+            _tensor(beta, "beta", torch.float32, (*lead, H), dev)
+        _tensor(log_decay, "log_decay", torch.float32, (*lead, H) if op == "gdn" else (*lead, H, dk), dev)
+        if cu_seqlens is not None:
+            if q.dim() != 3:
+                raise ValueError("cu_seqlens goes with packed tensors [T,H,d]")
+            if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+                raise ValueError("cu_seqlens: want a 1-D int32 GPU tensor of at least two offsets")
+            _tensor(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, dev)
+            cu_seqlens = cu_seqlens.contiguous()
+        if H < 1:
+            raise ValueError("q: want at least one head")
+        self.N = cu_seqlens.numel() - 1 if cu_seqlens is not None else lead[0] if len(lead) == 2 else 1
+        if self.N < 1:
+            raise ValueError("want at least one sequence")
+        T = q.numel() // (H * dk) if q.numel() else 0
+        if T >= 1 << 31:
+            raise ValueError(f"{T} tokens: want fewer than 2^31")
+        self.op, self.device, self.dtype, self.H, self.dk, self.dv = op, dev, q.dtype, H, dk, dv
+        self.shape = dict(q=q.shape, v=v.shape, h=(*lead, H), ld=log_decay.shape)
+        q, qs = _rows(q, len(lead))
+        k, ks = _rows(k, len(lead))
+        v, vs = _rows(v, len(lead))
+        beta = None if beta is None else beta.contiguous()
+        log_decay = log_decay.contiguous()
+        u = None if u is None else u.contiguous()
+        self.tensors = (q, k, v, beta, log_decay, u, cu_seqlens)  # kept alive with the descriptor
+
+        def p(t):
+            return None if t is None else t.data_ptr()
+        self.desc = dl_scan_desc(opi, dti, T, self.N, H, dk, dv, qs, ks, vs, p(cu_seqlens), p(q), p(k), p(v),
+                                 p(beta), p(log_decay), p(u))
+        if dl_scan_workspace_bytes(self.desc) == 0:
+            raise ValueError(f"unsupported scan shape {op} tokens={T} sequences={self.N} H={H} d_k={dk} d_v={dv}")
+
+    def state_shape(self):
+        return (self.N, self.H, self.dk, self.dv)
+
+    def rows_like(self, shape, dtype):
+        # rows that belong to no sequence are not written: they hold zeros
+        packed = self.tensors[6] is not None
+        return (torch.zeros if packed else torch.empty)(shape, dtype=dtype, device=self.device)
+
+    def forward(self, initial, final, rows, n_rows, saved=None):
+        o = self.rows_like(self.shape["v"], self.dtype)
+        ws = _bytes(dl_scan_workspace_bytes(self.desc), self.device)
+        _check(dl_scan(self.desc, initial, final, rows, n_rows, o, saved, ws), "dl_scan")
+        return o
+
+
+class _ScanFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, op, cu_seqlens, q, k, v, beta, log_decay, u, initial):
+        s = _Scan(op, q, k, v, beta, log_decay, u, cu_seqlens)
+        final = torch.empty(s.state_shape(), dtype=torch.float32, device=s.device)
+        saved = _bytes(dl_scan_saved_bytes(s.desc), s.device)
+        o = s.forward(initial, final, None, 0, saved)
+        ctx.set_materialize_grads(False)
+        # the tensors that the descriptor points at, guarded against changes
+        ctx.save_for_backward(*s.tensors, saved)
+        ctx.scan, ctx.with_initial = s, initial is not None
+        s.tensors = (None,) * 6 + (s.tensors[6],)
+        return o, final
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_o, d_final):
+        s = ctx.scan
+        saved = ctx.saved_tensors[-1]
+        with torch.cuda.device(s.device):
+            d_o = None if d_o is None else d_o.contiguous()
+            d_final = None if d_final is None else d_final.contiguous()
+            delta = s.op != "rwkv6"
+            dq, dk = s.rows_like(s.shape["q"], s.dtype), s.rows_like(s.shape["q"], s.dtype)
+            dv = s.rows_like(s.shape["v"], s.dtype)
+            dbeta = s.rows_like(s.shape["h"], torch.float32) if delta else None
+            dld = s.rows_like(s.shape["ld"], torch.float32)
+            du = None if delta else torch.empty(s.H, s.dk, dtype=torch.float32, device=s.device)
+            d0 = torch.empty(s.state_shape(), dtype=torch.float32, device=s.device) if ctx.with_initial else None
+            ws = _bytes(dl_scan_backward_workspace_bytes(s.desc), s.device)
+            _check(dl_scan_backward(s.desc, saved, d_o, d_final, dq, dk, dv, dbeta, dld, du, d0, ws),
+                   "dl_scan_backward")
+        return None, None, dq, dk, dv, dbeta, dld, du, d0
+
+
+def _initial(initial_state, shape, device):
+    if initial_state is None:
+        return None
+    _tensor(initial_state, "initial_state", torch.float32, shape, device)
+    return initial_state.contiguous()
+
+
+def scan(op: str, q, k, v, beta, log_decay, u=None, initial_state=None, cu_seqlens=None, stream=None):
+    """The recurrence of `DeltaLogState.step` over whole sequences.
+
+    q (r for RWKV6), k [T,H,d_k], v [T,H,d_v] (bf16 or fp32), beta [T,H] fp32
+    (None for RWKV6), log_decay fp32 [T,H] (GDN) or [T,H,d_k], u [H,d_k] fp32
+    (RWKV6 only): N sequences packed one after the other, sequence n being the
+    rows cu_seqlens[n] to cu_seqlens[n+1] (GPU, int32; default: one sequence).
+    Or all with a leading N: N sequences of equal length.  Rows of q, k and v
+    may be slices of one wider projection.  initial_state [N,H,d_k,d_v] fp32
+    (default: zero).
+
+    Returns o, shaped as v in the input dtype, and the end states
+    [N,H,d_k,d_v] fp32.  Rows behind the last sequence hold zeros, in o and in
+    the gradients.  d_k, d_v in {16, 32, 64, 128}.
+
+    Differentiable by q, k, v, beta, log_decay, u and initial_state.  A forward
+    pass that will be differentiated keeps, per 64 tokens and head, the state
+    and 64 d_v floats until its backward pass."""
+    probe = _Scan(op, q, k, v, beta, log_decay, u, cu_seqlens)
+    with _on(probe.device, stream):
+        initial = _initial(initial_state, probe.state_shape(), probe.device)
+        if torch.is_grad_enabled() and any(t is not None and t.requires_grad
+                                           for t in (q, k, v, beta, log_decay, u, initial_state)):
+            return _ScanFn.apply(op, cu_seqlens, q, k, v, beta, log_decay, u, initial)
+        final = torch.empty(probe.state_shape(), dtype=torch.float32, device=probe.device)
+        return probe.forward(initial, final, None, 0), final
+
+
+def _prefill(st, q, k, v, beta, log_decay, cu_seqlens, slots, stream):
+    s = _Scan(st.op, q, k, v, beta, log_decay, st.u, cu_seqlens)
+    if (s.H, s.dk, s.dv, s.dtype) != (st.H, st.d_k, st.d_v, st.dtype):
+        raise ValueError(f"prefill: the state has H={st.H} d_k={st.d_k} d_v={st.d_v} {st.dtype}, the inputs "
+                         f"H={s.H} d_k={s.dk} d_v={s.dv} {s.dtype}")
+    if s.device != st.base.device:
+        raise ValueError(f"q is on {s.device}, the state on {st.base.device}")
+    if slots is None:
+        if s.N != st.B:
+            raise ValueError(f"prefill: {s.N} prompts for {st.B} slots: name their slots")
+        names = range(st.B)
+    else:
+        names = [int(i) for i in slots]
+        if len(names) != s.N or len(set(names)) != s.N or not all(0 <= i < st.B for i in names):
+            raise ValueError(f"slots: want {s.N} distinct slots below {st.B}, got {names}")
+    if any(st.slot_log_len(i) != 0 for i in names):
+        raise ValueError("prefill: a slot's log holds entries; merge it first")
+    with _on(s.device, stream):
+        rows = None if slots is None else torch.tensor(names, dtype=torch.int32).to(s.device, non_blocking=True)
+        with torch.no_grad():
+            return s.forward(st.base, st.base, rows, st.B)
+
+
+# -------------------------------------------------------------------- norms --
+
+def _weight(w, name, n, device):
+    if w is None:
+        return None
+    _tensor(w, name, torch.float32, (n,), device)
+    return w.contiguous()
+
+
+class _GatedNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, o, gate, weight, eps):
+        H, d = o.shape[-2:]
+        rows = o.numel() // (H * d)
+        o = o.contiguous()
+        g, gs = _rows(gate, gate.dim() - 2)
+        weight = _weight(weight, "weight", d, o.device)
+        y = torch.empty(gate.shape, dtype=gate.dtype, device=o.device)
+        _check(dl_gated_norm(rows, H, d, DTYPES[o.dtype], DTYPES[gate.dtype], o, g, gs, weight, eps, y),
+               "dl_gated_norm")
+        ctx.save_for_backward(o, g, weight)
+        ctx.args = (rows, H, d, gs, eps)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        o, g, weight = ctx.saved_tensors
+        rows, H, d, gs, eps = ctx.args
+        with torch.cuda.device(o.device):
+            dy = dy.contiguous()
+            d_o = torch.empty_like(o)
+            dg = torch.empty(dy.shape, dtype=g.dtype, device=o.device)
+            dw = ws = None
+            if weight is not None and ctx.needs_input_grad[2]:
+                dw = torch.empty_like(weight)
+                ws = _bytes(dl_gated_norm_workspace_bytes(rows, H, d), o.device)
+            _check(dl_gated_norm_backward(rows, H, d, DTYPES[o.dtype], DTYPES[g.dtype], o, g, gs, weight, eps,
+                                          dy, d_o, dg, dw, ws), "dl_gated_norm_backward")
+        return d_o, dg, dw, None
+
+
+def gated_norm(o, gate, weight=None, eps: float = 1e-6, stream=None):
+    """rms(o) * weight * silu(gate) per head, rms(a) = a / sqrt(mean(a^2) +
+    eps) over the last dimension: the norm behind the recurrence with its
+    output gate.  o [...,H,d] fp32 (from `step`) or bf16 (from `scan`), gate
+    [...,H,d] bf16 or fp32 (its rows may be slices of a projection), weight
+    [d] fp32 or None.  Returns gate's dtype.  d in {16, 32, 64, 128}.
+    Differentiable by o, gate and weight."""
+    for t, name in ((o, "o"), (gate, "gate")):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() < 2:
+            raise ValueError(f"{name}: want a GPU tensor [...,H,d]")
+        _dtype_id(t.dtype)
+    _tensor(gate, "gate", gate.dtype, o.shape, o.device)
+    if o.shape[-1] not in (16, 32, 64, 128) or o.shape[-2] < 1:
+        raise ValueError(f"o: want heads of 16, 32, 64 or 128, got {tuple(o.shape)}")
+    if weight is not None:
+        _tensor(weight, "weight", torch.float32, (o.shape[-1],), o.device)
+    with _on(o.device, stream):
+        return _GatedNormFn.apply(o, gate, weight, float(eps))
+
+
+class _ResidualNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, y, scale, weight, eps, dtype):
+        D = x.shape[-1]
+        rows = x.numel() // D
+        x = x.contiguous()
+        y = None if y is None else y.contiguous()
+        scale, weight = _weight(scale, "scale", D, x.device), _weight(weight, "weight", D, x.device)
+        x_out = None if y is None else torch.empty_like(x)
+        h = torch.empty(x.shape, dtype=dtype, device=x.device)
+        _check(dl_residual_norm(rows, D, DTYPES[dtype], x, y, scale, weight, eps, x_out, h), "dl_residual_norm")
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(x if y is None else x_out, y if scale is not None else None, scale, weight)
+        ctx.args = (rows, D, eps, dtype, y is not None)
+        if y is None:
+            return h
+        return x_out, h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, *grads):
+        x, y, scale, weight = ctx.saved_tensors
+        rows, D, eps, dtype, added = ctx.args
+        d_x_out, d_h = grads if added else (None, grads[0])
+        with torch.cuda.device(x.device):
+            d_x_out = None if d_x_out is None else d_x_out.contiguous()
+            d_h = None if d_h is None else d_h.contiguous()
+            dx = torch.empty_like(x)
+            dy = torch.empty(x.shape, dtype=dtype, device=x.device) if added else None
+            ds = torch.empty_like(scale) if scale is not None and ctx.needs_input_grad[2] else None
+            dw = torch.empty_like(weight) if weight is not None and ctx.needs_input_grad[3] else None
+            ws = None
+            if ds is not None or dw is not None:
+                ws = _bytes(dl_residual_norm_workspace_bytes(rows, D), x.device)
+            _check(dl_residual_norm_backward(rows, D, DTYPES[dtype], x, y, scale, weight, eps, d_x_out, d_h, dx,
+                                             dy, ds, dw, ws), "dl_residual_norm_backward")
+        return dx, dy, ds, dw, None, None
+
+
+def residual_norm(x, y=None, scale=None, weight=None, eps: float = 1e-6, dtype=None, stream=None):
+    """x' = x + scale * y and h = rms(x') * weight over the last dimension: the
+    residual add behind one block with its per-channel scale, and the norm
+    before the next.  x [...,D] fp32 (the residual stream), y [...,D] bf16 or
+    fp32, scale and weight [D] fp32 or None; D <= 16384.  Returns (x', h), h in
+    y's dtype.  Without y (the first norm): (x, h) with h = rms(x) * weight in
+    ``dtype`` (default bf16).  Differentiable by x, y, scale and weight."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() < 1 or x.dtype != torch.float32:
+        raise ValueError("x: want an fp32 GPU tensor [...,D]")
+    D = x.shape[-1]
+    if not 1 <= D <= 16384:
+        raise ValueError(f"x: want 1 to 16384 columns, got {D}")
+    if y is None:
+        if scale is not None:
+            raise ValueError("scale goes with y")
+        dtype = torch.bfloat16 if dtype is None else dtype
+        _dtype_id(dtype)
+    else:
+        if not isinstance(y, torch.Tensor):
+            raise ValueError("y: want a GPU tensor shaped as x")
+        _dtype_id(y.dtype)
+        _tensor(y, "y", y.dtype, x.shape, x.device)
+        if dtype is not None and dtype != y.dtype:
+            raise ValueError(f"dtype: h has y's type, {y.dtype}")
+        dtype = y.dtype
+    for t, name in ((scale, "scale"), (weight, "weight")):
+        if t is not None:
+            _tensor(t, name, torch.float32, (D,), x.device)
+    with _on(x.device, stream):
+        if y is None:
+            return x, _ResidualNormFn.apply(x, None, None, weight, float(eps), dtype)
+        return _ResidualNormFn.apply(x, y, scale, weight, float(eps), dtype)
