@@ -88,11 +88,15 @@ constexpr int kScanChunk = 64; // tokens per chunk of the scan
 constexpr long scan_slots(long tokens, long seqs) { return tokens / kScanChunk + seqs; }
 // Keys as the kernels take them (d_k = 16 runs as 32, the rest zero).
 constexpr int scan_keys(int dk) { return dk < 32 ? 32 : dk; }
-// Bytes of one chunk and head's operands: three bf16 planes of three
-// chunk x keys and three chunk x chunk matrices, and a decay per key.
-constexpr size_t scan_op_bytes(int keys)
+// bf16 planes of the keys' operands: GDN's are the inputs themselves, exact in
+// one plane where they are bf16; the others carry fp32 decays.
+constexpr int scan_planes(int op, int dtype) { return op == GDN && dtype == BF16 ? 1 : 3; }
+// Bytes of one chunk and head's operands: three chunk x keys and three
+// chunk x chunk matrices, a decay per key, and three numbers per row.
+constexpr size_t scan_op_bytes(int planes, int keys)
 {
-    return size_t(2) * 3 * (3 * kScanChunk * keys + 3 * kScanChunk * kScanChunk) + 4 * keys;
+    return size_t(2) * 3 * (planes * kScanChunk * keys + 3 * kScanChunk * kScanChunk) +
+           4 * (keys + 3 * kScanChunk);
 }
 
 // One scan, forward or backward.  Token strides in elements.

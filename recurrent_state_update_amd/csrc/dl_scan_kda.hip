@@ -1,5 +1,5 @@
-// dl_scan_kda.hip -- KDA instantiations of the sequence-scan kernels (dl_scan.h).
-#include "dl_scan.h"
+// dl_scan_kda.hip -- KDA instantiations of the sequence-scan kernels.
+#include "dl_scan_launch.h"
 
 namespace dl {
 

@@ -1,0 +1,96 @@
+// dl_scan_launch.h -- launches of the scan, templated on the operator.
+#pragma once
+
+#include "dl_scan_carry.h"
+#include "dl_scan_grads.h"
+#include "dl_scan_prep.h"
+
+namespace dl {
+
+template <typename K> hipError_t set_lds(K *kernel, int bytes)
+{
+    return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                               bytes);
+}
+
+inline bool at16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+template <int OP, typename TIn, int DKP, bool BWD> hipError_t launch_prep(const ScanArgs &a, hipStream_t st)
+{
+    if (a.T == 0)
+        return hipSuccess;
+    const dim3 grid(a.slots * a.H);
+    if constexpr (OP == GDN) {
+        const bool vec = at16(a.q) && at16(a.k) && a.qs % 8 == 0 && a.ks % 8 == 0;
+        auto *prep = scan_prep_gdn_kernel<TIn, DKP, BWD>;
+        if (hipError_t e = set_lds(prep, sizeof(PrepGdnLds<TIn, DKP>)); e != hipSuccess)
+            return e;
+        hipLaunchKernelGGL(prep, grid, dim3(256), sizeof(PrepGdnLds<TIn, DKP>), st, a, vec);
+    } else {
+        auto *prep = scan_prep_kernel<OP, TIn, DKP, BWD>;
+        if (hipError_t e = set_lds(prep, sizeof(PrepLds<DKP>)); e != hipSuccess)
+            return e;
+        hipLaunchKernelGGL(prep, grid, dim3(256), sizeof(PrepLds<DKP>), st, a);
+    }
+    return hipGetLastError();
+}
+
+// Workgroups of a carry: a grid in which the value tiles of one sequence and
+// head run on one XCD (carry_work), which then reads their operands once.
+inline dim3 carry_grid(const ScanArgs &a, int nc)
+{
+    return dim3((a.N * a.H + kXcds - 1) / kXcds * kXcds * (a.dv / (16 * nc)));
+}
+
+template <int OP, typename TIn, int DKP> hipError_t scan_forward_t(const ScanArgs &a, hipStream_t st)
+{
+    if (hipError_t e = launch_prep<OP, TIn, DKP, false>(a, st); e != hipSuccess)
+        return e;
+    if (a.save_s)
+        hipLaunchKernelGGL((scan_carry_kernel<OP, TIn, DKP, 1, true>), carry_grid(a, 1), dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((scan_carry_kernel<OP, TIn, DKP, 1, false>), carry_grid(a, 1), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+template <int OP, typename TIn, int DKP> hipError_t scan_backward_t(const ScanArgs &a, hipStream_t st)
+{
+    if (hipError_t e = launch_prep<OP, TIn, DKP, true>(a, st); e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL((scan_carry_bwd_kernel<OP, TIn, DKP, 1>), carry_grid(a, 1), dim3(256), 0, st, a);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess)
+        return e;
+    auto *grads = scan_grads_kernel<OP, TIn, DKP>;
+    if (hipError_t e = set_lds(grads, sizeof(GradLds<DKP>)); e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL(grads, dim3(a.slots * a.H), dim3(DKP * 4), sizeof(GradLds<DKP>), st, a);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess)
+        return e;
+    if (OP == RWKV6) {
+        hipLaunchKernelGGL(scan_du_kernel, dim3((a.H * a.dk + 255) / 256), dim3(256), 0, st, a);
+        return hipGetLastError();
+    }
+    return hipSuccess;
+}
+
+template <int OP> hipError_t scan_launch(int dtype, bool backward, const ScanArgs &a, hipStream_t st)
+{
+#define DL_SCAN_CASE(TIN, DKP)                                                                                        \
+    return backward ? scan_backward_t<OP, TIN, DKP>(a, st) : scan_forward_t<OP, TIN, DKP>(a, st)
+    const int dkp = a.dk < 32 ? 32 : a.dk;
+    if (dtype == BF16) {
+        if (dkp == 128)
+            DL_SCAN_CASE(__bf16, 128);
+        if (dkp == 64)
+            DL_SCAN_CASE(__bf16, 64);
+        DL_SCAN_CASE(__bf16, 32);
+    }
+    if (dkp == 128)
+        DL_SCAN_CASE(float, 128);
+    if (dkp == 64)
+        DL_SCAN_CASE(float, 64);
+    DL_SCAN_CASE(float, 32);
+#undef DL_SCAN_CASE
+}
+
+} // namespace dl

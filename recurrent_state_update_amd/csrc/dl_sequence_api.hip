@@ -61,7 +61,7 @@ struct ScanSizes {
     size_t slot_heads, ops, states, rows_dv, db, du;
     explicit ScanSizes(const dl_scan_desc *d)
         : slot_heads(static_cast<size_t>(dl::scan_slots(d->tokens, d->seqs)) * d->H),
-          ops(up256(slot_heads * dl::scan_op_bytes(dl::scan_keys(d->d_k)))),
+          ops(up256(slot_heads * dl::scan_op_bytes(dl::scan_planes(d->op, d->in_dtype), dl::scan_keys(d->d_k)))),
           states(up256(slot_heads * d->d_k * d->d_v * 4)),
           rows_dv(d->op == DL_OP_RWKV6 ? 0 : up256(slot_heads * dl::kScanChunk * d->d_v * 4)),
           db(d->op == DL_OP_RWKV6 ? 0 : up256(slot_heads * (d->d_v / 16) * dl::kScanChunk * 4)),
