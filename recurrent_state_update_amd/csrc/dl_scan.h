@@ -230,10 +230,11 @@ template <int N, int ROWS, int K, Part PART = ALL, typename F> __device__ __forc
 // stride MLD, upper part of N zero beforehand): the four diagonal blocks by
 // forward substitution, wave w taking block w, one column per lane; then
 // N_IJ = -N_II sum_{J <= K < I} L_IK N_KJ by block diagonals on the fp32
-// matrix instructions.  tmp: 16 x 20 floats of this wave's own.  Four waves.
+// matrix instructions.  tmp: 16 x 20 floats of this wave's own.  For whole
+// workgroups of four waves or more.
 __device__ __forceinline__ void invert_unit_lower(const float *L, float *N, float *tmp, int w, int lane)
 {
-    if (lane < 16) {
+    if (w < 4 && lane < 16) {
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {

@@ -27,10 +27,11 @@ template <int OP, typename TIn, int DKP, bool BWD> hipError_t launch_prep(const 
             return e;
         hipLaunchKernelGGL(prep, grid, dim3(256), sizeof(PrepGdnLds<TIn, DKP>), st, a, vec);
     } else {
+        const bool vec = at16(a.q) && at16(a.k) && at16(a.ld) && a.qs % 8 == 0 && a.ks % 8 == 0;
         auto *prep = scan_prep_kernel<OP, TIn, DKP, BWD>;
-        if (hipError_t e = set_lds(prep, sizeof(PrepLds<DKP>)); e != hipSuccess)
+        if (hipError_t e = set_lds(prep, sizeof(PrepLds<OP, DKP>)); e != hipSuccess)
             return e;
-        hipLaunchKernelGGL(prep, grid, dim3(256), sizeof(PrepLds<DKP>), st, a);
+        hipLaunchKernelGGL(prep, grid, dim3(prep_threads<DKP>()), sizeof(PrepLds<OP, DKP>), st, a, vec);
     }
     return hipGetLastError();
 }

@@ -24,108 +24,168 @@ template <typename TIn> __device__ __forceinline__ void load_piece(TIn (&x)[8], 
     }
 }
 
-template <int DKP> struct PrepLds {
+template <int OP, int DKP> struct PrepLds {
     static constexpr int LD = DKP + 4;
     float k[C * LD], q[C * LD], e[C * LD];
-    float A[C * MLD], B[C * MLD];
-    float eb[4 * DKP], pre[4 * DKP], suf[4 * DKP]; // per 16-row block: its decay, that of the blocks before, after
-    float beta[C];
+    float B[C * MLD], A[OP == RWKV6 ? 4 : C * MLD];
+    float eb[4 * DKP], inv[4 * DKP]; // per 16-row block: its decay, and one over it
+    float pre[4 * DKP], suf[4 * DKP]; // that of the blocks before, after
+    float beta[C], diag[C];
+    int strong[4];
 };
 
 // One chunk of one head: loads q, k and the decays, forms A and B (and N),
 // and writes the operands of the forward carry, or (BWD) of the backward one.
 //
-// The pairs of tokens of one 16 x 16 diagonal block are formed on the vector
-// unit (a running product of decays per pair and key); pairs of different
-// blocks I > J as products of (prefix in I) and (suffix in J x blocks
-// between), both <= 1, on the fp32 matrix instructions.
+// Pairs of tokens of two blocks of 16 rows I >= J are products of rows scaled
+// by the decay from I's start (prefix) and to J's end (suffix x the blocks
+// between), all <= 1, on the fp32 matrix instructions.  Within a block (I = J)
+// that is Gam_C too much, and the suffix is divided by the block's decay:
+// relative rounding only, as long as the decay is far from underflow.  Blocks
+// where a key decays by more than 2^-40 take the vector unit instead, with a
+// running product of decays per pair and key.
+//
+// Bound by latency (one workgroup of eight waves fits a CU, for its LDS).
+template <int DKP> constexpr int prep_threads() { return DKP == 128 ? 512 : 256; }
+
 template <int OP, typename TIn, int DKP, bool BWD>
-__global__ __launch_bounds__(256) void scan_prep_kernel(ScanArgs a)
+__global__ __launch_bounds__(prep_threads<DKP>()) void scan_prep_kernel(ScanArgs a, bool vec)
 {
-    constexpr bool DELTA = OP != RWKV6;
-    constexpr int LD = DKP + 4;
+    using P = Plan<OP, TIn>;
+    constexpr bool DELTA = P::DELTA;
+    constexpr int LD = DKP + 4, NT = prep_threads<DKP>(), NW = NT / 64;
     extern __shared__ __align__(16) char smem[];
-    PrepLds<DKP> &s = *reinterpret_cast<PrepLds<DKP> *>(smem);
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    PrepLds<OP, DKP> &s = *reinterpret_cast<PrepLds<OP, DKP> *>(smem);
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H;
     const Chunk ch = chunk_of(a, slot);
     if (ch.rows <= 0)
         return;
-    using P = Plan<OP, TIn>;
     const Ops<P::NPX, DKP> ops(a, static_cast<long>(slot) * a.H + h);
 
     // rows behind the end: k = q = 0, no decay, beta = 0
-    for (int it = tid; it < C * DKP; it += 256) {
-        const int i = it / DKP, d = it % DKP;
-        const bool in = i < ch.rows && d < a.dk;
-        const long t = ch.t0 + i;
-        float kv = 0.f, qv = 0.f, ev = 1.f;
-        if (in) {
-            kv = from_in(static_cast<const TIn *>(a.k)[t * a.ks + static_cast<long>(h) * a.dk + d]);
-            qv = from_in(static_cast<const TIn *>(a.q)[t * a.qs + static_cast<long>(h) * a.dk + d]);
-            const float l = OP == GDN ? a.ld[t * a.H + h] : a.ld[(t * a.H + h) * a.dk + d];
-            ev = expf(floor_log_decay(l));
+    constexpr int PIECES = C * DKP / 8 / NT;
+    static_assert(PIECES >= 1, "every thread has a piece");
+    {
+        TIn xk[PIECES][8], xq[PIECES][8];
+        float xl[PIECES][8];
+#pragma unroll
+        for (int p = 0; p < PIECES; ++p) {
+            const int i = (p * NT + tid) / (DKP / 8), d = (p * NT + tid) % (DKP / 8) * 8;
+            const bool in = i < ch.rows && d < a.dk;
+            const long t = static_cast<long>(ch.t0) + i, c = static_cast<long>(h) * a.dk + d;
+            load_piece(xk[p], static_cast<const TIn *>(a.k) + t * a.ks + c, in, vec);
+            load_piece(xq[p], static_cast<const TIn *>(a.q) + t * a.qs + c, in, vec);
+            load_piece(xl[p], a.ld + t * a.H * a.dk + c, in, vec);
         }
-        s.k[i * LD + d] = kv;
-        s.q[i * LD + d] = qv;
-        s.e[i * LD + d] = ev;
+#pragma unroll
+        for (int p = 0; p < PIECES; ++p) {
+            const int i = (p * NT + tid) / (DKP / 8), d = (p * NT + tid) % (DKP / 8) * 8;
+#pragma unroll
+            for (int half = 0; half < 8; half += 4) {
+                f32x4 kv, qv, ev;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    kv[e] = from_in(xk[p][half + e]);
+                    qv[e] = from_in(xq[p][half + e]);
+                    ev[e] = expf(floor_log_decay(xl[p][half + e])); // 1 behind the end
+                }
+                *reinterpret_cast<f32x4 *>(&s.k[i * LD + d + half]) = kv;
+                *reinterpret_cast<f32x4 *>(&s.q[i * LD + d + half]) = qv;
+                *reinterpret_cast<f32x4 *>(&s.e[i * LD + d + half]) = ev;
+            }
+        }
     }
-    if (tid < C)
-        s.beta[tid] = DELTA && tid < ch.rows ? a.beta[static_cast<long>(ch.t0 + tid) * a.H + h] : 0.f;
-    for (int it = tid; it < C * MLD; it += 256)
-        s.A[it] = s.B[it] = 0.f;
+    if (tid < C) {
+        s.beta[tid] = DELTA && tid < ch.rows ? a.beta[(static_cast<long>(ch.t0) + tid) * a.H + h] : 0.f;
+        ops.row(2)[tid] = s.beta[tid];
+    }
+    if (tid < 4)
+        s.strong[tid] = 0;
+    for (int it = tid; it < C * MLD; it += NT) {
+        s.B[it] = 0.f;
+        if (DELTA)
+            s.A[it] = 0.f;
+    }
     __syncthreads();
 
-    // diagonal blocks: wave w takes block w; lane = (column j, quarter of the keys)
-    {
-        const int j = lane & 15, g = lane >> 4, r0 = w * 16;
-        float sa[16], sb[16], su = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            sa[i] = sb[i] = 0.f;
-        for (int d = g * (DKP / 4); d < (g + 1) * (DKP / 4); ++d) {
-            const float kj = s.k[(r0 + j) * LD + d];
-            float kd = 0.f; // P_ij k_j
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float e = s.e[(r0 + i) * LD + d], qi = s.q[(r0 + i) * LD + d];
-                if (!DELTA)
-                    sb[i] = fmaf(kd, qi, sb[i]); // before the decay of row i
-                kd = i == j ? kj : kd * e;
-                if (DELTA) {
-                    sb[i] = fmaf(kd, qi, sb[i]);
-                    sa[i] = fmaf(kd, s.k[(r0 + i) * LD + d], sa[i]);
-                }
-            }
-            if (!DELTA)
-                su += d < a.dk ? s.q[(r0 + j) * LD + d] * a.u[static_cast<long>(h) * a.dk + d] * kj : 0.f;
-        }
-        su = wave_sum_from<16>(su);
+    const int d = tid % DKP, I0 = tid / DKP, r0 = I0 * 16; // one thread per (key, block)
+    const bool mine = tid < 4 * DKP;
+    float ev[16];
+    if (mine) {
+        float p = 1.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float va = DELTA ? wave_sum_from<16>(sa[i]) : 0.f, vb = wave_sum_from<16>(sb[i]);
-            if (g == 0) {
-                s.A[(r0 + i) * MLD + r0 + j] = i > j ? va : 0.f;
-                s.B[(r0 + i) * MLD + r0 + j] = i > j ? vb : i < j ? 0.f : DELTA ? vb : su;
-            }
+            ev[i] = s.e[(r0 + i) * LD + d];
+            p *= ev[i];
         }
+        s.eb[tid] = p;
+        s.inv[tid] = 1.f / p;
+        if (!(p >= 0x1p-40f)) // a NaN decay takes the pairwise way as well
+            s.strong[I0] = 1;
+    }
+    if (!DELTA) { // B_ii = sum r u k: NT / 64 lanes per row
+        constexpr int G = NT / C;
+        const int i = tid / G;
+        float x = 0.f;
+        for (int c = tid % G; c < a.dk; c += G)
+            x = fmaf(s.q[i * LD + c] * a.u[static_cast<long>(h) * a.dk + c], s.k[i * LD + c], x);
+#pragma unroll
+        for (int m = 1; m < G; m *= 2)
+            x += __shfl_xor(x, m);
+        if (tid % G == 0)
+            s.diag[i] = x;
     }
     __syncthreads();
 
+    const int strong[4] = {s.strong[0], s.strong[1], s.strong[2], s.strong[3]};
+    if (strong[0] | strong[1] | strong[2] | strong[3]) {
+        // wave w takes block w; lane = (column j, quarter of the keys)
+        const int j = lane & 15, g = lane >> 4, b0 = w * 16;
+        if (w < 4 && s.strong[w]) {
+            float sa[16], sb[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                sa[i] = sb[i] = 0.f;
+            for (int c = g * (DKP / 4); c < (g + 1) * (DKP / 4); ++c) {
+                const float kj = s.k[(b0 + j) * LD + c];
+                float kd = 0.f; // P_ij k_j
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float e = s.e[(b0 + i) * LD + c], qi = s.q[(b0 + i) * LD + c];
+                    if (!DELTA)
+                        sb[i] = fmaf(kd, qi, sb[i]); // before the decay of row i
+                    kd = i == j ? kj : kd * e;
+                    if (DELTA) {
+                        sb[i] = fmaf(kd, qi, sb[i]);
+                        sa[i] = fmaf(kd, s.k[(b0 + i) * LD + c], sa[i]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float va = DELTA ? wave_sum_from<16>(sa[i]) : 0.f, vb = wave_sum_from<16>(sb[i]);
+                if (g == 0) {
+                    if (DELTA)
+                        s.A[(b0 + i) * MLD + b0 + j] = i > j ? va : 0.f;
+                    s.B[(b0 + i) * MLD + b0 + j] = i > j ? vb : i < j ? 0.f : DELTA ? vb : s.diag[b0 + i];
+                }
+            }
+        }
+        __syncthreads();
+    }
+
     // in place: k -> k (prefix in its block), q -> q (prefix), e -> k (suffix)
-    for (int it = tid; it < 4 * DKP; it += 256) {
-        const int d = it % DKP, r0 = it / DKP * 16;
-        float kv[16], ev[16], p = 1.f;
+    if (mine) {
+        float kv[16], p = 1.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             kv[i] = s.k[(r0 + i) * LD + d];
-            ev[i] = s.e[(r0 + i) * LD + d];
             const float before = p;
             p *= ev[i];
             s.q[(r0 + i) * LD + d] *= DELTA ? p : before;
             s.k[(r0 + i) * LD + d] = kv[i] * p;
         }
-        s.eb[it] = p;
         p = 1.f;
 #pragma unroll
         for (int i = 15; i >= 0; --i) {
@@ -133,7 +193,6 @@ __global__ __launch_bounds__(256) void scan_prep_kernel(ScanArgs a)
             p *= ev[i];
         }
     }
-    __syncthreads();
     if (tid < DKP) {
         float p = 1.f, q = 1.f;
 #pragma unroll
@@ -145,26 +204,35 @@ __global__ __launch_bounds__(256) void scan_prep_kernel(ScanArgs a)
         }
         ops.gam()[tid] = p;
     }
+    __syncthreads();
 
-    // pairs of different blocks
-    for (int pair = w; pair < 6; pair += 4) {
-        const int I = pair < 1 ? 1 : pair < 3 ? 2 : 3, J = pair - I * (I - 1) / 2;
-        f32x4 ca = {0, 0, 0, 0}, cb = {0, 0, 0, 0};
+    // pairs of tokens: a wave takes one of the ten block pairs, of A or of B
+    for (int task = w; task < (DELTA ? 20 : 10); task += NW) {
+        const bool isA = task >= 10;
+        const int pair = isA ? task - 10 : task;
+        const int I = pair < 1 ? 0 : pair < 3 ? 1 : pair < 6 ? 2 : 3, J = pair - I * (I + 1) / 2;
+        if (I == J && strong[I])
+            continue;
+        const float *left = isA ? s.k : s.q;
+        f32x4 x = {0, 0, 0, 0};
+#pragma unroll
         for (int ks = 0; ks < DKP / 16; ++ks) {
-            const int d = ks * 16 + (lane >> 4) * 4;
-            f32x4 r = *reinterpret_cast<const f32x4 *>(&s.e[(J * 16 + (lane & 15)) * LD + d]);
+            const int c = ks * 16 + (lane >> 4) * 4;
+            f32x4 r = *reinterpret_cast<const f32x4 *>(&s.e[(J * 16 + (lane & 15)) * LD + c]);
+            if (I == J)
+                r *= *reinterpret_cast<const f32x4 *>(&s.inv[I * DKP + c]);
             for (int K = J + 1; K < I; ++K)
-                r *= *reinterpret_cast<const f32x4 *>(&s.eb[K * DKP + d]);
-            cb = mfma32x4(*reinterpret_cast<const f32x4 *>(&s.q[(I * 16 + (lane & 15)) * LD + d]), r, cb);
-            if (DELTA)
-                ca = mfma32x4(*reinterpret_cast<const f32x4 *>(&s.k[(I * 16 + (lane & 15)) * LD + d]), r, ca);
+                r *= *reinterpret_cast<const f32x4 *>(&s.eb[K * DKP + c]);
+            x = mfma32x4(*reinterpret_cast<const f32x4 *>(&left[(I * 16 + (lane & 15)) * LD + c]), r, x);
         }
+        const int j = lane & 15;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int at = (I * 16 + (lane >> 4) * 4 + e) * MLD + J * 16 + (lane & 15);
-            s.B[at] = cb[e];
-            if (DELTA)
-                s.A[at] = ca[e];
+            const int i = (lane >> 4) * 4 + e;
+            float v = x[e];
+            if (I == J)
+                v = i > j ? v : i < j || isA ? 0.f : DELTA ? v : s.diag[I * 16 + i];
+            (isA ? s.A : s.B)[(I * 16 + i) * MLD + J * 16 + j] = v;
         }
     }
     __syncthreads();
@@ -196,7 +264,7 @@ __global__ __launch_bounds__(256) void scan_prep_kernel(ScanArgs a)
         static_assert(C * MLD + 4 * 16 * 20 <= 3 * C * LD, "N and the scratch of four waves fit");
         float *L = s.A, *N = area;
         __syncthreads();
-        for (int it = tid; it < C * C; it += 256) {
+        for (int it = tid; it < C * C; it += NT) {
             const int i = it / C, j = it % C;
             L[i * MLD + j] *= s.beta[j];
             N[i * MLD + j] = 0.f;
