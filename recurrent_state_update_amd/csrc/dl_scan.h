@@ -18,8 +18,8 @@
 //   S' = Gam_C (.) S + K^T^ b
 // so that all work except the carry from S to S' is matrix products over
 // chunks.  Its adjoint (dO, dS' given) has the same shape:
-//   db = B^T dO + K^ dS',  z = N^T (beta db),  y = db - A^T z,
-//   dbeta = y . E,  dv = z  (RWKV6: dv = db)
+//   db = B^T dO + K^ dS',  z = N^T (beta db),
+//   dbeta = (db - A^T z) . E,  dv = z  (RWKV6: dv = db)
 //   dS = Gam_C (.) dS' + Q~^T dO - K~^T z
 //   dQ~ = dO S^T, dK~ = -z S^T, dK^ = b dS'^T, dB = dO b^T, dA = -z b^T,
 // from which dq, dk and the log-decay's gradient follow within the chunk.
@@ -173,7 +173,7 @@ __device__ __forceinline__ Chunk chunk_of(const ScanArgs &a, int slot)
 // row l % 16, k from 8 (l / 16): one coalesced 1 KiB load per fragment.
 //   forward : op 0 K~ [C][DKP], 1 Q~ [C][DKP], 2 K^T^ [DKP][C]; mat 0 N, 1 B
 //   backward: op 0 K^ [C][DKP], 1 Q~^T [DKP][C], 2 K~^T [DKP][C]; mat 0 N^T,
-//             1 B^T, 2 A^T
+//             1 B^T, 2 A and (GDN) B in fp32 blocks (store_pairs)
 // (ROWS: K and Q without their decays.)  Of the triangular C x C operands the
 // fragments of zeros are neither written nor read.
 template <int NP, int DKP> struct Ops {
@@ -187,13 +187,15 @@ template <int NP, int DKP> struct Ops {
     __device__ __forceinline__ float *row(int i) const { return gam() + DKP + i * C; } // 0 Gam_i, 1 P_Ci, 2 beta
 };
 
+// (uniform base + 32-bit lane offset: the load's scalar-address form)
 template <int N>
 __device__ __forceinline__ void load_frag(bf16x8 (&f)[N], const __bf16 *op, int ksteps, int rb, int ks, int lane)
 {
-    const bf16x8 *p = reinterpret_cast<const bf16x8 *>(op) + ((rb * ksteps + ks) * N) * 64 + lane;
+    const char *base = reinterpret_cast<const char *>(op) + (rb * ksteps + ks) * N * 1024;
+    const unsigned off = lane * 16;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        f[i] = p[i * 64];
+        f[i] = *reinterpret_cast<const bf16x8 *>(base + (off + i * 1024));
 }
 template <int N>
 __device__ __forceinline__ void store_frag(__bf16 *op, int ksteps, int rb, int ks, int lane, const bf16x8 (&f)[N])

@@ -1,34 +1,76 @@
 // dl_scan_grads.h -- per chunk and head of a scan: the gradients of its inputs.
+//
+// With dS' and z from the backward carry, E and S from the forward one:
+//   dQ~ = dO S^T, dK~ = -z S^T, dK^ = b dS'^T        [C][d_k], over d_v
+//   dB = dO b^T, dA = -z b^T (lower triangles)       [C][C], over d_v
+// on the bf16 matrix instructions from fp32 split into planes, then within the
+// chunk (cq, cr: row i's parts through q and k as a reader; cc: through k as
+// what is read later)
+//   cq_i = Gam_i dQ~_i + sum_j dB_ij P_ij k_j,  cr_i = Gam_i dK~_i + sum_j dA_ij P_ij k_j
+//   cc_j = P_Cj dK^_j + sum_i P_ij (dA_ij k_i + dB_ij q_i)
+//   dq = cq, dk = cr + cc, and the log-decay's gradient, the sum over all
+// pairs whose decay contains it.  dbeta_j = (db . E)_j - sum_i A_ij z_i . E_j.
+//
+// One workgroup per chunk and head, one wave per 16 keys.  Bound by reading S
+// and dS' (128 KiB each at d = 128, the chunk's largest part) and by the
+// matrix products; one workgroup fits a CU, for its LDS.
 #pragma once
 
-#include "dl_scan.h"
+#include <type_traits>
+
+#include "dl_scan_carry.h"
+#include "dl_scan_prep.h"
 
 namespace dl {
 
-template <int DKP> struct GradLds {
-    static constexpr int LD = DKP + 4;
-    float k[C * LD], q[C * LD], e[C * LD];
-    union {
-        struct {
-            float dA[C * MLD], dB[C * MLD];
-        };
-        float buf[C * LD]; // one C x DKP product on its way to the keys' threads
-    };
-    float gam[DKP];     // sum_v S dS' per key
-    float part[4 * DKP]; // sums over the rows of a block
+// dO, -z and E (RWKV6: V) for 64 value columns, as planes.
+template <int OP, typename TIn> struct GradStage {
+    using P = Plan<OP, TIn>;
+    static constexpr int LD = 64 + 8, NE = P::DELTA ? 3 : P::NPI;
+    __bf16 g[P::NPI][C * LD], e[NE][C * LD];
+    __bf16 z[P::DELTA ? 3 : 1][P::DELTA ? C * LD : 8];
 };
 
-// One chunk of one head.  Wave w forms the 16 keys w of dQ~, dK~ and dK^ (all
-// C rows); then one thread per (key, 16-row block I) walks the rows outside I
-// with a running product of decays, and the pairs inside I.
+template <int OP, typename TIn, int DKP> struct GradLds {
+    static constexpr int LD = DKP + 4, XLD = C + 8;
+    // GDN: the weights dB P, its transpose and dA P + its transpose in planes
+    struct Rows {
+        __bf16 x1[3][C * XLD], x2[3][C * XLD], x3[3][C * XLD];
+    };
+    // per key: keys and queries scaled within their blocks, dA and dB
+    struct Keys {
+        float kr[C * LD], kl[C * LD], ql[C * LD];
+        float dB[C * MLD], dA[C * MLD];
+    };
+    static constexpr bool ROWS = OP == GDN;
+    union {
+        GradStage<OP, TIn> st;
+        std::conditional_t<ROWS, Rows, Keys> x;
+    };
+    float gs[DKP];                // sum_v S dS' per key
+    float beta[C], dbeta[10][16]; // per pair of blocks: sum_i A_ij (-z_i . E_j)
+    // per key
+    float eb[ROWS ? 1 : 4 * DKP], pre[ROWS ? 1 : 4 * DKP], suf[ROWS ? 1 : 4 * DKP]; // of, before, behind a block
+    float part[ROWS ? 1 : 4 * DKP], kh[ROWS ? 1 : 4 * DKP];
+    // GDN
+    TIn k[ROWS ? C * LD : 1], q[ROWS ? C * LD : 1];
+    float e[C], rpre[C], rsuf[C], reb[4];                      // decays of rows
+    float diag[ROWS ? 4 : 1][16 * 16];                         // P_ij of the diagonal blocks
+    float roww[10][16], colw[10][16];                          // sums of W_ij = dB B + dA A
+    float ra[ROWS ? DKP / 16 : 1][C], rh[ROWS ? DKP / 16 : 1][C]; // per 16 keys: reads of S, writes into S'
+};
+
 template <int OP, typename TIn, int DKP>
-__global__ __launch_bounds__(DKP * 4) void scan_grads_kernel(ScanArgs a)
+__global__ __launch_bounds__(DKP * 4) void scan_grads_kernel(ScanArgs a, bool vec, int tiles)
 {
-    constexpr bool DELTA = OP != RWKV6;
-    constexpr int LD = DKP + 4, NT = DKP * 4, NW = NT / 64;
+    using P = Plan<OP, TIn>;
+    using G = GradLds<OP, TIn, DKP>;
+    using St = GradStage<OP, TIn>;
+    constexpr bool DELTA = P::DELTA;
+    constexpr int LD = DKP + 4, NT = DKP * 4, NW = NT / 64, TASKS = (10 + NW - 1) / NW;
     extern __shared__ __align__(16) char smem[];
-    GradLds<DKP> &s = *reinterpret_cast<GradLds<DKP> *>(smem);
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    G &s = *reinterpret_cast<G *>(smem);
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H;
     const long slot_head = static_cast<long>(slot) * a.H + h;
     const Chunk ch = chunk_of(a, slot);
@@ -37,289 +79,582 @@ __global__ __launch_bounds__(DKP * 4) void scan_grads_kernel(ScanArgs a)
             a.w_du[slot_head * a.dk + tid] = 0.f;
         return;
     }
-    for (int it = tid; it < C * DKP; it += NT) {
-        const int i = it / DKP, d = it % DKP;
-        const bool in = i < ch.rows && d < a.dk;
-        const long t = ch.t0 + i;
-        float kv = 0.f, qv = 0.f, ev = 1.f;
-        if (in) {
-            kv = from_in(static_cast<const TIn *>(a.k)[t * a.ks + static_cast<long>(h) * a.dk + d]);
-            qv = from_in(static_cast<const TIn *>(a.q)[t * a.qs + static_cast<long>(h) * a.dk + d]);
-            const float l = OP == GDN ? a.ld[t * a.H + h] : a.ld[(t * a.H + h) * a.dk + d];
-            ev = expf(floor_log_decay(l));
-        }
-        s.k[i * LD + d] = kv;
-        s.q[i * LD + d] = qv;
-        s.e[i * LD + d] = ev;
-    }
+    const Ops<P::NPX, DKP> ops(a, slot_head);
+    const int c16 = lane & 15, r4 = (lane >> 4) * 4;
+    const int d = tid % DKP, I0 = tid / DKP, r0 = I0 * 16; // one thread per (key, block)
+    const long t0 = ch.t0;
 
-    const int r = lane & 15, k4 = (lane >> 4) * 4;
-    // rows of dO, z and b as product operands: four values from v of row i
-    auto ld_do = [&](int i, int v) {
-        f32x4 x = {0, 0, 0, 0};
-        if (i < ch.rows && a.d_o) {
+    // ---- what the chunk itself needs, ahead of the products over d_v
+    float kv[16], qv[16], ev[16]; // per key: this thread's rows
+    if constexpr (OP == GDN) {
+        for (int it = tid; it < C * DKP / 8; it += NT) {
+            const int i = it / (DKP / 8), c = it % (DKP / 8) * 8;
+            const bool in = i < ch.rows && c < a.dk;
+            const long at = static_cast<long>(h) * a.dk + c;
+            TIn x[8], y[8];
+            load_piece(x, static_cast<const TIn *>(a.k) + (t0 + i) * a.ks + at, in, vec);
+            load_piece(y, static_cast<const TIn *>(a.q) + (t0 + i) * a.qs + at, in, vec);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                x[e] = from_in(static_cast<const TIn *>(a.d_o)[((static_cast<long>(ch.t0) + i) * a.H + h) * a.dv + v + e]);
-        }
-        return x;
-    };
-    auto ld_b = [&](int i, int v) {
-        f32x4 x = {0, 0, 0, 0};
-        if (i < ch.rows) {
-            if constexpr (DELTA) {
-                x = *reinterpret_cast<const f32x4 *>(&a.save_e[(slot_head * C + i) * a.dv + v]) *
-                    a.beta[(static_cast<long>(ch.t0) + i) * a.H + h];
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    x[e] = from_in(static_cast<const TIn *>(
-                        a.v)[(static_cast<long>(ch.t0) + i) * a.vs + static_cast<long>(h) * a.dv + v + e]);
+            for (int e = 0; e < 8; ++e) {
+                s.k[i * LD + c + e] = x[e];
+                s.q[i * LD + c + e] = y[e];
             }
         }
-        return x;
-    };
-    auto ld_z = [&](int i, int v) {
-        return i < ch.rows ? *reinterpret_cast<const f32x4 *>(&a.w_z[(slot_head * C + i) * a.dv + v]) : f32x4{0, 0, 0, 0};
-    };
+        for (int i = tid; i < C; i += NT)
+            s.e[i] = i < ch.rows ? expf(floor_log_decay(a.ld[(t0 + i) * a.H + h])) : 1.f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const bool in = r0 + i < ch.rows && d < a.dk;
+            const long t = t0 + r0 + i, at = static_cast<long>(h) * a.dk + d;
+            kv[i] = in ? from_in(static_cast<const TIn *>(a.k)[t * a.ks + at]) : 0.f;
+            qv[i] = in ? from_in(static_cast<const TIn *>(a.q)[t * a.qs + at]) : 0.f;
+            ev[i] = in ? a.ld[t * a.H * a.dk + at] : 0.f;
+        }
+        float p = 1.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            ev[i] = expf(floor_log_decay(ev[i]));
+            p *= ev[i];
+        }
+        s.eb[tid] = p;
+    }
+    for (int i = tid; i < C; i += NT)
+        s.beta[i] = !DELTA ? 1.f : i < ch.rows ? a.beta[(t0 + i) * a.H + h] : 0.f;
 
-    f32x4 dQ[4], dK[4], dH[4];
+    // ---- products over d_v, 64 columns at a time
+    f32x4 dQ[4], dK[4], dH[4], xB[TASKS], xM[TASKS];
+    const f32x4 zero = {0, 0, 0, 0};
 #pragma unroll
     for (int I = 0; I < 4; ++I)
-        dQ[I] = dK[I] = dH[I] = f32x4{0, 0, 0, 0};
+        dQ[I] = dK[I] = dH[I] = zero;
+#pragma unroll
+    for (int p = 0; p < TASKS; ++p)
+        xB[p] = xM[p] = zero;
     float gs = 0.f;
-    const int kd = w * 16 + r; // the key whose row of S this lane reads
-    for (int v = k4; v < a.dv; v += 16) {
-        f32x4 S = {0, 0, 0, 0}, dS = {0, 0, 0, 0};
-        if (kd < a.dk) {
-            S = *reinterpret_cast<const f32x4 *>(&a.save_s[(slot_head * a.dk + kd) * a.dv + v]);
-            dS = *reinterpret_cast<const f32x4 *>(&a.w_ds[(slot_head * a.dk + kd) * a.dv + v]);
+    auto frag = [&](auto &f, const auto &x, int rb, int ks) {
+#pragma unroll
+        for (int n = 0; n < static_cast<int>(sizeof(f) / sizeof(f[0])); ++n)
+            f[n] = *reinterpret_cast<const bf16x8 *>(&x[n][(rb * 16 + c16) * St::LD + ks * 32 + (lane >> 4) * 8]);
+    };
+    for (int v0 = 0; v0 < a.dv; v0 += 64) {
+        const int ksteps = a.dv - v0 > 32 ? 2 : 1;
+        f32x8 S[2], dS[2]; // row d of the state, in the matrix instruction's order
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            const int v = v0 + ks * 32 + (lane >> 4) * 8, row = w * 16 + c16;
+            S[ks] = dS[ks] = f32x8{};
+            if (v < a.dv && row < a.dk) {
+                S[ks] = *reinterpret_cast<const f32x8 *>(&a.save_s[(slot_head * a.dk + row) * a.dv + v]);
+                dS[ks] = *reinterpret_cast<const f32x8 *>(&a.w_ds[(slot_head * a.dk + row) * a.dv + v]);
+            }
         }
+        if (v0 > 0)
+            __syncthreads(); // the stage before is read
+        for (int it = tid; it < C * 8; it += NT) {
+            const int i = it / 8, c = it % 8 * 8, v = v0 + c;
+            const bool in = i < ch.rows && v < a.dv;
+            const long t = t0 + i, at = (slot_head * C + i) * a.dv + v;
+            TIn x[8];
+            load_piece(x, static_cast<const TIn *>(a.d_o) + (t * a.H + h) * a.dv + v, in && a.d_o, vec);
+            bf16x8 pl[P::NPI];
+            if constexpr (P::BF)
+                pl[0] = __builtin_bit_cast(bf16x8, x);
+            else
+                split(__builtin_bit_cast(f32x8, x), pl);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            gs = fmaf(S[e], dS[e], gs);
+            for (int n = 0; n < P::NPI; ++n)
+                *reinterpret_cast<bf16x8 *>(&s.st.g[n][i * St::LD + c]) = pl[n];
+            if constexpr (DELTA) {
+                f32x8 z = {}, E = {};
+                if (in) {
+                    z = *reinterpret_cast<const f32x8 *>(&a.w_z[at]);
+                    E = *reinterpret_cast<const f32x8 *>(&a.save_e[at]);
+                }
+                bf16x8 pz[3], pe[3];
+                split(-z, pz);
+                split(E, pe);
 #pragma unroll
-        for (int I = 0; I < 4; ++I) {
-            dQ[I] = mfma32x4(ld_do(I * 16 + r, v), S, dQ[I]);
-            dH[I] = mfma32x4(ld_b(I * 16 + r, v), dS, dH[I]);
-            if (DELTA)
-                dK[I] = mfma32x4(ld_z(I * 16 + r, v), S, dK[I]);
+                for (int n = 0; n < 3; ++n) {
+                    *reinterpret_cast<bf16x8 *>(&s.st.z[n][i * St::LD + c]) = pz[n];
+                    *reinterpret_cast<bf16x8 *>(&s.st.e[n][i * St::LD + c]) = pe[n];
+                }
+            } else {
+                load_piece(x, static_cast<const TIn *>(a.v) + t * a.vs + static_cast<long>(h) * a.dv + v, in, vec);
+                if constexpr (P::BF)
+                    pl[0] = __builtin_bit_cast(bf16x8, x);
+                else
+                    split(__builtin_bit_cast(f32x8, x), pl);
+#pragma unroll
+                for (int n = 0; n < P::NPI; ++n)
+                    *reinterpret_cast<bf16x8 *>(&s.st.e[n][i * St::LD + c]) = pl[n];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            if (ks >= ksteps)
+                break;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                gs = fmaf(S[ks][e], dS[ks][e], gs);
+            bf16x8 ps[3], pd[3];
+            split(S[ks], ps);
+            split(dS[ks], pd);
+#pragma unroll
+            for (int I = 0; I < 4; ++I) {
+                bf16x8 g[P::NPI], e[St::NE];
+                frag(g, s.st.g, I, ks);
+                frag(e, s.st.e, I, ks);
+                dQ[I] = mma<3>(g, ps, dQ[I]);
+                dH[I] = mma<3>(e, pd, dH[I]);
+                if constexpr (DELTA) {
+                    bf16x8 z[3];
+                    frag(z, s.st.z, I, ks);
+                    dK[I] = mma<3>(z, ps, dK[I]);
+                }
+            }
+#pragma unroll
+            for (int p = 0; p < TASKS; ++p) {
+                const int b = w + p * NW;
+                if (b >= 10)
+                    break;
+                const int I = b < 1 ? 0 : b < 3 ? 1 : b < 6 ? 2 : 3, J = b - I * (I + 1) / 2;
+                bf16x8 g[P::NPI], e[St::NE];
+                frag(g, s.st.g, I, ks);
+                frag(e, s.st.e, J, ks);
+                xB[p] = mma<3>(g, e, xB[p]);
+                if constexpr (DELTA) {
+                    bf16x8 z[3];
+                    frag(z, s.st.z, I, ks);
+                    xM[p] = mma<3>(z, e, xM[p]);
+                }
+            }
         }
     }
     gs = wave_sum_from<16>(gs);
     if (lane < 16)
-        s.gam[kd] = gs;
+        s.gs[w * 16 + c16] = gs;
+    __syncthreads(); // the stage is read; e, eb, beta and gs are complete
 
-    // to one thread per (key, block of 16 rows)
-    const int d = tid % DKP, I = tid / DKP, r0 = I * 16;
-    float cq[16], cr[16], cc[16];
-    auto hand_over = [&](const f32x4 (&x)[4], float (&y)[16]) {
+    if constexpr (OP == GDN) {
+        // ---- the decays of pairs; zero the weights' planes
+        for (int b = w; b < 4; b += NW)
+            if (lane < 16) {
+                float p = 0.f, pre = 1.f, suf = 1.f, all = 1.f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float e = s.e[b * 16 + i];
+                    p = i == lane ? 1.f : p * e;
+                    s.diag[b][i * 16 + lane] = p;
+                    pre *= i <= lane ? e : 1.f;
+                    suf *= i > lane ? e : 1.f;
+                    all *= e;
+                }
+                s.rpre[b * 16 + lane] = pre;
+                s.rsuf[b * 16 + lane] = suf;
+                if (lane == 0)
+                    s.reb[b] = all;
+            }
+        constexpr int X = sizeof(typename G::Rows) / 16;
+        for (int it = tid; it < X; it += NT)
+            reinterpret_cast<f32x4 *>(&s.x)[it] = zero;
         __syncthreads();
 #pragma unroll
-        for (int J = 0; J < 4; ++J)
+        for (int p = 0; p < TASKS; ++p) {
+            const int b = w + p * NW;
+            if (b >= 10)
+                break;
+            const int I = b < 1 ? 0 : b < 3 ? 1 : b < 6 ? 2 : 3, J = b - I * (I + 1) / 2;
+            const f32x4 *ab = reinterpret_cast<const f32x4 *>(ops.mat(2));
+            const f32x4 A = ab[b * 64 + lane], B = ab[(10 + b) * 64 + lane];
+            const float beta = s.beta[J * 16 + c16];
+            float between = 1.f, cm = 0.f, cw = 0.f;
+            for (int K = J + 1; K < I; ++K)
+                between *= s.reb[K];
+            const float right = between * s.rsuf[J * 16 + c16];
+            f32x4 w1, w3;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                s.buf[(J * 16 + k4 + e) * LD + w * 16 + r] = x[J][e];
+            for (int e = 0; e < 4; ++e) {
+                const int i = r4 + e;
+                const bool below = I > J || i > c16, on = I == J && i == c16;
+                const float f = I == J ? s.diag[I][i * 16 + c16] : s.rpre[I * 16 + i] * right;
+                const float gb = below || on ? beta * xB[p][e] : 0.f, ga = below ? beta * xM[p][e] : 0.f;
+                w1[e] = gb * f;
+                w3[e] = ga * f;
+                const float W = below ? gb * B[e] + ga * A[e] : 0.f;
+                cw += W;
+                cm += below ? A[e] * xM[p][e] : 0.f;
+                float rw = W;
+                rw = add_row_ror<1>(rw);
+                rw = add_row_ror<2>(rw);
+                rw = add_row_ror<4>(rw);
+                rw = add_row_ror<8>(rw);
+                if (c16 == 0)
+                    s.roww[b][i] = rw;
+            }
+            cm = wave_sum_from<16>(cm);
+            cw = wave_sum_from<16>(cw);
+            if (lane < 16) {
+                s.dbeta[b][lane] = cm;
+                s.colw[b][lane] = cw;
+            }
+            bf16x4 p1[3], p3[3];
+            split(w1, p1);
+            split(w3, p3);
+#pragma unroll
+            for (int n = 0; n < 3; ++n) {
+                *reinterpret_cast<bf16x4 *>(&s.x.x2[n][(J * 16 + c16) * G::XLD + I * 16 + r4]) = p1[n];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = I * 16 + r4 + e, j = J * 16 + c16;
+                    s.x.x1[n][i * G::XLD + j] = p1[n][e];
+                    if (i > j) {
+                        s.x.x3[n][i * G::XLD + j] = p3[n][e];
+                        s.x.x3[n][j * G::XLD + i] = p3[n][e];
+                    }
+                }
+            }
+        }
         __syncthreads();
+        // ---- wave w: keys 16 w.., all rows
+        bf16x8 kt[2][P::NPX], qt[2][P::NPX];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            y[i] = s.buf[(r0 + i) * LD + d];
-    };
-    hand_over(dQ, cq);
-    hand_over(dH, cc);
-    if constexpr (DELTA) {
-        hand_over(dK, cr);
+        for (int ks = 0; ks < 2; ++ks) {
+            load_frag(qt[ks], ops.op(1), 2, w, ks, lane);
+            load_frag(kt[ks], ops.op(2), 2, w, ks, lane);
+        }
+        auto xfrag = [&](bf16x8 (&f)[3], const __bf16 (&x)[3][C * G::XLD], int rb, int ks) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            cr[i] = -cr[i];
-    }
-    __syncthreads();
-
-    // dA (strictly lower) and dB (lower)
-    for (int p = w; p < 10; p += NW) {
-        const int BI = p < 1 ? 0 : p < 3 ? 1 : p < 6 ? 2 : 3, BJ = p - BI * (BI + 1) / 2;
-        f32x4 xa = {0, 0, 0, 0}, xb = {0, 0, 0, 0};
-        for (int v = k4; v < a.dv; v += 16) {
-            const f32x4 b = ld_b(BJ * 16 + r, v);
-            xb = mfma32x4(ld_do(BI * 16 + r, v), b, xb);
+            for (int n = 0; n < 3; ++n)
+                f[n] = *reinterpret_cast<const bf16x8 *>(&x[n][(rb * 16 + c16) * G::XLD + ks * 32 + (lane >> 4) * 8]);
+        };
+#pragma unroll
+        for (int I = 0; I < 4; ++I) {
+            float bg = 1.f, ag = 1.f; // blocks before, after
+            for (int K = 0; K < 4; ++K) {
+                bg *= K < I ? s.reb[K] : 1.f;
+                ag *= K > I ? s.reb[K] : 1.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = I * 16 + r4 + e, at = i * LD + w * 16 + c16;
+                const float gam = bg * s.rpre[i], end = ag * s.rsuf[i] * s.beta[i];
+                dQ[I][e] *= gam;
+                dK[I][e] *= gam;
+                dH[I][e] *= end;
+                const float k = from_in(s.k[at]), q = from_in(s.q[at]);
+                float x = fmaf(q, dQ[I][e], k * dK[I][e]), y = k * dH[I][e];
+                x = add_row_ror<1>(x);
+                y = add_row_ror<1>(y);
+                x = add_row_ror<2>(x);
+                y = add_row_ror<2>(y);
+                x = add_row_ror<4>(x);
+                y = add_row_ror<4>(y);
+                x = add_row_ror<8>(x);
+                y = add_row_ror<8>(y);
+                if (c16 == 0) {
+                    s.ra[w][i] = x;
+                    s.rh[w][i] = y;
+                }
+                dK[I][e] += dH[I][e];
+            }
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                bf16x8 f[3];
+                if (frag_used(LOWER, I, ks)) {
+                    xfrag(f, s.x.x1, I, ks);
+                    dQ[I] = mma<3>(f, kt[ks], dQ[I]);
+                }
+                xfrag(f, s.x.x3, I, ks);
+                dK[I] = mma<3>(f, kt[ks], dK[I]);
+                if (frag_used(UPPER, I, ks)) {
+                    xfrag(f, s.x.x2, I, ks);
+                    dK[I] = mma<3>(f, qt[ks], dK[I]);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = I * 16 + r4 + e, key = w * 16 + c16;
+                if (i < ch.rows && key < a.dk) {
+                    const long at = ((t0 + i) * a.H + h) * a.dk + key;
+                    static_cast<TIn *>(a.d_q)[at] = static_cast<TIn>(dQ[I][e]);
+                    static_cast<TIn *>(a.d_k)[at] = static_cast<TIn>(dK[I][e]);
+                }
+            }
+        }
+        __syncthreads();
+        // ---- one lane per row: the log-decay's gradient at row t is the sum
+        // over what crosses it: Gam_C <S, dS'>, the reads of S at rows i >= t,
+        // the writes of rows j < t into S', and the pairs i >= t > j
+        if (tid < C) {
+            const int b = lane >> 4, i = lane & 15;
+            float x = 0.f, y = 0.f, g = 0.f, dbeta = 0.f;
+#pragma unroll
+            for (int n = 0; n < NW; ++n) {
+                x += s.ra[n][lane];
+                y += s.rh[n][lane];
+            }
+            for (int K = 0; K < DKP; K += 64)
+                g += K + lane < DKP ? s.gs[K + lane] : 0.f;
+            g = wave_sum_from<1>(g) * (s.reb[0] * s.reb[1] * s.reb[2] * s.reb[3]);
+            for (int K = 0; K <= b; ++K)
+                x += s.roww[b * (b + 1) / 2 + K][i];
+            for (int K = b; K < 4; ++K) {
+                x -= s.colw[K * (K + 1) / 2 + b][i];
+                dbeta += s.dbeta[K * (K + 1) / 2 + b][i];
+            }
+            float before = y; // sum of the y of the rows up to this one, x from this one on
+#pragma unroll
+            for (int m = 1; m < 64; m *= 2) {
+                const float u = __shfl_up(before, m), v = __shfl_down(x, m);
+                before += lane >= m ? u : 0.f;
+                x += lane + m < 64 ? v : 0.f;
+            }
+            for (int t = 0; t < tiles; ++t)
+                dbeta += a.w_db[(slot_head * tiles + t) * C + lane];
+            if (lane < ch.rows) {
+                const long at = (t0 + lane) * a.H + h;
+                a.d_ld[at] = a.ld[at] < kMinLogDecay ? 0.f : g + (before - y) + x; // below it the decay is held
+                a.d_beta[at] = dbeta;
+            }
+        }
+    } else {
+        // ---- dA, dB; keys and queries scaled within their blocks
+#pragma unroll
+        for (int p = 0; p < TASKS; ++p) {
+            const int b = w + p * NW;
+            if (b >= 10)
+                break;
+            const int I = b < 1 ? 0 : b < 3 ? 1 : b < 6 ? 2 : 3, J = b - I * (I + 1) / 2;
+            const float beta = s.beta[J * 16 + c16];
+            float cm = 0.f;
+            f32x4 A = zero;
             if (DELTA)
-                xa = mfma32x4(ld_z(BI * 16 + r, v), b, xa);
-        }
+                A = reinterpret_cast<const f32x4 *>(ops.mat(2))[b * 64 + lane];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = BI * 16 + k4 + e, j = BJ * 16 + r;
-            s.dA[i * MLD + j] = i > j ? -xa[e] : 0.f;
-            s.dB[i * MLD + j] = i >= j ? xb[e] : 0.f;
+            for (int e = 0; e < 4; ++e) {
+                const int i = I * 16 + r4 + e, j = J * 16 + c16;
+                s.x.dB[i * MLD + j] = i >= j ? beta * xB[p][e] : 0.f;
+                if (DELTA) {
+                    s.x.dA[i * MLD + j] = i > j ? beta * xM[p][e] : 0.f;
+                    cm += i > j ? A[e] * xM[p][e] : 0.f;
+                }
+            }
+            if (DELTA) {
+                cm = wave_sum_from<16>(cm);
+                if (lane < 16)
+                    s.dbeta[b][lane] = cm;
+            }
         }
-    }
-    __syncthreads();
-
-    // rows of I against the rows before: a running decay downwards
-    {
-        float tq[16], tr[16], f = 1.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            tq[i] = tr[i] = 0.f;
-        for (int j = r0 - 1; j >= 0; --j) {
-            const float kj = s.k[j * LD + d] * f;
+        {
+            float p = 1.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                tq[i] = fmaf(s.dB[(r0 + i) * MLD + j], kj, tq[i]);
+                const float before = p;
+                p *= ev[i];
+                s.x.ql[(r0 + i) * LD + d] = qv[i] * (DELTA ? p : before);
                 if (DELTA)
-                    tr[i] = fmaf(s.dA[(r0 + i) * MLD + j], kj, tr[i]);
+                    s.x.kl[(r0 + i) * LD + d] = kv[i] * p;
             }
-            f *= s.e[j * LD + d];
+            p = 1.f;
+#pragma unroll
+            for (int i = 15; i >= 0; --i) {
+                s.x.kr[(r0 + i) * LD + d] = kv[i] * p;
+                p *= ev[i];
+            }
+            float f = 1.f, g = 1.f;
+            for (int K = 0; K < 4; ++K) {
+                f *= K < I0 ? s.eb[K * DKP + d] : 1.f;
+                g *= K > I0 ? s.eb[K * DKP + d] : 1.f;
+            }
+            s.pre[tid] = f;
+            s.suf[tid] = g;
         }
-        float p = 1.f; // prefix in the block
+        __syncthreads();
+        // ---- wave w: keys 16 w.., pairs of rows of different blocks, up to
+        // the reader's prefix (cq, cr) and the read row's suffix (cc)
+        const int key = w * 16 + c16;
+#pragma unroll
+        for (int I = 0; I < 4; ++I) {
+            dQ[I] *= s.pre[I * DKP + key];
+            if (DELTA)
+                dK[I] *= s.pre[I * DKP + key];
+            const f32x4 beta = ld4(&s.beta[I * 16 + r4]);
+            dH[I] *= beta * s.suf[I * DKP + key];
+        }
+        auto column = [&](const float *x, int row, float f) { // four rows of a key
+            f32x4 y;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                y[e] = x[(row + r4 + e) * LD + key] * f;
+            return y;
+        };
+#pragma unroll
+        for (int I = 0; I < 4; ++I) { // what the block's rows write into S'
+            const f32x4 y = dH[I] * column(s.x.kr, I * 16, 1.f);
+            const float x = wave_sum_from<16>((y[0] + y[1]) + (y[2] + y[3]));
+            if (lane < 16)
+                s.kh[I * DKP + key] = x;
+        }
+#pragma unroll
+        for (int I = 1; I < 4; ++I) {
+            float f = 1.f;
+#pragma unroll
+            for (int J = I - 1; J >= 0; --J) {
+                const f32x4 k = column(s.x.kr, J * 16, f);
+                dQ[I] = mfma32x4(ld4(&s.x.dB[(I * 16 + c16) * MLD + J * 16 + r4]), k, dQ[I]);
+                if (DELTA)
+                    dK[I] = mfma32x4(ld4(&s.x.dA[(I * 16 + c16) * MLD + J * 16 + r4]), k, dK[I]);
+                f *= s.eb[J * DKP + key];
+            }
+        }
+#pragma unroll
+        for (int J = 0; J < 3; ++J) {
+            float f = 1.f;
+#pragma unroll
+            for (int I = J + 1; I < 4; ++I) {
+                f32x4 x, y;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[e] = s.x.dB[(I * 16 + r4 + e) * MLD + J * 16 + c16];
+                    if (DELTA)
+                        y[e] = s.x.dA[(I * 16 + r4 + e) * MLD + J * 16 + c16];
+                }
+                dH[J] = mfma32x4(x, column(s.x.ql, I * 16, f), dH[J]);
+                if (DELTA)
+                    dH[J] = mfma32x4(y, column(s.x.kl, I * 16, f), dH[J]);
+                f *= s.eb[I * DKP + key];
+            }
+        }
+        // ---- to one thread per (key, block)
+        float cq[16], cr[16], cc[16], hb[16];
+        auto hand_over = [&](const f32x4 (&x)[4], float (&y)[16]) {
+            __syncthreads(); // what is in kr has been read
+#pragma unroll
+            for (int J = 0; J < 4; ++J)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s.x.kr[(J * 16 + r4 + e) * LD + key] = x[J][e];
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                y[i] = s.x.kr[(r0 + i) * LD + d];
+        };
+        hand_over(dQ, cq);
+        hand_over(dH, cc);
+        if (DELTA)
+            hand_over(dK, cr);
+        {
+            float p = 1.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float before = p;
+                p *= ev[i];
+                cq[i] *= DELTA ? p : before;
+                cr[i] = DELTA ? cr[i] * p : 0.f;
+            }
+            p = 1.f;
+#pragma unroll
+            for (int i = 15; i >= 0; --i) {
+                cc[i] *= p;
+                p *= ev[i];
+            }
+        }
+        // ---- pairs inside the block: hb[j] = P_ij of the row i at hand
+        float gd[16]; // dB_ii
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float before = p;
-            p *= s.e[(r0 + i) * LD + d];
-            cq[i] = (tq[i] + f * cq[i]) * (DELTA ? p : before);
-            cr[i] = DELTA ? (tr[i] + f * cr[i]) * p : 0.f;
-        }
-    }
-    // rows of I against the rows behind: a running decay upwards
-    float kh = 0.f; // sum over the block of k . (its part of dK^)
-    {
-        float tc[16], f = 1.f;
+            f32x4 gb[4], ga[4];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            tc[j] = 0.f;
-        for (int m = r0 + 16; m < C; ++m) {
-            // RWKV6's row m reads the state before its own decay
-            const float qm0 = s.q[m * LD + d] * f;
-            f *= s.e[m * LD + d];
-            const float km = s.k[m * LD + d] * f, qm = DELTA ? s.q[m * LD + d] * f : qm0;
+            for (int q = 0; q < 4; ++q) {
+                if (q * 4 > i)
+                    continue;
+                gb[q] = ld4(&s.x.dB[(r0 + i) * MLD + r0 + q * 4]);
+                if (DELTA)
+                    ga[q] = ld4(&s.x.dA[(r0 + i) * MLD + r0 + q * 4]);
+            }
+            gd[i] = gb[i / 4][i % 4];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                tc[j] = fmaf(s.dB[m * MLD + r0 + j], qm, tc[j]);
-                if (DELTA)
-                    tc[j] = fmaf(s.dA[m * MLD + r0 + j], km, tc[j]);
+                if (j >= i)
+                    continue;
+                const float before = hb[j];
+                hb[j] *= ev[i];
+                const float b = gb[j / 4][j % 4], pq = DELTA ? hb[j] : before;
+                cq[i] = fmaf(b, pq * kv[j], cq[i]);
+                if (DELTA) {
+                    const float x = ga[j / 4][j % 4];
+                    cr[i] = fmaf(x, pq * kv[j], cr[i]);
+                    cc[j] = fmaf(pq, fmaf(b, qv[i], x * kv[i]), cc[j]);
+                } else {
+                    cc[j] = fmaf(pq, b * qv[i], cc[j]);
+                }
             }
+            hb[i] = 1.f;
         }
-        float p = 1.f; // suffix in the block
+        // ---- the log-decay's gradient: with G_i = ell_1 + ... + ell_i, row
+        // i's gradient by G_i is q cq + k cr - k cc (RWKV6's q reads at
+        // G_{i-1}), and G_C's besides that Gam_C sum_v S dS' and the rows'
+        // writes into S', sum_j k_j P_Cj dK^_j; ell_t's is the sum over the
+        // G_i, i >= t.
+        float gsum = 0.f, gl[16]; // suffix sums over the block
 #pragma unroll
-        for (int j = 15; j >= 0; --j) {
-            const float end = f * cc[j] * p;
-            kh = fmaf(s.k[(r0 + j) * LD + d], end, kh);
-            cc[j] = fmaf(tc[j], p, end);
-            p *= s.e[(r0 + j) * LD + d];
-        }
-    }
-    // pairs inside I
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const float kj = s.k[(r0 + j) * LD + d];
-        float p = 1.f;
-#pragma unroll
-        for (int i = j + 1; i < 16; ++i) {
-            const float before = p;
-            p *= s.e[(r0 + i) * LD + d];
-            const float gb = s.dB[(r0 + i) * MLD + r0 + j], qi = s.q[(r0 + i) * LD + d];
-            const float pq = DELTA ? p : before;
-            cq[i] = fmaf(gb * pq, kj, cq[i]);
-            cc[j] = fmaf(gb * pq, qi, cc[j]);
+        for (int i = 15; i >= 0; --i) {
             if (DELTA) {
-                const float ga = s.dA[(r0 + i) * MLD + r0 + j] * p;
-                cr[i] = fmaf(ga, kj, cr[i]);
-                cc[j] = fmaf(ga, s.k[(r0 + i) * LD + d], cc[j]);
+                gsum += qv[i] * cq[i] + kv[i] * (cr[i] - cc[i]);
+                gl[i] = gsum;
+            } else {
+                gsum -= kv[i] * cc[i];
+                gl[i] = gsum;
+                gsum += qv[i] * cq[i];
             }
         }
-    }
-    // The log-decay's gradient: with G_i = ell_1 + ... + ell_i, row i's
-    // gradient by G_i is q cq + k cr - k cc (RWKV6's q reads at G_{i-1}), and
-    // G_C's besides that Gam_C sum_v S dS' + sum_j k_j K^'s part; ell_t's is
-    // the sum over the G_i, i >= t.
-    float gsum = 0.f;
-    float gl[16]; // suffix sums over the block
-#pragma unroll
-    for (int i = 15; i >= 0; --i) {
-        const float qi = s.q[(r0 + i) * LD + d], ki = s.k[(r0 + i) * LD + d];
-        if (DELTA) {
-            gsum += qi * cq[i] + ki * (cr[i] - cc[i]);
-            gl[i] = gsum;
-        } else {
-            gsum -= ki * cc[i];
-            gl[i] = gsum;
-            gsum += qi * cq[i];
-        }
-    }
-    s.part[I * DKP + d] = gsum + kh;
-    float du = 0.f;
-    {
-        // the pairs (i, i), which no decay touches
+        s.part[tid] = gsum;
         const float ud = !DELTA && d < a.dk ? a.u[static_cast<long>(h) * a.dk + d] : 0.f;
+        float du = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float g = s.dB[(r0 + i) * MLD + r0 + i];
-            const float qi = s.q[(r0 + i) * LD + d], ki = s.k[(r0 + i) * LD + d];
-            const float f = DELTA ? g : g * ud;
-            const float oq = fmaf(f, ki, cq[i]), ok = fmaf(f, qi, cr[i] + cc[i]);
-            du = fmaf(g * qi, ki, du);
+            // the pairs (i, i), which no decay touches
+            const float f = DELTA ? gd[i] : gd[i] * ud;
+            const float oq = fmaf(f, kv[i], cq[i]), ok = fmaf(f, qv[i], cr[i] + cc[i]);
+            du = fmaf(gd[i] * qv[i], kv[i], du);
             if (r0 + i < ch.rows && d < a.dk) {
-                const long at = ((static_cast<long>(ch.t0) + r0 + i) * a.H + h) * a.dk + d;
+                const long at = ((t0 + r0 + i) * a.H + h) * a.dk + d;
                 static_cast<TIn *>(a.d_q)[at] = static_cast<TIn>(oq);
                 static_cast<TIn *>(a.d_k)[at] = static_cast<TIn>(ok);
             }
         }
-    }
-    __syncthreads();
-    {
-        // behind block I: the sums of the later blocks, every block's share
-        // of K^ (those up to I count at G_C), and Gam_C
-        float tail = 0.f, all = 1.f;
-        for (int J = I + 1; J < 4; ++J)
-            tail += s.part[J * DKP + d];
-        for (int i = 0; i < C; ++i)
-            all *= s.e[i * LD + d];
         __syncthreads();
-        s.part[I * DKP + d] = kh;
-        __syncthreads();
-        for (int J = 0; J <= I; ++J)
-            tail += s.part[J * DKP + d];
-        tail = fmaf(all, s.gam[d], tail);
+        {
+            // behind block I0: the later blocks' sums, and what counts at G_C
+            float tail = s.pre[3 * DKP + d] * s.eb[3 * DKP + d] * s.gs[d];
+            for (int K = 0; K < 4; ++K)
+                tail += s.kh[K * DKP + d] + (K > I0 ? s.part[K * DKP + d] : 0.f);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            gl[i] += tail;
-    }
-    if constexpr (OP != GDN) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (r0 + i < ch.rows && d < a.dk) {
-                const long at = ((static_cast<long>(ch.t0) + r0 + i) * a.H + h) * a.dk + d;
-                a.d_ld[at] = a.ld[at] < kMinLogDecay ? 0.f : gl[i]; // below it the decay is held
-            }
-    } else {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            s.e[(r0 + i) * LD + d] = d < a.dk ? gl[i] : 0.f;
-        __syncthreads();
-        for (int i = w; i < ch.rows; i += NW) {
-            float x = 0.f;
-            for (int c = lane; c < DKP; c += 64)
-                x += s.e[i * LD + c];
-            x = wave_sum_from<1>(x);
-            const long at = (static_cast<long>(ch.t0) + i) * a.H + h;
-            if (lane == 0)
-                a.d_ld[at] = a.ld[at] < kMinLogDecay ? 0.f : x;
+            for (int i = 0; i < 16; ++i)
+                if (r0 + i < ch.rows && d < a.dk) {
+                    const long at = ((t0 + r0 + i) * a.H + h) * a.dk + d;
+                    a.d_ld[at] = a.ld[at] < kMinLogDecay ? 0.f : gl[i] + tail; // below it the decay is held
+                }
         }
-    }
-    if constexpr (!DELTA) {
-        __syncthreads();
-        s.part[I * DKP + d] = du;
-        __syncthreads();
-        if (tid < a.dk)
-            a.w_du[slot_head * a.dk + tid] =
-                s.part[tid] + s.part[DKP + tid] + s.part[2 * DKP + tid] + s.part[3 * DKP + tid];
-    }
-    if (DELTA && tid < ch.rows) {
-        const int tiles = a.dv / 16;
-        float x = 0.f;
-        for (int t = 0; t < tiles; ++t)
-            x += a.w_db[(slot_head * tiles + t) * C + tid];
-        a.d_beta[(static_cast<long>(ch.t0) + tid) * a.H + h] = x;
+        if constexpr (!DELTA) {
+            __syncthreads();
+            s.part[tid] = du;
+            __syncthreads();
+            if (tid < a.dk)
+                a.w_du[slot_head * a.dk + tid] =
+                    s.part[tid] + s.part[DKP + tid] + s.part[2 * DKP + tid] + s.part[3 * DKP + tid];
+        } else if (tid < C) {
+            const int b = lane >> 4, i = lane & 15;
+            float dbeta = 0.f;
+            for (int K = b; K < 4; ++K)
+                dbeta += s.dbeta[K * (K + 1) / 2 + b][i];
+            for (int t = 0; t < tiles; ++t)
+                dbeta += a.w_db[(slot_head * tiles + t) * C + lane];
+            if (lane < ch.rows)
+                a.d_beta[(t0 + lane) * a.H + h] = dbeta;
+        }
     }
 }
 
@@ -334,6 +669,5 @@ __global__ inline __launch_bounds__(256) void scan_du_kernel(ScanArgs a)
         x += a.w_du[static_cast<long>(s) * n + i];
     a.d_u[i] = x;
 }
-
 
 } // namespace dl

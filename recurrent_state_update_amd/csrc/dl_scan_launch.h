@@ -48,9 +48,9 @@ template <int OP, typename TIn, int DKP> hipError_t scan_forward_t(const ScanArg
     if (hipError_t e = launch_prep<OP, TIn, DKP, false>(a, st); e != hipSuccess)
         return e;
     if (a.save_s)
-        hipLaunchKernelGGL((scan_carry_kernel<OP, TIn, DKP, 1, true>), carry_grid(a, 1), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((scan_carry_kernel<OP, TIn, DKP, 1, true>), carry_grid(a, 1), dim3(512), 0, st, a);
     else
-        hipLaunchKernelGGL((scan_carry_kernel<OP, TIn, DKP, 1, false>), carry_grid(a, 1), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((scan_carry_kernel<OP, TIn, DKP, 1, false>), carry_grid(a, 1), dim3(512), 0, st, a);
     return hipGetLastError();
 }
 
@@ -58,13 +58,17 @@ template <int OP, typename TIn, int DKP> hipError_t scan_backward_t(const ScanAr
 {
     if (hipError_t e = launch_prep<OP, TIn, DKP, true>(a, st); e != hipSuccess)
         return e;
-    hipLaunchKernelGGL((scan_carry_bwd_kernel<OP, TIn, DKP, 1>), carry_grid(a, 1), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((scan_carry_bwd_kernel<OP, TIn, DKP, 1>), carry_grid(a, 1), dim3(512), 0, st, a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess)
         return e;
+    const bool vec = at16(a.q) && at16(a.k) && at16(a.v) && at16(a.d_o) && a.qs % 8 == 0 && a.ks % 8 == 0 &&
+                     a.vs % 8 == 0;
+    using Lds = GradLds<OP, TIn, DKP>;
+    static_assert(sizeof(Lds) <= 160 * 1024, "a CU's LDS");
     auto *grads = scan_grads_kernel<OP, TIn, DKP>;
-    if (hipError_t e = set_lds(grads, sizeof(GradLds<DKP>)); e != hipSuccess)
+    if (hipError_t e = set_lds(grads, sizeof(Lds)); e != hipSuccess)
         return e;
-    hipLaunchKernelGGL(grads, dim3(a.slots * a.H), dim3(DKP * 4), sizeof(GradLds<DKP>), st, a);
+    hipLaunchKernelGGL(grads, dim3(a.slots * a.H), dim3(DKP * 4), sizeof(Lds), st, a, vec, a.dv / 16);
     if (hipError_t e = hipGetLastError(); e != hipSuccess)
         return e;
     if (OP == RWKV6) {

@@ -24,6 +24,22 @@ template <typename TIn> __device__ __forceinline__ void load_piece(TIn (&x)[8], 
     }
 }
 
+// A (and B) in fp32 for grads: the ten blocks of the lower triangle, a lane's
+// four rows of its column as in a product's result.
+__device__ __forceinline__ void store_pairs(__bf16 *mat, const float *A, const float *B, int n)
+{
+    for (int it = threadIdx.x; it < n * 640; it += blockDim.x) {
+        const int l = it & 63, b = (it >> 6) % 10;
+        const float *x = it < 640 ? A : B;
+        const int I = b < 1 ? 0 : b < 3 ? 1 : b < 6 ? 2 : 3, J = b - I * (I + 1) / 2;
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v[e] = x[(I * 16 + (l >> 4) * 4 + e) * MLD + J * 16 + (l & 15)];
+        reinterpret_cast<f32x4 *>(mat)[it] = v;
+    }
+}
+
 template <int OP, int DKP> struct PrepLds {
     static constexpr int LD = DKP + 4;
     float k[C * LD], q[C * LD], e[C * LD];
@@ -254,7 +270,7 @@ __global__ __launch_bounds__(prep_threads<DKP>()) void scan_prep_kernel(ScanArgs
             store_op<P::NPX, DKP, C>(ops.op(2), [&](int d, int i) { return kt(i, d); });
         store_op<3, C, C, UPPER>(ops.mat(1), [&](int i, int j) { return s.B[j * MLD + i]; });
         if (DELTA)
-            store_op<3, C, C, UPPER>(ops.mat(2), [&](int i, int j) { return s.A[j * MLD + i]; });
+            store_pairs(ops.mat(2), s.A, s.A, 1);
     }
     if (tid < C)
         ops.row(2)[tid] = s.beta[tid];
@@ -440,7 +456,7 @@ __global__ __launch_bounds__(256) void scan_prep_gdn_kernel(ScanArgs a, bool vec
         columns(std::integral_constant<int, NP>(), ops.op(1), s.q);
         columns(std::integral_constant<int, NP>(), ops.op(2), s.k);
         store_op<3, C, C, UPPER>(ops.mat(1), [&](int i, int j) { return s.N[j * MLD + i]; });
-        store_op<3, C, C, UPPER>(ops.mat(2), [&](int i, int j) { return s.A[j * MLD + i]; });
+        store_pairs(ops.mat(2), s.A, s.N, 2);
     }
     __syncthreads();
     for (int it = tid; it < C * C; it += 256) {

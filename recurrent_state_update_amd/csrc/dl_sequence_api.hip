@@ -88,7 +88,7 @@ dl_status scan_inputs(const dl_scan_desc *d, dl::ScanArgs &a, Span (&r)[7])
     const long long kw = static_cast<long long>(d->H) * d->d_k, vw = static_cast<long long>(d->H) * d->d_v;
     const long long qs = d->q_stride ? d->q_stride : kw, ks = d->k_stride ? d->k_stride : kw,
                     vs = d->v_stride ? d->v_stride : vw;
-    if (qs < kw || ks < kw || vs < vw)
+    if (qs < kw || ks < kw || vs < vw || qs > 0x7fffffff || ks > 0x7fffffff || vs > 0x7fffffff)
         return DL_E_INVALID;
     const size_t es = elem(d->in_dtype), T = d->tokens, last = any ? T - 1 : 0;
     if (!aligned(d->q, es) || !aligned(d->k, es) || !aligned(d->v, es) || !aligned(d->beta, 4) ||
