@@ -87,16 +87,34 @@ __device__ __forceinline__ f32x4 mma(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB
                 c = mfma16(a[i], b[s - i], c);
     return c;
 }
-// The first N planes of x (a sum of bf16 roundings).
+// x as a sum of N bf16 values, each the rounding of what is left: the planes of
+// an fp32 factor (three hold its 24 bits).  In pairs: one conversion packs
+// two values, whose fp32 forms are its halves.
 template <int N, typename V, typename F> __device__ __forceinline__ void split(F x, V (&p)[N])
 {
+    using f32x2 = float __attribute__((ext_vector_type(2)));
+    using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
+    constexpr int E = sizeof(F) / 4;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        p[i] = __builtin_convertvector(x, V);
-        if (i + 1 < N)
-            x = x - __builtin_convertvector(p[i], F);
+    for (int e = 0; e < E; e += 2) {
+        float u = x[e], v = x[e + 1];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const bf16x2 b = __builtin_convertvector((f32x2{u, v}), bf16x2);
+            p[i][e] = b[0];
+            p[i][e + 1] = b[1];
+            if (i + 1 < N) {
+                const unsigned raw = __builtin_bit_cast(unsigned, b);
+                u -= __uint_as_float(raw << 16);
+                v -= __uint_as_float(raw & 0xffff0000u);
+            }
+        }
     }
 }
+// Keeps the loads before it ahead of those behind it.  The counter that a wait
+// for a load compares counts in order, and where the loads ahead of a loop come
+// in another order than at its end, every wait in it is for the worse of both.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
 
 // How an operator with inputs of a type runs.
 template <int OP, typename TIn> struct Plan {

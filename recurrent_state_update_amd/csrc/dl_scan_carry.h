@@ -120,28 +120,33 @@ template <int DKP> struct Holder {
     }
 };
 
-// Rows i0..i0+3 (of those before `len`, the last one again behind it) of one
-// sequence's matrix of inputs, columns v0 + 16 x.
-template <typename TIn, int NC>
-__device__ __forceinline__ void load_col(TIn (&v)[NC][4], const TIn *p, int i0, int len, unsigned stride)
-{
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const unsigned i = i0 + e < len ? i0 + e : len - 1;
-        const TIn *r = p + static_cast<unsigned long>(i) * stride;
-#pragma unroll
-        for (int x = 0; x < NC; ++x)
-            v[x][e] = r[16 * x];
+// Rows of one chunk of a matrix of inputs, as a buffer of the rows that there
+// are: a load behind the end gives zero, a store there is dropped, so both
+// stay unconditional (and countable by the waits).
+template <typename TIn> struct ChunkRows {
+    rsrc_t r;
+    // p: row 0 of the sequence at the workgroup's first column
+    __device__ __forceinline__ ChunkRows(const TIn *p, unsigned stride, int c, int len, int width)
+        : r(make_rsrc(p + static_cast<long>(c) * C * stride,
+                      static_cast<unsigned>((((len - c * C < C ? len - c * C : C) - 1) * stride + width) * sizeof(TIn))))
+    {
     }
-}
-template <typename TIn> __device__ __forceinline__ f32x4 rows_of(const TIn (&v)[4], int i0, int rows)
-{
-    f32x4 x;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) // rows behind the end: zero
-        x[e] = i0 + e < rows ? from_in(v[e]) : 0.f;
-    return x;
-}
+    __device__ __forceinline__ TIn load(unsigned at) const
+    {
+        if constexpr (sizeof(TIn) == 2)
+            return __builtin_bit_cast(TIn, __builtin_amdgcn_raw_buffer_load_b16(r, at * 2u, 0, 0));
+        else
+            return __builtin_bit_cast(TIn, __builtin_amdgcn_raw_buffer_load_b32(r, at * 4u, 0, 0));
+    }
+    __device__ __forceinline__ void store(unsigned at, float x) const
+    {
+        const TIn v = static_cast<TIn>(x);
+        if constexpr (sizeof(TIn) == 2)
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v), r, at * 2u, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), r, at * 4u, 0, 0);
+    }
+};
 
 // Forward.  SAVE: keeps every chunk's start state and E.
 template <int OP, typename TIn, int DKP, int NC, bool SAVE>
@@ -163,6 +168,8 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
     const int h = wk.group % a.H, n = wk.group / a.H;
     const Seq sq = sequence(a, n);
     const int v0 = wk.tile * 16 * NC + col;
+    const long first = static_cast<long>(h) * a.dv + wk.tile * 16 * NC; // of a row, this workgroup's
+    const unsigned width = a.H * a.dv;
     const long row = state_row(a, n);
     const long st0 = (row * a.H + h) * a.dk * a.dv + v0;
     const int chunks = (sq.len + C - 1) / C;
@@ -187,7 +194,7 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int d = own.rb * 16 + r4 + e;
-                    if (d < a.dk)
+                    if (DKP > 32 || d < a.dk)
                         a.save_s[(sh * a.dk + d) * a.dv + v0 + 16 * t] = S[t][e];
                 }
             }
@@ -214,14 +221,19 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
     put_state(0);
 
     if (chunks > 0) {
-        load_t(0);
         if (w < 4) {
             bf16x8 kf[KS][P::NPX], nf[2][3];
             f32x4 gi, ge, beta;
             TIn v[NC][4];
-            const TIn *vp = static_cast<const TIn *>(a.v) + static_cast<long>(sq.start) * a.vs +
-                            static_cast<long>(h) * a.dv + v0;
-            auto load_v = [&](int c) { load_col(v, vp, c * C + i0, sq.len, static_cast<unsigned>(a.vs)); };
+            const TIn *vp = static_cast<const TIn *>(a.v) + static_cast<long>(sq.start) * a.vs + first;
+            auto load_v = [&](int c) {
+                const ChunkRows<TIn> rows(vp, static_cast<unsigned>(a.vs), c, sq.len, 16 * NC);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int t = 0; t < NC; ++t)
+                        v[t][e] = rows.load((i0 + e) * static_cast<unsigned>(a.vs) + col + 16 * t);
+            };
             auto load_k = [&](int c) {
                 if (DELTA)
                     load_rows(kf, ops(c).op(0), w, lane);
@@ -237,14 +249,19 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
                     ge = ld4(ops(c).row(1) + i0);
             };
             load_v(0);
+            keep_order();
             load_k(0);
+            keep_order();
             load_n(0);
+            keep_order();
+            load_t(0);
+            keep_order();
             for (int c = 0; c < chunks; ++c) {
                 const int next = c + 1 < chunks ? c + 1 : c;
                 f32x4 x[NC];
 #pragma unroll
                 for (int t = 0; t < NC; ++t)
-                    x[t] = rows_of(v[t], c * C + i0, sq.len);
+                    x[t] = f32x4{from_in(v[t][0]), from_in(v[t][1]), from_in(v[t][2]), from_in(v[t][3])};
                 load_v(next);
                 __syncthreads(); // the state's planes are complete
                 if constexpr (DELTA) {
@@ -292,22 +309,24 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
             };
             auto load_b = [&](int c) { load_tri(bf, ops(c).mat(1), LOWER, wb, lane); };
             // o of chunk c, `last` being its Q~ S
+            TIn *op = static_cast<TIn *>(a.o) + static_cast<long>(sq.start) * a.H * a.dv + first;
             auto finish = [&](int c, int next) {
+                const ChunkRows<TIn> rows(op, width, c, sq.len, 16 * NC);
 #pragma unroll
                 for (int t = 0; t < NC; ++t) {
                     last[t] = product_tri<P::ORDER_O>(bf, bp[c & 1][t], true, wb >= 2, lane, last[t]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int i = c * C + i0 + e;
-                        if (i < sq.len)
-                            static_cast<TIn *>(a.o)[((sq.start + static_cast<long>(i)) * a.H + h) * a.dv + v0 + 16 * t] =
-                                static_cast<TIn>(last[t][e]);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        rows.store((i0 + e) * width + col + 16 * t, last[t][e]);
                 }
                 load_b(next);
             };
             load_q(0);
+            keep_order();
             load_b(0);
+            keep_order();
+            load_t(0);
+            keep_order();
             for (int c = 0; c < chunks; ++c) {
                 const int next = c + 1 < chunks ? c + 1 : c;
                 __syncthreads();
@@ -320,9 +339,9 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
                 load_q(next);
                 if constexpr (DELTA)
                     __syncthreads();
-                // the chunk before is finished while the chain computes b
-                if (c > 0)
-                    finish(c - 1, c);
+                // the chunk before is finished while the chain computes b; the
+                // first turn has none (what it writes is written again)
+                finish(c > 0 ? c - 1 : 0, c);
                 __syncthreads();
 #pragma unroll
                 for (int t = 0; t < NC; ++t)
@@ -369,6 +388,8 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
     const int h = wk.group % a.H, n = wk.group / a.H;
     const Seq sq = sequence(a, n);
     const int v0 = wk.tile * 16 * NC + col;
+    const long first = static_cast<long>(h) * a.dv + wk.tile * 16 * NC; // of a row, this workgroup's
+    const unsigned width = a.H * a.dv;
     const long st0 = (static_cast<long>(n) * a.H + h) * a.dk * a.dv + v0;
     const int chunks = (sq.len + C - 1) / C;
     const Holder<DKP> own(w);
@@ -394,7 +415,7 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int d = own.rb * 16 + r4 + e;
-                    if (d < a.dk)
+                    if (DKP > 32 || d < a.dk)
                         a.w_ds[(sh * a.dk + d) * a.dv + v0 + 16 * t] = S[t][e];
                 }
             }
@@ -433,11 +454,11 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
     put_state(chunks - 1);
 
     if (chunks > 0) {
-        load_t(chunks - 1);
         if (w < 4) {
             bf16x8 kf[KS][P::NPX], bt[2][3], nt[2][3];
             f32x4 gi, ge, beta;
             float E[NC][4];
+            TIn *dvp = static_cast<TIn *>(a.d_v) + static_cast<long>(sq.start) * a.H * a.dv + first;
             auto load_db = [&](int c) {
                 load_tri(bt, ops(c).mat(1), UPPER, w, lane);
                 load_rows(kf, ops(c).op(0), w, lane);
@@ -462,8 +483,13 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
                         E[t][e] = a.save_e[((static_cast<long>(sq.base + c) * a.H + h) * C + i0 + e) * a.dv + v0 + 16 * t];
             };
             load_db(chunks - 1);
+            keep_order();
             load_n(chunks - 1);
+            keep_order();
+            load_t(chunks - 1);
+            keep_order();
             load_e(chunks - 1);
+            keep_order();
             for (int c = chunks - 1; c >= 0; --c) {
                 const int next = c > 0 ? c - 1 : 0;
                 const long sh = static_cast<long>(sq.base + c) * a.H + h;
@@ -493,14 +519,12 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
                 if constexpr (DELTA)
                     __syncthreads(); // z is complete
                 rest(c, next);
+                const ChunkRows<TIn> rows(dvp, width, c, sq.len, 16 * NC);
 #pragma unroll
                 for (int t = 0; t < NC; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int i = c * C + i0 + e;
-                        if (i < sq.len)
-                            static_cast<TIn *>(a.d_v)[((sq.start + static_cast<long>(i)) * a.H + h) * a.dv + v0 + 16 * t] =
-                                static_cast<TIn>(x[t][e]);
+                        rows.store((i0 + e) * width + col + 16 * t, x[t][e]);
                         if (DELTA)
                             a.w_z[(sh * C + i0 + e) * a.dv + v0 + 16 * t] = x[t][e];
                     }
@@ -527,18 +551,23 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
             // brings dO to LDS, a chunk ahead
             f32x4 gi;
             TIn g[NC][4];
-            const TIn *gbase = a.d_o ? static_cast<const TIn *>(a.d_o) + (static_cast<long>(sq.start) * a.H + h) * a.dv + v0
-                                     : nullptr;
+            const TIn *gbase = static_cast<const TIn *>(a.d_o) + static_cast<long>(sq.start) * a.H * a.dv + first;
             auto load_g = [&](int c) {
-                if (a.d_o)
-                    load_col(g, gbase, c * C + i0, sq.len, static_cast<unsigned>(a.H * a.dv));
+                if (a.d_o) {
+                    const ChunkRows<TIn> rows(gbase, width, c, sq.len, 16 * NC);
+#pragma unroll
+                    for (int t = 0; t < NC; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            g[t][e] = rows.load((i0 + e) * width + col + 16 * t);
+                }
                 if (ROWS)
                     gi = ld4(ops(c).row(0) + i0);
             };
             auto put_g = [&](int c) {
 #pragma unroll
                 for (int t = 0; t < NC; ++t) {
-                    const f32x4 x = a.d_o ? rows_of(g[t], c * C + i0, sq.len) : zero;
+                    const f32x4 x = a.d_o ? f32x4{from_in(g[t][0]), from_in(g[t][1]), from_in(g[t][2]), from_in(g[t][3])} : zero;
                     gp[c & 1][t].put(col, i0, x);
                     if (ROWS)
                         gg[c & 1][t].put(col, i0, x * gi);
@@ -546,7 +575,11 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
             };
             load_g(chunks - 1);
             put_g(chunks - 1);
+            keep_order();
             load_g(chunks > 1 ? chunks - 2 : 0);
+            keep_order();
+            load_t(chunks - 1);
+            keep_order();
             for (int c = chunks - 1; c >= 0; --c) {
                 const int next = c > 0 ? c - 1 : 0;
                 __syncthreads();

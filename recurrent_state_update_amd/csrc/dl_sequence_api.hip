@@ -42,6 +42,7 @@ template <int NW, int NR> bool clash(const Span (&w)[NW], const Span (&r)[NR])
 
 // Launches count work-items in 32 bits: at most 512 per chunk and head, and
 // 16 d_v per sequence and head.
+constexpr long long kMostStride = 1LL << 22;
 constexpr long kMostSlotHeads = 1L << 22, kMostSeqHeads = 1L << 20;
 
 dl_status check_sizes(const dl_scan_desc *d)
@@ -88,8 +89,11 @@ dl_status scan_inputs(const dl_scan_desc *d, dl::ScanArgs &a, Span (&r)[7])
     const long long kw = static_cast<long long>(d->H) * d->d_k, vw = static_cast<long long>(d->H) * d->d_v;
     const long long qs = d->q_stride ? d->q_stride : kw, ks = d->k_stride ? d->k_stride : kw,
                     vs = d->v_stride ? d->v_stride : vw;
-    if (qs < kw || ks < kw || vs < vw || qs > 0x7fffffff || ks > 0x7fffffff || vs > 0x7fffffff)
+    if (qs < kw || ks < kw || vs < vw)
         return DL_E_INVALID;
+    // a chunk's rows are addressed in 32 bits
+    if (qs > kMostStride || ks > kMostStride || vs > kMostStride)
+        return DL_E_SHAPE;
     const size_t es = elem(d->in_dtype), T = d->tokens, last = any ? T - 1 : 0;
     if (!aligned(d->q, es) || !aligned(d->k, es) || !aligned(d->v, es) || !aligned(d->beta, 4) ||
         !aligned(d->log_decay, 4) || !aligned(d->u, 4) || !aligned(d->cu_seqlens, 4))
