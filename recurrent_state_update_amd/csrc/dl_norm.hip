@@ -14,6 +14,8 @@ namespace dl {
 
 namespace {
 
+constexpr long kForwardBlocks = 2048; // eight per CU: every wave slot, several turns each
+
 template <typename T> __device__ __forceinline__ float to_f(T x) { return static_cast<float>(x); }
 
 // N consecutive elements from p, as floats (and back).  ALIGNED: p is aligned
@@ -68,28 +70,46 @@ template <int G> __device__ __forceinline__ float group_sum(float x)
 // --------------------------------------------------------------- gated norm --
 
 // A unit is one head of one row; G = d / 8 lanes hold it, eight columns each.
+// A workgroup takes every gridDim.x-th group of units (the weight is loaded
+// once), and loads a turn ahead of the sum that the stores wait for.
 template <typename TO, typename T, int D, bool ALIGNED>
 __global__ __launch_bounds__(256) void gated_norm_kernel(GatedNormArgs a)
 {
     constexpr int G = D / 8;
-    const long u = (static_cast<long>(blockIdx.x) * 256 + threadIdx.x) / G;
     const int c = threadIdx.x % G * 8;
+    const long step = static_cast<long>(gridDim.x) * (256 / G);
+    long u = (static_cast<long>(blockIdx.x) * 256 + threadIdx.x) / G;
     if (u >= a.units) // whole groups
         return;
-    float o[8], g[8], w[8];
-    load<8, ALIGNED>(o, static_cast<const TO *>(a.o) + u * D + c);
-    load<8, ALIGNED>(g, static_cast<const T *>(a.gate) + u / a.H * a.gate_stride + u % a.H * D + c);
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        w[i] = a.weight ? a.weight[c + i] : 1.f;
-        ss = fmaf(o[i], o[i], ss);
-    }
-    const float r = 1.f / sqrtf(group_sum<G>(ss) / D + a.eps);
+    float w[8], o[8], g[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        o[i] = o[i] * r * w[i] * (g[i] / (1.f + expf(-g[i])));
-    store<8, ALIGNED>(static_cast<T *>(a.y) + u * D + c, o);
+        w[i] = a.weight ? a.weight[c + i] : 1.f;
+    const auto read = [&](long v) {
+        load<8, ALIGNED>(o, static_cast<const TO *>(a.o) + v * D + c);
+        load<8, ALIGNED>(g, static_cast<const T *>(a.gate) + v / a.H * a.gate_stride + v % a.H * D + c);
+    };
+    read(u);
+    for (;;) {
+        float y[8], z[8], ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            y[i] = o[i];
+            z[i] = g[i];
+            ss = fmaf(y[i], y[i], ss);
+        }
+        const long next = u + step;
+        if (next < a.units)
+            read(next);
+        const float r = 1.f / sqrtf(group_sum<G>(ss) / D + a.eps);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            y[i] = y[i] * r * w[i] * (z[i] / (1.f + expf(-z[i])));
+        store<8, ALIGNED>(static_cast<T *>(a.y) + u * D + c, y);
+        if (next >= a.units)
+            return;
+        u = next;
+    }
 }
 
 // With n = rms(o), sig = sigmoid(g): dn = dy w g sig,
@@ -151,28 +171,45 @@ __global__ __launch_bounds__(256) void gated_norm_bwd_kernel(GatedNormArgs a)
     }
 }
 
-// out[j] = the sum over the blocks' rows of partial [blocks][n].  A workgroup
-// takes 32 columns; eight threads per column take every eighth row.
-__global__ __launch_bounds__(256) void column_sum_kernel(const float *partial, int blocks, int n, float *out)
+// out[j] = the sum over the blocks' rows of partial [blocks][n] (blockIdx.y:
+// the second such pair).  A workgroup takes 16 columns; 16 threads per column
+// take every 16th row, eight loads at a time.
+__global__ __launch_bounds__(256) void column_sum_kernel(const float *partial, int blocks, int n, float *out0,
+                                                         float *out1)
 {
-    __shared__ float part[8][33];
-    const int c = threadIdx.x % 32, s = threadIdx.x / 32, j = blockIdx.x * 32 + c;
+    __shared__ float part[16][17];
+    const int c = threadIdx.x % 16, s = threadIdx.x / 16, j = blockIdx.x * 16 + c;
+    partial += static_cast<long>(blockIdx.y) * blocks * n;
+    float *out = blockIdx.y ? out1 : out0;
     float x = 0.f;
-    if (j < n)
-        for (int b = s; b < blocks; b += 8)
+    if (j < n) {
+        int b = s;
+        for (; b + 7 * 16 < blocks; b += 8 * 16) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = partial[static_cast<long>(b + 16 * i) * n + j];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x += v[i];
+        }
+        for (; b < blocks; b += 16)
             x += partial[static_cast<long>(b) * n + j];
+    }
     part[s][c] = x;
     __syncthreads();
     if (s == 0 && j < n) {
-        for (int t = 1; t < 8; ++t)
+        for (int t = 1; t < 16; ++t)
             x += part[t][c];
         out[j] = x;
     }
 }
 
-hipError_t column_sum(const float *partial, int blocks, int n, float *out, hipStream_t st)
+// Sums of one [blocks][n] or, with out1, of two that follow each other.
+hipError_t column_sum(const float *partial, int blocks, int n, float *out0, float *out1, hipStream_t st)
 {
-    hipLaunchKernelGGL(column_sum_kernel, dim3((n + 31) / 32), dim3(256), 0, st, partial, blocks, n, out);
+    hipLaunchKernelGGL(column_sum_kernel, dim3((n + 15) / 16, out1 ? 2 : 1), dim3(256), 0, st, partial, blocks, n, out0,
+                       out1);
     return hipGetLastError();
 }
 
@@ -180,9 +217,10 @@ template <typename TO, typename T, int D>
 hipError_t gated_norm_t(bool aligned, bool backward, const GatedNormArgs &a, hipStream_t st)
 {
     if (!backward) {
-        const long blocks = (a.units * (D / 8) + 255) / 256;
-        if (blocks == 0)
+        const long groups = (a.units * (D / 8) + 255) / 256;
+        if (groups == 0)
             return hipSuccess;
+        const long blocks = groups < kForwardBlocks ? groups : kForwardBlocks;
         if (aligned)
             hipLaunchKernelGGL((gated_norm_kernel<TO, T, D, true>), dim3(blocks), dim3(256), 0, st, a);
         else
@@ -195,7 +233,7 @@ hipError_t gated_norm_t(bool aligned, bool backward, const GatedNormArgs &a, hip
         hipLaunchKernelGGL((gated_norm_bwd_kernel<TO, T, D, false>), dim3(a.blocks), dim3(256), 0, st, a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess || !a.d_weight)
         return e;
-    return column_sum(a.partial, a.blocks, D, a.d_weight, st);
+    return column_sum(a.partial, a.blocks, D, a.d_weight, nullptr, st);
 }
 
 template <typename TO, typename T>
@@ -213,8 +251,9 @@ bool at16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // ------------------------------------------------------------ residual norm --
 
-// NT threads per row, E x 8 columns each: VEC = 8 consecutive ones at a time
-// where every row starts on a 16-byte boundary, else single ones.
+// NT threads per row, E x 8 columns each: VEC = 4 consecutive ones at a time
+// (a wave's fp32 load is then one contiguous KiB) where every row starts on a
+// boundary of four elements, else single ones.
 template <int NT, int VEC, int E> struct Cols {
     static constexpr int K = E * 8 / VEC;
     static __device__ __forceinline__ int col(int k) { return (k * NT + static_cast<int>(threadIdx.x)) * VEC; }
@@ -236,49 +275,56 @@ template <int NT> __device__ __forceinline__ float row_sum(float x, float *part)
     return x;
 }
 
+// A workgroup takes every gridDim.x-th row; loads run a row ahead.
 template <typename T, int NT, int VEC, int E>
 __global__ __launch_bounds__(NT) void residual_norm_kernel(ResidualNormArgs a)
 {
     using L = Cols<NT, VEC, E>;
     __shared__ float part[NT / 64];
-    const long at = static_cast<long>(blockIdx.x) * a.D;
-    float x[L::K][VEC], ss = 0.f;
-#pragma unroll
-    for (int k = 0; k < L::K; ++k) {
-        const int c = L::col(k);
-        if (c < a.D)
-            load<VEC, true>(x[k], a.x + at + c);
-    }
-    if (a.y) {
+    float xn[L::K][VEC], yn[L::K][VEC];
+    const auto read = [&](long row) {
 #pragma unroll
         for (int k = 0; k < L::K; ++k) {
             const int c = L::col(k);
             if (c >= a.D)
                 continue;
-            float y[VEC];
-            load<VEC, true>(y, static_cast<const T *>(a.y) + at + c);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                x[k][i] += a.scale ? y[i] * a.scale[c + i] : y[i];
-            store<VEC, true>(a.x_out + at + c, x[k]);
+            load<VEC, true>(xn[k], a.x + row * a.D + c);
+            if (a.y)
+                load<VEC, true>(yn[k], static_cast<const T *>(a.y) + row * a.D + c);
         }
-    }
+    };
+    read(blockIdx.x);
+    for (long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const long at = row * a.D;
+        float x[L::K][VEC], ss = 0.f;
 #pragma unroll
-    for (int k = 0; k < L::K; ++k)
-        if (L::col(k) < a.D)
+        for (int k = 0; k < L::K; ++k) {
+            const int c = L::col(k);
+            if (c >= a.D)
+                continue;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                x[k][i] = xn[k][i];
+                if (a.y)
+                    x[k][i] += a.scale ? yn[k][i] * a.scale[c + i] : yn[k][i];
+                ss = fmaf(x[k][i], x[k][i], ss);
+            }
+            if (a.y)
+                store<VEC, true>(a.x_out + at + c, x[k]);
+        }
+        if (row + gridDim.x < a.rows)
+            read(row + gridDim.x);
+        const float r = 1.f / sqrtf(row_sum<NT>(ss, part) / a.D + a.eps);
+#pragma unroll
+        for (int k = 0; k < L::K; ++k) {
+            const int c = L::col(k);
+            if (c >= a.D)
+                continue;
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
-                ss = fmaf(x[k][i], x[k][i], ss);
-    const float r = 1.f / sqrtf(row_sum<NT>(ss, part) / a.D + a.eps);
-#pragma unroll
-    for (int k = 0; k < L::K; ++k) {
-        const int c = L::col(k);
-        if (c >= a.D)
-            continue;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            x[k][i] *= a.weight ? r * a.weight[c + i] : r;
-        store<VEC, true>(static_cast<T *>(a.h) + at + c, x[k]);
+                x[k][i] *= a.weight ? r * a.weight[c + i] : r;
+            store<VEC, true>(static_cast<T *>(a.h) + at + c, x[k]);
+        }
     }
 }
 
@@ -381,15 +427,14 @@ hipError_t residual_norm_t(bool backward, const ResidualNormArgs &a, hipStream_t
     if (!backward) {
         if (a.rows == 0)
             return hipSuccess;
-        hipLaunchKernelGGL((residual_norm_kernel<T, NT, VEC, E>), dim3(a.rows), dim3(NT), 0, st, a);
+        hipLaunchKernelGGL((residual_norm_kernel<T, NT, VEC, E>), dim3(a.rows < kForwardBlocks ? a.rows : kForwardBlocks),
+                           dim3(NT), 0, st, a);
         return hipGetLastError();
     }
     hipLaunchKernelGGL((residual_norm_bwd_kernel<T, NT, VEC, E>), dim3(a.blocks), dim3(NT), 0, st, a);
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess && a.d_scale)
-        e = column_sum(a.partial, a.blocks, a.D, a.d_scale, st);
-    if (e == hipSuccess && a.d_weight)
-        e = column_sum(a.partial + (a.d_scale ? static_cast<long>(a.blocks) * a.D : 0), a.blocks, a.D, a.d_weight, st);
+    if (e == hipSuccess && (a.d_scale || a.d_weight))
+        e = column_sum(a.partial, a.blocks, a.D, a.d_scale ? a.d_scale : a.d_weight, a.d_scale ? a.d_weight : nullptr, st);
     return e;
 }
 
@@ -424,11 +469,11 @@ hipError_t launch_gated_norm(int o_dtype, int dtype, bool backward, const GatedN
 
 hipError_t launch_residual_norm(int dtype, bool backward, const ResidualNormArgs &a, hipStream_t st)
 {
-    const bool aligned = a.D % 8 == 0 && at16(a.x) && at16(a.y) && at16(a.x_out) && at16(a.h) && at16(a.d_x_out) &&
+    const bool aligned = a.D % 4 == 0 && at16(a.x) && at16(a.y) && at16(a.x_out) && at16(a.h) && at16(a.d_x_out) &&
                          at16(a.d_h) && at16(a.d_x) && at16(a.d_y) && at16(a.partial); // NULL is aligned
     if (dtype == F32)
-        return aligned ? residual_norm_e<float, 8>(backward, a, st) : residual_norm_e<float, 1>(backward, a, st);
-    return aligned ? residual_norm_e<__bf16, 8>(backward, a, st) : residual_norm_e<__bf16, 1>(backward, a, st);
+        return aligned ? residual_norm_e<float, 4>(backward, a, st) : residual_norm_e<float, 1>(backward, a, st);
+    return aligned ? residual_norm_e<__bf16, 4>(backward, a, st) : residual_norm_e<__bf16, 1>(backward, a, st);
 }
 
 } // namespace dl

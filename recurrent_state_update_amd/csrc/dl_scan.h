@@ -73,9 +73,40 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// c += a b for factors in planes: the pairs of planes i + j < ORDER, smallest
-// first.  ORDER 3 leaves out what is below 2^-24 of the largest product;
-// ORDER 2 (where only an output rounded to bf16 is formed) what is below 2^-16.
+// A sum of products of factors in planes.  The pairs of planes i + j < ORDER
+// count: ORDER 3 leaves out what is below 2^-24 of the largest product, ORDER 2
+// (where only an output rounded to bf16 is formed) what is below 2^-16.  One
+// accumulator per order: their chains overlap, and small sums stay apart from
+// large ones until the end.
+template <int ORDER> struct Acc {
+    f32x4 c[ORDER];
+    __device__ __forceinline__ explicit Acc(f32x4 x = f32x4{0, 0, 0, 0})
+    {
+        c[0] = x;
+#pragma unroll
+        for (int s = 1; s < ORDER; ++s)
+            c[s] = f32x4{0, 0, 0, 0};
+    }
+    template <int NA, int NB> __device__ __forceinline__ void add(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB])
+    {
+#pragma unroll
+        for (int i = 0; i < ORDER; ++i) // in turn over the accumulators
+#pragma unroll
+            for (int s = ORDER - 1; s >= i; --s)
+                if (i < NA && s - i < NB)
+                    c[s] = mfma16(a[i], b[s - i], c[s]);
+    }
+    __device__ __forceinline__ f32x4 sum() const
+    {
+        f32x4 x = c[ORDER - 1];
+#pragma unroll
+        for (int s = ORDER - 2; s >= 0; --s)
+            x += c[s];
+        return x;
+    }
+};
+// The same with one accumulator, where registers are short and the products
+// of several sums overlap anyway.
 template <int ORDER, int NA, int NB>
 __device__ __forceinline__ f32x4 mma(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB], f32x4 c)
 {

@@ -52,18 +52,19 @@ template <int N, int K> struct Planes {
     }
 };
 
-// acc += a b, a row block's fragments of KS steps in registers
+// acc + a b, a row block's fragments of KS steps in registers
 template <int ORDER, int KS, int NA, int NB, int K>
 __device__ __forceinline__ f32x4 product(const bf16x8 (&a)[KS][NA], const Planes<NB, K> &b, int lane, f32x4 acc)
 {
+    constexpr int M = NB < ORDER ? NB : ORDER;
+    Acc<ORDER> c(acc);
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-        constexpr int M = NB < ORDER ? NB : ORDER;
         bf16x8 f[M];
         b.get(f, ks, lane);
-        acc = mma<ORDER>(a[ks], f, acc);
+        c.add(a[ks], f);
     }
-    return acc;
+    return c.sum();
 }
 // The same for a triangular C x C operand: the half that is zero is skipped
 // (first: whether k < 32 counts for this row block, second: k >= 32).
@@ -72,16 +73,17 @@ __device__ __forceinline__ f32x4 product_tri(const bf16x8 (&a)[2][NA], const Pla
                                              int lane, f32x4 acc)
 {
     constexpr int M = NB < ORDER ? NB : ORDER;
+    Acc<ORDER> c(acc);
     bf16x8 f[M];
     if (first) {
         b.get(f, 0, lane);
-        acc = mma<ORDER>(a[0], f, acc);
+        c.add(a[0], f);
     }
     if (second) {
         b.get(f, 1, lane);
-        acc = mma<ORDER>(a[1], f, acc);
+        c.add(a[1], f);
     }
-    return acc;
+    return c.sum();
 }
 template <int KS, int NP> __device__ __forceinline__ void load_rows(bf16x8 (&f)[KS][NP], const __bf16 *op, int rb, int lane)
 {
@@ -302,6 +304,9 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
             const int wb = w - 4;
             bf16x8 qf[KS][P::NPQ], bf[2][P::NPB];
             f32x4 gi, o[NC], last[NC];
+#pragma unroll
+            for (int t = 0; t < NC; ++t)
+                last[t] = zero;
             auto load_q = [&](int c) {
                 load_rows(qf, ops(c).op(1), wb, lane);
                 if (ROWS)

@@ -1,16 +1,29 @@
 // dl_scan_launch.h -- launches of the scan, templated on the operator.
 #pragma once
 
+#include <atomic>
+
 #include "dl_scan_carry.h"
 #include "dl_scan_grads.h"
 #include "dl_scan_prep.h"
 
 namespace dl {
 
-template <typename K> hipError_t set_lds(K *kernel, int bytes)
+// Allow a kernel its dynamic LDS, once per kernel and device (the pointer is
+// the template's argument: one flag each).
+template <auto *KERNEL> hipError_t set_lds(int bytes)
 {
-    return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
-                               bytes);
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    if (hipError_t e = hipGetDevice(&dev); e != hipSuccess)
+        return e;
+    if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_relaxed))
+        return hipSuccess;
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(KERNEL),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == hipSuccess && dev >= 0 && dev < 64)
+        done[dev].store(true, std::memory_order_relaxed);
+    return e;
 }
 
 inline bool at16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -22,14 +35,14 @@ template <int OP, typename TIn, int DKP, bool BWD> hipError_t launch_prep(const 
     const dim3 grid(a.slots * a.H);
     if constexpr (OP == GDN) {
         const bool vec = at16(a.q) && at16(a.k) && a.qs % 8 == 0 && a.ks % 8 == 0;
-        auto *prep = scan_prep_gdn_kernel<TIn, DKP, BWD>;
-        if (hipError_t e = set_lds(prep, sizeof(PrepGdnLds<TIn, DKP>)); e != hipSuccess)
+        constexpr auto *prep = scan_prep_gdn_kernel<TIn, DKP, BWD>;
+        if (hipError_t e = set_lds<prep>(sizeof(PrepGdnLds<TIn, DKP>)); e != hipSuccess)
             return e;
         hipLaunchKernelGGL(prep, grid, dim3(256), sizeof(PrepGdnLds<TIn, DKP>), st, a, vec);
     } else {
         const bool vec = at16(a.q) && at16(a.k) && at16(a.ld) && a.qs % 8 == 0 && a.ks % 8 == 0;
-        auto *prep = scan_prep_kernel<OP, TIn, DKP, BWD>;
-        if (hipError_t e = set_lds(prep, sizeof(PrepLds<OP, DKP>)); e != hipSuccess)
+        constexpr auto *prep = scan_prep_kernel<OP, TIn, DKP, BWD>;
+        if (hipError_t e = set_lds<prep>(sizeof(PrepLds<OP, DKP>)); e != hipSuccess)
             return e;
         hipLaunchKernelGGL(prep, grid, dim3(prep_threads<DKP>()), sizeof(PrepLds<OP, DKP>), st, a, vec);
     }
@@ -65,8 +78,8 @@ template <int OP, typename TIn, int DKP> hipError_t scan_backward_t(const ScanAr
                      a.vs % 8 == 0;
     using Lds = GradLds<OP, TIn, DKP>;
     static_assert(sizeof(Lds) <= 160 * 1024, "a CU's LDS");
-    auto *grads = scan_grads_kernel<OP, TIn, DKP>;
-    if (hipError_t e = set_lds(grads, sizeof(Lds)); e != hipSuccess)
+    constexpr auto *grads = scan_grads_kernel<OP, TIn, DKP>;
+    if (hipError_t e = set_lds<grads>(sizeof(Lds)); e != hipSuccess)
         return e;
     hipLaunchKernelGGL(grads, dim3(a.slots * a.H), dim3(DKP * 4), sizeof(Lds), st, a, vec, a.dv / 16);
     if (hipError_t e = hipGetLastError(); e != hipSuccess)

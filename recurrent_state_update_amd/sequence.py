@@ -21,17 +21,25 @@ from . import (DTYPES, OPS, _check, _dtype_id, _op_id, dl_gated_norm, dl_gated_n
                dl_scan_workspace_bytes)
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(device, stream):
     """The context of a call: its device current, and `stream` (a torch stream
     or a raw handle) in place of the current one, so that what is allocated
     belongs to it."""
+    if stream is None:
+        return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
     ctx = contextlib.ExitStack()
     ctx.enter_context(torch.cuda.device(device))
-    if stream is not None:
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=device)
-        ctx.enter_context(torch.cuda.stream(stream))
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    ctx.enter_context(torch.cuda.stream(stream))
     return ctx
+
+
+def _wants_grad(*tensors):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 
 def _bytes(n, device):
@@ -112,12 +120,12 @@ class _Scan:
             raise ValueError(f"{T} tokens: want fewer than 2^31")
         self.op, self.device, self.dtype, self.H, self.dk, self.dv = op, dev, q.dtype, H, dk, dv
         self.shape = dict(q=q.shape, v=v.shape, h=(*lead, H), ld=log_decay.shape)
-        q, qs = _rows(q, len(lead))
-        k, ks = _rows(k, len(lead))
-        v, vs = _rows(v, len(lead))
-        beta = None if beta is None else beta.contiguous()
-        log_decay = log_decay.contiguous()
-        u = None if u is None else u.contiguous()
+        q, qs = _rows(q.detach(), len(lead))
+        k, ks = _rows(k.detach(), len(lead))
+        v, vs = _rows(v.detach(), len(lead))
+        beta = None if beta is None else beta.detach().contiguous()
+        log_decay = log_decay.detach().contiguous()
+        u = None if u is None else u.detach().contiguous()
         self.tensors = (q, k, v, beta, log_decay, u, cu_seqlens)  # kept alive with the descriptor
 
         def p(t):
@@ -144,8 +152,7 @@ class _Scan:
 
 class _ScanFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, op, cu_seqlens, q, k, v, beta, log_decay, u, initial):
-        s = _Scan(op, q, k, v, beta, log_decay, u, cu_seqlens)
+    def forward(ctx, s, q, k, v, beta, log_decay, u, initial):
         final = torch.empty(s.state_shape(), dtype=torch.float32, device=s.device)
         saved = _bytes(dl_scan_saved_bytes(s.desc), s.device)
         o = s.forward(initial, final, None, 0, saved)
@@ -174,7 +181,7 @@ class _ScanFn(torch.autograd.Function):
             ws = _bytes(dl_scan_backward_workspace_bytes(s.desc), s.device)
             _check(dl_scan_backward(s.desc, saved, d_o, d_final, dq, dk, dv, dbeta, dld, du, d0, ws),
                    "dl_scan_backward")
-        return None, None, dq, dk, dv, dbeta, dld, du, d0
+        return None, dq, dk, dv, dbeta, dld, du, d0
 
 
 def _initial(initial_state, shape, device):
@@ -205,9 +212,8 @@ def scan(op: str, q, k, v, beta, log_decay, u=None, initial_state=None, cu_seqle
     probe = _Scan(op, q, k, v, beta, log_decay, u, cu_seqlens)
     with _on(probe.device, stream):
         initial = _initial(initial_state, probe.state_shape(), probe.device)
-        if torch.is_grad_enabled() and any(t is not None and t.requires_grad
-                                           for t in (q, k, v, beta, log_decay, u, initial_state)):
-            return _ScanFn.apply(op, cu_seqlens, q, k, v, beta, log_decay, u, initial)
+        if _wants_grad(q, k, v, beta, log_decay, u, initial):
+            return _ScanFn.apply(probe, q, k, v, beta, log_decay, u, initial)
         final = torch.empty(probe.state_shape(), dtype=torch.float32, device=probe.device)
         return probe.forward(initial, final, None, 0), final
 
@@ -237,26 +243,23 @@ def _prefill(st, q, k, v, beta, log_decay, cu_seqlens, slots, stream):
 
 # -------------------------------------------------------------------- norms --
 
-def _weight(w, name, n, device):
-    if w is None:
-        return None
-    _tensor(w, name, torch.float32, (n,), device)
-    return w.contiguous()
+def _gated_norm(o, gate, weight, eps):
+    """y, and what its backward pass needs."""
+    H, d = o.shape[-2:]
+    rows = o.numel() // (H * d)
+    o = o.contiguous()
+    g, gs = _rows(gate, gate.dim() - 2)
+    weight = None if weight is None else weight.contiguous()
+    y = torch.empty(gate.shape, dtype=gate.dtype, device=o.device)
+    _check(dl_gated_norm(rows, H, d, DTYPES[o.dtype], DTYPES[gate.dtype], o, g, gs, weight, eps, y), "dl_gated_norm")
+    return y, (o, g, weight), (rows, H, d, gs, eps)
 
 
 class _GatedNormFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, o, gate, weight, eps):
-        H, d = o.shape[-2:]
-        rows = o.numel() // (H * d)
-        o = o.contiguous()
-        g, gs = _rows(gate, gate.dim() - 2)
-        weight = _weight(weight, "weight", d, o.device)
-        y = torch.empty(gate.shape, dtype=gate.dtype, device=o.device)
-        _check(dl_gated_norm(rows, H, d, DTYPES[o.dtype], DTYPES[gate.dtype], o, g, gs, weight, eps, y),
-               "dl_gated_norm")
-        ctx.save_for_backward(o, g, weight)
-        ctx.args = (rows, H, d, gs, eps)
+        y, saved, ctx.args = _gated_norm(o, gate, weight, eps)
+        ctx.save_for_backward(*saved)
         return y
 
     @staticmethod
@@ -294,26 +297,30 @@ def gated_norm(o, gate, weight=None, eps: float = 1e-6, stream=None):
     if weight is not None:
         _tensor(weight, "weight", torch.float32, (o.shape[-1],), o.device)
     with _on(o.device, stream):
-        return _GatedNormFn.apply(o, gate, weight, float(eps))
+        if _wants_grad(o, gate, weight):
+            return _GatedNormFn.apply(o, gate, weight, float(eps))
+        return _gated_norm(o, gate, weight, float(eps))[0]
+
+
+def _residual_norm(x, y, scale, weight, eps, dtype):
+    """x' (None without y) and h, and what their backward pass needs."""
+    D = x.shape[-1]
+    rows = x.numel() // D
+    x, y, scale, weight = (None if t is None else t.contiguous() for t in (x, y, scale, weight))
+    x_out = None if y is None else torch.empty_like(x)
+    h = torch.empty(x.shape, dtype=dtype, device=x.device)
+    _check(dl_residual_norm(rows, D, DTYPES[dtype], x, y, scale, weight, eps, x_out, h), "dl_residual_norm")
+    return (x_out, h), (x if y is None else x_out, y if scale is not None else None, scale, weight), \
+        (rows, D, eps, dtype, y is not None)
 
 
 class _ResidualNormFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, y, scale, weight, eps, dtype):
-        D = x.shape[-1]
-        rows = x.numel() // D
-        x = x.contiguous()
-        y = None if y is None else y.contiguous()
-        scale, weight = _weight(scale, "scale", D, x.device), _weight(weight, "weight", D, x.device)
-        x_out = None if y is None else torch.empty_like(x)
-        h = torch.empty(x.shape, dtype=dtype, device=x.device)
-        _check(dl_residual_norm(rows, D, DTYPES[dtype], x, y, scale, weight, eps, x_out, h), "dl_residual_norm")
+        out, saved, ctx.args = _residual_norm(x, y, scale, weight, eps, dtype)
         ctx.set_materialize_grads(False)
-        ctx.save_for_backward(x if y is None else x_out, y if scale is not None else None, scale, weight)
-        ctx.args = (rows, D, eps, dtype, y is not None)
-        if y is None:
-            return h
-        return x_out, h
+        ctx.save_for_backward(*saved)
+        return out[1] if y is None else out
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -365,6 +372,8 @@ def residual_norm(x, y=None, scale=None, weight=None, eps: float = 1e-6, dtype=N
         if t is not None:
             _tensor(t, name, torch.float32, (D,), x.device)
     with _on(x.device, stream):
-        if y is None:
-            return x, _ResidualNormFn.apply(x, None, None, weight, float(eps), dtype)
-        return _ResidualNormFn.apply(x, y, scale, weight, float(eps), dtype)
+        if not _wants_grad(x, y, scale, weight):
+            out = _residual_norm(x, y, scale, weight, float(eps), dtype)[0]
+            return (x, out[1]) if y is None else out
+        out = _ResidualNormFn.apply(x, y, scale, weight, float(eps), dtype)
+        return (x, out) if y is None else out
