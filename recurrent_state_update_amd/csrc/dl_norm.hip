@@ -127,12 +127,25 @@ __global__ __launch_bounds__(256) void gated_norm_bwd_kernel(GatedNormArgs a)
         w[i] = a.weight ? a.weight[c + i] : 1.f;
         dw[i] = 0.f;
     }
-    for (long u = (static_cast<long>(blockIdx.x) * 256 + threadIdx.x) / G; u < a.units;
-         u += static_cast<long>(a.blocks) * (256 / G)) {
+    float on[8], gn[8], yn[8]; // the next turn's
+    const auto read = [&](long v) {
+        load<8, ALIGNED>(on, static_cast<const TO *>(a.o) + v * D + c);
+        load<8, ALIGNED>(gn, static_cast<const T *>(a.gate) + v / a.H * a.gate_stride + v % a.H * D + c);
+        load<8, ALIGNED>(yn, static_cast<const T *>(a.dy) + v * D + c);
+    };
+    const long first = (static_cast<long>(blockIdx.x) * 256 + threadIdx.x) / G, step = static_cast<long>(a.blocks) * (256 / G);
+    if (first < a.units)
+        read(first);
+    for (long u = first; u < a.units; u += step) {
         float o[8], g[8], dy[8], dn[8];
-        load<8, ALIGNED>(o, static_cast<const TO *>(a.o) + u * D + c);
-        load<8, ALIGNED>(g, static_cast<const T *>(a.gate) + u / a.H * a.gate_stride + u % a.H * D + c);
-        load<8, ALIGNED>(dy, static_cast<const T *>(a.dy) + u * D + c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            o[i] = on[i];
+            g[i] = gn[i];
+            dy[i] = yn[i];
+        }
+        if (u + step < a.units)
+            read(u + step);
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -293,8 +306,12 @@ __global__ __launch_bounds__(NT) void residual_norm_kernel(ResidualNormArgs a)
                 load<VEC, true>(yn[k], static_cast<const T *>(a.y) + row * a.D + c);
         }
     };
-    read(blockIdx.x);
+    constexpr bool AHEAD = E <= 2; // else the registers do not hold two rows
+    if (AHEAD)
+        read(blockIdx.x);
     for (long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        if (!AHEAD)
+            read(row);
         const long at = row * a.D;
         float x[L::K][VEC], ss = 0.f;
 #pragma unroll
@@ -312,7 +329,7 @@ __global__ __launch_bounds__(NT) void residual_norm_kernel(ResidualNormArgs a)
             if (a.y)
                 store<VEC, true>(a.x_out + at + c, x[k]);
         }
-        if (row + gridDim.x < a.rows)
+        if (AHEAD && row + gridDim.x < a.rows)
             read(row + gridDim.x);
         const float r = 1.f / sqrtf(row_sum<NT>(ss, part) / a.D + a.eps);
 #pragma unroll
@@ -342,26 +359,52 @@ __global__ __launch_bounds__(NT) void residual_norm_bwd_kernel(ResidualNormArgs 
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
             ds[k][i] = dw[k][i] = 0.f;
-    for (long row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const long at = row * a.D;
-        float x[L::K][VEC], dn[L::K][VEC], ss = 0.f, dot = 0.f;
+    // x', dh, dx' (and y) of the next row
+    float nx[L::K][VEC], nh[L::K][VEC], nd[L::K][VEC], ny[L::K][VEC];
+    const bool scaled = a.scale && a.d_y;
+#pragma unroll
+    for (int k = 0; k < L::K; ++k)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            nh[k][i] = nd[k][i] = ny[k][i] = 0.f;
+    const auto read = [&](long row) {
 #pragma unroll
         for (int k = 0; k < L::K; ++k) {
             const int c = L::col(k);
             if (c >= a.D)
                 continue;
-            load<VEC, true>(x[k], a.x + at + c);
-            if (a.d_h) {
-                load<VEC, true>(dn[k], static_cast<const T *>(a.d_h) + at + c);
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    dn[k][i] = 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                ss = fmaf(x[k][i], x[k][i], ss);
+            const long at = row * a.D + c;
+            load<VEC, true>(nx[k], a.x + at);
+            if (a.d_h)
+                load<VEC, true>(nh[k], static_cast<const T *>(a.d_h) + at);
+            if (a.d_x_out)
+                load<VEC, true>(nd[k], a.d_x_out + at);
+            if (scaled)
+                load<VEC, true>(ny[k], static_cast<const T *>(a.y) + at);
         }
+    };
+    constexpr bool AHEAD = E <= 2;
+    if (AHEAD && blockIdx.x < a.rows)
+        read(blockIdx.x);
+    for (long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        if (!AHEAD)
+            read(row);
+        const long at = row * a.D;
+        float x[L::K][VEC], dn[L::K][VEC], dx[L::K][VEC], y[L::K][VEC], ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int k = 0; k < L::K; ++k) {
+            const bool in = L::col(k) < a.D;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                x[k][i] = nx[k][i];
+                dn[k][i] = nh[k][i];
+                dx[k][i] = nd[k][i];
+                y[k][i] = ny[k][i];
+                ss = in ? fmaf(x[k][i], x[k][i], ss) : ss;
+            }
+        }
+        if (AHEAD && row + gridDim.x < a.rows)
+            read(row + gridDim.x);
         const float r = 1.f / sqrtf(row_sum<NT>(ss, part) / a.D + a.eps);
 #pragma unroll
         for (int k = 0; k < L::K; ++k) {
@@ -386,20 +429,13 @@ __global__ __launch_bounds__(NT) void residual_norm_bwd_kernel(ResidualNormArgs 
             float d[VEC];
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
-                d[i] = 0.f;
-            if (a.d_x_out)
-                load<VEC, true>(d, a.d_x_out + at + c);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                d[i] += r * (dn[k][i] - x[k][i] * dot);
+                d[i] = dx[k][i] + r * (dn[k][i] - x[k][i] * dot);
             store<VEC, true>(a.d_x + at + c, d);
             if (a.d_y) {
-                if (a.scale) {
-                    float y[VEC];
-                    load<VEC, true>(y, static_cast<const T *>(a.y) + at + c);
+                if (scaled) {
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) {
-                        ds[k][i] = fmaf(d[i], y[i], ds[k][i]);
+                        ds[k][i] = fmaf(d[i], y[k][i], ds[k][i]);
                         d[i] *= a.scale[c + i];
                     }
                 }

@@ -3,15 +3,16 @@
 //
 // One workgroup of eight waves per (sequence, head, NC x 16 value columns): the
 // columns of the state are independent.  The chunks are a chain, and with few
-// sequences and heads its latency is the time, so the waves are of two kinds,
-// two to a SIMD: waves 0-3 (rows 16 w.. of the chunk) form what the next state
-// waits for, waves 4-7 what only leaves the kernel (o; dS's other half); each
-// row block of the state is held by one wave, in fp32 registers.  What a
-// wave's product needs of another's rows passes through LDS as bf16 planes,
-// already in the order that the matrix instruction reads.  Each operand of the
-// next chunk is loaded into the registers of this one's right behind its last
-// use, and the value tiles of one (sequence, head) run on one XCD, whose L2
-// serves all but the first of them.
+// sequences and heads its latency is the time.  Two waves share a SIMD: waves
+// 0-3 hold rows 16 w.. of the chunk's products, waves 4-7 the row blocks of the
+// state (w - 4, w), in fp32 registers, and while the first form b, the chunk
+// before's o.  What a wave's product needs of another's rows
+// passes through LDS as bf16 planes, already in the order that the matrix
+// instruction reads; LDS bandwidth is most of a step, so what is read from it
+// serves every product that the wave forms with it.  Each operand of the next
+// chunk is loaded into the registers of this one's right behind its last use;
+// the value tiles of one (sequence, head) run on one XCD, whose L2 serves all
+// but the first of them.
 #pragma once
 
 #include "dl_scan.h"
@@ -52,18 +53,22 @@ template <int N, int K> struct Planes {
     }
 };
 
-// acc + a b, a row block's fragments of KS steps in registers
-template <int ORDER, int KS, int NA, int NB, int K>
-__device__ __forceinline__ f32x4 product(const bf16x8 (&a)[KS][NA], const Planes<NB, K> &b, int lane, f32x4 acc)
+// The fragments of planes in registers (the first M planes)
+template <int KS, int M, int N, int K> __device__ __forceinline__ void get_all(bf16x8 (&f)[KS][M], const Planes<N, K> &b, int lane)
 {
-    constexpr int M = NB < ORDER ? NB : ORDER;
+    static_assert(KS * 32 == K && M <= N, "all of it");
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+        b.get(f[ks], ks, lane);
+}
+// acc + a b, a row block's fragments and the columns' in registers
+template <int ORDER, int KS, int NA, int NB>
+__device__ __forceinline__ f32x4 product(const bf16x8 (&a)[KS][NA], const bf16x8 (&b)[KS][NB], f32x4 acc)
+{
     Acc<ORDER> c(acc);
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-        bf16x8 f[M];
-        b.get(f, ks, lane);
-        c.add(a[ks], f);
-    }
+    for (int ks = 0; ks < KS; ++ks)
+        c.add(a[ks], b[ks]);
     return c.sum();
 }
 // The same for a triangular C x C operand: the half that is zero is skipped
@@ -111,15 +116,12 @@ __device__ __forceinline__ long state_row(const ScanArgs &a, int n)
     return r >= 0 && r < a.nrows ? r : -1;
 }
 
-// Which wave holds which row block of the state: one each where there are
-// eight, else the waves off the chain.
+// The row blocks of the state that waves 4-7 hold: RB each, the r-th of wave
+// 4 + wb being wb + 4 r.
 template <int DKP> struct Holder {
-    bool has;
-    int rb;
-    __device__ __forceinline__ explicit Holder(int w)
-        : has(DKP == 128 || (w >= 4 && w - 4 < DKP / 16)), rb(DKP == 128 ? w : has ? w - 4 : 0)
-    {
-    }
+    static constexpr int RB = DKP == 128 ? 2 : 1;
+    static __device__ __forceinline__ bool has(int wb) { return DKP >= 64 || wb < DKP / 16; }
+    static __device__ __forceinline__ int block(int wb, int r) { return has(wb) ? wb + 4 * r : 0; }
 };
 
 // Rows of one chunk of a matrix of inputs, as a buffer of the rows that there
@@ -156,15 +158,20 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
 {
     using P = Plan<OP, TIn>;
     using O = Ops<P::NPX, DKP>;
+    using Own = Holder<DKP>;
     constexpr bool DELTA = P::DELTA, ROWS = P::ROWS;
-    constexpr int KS = DKP / 32;
-    __shared__ Planes<3, DKP> sp[NC];             // the state
+    constexpr int KS = DKP / 32, RB = Own::RB;
+    // Delta rule: three barriers a chunk, every buffer rewritten two behind its
+    // readers.  RWKV6's b is known ahead: one barrier, two buffers each.
+    constexpr int TWO = DELTA ? 1 : 2;
+    __shared__ Planes<3, DKP> sp[TWO][NC];        // the state
     __shared__ Planes<3, C> rp[DELTA ? NC : 1];   // V - K~ S
-    __shared__ Planes<3, C> hp[NC];               // b (ROWS: P_Ci b), for the state
-    __shared__ Planes<P::NPB, C> bp[2][NC];       // b, for o (in turn: read a chunk later)
+    __shared__ Planes<3, C> hp[TWO][NC];          // b (ROWS: P_Ci b), for the state
+    __shared__ Planes<P::NPB, C> bp[2][NC];       // b, for o (in turn: delta rule, read a chunk later)
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, r4 = (lane >> 4) * 4, i0 = (w & 3) * 16 + r4;
-    const CarryWork wk = carry_work(a.dv / (16 * NC));
+    const int tiles = a.dv / (16 * NC);
+    const CarryWork wk = carry_work(tiles);
     if (wk.group >= a.N * a.H)
         return;
     const int h = wk.group % a.H, n = wk.group / a.H;
@@ -172,199 +179,237 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
     const int v0 = wk.tile * 16 * NC + col;
     const long first = static_cast<long>(h) * a.dv + wk.tile * 16 * NC; // of a row, this workgroup's
     const unsigned width = a.H * a.dv;
-    const long row = state_row(a, n);
-    const long st0 = (row * a.H + h) * a.dk * a.dv + v0;
     const int chunks = (sq.len + C - 1) / C;
-    const Holder<DKP> own(w);
     const f32x4 zero = {0, 0, 0, 0};
-
-    f32x4 S[NC], gam;
-    bf16x8 tf[2][P::NPX];
     auto ops = [&](int c) { return O(a, static_cast<long>(sq.base + c) * a.H + h); };
-    auto load_t = [&](int c) {
-        load_rows(tf, ops(c).op(2), own.rb, lane);
-        gam = ld4(ops(c).gam() + own.rb * 16 + r4);
-    };
-    auto put_state = [&](int c) { // the planes of chunk c's start state
-        if (!own.has)
-            return;
-#pragma unroll
-        for (int t = 0; t < NC; ++t) {
-            sp[t].put(col, own.rb * 16 + r4, S[t]);
-            if (SAVE && c < chunks) {
-                const long sh = static_cast<long>(sq.base + c) * a.H + h;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int d = own.rb * 16 + r4 + e;
-                    if (DKP > 32 || d < a.dk)
-                        a.save_s[(sh * a.dk + d) * a.dv + v0 + 16 * t] = S[t][e];
-                }
-            }
-        }
-    };
-    auto update = [&](int c, int next) {
-        if (own.has) {
-#pragma unroll
-            for (int t = 0; t < NC; ++t)
-                S[t] = product<3>(tf, hp[t], lane, S[t] * gam);
-        }
-        put_state(c + 1);
-        load_t(next);
-    };
-    if (own.has) {
-#pragma unroll
-        for (int t = 0; t < NC; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int d = own.rb * 16 + r4 + e;
-                S[t][e] = a.init && row >= 0 && d < a.dk ? a.init[st0 + static_cast<long>(d) * a.dv + 16 * t] : 0.f;
-            }
-    }
-    put_state(0);
 
-    if (chunks > 0) {
-        if (w < 4) {
+    // o = Q~ S + B b of rows i0..
+    bf16x8 qf[KS][P::NPQ], bf[2][P::NPB];
+    TIn *op = static_cast<TIn *>(a.o) + static_cast<long>(sq.start) * width + first;
+    auto load_q = [&](int c) { load_rows(qf, ops(c).op(1), w & 3, lane); };
+    auto load_b = [&](int c) { load_tri(bf, ops(c).mat(1), LOWER, w & 3, lane); };
+    auto out = [&](int c, f32x4 o, const Planes<P::NPB, C> &b, int t) {
+        o = product_tri<P::ORDER_O>(bf, b, true, (w & 3) >= 2, lane, o);
+        const ChunkRows<TIn> rows(op, width, c, sq.len, 16 * NC);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            rows.store((i0 + e) * width + col + 16 * t, o[e]);
+    };
+
+    if (w < 4) {
+        if (chunks == 0)
+            return; // barriers count the waves that are left
+        TIn v[NC][4];
+        const TIn *vp = static_cast<const TIn *>(a.v) + static_cast<long>(sq.start) * a.vs + first;
+        auto load_v = [&](int c) {
+            const ChunkRows<TIn> rows(vp, static_cast<unsigned>(a.vs), c, sq.len, 16 * NC);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int t = 0; t < NC; ++t)
+                    v[t][e] = rows.load((i0 + e) * static_cast<unsigned>(a.vs) + col + 16 * t);
+        };
+        auto take_v = [&](int t) { return f32x4{from_in(v[t][0]), from_in(v[t][1]), from_in(v[t][2]), from_in(v[t][3])}; };
+        load_v(0);
+        keep_order();
+        if constexpr (DELTA) {
             bf16x8 kf[KS][P::NPX], nf[2][3];
             f32x4 gi, ge, beta;
-            TIn v[NC][4];
-            const TIn *vp = static_cast<const TIn *>(a.v) + static_cast<long>(sq.start) * a.vs + first;
-            auto load_v = [&](int c) {
-                const ChunkRows<TIn> rows(vp, static_cast<unsigned>(a.vs), c, sq.len, 16 * NC);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int t = 0; t < NC; ++t)
-                        v[t][e] = rows.load((i0 + e) * static_cast<unsigned>(a.vs) + col + 16 * t);
-            };
             auto load_k = [&](int c) {
-                if (DELTA)
-                    load_rows(kf, ops(c).op(0), w, lane);
+                load_rows(kf, ops(c).op(0), w, lane);
                 if (ROWS)
                     gi = ld4(ops(c).row(0) + i0);
             };
             auto load_n = [&](int c) {
-                if (DELTA) {
-                    load_tri(nf, ops(c).mat(0), LOWER, w, lane);
-                    beta = ld4(ops(c).row(2) + i0);
-                }
+                load_tri(nf, ops(c).mat(0), LOWER, w, lane);
+                beta = ld4(ops(c).row(2) + i0);
                 if (ROWS)
                     ge = ld4(ops(c).row(1) + i0);
             };
-            load_v(0);
-            keep_order();
             load_k(0);
             keep_order();
             load_n(0);
-            keep_order();
-            load_t(0);
             keep_order();
             for (int c = 0; c < chunks; ++c) {
                 const int next = c + 1 < chunks ? c + 1 : c;
                 f32x4 x[NC];
 #pragma unroll
                 for (int t = 0; t < NC; ++t)
-                    x[t] = f32x4{from_in(v[t][0]), from_in(v[t][1]), from_in(v[t][2]), from_in(v[t][3])};
+                    x[t] = take_v(t);
                 load_v(next);
                 __syncthreads(); // the state's planes are complete
-                if constexpr (DELTA) {
-#pragma unroll
-                    for (int t = 0; t < NC; ++t) {
-                        f32x4 ks = product<3>(kf, sp[t], lane, zero);
-                        if (ROWS)
-                            ks *= gi;
-                        rp[t].put(col, i0, x[t] - ks);
-                    }
-                    load_k(next);
-                    __syncthreads(); // V - K~ S is complete, and the state's planes are read
-#pragma unroll
-                    for (int t = 0; t < NC; ++t) {
-                        x[t] = product_tri<3>(nf, rp[t], true, w >= 2, lane, zero);
-                        if (SAVE) {
-                            const long sh = static_cast<long>(sq.base + c) * a.H + h;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                a.save_e[(sh * C + i0 + e) * a.dv + v0 + 16 * t] = x[t][e];
-                        }
-                        x[t] *= beta;
-                    }
-                }
 #pragma unroll
                 for (int t = 0; t < NC; ++t) {
+                    bf16x8 f[KS][3];
+                    get_all(f, sp[0][t], lane);
+                    f32x4 ks = product<3>(kf, f, zero);
                     if (ROWS)
-                        hp[t].put(col, i0, x[t] * ge);
-                    else
-                        hp[t].put(col, i0, x[t]);
+                        ks *= gi;
+                    rp[t].put(col, i0, x[t] - ks);
+                }
+                load_k(next);
+                __syncthreads(); // V - K~ S is complete, and the state's planes are read
+#pragma unroll
+                for (int t = 0; t < NC; ++t) {
+                    x[t] = product_tri<3>(nf, rp[t], true, w >= 2, lane, zero);
+                    if (SAVE) {
+                        const long sh = static_cast<long>(sq.base + c) * a.H + h;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            a.save_e[(sh * C + i0 + e) * a.dv + v0 + 16 * t] = x[t][e];
+                    }
+                    x[t] *= beta;
+                    hp[0][t].put(col, i0, ROWS ? x[t] * ge : x[t]);
                     bp[c & 1][t].put(col, i0, x[t]);
                 }
                 load_n(next);
-                __syncthreads(); // b is complete (RWKV6: and the state's planes are read)
-                update(c, next);
+                __syncthreads(); // b is complete
             }
         } else {
-            const int wb = w - 4;
-            bf16x8 qf[KS][P::NPQ], bf[2][P::NPB];
-            f32x4 gi, o[NC], last[NC];
-#pragma unroll
-            for (int t = 0; t < NC; ++t)
-                last[t] = zero;
-            auto load_q = [&](int c) {
-                load_rows(qf, ops(c).op(1), wb, lane);
-                if (ROWS)
-                    gi = ld4(ops(c).row(0) + i0);
-            };
-            auto load_b = [&](int c) { load_tri(bf, ops(c).mat(1), LOWER, wb, lane); };
-            // o of chunk c, `last` being its Q~ S
-            TIn *op = static_cast<TIn *>(a.o) + static_cast<long>(sq.start) * a.H * a.dv + first;
-            auto finish = [&](int c, int next) {
-                const ChunkRows<TIn> rows(op, width, c, sq.len, 16 * NC);
+            auto put_v = [&](int c) {
 #pragma unroll
                 for (int t = 0; t < NC; ++t) {
-                    last[t] = product_tri<P::ORDER_O>(bf, bp[c & 1][t], true, wb >= 2, lane, last[t]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        rows.store((i0 + e) * width + col + 16 * t, last[t][e]);
+                    hp[c & 1][t].put(col, i0, take_v(t));
+                    bp[c & 1][t].put(col, i0, take_v(t));
                 }
-                load_b(next);
             };
+            put_v(0);
+            load_v(chunks > 1 ? 1 : 0);
+            keep_order();
             load_q(0);
             keep_order();
             load_b(0);
             keep_order();
-            load_t(0);
-            keep_order();
             for (int c = 0; c < chunks; ++c) {
-                const int next = c + 1 < chunks ? c + 1 : c;
-                __syncthreads();
+                __syncthreads(); // state and b are complete
+                const int next = c + 1 < chunks ? c + 1 : c, after = c + 2 < chunks ? c + 2 : next;
 #pragma unroll
                 for (int t = 0; t < NC; ++t) {
-                    o[t] = product<P::ORDER_O>(qf, sp[t], lane, zero);
+                    bf16x8 f[KS][P::ORDER_O];
+                    get_all(f, sp[c & 1][t], lane);
+                    out(c, product<P::ORDER_O>(qf, f, zero), bp[c & 1][t], t);
+                }
+                put_v(c + 1); // (behind the last chunk: read by nobody)
+                load_v(after);
+                load_q(next);
+                load_b(next);
+            }
+        }
+        return;
+    }
+
+    const int wb = w - 4;
+    const bool has = Own::has(wb);
+    const long row = state_row(a, n);
+    const long st0 = (row * a.H + h) * a.dk * a.dv + v0;
+    f32x4 S[NC][RB], gam[RB];
+    bf16x8 tf[RB][2][P::NPX];
+    auto load_t = [&](int c) {
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            load_rows(tf[r], ops(c).op(2), Own::block(wb, r), lane);
+            gam[r] = ld4(ops(c).gam() + Own::block(wb, r) * 16 + r4);
+        }
+    };
+    auto put_state = [&](int c) { // the planes of chunk c's start state
+        if (!has)
+            return;
+#pragma unroll
+        for (int t = 0; t < NC; ++t)
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                const int d0 = Own::block(wb, r) * 16 + r4;
+                sp[DELTA ? 0 : c & 1][t].put(col, d0, S[t][r]);
+                if (SAVE && c < chunks) {
+                    const long sh = static_cast<long>(sq.base + c) * a.H + h;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (DKP > 32 || d0 + e < a.dk)
+                            a.save_s[(sh * a.dk + d0 + e) * a.dv + v0 + 16 * t] = S[t][r][e];
+                }
+            }
+    };
+#pragma unroll
+    for (int t = 0; t < NC; ++t)
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int d = Own::block(wb, r) * 16 + r4 + e;
+                S[t][r][e] = a.init && row >= 0 && has && d < a.dk ? a.init[st0 + static_cast<long>(d) * a.dv + 16 * t] : 0.f;
+            }
+    put_state(0);
+    if (chunks > 0) {
+        f32x4 gi = zero, o[NC], last[NC]; // delta rule: rows' decays, Q~ S of this chunk and the one before
+#pragma unroll
+        for (int t = 0; t < NC; ++t)
+            last[t] = zero;
+        auto load_gi = [&](int c) {
+            if (ROWS)
+                gi = ld4(ops(c).row(0) + i0);
+        };
+        if (DELTA) {
+            load_q(0);
+            load_gi(0);
+            keep_order();
+            load_b(0);
+            keep_order();
+        }
+        load_t(0);
+        keep_order();
+        for (int c = 0; c < chunks; ++c) {
+            const int next = c + 1 < chunks ? c + 1 : c;
+            __syncthreads();
+            if constexpr (DELTA) {
+#pragma unroll
+                for (int t = 0; t < NC; ++t) {
+                    bf16x8 f[KS][P::ORDER_O];
+                    get_all(f, sp[0][t], lane);
+                    o[t] = product<P::ORDER_O>(qf, f, zero);
                     if (ROWS)
                         o[t] *= gi;
                 }
                 load_q(next);
-                if constexpr (DELTA)
-                    __syncthreads();
-                // the chunk before is finished while the chain computes b; the
-                // first turn has none (what it writes is written again)
-                finish(c > 0 ? c - 1 : 0, c);
+                load_gi(next);
                 __syncthreads();
+                // the chunk before is finished while waves 0-3 form b; the first
+                // turn has none (what it writes is written again)
 #pragma unroll
-                for (int t = 0; t < NC; ++t)
+                for (int t = 0; t < NC; ++t) {
+                    out(c > 0 ? c - 1 : 0, last[t], bp[(c + 1) & 1][t], t);
                     last[t] = o[t];
-                update(c, next);
+                }
+                load_b(c);
+                __syncthreads();
             }
-            finish(chunks - 1, chunks - 1);
+#pragma unroll
+            for (int t = 0; t < NC; ++t) {
+                bf16x8 f[2][3];
+                get_all(f, hp[DELTA ? 0 : c & 1][t], lane);
+#pragma unroll
+                for (int r = 0; r < RB; ++r)
+                    S[t][r] = product<3>(tf[r], f, S[t][r] * gam[r]);
+            }
+            put_state(c + 1);
+            load_t(next);
+        }
+        if constexpr (DELTA) {
+#pragma unroll
+            for (int t = 0; t < NC; ++t)
+                out(chunks - 1, last[t], bp[(chunks - 1) & 1][t], t);
         }
     }
-    if (a.fin && row >= 0 && own.has) {
+    if (a.fin && row >= 0 && has) {
 #pragma unroll
         for (int t = 0; t < NC; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int d = own.rb * 16 + r4 + e;
-                if (d < a.dk)
-                    a.fin[st0 + static_cast<long>(d) * a.dv + 16 * t] = S[t][e];
-            }
+            for (int r = 0; r < RB; ++r)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int d = Own::block(wb, r) * 16 + r4 + e;
+                    if (d < a.dk)
+                        a.fin[st0 + static_cast<long>(d) * a.dv + 16 * t] = S[t][r][e];
+                }
     }
 }
 
@@ -377,9 +422,11 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
 {
     using P = Plan<OP, TIn>;
     using O = Ops<P::NPX, DKP>;
+    using Own = Holder<DKP>;
     constexpr bool DELTA = P::DELTA, ROWS = P::ROWS;
-    constexpr int KS = DKP / 32;
-    __shared__ Planes<3, DKP> sp[NC];                   // dS'
+    constexpr int KS = DKP / 32, RB = Own::RB;
+    constexpr int TWO = DELTA ? 1 : 2;                  // RWKV6: dS does not wait for db, one barrier a chunk
+    __shared__ Planes<3, DKP> sp[TWO][NC];              // dS'
     __shared__ Planes<P::NPI, C> gp[2][NC];             // dO (in turn: put a chunk ahead)
     __shared__ Planes<3, C> gg[2][ROWS ? NC : 1];       // ROWS: Gam_i dO
     __shared__ Planes<3, C> wp[DELTA ? NC : 1];         // beta db
@@ -395,220 +442,230 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
     const int v0 = wk.tile * 16 * NC + col;
     const long first = static_cast<long>(h) * a.dv + wk.tile * 16 * NC; // of a row, this workgroup's
     const unsigned width = a.H * a.dv;
-    const long st0 = (static_cast<long>(n) * a.H + h) * a.dk * a.dv + v0;
     const int chunks = (sq.len + C - 1) / C;
-    const Holder<DKP> own(w);
     const f32x4 zero = {0, 0, 0, 0};
-
-    f32x4 S[NC], gam; // dS'
-    bf16x8 qt[2][P::NPX], kt[2][P::NPX];
     auto ops = [&](int c) { return O(a, static_cast<long>(sq.base + c) * a.H + h); };
-    auto load_t = [&](int c) {
-        load_rows(qt, ops(c).op(1), own.rb, lane);
-        if (DELTA)
-            load_rows(kt, ops(c).op(2), own.rb, lane);
-        gam = ld4(ops(c).gam() + own.rb * 16 + r4);
-    };
-    auto put_state = [&](int c) { // the planes of the gradient of chunk c's end state
-        if (!own.has)
-            return;
-#pragma unroll
-        for (int t = 0; t < NC; ++t) {
-            sp[t].put(col, own.rb * 16 + r4, S[t]);
-            if (c >= 0) {
-                const long sh = static_cast<long>(sq.base + c) * a.H + h;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int d = own.rb * 16 + r4 + e;
-                    if (DKP > 32 || d < a.dk)
-                        a.w_ds[(sh * a.dk + d) * a.dv + v0 + 16 * t] = S[t][e];
-                }
-            }
-        }
-    };
-    // dS = Gam_C dS' + Q~^T dO - K~^T z, the first part ahead of z
-    auto part = [&](int c) {
-        if (!own.has)
-            return;
-#pragma unroll
-        for (int t = 0; t < NC; ++t) {
-            if constexpr (ROWS)
-                S[t] = product<3>(qt, gg[c & 1][t], lane, S[t] * gam);
-            else
-                S[t] = product<3>(qt, gp[c & 1][t], lane, S[t] * gam);
-        }
-    };
-    auto rest = [&](int c, int next) {
-        if (DELTA && own.has) {
+
+    if (w < 4) {
+        if (chunks == 0)
+            return; // barriers count the waves that are left
+        bf16x8 kf[KS][P::NPX], bt[2][3], nt[2][3];
+        f32x4 gi, ge, beta;
+        float E[NC][4];
+        TIn *dvp = static_cast<TIn *>(a.d_v) + static_cast<long>(sq.start) * width + first;
+        auto load_db = [&](int c) {
+            load_tri(bt, ops(c).mat(1), UPPER, w, lane);
+            load_rows(kf, ops(c).op(0), w, lane);
+            if (ROWS)
+                ge = ld4(ops(c).row(1) + i0);
+            if (DELTA)
+                beta = ld4(ops(c).row(2) + i0);
+        };
+        auto load_n = [&](int c) {
+            if (DELTA)
+                load_tri(nt, ops(c).mat(0), UPPER, w, lane);
+            if (ROWS)
+                gi = ld4(ops(c).row(0) + i0);
+        };
+        auto load_e = [&](int c) {
+            if (!DELTA)
+                return;
 #pragma unroll
             for (int t = 0; t < NC; ++t)
-                S[t] = product<3>(kt, zp[t], lane, S[t]);
-        }
-        put_state(c - 1);
-        load_t(next);
-    };
-    if (own.has) {
 #pragma unroll
-        for (int t = 0; t < NC; ++t)
+                for (int e = 0; e < 4; ++e)
+                    E[t][e] = a.save_e[((static_cast<long>(sq.base + c) * a.H + h) * C + i0 + e) * a.dv + v0 + 16 * t];
+        };
+        load_db(chunks - 1);
+        keep_order();
+        load_n(chunks - 1);
+        keep_order();
+        load_e(chunks - 1);
+        keep_order();
+        for (int c = chunks - 1; c >= 0; --c) {
+            const int next = c > 0 ? c - 1 : 0;
+            const long sh = static_cast<long>(sq.base + c) * a.H + h;
+            __syncthreads(); // dO and dS' are complete
+            f32x4 db[NC], x[NC];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int d = own.rb * 16 + r4 + e;
-                S[t][e] = a.dfin && d < a.dk ? a.dfin[st0 + static_cast<long>(d) * a.dv + 16 * t] : 0.f;
+            for (int t = 0; t < NC; ++t) {
+                bf16x8 f[KS][3];
+                get_all(f, sp[DELTA ? 0 : c & 1][t], lane);
+                db[t] = product<3>(kf, f, zero);
+                if (ROWS)
+                    db[t] *= ge;
+                db[t] = product_tri<3>(bt, gp[c & 1][t], w < 2, true, lane, db[t]);
+                x[t] = db[t];
+                if (DELTA)
+                    wp[t].put(col, i0, db[t] * beta);
             }
-    }
-    put_state(chunks - 1);
-
-    if (chunks > 0) {
-        if (w < 4) {
-            bf16x8 kf[KS][P::NPX], bt[2][3], nt[2][3];
-            f32x4 gi, ge, beta;
-            float E[NC][4];
-            TIn *dvp = static_cast<TIn *>(a.d_v) + static_cast<long>(sq.start) * a.H * a.dv + first;
-            auto load_db = [&](int c) {
-                load_tri(bt, ops(c).mat(1), UPPER, w, lane);
-                load_rows(kf, ops(c).op(0), w, lane);
-                if (ROWS)
-                    ge = ld4(ops(c).row(1) + i0);
-                if (DELTA)
-                    beta = ld4(ops(c).row(2) + i0);
-            };
-            auto load_n = [&](int c) {
-                if (DELTA)
-                    load_tri(nt, ops(c).mat(0), UPPER, w, lane);
-                if (ROWS)
-                    gi = ld4(ops(c).row(0) + i0);
-            };
-            auto load_e = [&](int c) {
-                if (!DELTA)
-                    return;
+            load_db(next);
+            if constexpr (DELTA) {
+                __syncthreads(); // beta db is complete; the planes of dS' are read
+#pragma unroll
+                for (int t = 0; t < NC; ++t) {
+                    x[t] = product_tri<3>(nt, wp[t], w < 2, true, lane, zero);
+                    zp[t].put(col, i0, ROWS ? -x[t] * gi : -x[t]);
+                }
+                load_n(next);
+                __syncthreads(); // z is complete
+            }
+            const ChunkRows<TIn> rows(dvp, width, c, sq.len, 16 * NC);
+#pragma unroll
+            for (int t = 0; t < NC; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    rows.store((i0 + e) * width + col + 16 * t, x[t][e]);
+                    if (DELTA)
+                        a.w_z[(sh * C + i0 + e) * a.dv + v0 + 16 * t] = x[t][e];
+                }
+            if constexpr (DELTA) {
+                f32x4 p = zero;
 #pragma unroll
                 for (int t = 0; t < NC; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        E[t][e] = a.save_e[((static_cast<long>(sq.base + c) * a.H + h) * C + i0 + e) * a.dv + v0 + 16 * t];
-            };
-            load_db(chunks - 1);
-            keep_order();
-            load_n(chunks - 1);
-            keep_order();
-            load_t(chunks - 1);
-            keep_order();
-            load_e(chunks - 1);
-            keep_order();
-            for (int c = chunks - 1; c >= 0; --c) {
-                const int next = c > 0 ? c - 1 : 0;
-                const long sh = static_cast<long>(sq.base + c) * a.H + h;
-                __syncthreads(); // dO and dS' are complete
-                f32x4 db[NC], x[NC];
+                        p[e] = fmaf(db[t][e], E[t][e], p[e]);
+                load_e(next);
 #pragma unroll
-                for (int t = 0; t < NC; ++t) {
-                    db[t] = product<3>(kf, sp[t], lane, zero);
-                    if (ROWS)
-                        db[t] *= ge;
-                    db[t] = product_tri<3>(bt, gp[c & 1][t], w < 2, true, lane, db[t]);
-                    x[t] = db[t];
-                    if (DELTA)
-                        wp[t].put(col, i0, db[t] * beta);
+                for (int e = 0; e < 4; ++e) {
+                    p[e] = add_row_ror<1>(p[e]);
+                    p[e] = add_row_ror<2>(p[e]);
+                    p[e] = add_row_ror<4>(p[e]);
+                    p[e] = add_row_ror<8>(p[e]);
                 }
-                load_db(next);
-                __syncthreads(); // beta db is complete; the planes of dS' are read
-                if constexpr (DELTA) {
-#pragma unroll
-                    for (int t = 0; t < NC; ++t) {
-                        x[t] = product_tri<3>(nt, wp[t], w < 2, true, lane, zero);
-                        zp[t].put(col, i0, ROWS ? -x[t] * gi : -x[t]);
-                    }
-                    load_n(next);
-                }
-                part(c);
-                if constexpr (DELTA)
-                    __syncthreads(); // z is complete
-                rest(c, next);
-                const ChunkRows<TIn> rows(dvp, width, c, sq.len, 16 * NC);
-#pragma unroll
-                for (int t = 0; t < NC; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        rows.store((i0 + e) * width + col + 16 * t, x[t][e]);
-                        if (DELTA)
-                            a.w_z[(sh * C + i0 + e) * a.dv + v0 + 16 * t] = x[t][e];
-                    }
-                if constexpr (DELTA) {
-                    f32x4 p = zero;
-#pragma unroll
-                    for (int t = 0; t < NC; ++t)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            p[e] = fmaf(db[t][e], E[t][e], p[e]);
-                    load_e(next);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        p[e] = add_row_ror<1>(p[e]);
-                        p[e] = add_row_ror<2>(p[e]);
-                        p[e] = add_row_ror<4>(p[e]);
-                        p[e] = add_row_ror<8>(p[e]);
-                        if (col == 0)
-                            a.w_db[(sh * tiles + wk.tile) * C + i0 + e] = p[e];
-                    }
-                }
-            }
-        } else {
-            // brings dO to LDS, a chunk ahead
-            f32x4 gi;
-            TIn g[NC][4];
-            const TIn *gbase = static_cast<const TIn *>(a.d_o) + static_cast<long>(sq.start) * a.H * a.dv + first;
-            auto load_g = [&](int c) {
-                if (a.d_o) {
-                    const ChunkRows<TIn> rows(gbase, width, c, sq.len, 16 * NC);
-#pragma unroll
-                    for (int t = 0; t < NC; ++t)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            g[t][e] = rows.load((i0 + e) * width + col + 16 * t);
-                }
-                if (ROWS)
-                    gi = ld4(ops(c).row(0) + i0);
-            };
-            auto put_g = [&](int c) {
-#pragma unroll
-                for (int t = 0; t < NC; ++t) {
-                    const f32x4 x = a.d_o ? f32x4{from_in(g[t][0]), from_in(g[t][1]), from_in(g[t][2]), from_in(g[t][3])} : zero;
-                    gp[c & 1][t].put(col, i0, x);
-                    if (ROWS)
-                        gg[c & 1][t].put(col, i0, x * gi);
-                }
-            };
-            load_g(chunks - 1);
-            put_g(chunks - 1);
-            keep_order();
-            load_g(chunks > 1 ? chunks - 2 : 0);
-            keep_order();
-            load_t(chunks - 1);
-            keep_order();
-            for (int c = chunks - 1; c >= 0; --c) {
-                const int next = c > 0 ? c - 1 : 0;
-                __syncthreads();
-                if (c > 0) {
-                    put_g(c - 1);
-                    load_g(c > 1 ? c - 2 : 0);
-                }
-                part(c);
-                __syncthreads();
-                if constexpr (DELTA)
-                    __syncthreads();
-                rest(c, next);
+                if (col == 0)
+                    *reinterpret_cast<f32x4 *>(&a.w_db[(sh * tiles + wk.tile) * C + i0]) = p;
             }
         }
+        return;
     }
-    if (a.dinit && own.has) {
+
+    const int wb = w - 4;
+    const bool has = Own::has(wb);
+    const long st0 = (static_cast<long>(n) * a.H + h) * a.dk * a.dv + v0;
+    f32x4 S[NC][RB], gam[RB], gi; // S: dS'
+    bf16x8 qt[RB][2][P::NPX], kt[RB][2][P::NPX];
+    TIn g[NC][4];
+    const TIn *gbase = static_cast<const TIn *>(a.d_o) + static_cast<long>(sq.start) * width + first;
+    auto load_g = [&](int c) {
+        if (a.d_o) {
+            const ChunkRows<TIn> rows(gbase, width, c, sq.len, 16 * NC);
+#pragma unroll
+            for (int t = 0; t < NC; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    g[t][e] = rows.load((i0 + e) * width + col + 16 * t);
+        }
+        if (ROWS)
+            gi = ld4(ops(c).row(0) + i0);
+    };
+    auto put_g = [&](int c) {
+#pragma unroll
+        for (int t = 0; t < NC; ++t) {
+            const f32x4 x = a.d_o ? f32x4{from_in(g[t][0]), from_in(g[t][1]), from_in(g[t][2]), from_in(g[t][3])} : zero;
+            gp[c & 1][t].put(col, i0, x);
+            if (ROWS)
+                gg[c & 1][t].put(col, i0, x * gi);
+        }
+    };
+    auto load_q = [&](int c) {
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            load_rows(qt[r], ops(c).op(1), Own::block(wb, r), lane);
+            gam[r] = ld4(ops(c).gam() + Own::block(wb, r) * 16 + r4);
+        }
+    };
+    auto load_k = [&](int c) {
+        if (!DELTA)
+            return;
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+            load_rows(kt[r], ops(c).op(2), Own::block(wb, r), lane);
+    };
+    auto put_state = [&](int c) { // the planes of the gradient of chunk c's end state
+        if (!has)
+            return;
 #pragma unroll
         for (int t = 0; t < NC; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int d = own.rb * 16 + r4 + e;
-                if (d < a.dk)
-                    a.dinit[st0 + static_cast<long>(d) * a.dv + 16 * t] = S[t][e];
+            for (int r = 0; r < RB; ++r) {
+                const int d0 = Own::block(wb, r) * 16 + r4;
+                sp[DELTA ? 0 : c & 1][t].put(col, d0, S[t][r]);
+                if (c >= 0) {
+                    const long sh = static_cast<long>(sq.base + c) * a.H + h;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (DKP > 32 || d0 + e < a.dk)
+                            a.w_ds[(sh * a.dk + d0 + e) * a.dv + v0 + 16 * t] = S[t][r][e];
+                }
             }
+    };
+#pragma unroll
+    for (int t = 0; t < NC; ++t)
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int d = Own::block(wb, r) * 16 + r4 + e;
+                S[t][r][e] = a.dfin && has && d < a.dk ? a.dfin[st0 + static_cast<long>(d) * a.dv + 16 * t] : 0.f;
+            }
+    put_state(chunks - 1);
+    if (chunks > 0) {
+        load_g(chunks - 1);
+        put_g(chunks - 1);
+        keep_order();
+        load_g(chunks > 1 ? chunks - 2 : 0);
+        keep_order();
+        load_q(chunks - 1);
+        keep_order();
+        load_k(chunks - 1);
+        keep_order();
+        for (int c = chunks - 1; c >= 0; --c) {
+            const int next = c > 0 ? c - 1 : 0;
+            __syncthreads();
+            // dS = Gam_C dS' + Q~^T dO - K~^T z, all but the last ahead of z
+#pragma unroll
+            for (int t = 0; t < NC; ++t) {
+                bf16x8 f[2][ROWS ? 3 : P::NPI];
+                if constexpr (ROWS)
+                    get_all(f, gg[c & 1][t], lane);
+                else
+                    get_all(f, gp[c & 1][t], lane);
+#pragma unroll
+                for (int r = 0; r < RB; ++r)
+                    S[t][r] = product<3>(qt[r], f, S[t][r] * gam[r]);
+            }
+            load_q(next);
+            put_g(c - 1); // (ahead of the first chunk: read by nobody)
+            load_g(c > 1 ? c - 2 : 0);
+            if constexpr (DELTA) {
+                __syncthreads();
+                __syncthreads();
+#pragma unroll
+                for (int t = 0; t < NC; ++t) {
+                    bf16x8 f[2][3];
+                    get_all(f, zp[t], lane);
+#pragma unroll
+                    for (int r = 0; r < RB; ++r)
+                        S[t][r] = product<3>(kt[r], f, S[t][r]);
+                }
+            }
+            put_state(c - 1);
+            load_k(next);
+        }
+    }
+    if (a.dinit && has) {
+#pragma unroll
+        for (int t = 0; t < NC; ++t)
+#pragma unroll
+            for (int r = 0; r < RB; ++r)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int d = Own::block(wb, r) * 16 + r4 + e;
+                    if (d < a.dk)
+                        a.dinit[st0 + static_cast<long>(d) * a.dv + 16 * t] = S[t][r][e];
+                }
     }
 }
 

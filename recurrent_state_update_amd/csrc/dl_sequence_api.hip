@@ -137,7 +137,7 @@ dl_status launch_scan(const dl_scan_desc *d, bool backward, const dl::ScanArgs &
     return e == hipSuccess ? DL_OK : DL_E_HIP;
 }
 
-constexpr long kNormBlocks = 512; // of a backward pass: two workgroups per CU, and as many partial sums per column
+constexpr long kNormBlocks = 1024; // of a backward pass: four workgroups per CU, and as many partial sums per column
 
 int gated_blocks(long rows, long H, int d)
 {

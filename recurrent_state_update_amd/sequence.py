@@ -38,6 +38,11 @@ def _on(device, stream):
     return ctx
 
 
+def _current(device):
+    """The raw handle of a device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _wants_grad(*tensors):
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
@@ -146,7 +151,8 @@ class _Scan:
     def forward(self, initial, final, rows, n_rows, saved=None):
         o = self.rows_like(self.shape["v"], self.dtype)
         ws = _bytes(dl_scan_workspace_bytes(self.desc), self.device)
-        _check(dl_scan(self.desc, initial, final, rows, n_rows, o, saved, ws), "dl_scan")
+        _check(dl_scan(self.desc, initial, final, rows, n_rows, o, saved, ws, _current(self.device)),
+               "dl_scan")
         return o
 
 
@@ -179,8 +185,8 @@ class _ScanFn(torch.autograd.Function):
             du = None if delta else torch.empty(s.H, s.dk, dtype=torch.float32, device=s.device)
             d0 = torch.empty(s.state_shape(), dtype=torch.float32, device=s.device) if ctx.with_initial else None
             ws = _bytes(dl_scan_backward_workspace_bytes(s.desc), s.device)
-            _check(dl_scan_backward(s.desc, saved, d_o, d_final, dq, dk, dv, dbeta, dld, du, d0, ws),
-                   "dl_scan_backward")
+            _check(dl_scan_backward(s.desc, saved, d_o, d_final, dq, dk, dv, dbeta, dld, du, d0, ws,
+                                    _current(s.device)), "dl_scan_backward")
         return None, dq, dk, dv, dbeta, dld, du, d0
 
 
@@ -251,7 +257,8 @@ def _gated_norm(o, gate, weight, eps):
     g, gs = _rows(gate, gate.dim() - 2)
     weight = None if weight is None else weight.contiguous()
     y = torch.empty(gate.shape, dtype=gate.dtype, device=o.device)
-    _check(dl_gated_norm(rows, H, d, DTYPES[o.dtype], DTYPES[gate.dtype], o, g, gs, weight, eps, y), "dl_gated_norm")
+    _check(dl_gated_norm(rows, H, d, DTYPES[o.dtype], DTYPES[gate.dtype], o, g, gs, weight, eps, y,
+                         _current(o.device)), "dl_gated_norm")
     return y, (o, g, weight), (rows, H, d, gs, eps)
 
 
@@ -276,7 +283,7 @@ class _GatedNormFn(torch.autograd.Function):
                 dw = torch.empty_like(weight)
                 ws = _bytes(dl_gated_norm_workspace_bytes(rows, H, d), o.device)
             _check(dl_gated_norm_backward(rows, H, d, DTYPES[o.dtype], DTYPES[g.dtype], o, g, gs, weight, eps,
-                                          dy, d_o, dg, dw, ws), "dl_gated_norm_backward")
+                                          dy, d_o, dg, dw, ws, _current(o.device)), "dl_gated_norm_backward")
         return d_o, dg, dw, None
 
 
@@ -309,7 +316,8 @@ def _residual_norm(x, y, scale, weight, eps, dtype):
     x, y, scale, weight = (None if t is None else t.contiguous() for t in (x, y, scale, weight))
     x_out = None if y is None else torch.empty_like(x)
     h = torch.empty(x.shape, dtype=dtype, device=x.device)
-    _check(dl_residual_norm(rows, D, DTYPES[dtype], x, y, scale, weight, eps, x_out, h), "dl_residual_norm")
+    _check(dl_residual_norm(rows, D, DTYPES[dtype], x, y, scale, weight, eps, x_out, h,
+                            _current(x.device)), "dl_residual_norm")
     return (x_out, h), (x if y is None else x_out, y if scale is not None else None, scale, weight), \
         (rows, D, eps, dtype, y is not None)
 
@@ -339,7 +347,7 @@ class _ResidualNormFn(torch.autograd.Function):
             if ds is not None or dw is not None:
                 ws = _bytes(dl_residual_norm_workspace_bytes(rows, D), x.device)
             _check(dl_residual_norm_backward(rows, D, DTYPES[dtype], x, y, scale, weight, eps, d_x_out, d_h, dx,
-                                             dy, ds, dw, ws), "dl_residual_norm_backward")
+                                             dy, ds, dw, ws, _current(x.device)), "dl_residual_norm_backward")
         return dx, dy, ds, dw, None, None
 
 
