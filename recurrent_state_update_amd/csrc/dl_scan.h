@@ -222,7 +222,7 @@ __device__ __forceinline__ Chunk chunk_of(const ScanArgs &a, int slot)
 // row l % 16, k from 8 (l / 16): one coalesced 1 KiB load per fragment.
 //   forward : op 0 K~ [C][DKP], 1 Q~ [C][DKP], 2 K^T^ [DKP][C]; mat 0 N, 1 B
 //   backward: op 0 K^ [C][DKP], 1 Q~^T [DKP][C], 2 K~^T [DKP][C]; mat 0 N^T,
-//             1 B^T, 2 A and (GDN) B in fp32 blocks (store_pairs)
+//             1 B^T, 2 A and (GDN) B in fp32 blocks (store_pair)
 // (ROWS: K and Q without their decays.)  Of the triangular C x C operands the
 // fragments of zeros are neither written nor read.
 template <int NP, int DKP> struct Ops {
@@ -278,7 +278,8 @@ template <int N, int ROWS, int K, Part PART = ALL, typename F> __device__ __forc
 }
 
 // N = (I + L)^-1 for a unit lower triangular I + L of C x C fp32 in LDS (row
-// stride MLD, upper part of N zero beforehand): the four diagonal blocks by
+// stride MLD; of L only what is below the diagonal is read, and of N the
+// blocks above it are zero beforehand): the four diagonal blocks by
 // forward substitution, wave w taking block w, one column per lane; then
 // N_IJ = -N_II sum_{J <= K < I} L_IK N_KJ by block diagonals on the fp32
 // matrix instructions.  tmp: 16 x 20 floats of this wave's own.  For whole

@@ -26,6 +26,8 @@ template <auto *KERNEL> hipError_t set_lds(int bytes)
     return e;
 }
 
+constexpr long kCus = 256;
+
 inline bool at16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 template <int OP, typename TIn, int DKP, bool BWD> hipError_t launch_prep(const ScanArgs &a, hipStream_t st)
@@ -56,14 +58,23 @@ inline dim3 carry_grid(const ScanArgs &a, int nc)
     return dim3((a.N * a.H + kXcds - 1) / kXcds * kXcds * (a.dv / (16 * nc)));
 }
 
+// Value tiles of 32 columns instead of 16 where they still give every CU a
+// workgroup: the operands are read half as often, but half as many workgroups
+// run.  Carry of 1024 tokens, d = 128, us (16 columns, 32): 256 workgroups of 32
+// GDN 60.5, 49.0, KDA 87.5, 63.3; 128 of them KDA 41.6, 54.9.
+inline bool wide_tiles(const ScanArgs &a)
+{
+    return a.dv % 32 == 0 && static_cast<long>(a.N) * a.H * (a.dv / 32) >= kCus;
+}
+
 template <int OP, typename TIn, int DKP> hipError_t scan_forward_t(const ScanArgs &a, hipStream_t st)
 {
     if (hipError_t e = launch_prep<OP, TIn, DKP, false>(a, st); e != hipSuccess)
         return e;
-    if (a.save_s)
-        hipLaunchKernelGGL((scan_carry_kernel<OP, TIn, DKP, 1, true>), carry_grid(a, 1), dim3(512), 0, st, a);
-    else
-        hipLaunchKernelGGL((scan_carry_kernel<OP, TIn, DKP, 1, false>), carry_grid(a, 1), dim3(512), 0, st, a);
+    const bool wide = wide_tiles(a);
+    auto *carry = a.save_s ? (wide ? scan_carry_kernel<OP, TIn, DKP, 2, true> : scan_carry_kernel<OP, TIn, DKP, 1, true>)
+                           : (wide ? scan_carry_kernel<OP, TIn, DKP, 2, false> : scan_carry_kernel<OP, TIn, DKP, 1, false>);
+    hipLaunchKernelGGL(carry, carry_grid(a, wide ? 2 : 1), dim3(512), 0, st, a);
     return hipGetLastError();
 }
 
@@ -71,7 +82,9 @@ template <int OP, typename TIn, int DKP> hipError_t scan_backward_t(const ScanAr
 {
     if (hipError_t e = launch_prep<OP, TIn, DKP, true>(a, st); e != hipSuccess)
         return e;
-    hipLaunchKernelGGL((scan_carry_bwd_kernel<OP, TIn, DKP, 1>), carry_grid(a, 1), dim3(512), 0, st, a);
+    const bool wide = wide_tiles(a);
+    auto *carry = wide ? scan_carry_bwd_kernel<OP, TIn, DKP, 2> : scan_carry_bwd_kernel<OP, TIn, DKP, 1>;
+    hipLaunchKernelGGL(carry, carry_grid(a, wide ? 2 : 1), dim3(512), 0, st, a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess)
         return e;
     const bool vec = at16(a.q) && at16(a.k) && at16(a.v) && at16(a.d_o) && a.qs % 8 == 0 && a.ks % 8 == 0 &&
@@ -81,7 +94,8 @@ template <int OP, typename TIn, int DKP> hipError_t scan_backward_t(const ScanAr
     constexpr auto *grads = scan_grads_kernel<OP, TIn, DKP>;
     if (hipError_t e = set_lds<grads>(sizeof(Lds)); e != hipSuccess)
         return e;
-    hipLaunchKernelGGL(grads, dim3(a.slots * a.H), dim3(DKP * 4), sizeof(Lds), st, a, vec, a.dv / 16);
+    hipLaunchKernelGGL(grads, dim3(a.slots * a.H), dim3(DKP * 4), sizeof(Lds), st, a, vec,
+                       a.dv / (wide ? 32 : 16));
     if (hipError_t e = hipGetLastError(); e != hipSuccess)
         return e;
     if (OP == RWKV6) {

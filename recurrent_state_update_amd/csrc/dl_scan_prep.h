@@ -24,28 +24,76 @@ template <typename TIn> __device__ __forceinline__ void load_piece(TIn (&x)[8], 
     }
 }
 
-// A (and B) in fp32 for grads: the ten blocks of the lower triangle, a lane's
-// four rows of its column as in a product's result.
-__device__ __forceinline__ void store_pairs(__bf16 *mat, const float *A, const float *B, int n)
+// The ten 16 x 16 blocks (I, J) of a lower triangle, numbered row by row.
+__device__ __forceinline__ int block_row(int b) { return b < 1 ? 0 : b < 3 ? 1 : b < 6 ? 2 : 3; }
+__device__ __forceinline__ int block_col(int b)
 {
-    for (int it = threadIdx.x; it < n * 640; it += blockDim.x) {
-        const int l = it & 63, b = (it >> 6) % 10;
-        const float *x = it < 640 ? A : B;
-        const int I = b < 1 ? 0 : b < 3 ? 1 : b < 6 ? 2 : 3, J = b - I * (I + 1) / 2;
-        f32x4 v;
+    const int I = block_row(b);
+    return b - I * (I + 1) / 2;
+}
+// A (and B) in fp32 for grads: the ten blocks, a lane's four rows of its
+// column as in a product's result; n: block, or 10 + block for B.
+__device__ __forceinline__ void store_pair(__bf16 *mat, int n, int lane, f32x4 v)
+{
+    reinterpret_cast<f32x4 *>(mat)[n * 64 + lane] = v;
+}
+
+// The C x C matrices of a chunk, once the keys' tiles are done with.
+struct PrepMats {
+    float L[C * MLD], B[C * MLD], N[C * MLD]; // L = A diag(beta); B's room then serves the inverse
+};
+// A result block in LDS.
+__device__ __forceinline__ void put_block(float *m, int I, int J, int lane, f32x4 v)
+{
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            v[e] = x[(I * 16 + (l >> 4) * 4 + e) * MLD + J * 16 + (l & 15)];
-        reinterpret_cast<f32x4 *>(mat)[it] = v;
+    for (int e = 0; e < 4; ++e)
+        m[(I * 16 + (lane >> 4) * 4 + e) * MLD + J * 16 + (lane & 15)] = v[e];
+}
+// Zero the six blocks above the diagonal.
+__device__ __forceinline__ void zero_above(float *m)
+{
+    for (int it = threadIdx.x; it < 6 * 64; it += blockDim.x) {
+        const int b = it >> 6, J = b < 1 ? 1 : b < 3 ? 2 : 3, I = b - J * (J - 1) / 2;
+        *reinterpret_cast<f32x4 *>(&m[(I * 16 + (it & 63) / 4) * MLD + J * 16 + it % 4 * 4]) = f32x4{0, 0, 0, 0};
+    }
+}
+// From L and B in LDS: B's and N's planes.
+template <int OP, typename TIn, bool BWD, int NP, int DKP>
+__device__ __forceinline__ void store_mats(PrepMats &m, const Ops<NP, DKP> &ops, int w, int lane)
+{
+    using P = Plan<OP, TIn>;
+    if (BWD)
+        store_op<3, C, C, UPPER>(ops.mat(1), [&](int i, int j) { return m.B[j * MLD + i]; });
+    else
+        store_op<P::NPB, C, C, LOWER>(ops.mat(1), [&](int i, int j) { return m.B[i * MLD + j]; });
+    if constexpr (P::DELTA) {
+        __syncthreads(); // B is read: its room is the waves' scratch
+        invert_unit_lower(m.L, m.N, m.B + (w & 3) * 16 * 20, w, lane);
+        if (BWD)
+            store_op<3, C, C, UPPER>(ops.mat(0), [&](int i, int j) { return m.N[j * MLD + i]; });
+        else
+            store_op<3, C, C, LOWER>(ops.mat(0), [&](int i, int j) { return m.N[i * MLD + j]; });
     }
 }
 
+// ---- per-key decays (KDA, RWKV6)
+
+// Keys are taken in passes of DP: their tiles then leave LDS for two
+// workgroups on a CU.
+template <int DKP> constexpr int prep_keys() { return DKP < 64 ? DKP : 64; }
+template <int DKP> constexpr int prep_threads() { return 8 * prep_keys<DKP>(); }
+
 template <int OP, int DKP> struct PrepLds {
-    static constexpr int LD = DKP + 4;
-    float k[C * LD], q[C * LD], e[C * LD];
-    float B[C * MLD], A[OP == RWKV6 ? 4 : C * MLD];
-    float eb[4 * DKP], inv[4 * DKP]; // per 16-row block: its decay, and one over it
-    float pre[4 * DKP], suf[4 * DKP]; // that of the blocks before, after
+    static constexpr int DP = prep_keys<DKP>(), LD = DP + 4;
+    union {
+        struct {
+            float k[C * LD], q[C * LD], e[C * LD];
+        };
+        PrepMats m;
+    };
+    float eb[4 * DP], inv[4 * DP]; // per 16-row block: its decay, and one over it
+    float pre[4 * DP], suf[4 * DP]; // that of the blocks before, after
+    float pair[2][4][16 * 16];      // B, A of diagonal blocks formed pair by pair
     float beta[C], diag[C];
     int strong[4];
 };
@@ -56,20 +104,19 @@ template <int OP, int DKP> struct PrepLds {
 // Pairs of tokens of two blocks of 16 rows I >= J are products of rows scaled
 // by the decay from I's start (prefix) and to J's end (suffix x the blocks
 // between), all <= 1, on the fp32 matrix instructions.  Within a block (I = J)
-// that is Gam_C too much, and the suffix is divided by the block's decay:
-// relative rounding only, as long as the decay is far from underflow.  Blocks
-// where a key decays by more than 2^-40 take the vector unit instead, with a
-// running product of decays per pair and key.
+// that is the block's decay too much, and the suffix is divided by it: relative
+// rounding only, as long as the decay is far from underflow.  Blocks where a
+// key decays by more than 2^-40 take the vector unit instead, with a running
+// product of decays per pair and key.
 //
-// Bound by latency (one workgroup of eight waves fits a CU, for its LDS).
-template <int DKP> constexpr int prep_threads() { return DKP == 128 ? 512 : 256; }
-
+// Bound by latency: a handful of short phases between barriers.
 template <int OP, typename TIn, int DKP, bool BWD>
-__global__ __launch_bounds__(prep_threads<DKP>()) void scan_prep_kernel(ScanArgs a, bool vec)
+__global__ __launch_bounds__(prep_threads<DKP>(), 4) void scan_prep_kernel(ScanArgs a, bool vec)
 {
     using P = Plan<OP, TIn>;
     constexpr bool DELTA = P::DELTA;
-    constexpr int LD = DKP + 4, NT = prep_threads<DKP>(), NW = NT / 64;
+    constexpr int DP = prep_keys<DKP>(), LD = DP + 4, NT = prep_threads<DKP>(), NW = NT / 64;
+    constexpr int TASKS = ((DELTA ? 20 : 10) + NW - 1) / NW;
     extern __shared__ __align__(16) char smem[];
     PrepLds<OP, DKP> &s = *reinterpret_cast<PrepLds<OP, DKP> *>(smem);
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -79,231 +126,260 @@ __global__ __launch_bounds__(prep_threads<DKP>()) void scan_prep_kernel(ScanArgs
         return;
     const Ops<P::NPX, DKP> ops(a, static_cast<long>(slot) * a.H + h);
 
-    // rows behind the end: k = q = 0, no decay, beta = 0
-    constexpr int PIECES = C * DKP / 8 / NT;
-    static_assert(PIECES >= 1, "every thread has a piece");
-    {
-        TIn xk[PIECES][8], xq[PIECES][8];
-        float xl[PIECES][8];
+    if (tid < C) {
+        s.beta[tid] = DELTA && tid < ch.rows ? a.beta[(static_cast<long>(ch.t0) + tid) * a.H + h] : 0.f;
+        ops.row(2)[tid] = s.beta[tid];
+    }
+    for (int it = tid; it < 2 * 4 * 256 / 4; it += NT)
+        reinterpret_cast<f32x4 *>(s.pair)[it] = f32x4{0, 0, 0, 0};
+    f32x4 acc[TASKS];
 #pragma unroll
-        for (int p = 0; p < PIECES; ++p) {
-            const int i = (p * NT + tid) / (DKP / 8), d = (p * NT + tid) % (DKP / 8) * 8;
-            const bool in = i < ch.rows && d < a.dk;
-            const long t = static_cast<long>(ch.t0) + i, c = static_cast<long>(h) * a.dk + d;
-            load_piece(xk[p], static_cast<const TIn *>(a.k) + t * a.ks + c, in, vec);
-            load_piece(xq[p], static_cast<const TIn *>(a.q) + t * a.qs + c, in, vec);
-            load_piece(xl[p], a.ld + t * a.H * a.dk + c, in, vec);
-        }
-#pragma unroll
-        for (int p = 0; p < PIECES; ++p) {
-            const int i = (p * NT + tid) / (DKP / 8), d = (p * NT + tid) % (DKP / 8) * 8;
+    for (int p = 0; p < TASKS; ++p)
+        acc[p] = f32x4{0, 0, 0, 0};
+    float ruk = 0.f; // RWKV6: B_ii = sum r u k, NT / C lanes per row
+
+#pragma unroll 1
+    for (int d0 = 0; d0 < DKP; d0 += DP) {
+        // rows behind the end: k = q = 0, no decay, beta = 0
+        constexpr int PIECES = C * DP / 8 / NT;
+        static_assert(PIECES == 1, "one piece per thread");
+        const int pi = tid / (DP / 8), pd = tid % (DP / 8) * 8;
+        {
+            TIn xk[8], xq[8];
+            float xl[8];
+            const bool in = pi < ch.rows && d0 + pd < a.dk;
+            const long t = static_cast<long>(ch.t0) + pi, c = static_cast<long>(h) * a.dk + d0 + pd;
+            load_piece(xk, static_cast<const TIn *>(a.k) + t * a.ks + c, in, vec);
+            load_piece(xq, static_cast<const TIn *>(a.q) + t * a.qs + c, in, vec);
+            load_piece(xl, a.ld + t * a.H * a.dk + c, in, vec);
+            if (d0 > 0)
+                __syncthreads(); // the pass before is read
+            if (tid < 4)
+                s.strong[tid] = 0;
 #pragma unroll
             for (int half = 0; half < 8; half += 4) {
                 f32x4 kv, qv, ev;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    kv[e] = from_in(xk[p][half + e]);
-                    qv[e] = from_in(xq[p][half + e]);
-                    ev[e] = expf(floor_log_decay(xl[p][half + e])); // 1 behind the end
+                    kv[e] = from_in(xk[half + e]);
+                    qv[e] = from_in(xq[half + e]);
+                    ev[e] = expf(floor_log_decay(xl[half + e])); // 1 behind the end
                 }
-                *reinterpret_cast<f32x4 *>(&s.k[i * LD + d + half]) = kv;
-                *reinterpret_cast<f32x4 *>(&s.q[i * LD + d + half]) = qv;
-                *reinterpret_cast<f32x4 *>(&s.e[i * LD + d + half]) = ev;
+                *reinterpret_cast<f32x4 *>(&s.k[pi * LD + pd + half]) = kv;
+                *reinterpret_cast<f32x4 *>(&s.q[pi * LD + pd + half]) = qv;
+                *reinterpret_cast<f32x4 *>(&s.e[pi * LD + pd + half]) = ev;
             }
         }
-    }
-    if (tid < C) {
-        s.beta[tid] = DELTA && tid < ch.rows ? a.beta[(static_cast<long>(ch.t0) + tid) * a.H + h] : 0.f;
-        ops.row(2)[tid] = s.beta[tid];
-    }
-    if (tid < 4)
-        s.strong[tid] = 0;
-    for (int it = tid; it < C * MLD; it += NT) {
-        s.B[it] = 0.f;
-        if (DELTA)
-            s.A[it] = 0.f;
-    }
-    __syncthreads();
+        __syncthreads();
 
-    const int d = tid % DKP, I0 = tid / DKP, r0 = I0 * 16; // one thread per (key, block)
-    const bool mine = tid < 4 * DKP;
-    float ev[16];
-    if (mine) {
-        float p = 1.f;
+        const int d = tid % DP, I0 = tid / DP, r0 = I0 * 16; // one thread per (key, block)
+        const bool mine = tid < 4 * DP;
+        float ev[16];
+        if (mine) {
+            float p = 1.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            ev[i] = s.e[(r0 + i) * LD + d];
-            p *= ev[i];
+            for (int i = 0; i < 16; ++i) {
+                ev[i] = s.e[(r0 + i) * LD + d];
+                p *= ev[i];
+            }
+            s.eb[tid] = p;
+            s.inv[tid] = 1.f / p;
+            if (!(p >= 0x1p-40f)) // a NaN decay takes the pairwise way as well
+                s.strong[I0] = 1;
         }
-        s.eb[tid] = p;
-        s.inv[tid] = 1.f / p;
-        if (!(p >= 0x1p-40f)) // a NaN decay takes the pairwise way as well
-            s.strong[I0] = 1;
-    }
-    if (!DELTA) { // B_ii = sum r u k: NT / 64 lanes per row
-        constexpr int G = NT / C;
-        const int i = tid / G;
-        float x = 0.f;
-        for (int c = tid % G; c < a.dk; c += G)
-            x = fmaf(s.q[i * LD + c] * a.u[static_cast<long>(h) * a.dk + c], s.k[i * LD + c], x);
-#pragma unroll
-        for (int m = 1; m < G; m *= 2)
-            x += __shfl_xor(x, m);
-        if (tid % G == 0)
-            s.diag[i] = x;
-    }
-    __syncthreads();
+        if (!DELTA) {
+            constexpr int G = NT / C;
+            for (int c = tid % G; c < DP && d0 + c < a.dk; c += G)
+                ruk = fmaf(s.q[tid / G * LD + c] * a.u[static_cast<long>(h) * a.dk + d0 + c], s.k[tid / G * LD + c], ruk);
+        }
+        __syncthreads();
 
-    const int strong[4] = {s.strong[0], s.strong[1], s.strong[2], s.strong[3]};
-    if (strong[0] | strong[1] | strong[2] | strong[3]) {
-        // wave w takes block w; lane = (column j, quarter of the keys)
-        const int j = lane & 15, g = lane >> 4, b0 = w * 16;
-        if (w < 4 && s.strong[w]) {
-            float sa[16], sb[16];
+        const int strong[4] = {s.strong[0], s.strong[1], s.strong[2], s.strong[3]};
+        if (strong[0] | strong[1] | strong[2] | strong[3]) {
+            // wave w takes block w; lane = (column j, quarter of the keys)
+            const int j = lane & 15, g = lane >> 4, b0 = w * 16;
+            if (w < 4 && s.strong[w]) {
+                float sa[16], sb[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                sa[i] = sb[i] = 0.f;
-            for (int c = g * (DKP / 4); c < (g + 1) * (DKP / 4); ++c) {
-                const float kj = s.k[(b0 + j) * LD + c];
-                float kd = 0.f; // P_ij k_j
+                for (int i = 0; i < 16; ++i)
+                    sa[i] = sb[i] = 0.f;
+                for (int c = g * (DP / 4); c < (g + 1) * (DP / 4); ++c) {
+                    const float kj = s.k[(b0 + j) * LD + c];
+                    float kd = 0.f; // P_ij k_j
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float e = s.e[(b0 + i) * LD + c], qi = s.q[(b0 + i) * LD + c];
+                        if (!DELTA)
+                            sb[i] = fmaf(kd, qi, sb[i]); // before the decay of row i
+                        kd = i == j ? kj : kd * e;
+                        if (DELTA) {
+                            sb[i] = fmaf(kd, qi, sb[i]);
+                            sa[i] = fmaf(kd, s.k[(b0 + i) * LD + c], sa[i]);
+                        }
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float e = s.e[(b0 + i) * LD + c], qi = s.q[(b0 + i) * LD + c];
-                    if (!DELTA)
-                        sb[i] = fmaf(kd, qi, sb[i]); // before the decay of row i
-                    kd = i == j ? kj : kd * e;
-                    if (DELTA) {
-                        sb[i] = fmaf(kd, qi, sb[i]);
-                        sa[i] = fmaf(kd, s.k[(b0 + i) * LD + c], sa[i]);
+                    const float va = DELTA ? wave_sum_from<16>(sa[i]) : 0.f, vb = wave_sum_from<16>(sb[i]);
+                    if (g == 0) {
+                        s.pair[0][w][i * 16 + j] += vb;
+                        s.pair[1][w][i * 16 + j] += va;
                     }
                 }
             }
+            __syncthreads();
+        }
+
+        // in place: k -> k (prefix in its block), q -> q (prefix), e -> k (suffix)
+        if (mine) {
+            float kv[16], p = 1.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float va = DELTA ? wave_sum_from<16>(sa[i]) : 0.f, vb = wave_sum_from<16>(sb[i]);
-                if (g == 0) {
-                    if (DELTA)
-                        s.A[(b0 + i) * MLD + b0 + j] = i > j ? va : 0.f;
-                    s.B[(b0 + i) * MLD + b0 + j] = i > j ? vb : i < j ? 0.f : DELTA ? vb : s.diag[b0 + i];
-                }
+                kv[i] = s.k[(r0 + i) * LD + d];
+                const float before = p;
+                p *= ev[i];
+                s.q[(r0 + i) * LD + d] *= DELTA ? p : before;
+                s.k[(r0 + i) * LD + d] = kv[i] * p;
+            }
+            p = 1.f;
+#pragma unroll
+            for (int i = 15; i >= 0; --i) {
+                s.e[(r0 + i) * LD + d] = kv[i] * p;
+                p *= ev[i];
+            }
+        } else if (tid - 4 * DP < DP) {
+            const int c = tid - 4 * DP;
+            float p = 1.f, q = 1.f;
+#pragma unroll
+            for (int I = 0; I < 4; ++I) {
+                s.pre[I * DP + c] = p;
+                p *= s.eb[I * DP + c];
+                s.suf[(3 - I) * DP + c] = q;
+                q *= s.eb[(3 - I) * DP + c];
+            }
+            ops.gam()[d0 + c] = p;
+        }
+        __syncthreads();
+
+        // pairs of tokens: a wave takes blocks of B (0-9) and A (10-19)
+#pragma unroll
+        for (int p = 0; p < TASKS; ++p) {
+            const int task = w + p * NW;
+            if (task >= (DELTA ? 20 : 10))
+                break;
+            const int b = task >= 10 ? task - 10 : task, I = block_row(b), J = block_col(b);
+            if (I == J && strong[I])
+                continue;
+            const float *left = task >= 10 ? s.k : s.q;
+#pragma unroll
+            for (int ks = 0; ks < DP / 16; ++ks) {
+                const int c = ks * 16 + (lane >> 4) * 4;
+                f32x4 r = *reinterpret_cast<const f32x4 *>(&s.e[(J * 16 + (lane & 15)) * LD + c]);
+                if (I == J)
+                    r *= *reinterpret_cast<const f32x4 *>(&s.inv[I * DP + c]);
+                for (int K = J + 1; K < I; ++K)
+                    r *= *reinterpret_cast<const f32x4 *>(&s.eb[K * DP + c]);
+                acc[p] = mfma32x4(*reinterpret_cast<const f32x4 *>(&left[(I * 16 + (lane & 15)) * LD + c]), r, acc[p]);
             }
         }
-        __syncthreads();
+
+        // operands of C x DKP: this pass's keys
+        constexpr int KP = DP / 32, KA = DKP / 32;
+        auto rows = [&](auto np, __bf16 *op, const float *x, const float *scale) {
+            constexpr int NPL = decltype(np)::value;
+            for (int it = tid; it < 4 * KP * 64; it += NT) {
+                const int l = it & 63, rb = (it >> 6) / KP, ks = (it >> 6) % KP, c = ks * 32 + (l >> 4) * 8;
+                f32x8 v;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = x[(rb * 16 + (l & 15)) * LD + c + e] * scale[rb * DP + c + e];
+                bf16x8 f[NPL];
+                split(v, f);
+                store_frag(op, KA, rb, d0 / 32 + ks, l, f);
+            }
+        };
+        auto columns = [&](auto np, __bf16 *op, const float *x, const float *scale) {
+            constexpr int NPL = decltype(np)::value;
+            for (int it = tid; it < DP / 16 * 2 * 64; it += NT) {
+                const int l = it & 63, rb = (it >> 6) / 2, ks = (it >> 6) % 2, c = rb * 16 + (l & 15), i = ks * 32 + (l >> 4) * 8;
+                const float f0 = scale[i / 16 * DP + c];
+                f32x8 v;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = x[(i + e) * LD + c] * f0;
+                bf16x8 f[NPL];
+                split(v, f);
+                store_frag(op, 2, d0 / 16 + rb, ks, l, f);
+            }
+        };
+        constexpr std::integral_constant<int, P::NPX> npx;
+        constexpr std::integral_constant<int, P::NPQ> npq;
+        if (!BWD) {
+            if (DELTA)
+                rows(npx, ops.op(0), s.k, s.pre);
+            rows(npq, ops.op(1), s.q, s.pre);
+            columns(npx, ops.op(2), s.e, s.suf);
+        } else {
+            rows(npx, ops.op(0), s.e, s.suf);
+            columns(npx, ops.op(1), s.q, s.pre);
+            if (DELTA)
+                columns(npx, ops.op(2), s.k, s.pre);
+        }
     }
 
-    // in place: k -> k (prefix in its block), q -> q (prefix), e -> k (suffix)
-    if (mine) {
-        float kv[16], p = 1.f;
+    if (!DELTA) {
+        constexpr int G = NT / C;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            kv[i] = s.k[(r0 + i) * LD + d];
-            const float before = p;
-            p *= ev[i];
-            s.q[(r0 + i) * LD + d] *= DELTA ? p : before;
-            s.k[(r0 + i) * LD + d] = kv[i] * p;
-        }
-        p = 1.f;
-#pragma unroll
-        for (int i = 15; i >= 0; --i) {
-            s.e[(r0 + i) * LD + d] = kv[i] * p;
-            p *= ev[i];
-        }
+        for (int m = 1; m < G; m *= 2)
+            ruk += __shfl_xor(ruk, m);
+        if (tid % G == 0)
+            s.diag[tid / G] = ruk;
     }
-    if (tid < DKP) {
-        float p = 1.f, q = 1.f;
+    __syncthreads(); // the tiles are read
+    zero_above(s.m.B);
+    if (DELTA)
+        zero_above(s.m.N);
 #pragma unroll
-        for (int I = 0; I < 4; ++I) {
-            s.pre[I * DKP + tid] = p;
-            p *= s.eb[I * DKP + tid];
-            s.suf[(3 - I) * DKP + tid] = q;
-            q *= s.eb[(3 - I) * DKP + tid];
-        }
-        ops.gam()[tid] = p;
-    }
-    __syncthreads();
-
-    // pairs of tokens: a wave takes one of the ten block pairs, of A or of B
-    for (int task = w; task < (DELTA ? 20 : 10); task += NW) {
+    for (int p = 0; p < TASKS; ++p) {
+        const int task = w + p * NW;
+        if (task >= (DELTA ? 20 : 10))
+            break;
         const bool isA = task >= 10;
-        const int pair = isA ? task - 10 : task;
-        const int I = pair < 1 ? 0 : pair < 3 ? 1 : pair < 6 ? 2 : 3, J = pair - I * (I + 1) / 2;
-        if (I == J && strong[I])
-            continue;
-        const float *left = isA ? s.k : s.q;
-        f32x4 x = {0, 0, 0, 0};
+        const int b = isA ? task - 10 : task, I = block_row(b), J = block_col(b), j = lane & 15;
+        f32x4 v = acc[p];
+        if (I == J) {
 #pragma unroll
-        for (int ks = 0; ks < DKP / 16; ++ks) {
-            const int c = ks * 16 + (lane >> 4) * 4;
-            f32x4 r = *reinterpret_cast<const f32x4 *>(&s.e[(J * 16 + (lane & 15)) * LD + c]);
-            if (I == J)
-                r *= *reinterpret_cast<const f32x4 *>(&s.inv[I * DKP + c]);
-            for (int K = J + 1; K < I; ++K)
-                r *= *reinterpret_cast<const f32x4 *>(&s.eb[K * DKP + c]);
-            x = mfma32x4(*reinterpret_cast<const f32x4 *>(&left[(I * 16 + (lane & 15)) * LD + c]), r, x);
+            for (int e = 0; e < 4; ++e) {
+                const int i = (lane >> 4) * 4 + e;
+                const float x = v[e] + s.pair[isA][I][i * 16 + j];
+                v[e] = i > j ? x : i < j || isA ? 0.f : DELTA ? x : s.diag[I * 16 + i];
+            }
         }
-        const int j = lane & 15;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = (lane >> 4) * 4 + e;
-            float v = x[e];
-            if (I == J)
-                v = i > j ? v : i < j || isA ? 0.f : DELTA ? v : s.diag[I * 16 + i];
-            (isA ? s.A : s.B)[(I * 16 + i) * MLD + J * 16 + j] = v;
+        if (isA) {
+            if (BWD)
+                store_pair(ops.mat(2), b, lane, v);
+            v *= s.beta[J * 16 + j];
         }
+        put_block(isA ? s.m.L : s.m.B, I, J, lane, v);
     }
     __syncthreads();
-
-    // operands of C x DKP
-    auto kt = [&](int i, int d) { return s.k[i * LD + d] * s.pre[(i >> 4) * DKP + d]; };
-    auto qt = [&](int i, int d) { return s.q[i * LD + d] * s.pre[(i >> 4) * DKP + d]; };
-    auto kh = [&](int i, int d) { return s.e[i * LD + d] * s.suf[(i >> 4) * DKP + d]; };
-    if (!BWD) {
-        if (DELTA)
-            store_op<P::NPX, C, DKP>(ops.op(0), kt);
-        store_op<P::NPQ, C, DKP>(ops.op(1), qt);
-        store_op<P::NPX, DKP, C>(ops.op(2), [&](int d, int i) { return kh(i, d); });
-        store_op<P::NPB, C, C, LOWER>(ops.mat(1), [&](int i, int j) { return s.B[i * MLD + j]; });
-    } else {
-        store_op<P::NPX, C, DKP>(ops.op(0), kh);
-        store_op<P::NPX, DKP, C>(ops.op(1), [&](int d, int i) { return qt(i, d); });
-        if (DELTA)
-            store_op<P::NPX, DKP, C>(ops.op(2), [&](int d, int i) { return kt(i, d); });
-        store_op<3, C, C, UPPER>(ops.mat(1), [&](int i, int j) { return s.B[j * MLD + i]; });
-        if (DELTA)
-            store_pairs(ops.mat(2), s.A, s.A, 1);
-    }
-    if (tid < C)
-        ops.row(2)[tid] = s.beta[tid];
-    if constexpr (DELTA) {
-        // the operands are written: their LDS is free
-        float *const area = reinterpret_cast<float *>(smem);
-        static_assert(C * MLD + 4 * 16 * 20 <= 3 * C * LD, "N and the scratch of four waves fit");
-        float *L = s.A, *N = area;
-        __syncthreads();
-        for (int it = tid; it < C * C; it += NT) {
-            const int i = it / C, j = it % C;
-            L[i * MLD + j] *= s.beta[j];
-            N[i * MLD + j] = 0.f;
-        }
-        __syncthreads();
-        invert_unit_lower(L, N, area + C * MLD + w * 16 * 20, w, lane);
-        if (BWD)
-            store_op<3, C, C, UPPER>(ops.mat(0), [&](int i, int j) { return N[j * MLD + i]; });
-        else
-            store_op<3, C, C, LOWER>(ops.mat(0), [&](int i, int j) { return N[i * MLD + j]; });
-    }
+    store_mats<OP, TIn, BWD>(s.m, ops, w, lane);
 }
 
-// GDN: the decay is one number per row, so A and B are K K^T and Q K^T (exact
-// products of the inputs' own planes) times the matrix of P_ij, and the keys'
-// operands are the inputs themselves.
+// ---- one decay per row (GDN)
+
+// A and B are K K^T and Q K^T (exact products of the inputs' own planes) times
+// the matrix of P_ij, and the keys' operands are the inputs themselves.
 template <typename TIn, int DKP> struct PrepGdnLds {
     static constexpr int NP = Plan<GDN, TIn>::NPX, LD = DKP + 8;
-    __bf16 k[NP][C * LD], q[NP][C * LD];
-    float A[C * MLD], N[C * MLD]; // N: first B
+    union {
+        struct {
+            __bf16 k[NP][C * LD], q[NP][C * LD];
+        };
+        PrepMats m;
+    };
     float e[C], beta[C], pre[C], suf[C], eb[4];
     float diag[4][16 * 16]; // P_ij of the diagonal blocks
-    float tmp[4][16 * 20];
 };
 
 template <typename TIn, int DKP, bool BWD>
@@ -324,40 +400,39 @@ __global__ __launch_bounds__(256) void scan_prep_gdn_kernel(ScanArgs a, bool vec
     // end are zero
     constexpr int PIECES = C * DKP / 8 / 256;
     static_assert(PIECES >= 1, "every thread has a piece");
+    {
+        TIn x[2][PIECES][8];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const TIn *src = static_cast<const TIn *>(t ? a.q : a.k);
-        const long stride = t ? a.qs : a.ks;
-        TIn x[PIECES][8];
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int p = 0; p < PIECES; ++p) {
-            const int i = (p * 256 + tid) / (DKP / 8), d = (p * 256 + tid) % (DKP / 8) * 8;
-            load_piece(x[p], src + (ch.t0 + static_cast<long>(i)) * stride + static_cast<long>(h) * a.dk + d,
-                       i < ch.rows && d < a.dk, vec);
-        }
-#pragma unroll
-        for (int p = 0; p < PIECES; ++p) {
-            const int i = (p * 256 + tid) / (DKP / 8), d = (p * 256 + tid) % (DKP / 8) * 8;
-            bf16x8 pl[NP];
-            if constexpr (P::BF) {
-                pl[0] = __builtin_bit_cast(bf16x8, x[p]);
-            } else {
-                split(__builtin_bit_cast(f32x8, x[p]), pl);
+            for (int p = 0; p < PIECES; ++p) {
+                const int i = (p * 256 + tid) / (DKP / 8), d = (p * 256 + tid) % (DKP / 8) * 8;
+                load_piece(x[t][p], static_cast<const TIn *>(t ? a.q : a.k) + (ch.t0 + static_cast<long>(i)) * (t ? a.qs : a.ks) +
+                                        static_cast<long>(h) * a.dk + d,
+                           i < ch.rows && d < a.dk, vec);
             }
-#pragma unroll
-            for (int n = 0; n < NP; ++n)
-                *reinterpret_cast<bf16x8 *>(&(t ? s.q : s.k)[n][i * LD + d]) = pl[n];
+        if (tid < C) {
+            const long at = (static_cast<long>(ch.t0) + tid) * a.H + h;
+            const bool in = tid < ch.rows;
+            s.e[tid] = in ? expf(floor_log_decay(a.ld[at])) : 1.f;
+            s.beta[tid] = in ? a.beta[at] : 0.f;
+            ops.row(2)[tid] = s.beta[tid];
         }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int p = 0; p < PIECES; ++p) {
+                const int i = (p * 256 + tid) / (DKP / 8), d = (p * 256 + tid) % (DKP / 8) * 8;
+                bf16x8 pl[NP];
+                if constexpr (P::BF)
+                    pl[0] = __builtin_bit_cast(bf16x8, x[t][p]);
+                else
+                    split(__builtin_bit_cast(f32x8, x[t][p]), pl);
+#pragma unroll
+                for (int n = 0; n < NP; ++n)
+                    *reinterpret_cast<bf16x8 *>(&(t ? s.q : s.k)[n][i * LD + d]) = pl[n];
+            }
     }
-    if (tid < C) {
-        const long at = (static_cast<long>(ch.t0) + tid) * a.H + h;
-        const bool in = tid < ch.rows;
-        s.e[tid] = in ? expf(floor_log_decay(a.ld[at])) : 1.f;
-        s.beta[tid] = in ? a.beta[at] : 0.f;
-        ops.row(2)[tid] = s.beta[tid];
-    }
-    for (int it = tid; it < C * MLD; it += 256)
-        s.A[it] = s.N[it] = 0.f;
     __syncthreads();
     if (lane < 16) { // products of decays within block w, column lane
         float p = 0.f, pre = 1.f, suf = 1.f, all = 1.f;
@@ -375,7 +450,63 @@ __global__ __launch_bounds__(256) void scan_prep_gdn_kernel(ScanArgs a, bool vec
         if (lane == 0)
             s.eb[w] = all;
     }
-    __syncthreads();
+
+    // a wave takes five of the twenty blocks of B (0-9) and A (10-19)
+    auto frag = [&](bf16x8 (&f)[NP], const __bf16 (&x)[NP][C * LD], int rb, int ks) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+            f[n] = *reinterpret_cast<const bf16x8 *>(&x[n][(rb * 16 + (lane & 15)) * LD + ks * 32 + (lane >> 4) * 8]);
+    };
+    f32x4 acc[5];
+#pragma unroll
+    for (int p = 0; p < 5; ++p) {
+        const int task = w + p * 4, b = task >= 10 ? task - 10 : task, I = block_row(b), J = block_col(b);
+        Acc<3> x;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            bf16x8 l[NP], r[NP];
+            if (task >= 10)
+                frag(l, s.k, I, ks);
+            else
+                frag(l, s.q, I, ks);
+            frag(r, s.k, J, ks);
+            x.add(l, r);
+        }
+        acc[p] = x.sum();
+    }
+    // the keys' operands: rows of the tiles, and their columns
+    auto rows = [&](auto np, __bf16 *op, const __bf16 (&x)[NP][C * LD]) {
+        constexpr int N = decltype(np)::value;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            bf16x8 f[N];
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                f[n] = *reinterpret_cast<const bf16x8 *>(&x[n][(w * 16 + (lane & 15)) * LD + ks * 32 + (lane >> 4) * 8]);
+            store_frag(op, KS, w, ks, lane, f);
+        }
+    };
+    auto columns = [&](__bf16 *op, const __bf16 (&x)[NP][C * LD]) {
+        for (int it = w; it < DKP / 16 * 2; it += 4) {
+            const int rb = it / 2, ks = it % 2;
+            bf16x8 f[NP];
+#pragma unroll
+            for (int n = 0; n < NP; ++n)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    f[n][e] = x[n][(ks * 32 + (lane >> 4) * 8 + e) * LD + rb * 16 + (lane & 15)];
+            store_frag(op, 2, rb, ks, lane, f);
+        }
+    };
+    rows(std::integral_constant<int, NP>(), ops.op(0), s.k);
+    if (!BWD) {
+        rows(std::integral_constant<int, P::NPQ>(), ops.op(1), s.q);
+        columns(ops.op(2), s.k);
+    } else {
+        columns(ops.op(1), s.q);
+        columns(ops.op(2), s.k);
+    }
+    __syncthreads(); // the tiles are read, the decays complete
     if (tid < C) {
         float g = s.pre[tid], e = s.suf[tid];
         for (int K = 0; K < 4; ++K) {
@@ -387,89 +518,31 @@ __global__ __launch_bounds__(256) void scan_prep_gdn_kernel(ScanArgs a, bool vec
     }
     for (int d = tid; d < DKP; d += 256)
         ops.gam()[d] = s.eb[0] * s.eb[1] * s.eb[2] * s.eb[3];
-
-    auto frag = [&](bf16x8 (&f)[NP], const __bf16 (&x)[NP][C * LD], int rb, int ks) {
+    zero_above(s.m.B);
+    zero_above(s.m.N);
 #pragma unroll
-        for (int n = 0; n < NP; ++n)
-            f[n] = *reinterpret_cast<const bf16x8 *>(&x[n][(rb * 16 + (lane & 15)) * LD + ks * 32 + (lane >> 4) * 8]);
-    };
-    {
-        bf16x8 ka[KS][NP], qa[KS][NP];
+    for (int p = 0; p < 5; ++p) {
+        const int task = w + p * 4, b = task >= 10 ? task - 10 : task, I = block_row(b), J = block_col(b);
+        const bool isA = task >= 10;
+        const int j = lane & 15, i0 = (lane >> 4) * 4;
+        float right = s.suf[J * 16 + j];
+        for (int K = J + 1; K < I; ++K)
+            right *= s.eb[K];
+        f32x4 v = acc[p];
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            frag(ka[ks], s.k, w, ks);
-            frag(qa[ks], s.q, w, ks);
-            if (!BWD) { // the rows of this wave are fragments of the operands already
-                store_frag(ops.op(0), KS, w, ks, lane, ka[ks]);
-                bf16x8 qo[P::NPQ];
-#pragma unroll
-                for (int n = 0; n < P::NPQ; ++n)
-                    qo[n] = qa[ks][n];
-                store_frag(ops.op(1), KS, w, ks, lane, qo);
-            } else {
-                store_frag(ops.op(0), KS, w, ks, lane, ka[ks]);
-            }
+        for (int e = 0; e < 4; ++e) {
+            const int i = i0 + e;
+            const float f = I == J ? s.diag[I][i * 16 + j] : s.pre[I * 16 + i] * right;
+            v[e] = I > J || i > j || (i == j && !isA) ? v[e] * f : 0.f;
         }
-        float between = 1.f;
-        for (int J = w; J >= 0; --J) {
-            f32x4 ca = {0, 0, 0, 0}, cb = {0, 0, 0, 0};
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                bf16x8 kb[NP];
-                frag(kb, s.k, J, ks);
-                ca = mma<3>(ka[ks], kb, ca);
-                cb = mma<3>(qa[ks], kb, cb);
-            }
-            const int j = lane & 15, i0 = (lane >> 4) * 4;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = i0 + e;
-                const float f = J == w ? s.diag[w][i * 16 + j]
-                                       : s.pre[w * 16 + i] * (between * s.suf[J * 16 + j]);
-                const bool below = J < w || i > j;
-                s.A[(w * 16 + i) * MLD + J * 16 + j] = below ? ca[e] * f : 0.f;
-                s.N[(w * 16 + i) * MLD + J * 16 + j] = below || i == j ? cb[e] * f : 0.f;
-            }
-            if (J < w)
-                between *= s.eb[J];
-        }
+        if (BWD)
+            store_pair(ops.mat(2), isA ? b : 10 + b, lane, v);
+        if (isA)
+            v *= s.beta[J * 16 + j];
+        put_block(isA ? s.m.L : s.m.B, I, J, lane, v);
     }
     __syncthreads();
-    // the operands whose rows are keys: columns of the staged tiles
-    auto columns = [&](auto np, __bf16 *op, const __bf16 (&x)[NP][C * LD]) {
-        constexpr int N = decltype(np)::value;
-        for (int it = tid; it < DKP / 16 * (C / 32) * 64; it += 256) {
-            const int l = it & 63, rb = (it >> 6) / (C / 32), ks = (it >> 6) % (C / 32);
-            bf16x8 f[N];
-#pragma unroll
-            for (int n = 0; n < N; ++n)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    f[n][e] = x[n][(ks * 32 + (l >> 4) * 8 + e) * LD + rb * 16 + (l & 15)];
-            store_frag(op, C / 32, rb, ks, l, f);
-        }
-    };
-    if (!BWD) {
-        columns(std::integral_constant<int, NP>(), ops.op(2), s.k);
-        store_op<P::NPB, C, C, LOWER>(ops.mat(1), [&](int i, int j) { return s.N[i * MLD + j]; });
-    } else {
-        columns(std::integral_constant<int, NP>(), ops.op(1), s.q);
-        columns(std::integral_constant<int, NP>(), ops.op(2), s.k);
-        store_op<3, C, C, UPPER>(ops.mat(1), [&](int i, int j) { return s.N[j * MLD + i]; });
-        store_pairs(ops.mat(2), s.A, s.N, 2);
-    }
-    __syncthreads();
-    for (int it = tid; it < C * C; it += 256) {
-        const int i = it / C, j = it % C;
-        s.A[i * MLD + j] *= s.beta[j];
-        s.N[i * MLD + j] = 0.f;
-    }
-    __syncthreads();
-    invert_unit_lower(s.A, s.N, s.tmp[w], w, lane);
-    if (BWD)
-        store_op<3, C, C, UPPER>(ops.mat(0), [&](int i, int j) { return s.N[j * MLD + i]; });
-    else
-        store_op<3, C, C, LOWER>(ops.mat(0), [&](int i, int j) { return s.N[i * MLD + j]; });
+    store_mats<GDN, TIn, BWD>(s.m, ops, w, lane);
 }
 
 } // namespace dl
