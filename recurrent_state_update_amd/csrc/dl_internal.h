@@ -84,8 +84,9 @@ hipError_t launch_step_rwkv6(int dtype, int dk, int dv, int mode, const StepArgs
 
 constexpr int kScanChunk = 64; // tokens per chunk of the scan
 
-// Chunk slots of a scan: every sequence has enough of them (dl_scan.h).
-constexpr long scan_slots(long tokens, long seqs) { return tokens / kScanChunk + seqs; }
+// Chunk slots of a scan: every sequence has enough of them, and the rows
+// behind the last one too (dl_scan.h).
+constexpr long scan_slots(long tokens, long seqs) { return tokens / kScanChunk + seqs + 1; }
 // Keys as the kernels take them (d_k = 16 runs as 32, the rest zero).
 constexpr int scan_keys(int dk) { return dk < 32 ? 32 : dk; }
 // bf16 planes of the keys' operands: GDN's are the inputs themselves, exact in

@@ -170,16 +170,18 @@ template <> __device__ __forceinline__ float from_in<__bf16>(__bf16 x) { return 
 // Chunks are numbered by slots: sequence n owns the slots from
 // base(n) = start(n) / C + n on, which leaves every sequence enough of them
 // (floor(a / C) + ceil((b - a) / C) <= floor(b / C) + 1) without a prefix sum
-// over the lengths; T / C + N slots in all.  Offsets read from cu are clamped
-// to [0, T], so a bad array cannot lead an access out of range.
+// over the lengths.  The rows behind the last sequence, T / C + N + 1 slots in
+// all, count as sequence N here: no carry has it, and prep zeroes the outputs'
+// rows.  Offsets read from cu are clamped to [0, T], so a bad array cannot lead
+// an access out of range.
 struct Seq {
     int start, len, base;
 };
 __device__ __forceinline__ int seq_start(const ScanArgs &a, int n)
 {
     if (!a.cu)
-        return static_cast<int>(static_cast<long>(a.T) * n / a.N);
-    const int s = a.cu[n];
+        return n >= a.N ? a.T : static_cast<int>(static_cast<long>(a.T) * n / a.N);
+    const int s = n > a.N ? a.T : a.cu[n];
     return s < 0 ? 0 : s > a.T ? a.T : s;
 }
 __device__ __forceinline__ Seq sequence(const ScanArgs &a, int n)
@@ -191,13 +193,15 @@ __device__ __forceinline__ Seq sequence(const ScanArgs &a, int n)
     s.base = s.start / C + n;
     return s;
 }
-// The chunk of a slot: its first token and its number of tokens (<= 0: none).
+// The chunk of a slot: its first token, its number of tokens (<= 0: none), and
+// whether it lies behind the last sequence.
 struct Chunk {
     int t0, rows;
+    bool behind;
 };
 __device__ __forceinline__ Chunk chunk_of(const ScanArgs &a, int slot)
 {
-    int lo = 0, hi = a.N - 1; // the last n with base(n) <= slot
+    int lo = 0, hi = a.N; // the last n with base(n) <= slot
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
         if (seq_start(a, mid) / C + mid <= slot)
@@ -210,6 +214,7 @@ __device__ __forceinline__ Chunk chunk_of(const ScanArgs &a, int slot)
     Chunk r;
     r.t0 = s.start + c * C;
     r.rows = c < 0 ? 0 : s.len - c * C < C ? s.len - c * C : C;
+    r.behind = lo == a.N;
     return r;
 }
 

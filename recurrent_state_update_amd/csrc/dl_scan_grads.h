@@ -74,7 +74,7 @@ __global__ __launch_bounds__(DKP * 4) void scan_grads_kernel(ScanArgs a, bool ve
     const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H;
     const long slot_head = static_cast<long>(slot) * a.H + h;
     const Chunk ch = chunk_of(a, slot);
-    if (ch.rows <= 0) {
+    if (ch.rows <= 0 || ch.behind) {
         if (!DELTA && tid < a.dk)
             a.w_du[slot_head * a.dk + tid] = 0.f;
         return;

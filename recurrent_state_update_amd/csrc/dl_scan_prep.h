@@ -24,6 +24,27 @@ template <typename TIn> __device__ __forceinline__ void load_piece(TIn (&x)[8], 
     }
 }
 
+// The outputs' rows of a chunk that belongs to no sequence: zero.
+template <typename T> __device__ __forceinline__ void zero_rows(void *p, const ScanArgs &a, const Chunk &ch, int h, int width)
+{
+    if (!p)
+        return;
+    for (int it = threadIdx.x; it < ch.rows * width; it += blockDim.x)
+        static_cast<T *>(p)[((static_cast<long>(ch.t0) + it / width) * a.H + h) * width + it % width] = T(0);
+}
+template <int OP, typename TIn, bool BWD> __device__ __forceinline__ void zero_behind(const ScanArgs &a, const Chunk &ch, int h)
+{
+    if (!BWD) {
+        zero_rows<TIn>(a.o, a, ch, h, a.dv);
+        return;
+    }
+    zero_rows<TIn>(a.d_q, a, ch, h, a.dk);
+    zero_rows<TIn>(a.d_k, a, ch, h, a.dk);
+    zero_rows<TIn>(a.d_v, a, ch, h, a.dv);
+    zero_rows<float>(a.d_beta, a, ch, h, 1);
+    zero_rows<float>(a.d_ld, a, ch, h, OP == GDN ? 1 : a.dk);
+}
+
 // The ten 16 x 16 blocks (I, J) of a lower triangle, numbered row by row.
 __device__ __forceinline__ int block_row(int b) { return b < 1 ? 0 : b < 3 ? 1 : b < 6 ? 2 : 3; }
 __device__ __forceinline__ int block_col(int b)
@@ -124,6 +145,8 @@ __global__ __launch_bounds__(prep_threads<DKP>(), 4) void scan_prep_kernel(ScanA
     const Chunk ch = chunk_of(a, slot);
     if (ch.rows <= 0)
         return;
+    if (ch.behind)
+        return zero_behind<OP, TIn, BWD>(a, ch, h);
     const Ops<P::NPX, DKP> ops(a, static_cast<long>(slot) * a.H + h);
 
     if (tid < C) {
@@ -394,6 +417,8 @@ __global__ __launch_bounds__(256) void scan_prep_gdn_kernel(ScanArgs a, bool vec
     const Chunk ch = chunk_of(a, slot);
     if (ch.rows <= 0)
         return;
+    if (ch.behind)
+        return zero_behind<GDN, TIn, BWD>(a, ch, h);
     const Ops<NP, DKP> ops(a, static_cast<long>(slot) * a.H + h);
 
     // eight elements of a row per thread and turn; rows and keys behind the

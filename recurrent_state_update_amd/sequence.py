@@ -14,12 +14,9 @@ import contextlib
 
 import torch
 
-from . import (DTYPES, OPS, _check, _dtype_id, _op_id, dl_gated_norm, dl_gated_norm_backward,
-               dl_gated_norm_workspace_bytes, dl_residual_norm, dl_residual_norm_backward,
-               dl_residual_norm_workspace_bytes, dl_scan, dl_scan_backward,
-               dl_scan_backward_workspace_bytes, dl_scan_desc, dl_scan_saved_bytes,
-               dl_scan_workspace_bytes)
-
+from . import (DTYPES, _check, _dtype_id, _lib, _op_id, dl_gated_norm_workspace_bytes,
+               dl_residual_norm_workspace_bytes, dl_scan_backward_workspace_bytes, dl_scan_desc,
+               dl_scan_saved_bytes, dl_scan_workspace_bytes)
 
 _HERE = contextlib.nullcontext()
 
@@ -54,10 +51,21 @@ def _bytes(n, device):
 def _tensor(t, name, dtype, shape, device):
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} is required")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name}: want {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if not t.is_cuda or t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} is on {t.device}, want {device}")
+
+
+def _gpu(t, name):
+    """The device of a tensor that has to be on a GPU."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: want a GPU tensor")
+    return t.device
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
 
 
 def _none(t, name, why):
@@ -69,6 +77,8 @@ def _rows(t, lead):
     """t [*lead, H, d] as rows of H*d elements a fixed distance apart: the
     tensor (copied only if it is not laid out so) and that distance."""
     H, d = t.shape[-2:]
+    if t.is_contiguous():
+        return t, H * d
     n = t.numel() // (H * d) if t.numel() else 0
     if n <= 1:
         return t.contiguous(), H * d
@@ -91,8 +101,8 @@ class _Scan:
 
     def __init__(self, op, q, k, v, beta, log_decay, u, cu_seqlens):
         opi = _op_id(op)
-        if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() not in (3, 4):
-            raise ValueError("q: want a GPU tensor [T,H,d_k] or [N,T,H,d_k]")
+        if q.dim() not in (3, 4):
+            raise ValueError(f"q: want [T,H,d_k] or [N,T,H,d_k], got {tuple(q.shape)}")
         dev, lead = q.device, tuple(q.shape[:-2])
         H, dk = q.shape[-2:]
         dti = _dtype_id(q.dtype)
@@ -132,34 +142,30 @@ class _Scan:
         log_decay = log_decay.detach().contiguous()
         u = None if u is None else u.detach().contiguous()
         self.tensors = (q, k, v, beta, log_decay, u, cu_seqlens)  # kept alive with the descriptor
-
-        def p(t):
-            return None if t is None else t.data_ptr()
-        self.desc = dl_scan_desc(opi, dti, T, self.N, H, dk, dv, qs, ks, vs, p(cu_seqlens), p(q), p(k), p(v),
-                                 p(beta), p(log_decay), p(u))
-        if dl_scan_workspace_bytes(self.desc) == 0:
+        self.desc = dl_scan_desc(opi, dti, T, self.N, H, dk, dv, qs, ks, vs, _p(cu_seqlens), q.data_ptr(),
+                                 k.data_ptr(), v.data_ptr(), _p(beta), log_decay.data_ptr(), _p(u))
+        self.workspace_bytes = dl_scan_workspace_bytes(self.desc)
+        if self.workspace_bytes == 0:
             raise ValueError(f"unsupported scan shape {op} tokens={T} sequences={self.N} H={H} d_k={dk} d_v={dv}")
 
     def state_shape(self):
         return (self.N, self.H, self.dk, self.dv)
 
-    def rows_like(self, shape, dtype):
-        # rows that belong to no sequence are not written: they hold zeros
-        packed = self.tensors[6] is not None
-        return (torch.zeros if packed else torch.empty)(shape, dtype=dtype, device=self.device)
+    def empty(self, shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=self.device)
 
     def forward(self, initial, final, rows, n_rows, saved=None):
-        o = self.rows_like(self.shape["v"], self.dtype)
-        ws = _bytes(dl_scan_workspace_bytes(self.desc), self.device)
-        _check(dl_scan(self.desc, initial, final, rows, n_rows, o, saved, ws, _current(self.device)),
-               "dl_scan")
+        o = self.empty(self.shape["v"], self.dtype)
+        ws = _bytes(self.workspace_bytes, self.device)
+        _check(_lib.dl_scan(self.desc, _p(initial), _p(final), _p(rows), n_rows, o.data_ptr(), _p(saved),
+                            ws.data_ptr(), _current(self.device)), "dl_scan")
         return o
 
 
 class _ScanFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, s, q, k, v, beta, log_decay, u, initial):
-        final = torch.empty(s.state_shape(), dtype=torch.float32, device=s.device)
+        final = s.empty(s.state_shape(), torch.float32)
         saved = _bytes(dl_scan_saved_bytes(s.desc), s.device)
         o = s.forward(initial, final, None, 0, saved)
         ctx.set_materialize_grads(False)
@@ -174,19 +180,20 @@ class _ScanFn(torch.autograd.Function):
     def backward(ctx, d_o, d_final):
         s = ctx.scan
         saved = ctx.saved_tensors[-1]
-        with torch.cuda.device(s.device):
+        with _on(s.device, None):
             d_o = None if d_o is None else d_o.contiguous()
             d_final = None if d_final is None else d_final.contiguous()
             delta = s.op != "rwkv6"
-            dq, dk = s.rows_like(s.shape["q"], s.dtype), s.rows_like(s.shape["q"], s.dtype)
-            dv = s.rows_like(s.shape["v"], s.dtype)
-            dbeta = s.rows_like(s.shape["h"], torch.float32) if delta else None
-            dld = s.rows_like(s.shape["ld"], torch.float32)
-            du = None if delta else torch.empty(s.H, s.dk, dtype=torch.float32, device=s.device)
-            d0 = torch.empty(s.state_shape(), dtype=torch.float32, device=s.device) if ctx.with_initial else None
+            dq, dk = s.empty(s.shape["q"], s.dtype), s.empty(s.shape["q"], s.dtype)
+            dv = s.empty(s.shape["v"], s.dtype)
+            dbeta = s.empty(s.shape["h"], torch.float32) if delta else None
+            dld = s.empty(s.shape["ld"], torch.float32)
+            du = None if delta else s.empty((s.H, s.dk), torch.float32)
+            d0 = s.empty(s.state_shape(), torch.float32) if ctx.with_initial else None
             ws = _bytes(dl_scan_backward_workspace_bytes(s.desc), s.device)
-            _check(dl_scan_backward(s.desc, saved, d_o, d_final, dq, dk, dv, dbeta, dld, du, d0, ws,
-                                    _current(s.device)), "dl_scan_backward")
+            _check(_lib.dl_scan_backward(s.desc, saved.data_ptr(), _p(d_o), _p(d_final), dq.data_ptr(), dk.data_ptr(),
+                                         dv.data_ptr(), _p(dbeta), dld.data_ptr(), _p(du), _p(d0), ws.data_ptr(),
+                                         _current(s.device)), "dl_scan_backward")
         return None, dq, dk, dv, dbeta, dld, du, d0
 
 
@@ -215,16 +222,21 @@ def scan(op: str, q, k, v, beta, log_decay, u=None, initial_state=None, cu_seqle
     Differentiable by q, k, v, beta, log_decay, u and initial_state.  A forward
     pass that will be differentiated keeps, per 64 tokens and head, the state
     and 64 d_v floats until its backward pass."""
-    probe = _Scan(op, q, k, v, beta, log_decay, u, cu_seqlens)
-    with _on(probe.device, stream):
+    with _on(_gpu(q, "q"), stream):
+        probe = _Scan(op, q, k, v, beta, log_decay, u, cu_seqlens)
         initial = _initial(initial_state, probe.state_shape(), probe.device)
         if _wants_grad(q, k, v, beta, log_decay, u, initial):
             return _ScanFn.apply(probe, q, k, v, beta, log_decay, u, initial)
-        final = torch.empty(probe.state_shape(), dtype=torch.float32, device=probe.device)
+        final = probe.empty(probe.state_shape(), torch.float32)
         return probe.forward(initial, final, None, 0), final
 
 
 def _prefill(st, q, k, v, beta, log_decay, cu_seqlens, slots, stream):
+    with _on(_gpu(q, "q"), stream):
+        return _prefill_here(st, q, k, v, beta, log_decay, cu_seqlens, slots)
+
+
+def _prefill_here(st, q, k, v, beta, log_decay, cu_seqlens, slots):
     s = _Scan(st.op, q, k, v, beta, log_decay, st.u, cu_seqlens)
     if (s.H, s.dk, s.dv, s.dtype) != (st.H, st.d_k, st.d_v, st.dtype):
         raise ValueError(f"prefill: the state has H={st.H} d_k={st.d_k} d_v={st.d_v} {st.dtype}, the inputs "
@@ -241,10 +253,8 @@ def _prefill(st, q, k, v, beta, log_decay, cu_seqlens, slots, stream):
             raise ValueError(f"slots: want {s.N} distinct slots below {st.B}, got {names}")
     if any(st.slot_log_len(i) != 0 for i in names):
         raise ValueError("prefill: a slot's log holds entries; merge it first")
-    with _on(s.device, stream):
-        rows = None if slots is None else torch.tensor(names, dtype=torch.int32).to(s.device, non_blocking=True)
-        with torch.no_grad():
-            return s.forward(st.base, st.base, rows, st.B)
+    rows = None if slots is None else torch.tensor(names, dtype=torch.int32, device=s.device)
+    return s.forward(st.base, st.base, rows, st.B)
 
 
 # -------------------------------------------------------------------- norms --
@@ -257,8 +267,8 @@ def _gated_norm(o, gate, weight, eps):
     g, gs = _rows(gate, gate.dim() - 2)
     weight = None if weight is None else weight.contiguous()
     y = torch.empty(gate.shape, dtype=gate.dtype, device=o.device)
-    _check(dl_gated_norm(rows, H, d, DTYPES[o.dtype], DTYPES[gate.dtype], o, g, gs, weight, eps, y,
-                         _current(o.device)), "dl_gated_norm")
+    _check(_lib.dl_gated_norm(rows, H, d, DTYPES[o.dtype], DTYPES[gate.dtype], o.data_ptr(), g.data_ptr(), gs,
+                              _p(weight), eps, y.data_ptr(), _current(o.device)), "dl_gated_norm")
     return y, (o, g, weight), (rows, H, d, gs, eps)
 
 
@@ -274,7 +284,7 @@ class _GatedNormFn(torch.autograd.Function):
     def backward(ctx, dy):
         o, g, weight = ctx.saved_tensors
         rows, H, d, gs, eps = ctx.args
-        with torch.cuda.device(o.device):
+        with _on(o.device, None):
             dy = dy.contiguous()
             d_o = torch.empty_like(o)
             dg = torch.empty(dy.shape, dtype=g.dtype, device=o.device)
@@ -282,8 +292,10 @@ class _GatedNormFn(torch.autograd.Function):
             if weight is not None and ctx.needs_input_grad[2]:
                 dw = torch.empty_like(weight)
                 ws = _bytes(dl_gated_norm_workspace_bytes(rows, H, d), o.device)
-            _check(dl_gated_norm_backward(rows, H, d, DTYPES[o.dtype], DTYPES[g.dtype], o, g, gs, weight, eps,
-                                          dy, d_o, dg, dw, ws, _current(o.device)), "dl_gated_norm_backward")
+            _check(_lib.dl_gated_norm_backward(rows, H, d, DTYPES[o.dtype], DTYPES[g.dtype], o.data_ptr(),
+                                               g.data_ptr(), gs, _p(weight), eps, dy.data_ptr(), d_o.data_ptr(),
+                                               dg.data_ptr(), _p(dw), _p(ws), _current(o.device)),
+                   "dl_gated_norm_backward")
         return d_o, dg, dw, None
 
 
@@ -294,12 +306,11 @@ def gated_norm(o, gate, weight=None, eps: float = 1e-6, stream=None):
     [...,H,d] bf16 or fp32 (its rows may be slices of a projection), weight
     [d] fp32 or None.  Returns gate's dtype.  d in {16, 32, 64, 128}.
     Differentiable by o, gate and weight."""
-    for t, name in ((o, "o"), (gate, "gate")):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() < 2:
-            raise ValueError(f"{name}: want a GPU tensor [...,H,d]")
-        _dtype_id(t.dtype)
-    _tensor(gate, "gate", gate.dtype, o.shape, o.device)
-    if o.shape[-1] not in (16, 32, 64, 128) or o.shape[-2] < 1:
+    dev = _gpu(o, "o")
+    _gpu(gate, "gate")
+    _dtype_id(o.dtype), _dtype_id(gate.dtype)
+    _tensor(gate, "gate", gate.dtype, o.shape, dev)
+    if o.dim() < 2 or o.shape[-1] not in (16, 32, 64, 128) or o.shape[-2] < 1:
         raise ValueError(f"o: want heads of 16, 32, 64 or 128, got {tuple(o.shape)}")
     if weight is not None:
         _tensor(weight, "weight", torch.float32, (o.shape[-1],), o.device)
@@ -316,8 +327,8 @@ def _residual_norm(x, y, scale, weight, eps, dtype):
     x, y, scale, weight = (None if t is None else t.contiguous() for t in (x, y, scale, weight))
     x_out = None if y is None else torch.empty_like(x)
     h = torch.empty(x.shape, dtype=dtype, device=x.device)
-    _check(dl_residual_norm(rows, D, DTYPES[dtype], x, y, scale, weight, eps, x_out, h,
-                            _current(x.device)), "dl_residual_norm")
+    _check(_lib.dl_residual_norm(rows, D, DTYPES[dtype], x.data_ptr(), _p(y), _p(scale), _p(weight), eps, _p(x_out),
+                                 h.data_ptr(), _current(x.device)), "dl_residual_norm")
     return (x_out, h), (x if y is None else x_out, y if scale is not None else None, scale, weight), \
         (rows, D, eps, dtype, y is not None)
 
@@ -336,7 +347,7 @@ class _ResidualNormFn(torch.autograd.Function):
         x, y, scale, weight = ctx.saved_tensors
         rows, D, eps, dtype, added = ctx.args
         d_x_out, d_h = grads if added else (None, grads[0])
-        with torch.cuda.device(x.device):
+        with _on(x.device, None):
             d_x_out = None if d_x_out is None else d_x_out.contiguous()
             d_h = None if d_h is None else d_h.contiguous()
             dx = torch.empty_like(x)
@@ -346,8 +357,9 @@ class _ResidualNormFn(torch.autograd.Function):
             ws = None
             if ds is not None or dw is not None:
                 ws = _bytes(dl_residual_norm_workspace_bytes(rows, D), x.device)
-            _check(dl_residual_norm_backward(rows, D, DTYPES[dtype], x, y, scale, weight, eps, d_x_out, d_h, dx,
-                                             dy, ds, dw, ws, _current(x.device)), "dl_residual_norm_backward")
+            _check(_lib.dl_residual_norm_backward(rows, D, DTYPES[dtype], x.data_ptr(), _p(y), _p(scale), _p(weight),
+                                                  eps, _p(d_x_out), _p(d_h), dx.data_ptr(), _p(dy), _p(ds), _p(dw),
+                                                  _p(ws), _current(x.device)), "dl_residual_norm_backward")
         return dx, dy, ds, dw, None, None
 
 
@@ -358,8 +370,9 @@ def residual_norm(x, y=None, scale=None, weight=None, eps: float = 1e-6, dtype=N
     fp32, scale and weight [D] fp32 or None; D <= 16384.  Returns (x', h), h in
     y's dtype.  Without y (the first norm): (x, h) with h = rms(x) * weight in
     ``dtype`` (default bf16).  Differentiable by x, y, scale and weight."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() < 1 or x.dtype != torch.float32:
-        raise ValueError("x: want an fp32 GPU tensor [...,D]")
+    _gpu(x, "x")
+    if x.dim() < 1 or x.dtype != torch.float32:
+        raise ValueError(f"x: want fp32 [...,D], got {x.dtype} {tuple(x.shape)}")
     D = x.shape[-1]
     if not 1 <= D <= 16384:
         raise ValueError(f"x: want 1 to 16384 columns, got {D}")
