@@ -287,7 +287,7 @@ template <int N, int ROWS, int K, Part PART = ALL, typename F> __device__ __forc
 // blocks above it are zero beforehand): the four diagonal blocks by
 // forward substitution, wave w taking block w, one column per lane; then
 // N_IJ = -N_II sum_{J <= K < I} L_IK N_KJ by block diagonals on the fp32
-// matrix instructions.  tmp: 16 x 20 floats of this wave's own.  For whole
+// matrix instructions.  tmp: 16 x 16 floats of this wave's own.  For whole
 // workgroups of four waves or more.
 __device__ __forceinline__ void invert_unit_lower(const float *L, float *N, float *tmp, int w, int lane)
 {
@@ -325,9 +325,9 @@ __device__ __forceinline__ void invert_unit_lower(const float *L, float *N, floa
             }
             // through this wave's own scratch into the other operand's
             // order; one wave's LDS accesses stay in order
-            *reinterpret_cast<f32x4 *>(&tmp[r * 20 + k0]) = t;
+            *reinterpret_cast<f32x4 *>(&tmp[r * 16 + k0]) = t;
             __builtin_amdgcn_wave_barrier();
-            const f32x4 x = *reinterpret_cast<const f32x4 *>(&tmp[r * 20 + k0]);
+            const f32x4 x = *reinterpret_cast<const f32x4 *>(&tmp[r * 16 + k0]);
             c = mfma32x4(*reinterpret_cast<const f32x4 *>(&N[(I * 16 + r) * MLD + I * 16 + k0]), x, c);
 #pragma unroll
             for (int e = 0; e < 4; ++e)

@@ -10,7 +10,8 @@
 // passes through LDS as bf16 planes, already in the order that the matrix
 // instruction reads; LDS bandwidth is most of a step, so what is read from it
 // serves every product that the wave forms with it.  Each operand of the next
-// chunk is loaded into the registers of this one's right behind its last use;
+// chunk is loaded into the registers of this one's right behind its last use,
+// and ahead of the stores of the same phase (waits count in order);
 // the value tiles of one (sequence, head) run on one XCD, whose L2 serves all
 // but the first of them.
 #pragma once
@@ -188,12 +189,16 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
     TIn *op = static_cast<TIn *>(a.o) + static_cast<long>(sq.start) * width + first;
     auto load_q = [&](int c) { load_rows(qf, ops(c).op(1), w & 3, lane); };
     auto load_b = [&](int c) { load_tri(bf, ops(c).mat(1), LOWER, w & 3, lane); };
-    auto out = [&](int c, f32x4 o, const Planes<P::NPB, C> &b, int t) {
-        o = product_tri<P::ORDER_O>(bf, b, true, (w & 3) >= 2, lane, o);
+    auto with_b = [&](f32x4 o, const Planes<P::NPB, C> &b) {
+        return product_tri<P::ORDER_O>(bf, b, true, (w & 3) >= 2, lane, o);
+    };
+    auto store_o = [&](int c, const f32x4 (&o)[NC]) {
         const ChunkRows<TIn> rows(op, width, c, sq.len, 16 * NC);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            rows.store((i0 + e) * width + col + 16 * t, o[e]);
+        for (int t = 0; t < NC; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                rows.store((i0 + e) * width + col + 16 * t, o[t][e]);
     };
 
     if (w < 4) {
@@ -252,17 +257,19 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
 #pragma unroll
                 for (int t = 0; t < NC; ++t) {
                     x[t] = product_tri<3>(nf, rp[t], true, w >= 2, lane, zero);
-                    if (SAVE) {
-                        const long sh = static_cast<long>(sq.base + c) * a.H + h;
+                    const f32x4 b = x[t] * beta;
+                    hp[0][t].put(col, i0, ROWS ? b * ge : b);
+                    bp[c & 1][t].put(col, i0, b);
+                }
+                load_n(next);
+                if (SAVE) {
+                    const long sh = static_cast<long>(sq.base + c) * a.H + h;
+#pragma unroll
+                    for (int t = 0; t < NC; ++t)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             a.save_e[(sh * C + i0 + e) * a.dv + v0 + 16 * t] = x[t][e];
-                    }
-                    x[t] *= beta;
-                    hp[0][t].put(col, i0, ROWS ? x[t] * ge : x[t]);
-                    bp[c & 1][t].put(col, i0, x[t]);
                 }
-                load_n(next);
                 __syncthreads(); // b is complete
             }
         } else {
@@ -283,16 +290,18 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
             for (int c = 0; c < chunks; ++c) {
                 __syncthreads(); // state and b are complete
                 const int next = c + 1 < chunks ? c + 1 : c, after = c + 2 < chunks ? c + 2 : next;
+                f32x4 o[NC];
 #pragma unroll
                 for (int t = 0; t < NC; ++t) {
                     bf16x8 f[KS][P::ORDER_O];
                     get_all(f, sp[c & 1][t], lane);
-                    out(c, product<P::ORDER_O>(qf, f, zero), bp[c & 1][t], t);
+                    o[t] = with_b(product<P::ORDER_O>(qf, f, zero), bp[c & 1][t]);
                 }
                 put_v(c + 1); // (behind the last chunk: read by nobody)
                 load_v(after);
                 load_q(next);
                 load_b(next);
+                store_o(c, o);
             }
         }
         return;
@@ -375,11 +384,13 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
                 // the chunk before is finished while waves 0-3 form b; the first
                 // turn has none (what it writes is written again)
 #pragma unroll
-                for (int t = 0; t < NC; ++t) {
-                    out(c > 0 ? c - 1 : 0, last[t], bp[(c + 1) & 1][t], t);
-                    last[t] = o[t];
-                }
+                for (int t = 0; t < NC; ++t)
+                    last[t] = with_b(last[t], bp[(c + 1) & 1][t]);
                 load_b(c);
+                store_o(c > 0 ? c - 1 : 0, last);
+#pragma unroll
+                for (int t = 0; t < NC; ++t)
+                    last[t] = o[t];
                 __syncthreads();
             }
 #pragma unroll
@@ -390,13 +401,14 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
                 for (int r = 0; r < RB; ++r)
                     S[t][r] = product<3>(tf[r], f, S[t][r] * gam[r]);
             }
-            put_state(c + 1);
             load_t(next);
+            put_state(c + 1);
         }
         if constexpr (DELTA) {
 #pragma unroll
             for (int t = 0; t < NC; ++t)
-                out(chunks - 1, last[t], bp[(chunks - 1) & 1][t], t);
+                last[t] = with_b(last[t], bp[(chunks - 1) & 1][t]);
+            store_o(chunks - 1, last);
         }
     }
     if (a.fin && row >= 0 && has) {
@@ -510,17 +522,8 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
                 load_n(next);
                 __syncthreads(); // z is complete
             }
-            const ChunkRows<TIn> rows(dvp, width, c, sq.len, 16 * NC);
-#pragma unroll
-            for (int t = 0; t < NC; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    rows.store((i0 + e) * width + col + 16 * t, x[t][e]);
-                    if (DELTA)
-                        a.w_z[(sh * C + i0 + e) * a.dv + v0 + 16 * t] = x[t][e];
-                }
+            f32x4 p = zero;
             if constexpr (DELTA) {
-                f32x4 p = zero;
 #pragma unroll
                 for (int t = 0; t < NC; ++t)
 #pragma unroll
@@ -534,9 +537,18 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
                     p[e] = add_row_ror<4>(p[e]);
                     p[e] = add_row_ror<8>(p[e]);
                 }
-                if (col == 0)
-                    *reinterpret_cast<f32x4 *>(&a.w_db[(sh * tiles + wk.tile) * C + i0]) = p;
             }
+            const ChunkRows<TIn> rows(dvp, width, c, sq.len, 16 * NC);
+#pragma unroll
+            for (int t = 0; t < NC; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    rows.store((i0 + e) * width + col + 16 * t, x[t][e]);
+                    if (DELTA)
+                        a.w_z[(sh * C + i0 + e) * a.dv + v0 + 16 * t] = x[t][e];
+                }
+            if (DELTA && col == 0)
+                *reinterpret_cast<f32x4 *>(&a.w_db[(sh * tiles + wk.tile) * C + i0]) = p;
         }
         return;
     }
@@ -615,9 +627,9 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
         load_g(chunks - 1);
         put_g(chunks - 1);
         keep_order();
-        load_g(chunks > 1 ? chunks - 2 : 0);
-        keep_order();
         load_q(chunks - 1);
+        keep_order();
+        load_g(chunks > 1 ? chunks - 2 : 0);
         keep_order();
         load_k(chunks - 1);
         keep_order();
@@ -651,8 +663,8 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
                         S[t][r] = product<3>(kt[r], f, S[t][r]);
                 }
             }
-            put_state(c - 1);
             load_k(next);
+            put_state(c - 1);
         }
     }
     if (a.dinit && has) {

@@ -12,8 +12,8 @@
 // pairs whose decay contains it.  dbeta_j = (db . E)_j - sum_i A_ij z_i . E_j.
 //
 // One workgroup per chunk and head, one wave per 16 keys.  Bound by reading S
-// and dS' (128 KiB each at d = 128, the chunk's largest part) and by the
-// matrix products; one workgroup fits a CU, for its LDS.
+// and dS' (64 KiB each at d = 128, the largest part of a chunk) and by the
+// latency of its phases.
 #pragma once
 
 #include <type_traits>
@@ -23,19 +23,21 @@
 
 namespace dl {
 
-// dO, -z and E (RWKV6: V) for 64 value columns, as planes.
+// dO, -z and E (RWKV6: V) for 32 value columns, as planes.
 template <int OP, typename TIn> struct GradStage {
     using P = Plan<OP, TIn>;
-    static constexpr int LD = 64 + 8, NE = P::DELTA ? 3 : P::NPI;
+    static constexpr int V = 32, LD = V + 8, NE = P::DELTA ? 3 : P::NPI;
     __bf16 g[P::NPI][C * LD], e[NE][C * LD];
     __bf16 z[P::DELTA ? 3 : 1][P::DELTA ? C * LD : 8];
 };
 
 template <int OP, typename TIn, int DKP> struct GradLds {
     static constexpr int LD = DKP + 4, XLD = C + 8;
-    // GDN: the weights dB P, its transpose and dA P + its transpose in planes
+    // GDN: the weights dB P, its transpose and dA P + its transpose in planes;
+    // they only reach dq and dk
+    static constexpr int NX = Plan<OP, TIn>::ORDER_O;
     struct Rows {
-        __bf16 x1[3][C * XLD], x2[3][C * XLD], x3[3][C * XLD];
+        __bf16 x1[NX][C * XLD], x2[NX][C * XLD], x3[NX][C * XLD];
     };
     // per key: keys and queries scaled within their blocks, dA and dB
     struct Keys {
@@ -53,15 +55,21 @@ template <int OP, typename TIn, int DKP> struct GradLds {
     float eb[ROWS ? 1 : 4 * DKP], pre[ROWS ? 1 : 4 * DKP], suf[ROWS ? 1 : 4 * DKP]; // of, before, behind a block
     float part[ROWS ? 1 : 4 * DKP], kh[ROWS ? 1 : 4 * DKP];
     // GDN
-    TIn k[ROWS ? C * LD : 1], q[ROWS ? C * LD : 1];
     float e[C], rpre[C], rsuf[C], reb[4];                      // decays of rows
     float diag[ROWS ? 4 : 1][16 * 16];                         // P_ij of the diagonal blocks
     float roww[10][16], colw[10][16];                          // sums of W_ij = dB B + dA A
     float ra[ROWS ? DKP / 16 : 1][C], rh[ROWS ? DKP / 16 : 1][C]; // per 16 keys: reads of S, writes into S'
 };
 
+// Waves to a SIMD that the registers are held to: two workgroups on a CU where
+// LDS allows them.
+template <int OP, typename TIn, int DKP> constexpr int grad_waves()
+{
+    return OP == GDN && sizeof(TIn) == 2 ? (DKP == 128 ? 4 : 3) : 2;
+}
+
 template <int OP, typename TIn, int DKP>
-__global__ __launch_bounds__(DKP * 4) void scan_grads_kernel(ScanArgs a, bool vec, int tiles)
+__global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_grads_kernel(ScanArgs a, bool vec, int tiles)
 {
     using P = Plan<OP, TIn>;
     using G = GradLds<OP, TIn, DKP>;
@@ -87,19 +95,6 @@ __global__ __launch_bounds__(DKP * 4) void scan_grads_kernel(ScanArgs a, bool ve
     // ---- what the chunk itself needs, ahead of the products over d_v
     float kv[16], qv[16], ev[16]; // per key: this thread's rows
     if constexpr (OP == GDN) {
-        for (int it = tid; it < C * DKP / 8; it += NT) {
-            const int i = it / (DKP / 8), c = it % (DKP / 8) * 8;
-            const bool in = i < ch.rows && c < a.dk;
-            const long at = static_cast<long>(h) * a.dk + c;
-            TIn x[8], y[8];
-            load_piece(x, static_cast<const TIn *>(a.k) + (t0 + i) * a.ks + at, in, vec);
-            load_piece(y, static_cast<const TIn *>(a.q) + (t0 + i) * a.qs + at, in, vec);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                s.k[i * LD + c + e] = x[e];
-                s.q[i * LD + c + e] = y[e];
-            }
-        }
         for (int i = tid; i < C; i += NT)
             s.e[i] = i < ch.rows ? expf(floor_log_decay(a.ld[(t0 + i) * a.H + h])) : 1.f;
     } else {
@@ -122,7 +117,7 @@ __global__ __launch_bounds__(DKP * 4) void scan_grads_kernel(ScanArgs a, bool ve
     for (int i = tid; i < C; i += NT)
         s.beta[i] = !DELTA ? 1.f : i < ch.rows ? a.beta[(t0 + i) * a.H + h] : 0.f;
 
-    // ---- products over d_v, 64 columns at a time
+    // ---- products over d_v, 32 columns at a time
     f32x4 dQ[4], dK[4], dH[4], xB[TASKS], xM[TASKS];
     const f32x4 zero = {0, 0, 0, 0};
 #pragma unroll
@@ -132,103 +127,91 @@ __global__ __launch_bounds__(DKP * 4) void scan_grads_kernel(ScanArgs a, bool ve
     for (int p = 0; p < TASKS; ++p)
         xB[p] = xM[p] = zero;
     float gs = 0.f;
-    auto frag = [&](auto &f, const auto &x, int rb, int ks) {
+    auto frag = [&](auto &f, const auto &x, int rb) {
 #pragma unroll
         for (int n = 0; n < static_cast<int>(sizeof(f) / sizeof(f[0])); ++n)
-            f[n] = *reinterpret_cast<const bf16x8 *>(&x[n][(rb * 16 + c16) * St::LD + ks * 32 + (lane >> 4) * 8]);
+            f[n] = *reinterpret_cast<const bf16x8 *>(&x[n][(rb * 16 + c16) * St::LD + (lane >> 4) * 8]);
     };
-    for (int v0 = 0; v0 < a.dv; v0 += 64) {
-        const int ksteps = a.dv - v0 > 32 ? 2 : 1;
-        f32x8 S[2], dS[2]; // row d of the state, in the matrix instruction's order
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            const int v = v0 + ks * 32 + (lane >> 4) * 8, row = w * 16 + c16;
-            S[ks] = dS[ks] = f32x8{};
+    for (int v0 = 0; v0 < a.dv; v0 += St::V) {
+        f32x8 S = {}, dS = {}; // row d of the state, in the matrix instruction's order
+        {
+            const int v = v0 + (lane >> 4) * 8, row = w * 16 + c16;
             if (v < a.dv && row < a.dk) {
-                S[ks] = *reinterpret_cast<const f32x8 *>(&a.save_s[(slot_head * a.dk + row) * a.dv + v]);
-                dS[ks] = *reinterpret_cast<const f32x8 *>(&a.w_ds[(slot_head * a.dk + row) * a.dv + v]);
+                S = *reinterpret_cast<const f32x8 *>(&a.save_s[(slot_head * a.dk + row) * a.dv + v]);
+                dS = *reinterpret_cast<const f32x8 *>(&a.w_ds[(slot_head * a.dk + row) * a.dv + v]);
             }
         }
         if (v0 > 0)
             __syncthreads(); // the stage before is read
-        for (int it = tid; it < C * 8; it += NT) {
-            const int i = it / 8, c = it % 8 * 8, v = v0 + c;
+        // pieces of eight columns: 256 of dO, then of E (V), then of z
+        constexpr int ARRAYS = DELTA ? 3 : 2;
+        for (int it = tid; it < ARRAYS * 256; it += NT) {
+            const int i = it / 4 % C, c = it % 4 * 8, v = v0 + c;
             const bool in = i < ch.rows && v < a.dv;
             const long t = t0 + i, at = (slot_head * C + i) * a.dv + v;
-            TIn x[8];
-            load_piece(x, static_cast<const TIn *>(a.d_o) + (t * a.H + h) * a.dv + v, in && a.d_o, vec);
-            bf16x8 pl[P::NPI];
-            if constexpr (P::BF)
-                pl[0] = __builtin_bit_cast(bf16x8, x);
-            else
-                split(__builtin_bit_cast(f32x8, x), pl);
-#pragma unroll
-            for (int n = 0; n < P::NPI; ++n)
-                *reinterpret_cast<bf16x8 *>(&s.st.g[n][i * St::LD + c]) = pl[n];
-            if constexpr (DELTA) {
-                f32x8 z = {}, E = {};
-                if (in) {
-                    z = *reinterpret_cast<const f32x8 *>(&a.w_z[at]);
-                    E = *reinterpret_cast<const f32x8 *>(&a.save_e[at]);
-                }
-                bf16x8 pz[3], pe[3];
-                split(-z, pz);
-                split(E, pe);
-#pragma unroll
-                for (int n = 0; n < 3; ++n) {
-                    *reinterpret_cast<bf16x8 *>(&s.st.z[n][i * St::LD + c]) = pz[n];
-                    *reinterpret_cast<bf16x8 *>(&s.st.e[n][i * St::LD + c]) = pe[n];
-                }
-            } else {
-                load_piece(x, static_cast<const TIn *>(a.v) + t * a.vs + static_cast<long>(h) * a.dv + v, in, vec);
+            if (it < 256 || (!DELTA && it < 512)) {
+                TIn x[8];
+                if (it < 256)
+                    load_piece(x, static_cast<const TIn *>(a.d_o) + (t * a.H + h) * a.dv + v, in && a.d_o, vec);
+                else
+                    load_piece(x, static_cast<const TIn *>(a.v) + t * a.vs + static_cast<long>(h) * a.dv + v, in, vec);
+                bf16x8 pl[P::NPI];
                 if constexpr (P::BF)
                     pl[0] = __builtin_bit_cast(bf16x8, x);
                 else
                     split(__builtin_bit_cast(f32x8, x), pl);
 #pragma unroll
                 for (int n = 0; n < P::NPI; ++n)
-                    *reinterpret_cast<bf16x8 *>(&s.st.e[n][i * St::LD + c]) = pl[n];
+                    *reinterpret_cast<bf16x8 *>(it < 256 ? &s.st.g[n][i * St::LD + c] : &s.st.e[n][i * St::LD + c]) = pl[n];
+            } else if constexpr (DELTA) {
+                f32x8 x = {};
+                if (in)
+                    x = *reinterpret_cast<const f32x8 *>(it < 512 ? &a.save_e[at] : &a.w_z[at]);
+                bf16x8 pl[3];
+                split(it < 512 ? x : -x, pl);
+#pragma unroll
+                for (int n = 0; n < 3; ++n)
+                    *reinterpret_cast<bf16x8 *>(it < 512 ? &s.st.e[n][i * St::LD + c] : &s.st.z[n][i * St::LD + c]) = pl[n];
             }
         }
         __syncthreads();
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            if (ks >= ksteps)
-                break;
+        for (int e = 0; e < 8; ++e)
+            gs = fmaf(S[e], dS[e], gs);
+        bf16x8 pl[3];
+        split(dS, pl);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                gs = fmaf(S[ks][e], dS[ks][e], gs);
-            bf16x8 ps[3], pd[3];
-            split(S[ks], ps);
-            split(dS[ks], pd);
+        for (int I = 0; I < 4; ++I) {
+            bf16x8 e[St::NE];
+            frag(e, s.st.e, I);
+            dH[I] = mma<3>(e, pl, dH[I]);
+        }
+        split(S, pl);
 #pragma unroll
-            for (int I = 0; I < 4; ++I) {
-                bf16x8 g[P::NPI], e[St::NE];
-                frag(g, s.st.g, I, ks);
-                frag(e, s.st.e, I, ks);
-                dQ[I] = mma<3>(g, ps, dQ[I]);
-                dH[I] = mma<3>(e, pd, dH[I]);
-                if constexpr (DELTA) {
-                    bf16x8 z[3];
-                    frag(z, s.st.z, I, ks);
-                    dK[I] = mma<3>(z, ps, dK[I]);
-                }
+        for (int I = 0; I < 4; ++I) {
+            bf16x8 g[P::NPI];
+            frag(g, s.st.g, I);
+            dQ[I] = mma<3>(g, pl, dQ[I]);
+            if constexpr (DELTA) {
+                bf16x8 z[3];
+                frag(z, s.st.z, I);
+                dK[I] = mma<3>(z, pl, dK[I]);
             }
+        }
 #pragma unroll
-            for (int p = 0; p < TASKS; ++p) {
-                const int b = w + p * NW;
-                if (b >= 10)
-                    break;
-                const int I = b < 1 ? 0 : b < 3 ? 1 : b < 6 ? 2 : 3, J = b - I * (I + 1) / 2;
-                bf16x8 g[P::NPI], e[St::NE];
-                frag(g, s.st.g, I, ks);
-                frag(e, s.st.e, J, ks);
-                xB[p] = mma<3>(g, e, xB[p]);
-                if constexpr (DELTA) {
-                    bf16x8 z[3];
-                    frag(z, s.st.z, I, ks);
-                    xM[p] = mma<3>(z, e, xM[p]);
-                }
+        for (int p = 0; p < TASKS; ++p) {
+            const int b = w + p * NW;
+            if (b >= 10)
+                break;
+            const int I = block_row(b), J = block_col(b);
+            bf16x8 g[P::NPI], e[St::NE];
+            frag(g, s.st.g, I);
+            frag(e, s.st.e, J);
+            xB[p] = mma<3>(g, e, xB[p]);
+            if constexpr (DELTA) {
+                bf16x8 z[3];
+                frag(z, s.st.z, I);
+                xM[p] = mma<3>(z, e, xM[p]);
             }
         }
     }
@@ -265,7 +248,7 @@ __global__ __launch_bounds__(DKP * 4) void scan_grads_kernel(ScanArgs a, bool ve
             const int b = w + p * NW;
             if (b >= 10)
                 break;
-            const int I = b < 1 ? 0 : b < 3 ? 1 : b < 6 ? 2 : 3, J = b - I * (I + 1) / 2;
+            const int I = block_row(b), J = block_col(b);
             const f32x4 *ab = reinterpret_cast<const f32x4 *>(ops.mat(2));
             const f32x4 A = ab[b * 64 + lane], B = ab[(10 + b) * 64 + lane];
             const float beta = s.beta[J * 16 + c16];
@@ -299,11 +282,11 @@ __global__ __launch_bounds__(DKP * 4) void scan_grads_kernel(ScanArgs a, bool ve
                 s.dbeta[b][lane] = cm;
                 s.colw[b][lane] = cw;
             }
-            bf16x4 p1[3], p3[3];
+            bf16x4 p1[G::NX], p3[G::NX];
             split(w1, p1);
             split(w3, p3);
 #pragma unroll
-            for (int n = 0; n < 3; ++n) {
+            for (int n = 0; n < G::NX; ++n) {
                 *reinterpret_cast<bf16x4 *>(&s.x.x2[n][(J * 16 + c16) * G::XLD + I * 16 + r4]) = p1[n];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -316,7 +299,6 @@ __global__ __launch_bounds__(DKP * 4) void scan_grads_kernel(ScanArgs a, bool ve
                 }
             }
         }
-        __syncthreads();
         // ---- wave w: keys 16 w.., all rows
         bf16x8 kt[2][P::NPX], qt[2][P::NPX];
 #pragma unroll
@@ -324,9 +306,21 @@ __global__ __launch_bounds__(DKP * 4) void scan_grads_kernel(ScanArgs a, bool ve
             load_frag(qt[ks], ops.op(1), 2, w, ks, lane);
             load_frag(kt[ks], ops.op(2), 2, w, ks, lane);
         }
-        auto xfrag = [&](bf16x8 (&f)[3], const __bf16 (&x)[3][C * G::XLD], int rb, int ks) {
+        TIn kx[4][4], qx[4][4]; // this lane's key in all rows
 #pragma unroll
-            for (int n = 0; n < 3; ++n)
+        for (int I = 0; I < 4; ++I)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = I * 16 + r4 + e, key = w * 16 + c16;
+                const bool in = i < ch.rows && key < a.dk;
+                const long at = static_cast<long>(h) * a.dk + key;
+                kx[I][e] = in ? static_cast<const TIn *>(a.k)[(t0 + i) * a.ks + at] : TIn(0);
+                qx[I][e] = in ? static_cast<const TIn *>(a.q)[(t0 + i) * a.qs + at] : TIn(0);
+            }
+        __syncthreads();
+        auto xfrag = [&](bf16x8 (&f)[G::NX], const __bf16 (&x)[G::NX][C * G::XLD], int rb, int ks) {
+#pragma unroll
+            for (int n = 0; n < G::NX; ++n)
                 f[n] = *reinterpret_cast<const bf16x8 *>(&x[n][(rb * 16 + c16) * G::XLD + ks * 32 + (lane >> 4) * 8]);
         };
 #pragma unroll
@@ -338,12 +332,12 @@ __global__ __launch_bounds__(DKP * 4) void scan_grads_kernel(ScanArgs a, bool ve
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int i = I * 16 + r4 + e, at = i * LD + w * 16 + c16;
+                const int i = I * 16 + r4 + e;
                 const float gam = bg * s.rpre[i], end = ag * s.rsuf[i] * s.beta[i];
                 dQ[I][e] *= gam;
                 dK[I][e] *= gam;
                 dH[I][e] *= end;
-                const float k = from_in(s.k[at]), q = from_in(s.q[at]);
+                const float k = from_in(kx[I][e]), q = from_in(qx[I][e]);
                 float x = fmaf(q, dQ[I][e], k * dK[I][e]), y = k * dH[I][e];
                 x = add_row_ror<1>(x);
                 y = add_row_ror<1>(y);
@@ -361,16 +355,16 @@ __global__ __launch_bounds__(DKP * 4) void scan_grads_kernel(ScanArgs a, bool ve
             }
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                bf16x8 f[3];
+                bf16x8 f[G::NX];
                 if (frag_used(LOWER, I, ks)) {
                     xfrag(f, s.x.x1, I, ks);
-                    dQ[I] = mma<3>(f, kt[ks], dQ[I]);
+                    dQ[I] = mma<P::ORDER_O>(f, kt[ks], dQ[I]);
                 }
                 xfrag(f, s.x.x3, I, ks);
-                dK[I] = mma<3>(f, kt[ks], dK[I]);
+                dK[I] = mma<P::ORDER_O>(f, kt[ks], dK[I]);
                 if (frag_used(UPPER, I, ks)) {
                     xfrag(f, s.x.x2, I, ks);
-                    dK[I] = mma<3>(f, qt[ks], dK[I]);
+                    dK[I] = mma<P::ORDER_O>(f, qt[ks], dK[I]);
                 }
             }
 #pragma unroll
@@ -426,7 +420,7 @@ __global__ __launch_bounds__(DKP * 4) void scan_grads_kernel(ScanArgs a, bool ve
             const int b = w + p * NW;
             if (b >= 10)
                 break;
-            const int I = b < 1 ? 0 : b < 3 ? 1 : b < 6 ? 2 : 3, J = b - I * (I + 1) / 2;
+            const int I = block_row(b), J = block_col(b);
             const float beta = s.beta[J * 16 + c16];
             float cm = 0.f;
             f32x4 A = zero;

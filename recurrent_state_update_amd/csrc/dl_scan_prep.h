@@ -61,7 +61,7 @@ __device__ __forceinline__ void store_pair(__bf16 *mat, int n, int lane, f32x4 v
 
 // The C x C matrices of a chunk, once the keys' tiles are done with.
 struct PrepMats {
-    float L[C * MLD], B[C * MLD], N[C * MLD]; // L = A diag(beta); B's room then serves the inverse
+    float L[C * MLD], B[C * MLD]; // L = A diag(beta); N takes B's room once B's planes are written
 };
 // A result block in LDS.
 __device__ __forceinline__ void put_block(float *m, int I, int J, int lane, f32x4 v)
@@ -78,9 +78,10 @@ __device__ __forceinline__ void zero_above(float *m)
         *reinterpret_cast<f32x4 *>(&m[(I * 16 + (it & 63) / 4) * MLD + J * 16 + it % 4 * 4]) = f32x4{0, 0, 0, 0};
     }
 }
-// From L and B in LDS: B's and N's planes.
+// From L and B in LDS: B's and N's planes.  tmp: 16 x 16 floats of a wave's own
+// (four waves).
 template <int OP, typename TIn, bool BWD, int NP, int DKP>
-__device__ __forceinline__ void store_mats(PrepMats &m, const Ops<NP, DKP> &ops, int w, int lane)
+__device__ __forceinline__ void store_mats(PrepMats &m, float *tmp, const Ops<NP, DKP> &ops, int w, int lane)
 {
     using P = Plan<OP, TIn>;
     if (BWD)
@@ -88,12 +89,12 @@ __device__ __forceinline__ void store_mats(PrepMats &m, const Ops<NP, DKP> &ops,
     else
         store_op<P::NPB, C, C, LOWER>(ops.mat(1), [&](int i, int j) { return m.B[i * MLD + j]; });
     if constexpr (P::DELTA) {
-        __syncthreads(); // B is read: its room is the waves' scratch
-        invert_unit_lower(m.L, m.N, m.B + (w & 3) * 16 * 20, w, lane);
+        __syncthreads(); // B is read (and zero above the diagonal, as N will be)
+        invert_unit_lower(m.L, m.B, tmp, w, lane);
         if (BWD)
-            store_op<3, C, C, UPPER>(ops.mat(0), [&](int i, int j) { return m.N[j * MLD + i]; });
+            store_op<3, C, C, UPPER>(ops.mat(0), [&](int i, int j) { return m.B[j * MLD + i]; });
         else
-            store_op<3, C, C, LOWER>(ops.mat(0), [&](int i, int j) { return m.N[i * MLD + j]; });
+            store_op<3, C, C, LOWER>(ops.mat(0), [&](int i, int j) { return m.B[i * MLD + j]; });
     }
 }
 
@@ -360,8 +361,6 @@ __global__ __launch_bounds__(prep_threads<DKP>(), 4) void scan_prep_kernel(ScanA
     }
     __syncthreads(); // the tiles are read
     zero_above(s.m.B);
-    if (DELTA)
-        zero_above(s.m.N);
 #pragma unroll
     for (int p = 0; p < TASKS; ++p) {
         const int task = w + p * NW;
@@ -386,7 +385,7 @@ __global__ __launch_bounds__(prep_threads<DKP>(), 4) void scan_prep_kernel(ScanA
         put_block(isA ? s.m.L : s.m.B, I, J, lane, v);
     }
     __syncthreads();
-    store_mats<OP, TIn, BWD>(s.m, ops, w, lane);
+    store_mats<OP, TIn, BWD>(s.m, s.pair[0][w & 3], ops, w, lane);
 }
 
 // ---- one decay per row (GDN)
@@ -544,7 +543,6 @@ __global__ __launch_bounds__(256) void scan_prep_gdn_kernel(ScanArgs a, bool vec
     for (int d = tid; d < DKP; d += 256)
         ops.gam()[d] = s.eb[0] * s.eb[1] * s.eb[2] * s.eb[3];
     zero_above(s.m.B);
-    zero_above(s.m.N);
 #pragma unroll
     for (int p = 0; p < 5; ++p) {
         const int task = w + p * 4, b = task >= 10 ? task - 10 : task, I = block_row(b), J = block_col(b);
@@ -567,7 +565,7 @@ __global__ __launch_bounds__(256) void scan_prep_gdn_kernel(ScanArgs a, bool vec
         put_block(isA ? s.m.L : s.m.B, I, J, lane, v);
     }
     __syncthreads();
-    store_mats<GDN, TIn, BWD>(s.m, ops, w, lane);
+    store_mats<GDN, TIn, BWD>(s.m, s.diag[w], ops, w, lane);
 }
 
 } // namespace dl
