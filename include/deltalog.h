@@ -305,14 +305,20 @@ size_t dl_scan_workspace_bytes(const dl_scan_desc *d);
 size_t dl_scan_saved_bytes(const dl_scan_desc *d);
 size_t dl_scan_backward_workspace_bytes(const dl_scan_desc *d);
 
-/* Forward: o [tokens,H,d_v] in in_dtype (the decode step's o is fp32; here it
+/* Supported sizes: d_k, d_v in {16, 32, 64, 128}; strides (so H*d too) of at
+ * most 2^22 elements; seqs*H <= 2^19 and (tokens/64 + seqs + 1)*H <= 2^22.
+ *
+ * Forward: o [tokens,H,d_v] in in_dtype (the decode step's o is fp32; here it
  * is as large as v, and is rounded once), and each sequence's end state.
  * `initial` (NULL: zero) and `final_state` (NULL: not wanted) are fp32 state
  * tensors [rows,H,d_k,d_v], 16-byte aligned; final_state may be `initial`
  * itself, else they must not overlap.  With state_rows NULL sequence n has
  * row n; else (device, [seqs] int32) row state_rows[n] of n_state_rows, no
  * row twice; a row out of range is not read (zero) nor written.  `saved`
- * (NULL: no backward pass will follow) keeps what dl_scan_backward needs. */
+ * (NULL: no backward pass will follow) keeps what dl_scan_backward needs.
+ * Tokens are taken in chunks of 64: a NaN or infinity among a token's inputs
+ * stays within its sequence and head, but may also reach the outputs of up to
+ * 63 tokens before it.  (A log-decay of -inf is no such value.) */
 dl_status dl_scan(const dl_scan_desc *d, const float *initial, float *final_state, const int *state_rows,
                   int n_state_rows, void *o, void *saved, void *workspace, void *stream);
 

@@ -41,9 +41,9 @@ template <int NW, int NR> bool clash(const Span (&w)[NW], const Span (&r)[NR])
 }
 
 // Launches count work-items in 32 bits: at most 512 per chunk and head, and
-// 16 d_v per sequence and head.
+// 32 d_v per sequence and head.
 constexpr long long kMostStride = 1LL << 22;
-constexpr long kMostSlotHeads = 1L << 22, kMostSeqHeads = 1L << 20;
+constexpr long kMostSlotHeads = 1L << 22, kMostSeqHeads = 1L << 19;
 
 dl_status check_sizes(const dl_scan_desc *d)
 {

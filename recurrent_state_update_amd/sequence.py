@@ -30,7 +30,7 @@ def _on(device, stream):
     ctx = contextlib.ExitStack()
     ctx.enter_context(torch.cuda.device(device))
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
     ctx.enter_context(torch.cuda.stream(stream))
     return ctx
 
@@ -251,7 +251,7 @@ def _prefill_here(st, q, k, v, beta, log_decay, cu_seqlens, slots):
         names = [int(i) for i in slots]
         if len(names) != s.N or len(set(names)) != s.N or not all(0 <= i < st.B for i in names):
             raise ValueError(f"slots: want {s.N} distinct slots below {st.B}, got {names}")
-    if any(st.slot_log_len(i) != 0 for i in names):
+    if any(st.slot_log_len(i) != 0 for i in (names if st._per_slot else names[:1])):
         raise ValueError("prefill: a slot's log holds entries; merge it first")
     rows = None if slots is None else torch.tensor(names, dtype=torch.int32, device=s.device)
     return s.forward(st.base, st.base, rows, st.B)

@@ -173,6 +173,7 @@ class DecoderShape:
     hidden: int
     ffn: int
     seed: int = 0
+    gated: bool = False   # a per-head norm with an output gate behind the step
 
     def describe(self) -> str:
         return (f"{self.op} L={self.L} B={self.B} H={self.H} dk={self.dk} dv={self.dv} "
@@ -197,8 +198,9 @@ def decoder_layer(ds: DecoderShape, layer: int) -> dict:
     """Random weights of one layer, float32, each N(0, 1/fan_in): W_in
     [hidden, sum(proj_split)], W_o [H*dv, hidden], W_gu [hidden, 2*ffn] (gate
     then up), W_dn [ffn, hidden]; RWKV6's u [H, dk] ~ N(0, 0.1) (else None);
-    and the layer's initial state [B, H, dk, dv] ~ N(0, 0.1).  Draw order as
-    listed, from stream layer+1."""
+    and the layer's initial state [B, H, dk, dv] ~ N(0, 0.1); gated shapes
+    then W_g [hidden, H*dv] and the norm's gain g [dv] ~ N(1, 0.1).  Draw order
+    as listed, from stream layer+1."""
     rng = _drng(ds, layer + 1)
     n_in = sum(ds.proj_split)
     out = {}
@@ -207,7 +209,15 @@ def decoder_layer(ds: DecoderShape, layer: int) -> dict:
         out[name] = _normal(rng, (fi, fo), 0.0, 1.0 / np.sqrt(fi))
     out["u"] = _normal(rng, (ds.H, ds.dk), 0.0, 0.1) if ds.op == "rwkv6" else None
     out["X0"] = _normal(rng, (ds.B, ds.H, ds.dk, ds.dv), 0.0, 0.1)
+    if ds.gated:
+        out["W_g"] = _normal(rng, (ds.hidden, ds.H * ds.dv), 0.0, 1.0 / np.sqrt(ds.hidden))
+        out["g"] = _normal(rng, (ds.dv,), 1.0, 0.1)
     return out
+
+
+def decoder_prompt(ds: DecoderShape, T: int) -> np.ndarray:
+    """A prompt's hidden inputs [B, T, hidden] ~ N(0, 1), stream L + 1."""
+    return _normal(_drng(ds, ds.L + 1), (ds.B, T, ds.hidden))
 
 
 def decoder_input(ds: DecoderShape) -> np.ndarray:

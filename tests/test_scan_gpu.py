@@ -362,3 +362,101 @@ def test_another_stream_and_two_at_once():
     torch.cuda.synchronize()
     for (o, s), a in zip(outs, alone):
         assert torch.equal(o, a["o"]) and torch.equal(s, a["state"])
+
+
+@needs_gpu
+def test_refusals():
+    """Shapes, types, devices and layouts that the entry point names."""
+    import recurrent_state_update_amd as rsu
+    c = {n: None if t is None else t.cuda() for n, t in inputs("gdn", [20, 12], 2, 16, 32, torch.float32)[0].items()}
+    cu = torch.tensor([0, 20, 32], dtype=torch.int32, device="cuda")
+
+    def call(op="gdn", cu_seqlens=cu, **kw):
+        x = {**c, **kw}
+        return rsu.scan(op, x["q"], x["k"], x["v"], x["beta"], x["log_decay"], u=x["u"],
+                        initial_state=x["initial_state"], cu_seqlens=cu_seqlens)
+    call()
+    bad = [dict(op="gla"), dict(op="rwkv6"), dict(op="kda"), dict(q=c["q"].half()), dict(k=c["k"][:, :1]),
+           dict(k=c["k"].bfloat16()), dict(v=c["v"][:31]), dict(v=c["v"][..., :24]), dict(beta=None),
+           dict(beta=c["beta"].double()), dict(log_decay=c["log_decay"][:, :1]), dict(u=c["q"][0]),
+           dict(initial_state=c["initial_state"][:1]), dict(initial_state=c["initial_state"].bfloat16()),
+           dict(beta=c["beta"].cpu()), dict(cu_seqlens=cu.long()), dict(cu_seqlens=cu.cpu()), dict(cu_seqlens=cu[:1]),
+           dict(cu_seqlens=None), dict(q=c["q"][0]), dict(q=c["q"][..., :8].repeat(1, 1, 3), k=c["k"][..., :8].repeat(1, 1, 3))]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            call(**kw)
+    st = rsu.DeltaLogState("gdn", 3, 2, 16, 32, 4, dtype=torch.float32)
+    a = tuple(c[n] for n in ("q", "k", "v", "beta", "log_decay"))
+    for slots in (None, [0], [0, 0], [0, 3], [-1, 0]):
+        with pytest.raises(ValueError):
+            st.prefill(*a, cu_seqlens=cu, slots=slots)
+    with pytest.raises(ValueError):
+        st.prefill(a[0].bfloat16(), a[1].bfloat16(), a[2].bfloat16(), *a[3:], cu_seqlens=cu, slots=[0, 1])
+    st.prefill(*a, cu_seqlens=cu, slots=[2, 0])
+    assert not st.base[1].any() and st.base[0].any() and st.base[2].any()
+    st.close()
+
+
+@needs_gpu
+@pytest.mark.parametrize("op", OPS)
+def test_bad_offsets_stay_in_range(op):
+    """Offsets out of order or out of range: meaningless results, no access
+    outside the tensors (guard rows around every output keep their values)."""
+    import recurrent_state_update_amd as rsu
+    T, H, d = 100, 2, 32
+    x = {n: None if t is None else t.cuda() for n, t in inputs(op, [T], H, d, d, torch.float32, init=False)[0].items()}
+    for cu in ([0, 70, 30, 100], [0, 200, 300, 400], [-50, -20, 40, 1 << 30], [100, 0, 0, 0], [0, 0, 0, 0]):
+        cut = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        o = torch.full((T + 2, H, d), 5.0, device="cuda")
+        fin = torch.full((3 + 2, H, d, d), 5.0, device="cuda")
+        p = {n: None if t is None else t.data_ptr() for n, t in x.items()}
+        desc = rsu.dl_scan_desc(rsu.OPS[op], 0, T, 3, H, d, d, 0, 0, 0, cut.data_ptr(), p["q"], p["k"], p["v"], p["beta"],
+                                p["log_decay"], p["u"])
+        n = rsu.dl_scan_workspace_bytes(desc)
+        ws = torch.full((n + 512,), 7, dtype=torch.uint8, device="cuda")
+        assert rsu.dl_scan(desc, None, fin[1], None, 0, o[1], None, ws) == 0
+        torch.cuda.synchronize()
+        assert (o[0] == 5).all() and (o[-1] == 5).all() and (fin[0] == 5).all() and (fin[-1] == 5).all()
+        assert (ws[n:] == 7).all()
+
+
+@needs_gpu
+@pytest.mark.parametrize("op", OPS)
+def test_state_rows_and_null_outputs(op):
+    """State rows by index, some out of range; no end state; no initial one."""
+    import recurrent_state_update_amd as rsu
+    H, d = 2, 32
+    x, cu, _, _ = inputs(op, [40, 30, 20], H, d, d, torch.float32, init=False)
+    c = {n: None if t is None else t.cuda() for n, t in x.items()}
+    want = gpu_run(op, x, cu, None, None, grad=False)
+    p = {n: None if t is None else t.data_ptr() for n, t in c.items()}
+    cut = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    desc = rsu.dl_scan_desc(rsu.OPS[op], 0, 90, 3, H, d, d, 0, 0, 0, cut.data_ptr(), p["q"], p["k"], p["v"], p["beta"],
+                            p["log_decay"], p["u"])
+    ws = torch.empty(rsu.dl_scan_workspace_bytes(desc), dtype=torch.uint8, device="cuda")
+    o = torch.empty(90, H, d, device="cuda")
+    base = torch.zeros(4, H, d, d, device="cuda")
+    rows = torch.tensor([3, 9, 0], dtype=torch.int32, device="cuda")
+    assert rsu.dl_scan(desc, base, base, rows, 4, o, None, ws) == 0
+    assert torch.equal(o, want["o"])
+    assert torch.equal(base[3], want["state"][0]) and torch.equal(base[0], want["state"][2])
+    assert not base[1:3].any()
+    o.zero_()
+    assert rsu.dl_scan(desc, None, None, None, 0, o, None, ws) == 0
+    assert torch.equal(o, want["o"])
+
+
+@needs_gpu
+@pytest.mark.parametrize("op", OPS)
+def test_nan_stays_in_its_sequence_and_head(op):
+    x, cu, _, _ = inputs(op, [70, 50], 3, 16, 16, torch.float32)
+    want = gpu_run(op, x, cu, None, None, grad=False)
+    for n in ("q", "k", "v", "log_decay"):
+        y = {m: None if t is None else t.clone() for m, t in x.items()}
+        y[n][80, 1] = float("nan")
+        got = gpu_run(op, y, cu, None, None, grad=False)
+        assert torch.equal(got["o"][:70], want["o"][:70]) and torch.equal(got["o"][:, [0, 2]], want["o"][:, [0, 2]])
+        assert torch.equal(got["state"][0], want["state"][0]) and torch.equal(got["state"][1][[0, 2]], want["state"][1][[0, 2]])
+        # RWKV6 reads the state before the token's own decay
+        row = 81 if (op, n) == ("rwkv6", "log_decay") else 80
+        assert not torch.isfinite(got["o"][row, 1]).all()
