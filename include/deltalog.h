@@ -288,8 +288,8 @@ int dl_slot_log_len(const dl_state *s, int slot);
  * the next (0: H*d).  beta [tokens,H], log_decay [tokens,H] (GDN) or
  * [tokens,H,d_k], u [H,d_k] as for dl_decode_step. */
 typedef struct {
-    dl_op op;
-    dl_dtype in_dtype;
+    int op;       /* a dl_op */
+    int in_dtype; /* a dl_dtype */
     int tokens, seqs, H, d_k, d_v;
     long long q_stride, k_stride, v_stride;
     const int *cu_seqlens;
