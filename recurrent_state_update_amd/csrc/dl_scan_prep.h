@@ -198,14 +198,11 @@ __global__ __launch_bounds__(prep_threads<DKP>(), 4) void scan_prep_kernel(ScanA
 
         const int d = tid % DP, I0 = tid / DP, r0 = I0 * 16; // one thread per (key, block)
         const bool mine = tid < 4 * DP;
-        float ev[16];
         if (mine) {
             float p = 1.f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                ev[i] = s.e[(r0 + i) * LD + d];
-                p *= ev[i];
-            }
+            for (int i = 0; i < 16; ++i)
+                p *= s.e[(r0 + i) * LD + d];
             s.eb[tid] = p;
             s.inv[tid] = 1.f / p;
             if (!(p >= 0x1p-40f)) // a NaN decay takes the pairwise way as well
@@ -223,31 +220,31 @@ __global__ __launch_bounds__(prep_threads<DKP>(), 4) void scan_prep_kernel(ScanA
             // wave w takes block w; lane = (column j, quarter of the keys)
             const int j = lane & 15, g = lane >> 4, b0 = w * 16;
             if (w < 4 && s.strong[w]) {
-                float sa[16], sb[16];
+#pragma unroll 1
+                for (int isA = 0; isA < (DELTA ? 2 : 1); ++isA) {
+                    const float *left = isA ? s.k : s.q;
+                    float x[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    sa[i] = sb[i] = 0.f;
-                for (int c = g * (DP / 4); c < (g + 1) * (DP / 4); ++c) {
-                    const float kj = s.k[(b0 + j) * LD + c];
-                    float kd = 0.f; // P_ij k_j
+                    for (int i = 0; i < 16; ++i)
+                        x[i] = 0.f;
+                    for (int c = g * (DP / 4); c < (g + 1) * (DP / 4); ++c) {
+                        const float kj = s.k[(b0 + j) * LD + c];
+                        float kd = 0.f; // P_ij k_j
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float e = s.e[(b0 + i) * LD + c], qi = s.q[(b0 + i) * LD + c];
-                        if (!DELTA)
-                            sb[i] = fmaf(kd, qi, sb[i]); // before the decay of row i
-                        kd = i == j ? kj : kd * e;
-                        if (DELTA) {
-                            sb[i] = fmaf(kd, qi, sb[i]);
-                            sa[i] = fmaf(kd, s.k[(b0 + i) * LD + c], sa[i]);
+                        for (int i = 0; i < 16; ++i) {
+                            const float e = s.e[(b0 + i) * LD + c], l = left[(b0 + i) * LD + c];
+                            if (!DELTA)
+                                x[i] = fmaf(kd, l, x[i]); // before the decay of row i
+                            kd = i == j ? kj : kd * e;
+                            if (DELTA)
+                                x[i] = fmaf(kd, l, x[i]);
                         }
                     }
-                }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float va = DELTA ? wave_sum_from<16>(sa[i]) : 0.f, vb = wave_sum_from<16>(sb[i]);
-                    if (g == 0) {
-                        s.pair[0][w][i * 16 + j] += vb;
-                        s.pair[1][w][i * 16 + j] += va;
+                    for (int i = 0; i < 16; ++i) {
+                        const float v = wave_sum_from<16>(x[i]);
+                        if (g == 0)
+                            s.pair[isA][w][i * 16 + j] += v;
                     }
                 }
             }
@@ -256,10 +253,11 @@ __global__ __launch_bounds__(prep_threads<DKP>(), 4) void scan_prep_kernel(ScanA
 
         // in place: k -> k (prefix in its block), q -> q (prefix), e -> k (suffix)
         if (mine) {
-            float kv[16], p = 1.f;
+            float kv[16], ev[16], p = 1.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 kv[i] = s.k[(r0 + i) * LD + d];
+                ev[i] = s.e[(r0 + i) * LD + d];
                 const float before = p;
                 p *= ev[i];
                 s.q[(r0 + i) * LD + d] *= DELTA ? p : before;
