@@ -92,12 +92,13 @@ constexpr int scan_keys(int dk) { return dk < 32 ? 32 : dk; }
 // bf16 planes of the keys' operands: GDN's are the inputs themselves, exact in
 // one plane where they are bf16; the others carry fp32 decays.
 constexpr int scan_planes(int op, int dtype) { return op == GDN && dtype == BF16 ? 1 : 3; }
-// Bytes of one chunk and head's operands: three chunk x keys and three
-// chunk x chunk matrices, a decay per key, and three numbers per row.
+// Bytes of one chunk and head's operands: three chunk x keys matrices (bf16
+// where one plane holds them, else fp32), two chunk x chunk ones, twenty
+// 16 x 16 blocks, a decay per key, and three numbers per row.
 constexpr size_t scan_op_bytes(int planes, int keys)
 {
-    return size_t(2) * 3 * (planes * kScanChunk * keys + 3 * kScanChunk * kScanChunk) +
-           4 * (keys + 3 * kScanChunk);
+    return size_t(3) * kScanChunk * keys * (planes == 1 ? 2 : 4) + size_t(2) * kScanChunk * kScanChunk * 4 +
+           20 * 16 * 16 * 4 + 4 * (keys + 3 * kScanChunk);
 }
 
 // One scan, forward or backward.  Token strides in elements.

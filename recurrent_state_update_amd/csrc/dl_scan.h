@@ -220,44 +220,79 @@ __device__ __forceinline__ Chunk chunk_of(const ScanArgs &a, int slot)
 
 // -------------------------------------------------------- operands in memory --
 //
-// Per slot and head: three operands of C x DKP elements and three of C x C in
-// bf16 planes, Gam_C, and per row i Gam_i, P_Ci (used where Plan::ROWS) and
-// beta_i (zero behind the end).  An operand [rows][k] is stored as matrix
-// fragments: (16 rows, 32 k, plane) -> 64 lanes x 8 elements, lane l holding
-// row l % 16, k from 8 (l / 16): one coalesced 1 KiB load per fragment.
+// Per slot and head: three operands of C x DKP elements, two of C x C, A and B
+// in blocks (backward), Gam_C, and per row i Gam_i, P_Ci (used where
+// Plan::ROWS) and beta_i (zero behind the end).  An operand [rows][k] is stored
+// as the fragments that the matrix instruction reads: of 16 rows x 32 k lane l
+// holds row l % 16, k from 8 (l / 16).  One or two planes are stored as such
+// (64 lanes x 8 bf16 each: one coalesced 1 KiB load); three are stored as the
+// fp32 values (four bytes, not six), 64 lanes x 4 twice, and split when read.
 //   forward : op 0 K~ [C][DKP], 1 Q~ [C][DKP], 2 K^T^ [DKP][C]; mat 0 N, 1 B
 //   backward: op 0 K^ [C][DKP], 1 Q~^T [DKP][C], 2 K~^T [DKP][C]; mat 0 N^T,
-//             1 B^T, 2 A and (GDN) B in fp32 blocks (store_pair)
+//             1 B^T; pairs: A and (GDN) B, fp32 (store_pair)
 // (ROWS: K and Q without their decays.)  Of the triangular C x C operands the
 // fragments of zeros are neither written nor read.
 template <int NP, int DKP> struct Ops {
-    static constexpr size_t kOp = size_t(NP) * C * DKP, kMat = size_t(3) * C * C; // elements
+    static constexpr size_t kOp = size_t(C) * DKP * (NP == 1 ? 2 : 4), kMat = size_t(C) * C * 4; // bytes
     static constexpr size_t kBytes = scan_op_bytes(NP, DKP);
     char *p;
     __device__ __forceinline__ Ops(const ScanArgs &a, long slot_head) : p(a.ops + slot_head * kBytes) {}
-    __device__ __forceinline__ __bf16 *op(int i) const { return reinterpret_cast<__bf16 *>(p) + i * kOp; }
-    __device__ __forceinline__ __bf16 *mat(int i) const { return reinterpret_cast<__bf16 *>(p) + 3 * kOp + i * kMat; }
-    __device__ __forceinline__ float *gam() const { return reinterpret_cast<float *>(p + 2 * (3 * kOp + 3 * kMat)); }
+    __device__ __forceinline__ char *op(int i) const { return p + i * kOp; }
+    __device__ __forceinline__ char *mat(int i) const { return p + 3 * kOp + i * kMat; }
+    __device__ __forceinline__ f32x4 *pairs() const { return reinterpret_cast<f32x4 *>(p + 3 * kOp + 2 * kMat); }
+    __device__ __forceinline__ float *gam() const { return reinterpret_cast<float *>(p + 3 * kOp + 2 * kMat + 20 * 1024); }
     __device__ __forceinline__ float *row(int i) const { return gam() + DKP + i * C; } // 0 Gam_i, 1 P_Ci, 2 beta
 };
 
+// A fragment in memory: its size, and a lane's loads and stores.
+template <int N> constexpr int frag_bytes() { return N == 3 ? 2048 : N * 1024; }
 // (uniform base + 32-bit lane offset: the load's scalar-address form)
 template <int N>
-__device__ __forceinline__ void load_frag(bf16x8 (&f)[N], const __bf16 *op, int ksteps, int rb, int ks, int lane)
+__device__ __forceinline__ void load_frag(bf16x8 (&f)[N], const char *op, int ksteps, int rb, int ks, int lane)
 {
-    const char *base = reinterpret_cast<const char *>(op) + (rb * ksteps + ks) * N * 1024;
+    static_assert(N < 3, "three planes are read as fp32");
+    const char *base = op + (rb * ksteps + ks) * frag_bytes<N>();
     const unsigned off = lane * 16;
 #pragma unroll
     for (int i = 0; i < N; ++i)
         f[i] = *reinterpret_cast<const bf16x8 *>(base + (off + i * 1024));
 }
-template <int N>
-__device__ __forceinline__ void store_frag(__bf16 *op, int ksteps, int rb, int ks, int lane, const bf16x8 (&f)[N])
+__device__ __forceinline__ f32x8 load_frag32(const char *op, int ksteps, int rb, int ks, int lane)
 {
-    bf16x8 *p = reinterpret_cast<bf16x8 *>(op) + ((rb * ksteps + ks) * N) * 64 + lane;
+    const char *base = op + (rb * ksteps + ks) * frag_bytes<3>();
+    const unsigned off = lane * 16;
+    const f32x4 x = *reinterpret_cast<const f32x4 *>(base + off), y = *reinterpret_cast<const f32x4 *>(base + (off + 1024));
+    return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+// Store x in N planes (three: as it is).
+template <int N> __device__ __forceinline__ void store_frag(char *op, int ksteps, int rb, int ks, int lane, f32x8 x)
+{
+    char *p = op + (rb * ksteps + ks) * frag_bytes<N>() + lane * 16;
+    if constexpr (N == 3) {
+        *reinterpret_cast<f32x4 *>(p) = __builtin_shufflevector(x, x, 0, 1, 2, 3);
+        *reinterpret_cast<f32x4 *>(p + 1024) = __builtin_shufflevector(x, x, 4, 5, 6, 7);
+    } else {
+        bf16x8 f[N];
+        split(x, f);
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        p[i * 64] = f[i];
+        for (int i = 0; i < N; ++i)
+            *reinterpret_cast<bf16x8 *>(p + i * 1024) = f[i];
+    }
+}
+// The same of planes in registers.
+template <int N, int M>
+__device__ __forceinline__ void store_frag(char *op, int ksteps, int rb, int ks, int lane, const bf16x8 (&f)[M])
+{
+    if constexpr (N == 3) {
+        store_frag<3>(op, ksteps, rb, ks, lane,
+                      __builtin_convertvector(f[0], f32x8) + __builtin_convertvector(f[1], f32x8) +
+                          __builtin_convertvector(f[2], f32x8));
+    } else {
+        char *p = op + (rb * ksteps + ks) * frag_bytes<N>() + lane * 16;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            *reinterpret_cast<bf16x8 *>(p + i * 1024) = f[i];
+    }
 }
 // Whether fragment (rb, ks) of a triangular C x C operand holds anything.
 enum Part { ALL, LOWER, UPPER };
@@ -266,7 +301,7 @@ __device__ __forceinline__ bool frag_used(Part part, int rb, int ks)
     return part == ALL || (part == LOWER ? ks == 0 || rb >= 2 : ks == 1 || rb < 2);
 }
 // Write the fragments of [ROWS][K] in N planes, element (r, k) given by f.
-template <int N, int ROWS, int K, Part PART = ALL, typename F> __device__ __forceinline__ void store_op(__bf16 *op, F f)
+template <int N, int ROWS, int K, Part PART = ALL, typename F> __device__ __forceinline__ void store_op(char *op, F f)
 {
     for (int it = threadIdx.x; it < ROWS / 16 * (K / 32) * 64; it += blockDim.x) {
         const int lane = it & 63, rb = (it >> 6) / (K / 32), ks = (it >> 6) % (K / 32);
@@ -276,9 +311,7 @@ template <int N, int ROWS, int K, Part PART = ALL, typename F> __device__ __forc
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             x[e] = f(rb * 16 + (lane & 15), ks * 32 + (lane >> 4) * 8 + e);
-        bf16x8 p[N];
-        split(x, p);
-        store_frag(op, K / 32, rb, ks, lane, p);
+        store_frag<N>(op, K / 32, rb, ks, lane, x);
     }
 }
 

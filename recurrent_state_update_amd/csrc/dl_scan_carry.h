@@ -91,20 +91,43 @@ __device__ __forceinline__ f32x4 product_tri(const bf16x8 (&a)[2][NA], const Pla
     }
     return c.sum();
 }
-template <int KS, int NP> __device__ __forceinline__ void load_rows(bf16x8 (&f)[KS][NP], const __bf16 *op, int rb, int lane)
-{
+// A row block's fragments of an operand in N planes: loaded some phases ahead,
+// and, where they come as fp32, split (ready) while the wave has nothing else
+// to do.
+template <int KS, int N> struct Operand {
+    bf16x8 f[KS][N];
+    f32x8 raw[N == 3 ? KS : 1];
+    __device__ __forceinline__ void one(const char *op, int rb, int at, int ks, int lane)
+    {
+        if constexpr (N == 3)
+            raw[at] = load_frag32(op, KS, rb, ks, lane);
+        else
+            load_frag(f[at], op, KS, rb, ks, lane);
+    }
+    __device__ __forceinline__ void load(const char *op, int rb, int lane)
+    {
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-        load_frag(f[ks], op, KS, rb, ks, lane);
-}
-// A row block of a triangular operand; the half that holds nothing is not
-// stored, and the other is loaded in its place (the load stays unconditional).
-template <int NP> __device__ __forceinline__ void load_tri(bf16x8 (&f)[2][NP], const __bf16 *op, Part part, int rb, int lane)
-{
+        for (int ks = 0; ks < KS; ++ks)
+            one(op, rb, ks, ks, lane);
+    }
+    // Of a triangular operand; the half that holds nothing is not stored, and
+    // the other is loaded in its place (the load stays unconditional).
+    __device__ __forceinline__ void load_tri(const char *op, Part part, int rb, int lane)
+    {
+        static_assert(KS == 2, "C x C");
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-        load_frag(f[ks], op, 2, rb, frag_used(part, rb, ks) ? ks : 1 - ks, lane);
-}
+        for (int ks = 0; ks < 2; ++ks)
+            one(op, rb, ks, frag_used(part, rb, ks) ? ks : 1 - ks, lane);
+    }
+    __device__ __forceinline__ void ready()
+    {
+        if constexpr (N == 3) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+                split(raw[ks], f[ks]);
+        }
+    }
+};
 __device__ __forceinline__ f32x4 ld4(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
 
 // The state row of a sequence: through a.rows if given; < 0 where the row is
@@ -185,12 +208,13 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
     auto ops = [&](int c) { return O(a, static_cast<long>(sq.base + c) * a.H + h); };
 
     // o = Q~ S + B b of rows i0..
-    bf16x8 qf[KS][P::NPQ], bf[2][P::NPB];
+    Operand<KS, P::NPQ> qf;
+    Operand<2, P::NPB> bf;
     TIn *op = static_cast<TIn *>(a.o) + static_cast<long>(sq.start) * width + first;
-    auto load_q = [&](int c) { load_rows(qf, ops(c).op(1), w & 3, lane); };
-    auto load_b = [&](int c) { load_tri(bf, ops(c).mat(1), LOWER, w & 3, lane); };
+    auto load_q = [&](int c) { qf.load(ops(c).op(1), w & 3, lane); };
+    auto load_b = [&](int c) { bf.load_tri(ops(c).mat(1), LOWER, w & 3, lane); };
     auto with_b = [&](f32x4 o, const Planes<P::NPB, C> &b) {
-        return product_tri<P::ORDER_O>(bf, b, true, (w & 3) >= 2, lane, o);
+        return product_tri<P::ORDER_O>(bf.f, b, true, (w & 3) >= 2, lane, o);
     };
     auto store_o = [&](int c, const f32x4 (&o)[NC]) {
         const ChunkRows<TIn> rows(op, width, c, sq.len, 16 * NC);
@@ -218,15 +242,16 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
         load_v(0);
         keep_order();
         if constexpr (DELTA) {
-            bf16x8 kf[KS][P::NPX], nf[2][3];
+            Operand<KS, P::NPX> kf;
+            Operand<2, 3> nf;
             f32x4 gi, ge, beta;
             auto load_k = [&](int c) {
-                load_rows(kf, ops(c).op(0), w, lane);
+                kf.load(ops(c).op(0), w, lane);
                 if (ROWS)
                     gi = ld4(ops(c).row(0) + i0);
             };
             auto load_n = [&](int c) {
-                load_tri(nf, ops(c).mat(0), LOWER, w, lane);
+                nf.load_tri(ops(c).mat(0), LOWER, w, lane);
                 beta = ld4(ops(c).row(2) + i0);
                 if (ROWS)
                     ge = ld4(ops(c).row(1) + i0);
@@ -235,6 +260,8 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
             keep_order();
             load_n(0);
             keep_order();
+            kf.ready();
+            nf.ready();
             for (int c = 0; c < chunks; ++c) {
                 const int next = c + 1 < chunks ? c + 1 : c;
                 f32x4 x[NC];
@@ -247,7 +274,7 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
                 for (int t = 0; t < NC; ++t) {
                     bf16x8 f[KS][3];
                     get_all(f, sp[0][t], lane);
-                    f32x4 ks = product<3>(kf, f, zero);
+                    f32x4 ks = product<3>(kf.f, f, zero);
                     if (ROWS)
                         ks *= gi;
                     rp[t].put(col, i0, x[t] - ks);
@@ -256,7 +283,7 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
                 __syncthreads(); // V - K~ S is complete, and the state's planes are read
 #pragma unroll
                 for (int t = 0; t < NC; ++t) {
-                    x[t] = product_tri<3>(nf, rp[t], true, w >= 2, lane, zero);
+                    x[t] = product_tri<3>(nf.f, rp[t], true, w >= 2, lane, zero);
                     const f32x4 b = x[t] * beta;
                     hp[0][t].put(col, i0, ROWS ? b * ge : b);
                     bp[c & 1][t].put(col, i0, b);
@@ -271,6 +298,8 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
                             a.save_e[(sh * C + i0 + e) * a.dv + v0 + 16 * t] = x[t][e];
                 }
                 __syncthreads(); // b is complete
+                kf.ready();
+                nf.ready();
             }
         } else {
             auto put_v = [&](int c) {
@@ -287,6 +316,8 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
             keep_order();
             load_b(0);
             keep_order();
+            qf.ready();
+            bf.ready();
             for (int c = 0; c < chunks; ++c) {
                 __syncthreads(); // state and b are complete
                 const int next = c + 1 < chunks ? c + 1 : c, after = c + 2 < chunks ? c + 2 : next;
@@ -295,13 +326,15 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
                 for (int t = 0; t < NC; ++t) {
                     bf16x8 f[KS][P::ORDER_O];
                     get_all(f, sp[c & 1][t], lane);
-                    o[t] = with_b(product<P::ORDER_O>(qf, f, zero), bp[c & 1][t]);
+                    o[t] = with_b(product<P::ORDER_O>(qf.f, f, zero), bp[c & 1][t]);
                 }
                 put_v(c + 1); // (behind the last chunk: read by nobody)
                 load_v(after);
                 load_q(next);
                 load_b(next);
                 store_o(c, o);
+                qf.ready();
+                bf.ready();
             }
         }
         return;
@@ -312,11 +345,11 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
     const long row = state_row(a, n);
     const long st0 = (row * a.H + h) * a.dk * a.dv + v0;
     f32x4 S[NC][RB], gam[RB];
-    bf16x8 tf[RB][2][P::NPX];
+    Operand<2, P::NPX> tf[RB];
     auto load_t = [&](int c) {
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
-            load_rows(tf[r], ops(c).op(2), Own::block(wb, r), lane);
+            tf[r].load(ops(c).op(2), Own::block(wb, r), lane);
             gam[r] = ld4(ops(c).gam() + Own::block(wb, r) * 16 + r4);
         }
     };
@@ -366,6 +399,10 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
         }
         load_t(0);
         keep_order();
+        if (DELTA) {
+            qf.ready();
+            bf.ready();
+        }
         for (int c = 0; c < chunks; ++c) {
             const int next = c + 1 < chunks ? c + 1 : c;
             __syncthreads();
@@ -374,7 +411,7 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
                 for (int t = 0; t < NC; ++t) {
                     bf16x8 f[KS][P::ORDER_O];
                     get_all(f, sp[0][t], lane);
-                    o[t] = product<P::ORDER_O>(qf, f, zero);
+                    o[t] = product<P::ORDER_O>(qf.f, f, zero);
                     if (ROWS)
                         o[t] *= gi;
                 }
@@ -391,15 +428,21 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
 #pragma unroll
                 for (int t = 0; t < NC; ++t)
                     last[t] = o[t];
-                __syncthreads();
+                qf.ready();
+                bf.ready();
             }
+#pragma unroll
+            for (int r = 0; r < RB; ++r)
+                tf[r].ready();
+            if constexpr (DELTA)
+                __syncthreads();
 #pragma unroll
             for (int t = 0; t < NC; ++t) {
                 bf16x8 f[2][3];
                 get_all(f, hp[DELTA ? 0 : c & 1][t], lane);
 #pragma unroll
                 for (int r = 0; r < RB; ++r)
-                    S[t][r] = product<3>(tf[r], f, S[t][r] * gam[r]);
+                    S[t][r] = product<3>(tf[r].f, f, S[t][r] * gam[r]);
             }
             load_t(next);
             put_state(c + 1);
@@ -461,13 +504,14 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
     if (w < 4) {
         if (chunks == 0)
             return; // barriers count the waves that are left
-        bf16x8 kf[KS][P::NPX], bt[2][3], nt[2][3];
+        Operand<KS, P::NPX> kf;
+        Operand<2, 3> bt, nt;
         f32x4 gi, ge, beta;
         float E[NC][4];
         TIn *dvp = static_cast<TIn *>(a.d_v) + static_cast<long>(sq.start) * width + first;
         auto load_db = [&](int c) {
-            load_tri(bt, ops(c).mat(1), UPPER, w, lane);
-            load_rows(kf, ops(c).op(0), w, lane);
+            bt.load_tri(ops(c).mat(1), UPPER, w, lane);
+            kf.load(ops(c).op(0), w, lane);
             if (ROWS)
                 ge = ld4(ops(c).row(1) + i0);
             if (DELTA)
@@ -475,7 +519,7 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
         };
         auto load_n = [&](int c) {
             if (DELTA)
-                load_tri(nt, ops(c).mat(0), UPPER, w, lane);
+                nt.load_tri(ops(c).mat(0), UPPER, w, lane);
             if (ROWS)
                 gi = ld4(ops(c).row(0) + i0);
         };
@@ -494,6 +538,13 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
         keep_order();
         load_e(chunks - 1);
         keep_order();
+        auto ready = [&] {
+            kf.ready();
+            bt.ready();
+            if (DELTA)
+                nt.ready();
+        };
+        ready();
         for (int c = chunks - 1; c >= 0; --c) {
             const int next = c > 0 ? c - 1 : 0;
             const long sh = static_cast<long>(sq.base + c) * a.H + h;
@@ -503,10 +554,10 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
             for (int t = 0; t < NC; ++t) {
                 bf16x8 f[KS][3];
                 get_all(f, sp[DELTA ? 0 : c & 1][t], lane);
-                db[t] = product<3>(kf, f, zero);
+                db[t] = product<3>(kf.f, f, zero);
                 if (ROWS)
                     db[t] *= ge;
-                db[t] = product_tri<3>(bt, gp[c & 1][t], w < 2, true, lane, db[t]);
+                db[t] = product_tri<3>(bt.f, gp[c & 1][t], w < 2, true, lane, db[t]);
                 x[t] = db[t];
                 if (DELTA)
                     wp[t].put(col, i0, db[t] * beta);
@@ -516,7 +567,7 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
                 __syncthreads(); // beta db is complete; the planes of dS' are read
 #pragma unroll
                 for (int t = 0; t < NC; ++t) {
-                    x[t] = product_tri<3>(nt, wp[t], w < 2, true, lane, zero);
+                    x[t] = product_tri<3>(nt.f, wp[t], w < 2, true, lane, zero);
                     zp[t].put(col, i0, ROWS ? -x[t] * gi : -x[t]);
                 }
                 load_n(next);
@@ -549,6 +600,7 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
                 }
             if (DELTA && col == 0)
                 *reinterpret_cast<f32x4 *>(&a.w_db[(sh * tiles + wk.tile) * C + i0]) = p;
+            ready();
         }
         return;
     }
@@ -557,7 +609,7 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
     const bool has = Own::has(wb);
     const long st0 = (static_cast<long>(n) * a.H + h) * a.dk * a.dv + v0;
     f32x4 S[NC][RB], gam[RB], gi; // S: dS'
-    bf16x8 qt[RB][2][P::NPX], kt[RB][2][P::NPX];
+    Operand<2, P::NPX> qt[RB], kt[RB];
     TIn g[NC][4];
     const TIn *gbase = static_cast<const TIn *>(a.d_o) + static_cast<long>(sq.start) * width + first;
     auto load_g = [&](int c) {
@@ -584,7 +636,7 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
     auto load_q = [&](int c) {
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
-            load_rows(qt[r], ops(c).op(1), Own::block(wb, r), lane);
+            qt[r].load(ops(c).op(1), Own::block(wb, r), lane);
             gam[r] = ld4(ops(c).gam() + Own::block(wb, r) * 16 + r4);
         }
     };
@@ -593,7 +645,7 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
             return;
 #pragma unroll
         for (int r = 0; r < RB; ++r)
-            load_rows(kt[r], ops(c).op(2), Own::block(wb, r), lane);
+            kt[r].load(ops(c).op(2), Own::block(wb, r), lane);
     };
     auto put_state = [&](int c) { // the planes of the gradient of chunk c's end state
         if (!has)
@@ -627,16 +679,23 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
         load_g(chunks - 1);
         put_g(chunks - 1);
         keep_order();
-        load_q(chunks - 1);
-        keep_order();
         load_g(chunks > 1 ? chunks - 2 : 0);
+        keep_order();
+        load_q(chunks - 1);
         keep_order();
         load_k(chunks - 1);
         keep_order();
         for (int c = chunks - 1; c >= 0; --c) {
             const int next = c > 0 ? c - 1 : 0;
             __syncthreads();
+            put_g(c - 1); // (ahead of the first chunk: read by nobody)
+            load_g(c > 1 ? c - 2 : 0);
+            if constexpr (DELTA)
+                __syncthreads();
             // dS = Gam_C dS' + Q~^T dO - K~^T z, all but the last ahead of z
+#pragma unroll
+            for (int r = 0; r < RB; ++r)
+                qt[r].ready();
 #pragma unroll
             for (int t = 0; t < NC; ++t) {
                 bf16x8 f[2][ROWS ? 3 : P::NPI];
@@ -646,13 +705,13 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
                     get_all(f, gp[c & 1][t], lane);
 #pragma unroll
                 for (int r = 0; r < RB; ++r)
-                    S[t][r] = product<3>(qt[r], f, S[t][r] * gam[r]);
+                    S[t][r] = product<3>(qt[r].f, f, S[t][r] * gam[r]);
             }
             load_q(next);
-            put_g(c - 1); // (ahead of the first chunk: read by nobody)
-            load_g(c > 1 ? c - 2 : 0);
             if constexpr (DELTA) {
-                __syncthreads();
+#pragma unroll
+                for (int r = 0; r < RB; ++r)
+                    kt[r].ready();
                 __syncthreads();
 #pragma unroll
                 for (int t = 0; t < NC; ++t) {
@@ -660,7 +719,7 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
                     get_all(f, zp[t], lane);
 #pragma unroll
                     for (int r = 0; r < RB; ++r)
-                        S[t][r] = product<3>(kt[r], f, S[t][r]);
+                        S[t][r] = product<3>(kt[r].f, f, S[t][r]);
                 }
             }
             load_k(next);

@@ -249,7 +249,7 @@ __global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_gr
             if (b >= 10)
                 break;
             const int I = block_row(b), J = block_col(b);
-            const f32x4 *ab = reinterpret_cast<const f32x4 *>(ops.mat(2));
+            const f32x4 *ab = ops.pairs();
             const f32x4 A = ab[b * 64 + lane], B = ab[(10 + b) * 64 + lane];
             const float beta = s.beta[J * 16 + c16];
             float between = 1.f, cm = 0.f, cw = 0.f;
@@ -300,12 +300,9 @@ __global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_gr
             }
         }
         // ---- wave w: keys 16 w.., all rows
-        bf16x8 kt[2][P::NPX], qt[2][P::NPX];
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            load_frag(qt[ks], ops.op(1), 2, w, ks, lane);
-            load_frag(kt[ks], ops.op(2), 2, w, ks, lane);
-        }
+        Operand<2, P::NPX> kt, qt;
+        qt.load(ops.op(1), w, lane);
+        kt.load(ops.op(2), w, lane);
         TIn kx[4][4], qx[4][4]; // this lane's key in all rows
 #pragma unroll
         for (int I = 0; I < 4; ++I)
@@ -318,6 +315,8 @@ __global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_gr
                 qx[I][e] = in ? static_cast<const TIn *>(a.q)[(t0 + i) * a.qs + at] : TIn(0);
             }
         __syncthreads();
+        qt.ready();
+        kt.ready();
         auto xfrag = [&](bf16x8 (&f)[G::NX], const __bf16 (&x)[G::NX][C * G::XLD], int rb, int ks) {
 #pragma unroll
             for (int n = 0; n < G::NX; ++n)
@@ -358,13 +357,13 @@ __global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_gr
                 bf16x8 f[G::NX];
                 if (frag_used(LOWER, I, ks)) {
                     xfrag(f, s.x.x1, I, ks);
-                    dQ[I] = mma<P::ORDER_O>(f, kt[ks], dQ[I]);
+                    dQ[I] = mma<P::ORDER_O>(f, kt.f[ks], dQ[I]);
                 }
                 xfrag(f, s.x.x3, I, ks);
-                dK[I] = mma<P::ORDER_O>(f, kt[ks], dK[I]);
+                dK[I] = mma<P::ORDER_O>(f, kt.f[ks], dK[I]);
                 if (frag_used(UPPER, I, ks)) {
                     xfrag(f, s.x.x2, I, ks);
-                    dK[I] = mma<P::ORDER_O>(f, qt[ks], dK[I]);
+                    dK[I] = mma<P::ORDER_O>(f, qt.f[ks], dK[I]);
                 }
             }
 #pragma unroll
@@ -425,7 +424,7 @@ __global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_gr
             float cm = 0.f;
             f32x4 A = zero;
             if (DELTA)
-                A = reinterpret_cast<const f32x4 *>(ops.mat(2))[b * 64 + lane];
+                A = ops.pairs()[b * 64 + lane];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = I * 16 + r4 + e, j = J * 16 + c16;

@@ -54,10 +54,7 @@ __device__ __forceinline__ int block_col(int b)
 }
 // A (and B) in fp32 for grads: the ten blocks, a lane's four rows of its
 // column as in a product's result; n: block, or 10 + block for B.
-__device__ __forceinline__ void store_pair(__bf16 *mat, int n, int lane, f32x4 v)
-{
-    reinterpret_cast<f32x4 *>(mat)[n * 64 + lane] = v;
-}
+__device__ __forceinline__ void store_pair(f32x4 *pairs, int n, int lane, f32x4 v) { pairs[n * 64 + lane] = v; }
 
 // The C x C matrices of a chunk, once the keys' tiles are done with.
 struct PrepMats {
@@ -307,7 +304,7 @@ __global__ __launch_bounds__(prep_threads<DKP>(), 4) void scan_prep_kernel(ScanA
 
         // operands of C x DKP: this pass's keys
         constexpr int KP = DP / 32, KA = DKP / 32;
-        auto rows = [&](auto np, __bf16 *op, const float *x, const float *scale) {
+        auto rows = [&](auto np, char *op, const float *x, const float *scale) {
             constexpr int NPL = decltype(np)::value;
             for (int it = tid; it < 4 * KP * 64; it += NT) {
                 const int l = it & 63, rb = (it >> 6) / KP, ks = (it >> 6) % KP, c = ks * 32 + (l >> 4) * 8;
@@ -315,12 +312,10 @@ __global__ __launch_bounds__(prep_threads<DKP>(), 4) void scan_prep_kernel(ScanA
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     v[e] = x[(rb * 16 + (l & 15)) * LD + c + e] * scale[rb * DP + c + e];
-                bf16x8 f[NPL];
-                split(v, f);
-                store_frag(op, KA, rb, d0 / 32 + ks, l, f);
+                store_frag<NPL>(op, KA, rb, d0 / 32 + ks, l, v);
             }
         };
-        auto columns = [&](auto np, __bf16 *op, const float *x, const float *scale) {
+        auto columns = [&](auto np, char *op, const float *x, const float *scale) {
             constexpr int NPL = decltype(np)::value;
             for (int it = tid; it < DP / 16 * 2 * 64; it += NT) {
                 const int l = it & 63, rb = (it >> 6) / 2, ks = (it >> 6) % 2, c = rb * 16 + (l & 15), i = ks * 32 + (l >> 4) * 8;
@@ -329,9 +324,7 @@ __global__ __launch_bounds__(prep_threads<DKP>(), 4) void scan_prep_kernel(ScanA
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     v[e] = x[(i + e) * LD + c] * f0;
-                bf16x8 f[NPL];
-                split(v, f);
-                store_frag(op, 2, d0 / 16 + rb, ks, l, f);
+                store_frag<NPL>(op, 2, d0 / 16 + rb, ks, l, v);
             }
         };
         constexpr std::integral_constant<int, P::NPX> npx;
@@ -377,7 +370,7 @@ __global__ __launch_bounds__(prep_threads<DKP>(), 4) void scan_prep_kernel(ScanA
         }
         if (isA) {
             if (BWD)
-                store_pair(ops.mat(2), b, lane, v);
+                store_pair(ops.pairs(), b, lane, v);
             v *= s.beta[J * 16 + j];
         }
         put_block(isA ? s.m.L : s.m.B, I, J, lane, v);
@@ -497,7 +490,7 @@ __global__ __launch_bounds__(256) void scan_prep_gdn_kernel(ScanArgs a, bool vec
         acc[p] = x.sum();
     }
     // the keys' operands: rows of the tiles, and their columns
-    auto rows = [&](auto np, __bf16 *op, const __bf16 (&x)[NP][C * LD]) {
+    auto rows = [&](auto np, char *op, const __bf16 (&x)[NP][C * LD]) {
         constexpr int N = decltype(np)::value;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
@@ -505,10 +498,10 @@ __global__ __launch_bounds__(256) void scan_prep_gdn_kernel(ScanArgs a, bool vec
 #pragma unroll
             for (int n = 0; n < N; ++n)
                 f[n] = *reinterpret_cast<const bf16x8 *>(&x[n][(w * 16 + (lane & 15)) * LD + ks * 32 + (lane >> 4) * 8]);
-            store_frag(op, KS, w, ks, lane, f);
+            store_frag<N>(op, KS, w, ks, lane, f);
         }
     };
-    auto columns = [&](__bf16 *op, const __bf16 (&x)[NP][C * LD]) {
+    auto columns = [&](char *op, const __bf16 (&x)[NP][C * LD]) {
         for (int it = w; it < DKP / 16 * 2; it += 4) {
             const int rb = it / 2, ks = it % 2;
             bf16x8 f[NP];
@@ -517,7 +510,7 @@ __global__ __launch_bounds__(256) void scan_prep_gdn_kernel(ScanArgs a, bool vec
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     f[n][e] = x[n][(ks * 32 + (lane >> 4) * 8 + e) * LD + rb * 16 + (lane & 15)];
-            store_frag(op, 2, rb, ks, lane, f);
+            store_frag<NP>(op, 2, rb, ks, lane, f);
         }
     };
     rows(std::integral_constant<int, NP>(), ops.op(0), s.k);
@@ -557,7 +550,7 @@ __global__ __launch_bounds__(256) void scan_prep_gdn_kernel(ScanArgs a, bool vec
             v[e] = I > J || i > j || (i == j && !isA) ? v[e] * f : 0.f;
         }
         if (BWD)
-            store_pair(ops.mat(2), isA ? b : 10 + b, lane, v);
+            store_pair(ops.pairs(), isA ? b : 10 + b, lane, v);
         if (isA)
             v *= s.beta[J * 16 + j];
         put_block(isA ? s.m.L : s.m.B, I, J, lane, v);
