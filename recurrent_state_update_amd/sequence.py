@@ -135,18 +135,22 @@ class _Scan:
             raise ValueError(f"{T} tokens: want fewer than 2^31")
         self.op, self.device, self.dtype, self.H, self.dk, self.dv = op, dev, q.dtype, H, dk, dv
         self.shape = dict(q=q.shape, v=v.shape, h=(*lead, H), ld=log_decay.shape)
-        q, qs = _rows(q.detach(), len(lead))
-        k, ks = _rows(k.detach(), len(lead))
-        v, vs = _rows(v.detach(), len(lead))
-        beta = None if beta is None else beta.detach().contiguous()
-        log_decay = log_decay.detach().contiguous()
-        u = None if u is None else u.detach().contiguous()
-        self.tensors = (q, k, v, beta, log_decay, u, cu_seqlens)  # kept alive with the descriptor
-        self.desc = dl_scan_desc(opi, dti, T, self.N, H, dk, dv, qs, ks, vs, _p(cu_seqlens), q.data_ptr(),
-                                 k.data_ptr(), v.data_ptr(), _p(beta), log_decay.data_ptr(), _p(u))
+        self.sizes = (opi, dti, T, self.N, H, dk, dv)
+        # the tensors are kept alive with the descriptor
+        self.tensors, self.desc = self.describe(
+            *(None if t is None else t.detach() for t in (q, k, v, beta, log_decay, u)), cu_seqlens)
         self.workspace_bytes = dl_scan_workspace_bytes(self.desc)
         if self.workspace_bytes == 0:
             raise ValueError(f"unsupported scan shape {op} tokens={T} sequences={self.N} H={H} d_k={dk} d_v={dv}")
+
+    def describe(self, q, k, v, beta, log_decay, u, cu_seqlens):
+        """These tensors, copied where the library cannot read them as they
+        are, and their descriptor."""
+        (q, qs), (k, ks), (v, vs) = (_rows(t, len(self.shape["h"]) - 1) for t in (q, k, v))
+        beta, log_decay, u = (None if t is None else t.contiguous() for t in (beta, log_decay, u))
+        return (q, k, v, beta, log_decay, u, cu_seqlens), dl_scan_desc(
+            *self.sizes, qs, ks, vs, _p(cu_seqlens), q.data_ptr(), k.data_ptr(), v.data_ptr(), _p(beta),
+            log_decay.data_ptr(), _p(u))
 
     def state_shape(self):
         return (self.N, self.H, self.dk, self.dv)
@@ -169,18 +173,20 @@ class _ScanFn(torch.autograd.Function):
         saved = _bytes(dl_scan_saved_bytes(s.desc), s.device)
         o = s.forward(initial, final, None, 0, saved)
         ctx.set_materialize_grads(False)
-        # the tensors that the descriptor points at, guarded against changes
+        # guarded against changes, and free to move until they are used
+        # (checkpoints, offloading): the backward pass describes them anew
         ctx.save_for_backward(*s.tensors, saved)
         ctx.scan, ctx.with_initial = s, initial is not None
-        s.tensors = (None,) * 6 + (s.tensors[6],)
+        s.tensors = s.desc = None
         return o, final
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, d_o, d_final):
         s = ctx.scan
-        saved = ctx.saved_tensors[-1]
+        *tensors, saved = ctx.saved_tensors
         with _on(s.device, None):
+            tensors, desc = s.describe(*tensors)
             d_o = None if d_o is None else d_o.contiguous()
             d_final = None if d_final is None else d_final.contiguous()
             delta = s.op != "rwkv6"
@@ -190,8 +196,8 @@ class _ScanFn(torch.autograd.Function):
             dld = s.empty(s.shape["ld"], torch.float32)
             du = None if delta else s.empty((s.H, s.dk), torch.float32)
             d0 = s.empty(s.state_shape(), torch.float32) if ctx.with_initial else None
-            ws = _bytes(dl_scan_backward_workspace_bytes(s.desc), s.device)
-            _check(_lib.dl_scan_backward(s.desc, saved.data_ptr(), _p(d_o), _p(d_final), dq.data_ptr(), dk.data_ptr(),
+            ws = _bytes(dl_scan_backward_workspace_bytes(desc), s.device)
+            _check(_lib.dl_scan_backward(desc, saved.data_ptr(), _p(d_o), _p(d_final), dq.data_ptr(), dk.data_ptr(),
                                          dv.data_ptr(), _p(dbeta), dld.data_ptr(), _p(du), _p(d0), ws.data_ptr(),
                                          _current(s.device)), "dl_scan_backward")
         return None, dq, dk, dv, dbeta, dld, du, d0
@@ -269,7 +275,7 @@ def _gated_norm(o, gate, weight, eps):
     y = torch.empty(gate.shape, dtype=gate.dtype, device=o.device)
     _check(_lib.dl_gated_norm(rows, H, d, DTYPES[o.dtype], DTYPES[gate.dtype], o.data_ptr(), g.data_ptr(), gs,
                               _p(weight), eps, y.data_ptr(), _current(o.device)), "dl_gated_norm")
-    return y, (o, g, weight), (rows, H, d, gs, eps)
+    return y, (o, g, weight), (rows, H, d, eps)
 
 
 class _GatedNormFn(torch.autograd.Function):
@@ -283,8 +289,9 @@ class _GatedNormFn(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         o, g, weight = ctx.saved_tensors
-        rows, H, d, gs, eps = ctx.args
+        rows, H, d, eps = ctx.args
         with _on(o.device, None):
+            g, gs = _rows(g, g.dim() - 2)  # its layout may be another than when it was saved
             dy = dy.contiguous()
             d_o = torch.empty_like(o)
             dg = torch.empty(dy.shape, dtype=g.dtype, device=o.device)
