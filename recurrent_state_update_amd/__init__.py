@@ -392,7 +392,8 @@ class DeltaLogState:
         int32) the offsets where they start and the last ends (or [n,T,H,..]
         tensors hold n of equal length; see `scan`).  ``slots``: the slot of
         each prompt, a sequence of distinct ints (default: prompt n is slot n
-        of all B).  The logs of these slots must be empty (a fresh state or
+        of all B; they are copied to the GPU, so not while a graph is
+        captured).  The logs of these slots must be empty (a fresh state or
         slot, or after a merge).  A new prompt starts from zero: zero
         ``base[slot]`` first.  Returns o in the input dtype, shaped as v."""
         from .sequence import _prefill

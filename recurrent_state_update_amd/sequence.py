@@ -6,7 +6,11 @@ Argument checks, output and workspace allocation and autograd nodes only: the
 arithmetic is in libdeltalog (dl_scan, dl_gated_norm, dl_residual_norm and
 their backward passes).  All three are differentiable once, asynchronous on
 the current stream (or ``stream``, on which their outputs are then allocated
-too) and capturable into HIP graphs.  Tensors may be on any one GPU.
+too; the inputs have to be ready there, as for torch's own operators) and
+capturable into HIP graphs.  Before a backward pass is captured, drop what
+still refers to the graph of an eager pass over the same leaves (its loss and
+outputs): torch ties a leaf's gradient to the stream of the oldest one.
+Tensors may be on any one GPU.
 """
 from __future__ import annotations
 
@@ -73,6 +77,13 @@ def _none(t, name, why):
         raise ValueError(f"{name}: {why} takes none")
 
 
+def _count(rows):
+    """The library counts rows in an int."""
+    if rows >= 1 << 31:
+        raise ValueError(f"{rows} rows: want fewer than 2^31")
+    return rows
+
+
 def _rows(t, lead):
     """t [*lead, H, d] as rows of H*d elements a fixed distance apart: the
     tensor (copied only if it is not laid out so) and that distance."""
@@ -130,9 +141,7 @@ class _Scan:
         self.N = cu_seqlens.numel() - 1 if cu_seqlens is not None else lead[0] if len(lead) == 2 else 1
         if self.N < 1:
             raise ValueError("want at least one sequence")
-        T = q.numel() // (H * dk) if q.numel() else 0
-        if T >= 1 << 31:
-            raise ValueError(f"{T} tokens: want fewer than 2^31")
+        T = _count(q.numel() // (H * dk) if q.numel() else 0)
         self.op, self.device, self.dtype, self.H, self.dk, self.dv = op, dev, q.dtype, H, dk, dv
         self.shape = dict(q=q.shape, v=v.shape, h=(*lead, H), ld=log_decay.shape)
         self.sizes = (opi, dti, T, self.N, H, dk, dv)
@@ -254,6 +263,8 @@ def _prefill_here(st, q, k, v, beta, log_decay, cu_seqlens, slots):
             raise ValueError(f"prefill: {s.N} prompts for {st.B} slots: name their slots")
         names = range(st.B)
     else:
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError("slots: their list cannot be copied to the GPU while a graph is captured")
         names = [int(i) for i in slots]
         if len(names) != s.N or len(set(names)) != s.N or not all(0 <= i < st.B for i in names):
             raise ValueError(f"slots: want {s.N} distinct slots below {st.B}, got {names}")
@@ -268,7 +279,7 @@ def _prefill_here(st, q, k, v, beta, log_decay, cu_seqlens, slots):
 def _gated_norm(o, gate, weight, eps):
     """y, and what its backward pass needs."""
     H, d = o.shape[-2:]
-    rows = o.numel() // (H * d)
+    rows = _count(o.numel() // (H * d))
     o = o.contiguous()
     g, gs = _rows(gate, gate.dim() - 2)
     weight = None if weight is None else weight.contiguous()
@@ -330,7 +341,7 @@ def gated_norm(o, gate, weight=None, eps: float = 1e-6, stream=None):
 def _residual_norm(x, y, scale, weight, eps, dtype):
     """x' (None without y) and h, and what their backward pass needs."""
     D = x.shape[-1]
-    rows = x.numel() // D
+    rows = _count(x.numel() // D)
     x, y, scale, weight = (None if t is None else t.contiguous() for t in (x, y, scale, weight))
     x_out = None if y is None else torch.empty_like(x)
     h = torch.empty(x.shape, dtype=dtype, device=x.device)

@@ -171,3 +171,14 @@ def test_norms_graph_replays_and_one_cotangent():
     parts = [torch.autograd.grad(t, [x, s], c, retain_graph=True) for t, c in ((xo, dx), (h, dh))]
     for i in range(2):
         assert far(parts[0][i] + parts[1][i], both[i].double().cpu()) <= 4 * FP32
+
+
+@needs_gpu
+def test_rows_past_an_int_are_refused():
+    import recurrent_state_update_amd as rsu
+    many = torch.zeros(1, device="cuda").expand(1 << 31, 1)
+    with pytest.raises(ValueError):
+        rsu.residual_norm(many)
+    heads = torch.zeros(16, device="cuda").expand(1 << 31, 1, 16)
+    with pytest.raises(ValueError):
+        rsu.gated_norm(heads, heads)

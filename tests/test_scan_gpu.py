@@ -346,6 +346,36 @@ def test_graph_replays(op):
 
 
 @needs_gpu
+def test_prefill_in_a_graph():
+    """Prompts continued by replays, against eager calls; a list of slots is
+    refused there, and the capture goes on."""
+    import recurrent_state_update_amd as rsu
+    x = {n: None if t is None else t.cuda() for n, t in inputs("kda", [70, 30], 2, 16, 32, torch.float32)[0].items()}
+    a = tuple(x[n] for n in ("q", "k", "v", "beta", "log_decay"))
+    cu = torch.tensor([0, 70, 100], dtype=torch.int32, device="cuda")
+    st, other = (rsu.DeltaLogState("kda", 2, 2, 16, 32, 4, dtype=torch.float32) for _ in range(2))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        st.prefill(*a, cu_seqlens=cu)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        with pytest.raises(ValueError):
+            st.prefill(*a, cu_seqlens=cu, slots=[1, 0])
+        o = st.prefill(*a, cu_seqlens=cu)
+    other.prefill(*a, cu_seqlens=cu)
+    for _ in range(3):
+        g.replay()
+        want = other.prefill(*a, cu_seqlens=cu)
+        torch.cuda.synchronize()
+        assert torch.equal(o, want) and torch.equal(st.base, other.base)
+    st.close()
+    other.close()
+
+
+@needs_gpu
 def test_another_stream_and_two_at_once():
     """Calls on streams of their own, at the same time, each with a workspace
     of its own: as alone."""
