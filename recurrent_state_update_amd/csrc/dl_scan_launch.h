@@ -58,13 +58,22 @@ inline dim3 carry_grid(const ScanArgs &a, int nc)
     return dim3((a.N * a.H + kXcds - 1) / kXcds * kXcds * (a.dv / (16 * nc)));
 }
 
-// Value tiles of 32 columns instead of 16 where they still give every CU a
-// workgroup: the operands are read half as often, but half as many workgroups
-// run.  Carry of 1024 tokens, d = 128, us (16 columns, 32): 256 workgroups of 32
-// GDN 60.5, 49.0, KDA 87.5, 63.3; 128 of them KDA 41.6, 54.9.
+// Value tiles of 32 columns instead of 16 where those of 16 are more than the
+// CUs: a workgroup is bound by its own chunk's chain, so while each has a CU to
+// itself more of them are faster, and beyond that the operands, read half as
+// often, count.  Forward, 1024 tokens, bf16, d = 128, us (16 columns, 32):
+//   heads            32 (256 tiles)   48 (384)        64 (512)
+//   GDN              32.8, 45.0       61.8, 47.1      64.8, 49.2
+//   KDA              46.3, 59.6       86.1, 62.5      91.0, 65.7
+//   RWKV6            29.6, 36.0                       45.3, 40.0
+// (backward, 36 heads: GDN 77.5, 56.8, KDA 106.6, 76.6; d = 64, 96 heads: GDN
+// 68.4, 60.4, RWKV6 43.3, 36.4).  Packed sequences count half: their lengths,
+// not known here, differ, and the long ones are left with the GPU (a KDA
+// training step over 1000, 17 and 911 tokens, 16 heads: 259 us, and 273 wide).
 inline bool wide_tiles(const ScanArgs &a)
 {
-    return a.dv % 32 == 0 && static_cast<long>(a.N) * a.H * (a.dv / 32) >= kCus;
+    const long tiles = static_cast<long>(a.N) * a.H * (a.dv / 16);
+    return a.dv % 32 == 0 && tiles >= (a.cu && a.N > 1 ? 2 * kCus : kCus + 1);
 }
 
 template <int OP, typename TIn, int DKP> hipError_t scan_forward_t(const ScanArgs &a, hipStream_t st)
