@@ -118,6 +118,18 @@ def test_lengths(op, lens):
 
 @needs_gpu
 @pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("dk,dv,n", [(16, 32, 20), (128, 32, 20), (64, 64, 10), (32, 128, 5)])
+def test_many_sequences_and_heads(op, dtype, dk, dv, n):
+    """More 16-column tiles than the GPU has CUs twice over (n 13 dv / 16 =
+    520): tiles of 32."""
+    lens = [65, 0, 1, 130, 64, 17, 3, 70, 0, 90][:n] * (n // 10 or 1)
+    x, cu, do, ds = inputs(op, lens, 13, dk, dv, dtype, seed=n, tail=3)
+    compare(op, x, cu, do, ds, dtype)
+
+
+@needs_gpu
+@pytest.mark.parametrize("op", OPS)
 @pytest.mark.parametrize("lens,tail", [([5, 70], 3), ([64], 64), ([0], 130), ([33, 31], 200)])
 def test_rows_behind_the_last_sequence(op, lens, tail):
     x, cu, do, ds = inputs(op, lens, 2, 16, 32, torch.float32, tail=tail)
