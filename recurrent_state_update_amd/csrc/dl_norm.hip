@@ -19,12 +19,14 @@ constexpr long kForwardBlocks = 2048; // eight per CU: every wave slot, several 
 template <typename T> __device__ __forceinline__ float to_f(T x) { return static_cast<float>(x); }
 
 // N consecutive elements from p, as floats (and back).  ALIGNED: p is aligned
-// to 16 bytes, or to the N elements where they are fewer.
-template <int N, bool ALIGNED, typename T> __device__ __forceinline__ void load(float (&x)[N], const T *p)
+// to 16 bytes, or to the N elements where they are fewer.  ONCE: loads that
+// leave the caches to others.
+template <int N, bool ALIGNED, bool ONCE = false, typename T>
+__device__ __forceinline__ void load(float (&x)[N], const T *p)
 {
     using V = T __attribute__((ext_vector_type(N)));
     if constexpr (ALIGNED && N > 1) {
-        const V v = *reinterpret_cast<const V *>(p);
+        const V v = ONCE ? __builtin_nontemporal_load(reinterpret_cast<const V *>(p)) : *reinterpret_cast<const V *>(p);
 #pragma unroll
         for (int i = 0; i < N; ++i)
             x[i] = to_f(v[i]);
@@ -289,7 +291,7 @@ template <int NT> __device__ __forceinline__ float row_sum(float x, float *part)
 }
 
 // A workgroup takes every gridDim.x-th row; loads run a row ahead.
-template <typename T, int NT, int VEC, int E>
+template <typename T, int NT, int VEC, int E, bool ONCE>
 __global__ __launch_bounds__(NT) void residual_norm_kernel(ResidualNormArgs a)
 {
     using L = Cols<NT, VEC, E>;
@@ -301,9 +303,9 @@ __global__ __launch_bounds__(NT) void residual_norm_kernel(ResidualNormArgs a)
             const int c = L::col(k);
             if (c >= a.D)
                 continue;
-            load<VEC, true>(xn[k], a.x + row * a.D + c);
+            load<VEC, true, ONCE>(xn[k], a.x + row * a.D + c);
             if (a.y)
-                load<VEC, true>(yn[k], static_cast<const T *>(a.y) + row * a.D + c);
+                load<VEC, true, ONCE>(yn[k], static_cast<const T *>(a.y) + row * a.D + c);
         }
     };
     constexpr bool AHEAD = E <= 2; // else the registers do not hold two rows
@@ -348,7 +350,7 @@ __global__ __launch_bounds__(NT) void residual_norm_kernel(ResidualNormArgs a)
 // With n = x' r: dn = dh w, d = dx' + r (dn - n mean(dn n)), dx = d,
 // dy = d s, ds = sum d y, dw = sum dh n.  A workgroup takes every
 // gridDim.x-th row and keeps its sums of ds and dw in registers.
-template <typename T, int NT, int VEC, int E>
+template <typename T, int NT, int VEC, int E, bool ONCE>
 __global__ __launch_bounds__(NT) void residual_norm_bwd_kernel(ResidualNormArgs a)
 {
     using L = Cols<NT, VEC, E>;
@@ -374,13 +376,13 @@ __global__ __launch_bounds__(NT) void residual_norm_bwd_kernel(ResidualNormArgs 
             if (c >= a.D)
                 continue;
             const long at = row * a.D + c;
-            load<VEC, true>(nx[k], a.x + at);
+            load<VEC, true, ONCE>(nx[k], a.x + at);
             if (a.d_h)
-                load<VEC, true>(nh[k], static_cast<const T *>(a.d_h) + at);
+                load<VEC, true, ONCE>(nh[k], static_cast<const T *>(a.d_h) + at);
             if (a.d_x_out)
-                load<VEC, true>(nd[k], a.d_x_out + at);
+                load<VEC, true, ONCE>(nd[k], a.d_x_out + at);
             if (scaled)
-                load<VEC, true>(ny[k], static_cast<const T *>(a.y) + at);
+                load<VEC, true, ONCE>(ny[k], static_cast<const T *>(a.y) + at);
         }
     };
     constexpr bool AHEAD = E <= 2;
@@ -457,21 +459,37 @@ __global__ __launch_bounds__(NT) void residual_norm_bwd_kernel(ResidualNormArgs 
     }
 }
 
-template <typename T, int NT, int VEC, int E>
-hipError_t residual_norm_t(bool backward, const ResidualNormArgs &a, hipStream_t st)
+template <typename T, int NT, int VEC, int E, bool ONCE>
+hipError_t residual_norm_k(bool backward, const ResidualNormArgs &a, hipStream_t st)
 {
     if (!backward) {
         if (a.rows == 0)
             return hipSuccess;
-        hipLaunchKernelGGL((residual_norm_kernel<T, NT, VEC, E>), dim3(a.rows < kForwardBlocks ? a.rows : kForwardBlocks),
+        hipLaunchKernelGGL((residual_norm_kernel<T, NT, VEC, E, ONCE>), dim3(a.rows < kForwardBlocks ? a.rows : kForwardBlocks),
                            dim3(NT), 0, st, a);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL((residual_norm_bwd_kernel<T, NT, VEC, E>), dim3(a.blocks), dim3(NT), 0, st, a);
+    hipLaunchKernelGGL((residual_norm_bwd_kernel<T, NT, VEC, E, ONCE>), dim3(a.blocks), dim3(NT), 0, st, a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && (a.d_scale || a.d_weight))
         e = column_sum(a.partial, a.blocks, a.D, a.d_scale ? a.d_scale : a.d_weight, a.d_scale ? a.d_weight : nullptr, st);
     return e;
+}
+
+// Loads past the caches where a pass moves more than the last-level cache's 256
+// MiB: nothing that it reads is still there, and it reads nothing twice.  us
+// (plain, past the caches) of D = 2048, bf16, with the data's last use just
+// before: 16384 rows forward 87.1, 81.7, backward 122.7, 107.0 (402 and 604 MB);
+// 4096 rows 21.6, 21.8 and 27.0, 31.5.  The gated norm gains nothing so.
+template <typename T, int NT, int VEC, int E>
+hipError_t residual_norm_t(bool backward, const ResidualNormArgs &a, hipStream_t st)
+{
+    const long per = backward ? 4 * (a.d_x_out ? 3 : 2) + sizeof(T) * ((a.d_h ? 1 : 0) + (a.d_y ? 1 : 0) + (a.scale && a.d_y ? 1 : 0))
+                              : 4 * (a.y ? 2 : 1) + sizeof(T) * (a.y ? 2 : 1);
+    if constexpr (VEC > 1)
+        if (a.rows * static_cast<long>(a.D) * per > (256L << 20))
+            return residual_norm_k<T, NT, VEC, E, true>(backward, a, st);
+    return residual_norm_k<T, NT, VEC, E, false>(backward, a, st);
 }
 
 template <typename T, int VEC> hipError_t residual_norm_e(bool backward, const ResidualNormArgs &a, hipStream_t st)

@@ -182,3 +182,28 @@ def test_rows_past_an_int_are_refused():
     heads = torch.zeros(16, device="cuda").expand(1 << 31, 1, 16)
     with pytest.raises(ValueError):
         rsu.gated_norm(heads, heads)
+
+
+@needs_gpu
+@pytest.mark.parametrize("t,n", [("f32", 18_000_000), ("bf16", 24_000_000)])
+@pytest.mark.parametrize("D", [128, 2000, 4096, 8000, 16384])
+def test_residual_norm_beyond_the_caches(t, n, D):
+    """More data than the last-level cache holds, against the same rows in two
+    halves that it does hold: rows bit for bit, the column sums (up to 190 terms
+    per thread, so some 4e-7 of rounding either way) within FP32 twice over."""
+    import recurrent_state_update_amd as rsu
+    rows = n // D // 2 * 2
+    g = torch.Generator("cuda").manual_seed(D)
+    x, y, dx, dh = (torch.randn(rows, D, generator=g, device="cuda") for _ in range(4))
+    y, dh = y.to(DT[t]), dh.to(DT[t])
+    s, w = (1 + 0.2 * torch.randn(D, generator=g, device="cuda") for _ in range(2))
+
+    def run(a, b):
+        leaves = [v.requires_grad_() for v in (x[a:b].clone(), y[a:b].clone(), s.clone(), w.clone())]
+        out = rsu.residual_norm(*leaves)
+        return [*out, *torch.autograd.grad(out, leaves, [dx[a:b], dh[a:b]])]
+    whole, one, two = run(0, rows), run(0, rows // 2), run(rows // 2, rows)
+    for a, b, c in list(zip(whole, one, two))[:4]:
+        assert torch.equal(a[:rows // 2], b) and torch.equal(a[rows // 2:], c)
+    for a, b, c in list(zip(whole, one, two))[4:]:
+        assert far(a, (b.double() + c.double()).cpu()) <= 2 * FP32
