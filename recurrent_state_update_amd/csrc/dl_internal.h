@@ -92,6 +92,25 @@ constexpr int scan_keys(int dk) { return dk < 32 ? 32 : dk; }
 // bf16 planes of the keys' operands: GDN's are the inputs themselves, exact in
 // one plane where they are bf16; the others carry fp32 decays.
 constexpr int scan_planes(int op, int dtype) { return op == GDN && dtype == BF16 ? 1 : 3; }
+// Chunks per segment where the forward carry cuts its sequences (dl_scan_carry.h),
+// 0 where it does not.  Uncut, a sequence's chunks are one chain of about 1.15 us
+// each on at most `tiles` CUs; cut, two chains of a segment's length and one
+// of a join per segment, and more work: worth it where a quarter of the CUs or
+// fewer have a tile and the chain is long.  Segments as many as give every CU
+// a tile, and no more than balance the joins.
+constexpr long kCus = 256;
+constexpr long scan_segment(long tokens, long seqs, long H, int dv)
+{
+    const long tiles = seqs * H * (dv / 16), chunks = tokens / kScanChunk / seqs;
+    if (tiles > kCus / 4 || chunks < 40)
+        return 0;
+    long n = 4;
+    while (n < kCus / tiles && (n + 1) * (n + 1) <= 2 * chunks)
+        ++n;
+    return (chunks + n - 1) / n;
+}
+constexpr long scan_segments(long tokens, long seqs, long segment) { return tokens / (kScanChunk * segment) + seqs + 1; }
+
 // Bytes of one chunk and head's operands: three chunk x keys matrices (bf16
 // where one plane holds them, else fp32), two chunk x chunk ones, twenty
 // 16 x 16 blocks, a decay per key, and three numbers per row.
@@ -115,6 +134,10 @@ struct ScanArgs {
     int nrows;         // state rows there are
     void *o;
     char *ops;     // [slots][H] operands
+    int seg;       // chunks per segment, or 0: sequences uncut
+    int segments;  // scan_segments(T, N, seg)
+    float *seg_s;  // [segments][H][dk][dv] a segment's start state (until joined, what its predecessor adds)
+    float *seg_m;  // [segments][H][dk][dk] its predecessor's transition
     float *save_s; // [slots][H][dk][dv] start state of every chunk, or NULL
     float *save_e; // [slots][H][chunk][dv] E (delta rule)
     // backward

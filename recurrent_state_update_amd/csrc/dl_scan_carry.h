@@ -181,10 +181,53 @@ template <typename TIn> struct ChunkRows {
 // -> 151 us.  The same for dS' and z, which the next kernel reads: no change).
 __device__ __forceinline__ void keep_for_backward(float *p, float x) { __builtin_nontemporal_store(x, p); }
 
+// Long sequences with few heads leave most CUs idle while their chunks pass one
+// by one.  There they are cut into segments of a.seg chunks (scan_segment):
+// over a segment the end state is linear in the start state, S' = M S + L.
+//   LOCAL  per segment but the last of its sequence, side by side: L, the carry
+//          from a zero state (from the initial one in the first segment), and
+//          M, the carry from each column of the identity with V = 0, as d_k more
+//          columns
+//   join   per sequence and head, over its segments: S = M S + L in fp32
+//   PLAIN (or SAVE), the carry itself, segment by segment from these states
+// One head of d = 128, GDN, bf16, us (uncut, cut): SEGMENT_FIGURES
+// A segment's slot is found as a chunk's: sequence n's first is
+// start / (64 a.seg) + n; a sequence without tokens has one too.
+struct Segment {
+    Seq s;
+    int n;
+    bool none, first, last;
+};
+__device__ __forceinline__ Segment segment_of(const ScanArgs &a, int slot)
+{
+    const int rows = C * a.seg;
+    int lo = 0, hi = a.N;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (seq_start(a, mid) / rows + mid <= slot)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    Segment g;
+    g.n = lo;
+    g.s = sequence(a, lo);
+    const int k = slot - (g.s.start / rows + lo), t0 = k * rows;
+    g.none = lo == a.N || k < 0 || (k > 0 && t0 >= g.s.len);
+    g.first = k == 0;
+    g.last = t0 + rows >= g.s.len;
+    g.s.start += t0;
+    g.s.len = g.s.len - t0 < rows ? g.s.len - t0 : rows;
+    g.s.base += k * a.seg;
+    return g;
+}
+
 // Forward.  SAVE: keeps every chunk's start state and E.
-template <int OP, typename TIn, int DKP, int NC, bool SAVE>
+enum CarryMode { PLAIN, SAVE, LOCAL };
+template <int OP, typename TIn, int DKP, int NC, CarryMode MODE>
 __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
 {
+    static_assert(MODE != LOCAL || NC == 1, "tiles of 16 keys");
     using P = Plan<OP, TIn>;
     using O = Ops<P::NPX, DKP>;
     using Own = Holder<DKP>;
@@ -200,13 +243,23 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, r4 = (lane >> 4) * 4, i0 = (w & 3) * 16 + r4;
     const int tiles = a.dv / (16 * NC);
-    const CarryWork wk = carry_work(tiles);
-    if (wk.group >= a.N * a.H)
+    const CarryWork wk = carry_work(MODE == LOCAL ? tiles + a.dk / 16 : tiles);
+    if (wk.group >= (a.seg ? a.segments : a.N) * a.H)
         return;
-    const int h = wk.group % a.H, n = wk.group / a.H;
-    const Seq sq = sequence(a, n);
-    const int v0 = wk.tile * 16 * NC + col;
-    const long first = static_cast<long>(h) * a.dv + wk.tile * 16 * NC; // of a row, this workgroup's
+    const int h = wk.group % a.H, item = wk.group / a.H; // a sequence or a segment
+    Segment sg = {{}, item, false, true, true};
+    if (MODE == LOCAL || a.seg)
+        sg = segment_of(a, item);
+    else
+        sg.s = sequence(a, item);
+    if (sg.none)
+        return;
+    const Seq sq = sg.s;
+    const bool unit = MODE == LOCAL && wk.tile >= tiles; // a transition's columns
+    if (MODE == LOCAL && (sg.last || (unit && sg.first)))
+        return;
+    const int tile = unit ? wk.tile - tiles : wk.tile, v0 = tile * 16 * NC + col;
+    const long first = static_cast<long>(h) * a.dv + (unit ? 0 : v0 - col); // of a row, this workgroup's
     const unsigned width = a.H * a.dv;
     const int chunks = (sq.len + C - 1) / C;
     const f32x4 zero = {0, 0, 0, 0};
@@ -243,7 +296,11 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
                 for (int t = 0; t < NC; ++t)
                     v[t][e] = rows.load((i0 + e) * static_cast<unsigned>(a.vs) + col + 16 * t);
         };
-        auto take_v = [&](int t) { return f32x4{from_in(v[t][0]), from_in(v[t][1]), from_in(v[t][2]), from_in(v[t][3])}; };
+        auto take_v = [&](int t) {
+            if (MODE == LOCAL && unit)
+                return zero;
+            return f32x4{from_in(v[t][0]), from_in(v[t][1]), from_in(v[t][2]), from_in(v[t][3])};
+        };
         load_v(0);
         keep_order();
         if constexpr (DELTA) {
@@ -294,7 +351,7 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
                     bp[c & 1][t].put(col, i0, b);
                 }
                 load_n(next);
-                if (SAVE) {
+                if (MODE == SAVE) {
                     const long sh = static_cast<long>(sq.base + c) * a.H + h;
 #pragma unroll
                     for (int t = 0; t < NC; ++t)
@@ -317,29 +374,34 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
             put_v(0);
             load_v(chunks > 1 ? 1 : 0);
             keep_order();
-            load_q(0);
-            keep_order();
-            load_b(0);
-            keep_order();
-            qf.ready();
-            bf.ready();
+            if (MODE != LOCAL) {
+                load_q(0);
+                keep_order();
+                load_b(0);
+                keep_order();
+                qf.ready();
+                bf.ready();
+            }
             for (int c = 0; c < chunks; ++c) {
                 __syncthreads(); // state and b are complete
                 const int next = c + 1 < chunks ? c + 1 : c, after = c + 2 < chunks ? c + 2 : next;
                 f32x4 o[NC];
+                if (MODE != LOCAL)
 #pragma unroll
-                for (int t = 0; t < NC; ++t) {
-                    bf16x8 f[KS][P::ORDER_O];
-                    get_all(f, sp[c & 1][t], lane);
-                    o[t] = with_b(product<P::ORDER_O>(qf.f, f, zero), bp[c & 1][t]);
-                }
+                    for (int t = 0; t < NC; ++t) {
+                        bf16x8 f[KS][P::ORDER_O];
+                        get_all(f, sp[c & 1][t], lane);
+                        o[t] = with_b(product<P::ORDER_O>(qf.f, f, zero), bp[c & 1][t]);
+                    }
                 put_v(c + 1); // (behind the last chunk: read by nobody)
                 load_v(after);
-                load_q(next);
-                load_b(next);
-                store_o(c, o);
-                qf.ready();
-                bf.ready();
+                if (MODE != LOCAL) {
+                    load_q(next);
+                    load_b(next);
+                    store_o(c, o);
+                    qf.ready();
+                    bf.ready();
+                }
             }
         }
         return;
@@ -347,8 +409,18 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
 
     const int wb = w - 4;
     const bool has = Own::has(wb);
-    const long row = state_row(a, n);
-    const long st0 = (row * a.H + h) * a.dk * a.dv + v0;
+    // where the state comes from and goes to (NULL: zero, nowhere)
+    const long row = state_row(a, sg.n), mat = static_cast<long>(a.dk) * a.dv, caller = (row * a.H + h) * mat + v0;
+    const long here = (static_cast<long>(item) * a.H + h) * mat + v0;
+    const float *from = sg.first ? (a.init && row >= 0 ? a.init + caller : nullptr) : nullptr;
+    float *to = a.fin && row >= 0 ? a.fin + caller : nullptr;
+    if (MODE == LOCAL)
+        to = unit ? a.seg_m + (static_cast<long>(item + 1) * a.H + h) * a.dk * a.dk + v0 : a.seg_s + here + a.H * mat;
+    else if (!sg.first || !sg.last) {
+        from = a.seg_s + here; // (the first's too: the caller's state may be overwritten by now)
+        to = sg.last ? to : nullptr;
+    }
+    const long ldw = unit ? a.dk : a.dv;
     f32x4 S[NC][RB], gam[RB];
     Operand<2, P::NPX> tf[RB];
     auto load_t = [&](int c) {
@@ -367,7 +439,7 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
             for (int r = 0; r < RB; ++r) {
                 const int d0 = Own::block(wb, r) * 16 + r4;
                 sp[DELTA ? 0 : c & 1][t].put(col, d0, S[t][r]);
-                if (SAVE && c < chunks) {
+                if (MODE == SAVE && c < chunks) {
                     const long sh = static_cast<long>(sq.base + c) * a.H + h;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -383,7 +455,10 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int d = Own::block(wb, r) * 16 + r4 + e;
-                S[t][r][e] = a.init && row >= 0 && has && d < a.dk ? a.init[st0 + static_cast<long>(d) * a.dv + 16 * t] : 0.f;
+                const bool in = has && d < a.dk;
+                S[t][r][e] = unit ? (in && d == v0 ? 1.f : 0.f) : from && in ? from[static_cast<long>(d) * a.dv + 16 * t] : 0.f;
+                if (MODE == LOCAL && sg.first && in)
+                    a.seg_s[here + static_cast<long>(d) * a.dv] = S[t][r][e];
             }
     put_state(0);
     if (chunks > 0) {
@@ -395,7 +470,7 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
             if (ROWS)
                 gi = ld4(ops(c).row(0) + i0);
         };
-        if (DELTA) {
+        if (DELTA && MODE != LOCAL) {
             load_q(0);
             load_gi(0);
             keep_order();
@@ -404,14 +479,16 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
         }
         load_t(0);
         keep_order();
-        if (DELTA) {
+        if (DELTA && MODE != LOCAL) {
             qf.ready();
             bf.ready();
         }
         for (int c = 0; c < chunks; ++c) {
             const int next = c + 1 < chunks ? c + 1 : c;
             __syncthreads();
-            if constexpr (DELTA) {
+            if constexpr (DELTA && MODE == LOCAL) {
+                __syncthreads();
+            } else if constexpr (DELTA) {
 #pragma unroll
                 for (int t = 0; t < NC; ++t) {
                     bf16x8 f[KS][P::ORDER_O];
@@ -452,14 +529,14 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
             load_t(next);
             put_state(c + 1);
         }
-        if constexpr (DELTA) {
+        if constexpr (DELTA && MODE != LOCAL) {
 #pragma unroll
             for (int t = 0; t < NC; ++t)
                 last[t] = with_b(last[t], bp[(chunks - 1) & 1][t]);
             store_o(chunks - 1, last);
         }
     }
-    if (a.fin && row >= 0 && has) {
+    if (to && has) {
 #pragma unroll
         for (int t = 0; t < NC; ++t)
 #pragma unroll
@@ -468,8 +545,54 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
                 for (int e = 0; e < 4; ++e) {
                     const int d = Own::block(wb, r) * 16 + r4 + e;
                     if (d < a.dk)
-                        a.fin[st0 + static_cast<long>(d) * a.dv + 16 * t] = S[t][r][e];
+                        to[d * ldw + 16 * t] = S[t][r][e];
                 }
+    }
+}
+
+// The start states of a sequence's segments, from the second of which on (the
+// first two come from LOCAL as they are): S = M S + L, 16 value columns per
+// workgroup, a wave per 16 keys.  Products on the fp32 matrix instruction; the
+// next transition is loaded a turn ahead.
+template <int DKP> __global__ __launch_bounds__(DKP * 4) void scan_join_kernel(ScanArgs a)
+{
+    __shared__ float x[2][16][DKP + 4]; // S by column
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, col = lane & 15, r4 = (lane >> 4) * 4;
+    const int tiles = a.dv / 16, tile = blockIdx.x % tiles, h = blockIdx.x / tiles % a.H, n = blockIdx.x / tiles / a.H;
+    const Seq sq = sequence(a, n);
+    const int rows = C * a.seg, slot = sq.start / rows + n, count = (sq.len + rows - 1) / rows;
+    if (count < 3)
+        return;
+    const bool in = w * 16 < a.dk;
+    const long mat = static_cast<long>(a.dk) * a.dv;
+    auto state = [&](int k) { return a.seg_s + (static_cast<long>(slot + k) * a.H + h) * mat + (w * 16 + r4) * a.dv + tile * 16 + col; };
+    f32x4 m[DKP / 16], l;
+    auto load = [&](int k) {
+        const float *p = a.seg_m + ((static_cast<long>(slot + k) * a.H + h) * a.dk + w * 16 + col) * a.dk + r4, *s = state(k);
+#pragma unroll
+        for (int j = 0; j < DKP / 16; ++j)
+            m[j] = in && j * 16 < a.dk ? *reinterpret_cast<const f32x4 *>(p + j * 16) : f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            l[e] = in ? s[e * a.dv] : 0.f;
+    };
+    load(1);
+    *reinterpret_cast<f32x4 *>(&x[1][col][w * 16 + r4]) = l;
+    load(2);
+    for (int k = 2; k < count; ++k) {
+        __syncthreads();
+        f32x4 y = l;
+#pragma unroll
+        for (int j = 0; j < DKP / 16; ++j)
+            y = mfma32x4(m[j], *reinterpret_cast<const f32x4 *>(&x[(k - 1) & 1][col][j * 16 + r4]), y);
+        load(k + 1 < count ? k + 1 : k);
+        *reinterpret_cast<f32x4 *>(&x[k & 1][col][w * 16 + r4]) = y;
+        if (in) {
+            float *s = state(k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                s[e * a.dv] = y[e];
+        }
     }
 }
 

@@ -26,8 +26,6 @@ template <auto *KERNEL> hipError_t set_lds(int bytes)
     return e;
 }
 
-constexpr long kCus = 256;
-
 inline bool at16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 template <int OP, typename TIn, int DKP, bool BWD> hipError_t launch_prep(const ScanArgs &a, hipStream_t st)
@@ -53,10 +51,7 @@ template <int OP, typename TIn, int DKP, bool BWD> hipError_t launch_prep(const 
 
 // Workgroups of a carry: a grid in which the value tiles of one sequence and
 // head run on one XCD (carry_work), which then reads their operands once.
-inline dim3 carry_grid(const ScanArgs &a, int nc)
-{
-    return dim3((a.N * a.H + kXcds - 1) / kXcds * kXcds * (a.dv / (16 * nc)));
-}
+inline dim3 carry_grid(long groups, int tiles) { return dim3((groups + kXcds - 1) / kXcds * kXcds * tiles); }
 
 // Value tiles of 32 columns instead of 16 where those of 16 are more than the
 // CUs: a workgroup is bound by its own chunk's chain, so while each has a CU to
@@ -80,10 +75,23 @@ template <int OP, typename TIn, int DKP> hipError_t scan_forward_t(const ScanArg
 {
     if (hipError_t e = launch_prep<OP, TIn, DKP, false>(a, st); e != hipSuccess)
         return e;
+    if (a.seg) {
+        const long groups = static_cast<long>(a.segments) * a.H;
+        hipLaunchKernelGGL((scan_carry_kernel<OP, TIn, DKP, 1, LOCAL>), carry_grid(groups, (a.dv + a.dk) / 16), dim3(512), 0,
+                           st, a);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess)
+            return e;
+        hipLaunchKernelGGL(scan_join_kernel<DKP>, dim3(a.N * a.H * (a.dv / 16)), dim3(DKP * 4), 0, st, a);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess)
+            return e;
+        auto *carry = a.save_s ? scan_carry_kernel<OP, TIn, DKP, 1, SAVE> : scan_carry_kernel<OP, TIn, DKP, 1, PLAIN>;
+        hipLaunchKernelGGL(carry, carry_grid(groups, a.dv / 16), dim3(512), 0, st, a);
+        return hipGetLastError();
+    }
     const bool wide = wide_tiles(a);
-    auto *carry = a.save_s ? (wide ? scan_carry_kernel<OP, TIn, DKP, 2, true> : scan_carry_kernel<OP, TIn, DKP, 1, true>)
-                           : (wide ? scan_carry_kernel<OP, TIn, DKP, 2, false> : scan_carry_kernel<OP, TIn, DKP, 1, false>);
-    hipLaunchKernelGGL(carry, carry_grid(a, wide ? 2 : 1), dim3(512), 0, st, a);
+    auto *carry = a.save_s ? (wide ? scan_carry_kernel<OP, TIn, DKP, 2, SAVE> : scan_carry_kernel<OP, TIn, DKP, 1, SAVE>)
+                           : (wide ? scan_carry_kernel<OP, TIn, DKP, 2, PLAIN> : scan_carry_kernel<OP, TIn, DKP, 1, PLAIN>);
+    hipLaunchKernelGGL(carry, carry_grid(static_cast<long>(a.N) * a.H, a.dv / (wide ? 32 : 16)), dim3(512), 0, st, a);
     return hipGetLastError();
 }
 
@@ -93,7 +101,7 @@ template <int OP, typename TIn, int DKP> hipError_t scan_backward_t(const ScanAr
         return e;
     const bool wide = wide_tiles(a);
     auto *carry = wide ? scan_carry_bwd_kernel<OP, TIn, DKP, 2> : scan_carry_bwd_kernel<OP, TIn, DKP, 1>;
-    hipLaunchKernelGGL(carry, carry_grid(a, wide ? 2 : 1), dim3(512), 0, st, a);
+    hipLaunchKernelGGL(carry, carry_grid(static_cast<long>(a.N) * a.H, a.dv / (wide ? 32 : 16)), dim3(512), 0, st, a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess)
         return e;
     const bool vec = at16(a.q) && at16(a.k) && at16(a.v) && at16(a.d_o) && a.qs % 8 == 0 && a.ks % 8 == 0 &&

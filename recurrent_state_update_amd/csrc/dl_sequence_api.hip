@@ -60,15 +60,22 @@ dl_status check_sizes(const dl_scan_desc *d)
 
 struct ScanSizes {
     size_t slot_heads, ops, states, rows_dv, db, du;
+    long segment, segments; // of the forward carry; 0: uncut
+    size_t seg_s, seg_m;
     explicit ScanSizes(const dl_scan_desc *d)
         : slot_heads(static_cast<size_t>(dl::scan_slots(d->tokens, d->seqs)) * d->H),
           ops(up256(slot_heads * dl::scan_op_bytes(dl::scan_planes(d->op, d->in_dtype), dl::scan_keys(d->d_k)))),
           states(up256(slot_heads * d->d_k * d->d_v * 4)),
           rows_dv(d->op == DL_OP_RWKV6 ? 0 : up256(slot_heads * dl::kScanChunk * d->d_v * 4)),
           db(d->op == DL_OP_RWKV6 ? 0 : up256(slot_heads * (d->d_v / 16) * dl::kScanChunk * 4)),
-          du(d->op == DL_OP_RWKV6 ? up256(slot_heads * d->d_k * 4) : 0)
+          du(d->op == DL_OP_RWKV6 ? up256(slot_heads * d->d_k * 4) : 0),
+          segment(dl::scan_segment(d->tokens, d->seqs, d->H, d->d_v)),
+          segments(segment ? dl::scan_segments(d->tokens, d->seqs, segment) : 0),
+          seg_s(up256(static_cast<size_t>(segments) * d->H * d->d_k * d->d_v * 4)),
+          seg_m(up256(static_cast<size_t>(segments) * d->H * d->d_k * d->d_k * 4))
     {
     }
+    size_t forward() const { return ops + seg_s + seg_m; }
     size_t saved() const { return states + rows_dv; }
     size_t backward() const { return ops + states + rows_dv + db + du; }
 };
@@ -184,7 +191,7 @@ extern "C" {
 
 size_t dl_scan_workspace_bytes(const dl_scan_desc *d)
 {
-    return check_sizes(d) == DL_OK ? ScanSizes(d).ops : 0;
+    return check_sizes(d) == DL_OK ? ScanSizes(d).forward() : 0;
 }
 
 size_t dl_scan_saved_bytes(const dl_scan_desc *d)
@@ -216,7 +223,7 @@ dl_status dl_scan(const dl_scan_desc *d, const float *initial, float *final_stat
     const Span w[4] = {{o, static_cast<size_t>(d->tokens) * d->H * d->d_v * elem(d->in_dtype)},
                        {final_state, states},
                        {saved, z.saved()},
-                       {workspace, z.ops}};
+                       {workspace, z.forward()}};
     const Span r[9] = {in[0], in[1], in[2], in[3], in[4], in[5], in[6],
                        {initial == final_state ? nullptr : initial, states},
                        {state_rows, static_cast<size_t>(d->seqs) * 4}};
@@ -228,6 +235,10 @@ dl_status dl_scan(const dl_scan_desc *d, const float *initial, float *final_stat
     a.nrows = n_state_rows;
     a.o = o;
     a.ops = static_cast<char *>(workspace);
+    a.seg = static_cast<int>(z.segment);
+    a.segments = static_cast<int>(z.segments);
+    a.seg_s = reinterpret_cast<float *>(a.ops + z.ops);
+    a.seg_m = reinterpret_cast<float *>(a.ops + z.ops + z.seg_s);
     if (saved) {
         a.save_s = static_cast<float *>(saved);
         a.save_e = reinterpret_cast<float *>(static_cast<char *>(saved) + z.states);

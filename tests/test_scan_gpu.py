@@ -130,6 +130,41 @@ def test_many_sequences_and_heads(op, dtype, dk, dv, n):
 
 @needs_gpu
 @pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("lens,H,dk,dv,tail,weak", [
+    ([2700], 1, 128, 128, 0, True),  # segments of 5 chunks, the last one of 3 with 12 tokens at its end
+    ([2700], 3, 16, 32, 0, False),
+    ([2562, 0, 130, 5100, 1], 2, 64, 16, 5200, True),  # several, one and no segment; rows behind
+], ids=["one", "heads", "packed"])
+def test_long_sequences_with_few_heads(op, dtype, lens, H, dk, dv, tail, weak):
+    """Sequences cut into segments and joined; weakly decaying, the state of
+    the first tokens reaches the last."""
+    x, cu, do, ds = inputs(op, lens, H, dk, dv, dtype, seed=H, tail=tail, decay=(lambda ld, g: ld * 0.004) if weak else None)
+    if weak and op == "rwkv6":
+        x["v"] = x["v"] / 8  # its state is a plain sum
+    compare(op, x, cu, do, ds, dtype)
+
+
+@needs_gpu
+@pytest.mark.parametrize("op", OPS)
+def test_long_prompt_in_place(op):
+    """The end state of a cut sequence over the initial one (prefill), against
+    tensors of their own, twice on."""
+    import recurrent_state_update_amd as rsu
+    x = {n: None if t is None else t.cuda() for n, t in inputs(op, [3000, 2700], 2, 32, 32, torch.bfloat16, seed=9)[0].items()}
+    cu = torch.tensor([0, 3000, 5700], dtype=torch.int32, device="cuda")
+    a = tuple(x[n] for n in ("q", "k", "v", "beta", "log_decay"))
+    st = rsu.DeltaLogState(op, 2, 2, 32, 32, 4, dtype=torch.bfloat16, base=x["initial_state"].clone(), u=x["u"])
+    s = x["initial_state"]
+    for _ in range(3):
+        o = st.prefill(*a, cu_seqlens=cu)
+        want, s = rsu.scan(op, *a, u=x["u"], initial_state=s, cu_seqlens=cu)
+        assert torch.equal(o, want) and torch.equal(st.base, s)
+    st.close()
+
+
+@needs_gpu
+@pytest.mark.parametrize("op", OPS)
 @pytest.mark.parametrize("lens,tail", [([5, 70], 3), ([64], 64), ([0], 130), ([33, 31], 200)])
 def test_rows_behind_the_last_sequence(op, lens, tail):
     x, cu, do, ds = inputs(op, lens, 2, 16, 32, torch.float32, tail=tail)
