@@ -93,16 +93,19 @@ constexpr int scan_keys(int dk) { return dk < 32 ? 32 : dk; }
 // one plane where they are bf16; the others carry fp32 decays.
 constexpr int scan_planes(int op, int dtype) { return op == GDN && dtype == BF16 ? 1 : 3; }
 // Chunks per segment where the forward carry cuts its sequences (dl_scan_carry.h),
-// 0 where it does not.  Uncut, a sequence's chunks are one chain of about 1.15 us
-// each on at most `tiles` CUs; cut, two chains of a segment's length and one
-// of a join per segment, and more work: worth it where a quarter of the CUs or
-// fewer have a tile and the chain is long.  Segments as many as give every CU
-// a tile, and no more than balance the joins.
+// 0 where it does not.  Uncut, a sequence's chunks are one chain, of 1.6 us each
+// (GDN, d = 128); cut, it is two chains of a segment's length and a join per
+// segment, and about three times the work: worth it where a quarter of the CUs or
+// fewer have a tile and the chain is long (1600 tokens, 1 head GDN 58 -> 49 us, 4
+// heads 59 -> 57, 8 heads 58 -> 60; RWKV6 54 -> 49, 54 -> 56, 55 -> 56; 2000
+// tokens, d = 64, 8 heads 49 -> 44 and 36 -> 35).  As many segments as give every
+// CU a tile, and no more than balance the joins (twice as many: 8192 tokens, 1
+// head 90 -> 105 us).
 constexpr long kCus = 256;
 constexpr long scan_segment(long tokens, long seqs, long H, int dv)
 {
     const long tiles = seqs * H * (dv / 16), chunks = tokens / kScanChunk / seqs;
-    if (tiles > kCus / 4 || chunks < 40)
+    if (tiles > kCus / 4 || chunks < 30)
         return 0;
     long n = 4;
     while (n < kCus / tiles && (n + 1) * (n + 1) <= 2 * chunks)

@@ -77,7 +77,12 @@ struct ScanSizes {
     }
     size_t forward() const { return ops + seg_s + seg_m; }
     size_t saved() const { return states + rows_dv; }
-    size_t backward() const { return ops + states + rows_dv + db + du; }
+    // (a buffer for it serves the forward pass too, with room to align it)
+    size_t backward() const
+    {
+        const size_t own = ops + states + rows_dv + db + du, both = forward() + 256;
+        return own > both ? own : both;
+    }
 };
 
 // Checks what both directions read, and fills their part of `a`.
