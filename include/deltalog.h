@@ -299,9 +299,8 @@ typedef struct {
 
 /* Device bytes of dl_scan's workspace, of the `saved` buffer that carries the
  * forward pass's intermediate results to the backward pass, and of
- * dl_scan_backward's workspace (each 256-byte aligned; the last is never less
- * than the first, and may be the same buffer).  Only the sizes, op and in_dtype
- * of `d` are read.  0 if they are invalid. */
+ * dl_scan_backward's workspace (each 256-byte aligned).  Only the sizes, op
+ * and in_dtype of `d` are read.  0 if they are invalid. */
 size_t dl_scan_workspace_bytes(const dl_scan_desc *d);
 size_t dl_scan_saved_bytes(const dl_scan_desc *d);
 size_t dl_scan_backward_workspace_bytes(const dl_scan_desc *d);

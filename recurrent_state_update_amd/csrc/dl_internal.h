@@ -92,8 +92,8 @@ constexpr int scan_keys(int dk) { return dk < 32 ? 32 : dk; }
 // bf16 planes of the keys' operands: GDN's are the inputs themselves, exact in
 // one plane where they are bf16; the others carry fp32 decays.
 constexpr int scan_planes(int op, int dtype) { return op == GDN && dtype == BF16 ? 1 : 3; }
-// Chunks per segment where the forward carry cuts its sequences (dl_scan_carry.h),
-// 0 where it does not.  Uncut, a sequence's chunks are one chain, of 1.6 us each
+// Chunks per segment where the carries cut their sequences (dl_scan_carry.h),
+// 0 where they do not.  Uncut, a sequence's chunks are one chain, of 1.6 us each
 // (GDN, d = 128); cut, it is two chains of a segment's length and a join per
 // segment, and about three times the work: worth it where a quarter of the CUs or
 // fewer have a tile and the chain is long (1600 tokens, 1 head GDN 58 -> 49 us, 4
@@ -139,8 +139,10 @@ struct ScanArgs {
     char *ops;     // [slots][H] operands
     int seg;       // chunks per segment, or 0: sequences uncut
     int segments;  // scan_segments(T, N, seg)
-    float *seg_s;  // [segments][H][dk][dv] a segment's start state (until joined, what its predecessor adds)
-    float *seg_m;  // [segments][H][dk][dk] its predecessor's transition
+    // [segments][H][dk][dv] a segment's start state (until joined, what its
+    // predecessor adds) and [segments][H][dk][dk] its predecessor's transition;
+    // backward: its end state's gradient, and what its successor adds and does
+    float *seg_s, *seg_m;
     float *save_s; // [slots][H][dk][dv] start state of every chunk, or NULL
     float *save_e; // [slots][H][chunk][dv] E (delta rule)
     // backward

@@ -190,11 +190,16 @@ __device__ __forceinline__ void keep_for_backward(float *p, float x) { __builtin
 //          columns
 //   join   per sequence and head, over its segments: S = M S + L in fp32
 //   PLAIN (or SAVE), the carry itself, segment by segment from these states
+// and the same backward, for the gradients of the end states.
 // A whole forward scan, d = 128, bf16, us (uncut, cut):
 //   tokens, heads   2600, 1     2600, 8     8192, 1     8192, 8     32768, 4
 //   GDN             84.5, 59.8  86.7, 82.7  221, 90     235, 160    876, 310
 //   KDA             116, 72.4   123, 116    306, 110    342, 253    1546, 543
 //   RWKV6           77.8, 56.5  83.2, 72.0  203, 87     228, 148    1081, 324
+// forward and backward (below 200 the host is the longer):
+//   GDN             224, 194    248, 229    564, 223    695, 534    2413, 1025
+//   KDA             295, 202    353, 342    749, 271    1025, 851   3706, 1712
+//   RWKV6           204, 195    249, 230    500, 244    733, 545    2640, 1189
 // A segment's slot is found as a chunk's: sequence n's first is
 // start / (64 a.seg) + n; a sequence without tokens has one too.
 struct Segment {
@@ -554,11 +559,12 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
     }
 }
 
-// The start states of a sequence's segments, from the second of which on (the
-// first two come from LOCAL as they are): S = M S + L, 16 value columns per
-// workgroup, a wave per 16 keys.  Products on the fp32 matrix instruction; the
-// next transition is loaded a turn ahead.
-template <int DKP> __global__ __launch_bounds__(DKP * 4) void scan_join_kernel(ScanArgs a)
+// The start states of a sequence's segments from the third on (the first two come
+// from LOCAL as they are): S = M S + L; BACK: the gradients of their end
+// states, from the third last on.  16 value columns per workgroup, a wave per
+// 16 keys.  Products on the fp32 matrix instruction; the next transition is
+// loaded a turn ahead.
+template <int DKP, bool BACK> __global__ __launch_bounds__(DKP * 4) void scan_join_kernel(ScanArgs a)
 {
     __shared__ float x[2][16][DKP + 4]; // S by column
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, col = lane & 15, r4 = (lane >> 4) * 4;
@@ -569,10 +575,11 @@ template <int DKP> __global__ __launch_bounds__(DKP * 4) void scan_join_kernel(S
         return;
     const bool in = w * 16 < a.dk;
     const long mat = static_cast<long>(a.dk) * a.dv;
-    auto state = [&](int k) { return a.seg_s + (static_cast<long>(slot + k) * a.H + h) * mat + (w * 16 + r4) * a.dv + tile * 16 + col; };
+    auto at = [&](int k) { return static_cast<long>(slot + (BACK ? count - 1 - k : k)) * a.H + h; };
+    auto state = [&](int k) { return a.seg_s + at(k) * mat + (w * 16 + r4) * a.dv + tile * 16 + col; };
     f32x4 m[DKP / 16], l;
     auto load = [&](int k) {
-        const float *p = a.seg_m + ((static_cast<long>(slot + k) * a.H + h) * a.dk + w * 16 + col) * a.dk + r4, *s = state(k);
+        const float *p = a.seg_m + (at(k) * a.dk + w * 16 + col) * a.dk + r4, *s = state(k);
 #pragma unroll
         for (int j = 0; j < DKP / 16; ++j)
             m[j] = in && j * 16 < a.dk ? *reinterpret_cast<const f32x4 *>(p + j * 16) : f32x4{0, 0, 0, 0};
@@ -604,9 +611,10 @@ template <int DKP> __global__ __launch_bounds__(DKP * 4) void scan_join_kernel(S
 // chunk's dS' and z (delta rule), dv, and per 16 NC value columns the partial
 // sums of db . E (of dbeta; grads adds the rest); at the end the initial
 // state's gradient.
-template <int OP, typename TIn, int DKP, int NC>
+template <int OP, typename TIn, int DKP, int NC, CarryMode MODE>
 __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
 {
+    static_assert(MODE == PLAIN || (MODE == LOCAL && NC == 1), "tiles of 16 keys");
     using P = Plan<OP, TIn>;
     using O = Ops<P::NPX, DKP>;
     using Own = Holder<DKP>;
@@ -621,20 +629,30 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, r4 = (lane >> 4) * 4, i0 = (w & 3) * 16 + r4;
     const int tiles = a.dv / (16 * NC);
-    const CarryWork wk = carry_work(tiles);
-    if (wk.group >= a.N * a.H)
+    const CarryWork wk = carry_work(MODE == LOCAL ? tiles + a.dk / 16 : tiles);
+    if (wk.group >= (a.seg ? a.segments : a.N) * a.H)
         return;
-    const int h = wk.group % a.H, n = wk.group / a.H;
-    const Seq sq = sequence(a, n);
-    const int v0 = wk.tile * 16 * NC + col;
-    const long first = static_cast<long>(h) * a.dv + wk.tile * 16 * NC; // of a row, this workgroup's
+    const int h = wk.group % a.H, item = wk.group / a.H; // a sequence or a segment
+    Segment sg = {{}, item, false, true, true};
+    if (MODE == LOCAL || a.seg)
+        sg = segment_of(a, item);
+    else
+        sg.s = sequence(a, item);
+    if (sg.none)
+        return;
+    const Seq sq = sg.s;
+    const bool unit = MODE == LOCAL && wk.tile >= tiles; // a transition's columns
+    if (MODE == LOCAL && (sg.first || (unit && sg.last)))
+        return;
+    const int tile = unit ? wk.tile - tiles : wk.tile, v0 = tile * 16 * NC + col;
+    const long first = static_cast<long>(h) * a.dv + (unit ? 0 : v0 - col); // of a row, this workgroup's
     const unsigned width = a.H * a.dv;
     const int chunks = (sq.len + C - 1) / C;
     const f32x4 zero = {0, 0, 0, 0};
     auto ops = [&](int c) { return O(a, static_cast<long>(sq.base + c) * a.H + h); };
 
     if (w < 4) {
-        if (chunks == 0)
+        if (chunks == 0 || (MODE == LOCAL && !DELTA))
             return; // barriers count the waves that are left
         Operand<KS, P::NPX> kf;
         Operand<2, 3> bt, nt;
@@ -656,7 +674,7 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
                 gi = ld4(ops(c).row(0) + i0);
         };
         auto load_e = [&](int c) {
-            if (!DELTA)
+            if (!DELTA || MODE == LOCAL)
                 return;
 #pragma unroll
             for (int t = 0; t < NC; ++t)
@@ -670,7 +688,7 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
         keep_order();
         load_e(chunks - 1);
         keep_order();
-        auto ready = [&] {
+        auto ready = [&]() __attribute__((always_inline)) { // (the operands live in registers)
             kf.ready();
             bt.ready();
             if (DELTA)
@@ -705,33 +723,35 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
                 load_n(next);
                 __syncthreads(); // z is complete
             }
-            f32x4 p = zero;
-            if constexpr (DELTA) {
+            if constexpr (MODE != LOCAL) {
+                f32x4 p = zero;
+                if constexpr (DELTA) {
+#pragma unroll
+                    for (int t = 0; t < NC; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            p[e] = fmaf(db[t][e], E[t][e], p[e]);
+                    load_e(next);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        p[e] = add_row_ror<1>(p[e]);
+                        p[e] = add_row_ror<2>(p[e]);
+                        p[e] = add_row_ror<4>(p[e]);
+                        p[e] = add_row_ror<8>(p[e]);
+                    }
+                }
+                const ChunkRows<TIn> rows(dvp, width, c, sq.len, 16 * NC);
 #pragma unroll
                 for (int t = 0; t < NC; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        p[e] = fmaf(db[t][e], E[t][e], p[e]);
-                load_e(next);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    p[e] = add_row_ror<1>(p[e]);
-                    p[e] = add_row_ror<2>(p[e]);
-                    p[e] = add_row_ror<4>(p[e]);
-                    p[e] = add_row_ror<8>(p[e]);
-                }
+                    for (int e = 0; e < 4; ++e) {
+                        rows.store((i0 + e) * width + col + 16 * t, x[t][e]);
+                        if (DELTA)
+                            a.w_z[(sh * C + i0 + e) * a.dv + v0 + 16 * t] = x[t][e];
+                    }
+                if (DELTA && col == 0)
+                    *reinterpret_cast<f32x4 *>(&a.w_db[(sh * tiles + wk.tile) * C + i0]) = p;
             }
-            const ChunkRows<TIn> rows(dvp, width, c, sq.len, 16 * NC);
-#pragma unroll
-            for (int t = 0; t < NC; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    rows.store((i0 + e) * width + col + 16 * t, x[t][e]);
-                    if (DELTA)
-                        a.w_z[(sh * C + i0 + e) * a.dv + v0 + 16 * t] = x[t][e];
-                }
-            if (DELTA && col == 0)
-                *reinterpret_cast<f32x4 *>(&a.w_db[(sh * tiles + wk.tile) * C + i0]) = p;
             ready();
         }
         return;
@@ -739,13 +759,21 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
 
     const int wb = w - 4;
     const bool has = Own::has(wb);
-    const long st0 = (static_cast<long>(n) * a.H + h) * a.dk * a.dv + v0;
+    // where the end state's gradient comes from and the start state's goes to
+    const long mat = static_cast<long>(a.dk) * a.dv, caller = (static_cast<long>(sg.n) * a.H + h) * mat + v0;
+    const long here = (static_cast<long>(item) * a.H + h) * mat + v0;
+    const float *from = sg.last ? (a.dfin ? a.dfin + caller : nullptr) : MODE == LOCAL ? nullptr : a.seg_s + here;
+    float *to = sg.first && a.dinit ? a.dinit + caller : nullptr;
+    if (MODE == LOCAL)
+        to = unit ? a.seg_m + (static_cast<long>(item - 1) * a.H + h) * a.dk * a.dk + v0 : a.seg_s + here - a.H * mat;
+    const long ldw = unit ? a.dk : a.dv;
+    const bool with_g = a.d_o && !unit;
     f32x4 S[NC][RB], gam[RB], gi; // S: dS'
     Operand<2, P::NPX> qt[RB], kt[RB];
     TIn g[NC][4];
     const TIn *gbase = static_cast<const TIn *>(a.d_o) + static_cast<long>(sq.start) * width + first;
     auto load_g = [&](int c) {
-        if (a.d_o) {
+        if (with_g) {
             const ChunkRows<TIn> rows(gbase, width, c, sq.len, 16 * NC);
 #pragma unroll
             for (int t = 0; t < NC; ++t)
@@ -759,7 +787,7 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
     auto put_g = [&](int c) {
 #pragma unroll
         for (int t = 0; t < NC; ++t) {
-            const f32x4 x = a.d_o ? f32x4{from_in(g[t][0]), from_in(g[t][1]), from_in(g[t][2]), from_in(g[t][3])} : zero;
+            const f32x4 x = with_g ? f32x4{from_in(g[t][0]), from_in(g[t][1]), from_in(g[t][2]), from_in(g[t][3])} : zero;
             gp[c & 1][t].put(col, i0, x);
             if (ROWS)
                 gg[c & 1][t].put(col, i0, x * gi);
@@ -788,7 +816,7 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
             for (int r = 0; r < RB; ++r) {
                 const int d0 = Own::block(wb, r) * 16 + r4;
                 sp[DELTA ? 0 : c & 1][t].put(col, d0, S[t][r]);
-                if (c >= 0) {
+                if (MODE != LOCAL && c >= 0) {
                     const long sh = static_cast<long>(sq.base + c) * a.H + h;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -804,7 +832,8 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int d = Own::block(wb, r) * 16 + r4 + e;
-                S[t][r][e] = a.dfin && has && d < a.dk ? a.dfin[st0 + static_cast<long>(d) * a.dv + 16 * t] : 0.f;
+                const bool in = has && d < a.dk;
+                S[t][r][e] = unit ? (in && d == v0 ? 1.f : 0.f) : from && in ? from[static_cast<long>(d) * a.dv + 16 * t] : 0.f;
             }
     put_state(chunks - 1);
     if (chunks > 0) {
@@ -858,7 +887,7 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
             put_state(c - 1);
         }
     }
-    if (a.dinit && has) {
+    if (to && has) {
 #pragma unroll
         for (int t = 0; t < NC; ++t)
 #pragma unroll
@@ -867,7 +896,7 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
                 for (int e = 0; e < 4; ++e) {
                     const int d = Own::block(wb, r) * 16 + r4 + e;
                     if (d < a.dk)
-                        a.dinit[st0 + static_cast<long>(d) * a.dv + 16 * t] = S[t][r][e];
+                        to[d * ldw + 16 * t] = S[t][r][e];
                 }
     }
 }

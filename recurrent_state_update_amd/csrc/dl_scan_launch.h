@@ -81,7 +81,7 @@ template <int OP, typename TIn, int DKP> hipError_t scan_forward_t(const ScanArg
                            st, a);
         if (hipError_t e = hipGetLastError(); e != hipSuccess)
             return e;
-        hipLaunchKernelGGL(scan_join_kernel<DKP>, dim3(a.N * a.H * (a.dv / 16)), dim3(DKP * 4), 0, st, a);
+        hipLaunchKernelGGL((scan_join_kernel<DKP, false>), dim3(a.N * a.H * (a.dv / 16)), dim3(DKP * 4), 0, st, a);
         if (hipError_t e = hipGetLastError(); e != hipSuccess)
             return e;
         auto *carry = a.save_s ? scan_carry_kernel<OP, TIn, DKP, 1, SAVE> : scan_carry_kernel<OP, TIn, DKP, 1, PLAIN>;
@@ -99,9 +99,19 @@ template <int OP, typename TIn, int DKP> hipError_t scan_backward_t(const ScanAr
 {
     if (hipError_t e = launch_prep<OP, TIn, DKP, true>(a, st); e != hipSuccess)
         return e;
-    const bool wide = wide_tiles(a);
-    auto *carry = wide ? scan_carry_bwd_kernel<OP, TIn, DKP, 2> : scan_carry_bwd_kernel<OP, TIn, DKP, 1>;
-    hipLaunchKernelGGL(carry, carry_grid(static_cast<long>(a.N) * a.H, a.dv / (wide ? 32 : 16)), dim3(512), 0, st, a);
+    const long groups = static_cast<long>(a.seg ? a.segments : a.N) * a.H;
+    if (a.seg) {
+        hipLaunchKernelGGL((scan_carry_bwd_kernel<OP, TIn, DKP, 1, LOCAL>), carry_grid(groups, (a.dv + a.dk) / 16), dim3(512),
+                           0, st, a);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess)
+            return e;
+        hipLaunchKernelGGL((scan_join_kernel<DKP, true>), dim3(a.N * a.H * (a.dv / 16)), dim3(DKP * 4), 0, st, a);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess)
+            return e;
+    }
+    const bool wide = !a.seg && wide_tiles(a);
+    auto *carry = wide ? scan_carry_bwd_kernel<OP, TIn, DKP, 2, PLAIN> : scan_carry_bwd_kernel<OP, TIn, DKP, 1, PLAIN>;
+    hipLaunchKernelGGL(carry, carry_grid(groups, a.dv / (wide ? 32 : 16)), dim3(512), 0, st, a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess)
         return e;
     const bool vec = at16(a.q) && at16(a.k) && at16(a.v) && at16(a.d_o) && a.qs % 8 == 0 && a.ks % 8 == 0 &&

@@ -60,7 +60,7 @@ dl_status check_sizes(const dl_scan_desc *d)
 
 struct ScanSizes {
     size_t slot_heads, ops, states, rows_dv, db, du;
-    long segment, segments; // of the forward carry; 0: uncut
+    long segment, segments; // of the carries; 0: uncut
     size_t seg_s, seg_m;
     explicit ScanSizes(const dl_scan_desc *d)
         : slot_heads(static_cast<size_t>(dl::scan_slots(d->tokens, d->seqs)) * d->H),
@@ -77,12 +77,17 @@ struct ScanSizes {
     }
     size_t forward() const { return ops + seg_s + seg_m; }
     size_t saved() const { return states + rows_dv; }
-    // (a buffer for it serves the forward pass too, with room to align it)
-    size_t backward() const
+    // What both passes keep at the workspace's front; returns its end.
+    char *place(dl::ScanArgs &a, void *workspace) const
     {
-        const size_t own = ops + states + rows_dv + db + du, both = forward() + 256;
-        return own > both ? own : both;
+        a.ops = static_cast<char *>(workspace);
+        a.seg = static_cast<int>(segment);
+        a.segments = static_cast<int>(segments);
+        a.seg_s = reinterpret_cast<float *>(a.ops + ops);
+        a.seg_m = reinterpret_cast<float *>(a.ops + ops + seg_s);
+        return a.ops + forward();
     }
+    size_t backward() const { return forward() + states + rows_dv + db + du; }
 };
 
 // Checks what both directions read, and fills their part of `a`.
@@ -239,11 +244,7 @@ dl_status dl_scan(const dl_scan_desc *d, const float *initial, float *final_stat
     a.rows = state_rows;
     a.nrows = n_state_rows;
     a.o = o;
-    a.ops = static_cast<char *>(workspace);
-    a.seg = static_cast<int>(z.segment);
-    a.segments = static_cast<int>(z.segments);
-    a.seg_s = reinterpret_cast<float *>(a.ops + z.ops);
-    a.seg_m = reinterpret_cast<float *>(a.ops + z.ops + z.seg_s);
+    z.place(a, workspace);
     if (saved) {
         a.save_s = static_cast<float *>(saved);
         a.save_e = reinterpret_cast<float *>(static_cast<char *>(saved) + z.states);
@@ -296,9 +297,8 @@ dl_status dl_scan_backward(const dl_scan_desc *d, const void *saved, const void 
     a.d_ld = dlog_decay;
     a.d_u = du;
     a.dinit = d_initial;
-    char *p = static_cast<char *>(workspace);
-    a.ops = p;
-    a.w_ds = reinterpret_cast<float *>(p += z.ops);
+    char *p = z.place(a, workspace);
+    a.w_ds = reinterpret_cast<float *>(p);
     a.w_z = reinterpret_cast<float *>(p += z.states);
     a.w_db = reinterpret_cast<float *>(p += z.rows_dv);
     a.w_du = reinterpret_cast<float *>(p += z.db);
