@@ -28,10 +28,11 @@
 // never the exponential of a difference of two cumulative sums: full
 // forgetting (e = 0) and any strong decay are exact and cannot overflow.
 //
-// Kernels: prep (per chunk and head: the scaled operands, B and N, split
-// into bf16 planes in the matrix instruction's own register order); the
-// forward carry and the backward carry (per sequence, head and 16 value
-// columns: the columns of S are independent); grads (per chunk and head).
+// Kernels: prep (per chunk and head: the scaled operands, B and N, in the matrix
+// instruction's own register order); the forward carry and the backward carry
+// (per sequence, head and 16 or 32 value columns: the columns of S are
+// independent; long sequences with few heads in segments, which a small kernel
+// joins); grads (per chunk and head).
 //
 // Precision.  The products run on the bf16 matrix instructions, but state,
 // sums and factors are held in 32 bits: an fp32 factor is split into three

@@ -101,6 +101,38 @@ int main()
                             for (const void *p : {(void *)b.w_ds, (void *)b.w_z, (void *)b.w_db, (void *)b.w_du})
                                 CHECK((uintptr_t)p % 256 == 0);
                         }
+    // long sequences with few heads: segments, behind the operands, in both passes
+    for (int op : {DL_OP_GDN, DL_OP_KDA, DL_OP_RWKV6})
+        for (int dk : dims)
+            for (int dv : dims)
+                for (int N : {1, 3})
+                    for (int T : {1919 * N, 1920 * N, 100000 * N, 4194304 * N}) {
+                        dl_scan_desc d{};
+                        d.op = op;
+                        d.in_dtype = DL_BF16;
+                        d.tokens = T;
+                        d.seqs = N;
+                        d.H = 2;
+                        d.d_k = dk;
+                        d.d_v = dv;
+                        d.cu_seqlens = reinterpret_cast<int *>(16);
+                        d.q = d.k = d.v = reinterpret_cast<void *>(16);
+                        d.beta = d.log_decay = d.u = reinterpret_cast<float *>(16);
+                        const size_t ws = dl_scan_workspace_bytes(&d);
+                        char *const at = reinterpret_cast<char *>(size_t(1) << 44), *const o = reinterpret_cast<char *>(size_t(1) << 45);
+                        float *const st = reinterpret_cast<float *>(size_t(1) << 46);
+                        CHECK(dl_scan(&d, nullptr, st, nullptr, 0, o, nullptr, at, nullptr) == DL_OK);
+                        const dl::ScanArgs f = dl::g_scan;
+                        CHECK((f.seg > 0) == (T >= 1920 * N && N * 2 * (dv / 16) <= 64));
+                        if (f.seg == 0)
+                            continue;
+                        // a sequence has four segments or more, and every one a slot
+                        CHECK(f.seg * 64L * 3 < T / N && f.segments >= T / (64L * f.seg) + N + 1);
+                        const size_t sh = size_t(f.segments) * 2;
+                        CHECK((char *)f.seg_s >= f.ops + size_t(f.slots) * 2 * dl::scan_op_bytes(dl::scan_planes(op, DL_BF16), dk < 32 ? 32 : dk));
+                        CHECK((char *)f.seg_m >= (char *)f.seg_s + sh * dk * dv * 4 && (char *)f.seg_m + sh * dk * dk * 4 <= at + ws);
+                        CHECK((uintptr_t)f.seg_s % 256 == 0 && (uintptr_t)f.seg_m % 256 == 0);
+                    }
     const int bad[] = {INT_MIN, -1, 0, 17, 24, 129, INT_MAX};
     int launched = dl::g_scans;
     for (int x : bad)

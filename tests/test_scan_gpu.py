@@ -393,6 +393,39 @@ def test_graph_replays(op):
 
 
 @needs_gpu
+def test_long_sequence_in_a_graph():
+    """Segments in a captured training step, replayed on new inputs among other
+    work, against eager calls: bit for bit."""
+    import recurrent_state_update_amd as rsu
+    sets = [inputs("gdn", [2700], 2, 32, 32, torch.bfloat16, seed=s) for s in range(3)]
+    x = {n: t.cuda().requires_grad_(True) for n, t in sets[0][0].items() if t is not None}
+    do, ds = sets[0][2].cuda(), sets[0][3].cuda()
+
+    def step():
+        o, s = rsu.scan("gdn", x["q"], x["k"], x["v"], x["beta"], x["log_decay"], initial_state=x["initial_state"])
+        return [o, s, *torch.autograd.grad([o, s], list(x.values()), [do, ds])]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = [t.detach() for t in step()]
+    for new, cu, ndo, nds in sets[1:] + sets[:1]:
+        with torch.no_grad():
+            for n, t in x.items():
+                t.copy_(new[n])
+            do.copy_(ndo)
+            ds.copy_(nds)
+        g.replay()
+        got = [t.clone() for t in outs]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, gpu_run("gdn", new, cu, ndo, nds).values()))
+
+
+@needs_gpu
 def test_prefill_in_a_graph():
     """Prompts continued by replays, against eager calls; a list of slots is
     refused there, and the capture goes on."""
