@@ -74,12 +74,12 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// A sum of products of factors in planes.  The pairs of planes i + j < ORDER
-// count: ORDER 3 leaves out what is below 2^-24 of the largest product, ORDER 2
-// (where only an output rounded to bf16 is formed) what is below 2^-16.  One
-// accumulator per order: their chains overlap, and small sums stay apart from
-// large ones until the end.
-template <int ORDER> struct Acc {
+// A sum of products of factors in planes.  The pairs of planes i + j < 3 count:
+// what is left out is below 2^-24 of the largest product.  One accumulator per
+// order: their chains overlap, and small sums stay apart from large ones until
+// the end.
+constexpr int ORDER = 3;
+struct Acc {
     f32x4 c[ORDER];
     __device__ __forceinline__ explicit Acc(f32x4 x = f32x4{0, 0, 0, 0})
     {
@@ -108,7 +108,7 @@ template <int ORDER> struct Acc {
 };
 // The same with one accumulator, where registers are short and the products
 // of several sums overlap anyway.
-template <int ORDER, int NA, int NB>
+template <int NA, int NB>
 __device__ __forceinline__ f32x4 mma(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB], f32x4 c)
 {
 #pragma unroll
@@ -156,10 +156,8 @@ template <int OP, typename TIn> struct Plan {
     // rows of the products
     static constexpr bool ROWS = OP == GDN;
     static constexpr int NPX = scan_planes(OP, BF ? BF16 : F32); // planes of the keys' operands
-    // planes and order where the product only reaches o
-    static constexpr int ORDER_O = BF ? 2 : 3;
-    static constexpr int NPQ = NPX < ORDER_O ? NPX : ORDER_O, NPB = ORDER_O;
     static constexpr int NPI = BF ? 1 : 3; // planes of an input
+    static constexpr int NPB = DELTA ? 3 : NPI; // planes of b
 };
 
 template <typename TIn> __device__ __forceinline__ float from_in(TIn x);

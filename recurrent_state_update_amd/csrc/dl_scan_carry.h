@@ -63,10 +63,10 @@ template <int KS, int M, int N, int K> __device__ __forceinline__ void get_all(b
         b.get(f[ks], ks, lane);
 }
 // acc + a b, a row block's fragments and the columns' in registers
-template <int ORDER, int KS, int NA, int NB>
+template <int KS, int NA, int NB>
 __device__ __forceinline__ f32x4 product(const bf16x8 (&a)[KS][NA], const bf16x8 (&b)[KS][NB], f32x4 acc)
 {
-    Acc<ORDER> c(acc);
+    Acc c(acc);
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
         c.add(a[ks], b[ks]);
@@ -74,13 +74,12 @@ __device__ __forceinline__ f32x4 product(const bf16x8 (&a)[KS][NA], const bf16x8
 }
 // The same for a triangular C x C operand: the half that is zero is skipped
 // (first: whether k < 32 counts for this row block, second: k >= 32).
-template <int ORDER, int NA, int NB>
+template <int NA, int NB>
 __device__ __forceinline__ f32x4 product_tri(const bf16x8 (&a)[2][NA], const Planes<NB, C> &b, bool first, bool second,
                                              int lane, f32x4 acc)
 {
-    constexpr int M = NB < ORDER ? NB : ORDER;
-    Acc<ORDER> c(acc);
-    bf16x8 f[M];
+    Acc c(acc);
+    bf16x8 f[NB];
     if (first) {
         b.get(f, 0, lane);
         c.add(a[0], f);
@@ -247,8 +246,8 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
     constexpr int TWO = DELTA ? 1 : 2;
     __shared__ Planes<3, DKP> sp[TWO][NC];        // the state
     __shared__ Planes<3, C> rp[DELTA ? NC : 1];   // V - K~ S
-    __shared__ Planes<3, C> hp[TWO][NC];          // b (ROWS: P_Ci b), for the state
-    __shared__ Planes<P::NPB, C> bp[2][NC];       // b, for o (in turn: delta rule, read a chunk later)
+    __shared__ Planes<P::NPB, C> bp[2][NC];       // b (in turn: the delta rule's o reads it a chunk later)
+    __shared__ Planes<3, C> hp[ROWS ? NC : 1];    // P_Ci b, for the state
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, r4 = (lane >> 4) * 4, i0 = (w & 3) * 16 + r4;
     const int tiles = a.dv / (16 * NC);
@@ -275,13 +274,13 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
     auto ops = [&](int c) { return O(a, static_cast<long>(sq.base + c) * a.H + h); };
 
     // o = Q~ S + B b of rows i0..
-    Operand<KS, P::NPQ> qf;
-    Operand<2, P::NPB> bf;
+    Operand<KS, P::NPX> qf;
+    Operand<2, 3> bf;
     TIn *op = static_cast<TIn *>(a.o) + static_cast<long>(sq.start) * width + first;
     auto load_q = [&](int c) { qf.load(ops(c).op(1), w & 3, lane); };
     auto load_b = [&](int c) { bf.load_tri(ops(c).mat(1), LOWER, w & 3, lane); };
     auto with_b = [&](f32x4 o, const Planes<P::NPB, C> &b) {
-        return product_tri<P::ORDER_O>(bf.f, b, true, (w & 3) >= 2, lane, o);
+        return product_tri(bf.f, b, true, (w & 3) >= 2, lane, o);
     };
     auto store_o = [&](int c, const f32x4 (&o)[NC]) {
         const ChunkRows<TIn> rows(op, width, c, sq.len, 16 * NC);
@@ -345,7 +344,7 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
                 for (int t = 0; t < NC; ++t) {
                     bf16x8 f[KS][3];
                     get_all(f, sp[0][t], lane);
-                    f32x4 ks = product<3>(kf.f, f, zero);
+                    f32x4 ks = product(kf.f, f, zero);
                     if (ROWS)
                         ks *= gi;
                     rp[t].put(col, i0, x[t] - ks);
@@ -354,9 +353,10 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
                 __syncthreads(); // V - K~ S is complete, and the state's planes are read
 #pragma unroll
                 for (int t = 0; t < NC; ++t) {
-                    x[t] = product_tri<3>(nf.f, rp[t], true, w >= 2, lane, zero);
+                    x[t] = product_tri(nf.f, rp[t], true, w >= 2, lane, zero);
                     const f32x4 b = x[t] * beta;
-                    hp[0][t].put(col, i0, ROWS ? b * ge : b);
+                    if (ROWS)
+                        hp[t].put(col, i0, b * ge);
                     bp[c & 1][t].put(col, i0, b);
                 }
                 load_n(next);
@@ -375,10 +375,8 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
         } else {
             auto put_v = [&](int c) {
 #pragma unroll
-                for (int t = 0; t < NC; ++t) {
-                    hp[c & 1][t].put(col, i0, take_v(t));
+                for (int t = 0; t < NC; ++t)
                     bp[c & 1][t].put(col, i0, take_v(t));
-                }
             };
             put_v(0);
             load_v(chunks > 1 ? 1 : 0);
@@ -398,9 +396,9 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
                 if (MODE != LOCAL)
 #pragma unroll
                     for (int t = 0; t < NC; ++t) {
-                        bf16x8 f[KS][P::ORDER_O];
+                        bf16x8 f[KS][3];
                         get_all(f, sp[c & 1][t], lane);
-                        o[t] = with_b(product<P::ORDER_O>(qf.f, f, zero), bp[c & 1][t]);
+                        o[t] = with_b(product(qf.f, f, zero), bp[c & 1][t]);
                     }
                 put_v(c + 1); // (behind the last chunk: read by nobody)
                 load_v(after);
@@ -500,9 +498,9 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
             } else if constexpr (DELTA) {
 #pragma unroll
                 for (int t = 0; t < NC; ++t) {
-                    bf16x8 f[KS][P::ORDER_O];
+                    bf16x8 f[KS][3];
                     get_all(f, sp[0][t], lane);
-                    o[t] = product<P::ORDER_O>(qf.f, f, zero);
+                    o[t] = product(qf.f, f, zero);
                     if (ROWS)
                         o[t] *= gi;
                 }
@@ -529,11 +527,14 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
                 __syncthreads();
 #pragma unroll
             for (int t = 0; t < NC; ++t) {
-                bf16x8 f[2][3];
-                get_all(f, hp[DELTA ? 0 : c & 1][t], lane);
+                bf16x8 f[2][P::NPB];
+                if constexpr (ROWS)
+                    get_all(f, hp[t], lane);
+                else
+                    get_all(f, bp[c & 1][t], lane);
 #pragma unroll
                 for (int r = 0; r < RB; ++r)
-                    S[t][r] = product<3>(tf[r].f, f, S[t][r] * gam[r]);
+                    S[t][r] = product(tf[r].f, f, S[t][r] * gam[r]);
             }
             load_t(next);
             put_state(c + 1);
@@ -704,10 +705,10 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
             for (int t = 0; t < NC; ++t) {
                 bf16x8 f[KS][3];
                 get_all(f, sp[DELTA ? 0 : c & 1][t], lane);
-                db[t] = product<3>(kf.f, f, zero);
+                db[t] = product(kf.f, f, zero);
                 if (ROWS)
                     db[t] *= ge;
-                db[t] = product_tri<3>(bt.f, gp[c & 1][t], w < 2, true, lane, db[t]);
+                db[t] = product_tri(bt.f, gp[c & 1][t], w < 2, true, lane, db[t]);
                 x[t] = db[t];
                 if (DELTA)
                     wp[t].put(col, i0, db[t] * beta);
@@ -717,7 +718,7 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
                 __syncthreads(); // beta db is complete; the planes of dS' are read
 #pragma unroll
                 for (int t = 0; t < NC; ++t) {
-                    x[t] = product_tri<3>(nt.f, wp[t], w < 2, true, lane, zero);
+                    x[t] = product_tri(nt.f, wp[t], w < 2, true, lane, zero);
                     zp[t].put(col, i0, ROWS ? -x[t] * gi : -x[t]);
                 }
                 load_n(next);
@@ -866,7 +867,7 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
                     get_all(f, gp[c & 1][t], lane);
 #pragma unroll
                 for (int r = 0; r < RB; ++r)
-                    S[t][r] = product<3>(qt[r].f, f, S[t][r] * gam[r]);
+                    S[t][r] = product(qt[r].f, f, S[t][r] * gam[r]);
             }
             load_q(next);
             if constexpr (DELTA) {
@@ -880,7 +881,7 @@ __global__ __launch_bounds__(512) void scan_carry_bwd_kernel(ScanArgs a)
                     get_all(f, zp[t], lane);
 #pragma unroll
                     for (int r = 0; r < RB; ++r)
-                        S[t][r] = product<3>(kt[r].f, f, S[t][r]);
+                        S[t][r] = product(kt[r].f, f, S[t][r]);
                 }
             }
             load_k(next);

@@ -32,12 +32,11 @@ template <int OP, typename TIn> struct GradStage {
 };
 
 template <int OP, typename TIn, int DKP> struct GradLds {
-    static constexpr int LD = DKP + 4, XLD = C + 8;
-    // GDN: the weights dB P, its transpose and dA P + its transpose in planes;
-    // they only reach dq and dk
-    static constexpr int NX = Plan<OP, TIn>::ORDER_O;
+    static constexpr int LD = DKP + 4;
+    // GDN: the weights dB P, its transpose and dA P + its transpose (fp32, split
+    // when read: in planes they would leave room for one workgroup on a CU)
     struct Rows {
-        __bf16 x1[NX][C * XLD], x2[NX][C * XLD], x3[NX][C * XLD];
+        float x1[C * MLD], x2[C * MLD], x3[C * MLD];
     };
     // per key: keys and queries scaled within their blocks, dA and dB
     struct Keys {
@@ -184,18 +183,18 @@ __global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_gr
         for (int I = 0; I < 4; ++I) {
             bf16x8 e[St::NE];
             frag(e, s.st.e, I);
-            dH[I] = mma<3>(e, pl, dH[I]);
+            dH[I] = mma(e, pl, dH[I]);
         }
         split(S, pl);
 #pragma unroll
         for (int I = 0; I < 4; ++I) {
             bf16x8 g[P::NPI];
             frag(g, s.st.g, I);
-            dQ[I] = mma<3>(g, pl, dQ[I]);
+            dQ[I] = mma(g, pl, dQ[I]);
             if constexpr (DELTA) {
                 bf16x8 z[3];
                 frag(z, s.st.z, I);
-                dK[I] = mma<3>(z, pl, dK[I]);
+                dK[I] = mma(z, pl, dK[I]);
             }
         }
 #pragma unroll
@@ -207,11 +206,11 @@ __global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_gr
             bf16x8 g[P::NPI], e[St::NE];
             frag(g, s.st.g, I);
             frag(e, s.st.e, J);
-            xB[p] = mma<3>(g, e, xB[p]);
+            xB[p] = mma(g, e, xB[p]);
             if constexpr (DELTA) {
                 bf16x8 z[3];
                 frag(z, s.st.z, I);
-                xM[p] = mma<3>(z, e, xM[p]);
+                xM[p] = mma(z, e, xM[p]);
             }
         }
     }
@@ -221,7 +220,7 @@ __global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_gr
     __syncthreads(); // the stage is read; e, eb, beta and gs are complete
 
     if constexpr (OP == GDN) {
-        // ---- the decays of pairs; zero the weights' planes
+        // ---- the decays of pairs; zero the weights
         for (int b = w; b < 4; b += NW)
             if (lane < 16) {
                 float p = 0.f, pre = 1.f, suf = 1.f, all = 1.f;
@@ -282,20 +281,14 @@ __global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_gr
                 s.dbeta[b][lane] = cm;
                 s.colw[b][lane] = cw;
             }
-            bf16x4 p1[G::NX], p3[G::NX];
-            split(w1, p1);
-            split(w3, p3);
+            *reinterpret_cast<f32x4 *>(&s.x.x2[(J * 16 + c16) * MLD + I * 16 + r4]) = w1;
 #pragma unroll
-            for (int n = 0; n < G::NX; ++n) {
-                *reinterpret_cast<bf16x4 *>(&s.x.x2[n][(J * 16 + c16) * G::XLD + I * 16 + r4]) = p1[n];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = I * 16 + r4 + e, j = J * 16 + c16;
-                    s.x.x1[n][i * G::XLD + j] = p1[n][e];
-                    if (i > j) {
-                        s.x.x3[n][i * G::XLD + j] = p3[n][e];
-                        s.x.x3[n][j * G::XLD + i] = p3[n][e];
-                    }
+            for (int e = 0; e < 4; ++e) {
+                const int i = I * 16 + r4 + e, j = J * 16 + c16;
+                s.x.x1[i * MLD + j] = w1[e];
+                if (i > j) {
+                    s.x.x3[i * MLD + j] = w3[e];
+                    s.x.x3[j * MLD + i] = w3[e];
                 }
             }
         }
@@ -317,10 +310,10 @@ __global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_gr
         __syncthreads();
         qt.ready();
         kt.ready();
-        auto xfrag = [&](bf16x8 (&f)[G::NX], const __bf16 (&x)[G::NX][C * G::XLD], int rb, int ks) {
-#pragma unroll
-            for (int n = 0; n < G::NX; ++n)
-                f[n] = *reinterpret_cast<const bf16x8 *>(&x[n][(rb * 16 + c16) * G::XLD + ks * 32 + (lane >> 4) * 8]);
+        auto xfrag = [&](bf16x8 (&f)[3], const float (&x)[C * MLD], int rb, int ks) {
+            const float *p = &x[(rb * 16 + c16) * MLD + ks * 32 + (lane >> 4) * 8];
+            const f32x4 lo = ld4(p), hi = ld4(p + 4);
+            split(f32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}, f);
         };
 #pragma unroll
         for (int I = 0; I < 4; ++I) {
@@ -354,16 +347,16 @@ __global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_gr
             }
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                bf16x8 f[G::NX];
+                bf16x8 f[3];
                 if (frag_used(LOWER, I, ks)) {
                     xfrag(f, s.x.x1, I, ks);
-                    dQ[I] = mma<P::ORDER_O>(f, kt.f[ks], dQ[I]);
+                    dQ[I] = mma(f, kt.f[ks], dQ[I]);
                 }
                 xfrag(f, s.x.x3, I, ks);
-                dK[I] = mma<P::ORDER_O>(f, kt.f[ks], dK[I]);
+                dK[I] = mma(f, kt.f[ks], dK[I]);
                 if (frag_used(UPPER, I, ks)) {
                     xfrag(f, s.x.x2, I, ks);
-                    dK[I] = mma<P::ORDER_O>(f, qt.f[ks], dK[I]);
+                    dK[I] = mma(f, qt.f[ks], dK[I]);
                 }
             }
 #pragma unroll

@@ -84,7 +84,7 @@ __device__ __forceinline__ void store_mats(PrepMats &m, float *tmp, const Ops<NP
     if (BWD)
         store_op<3, C, C, UPPER>(ops.mat(1), [&](int i, int j) { return m.B[j * MLD + i]; });
     else
-        store_op<P::NPB, C, C, LOWER>(ops.mat(1), [&](int i, int j) { return m.B[i * MLD + j]; });
+        store_op<3, C, C, LOWER>(ops.mat(1), [&](int i, int j) { return m.B[i * MLD + j]; });
     if constexpr (P::DELTA) {
         __syncthreads(); // B is read (and zero above the diagonal, as N will be)
         invert_unit_lower(m.L, m.B, tmp, w, lane);
@@ -328,11 +328,10 @@ __global__ __launch_bounds__(prep_threads<DKP>(), 4) void scan_prep_kernel(ScanA
             }
         };
         constexpr std::integral_constant<int, P::NPX> npx;
-        constexpr std::integral_constant<int, P::NPQ> npq;
         if (!BWD) {
             if (DELTA)
                 rows(npx, ops.op(0), s.k, s.pre);
-            rows(npq, ops.op(1), s.q, s.pre);
+            rows(npx, ops.op(1), s.q, s.pre);
             columns(npx, ops.op(2), s.e, s.suf);
         } else {
             rows(npx, ops.op(0), s.e, s.suf);
@@ -476,7 +475,7 @@ __global__ __launch_bounds__(256) void scan_prep_gdn_kernel(ScanArgs a, bool vec
 #pragma unroll
     for (int p = 0; p < 5; ++p) {
         const int task = w + p * 4, b = task >= 10 ? task - 10 : task, I = block_row(b), J = block_col(b);
-        Acc<3> x;
+        Acc x;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             bf16x8 l[NP], r[NP];
@@ -490,15 +489,12 @@ __global__ __launch_bounds__(256) void scan_prep_gdn_kernel(ScanArgs a, bool vec
         acc[p] = x.sum();
     }
     // the keys' operands: rows of the tiles, and their columns
-    auto rows = [&](auto np, char *op, const __bf16 (&x)[NP][C * LD]) {
-        constexpr int N = decltype(np)::value;
+    auto rows = [&](char *op, const __bf16 (&x)[NP][C * LD]) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            bf16x8 f[N];
-#pragma unroll
-            for (int n = 0; n < N; ++n)
-                f[n] = *reinterpret_cast<const bf16x8 *>(&x[n][(w * 16 + (lane & 15)) * LD + ks * 32 + (lane >> 4) * 8]);
-            store_frag<N>(op, KS, w, ks, lane, f);
+            bf16x8 f[NP];
+            frag(f, x, w, ks);
+            store_frag<NP>(op, KS, w, ks, lane, f);
         }
     };
     auto columns = [&](char *op, const __bf16 (&x)[NP][C * LD]) {
@@ -513,9 +509,9 @@ __global__ __launch_bounds__(256) void scan_prep_gdn_kernel(ScanArgs a, bool vec
             store_frag<NP>(op, 2, rb, ks, lane, f);
         }
     };
-    rows(std::integral_constant<int, NP>(), ops.op(0), s.k);
+    rows(ops.op(0), s.k);
     if (!BWD) {
-        rows(std::integral_constant<int, P::NPQ>(), ops.op(1), s.q);
+        rows(ops.op(1), s.q);
         columns(ops.op(2), s.k);
     } else {
         columns(ops.op(1), s.q);
