@@ -8,8 +8,17 @@
 // what is read later)
 //   cq_i = Gam_i dQ~_i + sum_j dB_ij P_ij k_j,  cr_i = Gam_i dK~_i + sum_j dA_ij P_ij k_j
 //   cc_j = P_Cj dK^_j + sum_i P_ij (dA_ij k_i + dB_ij q_i)
-//   dq = cq, dk = cr + cc, and the log-decay's gradient, the sum over all
-// pairs whose decay contains it.  dbeta_j = (db . E)_j - sum_i A_ij z_i . E_j.
+//   dq = cq, dk = cr + cc.  dbeta_j = (db . E)_j - sum_i A_ij z_i . E_j.
+// The log-decay's gradient at row t is the sum of what its decay is a factor of,
+// per key (GDN: over the keys)
+//   Gam_C <S, dS'>                                              for every t
+//   reads of S, q_i Gam_i dQ~_i + k_i Gam_i dK~_i              rows i >= t
+//   writes into S', k_j P_Cj dK^_j                              rows j < t
+//   pairs, P_ij (q_i dB_ij + k_i dA_ij) k_j                     i >= t > j
+// (RWKV6's reads and pairs, i > t), and of nothing else.  As a difference of sums
+// over all rows or pairs it would carry the rounding of terms that the decay does
+// not touch: a strong decay's gradient, which is as small as the decay, would be
+// lost in it.
 //
 // One workgroup per chunk and head, one wave per 16 keys.  Bound by reading S
 // and dS' (64 KiB each at d = 128, the largest part of a chunk) and by the
@@ -52,13 +61,19 @@ template <int OP, typename TIn, int DKP> struct GradLds {
     float beta[C], dbeta[10][16]; // per pair of blocks: sum_i A_ij (-z_i . E_j)
     // per key
     float eb[ROWS ? 1 : 4 * DKP], pre[ROWS ? 1 : 4 * DKP], suf[ROWS ? 1 : 4 * DKP]; // of, before, behind a block
-    float part[ROWS ? 1 : 4 * DKP], kh[ROWS ? 1 : 4 * DKP];
+    float part[ROWS ? 1 : 4 * DKP], cross[ROWS ? 1 : 4 * DKP]; // what crosses all of a block
     // GDN
     float e[C], rpre[C], rsuf[C], reb[4];                      // decays of rows
     float diag[ROWS ? 4 : 1][16 * 16];                         // P_ij of the diagonal blocks
-    float roww[10][16], colw[10][16];                          // sums of W_ij = dB B + dA A
+    // sums of W_ij = dB B + dA A: over a row's columns, a column's rows, the
+    // pair of blocks; within a block, over the pairs i >= t > j
+    float roww[10][16], colw[10][16], allw[10];
     float ra[ROWS ? DKP / 16 : 1][C], rh[ROWS ? DKP / 16 : 1][C]; // per 16 keys: reads of S, writes into S'
 };
+
+// x is formed here: the compiler would else move the sums that only a store under
+// a condition takes behind that condition, and keep all their terms until then.
+__device__ __forceinline__ void formed(float &x) { asm volatile("" : "+v"(x)); }
 
 // Waves to a SIMD that the registers are held to: two workgroups on a CU where
 // LDS allows them.
@@ -255,7 +270,7 @@ __global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_gr
             for (int K = J + 1; K < I; ++K)
                 between *= s.reb[K];
             const float right = between * s.rsuf[J * 16 + c16];
-            f32x4 w1, w3;
+            f32x4 w1, w3, W;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = r4 + e;
@@ -264,16 +279,28 @@ __global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_gr
                 const float gb = below || on ? beta * xB[p][e] : 0.f, ga = below ? beta * xM[p][e] : 0.f;
                 w1[e] = gb * f;
                 w3[e] = ga * f;
-                const float W = below ? gb * B[e] + ga * A[e] : 0.f;
-                cw += W;
+                W[e] = below ? gb * B[e] + ga * A[e] : 0.f;
+                cw += W[e];
                 cm += below ? A[e] * xM[p][e] : 0.f;
-                float rw = W;
+            }
+            if (I == J) { // of column j's rows, those from row t on, for the t behind j
+                const float t1 = __shfl_down(cw, 16), t2 = __shfl_down(cw, 32), t3 = __shfl_down(cw, 48);
+                float from = (lane < 48 ? t1 : 0.f) + (lane < 32 ? t2 : 0.f) + (lane < 16 ? t3 : 0.f);
+#pragma unroll
+                for (int e = 3; e >= 0; --e) {
+                    from += W[e];
+                    W[e] = r4 + e > c16 ? from : 0.f;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float rw = W[e];
                 rw = add_row_ror<1>(rw);
                 rw = add_row_ror<2>(rw);
                 rw = add_row_ror<4>(rw);
                 rw = add_row_ror<8>(rw);
                 if (c16 == 0)
-                    s.roww[b][i] = rw;
+                    s.roww[b][r4 + e] = rw;
             }
             cm = wave_sum_from<16>(cm);
             cw = wave_sum_from<16>(cw);
@@ -281,6 +308,12 @@ __global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_gr
                 s.dbeta[b][lane] = cm;
                 s.colw[b][lane] = cw;
             }
+            cw = add_row_ror<1>(cw);
+            cw = add_row_ror<2>(cw);
+            cw = add_row_ror<4>(cw);
+            cw = add_row_ror<8>(cw);
+            if (lane == 0)
+                s.allw[b] = cw;
             *reinterpret_cast<f32x4 *>(&s.x.x2[(J * 16 + c16) * MLD + I * 16 + r4]) = w1;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -370,11 +403,11 @@ __global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_gr
             }
         }
         __syncthreads();
-        // ---- one lane per row: the log-decay's gradient at row t is the sum
-        // over what crosses it: Gam_C <S, dS'>, the reads of S at rows i >= t,
-        // the writes of rows j < t into S', and the pairs i >= t > j
+        // ---- one lane per row t
         if (tid < C) {
             const int b = lane >> 4, i = lane & 15;
+            // x: reads; y: writes; in: pairs within t's block, of it and earlier
+            // ones, of later ones and it; all: of later ones and earlier ones
             float x = 0.f, y = 0.f, g = 0.f, dbeta = 0.f;
 #pragma unroll
             for (int n = 0; n < NW; ++n) {
@@ -384,24 +417,36 @@ __global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_gr
             for (int K = 0; K < DKP; K += 64)
                 g += K + lane < DKP ? s.gs[K + lane] : 0.f;
             g = wave_sum_from<1>(g) * (s.reb[0] * s.reb[1] * s.reb[2] * s.reb[3]);
-            for (int K = 0; K <= b; ++K)
-                x += s.roww[b * (b + 1) / 2 + K][i];
+            const float in = s.roww[b * (b + 3) / 2][i];
+            float early = 0.f, late = 0.f;
+            for (int K = 0; K < b; ++K)
+                early += s.roww[b * (b + 1) / 2 + K][i];
             for (int K = b; K < 4; ++K) {
-                x -= s.colw[K * (K + 1) / 2 + b][i];
+                late += K > b ? s.colw[K * (K + 1) / 2 + b][i] : 0.f;
                 dbeta += s.dbeta[K * (K + 1) / 2 + b][i];
             }
-            float before = y; // sum of the y of the rows up to this one, x from this one on
+            const float all = b == 1 ? s.allw[3] + s.allw[6] : b == 2 ? s.allw[6] + s.allw[7] : 0.f;
+            // rows from t on, rows before t
+            y = __shfl_up(y, 1);
+            y = lane > 0 ? y : 0.f;
+            late = __shfl_up(late, 1);
+            late = i > 0 ? late : 0.f;
 #pragma unroll
             for (int m = 1; m < 64; m *= 2) {
-                const float u = __shfl_up(before, m), v = __shfl_down(x, m);
-                before += lane >= m ? u : 0.f;
+                const float u = __shfl_up(y, m), v = __shfl_down(x, m);
+                y += lane >= m ? u : 0.f;
                 x += lane + m < 64 ? v : 0.f;
+                if (m < 16) {
+                    const float p = __shfl_up(late, m), q = __shfl_down(early, m);
+                    late += i >= m ? p : 0.f;
+                    early += i + m < 16 ? q : 0.f;
+                }
             }
             for (int t = 0; t < tiles; ++t)
                 dbeta += a.w_db[(slot_head * tiles + t) * C + lane];
             if (lane < ch.rows) {
                 const long at = (t0 + lane) * a.H + h;
-                a.d_ld[at] = a.ld[at] < kMinLogDecay ? 0.f : g + (before - y) + x; // below it the decay is held
+                a.d_ld[at] = a.ld[at] < kMinLogDecay ? 0.f : g + x + y + in + early + late + all; // below it the decay is held
                 a.d_beta[at] = dbeta;
             }
         }
@@ -476,23 +521,58 @@ __global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_gr
                 y[e] = x[(row + r4 + e) * LD + key] * f;
             return y;
         };
+        // what crosses whole blocks, per key: the block's reads of S and writes into
+        // S', and the pairs of blocks with others between them
+        auto rows_sum = [&](f32x4 y) { return wave_sum_from<16>((y[0] + y[1]) + (y[2] + y[3])); };
+        auto reads = [&](f32x4 q, f32x4 k, int I) { // by block I, given their parts
+            f32x4 y = q * column(s.x.ql, I * 16, 1.f);
+            if (DELTA)
+                y += k * column(s.x.kl, I * 16, 1.f);
+            return y;
+        };
+        float rs[4], kh[4];
 #pragma unroll
-        for (int I = 0; I < 4; ++I) { // what the block's rows write into S'
-            const f32x4 y = dH[I] * column(s.x.kr, I * 16, 1.f);
-            const float x = wave_sum_from<16>((y[0] + y[1]) + (y[2] + y[3]));
-            if (lane < 16)
-                s.kh[I * DKP + key] = x;
-        }
+        for (int I = 1; I < 4; ++I)
+            rs[I] = rows_sum(reads(dQ[I], dK[I], I));
+#pragma unroll
+        for (int I = 0; I < 3; ++I)
+            kh[I] = rows_sum(dH[I] * column(s.x.kr, I * 16, 1.f));
+        f32x4 over1 = zero, over2 = zero; // pairs across block 1, across block 2
 #pragma unroll
         for (int I = 1; I < 4; ++I) {
             float f = 1.f;
 #pragma unroll
             for (int J = I - 1; J >= 0; --J) {
                 const f32x4 k = column(s.x.kr, J * 16, f);
-                dQ[I] = mfma32x4(ld4(&s.x.dB[(I * 16 + c16) * MLD + J * 16 + r4]), k, dQ[I]);
+                const bool next = J == I - 1;
+                const f32x4 q = mfma32x4(ld4(&s.x.dB[(I * 16 + c16) * MLD + J * 16 + r4]), k, next ? dQ[I] : zero);
+                f32x4 c = zero;
                 if (DELTA)
-                    dK[I] = mfma32x4(ld4(&s.x.dA[(I * 16 + c16) * MLD + J * 16 + r4]), k, dK[I]);
+                    c = mfma32x4(ld4(&s.x.dA[(I * 16 + c16) * MLD + J * 16 + r4]), k, next ? dK[I] : zero);
+                if (next) {
+                    dQ[I] = q;
+                    dK[I] = c;
+                } else {
+                    const f32x4 y = reads(q, c, I);
+                    if (J == 0)
+                        over1 += y;
+                    if (I == 3)
+                        over2 += y;
+                    dQ[I] += q;
+                    dK[I] += c;
+                }
                 f *= s.eb[J * DKP + key];
+                keep_order(); // (one pair's operands at a time: the registers are full)
+            }
+        }
+        {
+            const float all = s.pre[3 * DKP + key] * s.eb[3 * DKP + key] * s.gs[key];
+            const float o1 = rows_sum(over1), o2 = rows_sum(over2);
+            if (lane < 16) {
+                s.cross[key] = all + (rs[1] + rs[2] + rs[3]);
+                s.cross[DKP + key] = all + (rs[2] + rs[3]) + kh[0] + o1;
+                s.cross[2 * DKP + key] = all + rs[3] + (kh[0] + kh[1]) + o2;
+                s.cross[3 * DKP + key] = all + (kh[0] + kh[1] + kh[2]);
             }
         }
 #pragma unroll
@@ -547,8 +627,27 @@ __global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_gr
                 p *= ev[i];
             }
         }
-        // ---- pairs inside the block: hb[j] = P_ij of the row i at hand
-        float gd[16]; // dB_ii
+        // ---- the log-decay's gradient: reads and writes of the block's rows, across
+        // its border
+        float gl[16];
+        {
+            float x = 0.f, y = 0.f;
+#pragma unroll
+            for (int i = 15; i >= 0; --i) {
+                const float before = x;
+                x += DELTA ? fmaf(qv[i], cq[i], kv[i] * cr[i]) : qv[i] * cq[i];
+                gl[i] = DELTA ? x : before;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                gl[i] += y;
+                y = fmaf(kv[i], cc[i], y);
+            }
+        }
+        // ---- pairs inside the block: hb[j] = P_ij of the row i at hand; its pairs
+        // with the rows up to j cross row j + 1
+        const float ud = !DELTA && d < a.dk ? a.u[static_cast<long>(h) * a.dk + d] : 0.f;
+        float du = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             f32x4 gb[4], ga[4];
@@ -560,72 +659,50 @@ __global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_gr
                 if (DELTA)
                     ga[q] = ld4(&s.x.dA[(r0 + i) * MLD + r0 + q * 4]);
             }
-            gd[i] = gb[i / 4][i % 4];
+            const float own = gb[i / 4][i % 4]; // dB_ii: the pair (i, i), which no decay touches
+            const float f = DELTA ? own : own * ud;
+            float pairs = 0.f;
+            cq[i] = fmaf(f, kv[i], cq[i]);
+            cc[i] = fmaf(f, qv[i], cr[i] + cc[i]);
+            du = fmaf(own * qv[i], kv[i], du);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 if (j >= i)
                     continue;
                 const float before = hb[j];
                 hb[j] *= ev[i];
-                const float b = gb[j / 4][j % 4], pq = DELTA ? hb[j] : before;
-                cq[i] = fmaf(b, pq * kv[j], cq[i]);
+                const float b = gb[j / 4][j % 4], pq = DELTA ? hb[j] : before, pk = pq * kv[j];
+                cq[i] = fmaf(b, pk, cq[i]);
+                float x = b * qv[i];
                 if (DELTA) {
-                    const float x = ga[j / 4][j % 4];
-                    cr[i] = fmaf(x, pq * kv[j], cr[i]);
-                    cc[j] = fmaf(pq, fmaf(b, qv[i], x * kv[i]), cc[j]);
-                } else {
-                    cc[j] = fmaf(pq, b * qv[i], cc[j]);
+                    const float m = ga[j / 4][j % 4];
+                    cc[i] = fmaf(m, pk, cc[i]);
+                    x = fmaf(m, kv[i], x);
+                }
+                cc[j] = fmaf(pq, x, cc[j]);
+                if (DELTA || j + 1 < i) {
+                    pairs = fmaf(pk, x, pairs);
+                    gl[j + 1] += pairs;
                 }
             }
             hb[i] = 1.f;
         }
-        // ---- the log-decay's gradient: with G_i = ell_1 + ... + ell_i, row
-        // i's gradient by G_i is q cq + k cr - k cc (RWKV6's q reads at
-        // G_{i-1}), and G_C's besides that Gam_C sum_v S dS' and the rows'
-        // writes into S', sum_j k_j P_Cj dK^_j; ell_t's is the sum over the
-        // G_i, i >= t.
-        float gsum = 0.f, gl[16]; // suffix sums over the block
-#pragma unroll
-        for (int i = 15; i >= 0; --i) {
-            if (DELTA) {
-                gsum += qv[i] * cq[i] + kv[i] * (cr[i] - cc[i]);
-                gl[i] = gsum;
-            } else {
-                gsum -= kv[i] * cc[i];
-                gl[i] = gsum;
-                gsum += qv[i] * cq[i];
-            }
-        }
-        s.part[tid] = gsum;
-        const float ud = !DELTA && d < a.dk ? a.u[static_cast<long>(h) * a.dk + d] : 0.f;
-        float du = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            // the pairs (i, i), which no decay touches
-            const float f = DELTA ? gd[i] : gd[i] * ud;
-            const float oq = fmaf(f, kv[i], cq[i]), ok = fmaf(f, qv[i], cr[i] + cc[i]);
-            du = fmaf(gd[i] * qv[i], kv[i], du);
+            formed(cq[i]);
+            formed(cc[i]);
+            formed(gl[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
             if (r0 + i < ch.rows && d < a.dk) {
                 const long at = ((t0 + r0 + i) * a.H + h) * a.dk + d;
-                static_cast<TIn *>(a.d_q)[at] = static_cast<TIn>(oq);
-                static_cast<TIn *>(a.d_k)[at] = static_cast<TIn>(ok);
+                static_cast<TIn *>(a.d_q)[at] = static_cast<TIn>(cq[i]);
+                static_cast<TIn *>(a.d_k)[at] = static_cast<TIn>(cc[i]);
+                a.d_ld[at] = a.ld[at] < kMinLogDecay ? 0.f : gl[i] + s.cross[tid]; // below it the decay is held
             }
         }
-        __syncthreads();
-        {
-            // behind block I0: the later blocks' sums, and what counts at G_C
-            float tail = s.pre[3 * DKP + d] * s.eb[3 * DKP + d] * s.gs[d];
-            for (int K = 0; K < 4; ++K)
-                tail += s.kh[K * DKP + d] + (K > I0 ? s.part[K * DKP + d] : 0.f);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (r0 + i < ch.rows && d < a.dk) {
-                    const long at = ((t0 + r0 + i) * a.H + h) * a.dk + d;
-                    a.d_ld[at] = a.ld[at] < kMinLogDecay ? 0.f : gl[i] + tail; // below it the decay is held
-                }
-        }
         if constexpr (!DELTA) {
-            __syncthreads();
             s.part[tid] = du;
             __syncthreads();
             if (tid < a.dk)
