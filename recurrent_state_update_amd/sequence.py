@@ -84,6 +84,14 @@ def _count(rows):
     return rows
 
 
+def _state(t):
+    """t as the library takes states: contiguous, and on a 16-byte boundary,
+    where a view of something larger (an entry of a flat cache, a gradient
+    that torch.cat's backward pass cuts out) need not be."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _rows(t, lead):
     """t [*lead, H, d] as rows of H*d elements a fixed distance apart: the
     tensor (copied only if it is not laid out so) and that distance."""
@@ -197,7 +205,7 @@ class _ScanFn(torch.autograd.Function):
         with _on(s.device, None):
             tensors, desc = s.describe(*tensors)
             d_o = None if d_o is None else d_o.contiguous()
-            d_final = None if d_final is None else d_final.contiguous()
+            d_final = None if d_final is None else _state(d_final)
             delta = s.op != "rwkv6"
             dq, dk = s.empty(s.shape["q"], s.dtype), s.empty(s.shape["q"], s.dtype)
             dv = s.empty(s.shape["v"], s.dtype)
@@ -216,7 +224,7 @@ def _initial(initial_state, shape, device):
     if initial_state is None:
         return None
     _tensor(initial_state, "initial_state", torch.float32, shape, device)
-    return initial_state.contiguous()
+    return _state(initial_state)
 
 
 def scan(op: str, q, k, v, beta, log_decay, u=None, initial_state=None, cu_seqlens=None, stream=None):
