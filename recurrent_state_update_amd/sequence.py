@@ -92,9 +92,13 @@ def _state(t):
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
-def _rows(t, lead):
-    """t [*lead, H, d] as rows of H*d elements a fixed distance apart: the
-    tensor (copied only if it is not laid out so) and that distance."""
+_MOST_STRIDE = 1 << 22  # elements from one token's row to the next, as dl_scan takes them
+
+
+def _rows(t, lead, most=None):
+    """t [*lead, H, d] as rows of H*d elements a fixed distance apart, of
+    ``most`` at the most: the tensor (copied only if it is not laid out so)
+    and that distance."""
     H, d = t.shape[-2:]
     if t.is_contiguous():
         return t, H * d
@@ -108,7 +112,7 @@ def _rows(t, lead):
         if t.shape[i] > 1 and t.stride(i) != span:
             outer = False
         span *= t.shape[i]
-    if inner and outer and step >= H * d:
+    if inner and outer and step >= H * d and (most is None or step <= most):
         return t, step
     return t.contiguous(), H * d
 
@@ -163,7 +167,7 @@ class _Scan:
     def describe(self, q, k, v, beta, log_decay, u, cu_seqlens):
         """These tensors, copied where the library cannot read them as they
         are, and their descriptor."""
-        (q, qs), (k, ks), (v, vs) = (_rows(t, len(self.shape["h"]) - 1) for t in (q, k, v))
+        (q, qs), (k, ks), (v, vs) = (_rows(t, len(self.shape["h"]) - 1, _MOST_STRIDE) for t in (q, k, v))
         beta, log_decay, u = (None if t is None else t.contiguous() for t in (beta, log_decay, u))
         return (q, k, v, beta, log_decay, u, cu_seqlens), dl_scan_desc(
             *self.sizes, qs, ks, vs, _p(cu_seqlens), q.data_ptr(), k.data_ptr(), v.data_ptr(), _p(beta),

@@ -47,3 +47,32 @@ def test_states_off_the_boundary(op):
         want = run(op, x)
         got = run(op, {**x, "initial_state": off_by_one(x["initial_state"])})
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@needs_gpu
+@pytest.mark.parametrize("op", OPS)
+def test_rows_far_apart(op):
+    """One batch entry of [T,B,W] tensors: rows further apart than the library
+    takes them."""
+    T, H, dk, dv, W = 6, 2, 16, 32, 1 << 22
+    x = {n: None if t is None else t.cuda() for n, t in inputs(op, [T], H, dk, dv, torch.bfloat16, seed=2)[0].items()}
+    wide = torch.zeros(T, 2, W, dtype=torch.bfloat16, device="cuda")
+    y, at = dict(x), 0
+    for n in "qkv":
+        d = x[n].shape[-1]
+        y[n] = wide[:, 1, at:at + H * d].unflatten(1, (H, d))
+        y[n].copy_(x[n])
+        at += H * d
+    assert all(torch.equal(a, b) for a, b in zip(run(op, y), run(op, x)))
+
+
+@needs_gpu
+def test_gate_rows_far_apart():
+    import recurrent_state_update_amd as rsu
+    T, H, d, W = 6, 2, 16, 1 << 22
+    g = torch.Generator().manual_seed(3)
+    o, gate = (torch.randn(T, H, d, generator=g).bfloat16().cuda() for _ in range(2))
+    wide = torch.zeros(T, 2, W, dtype=torch.bfloat16, device="cuda")
+    far = wide[:, 1, :H * d].unflatten(1, (H, d))
+    far.copy_(gate)
+    assert torch.equal(rsu.gated_norm(o, far), rsu.gated_norm(o, gate))
