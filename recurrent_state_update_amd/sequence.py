@@ -4,10 +4,11 @@ recurrence over whole sequences: prefill and training), `gated_norm` and
 
 Argument checks, output and workspace allocation and autograd nodes only: the
 arithmetic is in libdeltalog (dl_scan, dl_gated_norm, dl_residual_norm and
-their backward passes).  All three are differentiable once, asynchronous on
-the current stream (or ``stream``, on which their outputs are then allocated
-too; the inputs have to be ready there, as for torch's own operators) and
-capturable into HIP graphs.  Before a backward pass is captured, drop what
+their backward passes).  All three are differentiable once (in reverse;
+forward-mode derivatives and tracing are refused), asynchronous on the current
+stream (or ``stream``, on which their outputs are then allocated too; the
+inputs have to be ready there, as for torch's own operators) and capturable
+into HIP graphs.  Before a backward pass is captured, drop what
 still refers to the graph of an eager pass over the same leaves (its loss and
 outputs): torch ties a leaf's gradient to the stream of the oldest one.
 Tensors may be on any one GPU.
@@ -15,8 +16,10 @@ Tensors may be on any one GPU.
 from __future__ import annotations
 
 import contextlib
+import sys
 
 import torch
+import torch.autograd.forward_ad as _forward_ad
 
 from . import (DTYPES, _check, _dtype_id, _lib, _op_id, dl_gated_norm_workspace_bytes,
                dl_residual_norm_workspace_bytes, dl_scan_backward_workspace_bytes, dl_scan_desc,
@@ -42,6 +45,18 @@ def _on(device, stream):
 def _current(device):
     """The raw handle of a device's current stream."""
     return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _plain(name, *tensors):
+    """Refuse the transforms that would take a call of the library for no
+    operation at all: forward-mode derivatives would come out as zero, and a
+    traced function would return memory that nothing has written."""
+    if _forward_ad._current_level >= 0 and any(
+            isinstance(t, torch.Tensor) and _forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError(f"{name} has no forward-mode derivative")
+    proxies = sys.modules.get("torch.fx.experimental.proxy_tensor")
+    if torch._C._get_tracing_state() is not None or (proxies is not None and proxies.get_proxy_mode() is not None):
+        raise NotImplementedError(f"{name} cannot be traced")
 
 
 def _wants_grad(*tensors):
@@ -249,6 +264,7 @@ def scan(op: str, q, k, v, beta, log_decay, u=None, initial_state=None, cu_seqle
     Differentiable by q, k, v, beta, log_decay, u and initial_state.  A forward
     pass that will be differentiated keeps, per 64 tokens and head, the state
     and 64 d_v floats until its backward pass."""
+    _plain("scan", q, k, v, beta, log_decay, u, initial_state)
     with _on(_gpu(q, "q"), stream):
         probe = _Scan(op, q, k, v, beta, log_decay, u, cu_seqlens)
         initial = _initial(initial_state, probe.state_shape(), probe.device)
@@ -259,6 +275,7 @@ def scan(op: str, q, k, v, beta, log_decay, u=None, initial_state=None, cu_seqle
 
 
 def _prefill(st, q, k, v, beta, log_decay, cu_seqlens, slots, stream):
+    _plain("prefill", q, k, v, beta, log_decay)
     with _on(_gpu(q, "q"), stream):
         return _prefill_here(st, q, k, v, beta, log_decay, cu_seqlens, slots)
 
@@ -336,6 +353,7 @@ def gated_norm(o, gate, weight=None, eps: float = 1e-6, stream=None):
     [...,H,d] bf16 or fp32 (its rows may be slices of a projection), weight
     [d] fp32 or None.  Returns gate's dtype.  d in {16, 32, 64, 128}.
     Differentiable by o, gate and weight."""
+    _plain("gated_norm", o, gate, weight)
     dev = _gpu(o, "o")
     _gpu(gate, "gate")
     _dtype_id(o.dtype), _dtype_id(gate.dtype)
@@ -400,6 +418,7 @@ def residual_norm(x, y=None, scale=None, weight=None, eps: float = 1e-6, dtype=N
     fp32, scale and weight [D] fp32 or None; D <= 16384.  Returns (x', h), h in
     y's dtype.  Without y (the first norm): (x, h) with h = rms(x) * weight in
     ``dtype`` (default bf16).  Differentiable by x, y, scale and weight."""
+    _plain("residual_norm", x, y, scale, weight)
     _gpu(x, "x")
     if x.dim() < 1 or x.dtype != torch.float32:
         raise ValueError(f"x: want fp32 [...,D], got {x.dtype} {tuple(x.shape)}")
