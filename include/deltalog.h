@@ -277,10 +277,10 @@ int dl_slot_log_len(const dl_state *s, int slot);
  * ------------------------------------------------------------------------ */
 
 /* The sequences of one scan: `tokens` rows of all sequences, packed one after
- * the other.  cu_seqlens (device, [seqs + 1] int32, non-decreasing, first 0,
- * last <= tokens): sequence n is the rows cu_seqlens[n] .. cu_seqlens[n+1]-1,
- * possibly none; rows behind the last sequence belong to none, and are zero in
- * every output.  NULL: `seqs` sequences of tokens / seqs rows each.
+ * the other.  cu_seqlens (device, [seqs + 1] int32, non-decreasing, from 0 to
+ * tokens): sequence n is the rows cu_seqlens[n] .. cu_seqlens[n+1]-1, possibly
+ * none; rows ahead of the first sequence and behind the last belong to none,
+ * and are zero in every output.  NULL: `seqs` sequences of tokens / seqs rows each.
  * (Offsets out of order give meaningless results, but no access out of
  * range.)  q (r for RWKV6), k [tokens,H,d_k] and v [tokens,H,d_v] in in_dtype
  * may have rows further apart than H*d elements, e.g. as slices of one

@@ -171,7 +171,8 @@ template <> __device__ __forceinline__ float from_in<__bf16>(__bf16 x) { return 
 // (floor(a / C) + ceil((b - a) / C) <= floor(b / C) + 1) without a prefix sum
 // over the lengths.  The rows behind the last sequence, T / C + N + 1 slots in
 // all, count as sequence N here: no carry has it, and prep zeroes the outputs'
-// rows.  Offsets read from cu are clamped to [0, T], so a bad array cannot lead
+// rows (those ahead of the first sequence too, C of them at slot 0 and so on).
+// Offsets read from cu are clamped to [0, T], so a bad array cannot lead
 // an access out of range.
 struct Seq {
     int start, len, base;

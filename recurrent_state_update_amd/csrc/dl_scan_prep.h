@@ -32,7 +32,7 @@ template <typename T> __device__ __forceinline__ void zero_rows(void *p, const S
     for (int it = threadIdx.x; it < ch.rows * width; it += blockDim.x)
         static_cast<T *>(p)[((static_cast<long>(ch.t0) + it / width) * a.H + h) * width + it % width] = T(0);
 }
-template <int OP, typename TIn, bool BWD> __device__ __forceinline__ void zero_behind(const ScanArgs &a, const Chunk &ch, int h)
+template <int OP, typename TIn, bool BWD> __device__ __forceinline__ void zero_chunk(const ScanArgs &a, const Chunk &ch, int h)
 {
     if (!BWD) {
         zero_rows<TIn>(a.o, a, ch, h, a.dv);
@@ -43,6 +43,21 @@ template <int OP, typename TIn, bool BWD> __device__ __forceinline__ void zero_b
     zero_rows<TIn>(a.d_v, a, ch, h, a.dv);
     zero_rows<float>(a.d_beta, a, ch, h, 1);
     zero_rows<float>(a.d_ld, a, ch, h, OP == GDN ? 1 : a.dk);
+}
+
+// The chunk of a workgroup that has operands to form (rows > 0); the outputs' rows
+// of no sequence, ahead of the first and behind the last, are zeroed here.
+template <int OP, typename TIn, bool BWD> __device__ __forceinline__ Chunk prep_chunk(const ScanArgs &a, int slot, int h)
+{
+    const int before = seq_start(a, 0) - slot * C;
+    if (before > 0)
+        zero_chunk<OP, TIn, BWD>(a, {slot * C, before < C ? before : C, true}, h);
+    Chunk ch = chunk_of(a, slot);
+    if (ch.behind && ch.rows > 0) {
+        zero_chunk<OP, TIn, BWD>(a, ch, h);
+        ch.rows = 0;
+    }
+    return ch;
 }
 
 // The ten 16 x 16 blocks (I, J) of a lower triangle, numbered row by row.
@@ -140,11 +155,9 @@ __global__ __launch_bounds__(prep_threads<DKP>(), 4) void scan_prep_kernel(ScanA
     PrepLds<OP, DKP> &s = *reinterpret_cast<PrepLds<OP, DKP> *>(smem);
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H;
-    const Chunk ch = chunk_of(a, slot);
+    const Chunk ch = prep_chunk<OP, TIn, BWD>(a, slot, h);
     if (ch.rows <= 0)
         return;
-    if (ch.behind)
-        return zero_behind<OP, TIn, BWD>(a, ch, h);
     const Ops<P::NPX, DKP> ops(a, static_cast<long>(slot) * a.H + h);
 
     if (tid < C) {
@@ -403,11 +416,9 @@ __global__ __launch_bounds__(256) void scan_prep_gdn_kernel(ScanArgs a, bool vec
     PrepGdnLds<TIn, DKP> &s = *reinterpret_cast<PrepGdnLds<TIn, DKP> *>(smem);
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H;
-    const Chunk ch = chunk_of(a, slot);
+    const Chunk ch = prep_chunk<GDN, TIn, BWD>(a, slot, h);
     if (ch.rows <= 0)
         return;
-    if (ch.behind)
-        return zero_behind<GDN, TIn, BWD>(a, ch, h);
     const Ops<NP, DKP> ops(a, static_cast<long>(slot) * a.H + h);
 
     // eight elements of a row per thread and turn; rows and keys behind the

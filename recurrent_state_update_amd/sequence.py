@@ -258,8 +258,8 @@ def scan(op: str, q, k, v, beta, log_decay, u=None, initial_state=None, cu_seqle
     (default: zero).
 
     Returns o, shaped as v in the input dtype, and the end states
-    [N,H,d_k,d_v] fp32.  Rows behind the last sequence hold zeros, in o and in
-    the gradients.  d_k, d_v in {16, 32, 64, 128}.
+    [N,H,d_k,d_v] fp32.  Rows ahead of the first sequence and behind the last
+    hold zeros, in o and in the gradients.  d_k, d_v in {16, 32, 64, 128}.
 
     Differentiable by q, k, v, beta, log_decay, u and initial_state.  A forward
     pass that will be differentiated keeps, per 64 tokens and head, the state
