@@ -721,16 +721,24 @@ __global__ __launch_bounds__(DKP * 4, (grad_waves<OP, TIn, DKP>())) void scan_gr
     }
 }
 
-// du: the sum over all chunks, in their order.
+// du: the sum over all chunks, as many as a sequence is long, in 64 bits.  16
+// columns per workgroup, 16 threads each, which take every 16th chunk.
 __global__ inline __launch_bounds__(256) void scan_du_kernel(ScanArgs a)
 {
-    const int i = blockIdx.x * 256 + threadIdx.x, n = a.H * a.dk;
-    if (i >= n)
-        return;
-    float x = 0.f;
-    for (int s = 0; s < a.slots; ++s)
-        x += a.w_du[static_cast<long>(s) * n + i];
-    a.d_u[i] = x;
+    __shared__ double part[16][17];
+    const int c = threadIdx.x % 16, first = threadIdx.x / 16, i = blockIdx.x * 16 + c, n = a.H * a.dk;
+    double x = 0.;
+    if (i < n)
+#pragma unroll 4
+        for (int s = first; s < a.slots; s += 16)
+            x += a.w_du[static_cast<long>(s) * n + i];
+    part[first][c] = x;
+    __syncthreads();
+    if (first == 0 && i < n) {
+        for (int t = 1; t < 16; ++t)
+            x += part[t][c];
+        a.d_u[i] = static_cast<float>(x);
+    }
 }
 
 } // namespace dl

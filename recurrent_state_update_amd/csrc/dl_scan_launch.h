@@ -126,7 +126,7 @@ template <int OP, typename TIn, int DKP> hipError_t scan_backward_t(const ScanAr
     if (hipError_t e = hipGetLastError(); e != hipSuccess)
         return e;
     if (OP == RWKV6) {
-        hipLaunchKernelGGL(scan_du_kernel, dim3((a.H * a.dk + 255) / 256), dim3(256), 0, st, a);
+        hipLaunchKernelGGL(scan_du_kernel, dim3((a.H * a.dk + 15) / 16), dim3(256), 0, st, a);
         return hipGetLastError();
     }
     return hipSuccess;

@@ -107,3 +107,25 @@ def test_gradient_of_a_query(op, dtype, dk):
     do[3] = 0.5 + torch.rand(H, 16, generator=g)
     got, want = both_ways(op, x, DT[dtype], do)
     close(got[3], want[3], 4 + 6 + 32 + 1, dtype)
+
+
+@needs_gpu
+@both
+def test_gradient_of_u_over_many_chunks(dtype):
+    """A large chunk and 69 others of 2^-24 of it each, behind it and before:
+    du = sum_t q k (dO.v), which no decay enters.  One rounding to fp32."""
+    import recurrent_state_update_amd as rsu
+    T, H, d = 70 * 64, 2, 16
+    x = zeros("rwkv6", T, H, d, d)
+    x["q"] += 1
+    x["k"] += 1
+    x["v"][:, :, 0] = 1
+    do = torch.zeros(T, H, d)
+    do[5::64, :, 0] = 1
+    do[5, 0, 0] = do[-59, 1, 0] = 2.0 ** 24
+    x = {n: None if t is None else (t.to(DT[dtype]) if n in "qkv" else t).cuda() for n, t in x.items()}
+    u = x["u"].requires_grad_()
+    o, _ = rsu.scan("rwkv6", x["q"], x["k"], x["v"], None, x["log_decay"], u)
+    (du,) = torch.autograd.grad(o, u, do.to(DT[dtype]).cuda())
+    want = do.double().sum((0, 2)).view(H, 1).expand(H, d)
+    assert far(du, want) <= 2.0 ** -24
