@@ -320,9 +320,8 @@ template <int N, int ROWS, int K, Part PART = ALL, typename F> __device__ __forc
 // blocks above it are zero beforehand): the four diagonal blocks by
 // forward substitution, wave w taking block w, one column per lane; then
 // N_IJ = -N_II sum_{J <= K < I} L_IK N_KJ by block diagonals on the fp32
-// matrix instructions.  tmp: 16 x 16 floats of this wave's own.  For whole
-// workgroups of four waves or more.
-__device__ __forceinline__ void invert_unit_lower(const float *L, float *N, float *tmp, int w, int lane)
+// matrix instructions.  For whole workgroups of four waves or more.
+__device__ __forceinline__ void invert_unit_lower(const float *L, float *N, int w, int lane)
 {
     if (w < 4 && lane < 16) {
         float x[16];
@@ -356,12 +355,8 @@ __device__ __forceinline__ void invert_unit_lower(const float *L, float *N, floa
                     x[e] = N[(K * 16 + k0 + e) * MLD + J * 16 + r];
                 t = mfma32x4(*reinterpret_cast<const f32x4 *>(&L[(I * 16 + r) * MLD + K * 16 + k0]), x, t);
             }
-            // through this wave's own scratch into the other operand's
-            // order; one wave's LDS accesses stay in order
-            *reinterpret_cast<f32x4 *>(&tmp[r * 16 + k0]) = t;
-            __builtin_amdgcn_wave_barrier();
-            const f32x4 x = *reinterpret_cast<const f32x4 *>(&tmp[r * 16 + k0]);
-            c = mfma32x4(*reinterpret_cast<const f32x4 *>(&N[(I * 16 + r) * MLD + I * 16 + k0]), x, c);
+            // a product's result is in the second operand's order
+            c = mfma32x4(*reinterpret_cast<const f32x4 *>(&N[(I * 16 + r) * MLD + I * 16 + k0]), t, c);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 N[(I * 16 + k0 + e) * MLD + J * 16 + r] = -c[e];

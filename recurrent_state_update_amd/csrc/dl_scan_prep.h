@@ -90,10 +90,9 @@ __device__ __forceinline__ void zero_above(float *m)
         *reinterpret_cast<f32x4 *>(&m[(I * 16 + (it & 63) / 4) * MLD + J * 16 + it % 4 * 4]) = f32x4{0, 0, 0, 0};
     }
 }
-// From L and B in LDS: B's and N's planes.  tmp: 16 x 16 floats of a wave's own
-// (four waves).
+// From L and B in LDS: B's and N's planes.
 template <int OP, typename TIn, bool BWD, int NP, int DKP>
-__device__ __forceinline__ void store_mats(PrepMats &m, float *tmp, const Ops<NP, DKP> &ops, int w, int lane)
+__device__ __forceinline__ void store_mats(PrepMats &m, const Ops<NP, DKP> &ops, int w, int lane)
 {
     using P = Plan<OP, TIn>;
     if (BWD)
@@ -102,7 +101,7 @@ __device__ __forceinline__ void store_mats(PrepMats &m, float *tmp, const Ops<NP
         store_op<3, C, C, LOWER>(ops.mat(1), [&](int i, int j) { return m.B[i * MLD + j]; });
     if constexpr (P::DELTA) {
         __syncthreads(); // B is read (and zero above the diagonal, as N will be)
-        invert_unit_lower(m.L, m.B, tmp, w, lane);
+        invert_unit_lower(m.L, m.B, w, lane);
         if (BWD)
             store_op<3, C, C, UPPER>(ops.mat(0), [&](int i, int j) { return m.B[j * MLD + i]; });
         else
@@ -388,7 +387,7 @@ __global__ __launch_bounds__(prep_threads<DKP>(), 4) void scan_prep_kernel(ScanA
         put_block(isA ? s.m.L : s.m.B, I, J, lane, v);
     }
     __syncthreads();
-    store_mats<OP, TIn, BWD>(s.m, s.pair[0][w & 3], ops, w, lane);
+    store_mats<OP, TIn, BWD>(s.m, ops, w, lane);
 }
 
 // ---- one decay per row (GDN)
@@ -563,7 +562,7 @@ __global__ __launch_bounds__(256) void scan_prep_gdn_kernel(ScanArgs a, bool vec
         put_block(isA ? s.m.L : s.m.B, I, J, lane, v);
     }
     __syncthreads();
-    store_mats<GDN, TIn, BWD>(s.m, s.diag[w], ops, w, lane);
+    store_mats<GDN, TIn, BWD>(s.m, ops, w, lane);
 }
 
 } // namespace dl
