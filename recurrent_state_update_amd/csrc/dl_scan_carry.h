@@ -512,13 +512,13 @@ __global__ __launch_bounds__(512) void scan_carry_kernel(ScanArgs a)
 #pragma unroll
                 for (int t = 0; t < NC; ++t)
                     last[t] = with_b(last[t], bp[(c + 1) & 1][t]);
-                load_b(c);
+                bf.ready(); // this chunk's, loaded a turn ago, for the next turn
+                load_b(next);
                 store_o(c > 0 ? c - 1 : 0, last);
 #pragma unroll
                 for (int t = 0; t < NC; ++t)
                     last[t] = o[t];
                 qf.ready();
-                bf.ready();
             }
 #pragma unroll
             for (int r = 0; r < RB; ++r)
