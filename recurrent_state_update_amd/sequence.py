@@ -34,6 +34,8 @@ def _on(device, stream):
     belongs to it."""
     if stream is None:
         return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    if not isinstance(stream, int) and getattr(stream, "device", None) != device:
+        raise ValueError(f"stream: want a stream of {device}, got {stream}")
     ctx = contextlib.ExitStack()
     ctx.enter_context(torch.cuda.device(device))
     if isinstance(stream, int):
