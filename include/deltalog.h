@@ -337,8 +337,8 @@ dl_status dl_scan_backward(const dl_scan_desc *d, const void *saved, const void 
  * norm behind the recurrence with its output gate.  o [rows,H,d] in o_dtype
  * (fp32 from dl_decode_step, in_dtype from dl_scan), gate and y [rows,H,d] in
  * dtype, gate rows gate_stride elements apart (0: H*d); weight [d] fp32 or
- * NULL (1).  d in {16, 32, 64, 128}.  y may be o or gate itself where type
- * and layout agree. */
+ * NULL (1).  d in {16, 32, 64, 128}; rows*H*d < 2^33.  y may be o or gate
+ * itself where type and layout agree. */
 dl_status dl_gated_norm(int rows, int H, int d, dl_dtype o_dtype, dl_dtype dtype, const void *o,
                         const void *gate, long long gate_stride, const float *weight, float eps, void *y,
                         void *stream);

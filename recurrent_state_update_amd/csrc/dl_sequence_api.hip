@@ -154,6 +154,10 @@ dl_status launch_scan(const dl_scan_desc *d, bool backward, const dl::ScanArgs &
     return e == hipSuccess ? DL_OK : DL_E_HIP;
 }
 
+// Elements that the gated norm takes, below 2^33.  (rows and H have 31 bits each:
+// their product with d would pass 64.)
+bool gated_size_ok(int rows, int H, int d) { return static_cast<long long>(rows) * H < (1LL << 33) / d; }
+
 constexpr long kNormBlocks = 1024; // of a backward pass: four workgroups per CU, and as many partial sums per column
 
 int gated_blocks(long rows, long H, int d)
@@ -172,7 +176,7 @@ dl_status gated_inputs(int rows, int H, int d, int o_dtype, int dtype, const voi
 {
     if (rows < 0 || H < 1 || !dtype_ok(o_dtype) || !dtype_ok(dtype) || !eps_ok(eps))
         return DL_E_INVALID;
-    if (!dim_ok(d) || static_cast<long long>(rows) * H * d >= (1LL << 33))
+    if (!dim_ok(d) || !gated_size_ok(rows, H, d))
         return DL_E_SHAPE;
     const long long width = static_cast<long long>(H) * d, gs = gate_stride ? gate_stride : width;
     if ((rows > 0 && (!o || !gate)) || gs < width)
@@ -334,7 +338,7 @@ dl_status dl_gated_norm(int rows, int H, int d, dl_dtype o_dtype, dl_dtype dtype
 
 size_t dl_gated_norm_workspace_bytes(int rows, int H, int d)
 {
-    if (rows < 0 || H < 1 || !dim_ok(d))
+    if (rows < 0 || H < 1 || !dim_ok(d) || !gated_size_ok(rows, H, d))
         return 0;
     return up256(static_cast<size_t>(gated_blocks(rows, H, d)) * d * 4);
 }
