@@ -188,15 +188,16 @@ __global__ __launch_bounds__(256) void gated_norm_bwd_kernel(GatedNormArgs a)
 
 // out[j] = the sum over the blocks' rows of partial [blocks][n] (blockIdx.y:
 // the second such pair).  A workgroup takes 16 columns; 16 threads per column
-// take every 16th row, eight loads at a time.
+// take every 16th row, eight loads at a time.  In 64 bits: up to 1024 rows are
+// summed, and the time is the loads'.
 __global__ __launch_bounds__(256) void column_sum_kernel(const float *partial, int blocks, int n, float *out0,
                                                          float *out1)
 {
-    __shared__ float part[16][17];
+    __shared__ double part[16][17];
     const int c = threadIdx.x % 16, s = threadIdx.x / 16, j = blockIdx.x * 16 + c;
     partial += static_cast<long>(blockIdx.y) * blocks * n;
     float *out = blockIdx.y ? out1 : out0;
-    float x = 0.f;
+    double x = 0.;
     if (j < n) {
         int b = s;
         for (; b + 7 * 16 < blocks; b += 8 * 16) {
@@ -216,7 +217,7 @@ __global__ __launch_bounds__(256) void column_sum_kernel(const float *partial, i
     if (s == 0 && j < n) {
         for (int t = 1; t < 16; ++t)
             x += part[t][c];
-        out[j] = x;
+        out[j] = static_cast<float>(x);
     }
 }
 
