@@ -395,7 +395,9 @@ class DeltaLogState:
         of all B; they are copied to the GPU, so not while a graph is
         captured).  The logs of these slots must be empty (a fresh state or
         slot, or after a merge).  A new prompt starts from zero: zero
-        ``base[slot]`` first.  Returns o in the input dtype, shaped as v."""
+        ``base[slot]`` first.  As `step`, it takes its inputs as values, and no
+        gradient flows through it (`scan` is the differentiable form).
+        Returns o in the input dtype, shaped as v."""
         from .sequence import _prefill
         return _prefill(self, q, k, v, beta, log_decay, cu_seqlens, slots, stream)
 
