@@ -93,14 +93,19 @@ constexpr int scan_keys(int dk) { return dk < 32 ? 32 : dk; }
 // one plane where they are bf16; the others carry fp32 decays.
 constexpr int scan_planes(int op, int dtype) { return op == GDN && dtype == BF16 ? 1 : 3; }
 // Chunks per segment where the carries cut their sequences (dl_scan_carry.h),
-// 0 where they do not.  Uncut, a sequence's chunks are one chain, of 1.6 us each
+// 0 where they do not.  Uncut, a sequence's chunks are one chain, of 1.8 us each
 // (GDN, d = 128); cut, it is two chains of a segment's length and a join per
 // segment, and about three times the work: worth it where a quarter of the CUs or
-// fewer have a tile and the chain is long (1600 tokens, 1 head GDN 58 -> 49 us, 4
-// heads 59 -> 57, 8 heads 58 -> 60; RWKV6 54 -> 49, 54 -> 56, 55 -> 56; 2000
-// tokens, d = 64, 8 heads 49 -> 44 and 36 -> 35).  As many segments as give every
-// CU a tile, and no more than balance the joins (twice as many: 8192 tokens, 1
-// head 90 -> 105 us).
+// fewer have a tile and the chain is long.  us, uncut -> cut, of a forward scan:
+//   tokens, heads   1100, 1   1100, 8   1600, 1   1600, 8   1900, 1   1900, 8
+//   GDN             46 -> 43  46 -> 51  58 -> 48  59 -> 59  67 -> 49  68 -> 62
+//   KDA             72 -> 59  71 -> 71  92 -> 64  92 -> 83  105 -> 68 106 -> 90
+//   RWKV6           47 -> 43  47 -> 48  61 -> 48  59 -> 55  69 -> 49  69 -> 58
+// (d = 64, 2000 tokens, 8 heads: 52 -> 42, 74 -> 51, 40 -> 35.  The host takes
+// 10 us more for the two launches more in either direction, which is all that
+// a training step of these shows.)  As many segments as give every CU a tile, and
+// no more than balance the joins (twice as many: GDN, 8192 tokens, 1 head
+// 88 -> 124 us).
 constexpr long kCus = 256;
 constexpr long scan_segment(long tokens, long seqs, long H, int dv)
 {

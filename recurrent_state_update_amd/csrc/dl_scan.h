@@ -24,9 +24,10 @@
 //   dQ~ = dO S^T, dK~ = -z S^T, dK^ = b dS'^T, dB = dO b^T, dA = -z b^T,
 // from which dq, dk and the log-decay's gradient follow within the chunk.
 //
-// Every decay is a product of factors e_m in [0, 1], never a quotient and
-// never the exponential of a difference of two cumulative sums: full
-// forgetting (e = 0) and any strong decay are exact and cannot overflow.
+// Every decay is a product of factors e_m in [0, 1] (prep divides one by its
+// block's, where that is far from underflow) and never the exponential of a
+// difference of two cumulative sums: full forgetting (e = 0) and strong decays
+// neither overflow nor lose what they multiply.
 //
 // Kernels: prep (per chunk and head: the scaled operands, B and N, in the matrix
 // instruction's own register order); the forward carry and the backward carry

@@ -176,8 +176,8 @@ template <typename TIn> struct ChunkRows {
 };
 
 // What only the backward pass reads, stored past the caches, where it would push
-// out the operands that the value tiles share (4096 tokens, 32 heads, GDN: 174
-// -> 151 us.  The same for dS' and z, which the next kernel reads: no change).
+// out the operands that the value tiles share (4096 tokens, 32 heads, GDN: 203
+// -> 172 us.  The same for dS' and z, which the next kernel reads: no change).
 __device__ __forceinline__ void keep_for_backward(float *p, float x) { __builtin_nontemporal_store(x, p); }
 
 // Long sequences with few heads leave most CUs idle while their chunks pass one
@@ -192,13 +192,13 @@ __device__ __forceinline__ void keep_for_backward(float *p, float x) { __builtin
 // and the same backward, for the gradients of the end states.
 // A whole forward scan, d = 128, bf16, us (uncut, cut):
 //   tokens, heads   2600, 1     2600, 8     8192, 1     8192, 8     32768, 4
-//   GDN             84.5, 59.8  86.7, 82.7  221, 90     235, 160    876, 310
-//   KDA             116, 72.4   123, 116    306, 110    342, 253    1546, 543
-//   RWKV6           77.8, 56.5  83.2, 72.0  203, 87     228, 148    1081, 324
-// forward and backward (below 200 the host is the longer):
-//   GDN             224, 194    248, 229    564, 223    695, 534    2413, 1025
-//   KDA             295, 202    353, 342    749, 271    1025, 851   3706, 1712
-//   RWKV6           204, 195    249, 230    500, 244    733, 545    2640, 1189
+//   GDN             86.4, 56.5  89.8, 83.8  232, 88     246, 159    920, 306
+//   KDA             136, 75.2   140, 116    372, 114    402, 262    1636, 551
+//   RWKV6           89.3, 56.7  91.4, 74.5  240, 88     258, 150    1130, 323
+// forward and backward (below 210 the host is the longer):
+//   GDN             234, 206    260, 230    597, 222    746, 541    2600, 1051
+//   KDA             317, 206    373, 340    816, 273    1097, 863   3989, 1745
+//   RWKV6           198, 204    237, 211    483, 208    713, 504    2469, 1025
 // A segment's slot is found as a chunk's: sequence n's first is
 // start / (64 a.seg) + n; a sequence without tokens has one too.
 struct Segment {

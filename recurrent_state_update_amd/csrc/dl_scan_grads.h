@@ -76,7 +76,9 @@ template <int OP, typename TIn, int DKP> struct GradLds {
 __device__ __forceinline__ void formed(float &x) { asm volatile("" : "+v"(x)); }
 
 // Waves to a SIMD that the registers are held to: two workgroups on a CU where
-// LDS allows them.
+// LDS allows them (GDN, d_k = 128, bf16: 128 registers and 24 bytes a lane in
+// scratch, 217 us of a training step over 4096 tokens, 32 heads; with 140 and one
+// workgroup 283).
 template <int OP, typename TIn, int DKP> constexpr int grad_waves()
 {
     return OP == GDN && sizeof(TIn) == 2 ? (DKP == 128 ? 4 : 3) : 2;

@@ -56,15 +56,22 @@ inline dim3 carry_grid(long groups, int tiles) { return dim3((groups + kXcds - 1
 // Value tiles of 32 columns instead of 16 where those of 16 are more than the
 // CUs: a workgroup is bound by its own chunk's chain, so while each has a CU to
 // itself more of them are faster, and beyond that the operands, read half as
-// often, count.  Forward, 1024 tokens, bf16, d = 128, us (16 columns, 32):
+// often, count.  Forward carry, 1024 tokens, bf16, d = 128, us (16 columns, 32):
 //   heads            32 (256 tiles)   48 (384)        64 (512)
-//   GDN              32.8, 45.0       61.8, 47.1      64.8, 49.2
-//   KDA              46.3, 59.6       86.1, 62.5      91.0, 65.7
-//   RWKV6            29.6, 36.0                       45.3, 40.0
-// (backward, 36 heads: GDN 77.5, 56.8, KDA 106.6, 76.6; d = 64, 96 heads: GDN
-// 68.4, 60.4, RWKV6 43.3, 36.4).  Packed sequences count half: their lengths,
-// not known here, differ, and the long ones are left with the GPU (a KDA
-// training step over 1000, 17 and 911 tokens, 16 heads: 259 us, and 273 wide).
+//   GDN              36.2, 48.9       64.3, 49.8      63.9, 51.6
+//   KDA              58.5, 70.5       98.4, 70.6      97.1, 70.0
+//   RWKV6            35.2, 42.2       62.3, 42.3      62.2, 42.8
+// (backward, 36 heads: 82.2, 61.2; 107, 76.3; 49.6, 44.2; d = 64, 96 heads: 72.5,
+// 62.8; 83.2, 63.8; 38.3, 33.7).  Packed sequences count half: where their
+// lengths, not known here, differ, the short ones' tiles end early, and the
+// long ones are left alone with the GPU.  A whole forward scan of 288 to 480 tiles:
+//   tokens of each   3 x 1024 (16 heads)  82, 1605, 1312 (16)  3000, 40 (20)
+//   GDN              82.7, 67.2           73.0, 92.9           110, 148
+//   tokens of each   3 x 1024 (16)        1950, 876, 172 (16)  3000, 40 (20)
+//   KDA              138, 110             137, 167             183, 232
+// (of 45 packings, those of equal lengths gain up to 23 %, uneven ones lose up to
+// 35 %; with the backward pass 26 and 24 %.  Equal lengths can come as a batch,
+// which does not count half.)
 inline bool wide_tiles(const ScanArgs &a)
 {
     const long tiles = static_cast<long>(a.N) * a.H * (a.dv / 16);
