@@ -14,8 +14,8 @@ pytestmark = pytest.mark.gpu
 needs_gpu = pytest.mark.skipif(not torch.cuda.is_available(), reason="no GPU")
 
 
-def decays(op, kind, g):
-    """A map of log-decays, and the rows to judge apart (None: all as one)."""
+def decays(kind):
+    """A map of log-decays, and the rows to compare apart (none: all as one)."""
     strong = {}
 
     def change(ld, g):
@@ -50,7 +50,7 @@ def worst(got, want, rows):
                          ids=["32-f32", "128-f32", "128-bf16"])
 @pytest.mark.parametrize("kind", [-8.0, -12.0, -16.0, "channels", "rows", "blocks"])
 def test_channels(op, dk, dtype, kind):
-    change, strong = decays(op, kind, None)
+    change, strong = decays(kind)
     x, cu, do, ds = inputs(op, [150, 70], 3, dk, 32, dtype, seed=11, decay=change)
     got, want = gpu_run(op, x, cu, do, ds)["dlog_decay"], ref_run(op, x, cu, do, ds)["dlog_decay"]
     rows = strong.get("rows")
