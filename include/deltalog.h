@@ -368,6 +368,102 @@ dl_status dl_residual_norm_backward(int rows, int D, dl_dtype dtype, const float
                                     const float *d_x_out, const void *d_h, float *d_x, void *d_y,
                                     float *d_scale, float *d_weight, void *workspace, void *stream);
 
+/* ------------------------------------------------------------------------
+ * State space layers: the short causal convolution in front of a recurrence
+ * (of GDN and KDA layers, on q, k and v, as of state space ones), the selective
+ * state space scan, both also for one token of each of many requests, and the
+ * residual norm with an output in 8 bits.  Everything said above of the sequence
+ * operators holds for them too: packed sequences, streams, graphs, errors, and
+ * rows ahead of the first sequence and behind the last, which belong to none
+ * and are zero in every output.
+ * ------------------------------------------------------------------------ */
+
+/* tokens rows of `channels` elements of all sequences, packed as for dl_scan
+ * (cu_seqlens [seqs + 1], or NULL: equal lengths); rows of x x_stride elements
+ * apart (0: channels).  weight [channels, taps] fp32, the oldest token's tap
+ * first; bias [channels] fp32 or NULL (0); silu: y = s sigmoid(s), else y = s. */
+typedef struct {
+    int dtype; /* a dl_dtype: x's and y's, and the states' */
+    int tokens, seqs, channels, taps, silu;
+    long long x_stride;
+    const int *cu_seqlens;
+    const void *x;
+    const float *weight, *bias;
+} dl_conv_desc;
+
+/* s_t = bias + sum_j weight[.][j] x_{t-taps+1+j} per channel, x ahead of a sequence
+ * being its row of `initial` [seqs, taps - 1, channels] (its last inputs, the oldest
+ * first; NULL: zero).  y [tokens, channels] contiguous; final_state (NULL: not
+ * wanted) as initial, for what follows.  Nothing may overlap what is written.
+ * Sizes: 2 <= taps <= 4, channels <= 2^20, tokens and seqs <= 2^30,
+ * (tokens + seqs) * channels < 2^34. */
+dl_status dl_short_conv(const dl_conv_desc *d, const void *initial, void *final_state, void *y, void *stream);
+/* Its gradients from dy [tokens, channels] and d_final (as final_state; either
+ * NULL: zero): dx (contiguous), dweight, dbias (NULL: not wanted; else the
+ * workspace is needed, 256-byte aligned), d_initial (NULL: not wanted). */
+size_t dl_short_conv_workspace_bytes(const dl_conv_desc *d);
+dl_status dl_short_conv_backward(const dl_conv_desc *d, const void *initial, const void *dy, const void *d_final,
+                                 void *dx, float *dweight, float *dbias, void *d_initial, void *workspace,
+                                 void *stream);
+/* One token of each of `tokens` requests (seqs and cu_seqlens are not read,
+ * seqs >= 1): request t's state is row state_rows[t] (NULL: row t) of `state`
+ * [n_state_rows, taps - 1, channels], which is moved on in place; no row twice.  A
+ * row out of range (a padded batch's) is not read (zero) nor written. */
+dl_status dl_short_conv_step(const dl_conv_desc *d, void *state, const int *state_rows, int n_state_rows, void *y,
+                             void *stream);
+
+/* Per channel c and state n, with delta = softplus(dt + dt_bias) (softplus 0: their
+ * sum) and group g = c / (channels / groups):
+ *   h = exp(delta a[c][n]) h + delta x b[g][n];  y = (sum_n c[g][n] h + d x) z sigmoid(z)
+ * x, dt, z (NULL: no gate) [tokens, channels], b, c [tokens, groups, states] in
+ * dtype, their rows *_stride elements apart (0: contiguous; a row's groups are);
+ * a [channels, states], d (NULL: 0), dt_bias (NULL: 0) [channels] fp32. */
+typedef struct {
+    int dtype; /* a dl_dtype */
+    int tokens, seqs, channels, states, groups, softplus;
+    long long x_stride, dt_stride, z_stride, b_stride, c_stride;
+    const int *cu_seqlens;
+    const void *x, *dt, *z, *b, *c;
+    const float *a, *d, *dt_bias;
+} dl_ssm_desc;
+
+/* Device bytes of the scan's workspace, of the `saved` buffer that a backward pass
+ * needs (the state ahead of every 16 tokens), and of the backward pass's
+ * workspace, each 256-byte aligned; 0 for sizes that are not supported: 1 <=
+ * states <= 64, channels a multiple of groups, channels <= 2^20, tokens and seqs
+ * <= 2^30, (seqs + tokens/64) * channels/16 < 2^24 (channels rounded up to
+ * sixteens per group), tokens * groups * states < 2^31. */
+size_t dl_ssm_workspace_bytes(const dl_ssm_desc *d);
+size_t dl_ssm_saved_bytes(const dl_ssm_desc *d);
+size_t dl_ssm_backward_workspace_bytes(const dl_ssm_desc *d);
+
+/* initial, final_state: fp32 [seqs, channels, states] (NULL: zero; not wanted); y
+ * [tokens, channels] contiguous; saved NULL: no backward pass will follow.
+ * Nothing may overlap what is written. */
+dl_status dl_ssm_scan(const dl_ssm_desc *d, const float *initial, float *final_state, void *y, void *saved,
+                      void *workspace, void *stream);
+/* From dy [tokens, channels] and d_final (NULL: zero) the gradients dx, ddt, dz
+ * (NULL without z), db, dc (dtype, contiguous), da, dd, ddt_bias, d_initial (fp32;
+ * the latter three NULL: not wanted, dd and ddt_bias only where d and dt_bias are
+ * given). */
+dl_status dl_ssm_scan_backward(const dl_ssm_desc *d, const void *saved, const void *dy, const float *d_final,
+                               void *dx, void *ddt, void *dz, void *db, void *dc, float *da, float *dd,
+                               float *ddt_bias, float *d_initial, void *workspace, void *stream);
+/* One token of each of `tokens` requests, rows of `state` [n_state_rows, channels,
+ * states] fp32 as for dl_short_conv_step; tokens * channels < 2^28. */
+dl_status dl_ssm_step(const dl_ssm_desc *d, float *state, const int *state_rows, int n_state_rows, void *y,
+                      void *stream);
+
+/* dl_residual_norm with h in 8 bits (e4m3: 4 exponent and 3 mantissa bits, largest
+ * 448): rms(x_out) weight = h h_scale, h_scale such that the largest of a row (group
+ * 0, h_scale [rows]) or of every 128 columns (group 128, h_scale [rows, D / 128])
+ * is 448.  Rows and groups of zeros have a scale too (tiny, above zero); a row with
+ * a NaN has NaN scales, one with an infinity a NaN scale where that is.  dtype is
+ * y's.  h [rows, D]; with group 128, x, y, x_out and h are 16-byte aligned. */
+dl_status dl_residual_norm_quant(int rows, int D, dl_dtype dtype, const float *x, const void *y, const float *scale,
+                               const float *weight, float eps, float *x_out, int group, void *h, float *h_scale,
+                               void *stream);
+
 /* Static description of a status code (never NULL; owned by the library). */
 const char *dl_status_string(dl_status st);
 

@@ -35,7 +35,10 @@ EXPORTS = ("dl_workspace_bytes", "dl_state_create", "dl_decode_step", "dl_replay
            "dl_scan_workspace_bytes", "dl_scan_saved_bytes", "dl_scan_backward_workspace_bytes",
            "dl_scan", "dl_scan_backward", "dl_gated_norm_workspace_bytes", "dl_gated_norm",
            "dl_gated_norm_backward", "dl_residual_norm_workspace_bytes", "dl_residual_norm",
-           "dl_residual_norm_backward")
+           "dl_residual_norm_backward", "dl_short_conv_workspace_bytes", "dl_short_conv",
+           "dl_short_conv_backward", "dl_short_conv_step", "dl_ssm_workspace_bytes", "dl_ssm_saved_bytes",
+           "dl_ssm_backward_workspace_bytes", "dl_ssm_scan", "dl_ssm_scan_backward", "dl_ssm_step",
+           "dl_residual_norm_quant")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built; run `python recurrent_state_update_amd/_build.py` "
@@ -53,7 +56,22 @@ class dl_scan_desc(ctypes.Structure):
                 ("q", _p), ("k", _p), ("v", _p), ("beta", _p), ("log_decay", _p), ("u", _p)]
 
 
+class dl_conv_desc(ctypes.Structure):
+    """The rows of one short convolution (include/deltalog.h)."""
+    _fields_ = [("dtype", _i), ("tokens", _i), ("seqs", _i), ("channels", _i), ("taps", _i), ("silu", _i),
+                ("x_stride", _l), ("cu_seqlens", _p), ("x", _p), ("weight", _p), ("bias", _p)]
+
+
+class dl_ssm_desc(ctypes.Structure):
+    """The rows of one selective scan (include/deltalog.h)."""
+    _fields_ = [("dtype", _i), ("tokens", _i), ("seqs", _i), ("channels", _i), ("states", _i), ("groups", _i),
+                ("softplus", _i), ("x_stride", _l), ("dt_stride", _l), ("z_stride", _l), ("b_stride", _l),
+                ("c_stride", _l), ("cu_seqlens", _p), ("x", _p), ("dt", _p), ("z", _p), ("b", _p), ("c", _p),
+                ("a", _p), ("d", _p), ("dt_bias", _p)]
+
+
 _desc = ctypes.POINTER(dl_scan_desc)
+_conv, _ssm = ctypes.POINTER(dl_conv_desc), ctypes.POINTER(dl_ssm_desc)
 
 _SIG = {
     "dl_workspace_bytes": ([_i] * 7, _sz),
@@ -87,6 +105,17 @@ _SIG = {
     "dl_residual_norm_workspace_bytes": ([_i] * 2, _sz),
     "dl_residual_norm": ([_i] * 3 + [_p] * 4 + [_fl] + [_p] * 3, _i),
     "dl_residual_norm_backward": ([_i] * 3 + [_p] * 4 + [_fl] + [_p] * 8, _i),
+    "dl_short_conv": ([_conv] + [_p] * 4, _i),
+    "dl_short_conv_workspace_bytes": ([_conv], _sz),
+    "dl_short_conv_backward": ([_conv] + [_p] * 9, _i),
+    "dl_short_conv_step": ([_conv, _p, _p, _i, _p, _p], _i),
+    "dl_ssm_workspace_bytes": ([_ssm], _sz),
+    "dl_ssm_saved_bytes": ([_ssm], _sz),
+    "dl_ssm_backward_workspace_bytes": ([_ssm], _sz),
+    "dl_ssm_scan": ([_ssm] + [_p] * 6, _i),
+    "dl_ssm_scan_backward": ([_ssm] + [_p] * 14, _i),
+    "dl_ssm_step": ([_ssm, _p, _p, _i, _p, _p], _i),
+    "dl_residual_norm_quant": ([_i] * 3 + [_p] * 4 + [_fl, _p, _i] + [_p] * 3, _i),
 }
 for _name, (_args, _res) in _SIG.items():
     _f = getattr(_lib, _name)
@@ -272,6 +301,59 @@ def dl_residual_norm_backward(rows, D, dtype, x_out, y, scale, weight, eps, d_x_
     return _lib.dl_residual_norm_backward(rows, D, dtype, _ptr(x_out), _ptr(y), _ptr(scale), _ptr(weight), eps,
                                           _ptr(d_x_out), _ptr(d_h), _ptr(d_x), _ptr(d_y), _ptr(d_scale),
                                           _ptr(d_weight), _ptr(workspace), _stream(stream))
+
+
+def dl_short_conv(desc, initial, final_state, y, stream=None):
+    return _lib.dl_short_conv(ctypes.byref(desc), _ptr(initial), _ptr(final_state), _ptr(y), _stream(stream))
+
+
+def dl_short_conv_workspace_bytes(desc) -> int:
+    return int(_lib.dl_short_conv_workspace_bytes(ctypes.byref(desc)))
+
+
+def dl_short_conv_backward(desc, initial, dy, d_final, dx, dweight, dbias, d_initial, workspace, stream=None):
+    return _lib.dl_short_conv_backward(ctypes.byref(desc), _ptr(initial), _ptr(dy), _ptr(d_final), _ptr(dx),
+                                       _ptr(dweight), _ptr(dbias), _ptr(d_initial), _ptr(workspace),
+                                       _stream(stream))
+
+
+def dl_short_conv_step(desc, state, state_rows, n_state_rows, y, stream=None):
+    return _lib.dl_short_conv_step(ctypes.byref(desc), _ptr(state), _ptr(state_rows), n_state_rows, _ptr(y),
+                                   _stream(stream))
+
+
+def dl_ssm_workspace_bytes(desc) -> int:
+    return int(_lib.dl_ssm_workspace_bytes(ctypes.byref(desc)))
+
+
+def dl_ssm_saved_bytes(desc) -> int:
+    return int(_lib.dl_ssm_saved_bytes(ctypes.byref(desc)))
+
+
+def dl_ssm_backward_workspace_bytes(desc) -> int:
+    return int(_lib.dl_ssm_backward_workspace_bytes(ctypes.byref(desc)))
+
+
+def dl_ssm_scan(desc, initial, final_state, y, saved, workspace, stream=None):
+    return _lib.dl_ssm_scan(ctypes.byref(desc), _ptr(initial), _ptr(final_state), _ptr(y), _ptr(saved),
+                            _ptr(workspace), _stream(stream))
+
+
+def dl_ssm_scan_backward(desc, saved, dy, d_final, dx, ddt, dz, db, dc, da, dd, ddt_bias, d_initial, workspace,
+                         stream=None):
+    return _lib.dl_ssm_scan_backward(ctypes.byref(desc), _ptr(saved), _ptr(dy), _ptr(d_final), _ptr(dx), _ptr(ddt),
+                                     _ptr(dz), _ptr(db), _ptr(dc), _ptr(da), _ptr(dd), _ptr(ddt_bias),
+                                     _ptr(d_initial), _ptr(workspace), _stream(stream))
+
+
+def dl_ssm_step(desc, state, state_rows, n_state_rows, y, stream=None):
+    return _lib.dl_ssm_step(ctypes.byref(desc), _ptr(state), _ptr(state_rows), n_state_rows, _ptr(y),
+                            _stream(stream))
+
+
+def dl_residual_norm_quant(rows, D, dtype, x, y, scale, weight, eps, x_out, group, h, h_scale, stream=None):
+    return _lib.dl_residual_norm_quant(rows, D, dtype, _ptr(x), _ptr(y), _ptr(scale), _ptr(weight), eps, _ptr(x_out),
+                                     group, _ptr(h), _ptr(h_scale), _stream(stream))
 
 
 def dl_status_string(st) -> str:
@@ -462,4 +544,5 @@ def eager_step(op: str, S, q, k, v, beta, log_decay, u=None, o=None, stream=None
     return o
 
 
-from .sequence import gated_norm, residual_norm, scan  # noqa: E402,F401
+from .sequence import gated_norm, residual_norm, residual_norm_fp8, scan  # noqa: E402,F401
+from .state_space import short_conv, short_conv_step, ssm_scan, ssm_step  # noqa: E402,F401

@@ -1,0 +1,420 @@
+// dl_conv.hip -- the short causal convolution in front of a recurrence, forward,
+// backward and for single tokens.  Per channel, with W taps, x_{-1}, x_{-2}, ...
+// of a sequence being its initial state's last rows (or zero):
+//   s_t = bias + sum_j w_j x_{t-W+1+j},   y_t = s_t sigmoid(s_t)  (or s_t)
+//   ds = dy silu'(s),  dx_t = sum_k w_{W-1-k} ds_{t+k},
+//   dw_j = sum_t ds_t x_{t-W+1+j},  dbias = sum_t ds_t
+// A few operations per byte, bound by HBM: a lane walks down a run of tokens with
+// a few channels (one vector load and store a token), the last W - 1 inputs and
+// the weights in registers, and re-reads the W - 1 tokens ahead of its run
+// (backward: behind it).
+#include "dl_vec.h"
+
+#include "dl_internal.h"
+#include "dl_sequences.h"
+
+namespace dl {
+
+namespace {
+
+constexpr int NT = 256;
+
+// What a lane works on: channels c ... c + V - 1 (m of them there), and a walk over
+// tokens in ascending order that knows each one's sequence.
+template <typename T, int W, int V> struct Lane {
+    const ConvArgs &a;
+    const Sequences seqs;
+    const int c, m;
+    float w[W][V], bias[V];
+    float x[W][V]; // x[W - 1]: the token's own, x[W - 1 - k]: k tokens back
+    int n, start, end;
+
+    __device__ __forceinline__ Lane(const ConvArgs &a, int c)
+        : a(a), seqs{a.cu, a.T, a.N}, c(c), m(min(V, a.C - c))
+    {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            bias[i] = a.bias && i < m ? a.bias[c + i] : 0.f;
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                w[j][i] = i < m ? a.weight[static_cast<long>(c + i) * W + j] : 0.f;
+        }
+    }
+    __device__ __forceinline__ void row(float (&out)[V], const void *base, long at) const
+    {
+        Cells<V, T> r;
+        r.load(static_cast<const T *>(base) + at + c, m, a.vec);
+        r.get(out);
+    }
+    // row j of sequence n's initial state
+    __device__ __forceinline__ void initial(float (&out)[V], int j) const
+    {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            out[i] = 0.f;
+        if (a.init)
+            row(out, a.init, (static_cast<long>(n) * (W - 1) + j) * a.C);
+    }
+    __device__ __forceinline__ void sequence(int k)
+    {
+        n = k;
+        start = seqs.at(k);
+        end = seqs.at(k + 1);
+    }
+    // The sequence of token t, and the tokens ahead of it.
+    __device__ __forceinline__ void begin(int t)
+    {
+        sequence(seqs.of_token(t));
+        if (t != start)
+            window(t);
+    }
+    __device__ __forceinline__ void window(int t)
+    {
+#pragma unroll
+        for (int k = 1; k < W; ++k) {
+            const int pos = t - start;
+            if (pos >= k)
+                row(x[W - 1 - k], a.x, (t - k) * a.xs);
+            else if (pos >= 0)
+                initial(x[W - 1 - k], W - 1 - k + pos);
+            else
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    x[W - 1 - k][i] = 0.f;
+        }
+    }
+    // Goes on to token t, the next one; whether it is a sequence's.
+    __device__ __forceinline__ bool enter(int t)
+    {
+        while (t >= end && n + 1 < a.N)
+            sequence(n + 1);
+        if (t == start)
+            window(t);
+        return t >= start && t < end;
+    }
+    __device__ __forceinline__ void sums(float (&s)[V]) const
+    {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            s[i] = bias[i];
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                s[i] = fmaf(w[j][i], x[j][i], s[i]);
+        }
+    }
+    __device__ __forceinline__ void leave() // the token joins those behind it
+    {
+#pragma unroll
+        for (int j = 0; j + 1 < W; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                x[j][i] = x[j + 1][i];
+    }
+    // ds of the token from dy
+    __device__ __forceinline__ void slope(float (&ds)[V], const float (&dy)[V]) const
+    {
+        float s[V];
+        sums(s);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float sig = 1.f / (1.f + expf(-s[i]));
+            ds[i] = a.silu ? dy[i] * sig * fmaf(s[i], 1.f - sig, 1.f) : dy[i];
+        }
+    }
+};
+
+// Units of V channels: first `runs` runs of tokens, then (fin) the N end states.
+template <typename T, int W, int V> __global__ __launch_bounds__(NT) void conv_kernel(ConvArgs a)
+{
+    constexpr int U = 4; // tokens loaded ahead
+    const long unit = static_cast<long>(blockIdx.x) * NT + threadIdx.x;
+    const int groups = (a.C + V - 1) / V, run = unit / groups, c = unit % groups * V;
+    if (run >= a.runs) {
+        const int n = run - a.runs;
+        if (n >= a.N || !a.fin)
+            return;
+        const Sequences seqs{a.cu, a.T, a.N};
+        const int start = seqs.at(n), end = max(start, seqs.at(n + 1)), m = min(V, a.C - c);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+            const int pos = end - start - (W - 1) + j;
+            Cells<V, T> r;
+            if (pos >= 0)
+                r.load(static_cast<const T *>(a.x) + (start + pos) * a.xs + c, m, a.vec);
+            else if (a.init)
+                r.load(static_cast<const T *>(a.init) + (static_cast<long>(n) * (W - 1) + pos + W - 1) * a.C + c, m, a.vec);
+            else
+                r.load(nullptr, 0, false);
+            r.store(static_cast<T *>(a.fin) + (static_cast<long>(n) * (W - 1) + j) * a.C + c, m, a.vec);
+        }
+        return;
+    }
+    const int t0 = run * a.run, t1 = min(t0 + a.run, a.T);
+    if (t0 >= t1)
+        return;
+    Lane<T, W, V> l(a, c);
+    Cells<V, T> next[U];
+    const auto read = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (t + i < t1)
+                next[i].load(static_cast<const T *>(a.x) + (t + i) * a.xs + c, l.m, a.vec);
+    };
+    read(t0);
+    l.begin(t0);
+    for (int t = t0; t < t1; t += U) {
+        Cells<V, T> now[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            now[i] = next[i];
+        read(t + U);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (t + i >= t1)
+                break;
+            const bool live = l.enter(t + i);
+            now[i].get(l.x[W - 1]);
+            float s[V];
+            l.sums(s);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                if (a.silu)
+                    s[e] = s[e] / (1.f + expf(-s[e]));
+                s[e] = live ? s[e] : 0.f;
+            }
+            Cells<V, T> y;
+            y.put(s);
+            y.store(static_cast<T *>(a.y) + static_cast<long>(t + i) * a.C + c, l.m, a.vec);
+            l.leave();
+        }
+    }
+}
+
+// Runs as above; then the N initial states' gradients.  dx of a token is done W - 1
+// tokens behind it, or at its sequence's end: g[k] is what is gathered of that k
+// tokens back.
+template <typename T, int W, int V> __global__ __launch_bounds__(NT) void conv_bwd_kernel(ConvArgs a)
+{
+    const long unit = static_cast<long>(blockIdx.x) * NT + threadIdx.x;
+    const int groups = (a.C + V - 1) / V, run = unit / groups, c = unit % groups * V;
+    if (run >= a.runs + (a.dinit ? a.N : 0))
+        return;
+    Lane<T, W, V> l(a, c);
+    const auto add_final = [&](float (&x)[V], int j) { // row j of the end state's gradient
+        float d[V];
+        l.row(d, a.dfin, (static_cast<long>(l.n) * (W - 1) + j) * a.C);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            x[i] += d[i];
+    };
+    if (run >= a.runs) {
+        l.sequence(run - a.runs);
+        const int len = max(l.end - l.start, 0);
+        float d[W - 1][V];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                d[j][i] = 0.f;
+        l.window(l.start);
+#pragma unroll
+        for (int p = 0; p < W - 1; ++p) {
+            if (p >= len)
+                break;
+            float dy[V], ds[V];
+            l.row(l.x[W - 1], a.x, (l.start + p) * a.xs);
+            for (int i = 0; i < V; ++i)
+                dy[i] = 0.f;
+            if (a.dy)
+                l.row(dy, a.dy, static_cast<long>(l.start + p) * a.C);
+            l.slope(ds, dy);
+#pragma unroll
+            for (int j = p; j < W - 1; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    d[j][i] = fmaf(l.w[j - p][i], ds[i], d[j][i]);
+            l.leave();
+        }
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+            if (a.dfin && j >= len)
+                add_final(d[j], j - len);
+            Cells<V, T> r;
+            r.put(d[j]);
+            r.store(static_cast<T *>(a.dinit) + (static_cast<long>(l.n) * (W - 1) + j) * a.C + c, l.m, a.vec);
+        }
+        return;
+    }
+    const int t0 = run * a.run, t1 = min(t0 + a.run, a.T);
+    float g[W][V], dw[W][V], db[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        db[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            g[j][i] = dw[j][i] = 0.f;
+    }
+    const auto done = [&](float (&x)[V], int t) { // token t of the sequence
+        if (t < t0 || t >= t1 || t < l.start)
+            return;
+        if (a.dfin && t >= l.end - (W - 1))
+            add_final(x, t - (l.end - (W - 1)));
+        Cells<V, T> r;
+        r.put(x);
+        r.store(static_cast<T *>(a.dx) + static_cast<long>(t) * a.C + c, l.m, a.vec);
+    };
+    if (t0 < t1) {
+        Cells<V, T> nx, ny;
+        const auto read = [&](int t) {
+            if (t < min(t1 + W - 1, a.T)) {
+                nx.load(static_cast<const T *>(a.x) + t * a.xs + c, l.m, a.vec);
+                if (a.dy)
+                    ny.load(static_cast<const T *>(a.dy) + static_cast<long>(t) * a.C + c, l.m, a.vec);
+            }
+        };
+        read(t0);
+        l.begin(t0);
+        int t = t0;
+        for (; t < t1 + W - 1; ++t) {
+            if (t == l.end) { // behind a sequence's last token: what is gathered is whole
+#pragma unroll
+                for (int k = 1; k < W; ++k) {
+                    done(g[k], t - k);
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        g[k][i] = 0.f;
+                }
+            }
+            if (t >= a.T || (t >= t1 && t >= l.end))
+                break;
+            const bool live = l.enter(t);
+            float dy[V], ds[V];
+            nx.get(l.x[W - 1]);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                dy[i] = 0.f;
+            if (a.dy)
+                ny.get(dy);
+            read(t + 1);
+            if (!live) { // of no sequence
+                if (t < t1) {
+                    Cells<V, T> zero;
+                    zero.load(nullptr, 0, false);
+                    zero.store(static_cast<T *>(a.dx) + static_cast<long>(t) * a.C + c, l.m, a.vec);
+                }
+                continue;
+            }
+            l.slope(ds, dy);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+                    g[k][i] = fmaf(l.w[W - 1 - k][i], ds[i], g[k][i]);
+                if (t < t1) {
+                    db[i] += ds[i];
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        dw[j][i] = fmaf(ds[i], l.x[j][i], dw[j][i]);
+                }
+            }
+            done(g[W - 1], t - (W - 1));
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+#pragma unroll
+                for (int k = W - 1; k > 0; --k)
+                    g[k][i] = g[k - 1][i];
+                g[0][i] = 0.f;
+            }
+            l.leave();
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (i < l.m) {
+            if (a.part_w)
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    a.part_w[(static_cast<long>(run) * a.C + c + i) * W + j] = dw[j][i];
+            if (a.part_b)
+                a.part_b[static_cast<long>(run) * a.C + c + i] = db[i];
+        }
+}
+
+// One token each: state row r = [W - 1][C] moves up by one and takes x.
+template <typename T, int W, int V> __global__ __launch_bounds__(NT) void conv_step_kernel(ConvArgs a)
+{
+    const long unit = static_cast<long>(blockIdx.x) * NT + threadIdx.x;
+    const int groups = (a.C + V - 1) / V, t = unit / groups, c = unit % groups * V;
+    if (t >= a.T)
+        return;
+    Lane<T, W, V> l(a, c);
+    const int r = a.rows ? a.rows[t] : t;
+    const bool known = r >= 0 && r < a.n_rows;
+    T *const state = static_cast<T *>(a.state) + static_cast<long>(r) * (W - 1) * a.C + c;
+    Cells<V, T> seen[W];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+        seen[j].load(state + j * a.C, known ? l.m : 0, a.vec);
+    seen[W - 1].load(static_cast<const T *>(a.x) + t * a.xs + c, l.m, a.vec);
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+        seen[j].get(l.x[j]);
+    float s[V];
+    l.sums(s);
+    if (a.silu)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            s[i] = s[i] / (1.f + expf(-s[i]));
+    Cells<V, T> y;
+    y.put(s);
+    y.store(static_cast<T *>(a.y) + static_cast<long>(t) * a.C + c, l.m, a.vec);
+    if (known)
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+            seen[j + 1].store(state + j * a.C, l.m, a.vec);
+}
+
+enum Kind { FORWARD, BACKWARD, STEP };
+
+template <typename T, int W, int V> hipError_t conv_w(Kind kind, const ConvArgs &a, hipStream_t st)
+{
+    const long groups = (a.C + V - 1) / V;
+    const long units = groups * (kind == STEP ? a.T : a.runs + ((kind == FORWARD ? a.fin : a.dinit) ? a.N : 0));
+    if (units == 0)
+        return hipSuccess;
+    const dim3 grid(static_cast<unsigned>((units + NT - 1) / NT));
+    if (kind == FORWARD)
+        hipLaunchKernelGGL((conv_kernel<T, W, V>), grid, dim3(NT), 0, st, a);
+    else if (kind == BACKWARD)
+        hipLaunchKernelGGL((conv_bwd_kernel<T, W, V>), grid, dim3(NT), 0, st, a);
+    else
+        hipLaunchKernelGGL((conv_step_kernel<T, W, V>), grid, dim3(NT), 0, st, a);
+    return hipGetLastError();
+}
+template <typename T, int V> hipError_t conv_t(Kind kind, const ConvArgs &a, hipStream_t st)
+{
+    return a.W == 2 ? conv_w<T, 2, V>(kind, a, st) : a.W == 3 ? conv_w<T, 3, V>(kind, a, st) : conv_w<T, 4, V>(kind, a, st);
+}
+hipError_t conv(Kind kind, int dtype, const ConvArgs &a, hipStream_t st)
+{
+    static_assert(kConvChannels == 4, "every kernel's");
+    return dtype == F32 ? conv_t<float, kConvChannels>(kind, a, st) : conv_t<__bf16, kConvChannels>(kind, a, st);
+}
+
+} // namespace
+
+hipError_t launch_short_conv(int dtype, const ConvArgs &a, hipStream_t st) { return conv(FORWARD, dtype, a, st); }
+
+hipError_t launch_short_conv_backward(int dtype, const ConvArgs &a, hipStream_t st)
+{
+    hipError_t e = conv(BACKWARD, dtype, a, st);
+    if (e == hipSuccess && a.d_weight)
+        e = column_sum(a.part_w, a.runs, a.C * a.W, a.d_weight, nullptr, st);
+    if (e == hipSuccess && a.d_bias)
+        e = column_sum(a.part_b, a.runs, a.C, a.d_bias, nullptr, st);
+    return e;
+}
+
+hipError_t launch_short_conv_step(int dtype, const ConvArgs &a, hipStream_t st) { return conv(STEP, dtype, a, st); }
+
+} // namespace dl

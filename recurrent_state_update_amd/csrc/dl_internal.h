@@ -164,6 +164,10 @@ hipError_t launch_scan_gdn(int dtype, bool backward, const ScanArgs &a, hipStrea
 hipError_t launch_scan_kda(int dtype, bool backward, const ScanArgs &a, hipStream_t st);
 hipError_t launch_scan_rwkv6(int dtype, bool backward, const ScanArgs &a, hipStream_t st);
 
+// out0[j] = the sum over the rows of partial [blocks][n], in 64 bits and in a fixed
+// order; with out1 the same of a second such array right behind the first (dl_norm.hip).
+hipError_t column_sum(const float *partial, int blocks, int n, float *out0, float *out1, hipStream_t st);
+
 struct GatedNormArgs {
     long units; // rows x H
     int H, d;
@@ -194,5 +198,92 @@ struct ResidualNormArgs {
     int blocks;
 };
 hipError_t launch_residual_norm(int dtype, bool backward, const ResidualNormArgs &a, hipStream_t st);
+
+// ---- state space layers (dl_layer_api.hip; kernels in dl_ssm.h, dl_conv.hip)
+
+constexpr int kSsmBlock = 16;    // tokens between two saved states
+constexpr int kSsmTile = 16;     // channels per workgroup, forward
+constexpr int kSsmGradTile = 64; // and backward
+constexpr int kConvChannels = 4; // per lane
+
+// A sequence's blocks (or segments of `seg` tokens) have slots of their own,
+// found without a table: sequence n's are those from start / seg + n on.
+constexpr long ssm_slots(long tokens, long seqs, long seg) { return tokens / seg + seqs; }
+
+// One scan, forward, backward or of single tokens.  Strides in elements.
+struct SsmArgs {
+    int T, N;       // tokens in all, sequences
+    int C, S, G, CG; // channels, states, groups, channels per group
+    int softplus;
+    const int *cu; // [N + 1] token offsets, or NULL: N equal lengths
+    const void *x, *dt, *z, *b, *c;
+    long xs, dts, zs, bs, cs;
+    const float *A, *D, *dt_bias;
+    bool vec_x, vec_b, vec_s; // rows of channels, of states, of fp32 states are whole vectors
+    const float *init; // [N][C][S], or NULL (zero)
+    float *fin;        // [N][C][S], or NULL
+    void *y;           // [T][C]
+    int seg;           // tokens per segment (a multiple of every stage's), or 0: sequences uncut
+    int slots, tiles;  // pieces (N, or segments' slots), channel tiles
+    // [slots][C][S] a segment's end state from zero and [slots][C] its sum of
+    // delta; backward: the gradient of its start state, from zero behind it
+    float *seg_h, *seg_d;
+    float *saved; // [ssm_slots(T, N, kSsmBlock)][C][S] the state ahead of every block, or NULL
+    // single tokens
+    float *state;    // [n_rows][C][S]
+    const int *rows; // [T], or NULL: row t
+    int n_rows;
+    // backward
+    const void *dy;    // [T][C]
+    const float *dfin; // [N][C][S], or NULL (zero)
+    void *dx, *ddt, *dz, *db, *dc;
+    float *d_A, *d_D, *d_bias, *dinit;
+    float *part_bc;                       // [tiles of a group][T][G][2][S]
+    float *part_a, *part_d, *part_bias;   // [slots][C][S], [slots][C], [slots][C]
+};
+hipError_t launch_ssm_scan(int dtype, const SsmArgs &a, hipStream_t st);
+// The adjoint's segments; `ahead` has the forward kernel's tiles.
+hipError_t launch_ssm_ahead_of_adjoint(int dtype, const SsmArgs &a, hipStream_t st);
+hipError_t launch_ssm_backward(int dtype, const SsmArgs &ahead, const SsmArgs &a, hipStream_t st);
+hipError_t launch_ssm_step(int dtype, const SsmArgs &a, hipStream_t st);
+
+// The short convolution, forward, backward or of single tokens.
+struct ConvArgs {
+    int T, N, C, W, silu;
+    const int *cu;
+    const void *x;
+    long xs;
+    const float *weight, *bias; // [C][W], [C] or NULL
+    bool vec;                   // rows of channels are whole vectors
+    const void *init;           // [N][W - 1][C], or NULL (zero)
+    void *fin;                  // [N][W - 1][C], or NULL
+    void *y;
+    int run, runs; // tokens per thread, such runs
+    // single tokens
+    void *state;
+    const int *rows;
+    int n_rows;
+    // backward
+    const void *dy, *dfin;
+    void *dx, *dinit;
+    float *d_weight, *d_bias;
+    float *part_w, *part_b; // [runs][C][W], [runs][C]
+};
+hipError_t launch_short_conv(int dtype, const ConvArgs &a, hipStream_t st);
+hipError_t launch_short_conv_backward(int dtype, const ConvArgs &a, hipStream_t st);
+hipError_t launch_short_conv_step(int dtype, const ConvArgs &a, hipStream_t st);
+
+struct NormFp8Args {
+    long rows;
+    int D, group; // group: columns per scale, 128 or D
+    const float *x;
+    const void *y;
+    const float *scale, *weight;
+    float eps;
+    float *x_out;
+    unsigned char *h;
+    float *h_scale;
+};
+hipError_t launch_residual_norm_fp8(int dtype, const NormFp8Args &a, hipStream_t st);
 
 } // namespace dl

@@ -9,65 +9,13 @@
 #include <hip/hip_runtime.h>
 
 #include "dl_internal.h"
+#include "dl_vec.h"
 
 namespace dl {
 
 namespace {
 
 constexpr long kForwardBlocks = 2048; // eight per CU: every wave slot, several turns each
-
-template <typename T> __device__ __forceinline__ float to_f(T x) { return static_cast<float>(x); }
-
-// N consecutive elements from p, as floats (and back).  ALIGNED: p is aligned
-// to 16 bytes, or to the N elements where they are fewer.  ONCE: loads that
-// leave the caches to others.
-template <int N, bool ALIGNED, bool ONCE = false, typename T>
-__device__ __forceinline__ void load(float (&x)[N], const T *p)
-{
-    using V = T __attribute__((ext_vector_type(N)));
-    if constexpr (ALIGNED && N > 1) {
-        const V v = ONCE ? __builtin_nontemporal_load(reinterpret_cast<const V *>(p)) : *reinterpret_cast<const V *>(p);
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            x[i] = to_f(v[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            x[i] = to_f(p[i]);
-    }
-}
-template <int N, bool ALIGNED, typename T> __device__ __forceinline__ void store(T *p, const float (&x)[N])
-{
-    using V = T __attribute__((ext_vector_type(N)));
-    if constexpr (ALIGNED && N > 1) {
-        V v;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            v[i] = static_cast<T>(x[i]);
-        *reinterpret_cast<V *>(p) = v;
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            p[i] = static_cast<T>(x[i]);
-    }
-}
-
-template <int CTRL> __device__ __forceinline__ float add_dpp(float x)
-{
-    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, false));
-}
-// Sum over groups of G consecutive lanes (2 <= G <= 64), in every lane of the
-// group: swaps within four lanes, mirrors of 8 and of 16, then across rows.
-template <int G> __device__ __forceinline__ float group_sum(float x)
-{
-    x = add_dpp<0xB1>(x);                        // quad_perm 1 0 3 2
-    if constexpr (G >= 4) x = add_dpp<0x4E>(x);  // quad_perm 2 3 0 1
-    if constexpr (G >= 8) x = add_dpp<0x141>(x); // row_half_mirror
-    if constexpr (G >= 16) x = add_dpp<0x140>(x); // row_mirror
-    if constexpr (G >= 32) x += __shfl_xor(x, 16);
-    if constexpr (G >= 64) x += __shfl_xor(x, 32);
-    return x;
-}
 
 // --------------------------------------------------------------- gated norm --
 
@@ -221,13 +169,16 @@ __global__ __launch_bounds__(256) void column_sum_kernel(const float *partial, i
     }
 }
 
-// Sums of one [blocks][n] or, with out1, of two that follow each other.
+} // namespace
+
 hipError_t column_sum(const float *partial, int blocks, int n, float *out0, float *out1, hipStream_t st)
 {
     hipLaunchKernelGGL(column_sum_kernel, dim3((n + 15) / 16, out1 ? 2 : 1), dim3(256), 0, st, partial, blocks, n, out0,
                        out1);
     return hipGetLastError();
 }
+
+namespace {
 
 template <typename TO, typename T, int D>
 hipError_t gated_norm_t(bool aligned, bool backward, const GatedNormArgs &a, hipStream_t st)
@@ -508,6 +459,156 @@ template <typename T, int VEC> hipError_t residual_norm_e(bool backward, const R
     return residual_norm_t<T, 256, VEC, 8>(backward, a, st);
 }
 
+// ------------------------------------------- residual norm, output in 8 bits --
+
+// The maximum over G = 32 or 64 consecutive lanes.
+template <int G> __device__ __forceinline__ float group_max(float x)
+{
+    x = fmaxf(x, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0xB1, 0xF, 0xF, false)));
+    x = fmaxf(x, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x4E, 0xF, 0xF, false)));
+    x = fmaxf(x, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x141, 0xF, 0xF, false)));
+    x = fmaxf(x, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x140, 0xF, 0xF, false)));
+    x = fmaxf(x, __shfl_xor(x, 16));
+    if constexpr (G == 64)
+        x = fmaxf(x, __shfl_xor(x, 32));
+    return x;
+}
+
+constexpr float kE4m3Most = 448.f;
+
+// As residual_norm_kernel, with h = rms(x') w as e4m3 values times a scale, of a
+// row or (GROUPS) of 128 columns.  With m = max |x' w| and r the row's 1 / rms, the
+// scale is r m / 448 and the value x' w (448 / m): one pass, since r cancels, and
+// the largest is 448 whatever the rounding.  m is 1e-30 at the least, so that a
+// group of zeros has a scale, too; a row that holds a NaN or an infinity has a
+// scale of NaN.
+template <typename T, int NT, int VEC, int E, bool GROUPS, bool ONCE>
+__global__ __launch_bounds__(NT) void residual_norm_fp8_kernel(NormFp8Args a)
+{
+    using L = Cols<NT, VEC, E>;
+    __shared__ float part[2 * (NT / 64)];
+    float xn[L::K][VEC], yn[L::K][VEC];
+    const auto read = [&](long row) {
+#pragma unroll
+        for (int k = 0; k < L::K; ++k) {
+            const int c = L::col(k);
+            if (c >= a.D)
+                continue;
+            load<VEC, true, ONCE>(xn[k], a.x + row * a.D + c);
+            if (a.y)
+                load<VEC, true, ONCE>(yn[k], static_cast<const T *>(a.y) + row * a.D + c);
+        }
+    };
+    constexpr bool AHEAD = E <= 2; // else the registers do not hold two rows
+    if (AHEAD)
+        read(blockIdx.x);
+    for (long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        if (!AHEAD)
+            read(row);
+        const long at = row * a.D;
+        float x[L::K][VEC], m[GROUPS ? L::K : 1], ss = 0.f;
+        m[0] = 0.f;
+#pragma unroll
+        for (int k = 0; k < L::K; ++k) {
+            const int c = L::col(k);
+            if constexpr (GROUPS)
+                m[k] = 0.f;
+            if (c >= a.D)
+                continue;
+            float &most = m[GROUPS ? k : 0];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                x[k][i] = xn[k][i];
+                if (a.y)
+                    x[k][i] += a.scale ? yn[k][i] * a.scale[c + i] : yn[k][i];
+                ss = fmaf(x[k][i], x[k][i], ss);
+            }
+            if (a.y)
+                store<VEC, true>(a.x_out + at + c, x[k]);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                if (a.weight)
+                    x[k][i] *= a.weight[c + i];
+                most = fmaxf(most, fabsf(x[k][i]));
+            }
+        }
+        if (AHEAD && row + gridDim.x < a.rows)
+            read(row + gridDim.x);
+        ss = group_sum<64>(ss);
+        if constexpr (!GROUPS)
+            m[0] = group_max<64>(m[0]);
+        if constexpr (NT > 64) {
+            __syncthreads(); // part's last use
+            if (threadIdx.x % 64 == 0) {
+                part[threadIdx.x / 64] = ss;
+                if constexpr (!GROUPS)
+                    part[NT / 64 + threadIdx.x / 64] = m[0];
+            }
+            __syncthreads();
+            ss = 0.f;
+#pragma unroll
+            for (int w = 0; w < NT / 64; ++w) {
+                ss += part[w];
+                if constexpr (!GROUPS)
+                    m[0] = fmaxf(m[0], part[NT / 64 + w]);
+            }
+        }
+        const float r = 1.f / sqrtf(ss / a.D + a.eps);
+#pragma unroll
+        for (int k = 0; k < L::K; ++k) {
+            if constexpr (GROUPS)
+                m[k] = group_max<32>(m[k]); // whole groups are there or none of their lanes
+            const int c = L::col(k);
+            if (c >= a.D)
+                continue;
+            const float most = fmaxf(m[GROUPS ? k : 0], 1e-30f), scale = r * (most / kE4m3Most);
+            // 0 r: NaN where the row's norm is none
+            const float by = kE4m3Most / most + 0.f * r;
+            if constexpr (VEC == 4) {
+                unsigned v = __builtin_amdgcn_cvt_pk_fp8_f32(x[k][0] * by, x[k][1] * by, 0, false);
+                v = __builtin_amdgcn_cvt_pk_fp8_f32(x[k][2] * by, x[k][3] * by, v, true);
+                *reinterpret_cast<unsigned *>(a.h + at + c) = v;
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    a.h[at + c + i] = __builtin_amdgcn_cvt_pk_fp8_f32(x[k][i] * by, 0.f, 0, false) & 0xFF;
+            }
+            if constexpr (GROUPS) {
+                if (c % 128 == 0)
+                    a.h_scale[row * (a.D / 128) + c / 128] = scale;
+            } else if (c == 0) {
+                a.h_scale[row] = scale;
+            }
+        }
+    }
+}
+
+template <typename T, int NT, int VEC, int E> hipError_t norm_fp8_k(const NormFp8Args &a, hipStream_t st)
+{
+    const dim3 grid(static_cast<unsigned>(a.rows < kForwardBlocks ? a.rows : kForwardBlocks));
+    if constexpr (VEC > 1)
+        if (a.group != a.D) {
+            hipLaunchKernelGGL((residual_norm_fp8_kernel<T, NT, VEC, E, true, false>), grid, dim3(NT), 0, st, a);
+            return hipGetLastError();
+        }
+    hipLaunchKernelGGL((residual_norm_fp8_kernel<T, NT, VEC, E, false, false>), grid, dim3(NT), 0, st, a);
+    return hipGetLastError();
+}
+
+template <typename T, int VEC> hipError_t norm_fp8_e(const NormFp8Args &a, hipStream_t st)
+{
+    // as residual_norm_e
+    if (a.D <= 512)
+        return norm_fp8_k<T, 64, VEC, 1>(a, st);
+    if (a.D <= 2048)
+        return norm_fp8_k<T, 256, VEC, 1>(a, st);
+    if (a.D <= 4096)
+        return norm_fp8_k<T, 256, VEC, 2>(a, st);
+    if (a.D <= 8192)
+        return norm_fp8_k<T, 256, VEC, 4>(a, st);
+    return norm_fp8_k<T, 256, VEC, 8>(a, st);
+}
+
 } // namespace
 
 hipError_t launch_gated_norm(int o_dtype, int dtype, bool backward, const GatedNormArgs &a, hipStream_t st)
@@ -529,6 +630,16 @@ hipError_t launch_residual_norm(int dtype, bool backward, const ResidualNormArgs
     if (dtype == F32)
         return aligned ? residual_norm_e<float, 4>(backward, a, st) : residual_norm_e<float, 1>(backward, a, st);
     return aligned ? residual_norm_e<__bf16, 4>(backward, a, st) : residual_norm_e<__bf16, 1>(backward, a, st);
+}
+
+hipError_t launch_residual_norm_fp8(int dtype, const NormFp8Args &a, hipStream_t st)
+{
+    const bool aligned = a.D % 4 == 0 && at16(a.x) && at16(a.y) && at16(a.x_out) && at16(a.h); // NULL is aligned
+    if (!aligned && a.group != a.D)
+        return hipErrorInvalidValue;
+    if (dtype == F32)
+        return aligned ? norm_fp8_e<float, 4>(a, st) : norm_fp8_e<float, 1>(a, st);
+    return aligned ? norm_fp8_e<__bf16, 4>(a, st) : norm_fp8_e<__bf16, 1>(a, st);
 }
 
 } // namespace dl

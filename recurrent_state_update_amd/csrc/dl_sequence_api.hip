@@ -3,42 +3,14 @@
 // layouts, dispatch.  Plain host code, like dl_api.hip: kernels are reached
 // only through the launchers declared in dl_internal.h.
 #include "deltalog.h"
+#include "dl_check.h"
 #include "dl_internal.h"
 
 namespace {
 
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+using namespace dl::host;
+
 bool dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
-bool dtype_ok(int t) { return t == DL_F32 || t == DL_BF16; }
-size_t elem(int t) { return t == DL_BF16 ? 2 : 4; }
-size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-
-struct Span {
-    const void *p;
-    size_t bytes;
-};
-
-bool overlap(Span a, Span b)
-{
-    if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0)
-        return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return x < y + b.bytes && y < x + a.bytes;
-}
-
-// Whether a written buffer overlaps another written or a read one.
-template <int NW, int NR> bool clash(const Span (&w)[NW], const Span (&r)[NR])
-{
-    for (int i = 0; i < NW; ++i) {
-        for (int j = i + 1; j < NW; ++j)
-            if (overlap(w[i], w[j]))
-                return true;
-        for (int j = 0; j < NR; ++j)
-            if (overlap(w[i], r[j]))
-                return true;
-    }
-    return false;
-}
 
 // Launches count work-items in 32 bits: at most 512 per chunk and head, and
 // 32 d_v per sequence and head.
@@ -167,9 +139,6 @@ int gated_blocks(long rows, long H, int d)
 }
 
 int residual_blocks(long rows) { return static_cast<int>(rows < 1 ? 1 : rows < kNormBlocks ? rows : kNormBlocks); }
-
-// eps > 0 keeps the norm of a zero row finite; NaN is refused
-bool eps_ok(float eps) { return eps > 0.f && eps < 1e30f; }
 
 dl_status gated_inputs(int rows, int H, int d, int o_dtype, int dtype, const void *o, const void *gate,
                        long long gate_stride, const float *weight, float eps, dl::GatedNormArgs &a, Span (&r)[3])

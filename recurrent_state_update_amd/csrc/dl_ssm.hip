@@ -1,0 +1,344 @@
+// dl_ssm.hip -- the selective state space scan forward, over sequences and for
+// single tokens (the mathematics is in dl_ssm.h).
+#include "dl_ssm.h"
+
+namespace dl {
+
+using namespace ssm;
+
+namespace {
+
+// ------------------------------------------------------------------- scan --
+
+// What a pass of a piece of a sequence is for.
+enum Pass {
+    MAIN,     // y, from the state ahead of the piece
+    AHEAD,    // the state behind it from zero, and its sum of delta
+    BACKWARD, // the same of the adjoint: G ahead of it, from zero behind it
+};
+
+// Tokens per stage: a stage's operands are loaded while the one before is worked
+// on, and pass through LDS once.
+constexpr int stage_tokens(int S) { return S == 1 ? 64 : 32; }
+constexpr int CH = kSsmTile; // channels per workgroup: four waves of four
+constexpr int NT = 256;
+static_assert(CH == 16, "four waves of four rows");
+
+template <int S> struct Stage {
+    static constexpr int TT = stage_tokens(S), XLD = TT + 2, BLD = TT + 4;
+    float x[CH][XLD], dt[CH][XLD], z[CH][XLD];
+    alignas(16) float b[16 * S][BLD], c[16 * S][BLD];
+};
+template <int S> struct Shared {
+    Stage<S> in[2];
+    float y[2][CH][Stage<S>::XLD];
+};
+
+// One workgroup per channel tile and piece.  A wave's row of lanes is a channel,
+// with S states per lane.
+template <typename T, int S, Pass PASS> __global__ __launch_bounds__(NT) void ssm_kernel(SsmArgs a)
+{
+    constexpr int TT = Stage<S>::TT, XV = CH * TT / NT, XPR = CH / XV; // a thread's channels, threads per token
+    constexpr int BV = 4, BPR = 16 * S / BV, BTOK = NT / BPR, BK = TT / BTOK; // its states, threads per token, turns
+    static_assert(XPR * TT == NT && BK * BTOK == TT, "every thread loads as much");
+    __shared__ Shared<S> sh;
+
+    const long work = xcd_order(blockIdx.x, gridDim.x);
+    const int slot = work / a.tiles, tile = work % a.tiles;
+    const int per = (a.CG + CH - 1) / CH, g = tile / per, c0 = g * a.CG + tile % per * CH;
+    const int nc = min(CH, (g + 1) * a.CG - c0); // channels there are
+    const Sequences seqs{a.cu, a.T, a.N};
+    const int tid = threadIdx.x, lane = tid % 64, j = lane % 16, row = tid / 16;
+    const int xt = tid / XPR, xc = tid % XPR * XV, bt = tid / BPR, bn = tid % BPR * BV;
+
+    if constexpr (PASS == MAIN) {
+        // rows of no sequence, a share for every piece
+        const int first = seqs.at(0), behind = seqs.at(a.N), zeros = first + a.T - behind;
+        Cells<XV, T> zero;
+        zero.load(nullptr, 0, false);
+        for (int i = slot * TT + xt; i < zeros; i += a.slots * TT) {
+            const long t = i < first ? i : behind + i - first;
+            zero.store(static_cast<T *>(a.y) + t * a.C + c0 + xc, nc - xc, a.vec_x);
+        }
+    }
+    const Piece p(seqs, slot, a.seg);
+    if (p.none())
+        return;
+    if (PASS == AHEAD && p.last)
+        return;
+    if (PASS == BACKWARD && p.index == 0)
+        return;
+
+    const int c = c0 + min(row, nc - 1); // this row's channel
+    const bool there = row < nc;
+    float rate[S], h[S];
+    bool has[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        has[s] = there && j + 16 * s < a.S;
+        rate[s] = has[s] ? finite_rate(a.A[static_cast<long>(c) * a.S + j + 16 * s] * kLog2e) : 0.f;
+        h[s] = 0.f;
+    }
+    const long of_c = static_cast<long>(c) * a.S + j, states = static_cast<long>(a.C) * a.S;
+    if constexpr (PASS == MAIN) {
+        if (a.init)
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                h[s] = has[s] ? a.init[p.n * states + of_c + 16 * s] : 0.f;
+        for (int i = 0; i < p.index; ++i) { // the segments ahead
+            const float sum = a.seg_d[static_cast<long>(p.base + i) * a.C + c];
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                if (has[s])
+                    h[s] = fmaf(__builtin_amdgcn_exp2f(sum * rate[s]), h[s], a.seg_h[(p.base + i) * states + of_c + 16 * s]);
+        }
+    }
+    const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = PASS == MAIN && a.D ? a.D[c] : 0.f;
+    // what a stage is made of: x and B, or for the adjoint dy and C
+    const T *const px = static_cast<const T *>(PASS == BACKWARD ? a.dy : a.x) + c0 + xc,
+            *const pd = static_cast<const T *>(a.dt) + c0 + xc, *const pz = static_cast<const T *>(a.z) + c0 + xc;
+    const T *const pb = static_cast<const T *>(PASS == BACKWARD ? a.c : a.b) + static_cast<long>(g) * a.S + bn,
+            *const pc = static_cast<const T *>(a.c) + static_cast<long>(g) * a.S + bn;
+    const long xs = PASS == BACKWARD ? a.C : a.xs, bs = PASS == BACKWARD ? a.cs : a.bs;
+    const bool gate = PASS != AHEAD && a.z;
+
+    Cells<XV, T> rx, rd, rz;
+    Cells<BV, T> rb[BK], rc[BK];
+    const auto read = [&](int t0) { // the stage from token t0 of the piece on
+        const int n = t0 + xt < p.len ? nc - xc : 0;
+        const long t = p.t0 + t0 + xt;
+        rx.load(px + t * xs, n, a.vec_x);
+        rd.load(pd + t * a.dts, n, a.vec_x);
+        if (gate)
+            rz.load(pz + t * a.zs, n, a.vec_x);
+#pragma unroll
+        for (int k = 0; k < BK; ++k) {
+            const int i = t0 + bt + k * BTOK, m = i < p.len ? a.S - bn : 0;
+            rb[k].load(pb + static_cast<long>(p.t0 + i) * bs, m, a.vec_b);
+            if constexpr (PASS == MAIN)
+                rc[k].load(pc + static_cast<long>(p.t0 + i) * a.cs, m, a.vec_b);
+        }
+    };
+    const auto put = [&](Stage<S> &st) {
+#pragma unroll
+        for (int i = 0; i < XV; ++i) {
+            st.x[xc + i][xt] = to_f(rx.v[i]);
+            st.dt[xc + i][xt] = to_f(rd.v[i]);
+            if (gate)
+                st.z[xc + i][xt] = to_f(rz.v[i]);
+        }
+#pragma unroll
+        for (int k = 0; k < BK; ++k)
+#pragma unroll
+            for (int i = 0; i < BV; ++i) {
+                st.b[bn + i][bt + k * BTOK] = to_f(rb[k].v[i]);
+                if constexpr (PASS == MAIN)
+                    st.c[bn + i][bt + k * BTOK] = to_f(rc[k].v[i]);
+            }
+    };
+
+    const int stages = (p.len + TT - 1) / TT;
+    const auto from = [&](int k) { return (PASS == BACKWARD ? stages - 1 - k : k) * TT; };
+    float sum = 0.f; // of delta, this lane's tokens
+    if (stages > 0) {
+        read(from(0));
+        put(sh.in[0]);
+    }
+    __syncthreads();
+    for (int k = 0; k < stages; ++k) {
+        const Stage<S> &st = sh.in[k % 2];
+        const int t0 = from(k);
+        if (k + 1 < stages)
+            read(from(k + 1));
+        const int blocks = (min(TT, p.len - t0) + TB - 1) / TB;
+        for (int i = 0; i < blocks; ++i) {
+            const int blk = PASS == BACKWARD ? blocks - 1 - i : i, at = blk * TB;
+            const bool live = t0 + at + j < p.len;
+            float e;
+            float delta = st.dt[row][at + j] + bias, x = st.x[row][at + j], z = 0.f;
+            delta = a.softplus ? softplus(delta, e) : delta;
+            delta = live ? delta : 0.f;
+            if (gate) {
+                z = st.z[row][at + j];
+                z *= sigmoid(z);
+            }
+            float u; // what the state takes of B (or C)
+            if constexpr (PASS == BACKWARD)
+                u = gate ? x * z : x;
+            else
+                u = delta * x;
+            if constexpr (PASS == MAIN)
+                if (a.saved) {
+                    const long block = p.start / TB + p.n + (p.t0 - p.start + t0 + at) / TB;
+#pragma unroll
+                    for (int s = 0; s < S; ++s)
+                        if (has[s])
+                            a.saved[block * states + of_c + 16 * s] = h[s];
+                }
+            float y[TB];
+            f32x4 B[S], C[S];
+            const auto token = [&](auto J) {
+                constexpr int t = decltype(J)::value;
+                if constexpr (t % 4 == (PASS == BACKWARD ? 3 : 0)) {
+#pragma unroll
+                    for (int s = 0; s < S; ++s) {
+                        B[s] = *reinterpret_cast<const f32x4 *>(&st.b[j + 16 * s][at + t / 4 * 4]);
+                        if constexpr (PASS == MAIN)
+                            C[s] = *reinterpret_cast<const f32x4 *>(&st.c[j + 16 * s][at + t / 4 * 4]);
+                    }
+                }
+                y[t] = 0.f;
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    const float d = __builtin_amdgcn_exp2f(row_bcast<t>(delta) * rate[s]);
+                    const float v = row_bcast<t>(u) * B[s][t % 4];
+                    h[s] = PASS == BACKWARD ? d * (h[s] + v) : fmaf(d, h[s], v);
+                    if constexpr (PASS == MAIN)
+                        y[t] = s ? fmaf(C[s][t % 4], h[s], y[t]) : C[s][t % 4] * h[s];
+                }
+            };
+            if constexpr (PASS == BACKWARD)
+                for_tokens_down(token);
+            else
+                for_tokens(token);
+            if constexpr (PASS == MAIN) {
+                float out = fmaf(skip, x, row_sums(y, j));
+                sh.y[k % 2][row][at + j] = gate ? out * z : out;
+            } else {
+                sum += delta;
+            }
+        }
+        if (k + 1 < stages)
+            put(sh.in[(k + 1) % 2]);
+        __syncthreads();
+        if constexpr (PASS == MAIN)
+            if (t0 + xt < p.len) {
+                Cells<XV, T> ry;
+#pragma unroll
+                for (int i = 0; i < XV; ++i)
+                    ry.v[i] = static_cast<T>(sh.y[k % 2][xc + i][xt]);
+                ry.store(static_cast<T *>(a.y) + static_cast<long>(p.t0 + t0 + xt) * a.C + c0 + xc, nc - xc, a.vec_x);
+            }
+    }
+    if constexpr (PASS == MAIN) {
+        if (a.fin && p.last)
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                if (has[s])
+                    a.fin[p.n * states + of_c + 16 * s] = h[s];
+    } else {
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+            if (has[s])
+                a.seg_h[slot * states + of_c + 16 * s] = h[s];
+        sum = row_sum(sum);
+        if (there && j == 0)
+            a.seg_d[static_cast<long>(slot) * a.C + c] = sum;
+    }
+}
+
+template <typename T, int S> hipError_t scan_s(const SsmArgs &a, Pass pass, hipStream_t st)
+{
+    const dim3 grid(static_cast<unsigned>(static_cast<long>(a.slots) * a.tiles));
+    if (pass == MAIN)
+        hipLaunchKernelGGL((ssm_kernel<T, S, MAIN>), grid, dim3(NT), 0, st, a);
+    else if (pass == AHEAD)
+        hipLaunchKernelGGL((ssm_kernel<T, S, AHEAD>), grid, dim3(NT), 0, st, a);
+    else
+        hipLaunchKernelGGL((ssm_kernel<T, S, BACKWARD>), grid, dim3(NT), 0, st, a);
+    return hipGetLastError();
+}
+template <typename T> hipError_t scan_t(const SsmArgs &a, Pass pass, hipStream_t st)
+{
+    return a.S <= 16 ? scan_s<T, 1>(a, pass, st) : a.S <= 32 ? scan_s<T, 2>(a, pass, st) : scan_s<T, 4>(a, pass, st);
+}
+hipError_t scan_pass(int dtype, const SsmArgs &a, Pass pass, hipStream_t st)
+{
+    return dtype == F32 ? scan_t<float>(a, pass, st) : scan_t<__bf16>(a, pass, st);
+}
+
+// ---------------------------------------------------------- single tokens --
+
+// Four states per lane, L = 1 ... 16 lanes (a power of two) per channel; the
+// state's 8 bytes per element are all of the traffic that counts.  VEC: its rows
+// are whole vectors.
+template <typename T, int L, bool VEC> __global__ __launch_bounds__(NT) void ssm_step_kernel(SsmArgs a)
+{
+    const long unit = (static_cast<long>(blockIdx.x) * NT + threadIdx.x) / L; // row and channel
+    const int n0 = threadIdx.x % L * 4;
+    if (unit >= static_cast<long>(a.T) * a.C) // whole groups of lanes
+        return;
+    const int t = unit / a.C, c = unit % a.C, g = c / a.CG, m = a.S - n0; // states of this lane, if positive
+    const int r = a.rows ? a.rows[t] : t;
+    float *const state = a.state + (static_cast<long>(r) * a.C + c) * a.S + n0;
+    const bool known = r >= 0 && r < a.n_rows;
+    Cells<4, float> h, rate;
+    Cells<4, T> b, k;
+    h.load(state, known ? m : 0, VEC);
+    rate.load(a.A + static_cast<long>(c) * a.S + n0, m, VEC);
+    b.load(static_cast<const T *>(a.b) + t * a.bs + static_cast<long>(g) * a.S + n0, m, a.vec_b);
+    k.load(static_cast<const T *>(a.c) + t * a.cs + static_cast<long>(g) * a.S + n0, m, a.vec_b);
+    const float x = to_f(static_cast<const T *>(a.x)[t * a.xs + c]);
+    float delta = to_f(static_cast<const T *>(a.dt)[t * a.dts + c]) + (a.dt_bias ? a.dt_bias[c] : 0.f), e;
+    delta = a.softplus ? softplus(delta, e) : delta;
+    const float u = delta * x;
+    float y = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h.v[i] = fmaf(__builtin_amdgcn_exp2f(delta * finite_rate(rate.v[i] * kLog2e)), h.v[i], u * to_f(b.v[i]));
+        y = fmaf(to_f(k.v[i]), h.v[i], y);
+    }
+    if (known)
+        h.store(state, m, VEC);
+    if constexpr (L > 1)
+        y = group_sum<L>(y);
+    if (n0 == 0) {
+        y = a.D ? fmaf(a.D[c], x, y) : y;
+        if (a.z) {
+            const float z = to_f(static_cast<const T *>(a.z)[t * a.zs + c]);
+            y *= z * sigmoid(z);
+        }
+        static_cast<T *>(a.y)[static_cast<long>(t) * a.C + c] = static_cast<T>(y);
+    }
+}
+
+template <typename T, int L> hipError_t step_l(const SsmArgs &a, hipStream_t st)
+{
+    const long lanes = static_cast<long>(a.T) * a.C * L;
+    const dim3 grid(static_cast<unsigned>((lanes + NT - 1) / NT));
+    if (a.vec_s)
+        hipLaunchKernelGGL((ssm_step_kernel<T, L, true>), grid, dim3(NT), 0, st, a);
+    else
+        hipLaunchKernelGGL((ssm_step_kernel<T, L, false>), grid, dim3(NT), 0, st, a);
+    return hipGetLastError();
+}
+template <typename T> hipError_t step_t(const SsmArgs &a, hipStream_t st)
+{
+    return a.S <= 4    ? step_l<T, 1>(a, st)
+           : a.S <= 8  ? step_l<T, 2>(a, st)
+           : a.S <= 16 ? step_l<T, 4>(a, st)
+           : a.S <= 32 ? step_l<T, 8>(a, st)
+                       : step_l<T, 16>(a, st);
+}
+
+} // namespace
+
+hipError_t launch_ssm_scan(int dtype, const SsmArgs &a, hipStream_t st)
+{
+    if (a.seg)
+        if (hipError_t e = scan_pass(dtype, a, AHEAD, st); e != hipSuccess)
+            return e;
+    return scan_pass(dtype, a, MAIN, st);
+}
+
+hipError_t launch_ssm_ahead_of_adjoint(int dtype, const SsmArgs &a, hipStream_t st)
+{
+    return scan_pass(dtype, a, BACKWARD, st);
+}
+
+hipError_t launch_ssm_step(int dtype, const SsmArgs &a, hipStream_t st)
+{
+    return dtype == F32 ? step_t<float>(a, st) : step_t<__bf16>(a, st);
+}
+
+} // namespace dl

@@ -1,0 +1,413 @@
+// dl_ssm_bwd.hip -- the selective state space scan backward (the mathematics is
+// in dl_ssm.h).
+#include "dl_ssm.h"
+
+namespace dl {
+
+using namespace ssm;
+
+namespace {
+
+constexpr int NT = 256, WAVES = 4;
+constexpr int CH = kSsmGradTile; // channels per workgroup
+constexpr int R = CH / (WAVES * 4); // channels of a row of lanes, one after the other
+constexpr int LD = TB + 1, BLD = TB + 4;
+static_assert(CH * TB == NT * 4, "four channels of a token per thread");
+
+template <int S> struct Stage {
+    float x[CH][LD], dt[CH][LD], z[CH][LD], dy[CH][LD];
+    alignas(16) float b[16 * S][BLD], c[16 * S][BLD];
+};
+// A lane puts dx, ddt and dz where x, dt and z were, which nothing else reads:
+// three stages, so that one can be stored while the next but one is put in.
+template <int S> struct Shared {
+    Stage<S> in[3];
+    alignas(16) float db[2][WAVES][16 * S][TB], dc[2][WAVES][16 * S][TB];
+};
+
+// x[0 ... 3] of row r: the sums over the wave's four rows of x[4 r ... 4 r + 3].
+__device__ __forceinline__ void rows_sum(float (&x)[TB])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const auto v = __builtin_amdgcn_permlane32_swap(__float_as_uint(x[i]), __float_as_uint(x[i + 8]), false, false);
+        x[i] = __uint_as_float(v[0]) + __uint_as_float(v[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const auto v = __builtin_amdgcn_permlane16_swap(__float_as_uint(x[i]), __float_as_uint(x[i + 4]), false, false);
+        x[i] = __uint_as_float(v[0]) + __uint_as_float(v[1]);
+    }
+}
+
+// What is above is done before what is below: else the compiler works on all of a
+// wave's channels at once, and their registers are more than there are.
+template <int N> __device__ __forceinline__ void in_order(float *const (&x)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        asm volatile("" : "+v"(*x[i]));
+}
+
+// acc[i] += (lane T0 + i's x) * v[i]: the broadcast as the multiplication's own
+// modifier, which the compiler does not find for sums of products (it spends an
+// instruction and a register on each).  Two wait states before a row broadcast
+// reads what the instruction ahead may have written, and after the last for one
+// that the compiler may place behind.
+template <int T0> __device__ __forceinline__ void fma_bcast(float *acc, float x, const float *v)
+{
+    asm("s_nop 1\n"
+        "v_fmac_f32_dpp %0, %8, %9 row_newbcast:%c17 row_mask:0xf bank_mask:0xf\n"
+        "v_fmac_f32_dpp %1, %8, %10 row_newbcast:%c18 row_mask:0xf bank_mask:0xf\n"
+        "v_fmac_f32_dpp %2, %8, %11 row_newbcast:%c19 row_mask:0xf bank_mask:0xf\n"
+        "v_fmac_f32_dpp %3, %8, %12 row_newbcast:%c20 row_mask:0xf bank_mask:0xf\n"
+        "v_fmac_f32_dpp %4, %8, %13 row_newbcast:%c21 row_mask:0xf bank_mask:0xf\n"
+        "v_fmac_f32_dpp %5, %8, %14 row_newbcast:%c22 row_mask:0xf bank_mask:0xf\n"
+        "v_fmac_f32_dpp %6, %8, %15 row_newbcast:%c23 row_mask:0xf bank_mask:0xf\n"
+        "v_fmac_f32_dpp %7, %8, %16 row_newbcast:%c24 row_mask:0xf bank_mask:0xf\n"
+        "s_nop 1"
+        : "+v"(acc[0]), "+v"(acc[1]), "+v"(acc[2]), "+v"(acc[3]), "+v"(acc[4]), "+v"(acc[5]), "+v"(acc[6]), "+v"(acc[7])
+        : "v"(x), "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(v[4]), "v"(v[5]), "v"(v[6]), "v"(v[7]), "n"(T0),
+          "n"(T0 + 1), "n"(T0 + 2), "n"(T0 + 3), "n"(T0 + 4), "n"(T0 + 5), "n"(T0 + 6), "n"(T0 + 7));
+}
+// The same into two sums.
+template <int T0> __device__ __forceinline__ void fma_bcast_sum(float &even, float &odd, float x, const float *v)
+{
+    asm("s_nop 1\n"
+        "v_fmac_f32_dpp %0, %2, %3 row_newbcast:%c11 row_mask:0xf bank_mask:0xf\n"
+        "v_fmac_f32_dpp %1, %2, %4 row_newbcast:%c12 row_mask:0xf bank_mask:0xf\n"
+        "v_fmac_f32_dpp %0, %2, %5 row_newbcast:%c13 row_mask:0xf bank_mask:0xf\n"
+        "v_fmac_f32_dpp %1, %2, %6 row_newbcast:%c14 row_mask:0xf bank_mask:0xf\n"
+        "v_fmac_f32_dpp %0, %2, %7 row_newbcast:%c15 row_mask:0xf bank_mask:0xf\n"
+        "v_fmac_f32_dpp %1, %2, %8 row_newbcast:%c16 row_mask:0xf bank_mask:0xf\n"
+        "v_fmac_f32_dpp %0, %2, %9 row_newbcast:%c17 row_mask:0xf bank_mask:0xf\n"
+        "v_fmac_f32_dpp %1, %2, %10 row_newbcast:%c18 row_mask:0xf bank_mask:0xf\n"
+        "s_nop 1"
+        : "+v"(even), "+v"(odd)
+        : "v"(x), "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(v[4]), "v"(v[5]), "v"(v[6]), "v"(v[7]), "n"(T0),
+          "n"(T0 + 1), "n"(T0 + 2), "n"(T0 + 3), "n"(T0 + 4), "n"(T0 + 5), "n"(T0 + 6), "n"(T0 + 7));
+}
+
+// One workgroup per tile of 64 channels and piece of a sequence: blocks of
+// sixteen tokens from its end.  Per block the states are formed anew from the
+// saved one ahead of it, sixteen in registers with their decays; then the adjoint
+// goes back over them.  A wave takes four channels at a time, four times: what
+// it adds up of dB and dC over channels stays in registers meanwhile, B and C too.
+template <typename T, int S> __global__ __launch_bounds__(NT, S == 1 ? 2 : 1) void ssm_bwd_kernel(SsmArgs a)
+{
+    constexpr int XV = 4, XPR = CH / XV;
+    constexpr int BN = 16 * S * TB / NT; // states of a token per thread
+    __shared__ Shared<S> sh;
+
+    const long work = xcd_order(blockIdx.x, gridDim.x);
+    const int slot = work / a.tiles, tile = work % a.tiles;
+    const int per = (a.CG + CH - 1) / CH, g = tile / per, c0 = g * a.CG + tile % per * CH;
+    const int nc = min(CH, (g + 1) * a.CG - c0);
+    const Sequences seqs{a.cu, a.T, a.N};
+    const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, j = lane % 16, row = lane / 16;
+    const int xt = tid / XPR, xc = tid % XPR * XV, bt = tid / 16, bn = tid % 16 * BN;
+    const bool gate = a.z;
+    const long states = static_cast<long>(a.C) * a.S;
+
+    {   // rows of no sequence, a share for every piece
+        const int first = seqs.at(0), behind = seqs.at(a.N), zeros = first + a.T - behind;
+        Cells<XV, T> zero;
+        zero.load(nullptr, 0, false);
+        for (int i = slot * TB + xt; i < zeros; i += a.slots * TB) {
+            const long to = static_cast<long>(i < first ? i : behind + i - first) * a.C + c0 + xc;
+            zero.store(static_cast<T *>(a.dx) + to, nc - xc, a.vec_x);
+            zero.store(static_cast<T *>(a.ddt) + to, nc - xc, a.vec_x);
+            if (gate)
+                zero.store(static_cast<T *>(a.dz) + to, nc - xc, a.vec_x);
+        }
+    }
+    const Piece p(seqs, slot, a.seg);
+    const int len = p.none() ? 0 : p.len; // a slot of no piece adds zeros to the sums
+
+    // this row's channels are ch(0) ... ch(R - 1)
+    const auto in_tile = [&](int i) { return wave * 4 * R + i * 4 + row; };
+    float rate[R][S], G[R][S], dA[R][S], skip[R], bias[R], dD[R], dbias[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int c = c0 + min(in_tile(i), nc - 1);
+        skip[i] = a.D ? a.D[c] : 0.f;
+        bias[i] = a.dt_bias ? a.dt_bias[c] : 0.f;
+        dD[i] = dbias[i] = 0.f;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const bool has = in_tile(i) < nc && j + 16 * s < a.S;
+            const long at = static_cast<long>(c) * a.S + j + 16 * s;
+            rate[i][s] = has ? finite_rate(a.A[at] * kLog2e) : 0.f;
+            dA[i][s] = 0.f;
+            G[i][s] = 0.f;
+            if (has && !p.none() && a.dfin)
+                G[i][s] = a.dfin[p.n * states + at];
+        }
+    }
+    if (len > 0 && a.seg) { // the segments behind
+        const int count = (p.end - p.start + a.seg - 1) / a.seg;
+        for (int k = count - 1; k > p.index; --k)
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int c = c0 + min(in_tile(i), nc - 1);
+                const float sum = a.seg_d[static_cast<long>(p.base + k) * a.C + c];
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    if (in_tile(i) < nc && j + 16 * s < a.S)
+                        G[i][s] = fmaf(__builtin_amdgcn_exp2f(sum * rate[i][s]), G[i][s],
+                                       a.seg_h[(p.base + k) * states + static_cast<long>(c) * a.S + j + 16 * s]);
+            }
+    }
+
+    Cells<XV, T> rx, rd, rz, ry;
+    Cells<BN, T> rb, rc;
+    const auto read = [&](int t0) {
+        const int n = t0 + xt < len ? nc - xc : 0;
+        const long t = p.t0 + t0 + xt, col = c0 + xc;
+        rx.load(static_cast<const T *>(a.x) + t * a.xs + col, n, a.vec_x);
+        rd.load(static_cast<const T *>(a.dt) + t * a.dts + col, n, a.vec_x);
+        ry.load(static_cast<const T *>(a.dy) + t * a.C + col, n, a.vec_x);
+        if (gate)
+            rz.load(static_cast<const T *>(a.z) + t * a.zs + col, n, a.vec_x);
+        const int m = t0 + bt < len ? a.S - bn : 0;
+        const long tb = p.t0 + t0 + bt, of_g = static_cast<long>(g) * a.S + bn;
+        rb.load(static_cast<const T *>(a.b) + tb * a.bs + of_g, m, a.vec_b);
+        rc.load(static_cast<const T *>(a.c) + tb * a.cs + of_g, m, a.vec_b);
+    };
+    const auto put = [&](Stage<S> &st) {
+#pragma unroll
+        for (int i = 0; i < XV; ++i) {
+            st.x[xc + i][xt] = to_f(rx.v[i]);
+            st.dt[xc + i][xt] = to_f(rd.v[i]);
+            st.dy[xc + i][xt] = to_f(ry.v[i]);
+            if (gate)
+                st.z[xc + i][xt] = to_f(rz.v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < BN; ++i) {
+            st.b[bn + i][bt] = to_f(rb.v[i]);
+            st.c[bn + i][bt] = to_f(rc.v[i]);
+        }
+    };
+
+    const int blocks = (len + TB - 1) / TB;
+    if (blocks > 0) {
+        read((blocks - 1) * TB);
+        put(sh.in[0]);
+    }
+    __syncthreads();
+    for (int k = 0; k < blocks; ++k) {
+        Stage<S> &st = sh.in[k % 3];
+        const int t0 = (blocks - 1 - k) * TB;
+        if (k + 1 < blocks)
+            read(t0 - TB);
+        const float *saved = a.saved + (p.start / TB + p.n + (p.t0 - p.start + t0) / TB) * states;
+        const bool live = t0 + j < len;
+        float sy[R], sq[R], sr[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            sy[i] = sq[i] = sr[i] = 0.f;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            float B[TB], C[TB], dB[TB], dC[TB], start[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                start[i] = in_tile(i) < nc && j + 16 * s < a.S
+                               ? saved[static_cast<long>(c0 + in_tile(i)) * a.S + j + 16 * s] : 0.f;
+#pragma unroll
+            for (int t = 0; t < TB; t += 4) {
+                const f32x4 b = *reinterpret_cast<const f32x4 *>(&st.b[j + 16 * s][t]),
+                            c = *reinterpret_cast<const f32x4 *>(&st.c[j + 16 * s][t]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    B[t + i] = b[i];
+                    C[t + i] = c[i];
+                    dB[t + i] = dC[t + i] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int c = in_tile(i);
+                float delta = st.dt[c][j] + bias[i], e;
+                delta = a.softplus ? softplus(delta, e) : delta;
+                delta = live ? delta : 0.f;
+                float dy = st.dy[c][j];
+                if (gate) {
+                    const float z = st.z[c][j];
+                    dy *= z * sigmoid(z);
+                }
+                float u = delta * st.x[c][j];
+                in_order({&delta, &u, &dy, &start[i]});
+                // forward over the block
+                float d[TB], h[TB + 1], y[TB], f = G[i][s];
+                h[0] = start[i];
+                for_tokens([&](auto J) {
+                    constexpr int t = decltype(J)::value;
+                    d[t] = __builtin_amdgcn_exp2f(row_bcast<t>(delta) * rate[i][s]);
+                    h[t + 1] = fmaf(d[t], h[t], row_bcast<t>(u) * B[t]);
+                    y[t] = C[t] * h[t + 1];
+                });
+                fma_bcast<0>(dC, dy, h + 1);
+                fma_bcast<8>(dC + 8, dy, h + 9);
+                if (gate)
+                    sy[i] += row_sums(y, j);
+                in_order({&sy[i], &f});
+                // and back
+                float q[TB], r[TB], F[TB], moved[TB], odd = 0.f;
+                const auto back = [&](auto J) {
+                    constexpr int t = decltype(J)::value;
+                    F[t] = f + row_bcast<t>(dy) * C[t];
+                    q[t] = F[t] * B[t];
+                    f = F[t] * d[t];
+                    moved[t] = f * h[t];
+                    r[t] = moved[t] * rate[i][s];
+                };
+                for_tokens_down<15, 8>(back);
+                fma_bcast<8>(dB + 8, u, F + 8);
+                fma_bcast_sum<8>(dA[i][s], odd, delta, moved + 8);
+                for_tokens_down<7, 0>(back);
+                fma_bcast<0>(dB, u, F);
+                fma_bcast_sum<0>(dA[i][s], odd, delta, moved);
+                dA[i][s] += odd;
+                G[i][s] = f;
+                sq[i] += row_sums(q, j);
+                sr[i] += row_sums(r, j);
+                in_order({&G[i][s], &dA[i][s], &sq[i], &sr[i]});
+            }
+            rows_sum(dB);
+            rows_sum(dC);
+            *reinterpret_cast<f32x4 *>(&sh.db[k % 2][wave][j + 16 * s][4 * row]) = f32x4{dB[0], dB[1], dB[2], dB[3]};
+            *reinterpret_cast<f32x4 *>(&sh.dc[k % 2][wave][j + 16 * s][4 * row]) = f32x4{dC[0], dC[1], dC[2], dC[3]};
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int c = in_tile(i);
+            const float raw = st.dt[c][j] + bias[i], x = st.x[c][j];
+            float delta = raw, slope = 1.f, e;
+            if (a.softplus) {
+                delta = softplus(raw, e);
+                slope = softplus_slope(raw, e);
+            }
+            delta = live ? delta : 0.f;
+            float dy = st.dy[c][j];
+            if (gate) {
+                const float z = st.z[c][j], sg = sigmoid(z);
+                st.z[c][j] = dy * fmaf(skip[i], x, sy[i]) * sg * fmaf(z, 1.f - sg, 1.f);
+                dy *= z * sg;
+            }
+            const float dt = live ? fmaf(x, sq[i], sr[i] * (1.f / kLog2e)) * slope : 0.f;
+            st.x[c][j] = fmaf(delta, sq[i], skip[i] * dy);
+            st.dt[c][j] = dt;
+            dD[i] = fmaf(dy, x, dD[i]);
+            dbias[i] += dt;
+        }
+        if (k + 1 < blocks)
+            put(sh.in[(k + 1) % 3]);
+        __syncthreads();
+        if (t0 + xt < len) {
+            const long to = static_cast<long>(p.t0 + t0 + xt) * a.C + c0 + xc;
+            Cells<XV, T> v;
+            const auto out = [&](void *dst, const float (&src)[CH][LD]) {
+#pragma unroll
+                for (int i = 0; i < XV; ++i)
+                    v.v[i] = static_cast<T>(src[xc + i][xt]);
+                v.store(static_cast<T *>(dst) + to, nc - xc, a.vec_x);
+            };
+            out(a.dx, st.x);
+            out(a.ddt, st.dt);
+            if (gate)
+                out(a.dz, st.z);
+        }
+        if (t0 + bt < len) {
+            // [tile of the group][token][group][B's states, C's states]
+            float *to = a.part_bc + ((static_cast<long>(tile % per) * a.T + p.t0 + t0 + bt) * a.G + g) * 2 * a.S;
+#pragma unroll
+            for (int i = 0; i < BN; ++i) {
+                const int n = bn + i;
+                float x = 0.f, y = 0.f;
+#pragma unroll
+                for (int w = 0; w < WAVES; ++w) {
+                    x += sh.db[k % 2][w][n][bt];
+                    y += sh.dc[k % 2][w][n][bt];
+                }
+                if (n < a.S) {
+                    to[n] = x;
+                    to[a.S + n] = y;
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const long c = c0 + in_tile(i);
+        const bool there = in_tile(i) < nc;
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+            if (there && j + 16 * s < a.S) {
+                a.part_a[slot * states + c * a.S + j + 16 * s] = dA[i][s];
+                if (!p.none() && p.index == 0 && a.dinit)
+                    a.dinit[p.n * states + c * a.S + j + 16 * s] = G[i][s];
+            }
+        const float x = row_sum(dD[i]), y = row_sum(dbias[i]);
+        if (there && j == 0) {
+            if (a.part_d)
+                a.part_d[static_cast<long>(slot) * a.C + c] = x;
+            if (a.part_bias)
+                a.part_bias[static_cast<long>(slot) * a.C + c] = y;
+        }
+    }
+}
+
+// dB and dC from the tiles' sums, zero for tokens of no sequence.  In 64 bits:
+// up to hundreds are added, and the time is the loads'.
+template <typename T> __global__ __launch_bounds__(NT) void ssm_bc_kernel(SsmArgs a, int tiles)
+{
+    const long width = 2L * a.G * a.S, i = static_cast<long>(blockIdx.x) * NT + threadIdx.x;
+    if (i >= a.T * width)
+        return;
+    const int t = i / width, k = i % width, g = k / (2 * a.S), n = k % (2 * a.S);
+    const Sequences seqs{a.cu, a.T, a.N};
+    double x = 0.;
+    if (t >= seqs.at(0) && t < seqs.at(a.N))
+        for (int p = 0; p < tiles; ++p)
+            x += a.part_bc[p * (a.T * width) + i];
+    T *const out = static_cast<T *>(n < a.S ? a.db : a.dc);
+    out[(static_cast<long>(t) * a.G + g) * a.S + (n < a.S ? n : n - a.S)] = static_cast<T>(static_cast<float>(x));
+}
+
+template <typename T> hipError_t bwd_t(const SsmArgs &a, hipStream_t st)
+{
+    const dim3 grid(static_cast<unsigned>(static_cast<long>(a.slots) * a.tiles));
+    if (a.S <= 16)
+        hipLaunchKernelGGL((ssm_bwd_kernel<T, 1>), grid, dim3(NT), 0, st, a);
+    else if (a.S <= 32)
+        hipLaunchKernelGGL((ssm_bwd_kernel<T, 2>), grid, dim3(NT), 0, st, a);
+    else
+        hipLaunchKernelGGL((ssm_bwd_kernel<T, 4>), grid, dim3(NT), 0, st, a);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess || a.T == 0)
+        return e;
+    const long n = static_cast<long>(a.T) * 2 * a.G * a.S;
+    hipLaunchKernelGGL((ssm_bc_kernel<T>), dim3(static_cast<unsigned>((n + NT - 1) / NT)), dim3(NT), 0, st, a,
+                       (a.CG + CH - 1) / CH);
+    return hipGetLastError();
+}
+
+} // namespace
+
+hipError_t launch_ssm_backward(int dtype, const SsmArgs &ahead, const SsmArgs &a, hipStream_t st)
+{
+    hipError_t e = hipSuccess;
+    if (a.seg)
+        e = launch_ssm_ahead_of_adjoint(dtype, ahead, st);
+    if (e == hipSuccess)
+        e = dtype == F32 ? bwd_t<float>(a, st) : bwd_t<__bf16>(a, st);
+    if (e == hipSuccess)
+        e = column_sum(a.part_a, a.slots, a.C * a.S, a.d_A, nullptr, st);
+    if (e == hipSuccess && a.part_d)
+        e = column_sum(a.part_d, a.slots, a.C, a.d_D, nullptr, st);
+    if (e == hipSuccess && a.part_bias)
+        e = column_sum(a.part_bias, a.slots, a.C, a.d_bias, nullptr, st);
+    return e;
+}
+
+} // namespace dl

@@ -65,6 +65,12 @@ def _wants_grad(*tensors):
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 
+def _no_grad(name, *tensors):
+    """Refuse inputs that want a gradient of an operator that has none."""
+    if _wants_grad(*tensors):
+        raise NotImplementedError(f"{name} has no gradient: call it under torch.no_grad()")
+
+
 def _bytes(n, device):
     return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
 
@@ -449,3 +455,47 @@ def residual_norm(x, y=None, scale=None, weight=None, eps: float = 1e-6, dtype=N
             return (x, out[1]) if y is None else out
         out = _ResidualNormFn.apply(x, y, scale, weight, float(eps), dtype)
         return (x, out) if y is None else out
+
+
+def residual_norm_fp8(x, y=None, scale=None, weight=None, eps: float = 1e-6, group=None, stream=None):
+    """`residual_norm` with h in 8 bits, for a projection that takes its input so:
+    x' as there, and rms(x') * weight = h * h_scale with h [...,D] in
+    torch.float8_e4m3fn and h_scale fp32, [...] (a scale for each row) or, with
+    ``group`` 128, [...,D/128] (one for every 128 columns): the largest of each is
+    448.  Returns (x', h, h_scale), x itself in place of x' without y.  For
+    inference: it has no gradient and refuses inputs that want one."""
+    _plain("residual_norm_fp8", x, y, scale, weight)
+    _gpu(x, "x")
+    if x.dim() < 1 or x.dtype != torch.float32:
+        raise ValueError(f"x: want fp32 [...,D], got {x.dtype} {tuple(x.shape)}")
+    D, lead = x.shape[-1], x.shape[:-1]
+    if not 1 <= D <= 16384:
+        raise ValueError(f"x: want 1 to 16384 columns, got {D}")
+    if group is not None and (group != 128 or D % 128 != 0):
+        raise ValueError(f"group: want None or 128 with a multiple of 128 columns, got {group} with {D}")
+    if y is None:
+        if scale is not None:
+            raise ValueError("scale goes with y")
+        dtype = torch.bfloat16
+    else:
+        if not isinstance(y, torch.Tensor):
+            raise ValueError("y: want a GPU tensor shaped as x")
+        dtype = y.dtype
+        _dtype_id(dtype)
+        _tensor(y, "y", dtype, x.shape, x.device)
+    for t, name in ((scale, "scale"), (weight, "weight")):
+        if t is not None:
+            _tensor(t, name, torch.float32, (D,), x.device)
+    _no_grad("residual_norm_fp8", x, y, scale, weight)
+    with _on(x.device, stream):
+        rows = _count(x.numel() // D)
+        # (groups are read as vectors)
+        xs, y = (None if t is None else _state(t) if group else t.contiguous() for t in (x, y))
+        scale, weight = (None if t is None else t.contiguous() for t in (scale, weight))
+        x_out = None if y is None else torch.empty_like(xs)
+        h = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        h_scale = torch.empty((*lead, D // 128) if group else lead, dtype=torch.float32, device=x.device)
+        _check(_lib.dl_residual_norm_quant(rows, D, DTYPES[dtype], xs.data_ptr(), _p(y), _p(scale), _p(weight), float(eps),
+                                         _p(x_out), group or 0, h.data_ptr(), h_scale.data_ptr(), _current(x.device)),
+               "dl_residual_norm_quant")
+        return x if x_out is None else x_out, h, h_scale
