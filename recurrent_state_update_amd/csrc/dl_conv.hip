@@ -21,7 +21,7 @@ constexpr int NT = 256;
 
 // What a lane works on: channels c ... c + V - 1 (m of them there), and a walk over
 // tokens in ascending order that knows each one's sequence.
-template <typename T, int W, int V> struct Lane {
+template <typename T, int W, int V, bool VEC> struct Lane {
     const ConvArgs &a;
     const Sequences seqs;
     const int c, m;
@@ -42,8 +42,9 @@ template <typename T, int W, int V> struct Lane {
     }
     __device__ __forceinline__ void row(float (&out)[V], const void *base, long at) const
     {
-        Cells<V, T> r;
-        r.load(static_cast<const T *>(base) + at + c, m, a.vec);
+        Cells<V, T, VEC> r;
+        r.load(static_cast<const T *>(base) + at + c, m);
+        r.keep(m);
         r.get(out);
     }
     // row j of sequence n's initial state
@@ -124,7 +125,7 @@ template <typename T, int W, int V> struct Lane {
 };
 
 // Units of V channels: first `runs` runs of tokens, then (fin) the N end states.
-template <typename T, int W, int V> __global__ __launch_bounds__(NT) void conv_kernel(ConvArgs a)
+template <typename T, int W, int V, bool VEC> __global__ __launch_bounds__(NT) void conv_kernel(ConvArgs a)
 {
     constexpr int U = 4; // tokens loaded ahead
     const long unit = static_cast<long>(blockIdx.x) * NT + threadIdx.x;
@@ -138,32 +139,31 @@ template <typename T, int W, int V> __global__ __launch_bounds__(NT) void conv_k
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             const int pos = end - start - (W - 1) + j;
-            Cells<V, T> r;
+            Cells<V, T, VEC> r;
             if (pos >= 0)
-                r.load(static_cast<const T *>(a.x) + (start + pos) * a.xs + c, m, a.vec);
+                r.load(static_cast<const T *>(a.x) + (start + pos) * a.xs + c, m);
             else if (a.init)
-                r.load(static_cast<const T *>(a.init) + (static_cast<long>(n) * (W - 1) + pos + W - 1) * a.C + c, m, a.vec);
+                r.load(static_cast<const T *>(a.init) + (static_cast<long>(n) * (W - 1) + pos + W - 1) * a.C + c, m);
             else
-                r.load(nullptr, 0, false);
-            r.store(static_cast<T *>(a.fin) + (static_cast<long>(n) * (W - 1) + j) * a.C + c, m, a.vec);
+                r.zero();
+            r.store(static_cast<T *>(a.fin) + (static_cast<long>(n) * (W - 1) + j) * a.C + c, m);
         }
         return;
     }
     const int t0 = run * a.run, t1 = min(t0 + a.run, a.T);
     if (t0 >= t1)
         return;
-    Lane<T, W, V> l(a, c);
-    Cells<V, T> next[U];
+    Lane<T, W, V, VEC> l(a, c);
+    Cells<V, T, VEC> next[U];
     const auto read = [&](int t) {
 #pragma unroll
         for (int i = 0; i < U; ++i)
-            if (t + i < t1)
-                next[i].load(static_cast<const T *>(a.x) + (t + i) * a.xs + c, l.m, a.vec);
+            next[i].load(static_cast<const T *>(a.x) + min(t + i, t1 - 1) * a.xs + c, l.m);
     };
     read(t0);
     l.begin(t0);
     for (int t = t0; t < t1; t += U) {
-        Cells<V, T> now[U];
+        Cells<V, T, VEC> now[U];
 #pragma unroll
         for (int i = 0; i < U; ++i)
             now[i] = next[i];
@@ -182,9 +182,9 @@ template <typename T, int W, int V> __global__ __launch_bounds__(NT) void conv_k
                     s[e] = s[e] / (1.f + expf(-s[e]));
                 s[e] = live ? s[e] : 0.f;
             }
-            Cells<V, T> y;
+            Cells<V, T, VEC> y;
             y.put(s);
-            y.store(static_cast<T *>(a.y) + static_cast<long>(t + i) * a.C + c, l.m, a.vec);
+            y.store(static_cast<T *>(a.y) + static_cast<long>(t + i) * a.C + c, l.m);
             l.leave();
         }
     }
@@ -193,13 +193,13 @@ template <typename T, int W, int V> __global__ __launch_bounds__(NT) void conv_k
 // Runs as above; then the N initial states' gradients.  dx of a token is done W - 1
 // tokens behind it, or at its sequence's end: g[k] is what is gathered of that k
 // tokens back.
-template <typename T, int W, int V> __global__ __launch_bounds__(NT) void conv_bwd_kernel(ConvArgs a)
+template <typename T, int W, int V, bool VEC> __global__ __launch_bounds__(NT) void conv_bwd_kernel(ConvArgs a)
 {
     const long unit = static_cast<long>(blockIdx.x) * NT + threadIdx.x;
     const int groups = (a.C + V - 1) / V, run = unit / groups, c = unit % groups * V;
     if (run >= a.runs + (a.dinit ? a.N : 0))
         return;
-    Lane<T, W, V> l(a, c);
+    Lane<T, W, V, VEC> l(a, c);
     const auto add_final = [&](float (&x)[V], int j) { // row j of the end state's gradient
         float d[V];
         l.row(d, a.dfin, (static_cast<long>(l.n) * (W - 1) + j) * a.C);
@@ -239,9 +239,9 @@ template <typename T, int W, int V> __global__ __launch_bounds__(NT) void conv_b
         for (int j = 0; j < W - 1; ++j) {
             if (a.dfin && j >= len)
                 add_final(d[j], j - len);
-            Cells<V, T> r;
+            Cells<V, T, VEC> r;
             r.put(d[j]);
-            r.store(static_cast<T *>(a.dinit) + (static_cast<long>(l.n) * (W - 1) + j) * a.C + c, l.m, a.vec);
+            r.store(static_cast<T *>(a.dinit) + (static_cast<long>(l.n) * (W - 1) + j) * a.C + c, l.m);
         }
         return;
     }
@@ -259,18 +259,17 @@ template <typename T, int W, int V> __global__ __launch_bounds__(NT) void conv_b
             return;
         if (a.dfin && t >= l.end - (W - 1))
             add_final(x, t - (l.end - (W - 1)));
-        Cells<V, T> r;
+        Cells<V, T, VEC> r;
         r.put(x);
-        r.store(static_cast<T *>(a.dx) + static_cast<long>(t) * a.C + c, l.m, a.vec);
+        r.store(static_cast<T *>(a.dx) + static_cast<long>(t) * a.C + c, l.m);
     };
     if (t0 < t1) {
-        Cells<V, T> nx, ny;
+        Cells<V, T, VEC> nx, ny;
         const auto read = [&](int t) {
-            if (t < min(t1 + W - 1, a.T)) {
-                nx.load(static_cast<const T *>(a.x) + t * a.xs + c, l.m, a.vec);
-                if (a.dy)
-                    ny.load(static_cast<const T *>(a.dy) + static_cast<long>(t) * a.C + c, l.m, a.vec);
-            }
+            t = min(t, a.T - 1);
+            nx.load(static_cast<const T *>(a.x) + t * a.xs + c, l.m);
+            if (a.dy)
+                ny.load(static_cast<const T *>(a.dy) + static_cast<long>(t) * a.C + c, l.m);
         };
         read(t0);
         l.begin(t0);
@@ -298,9 +297,9 @@ template <typename T, int W, int V> __global__ __launch_bounds__(NT) void conv_b
             read(t + 1);
             if (!live) { // of no sequence
                 if (t < t1) {
-                    Cells<V, T> zero;
-                    zero.load(nullptr, 0, false);
-                    zero.store(static_cast<T *>(a.dx) + static_cast<long>(t) * a.C + c, l.m, a.vec);
+                    Cells<V, T, VEC> zero;
+                    zero.zero();
+                    zero.store(static_cast<T *>(a.dx) + static_cast<long>(t) * a.C + c, l.m);
                 }
                 continue;
             }
@@ -341,21 +340,24 @@ template <typename T, int W, int V> __global__ __launch_bounds__(NT) void conv_b
 }
 
 // One token each: state row r = [W - 1][C] moves up by one and takes x.
-template <typename T, int W, int V> __global__ __launch_bounds__(NT) void conv_step_kernel(ConvArgs a)
+template <typename T, int W, int V, bool VEC> __global__ __launch_bounds__(NT) void conv_step_kernel(ConvArgs a)
 {
     const long unit = static_cast<long>(blockIdx.x) * NT + threadIdx.x;
     const int groups = (a.C + V - 1) / V, t = unit / groups, c = unit % groups * V;
     if (t >= a.T)
         return;
-    Lane<T, W, V> l(a, c);
+    Lane<T, W, V, VEC> l(a, c);
     const int r = a.rows ? a.rows[t] : t;
     const bool known = r >= 0 && r < a.n_rows;
     T *const state = static_cast<T *>(a.state) + static_cast<long>(r) * (W - 1) * a.C + c;
-    Cells<V, T> seen[W];
+    Cells<V, T, VEC> seen[W];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
-        seen[j].load(state + j * a.C, known ? l.m : 0, a.vec);
-    seen[W - 1].load(static_cast<const T *>(a.x) + t * a.xs + c, l.m, a.vec);
+        seen[j].load((known ? state : static_cast<const T *>(a.state) + c) + j * a.C, l.m);
+    seen[W - 1].load(static_cast<const T *>(a.x) + t * a.xs + c, l.m);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+        seen[j].keep(known ? l.m : 0);
 #pragma unroll
     for (int j = 0; j < W; ++j)
         seen[j].get(l.x[j]);
@@ -365,18 +367,18 @@ template <typename T, int W, int V> __global__ __launch_bounds__(NT) void conv_s
 #pragma unroll
         for (int i = 0; i < V; ++i)
             s[i] = s[i] / (1.f + expf(-s[i]));
-    Cells<V, T> y;
+    Cells<V, T, VEC> y;
     y.put(s);
-    y.store(static_cast<T *>(a.y) + static_cast<long>(t) * a.C + c, l.m, a.vec);
+    y.store(static_cast<T *>(a.y) + static_cast<long>(t) * a.C + c, l.m);
     if (known)
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
-            seen[j + 1].store(state + j * a.C, l.m, a.vec);
+            seen[j + 1].store(state + j * a.C, l.m);
 }
 
 enum Kind { FORWARD, BACKWARD, STEP };
 
-template <typename T, int W, int V> hipError_t conv_w(Kind kind, const ConvArgs &a, hipStream_t st)
+template <typename T, int W, int V, bool VEC> hipError_t conv_v(Kind kind, const ConvArgs &a, hipStream_t st)
 {
     const long groups = (a.C + V - 1) / V;
     const long units = groups * (kind == STEP ? a.T : a.runs + ((kind == FORWARD ? a.fin : a.dinit) ? a.N : 0));
@@ -384,12 +386,16 @@ template <typename T, int W, int V> hipError_t conv_w(Kind kind, const ConvArgs 
         return hipSuccess;
     const dim3 grid(static_cast<unsigned>((units + NT - 1) / NT));
     if (kind == FORWARD)
-        hipLaunchKernelGGL((conv_kernel<T, W, V>), grid, dim3(NT), 0, st, a);
+        hipLaunchKernelGGL((conv_kernel<T, W, V, VEC>), grid, dim3(NT), 0, st, a);
     else if (kind == BACKWARD)
-        hipLaunchKernelGGL((conv_bwd_kernel<T, W, V>), grid, dim3(NT), 0, st, a);
+        hipLaunchKernelGGL((conv_bwd_kernel<T, W, V, VEC>), grid, dim3(NT), 0, st, a);
     else
-        hipLaunchKernelGGL((conv_step_kernel<T, W, V>), grid, dim3(NT), 0, st, a);
+        hipLaunchKernelGGL((conv_step_kernel<T, W, V, VEC>), grid, dim3(NT), 0, st, a);
     return hipGetLastError();
+}
+template <typename T, int W, int V> hipError_t conv_w(Kind kind, const ConvArgs &a, hipStream_t st)
+{
+    return a.vec ? conv_v<T, W, V, true>(kind, a, st) : conv_v<T, W, V, false>(kind, a, st);
 }
 template <typename T, int V> hipError_t conv_t(Kind kind, const ConvArgs &a, hipStream_t st)
 {

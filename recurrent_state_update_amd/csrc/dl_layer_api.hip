@@ -195,7 +195,7 @@ dl_status ssm_inputs(const dl_ssm_desc *d, bool step, dl::SsmArgs &a, Span (&r)[
     a.D = d->d;
     a.dt_bias = d->dt_bias;
     a.vec_x = vectors(d->x, xs, es) && vectors(d->dt, dts, es) && (!d->z || vectors(d->z, zs, es)) && a.CG % 4 == 0;
-    a.vec_b = vectors(d->b, bs, es) && vectors(d->c, cs, es) && (d->groups == 1 || d->states % 4 == 0);
+    a.vec_b = vectors(d->b, bs, es) && vectors(d->c, cs, es) && d->states % 4 == 0;
     r[0] = {d->x, rows_bytes(d->tokens, xs, C, es)};
     r[1] = {d->dt, rows_bytes(d->tokens, dts, C, es)};
     r[2] = {d->z, rows_bytes(d->tokens, zs, C, es)};

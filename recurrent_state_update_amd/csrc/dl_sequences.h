@@ -47,25 +47,39 @@ struct Sequences {
     }
 };
 
-// V consecutive elements of a row: a vector where `vec` says that it is whole and
-// aligned, else the first n of them (the rest zero).
-template <int V, typename T> struct Cells {
+// The first n of V consecutive elements of a row.  VEC: rows are whole vectors, and n
+// is V or more, or not above 0.  Loads are not conditional, so that nothing waits for
+// them before they are used: p is readable (its first element; VEC: the vector)
+// whatever n is, and keep() drops what is not there.
+template <int V, typename T, bool VEC> struct Cells {
     using Vec = T __attribute__((ext_vector_type(V)));
     Vec v;
-    __device__ __forceinline__ void load(const T *p, int n, bool vec)
+    __device__ __forceinline__ void load(const T *p, int n)
     {
-        if (vec && n >= V)
+        if constexpr (VEC)
             v = *reinterpret_cast<const Vec *>(p);
         else
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                v[i] = i < n ? p[i] : static_cast<T>(0.f);
+                v[i] = p[i < n ? i : 0];
     }
-    __device__ __forceinline__ void store(T *p, int n, bool vec) const
+    __device__ __forceinline__ void keep(int n)
     {
-        if (vec && n >= V)
-            *reinterpret_cast<Vec *>(p) = v;
-        else
+        if constexpr (VEC && V * sizeof(T) >= 4) {
+            using Bits = unsigned __attribute__((ext_vector_type(V * sizeof(T) / 4)));
+            v = __builtin_bit_cast(Vec, n > 0 ? __builtin_bit_cast(Bits, v) : Bits{});
+        } else
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                v[i] = i < n ? v[i] : static_cast<T>(0.f);
+    }
+    __device__ __forceinline__ void zero() { keep(0); }
+    __device__ __forceinline__ void store(T *p, int n) const
+    {
+        if constexpr (VEC) {
+            if (n > 0)
+                *reinterpret_cast<Vec *>(p) = v;
+        } else
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 if (i < n)

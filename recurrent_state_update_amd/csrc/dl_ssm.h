@@ -71,21 +71,47 @@ template <int J = TB - 1, int TO = 0, typename F> __device__ __forceinline__ voi
     }
 }
 
-// Lane j gets the sum over its row of p[j]: halves of the row trade what the
-// other half keeps, four times.  lane: the lane's place in its row.
-__device__ __forceinline__ float row_sums(const float (&p)[TB], int lane)
+// Lane j gets the sum over its row of p[j] (lane: its place in the row): halves of
+// the row trade what the other half keeps, four times.  The first two are masked
+// additions, each writing the half of the lanes that keeps its sum: 33 instructions,
+// where selecting ahead of every addition takes 45.  (Two wait states before a row
+// operation reads what the instruction ahead may have written, and behind the last
+// for what the compiler places there.)
+__device__ __forceinline__ float row_sums(float (&p)[TB], int lane)
 {
-    float a[8], b[4], c[2];
-    const bool h8 = lane & 8, h4 = lane & 4, h2 = lane & 2, h1 = lane & 1;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        a[i] = (h8 ? p[i + 8] : p[i]) + dpp<0x128>(h8 ? p[i] : p[i + 8]); // row_ror:8
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        b[i] = (h4 ? a[i + 4] : a[i]) + dpp<0x141>(h4 ? a[i] : a[i + 4]); // row_half_mirror
+    asm("s_nop 1\n"
+        "v_add_f32_dpp %0, %0, %0 row_ror:8 row_mask:0xf bank_mask:0x3\n"
+        "v_add_f32_dpp %1, %1, %1 row_ror:8 row_mask:0xf bank_mask:0x3\n"
+        "v_add_f32_dpp %2, %2, %2 row_ror:8 row_mask:0xf bank_mask:0x3\n"
+        "v_add_f32_dpp %3, %3, %3 row_ror:8 row_mask:0xf bank_mask:0x3\n"
+        "v_add_f32_dpp %4, %4, %4 row_ror:8 row_mask:0xf bank_mask:0x3\n"
+        "v_add_f32_dpp %5, %5, %5 row_ror:8 row_mask:0xf bank_mask:0x3\n"
+        "v_add_f32_dpp %6, %6, %6 row_ror:8 row_mask:0xf bank_mask:0x3\n"
+        "v_add_f32_dpp %7, %7, %7 row_ror:8 row_mask:0xf bank_mask:0x3\n"
+        "v_add_f32_dpp %0, %8, %8 row_ror:8 row_mask:0xf bank_mask:0xc\n"
+        "v_add_f32_dpp %4, %12, %12 row_ror:8 row_mask:0xf bank_mask:0xc\n"
+        "v_add_f32_dpp %1, %9, %9 row_ror:8 row_mask:0xf bank_mask:0xc\n"
+        "v_add_f32_dpp %5, %13, %13 row_ror:8 row_mask:0xf bank_mask:0xc\n"
+        "v_add_f32_dpp %2, %10, %10 row_ror:8 row_mask:0xf bank_mask:0xc\n"
+        "v_add_f32_dpp %6, %14, %14 row_ror:8 row_mask:0xf bank_mask:0xc\n"
+        "v_add_f32_dpp %3, %11, %11 row_ror:8 row_mask:0xf bank_mask:0xc\n"
+        "v_add_f32_dpp %7, %15, %15 row_ror:8 row_mask:0xf bank_mask:0xc\n"
+        "v_add_f32_dpp %0, %0, %0 row_half_mirror row_mask:0xf bank_mask:0x5\n"
+        "v_add_f32_dpp %1, %1, %1 row_half_mirror row_mask:0xf bank_mask:0x5\n"
+        "v_add_f32_dpp %2, %2, %2 row_half_mirror row_mask:0xf bank_mask:0x5\n"
+        "v_add_f32_dpp %3, %3, %3 row_half_mirror row_mask:0xf bank_mask:0x5\n"
+        "v_add_f32_dpp %0, %4, %4 row_half_mirror row_mask:0xf bank_mask:0xa\n"
+        "v_add_f32_dpp %1, %5, %5 row_half_mirror row_mask:0xf bank_mask:0xa\n"
+        "v_add_f32_dpp %2, %6, %6 row_half_mirror row_mask:0xf bank_mask:0xa\n"
+        "v_add_f32_dpp %3, %7, %7 row_half_mirror row_mask:0xf bank_mask:0xa\n"
+        "s_nop 1"
+        : "+v"(p[0]), "+v"(p[1]), "+v"(p[2]), "+v"(p[3]), "+v"(p[4]), "+v"(p[5]), "+v"(p[6]), "+v"(p[7])
+        : "v"(p[8]), "v"(p[9]), "v"(p[10]), "v"(p[11]), "v"(p[12]), "v"(p[13]), "v"(p[14]), "v"(p[15]));
+    const bool h2 = lane & 2, h1 = lane & 1;
+    float c[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        c[i] = (h2 ? b[i + 2] : b[i]) + dpp<0x4E>(h2 ? b[i] : b[i + 2]); // quad_perm 2 3 0 1
+        c[i] = (h2 ? p[i + 2] : p[i]) + dpp<0x4E>(h2 ? p[i] : p[i + 2]); // quad_perm 2 3 0 1
     return (h1 ? c[1] : c[0]) + dpp<0xB1>(h1 ? c[0] : c[1]);             // quad_perm 1 0 3 2
 }
 // The sum over the row, in every lane of it.
@@ -95,23 +121,20 @@ __device__ __forceinline__ float row_sum(float x)
 }
 
 // softplus(r) = max(r, 0) + log1p(e), e = e^{-|r|}: the logarithm as
-// 2 artanh(s), s = e / (2 + e) <= 1/3, in odd powers of s up to the 17th (what is
-// left out is below 2^-29 of it), so that small results keep all their bits.
+// 2 artanh(s), s = e / (2 + e) <= 1/3, so that small results keep all their bits.
+// artanh(s) / s is a polynomial in s^2, the best of degree 4 on [0, 1/9] (off by
+// 2^-27.9 at the most).
 __device__ __forceinline__ float softplus(float r, float &e)
 {
     e = __builtin_amdgcn_exp2f(-fabsf(r) * kLog2e);
     const float s = e * __builtin_amdgcn_rcpf(2.f + e), w = s * s;
-    float p = 1.f / 17;
-    p = fmaf(p, w, 1.f / 15);
-    p = fmaf(p, w, 1.f / 13);
-    p = fmaf(p, w, 1.f / 11);
-    p = fmaf(p, w, 1.f / 9);
-    p = fmaf(p, w, 1.f / 7);
-    p = fmaf(p, w, 1.f / 5);
-    p = fmaf(p, w, 1.f / 3);
+    float p = 0.140891671f;
+    p = fmaf(p, w, 0.139803007f);
+    p = fmaf(p, w, 0.200124547f);
+    p = fmaf(p, w, 0.333331585f);
     p = fmaf(p, w, 1.f);
     // (r > 0 ? r : 0 would lose a NaN)
-    return (r < 0.f ? 0.f : r) + 2.f * s * p;
+    return fmaf(2.f * s, p, r < 0.f ? 0.f : r);
 }
 // Its derivative, from the same e.
 __device__ __forceinline__ float softplus_slope(float r, float e)

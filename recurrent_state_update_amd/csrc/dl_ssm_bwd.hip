@@ -93,7 +93,7 @@ template <int T0> __device__ __forceinline__ void fma_bcast_sum(float &even, flo
 // saved one ahead of it, sixteen in registers with their decays; then the adjoint
 // goes back over them.  A wave takes four channels at a time, four times: what
 // it adds up of dB and dC over channels stays in registers meanwhile, B and C too.
-template <typename T, int S> __global__ __launch_bounds__(NT, S == 1 ? 2 : 1) void ssm_bwd_kernel(SsmArgs a)
+template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ? 2 : 1) void ssm_bwd_kernel(SsmArgs a)
 {
     constexpr int XV = 4, XPR = CH / XV;
     constexpr int BN = 16 * S * TB / NT; // states of a token per thread
@@ -111,14 +111,14 @@ template <typename T, int S> __global__ __launch_bounds__(NT, S == 1 ? 2 : 1) vo
 
     {   // rows of no sequence, a share for every piece
         const int first = seqs.at(0), behind = seqs.at(a.N), zeros = first + a.T - behind;
-        Cells<XV, T> zero;
-        zero.load(nullptr, 0, false);
+        Cells<XV, T, VEC> zero;
+        zero.zero();
         for (int i = slot * TB + xt; i < zeros; i += a.slots * TB) {
             const long to = static_cast<long>(i < first ? i : behind + i - first) * a.C + c0 + xc;
-            zero.store(static_cast<T *>(a.dx) + to, nc - xc, a.vec_x);
-            zero.store(static_cast<T *>(a.ddt) + to, nc - xc, a.vec_x);
+            zero.store(static_cast<T *>(a.dx) + to, nc - xc);
+            zero.store(static_cast<T *>(a.ddt) + to, nc - xc);
             if (gate)
-                zero.store(static_cast<T *>(a.dz) + to, nc - xc, a.vec_x);
+                zero.store(static_cast<T *>(a.dz) + to, nc - xc);
         }
     }
     const Piece p(seqs, slot, a.seg);
@@ -159,22 +159,39 @@ template <typename T, int S> __global__ __launch_bounds__(NT, S == 1 ? 2 : 1) vo
             }
     }
 
-    Cells<XV, T> rx, rd, rz, ry;
-    Cells<BN, T> rb, rc;
+    // Loads beyond the channels, states or tokens there are go to the first or last that
+    // is, and are dropped.  The state ahead of a block is loaded with the rest.
+    Cells<XV, T, VEC> rx, rd, rz, ry;
+    Cells<BN, T, VEC> rb, rc;
+    float ahead[S][R];
+    const int col = c0 + (xc < nc ? xc : 0), bcol = g * a.S + (bn < a.S ? bn : 0);
+    const float *const saved = a.saved + (p.none() ? 0 : p.start / TB + p.n + (p.t0 - p.start) / TB) * states;
     const auto read = [&](int t0) {
-        const int n = t0 + xt < len ? nc - xc : 0;
-        const long t = p.t0 + t0 + xt, col = c0 + xc;
-        rx.load(static_cast<const T *>(a.x) + t * a.xs + col, n, a.vec_x);
-        rd.load(static_cast<const T *>(a.dt) + t * a.dts + col, n, a.vec_x);
-        ry.load(static_cast<const T *>(a.dy) + t * a.C + col, n, a.vec_x);
+        const long t = p.t0 + min(t0 + xt, len - 1);
+        rx.load(static_cast<const T *>(a.x) + t * a.xs + col, nc - xc);
+        rd.load(static_cast<const T *>(a.dt) + t * a.dts + col, nc - xc);
+        ry.load(static_cast<const T *>(a.dy) + t * a.C + col, nc - xc);
         if (gate)
-            rz.load(static_cast<const T *>(a.z) + t * a.zs + col, n, a.vec_x);
-        const int m = t0 + bt < len ? a.S - bn : 0;
-        const long tb = p.t0 + t0 + bt, of_g = static_cast<long>(g) * a.S + bn;
-        rb.load(static_cast<const T *>(a.b) + tb * a.bs + of_g, m, a.vec_b);
-        rc.load(static_cast<const T *>(a.c) + tb * a.cs + of_g, m, a.vec_b);
+            rz.load(static_cast<const T *>(a.z) + t * a.zs + col, nc - xc);
+        const long u = p.t0 + min(t0 + bt, len - 1);
+        rb.load(static_cast<const T *>(a.b) + u * a.bs + bcol, a.S - bn);
+        rc.load(static_cast<const T *>(a.c) + u * a.cs + bcol, a.S - bn);
+        const float *const from = saved + t0 / TB * states;
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                ahead[s][i] = from[static_cast<long>(c0 + min(in_tile(i), nc - 1)) * a.S + min(j + 16 * s, a.S - 1)];
     };
-    const auto put = [&](Stage<S> &st) {
+    const auto put = [&](Stage<S> &st, int t0) {
+        const int n = t0 + xt < len ? nc - xc : 0, m = t0 + bt < len ? a.S - bn : 0;
+        rx.keep(n);
+        rd.keep(n);
+        ry.keep(n);
+        if (gate)
+            rz.keep(n);
+        rb.keep(m);
+        rc.keep(m);
 #pragma unroll
         for (int i = 0; i < XV; ++i) {
             st.x[xc + i][xt] = to_f(rx.v[i]);
@@ -191,9 +208,18 @@ template <typename T, int S> __global__ __launch_bounds__(NT, S == 1 ? 2 : 1) vo
     };
 
     const int blocks = (len + TB - 1) / TB;
+    float start[S][R]; // the states ahead of the block
+    const auto take = [&] {
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                start[s][i] = in_tile(i) < nc && j + 16 * s < a.S ? ahead[s][i] : 0.f;
+    };
     if (blocks > 0) {
         read((blocks - 1) * TB);
-        put(sh.in[0]);
+        put(sh.in[0], (blocks - 1) * TB);
+        take();
     }
     __syncthreads();
     for (int k = 0; k < blocks; ++k) {
@@ -201,7 +227,6 @@ template <typename T, int S> __global__ __launch_bounds__(NT, S == 1 ? 2 : 1) vo
         const int t0 = (blocks - 1 - k) * TB;
         if (k + 1 < blocks)
             read(t0 - TB);
-        const float *saved = a.saved + (p.start / TB + p.n + (p.t0 - p.start + t0) / TB) * states;
         const bool live = t0 + j < len;
         float sy[R], sq[R], sr[R];
 #pragma unroll
@@ -209,11 +234,7 @@ template <typename T, int S> __global__ __launch_bounds__(NT, S == 1 ? 2 : 1) vo
             sy[i] = sq[i] = sr[i] = 0.f;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            float B[TB], C[TB], dB[TB], dC[TB], start[R];
-#pragma unroll
-            for (int i = 0; i < R; ++i)
-                start[i] = in_tile(i) < nc && j + 16 * s < a.S
-                               ? saved[static_cast<long>(c0 + in_tile(i)) * a.S + j + 16 * s] : 0.f;
+            float B[TB], C[TB], dB[TB], dC[TB];
 #pragma unroll
             for (int t = 0; t < TB; t += 4) {
                 const f32x4 b = *reinterpret_cast<const f32x4 *>(&st.b[j + 16 * s][t]),
@@ -237,10 +258,10 @@ template <typename T, int S> __global__ __launch_bounds__(NT, S == 1 ? 2 : 1) vo
                     dy *= z * sigmoid(z);
                 }
                 float u = delta * st.x[c][j];
-                in_order({&delta, &u, &dy, &start[i]});
+                in_order({&delta, &u, &dy, &start[s][i]});
                 // forward over the block
                 float d[TB], h[TB + 1], y[TB], f = G[i][s];
-                h[0] = start[i];
+                h[0] = start[s][i];
                 for_tokens([&](auto J) {
                     constexpr int t = decltype(J)::value;
                     d[t] = __builtin_amdgcn_exp2f(row_bcast<t>(delta) * rate[i][s]);
@@ -301,17 +322,19 @@ template <typename T, int S> __global__ __launch_bounds__(NT, S == 1 ? 2 : 1) vo
             dD[i] = fmaf(dy, x, dD[i]);
             dbias[i] += dt;
         }
-        if (k + 1 < blocks)
-            put(sh.in[(k + 1) % 3]);
+        if (k + 1 < blocks) {
+            put(sh.in[(k + 1) % 3], t0 - TB);
+            take();
+        }
         __syncthreads();
         if (t0 + xt < len) {
             const long to = static_cast<long>(p.t0 + t0 + xt) * a.C + c0 + xc;
-            Cells<XV, T> v;
+            Cells<XV, T, VEC> v;
             const auto out = [&](void *dst, const float (&src)[CH][LD]) {
 #pragma unroll
                 for (int i = 0; i < XV; ++i)
                     v.v[i] = static_cast<T>(src[xc + i][xt]);
-                v.store(static_cast<T *>(dst) + to, nc - xc, a.vec_x);
+                v.store(static_cast<T *>(dst) + to, nc - xc);
             };
             out(a.dx, st.x);
             out(a.ddt, st.dt);
@@ -375,15 +398,20 @@ template <typename T> __global__ __launch_bounds__(NT) void ssm_bc_kernel(SsmArg
     out[(static_cast<long>(t) * a.G + g) * a.S + (n < a.S ? n : n - a.S)] = static_cast<T>(static_cast<float>(x));
 }
 
+template <typename T, int S, bool VEC> void launch(const SsmArgs &a, dim3 grid, hipStream_t st)
+{
+    hipLaunchKernelGGL((ssm_bwd_kernel<T, S, VEC>), grid, dim3(NT), 0, st, a);
+}
 template <typename T> hipError_t bwd_t(const SsmArgs &a, hipStream_t st)
 {
     const dim3 grid(static_cast<unsigned>(static_cast<long>(a.slots) * a.tiles));
+    const bool vec = a.vec_x && a.vec_b;
     if (a.S <= 16)
-        hipLaunchKernelGGL((ssm_bwd_kernel<T, 1>), grid, dim3(NT), 0, st, a);
+        vec ? launch<T, 1, true>(a, grid, st) : launch<T, 1, false>(a, grid, st);
     else if (a.S <= 32)
-        hipLaunchKernelGGL((ssm_bwd_kernel<T, 2>), grid, dim3(NT), 0, st, a);
+        vec ? launch<T, 2, true>(a, grid, st) : launch<T, 2, false>(a, grid, st);
     else
-        hipLaunchKernelGGL((ssm_bwd_kernel<T, 4>), grid, dim3(NT), 0, st, a);
+        vec ? launch<T, 4, true>(a, grid, st) : launch<T, 4, false>(a, grid, st);
     if (hipError_t e = hipGetLastError(); e != hipSuccess || a.T == 0)
         return e;
     const long n = static_cast<long>(a.T) * 2 * a.G * a.S;
