@@ -431,8 +431,9 @@ typedef struct {
  * needs (the state ahead of every 16 tokens), and of the backward pass's
  * workspace, each 256-byte aligned; 0 for sizes that are not supported: 1 <=
  * states <= 64, channels a multiple of groups, channels <= 2^20, tokens and seqs
- * <= 2^30, (seqs + tokens/64) * channels/16 < 2^24 (channels rounded up to
- * sixteens per group), tokens * groups * states < 2^31. */
+ * <= 2^30, (seqs + tokens/64) * channels/16 < 2^23 (channels rounded up to
+ * sixteens per group, and their number to a multiple of eight), tokens * groups *
+ * states < 2^31, strides <= 2^22. */
 size_t dl_ssm_workspace_bytes(const dl_ssm_desc *d);
 size_t dl_ssm_saved_bytes(const dl_ssm_desc *d);
 size_t dl_ssm_backward_workspace_bytes(const dl_ssm_desc *d);

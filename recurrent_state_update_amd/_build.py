@@ -27,7 +27,8 @@ LIB = os.path.join(PKG, "libdeltalog.so")
 CEILING_LIB = os.path.join(PKG, "libdlceiling.so")
 SOURCES = ["dl_api.hip", "dl_device.hip", "dl_gdn.hip", "dl_kda.hip", "dl_rwkv6.hip",
            "dl_sequence_api.hip", "dl_scan_gdn.hip", "dl_scan_kda.hip", "dl_scan_rwkv6.hip", "dl_norm.hip",
-           "dl_layer_api.hip", "dl_conv.hip", "dl_ssm.hip", "dl_ssm_bwd.hip"]
+           "dl_layer_api.hip", "dl_conv.hip", "dl_ssm.hip", "dl_ssm_ahead.hip",
+           "dl_ssm_bwd.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

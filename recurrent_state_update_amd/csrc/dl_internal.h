@@ -242,8 +242,9 @@ struct SsmArgs {
     float *part_a, *part_d, *part_bias;   // [slots][C][S], [slots][C], [slots][C]
 };
 hipError_t launch_ssm_scan(int dtype, const SsmArgs &a, hipStream_t st);
-// The adjoint's segments; `ahead` has the forward kernel's tiles.
-hipError_t launch_ssm_ahead_of_adjoint(int dtype, const SsmArgs &a, hipStream_t st);
+// What segments add to the state behind them, or the gradient ahead of them.
+hipError_t launch_ssm_ahead(int dtype, bool adjoint, const SsmArgs &a, hipStream_t st);
+// `ahead`: the same with the forward kernel's tiles.
 hipError_t launch_ssm_backward(int dtype, const SsmArgs &ahead, const SsmArgs &a, hipStream_t st);
 hipError_t launch_ssm_step(int dtype, const SsmArgs &a, hipStream_t st);
 

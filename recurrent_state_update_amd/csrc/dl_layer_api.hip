@@ -14,6 +14,7 @@ using namespace dl::host;
 // Launches count work-items in 32 bits, 256 a workgroup.
 constexpr long long kMostBlocks = 1LL << 24;
 constexpr int kMostStates = 64, kMostChannels = 1 << 20;
+constexpr long long kMostStride = 1LL << 22;
 
 dl_status status(hipError_t e) { return e == hipSuccess ? DL_OK : DL_E_HIP; }
 
@@ -101,7 +102,7 @@ dl_status check_ssm(const dl_ssm_desc *d)
                             ((d->channels / d->groups + dl::kSsmTile - 1) / dl::kSsmTile);
     // a workgroup per sequence (or segment, not shorter than 64 tokens) and tile; a
     // thread per element of dB and dC
-    if ((static_cast<long long>(d->seqs) + d->tokens / 64) * tiles >= kMostBlocks ||
+    if ((static_cast<long long>(d->seqs) + d->tokens / 64) * ((tiles + 7) / 8 * 8) * 2 >= kMostBlocks ||
         2LL * d->tokens * d->groups * d->states >= kMostBlocks * 256)
         return DL_E_SHAPE;
     return DL_OK;
@@ -166,6 +167,10 @@ dl_status ssm_inputs(const dl_ssm_desc *d, bool step, dl::SsmArgs &a, Span (&r)[
                     cs = d->c_stride ? d->c_stride : GS;
     if (xs < C || dts < C || zs < C || bs < GS || cs < GS)
         return DL_E_INVALID;
+    // a stage's rows are addressed in 32 bits
+    for (long long stride : {xs, dts, zs, bs, cs})
+        if (stride > kMostStride)
+            return DL_E_SHAPE;
     const size_t es = elem(d->dtype);
     for (const void *p : {d->x, d->dt, d->z, d->b, d->c})
         if (!aligned(p, es))

@@ -183,12 +183,156 @@ struct Piece {
     __device__ __forceinline__ bool none() const { return n < 0; }
 };
 
-// Work-items of consecutive numbers on one XCD (workgroup b runs on XCD b % 8):
-// neighbouring channel tiles share cache lines, which the XCD's L2 then holds once.
-__device__ __forceinline__ long xcd_order(long b, long total)
-{
-    const long q = total / 8, r = total % 8, x = b % 8;
-    return x * q + (x < r ? x : r) + b / 8;
-}
+// The slot and tile of a workgroup, which runs on XCD b % 8: every slot's tiles go to
+// the XCDs in runs, since neighbours share cache lines, which the XCD's L2 then holds
+// once; all slots alike (sequences differ in length), each a run further, which evens
+// out what 8 does not divide.  tile: -1 if there is none.
+struct Work {
+    int slot, tile;
+    __device__ __forceinline__ Work(unsigned b, int tiles)
+    {
+        const int run = (tiles + 7) / 8, i = b / 8;
+        slot = i / run;
+        tile = (b + slot) % 8 * run + i % run;
+        if (tile >= tiles)
+            tile = -1;
+    }
+};
+inline long work_groups(const SsmArgs &a) { return static_cast<long>(a.slots) * ((a.tiles + 7) / 8) * 8; }
+
+// ---- the forward kernels' operands: a stage of TT tokens of a workgroup's channels
+
+constexpr int CH = kSsmTile; // channels per workgroup: four waves of four
+constexpr int LOADERS = 256; // threads that bring a stage in
+static_assert(CH == 16, "four waves of four rows");
+
+template <int S, int TT> struct Stage {
+    static constexpr int XLD = TT + 2, BLD = TT + 4;
+    float x[CH][XLD], dt[CH][XLD], z[CH][XLD];
+    alignas(16) float b[16 * S][BLD], c[16 * S][BLD];
+};
+
+// What of it a kernel reads: the adjoint's has dy and C in the place of x and B.
+struct Sources {
+    const void *x, *dt, *z, *b, *c; // z: NULL without a gate
+    long xs, dts, zs, bs, cs;
+};
+
+// A thread's part: a few channels (states) of one token, next to each other, loaded
+// into registers while the stage before is worked on, and put in LDS transposed.
+// Every load goes to a row that is there, without a condition, so that nothing waits
+// for it early; what is not there is dropped when put.
+template <typename T, int S, int TT, bool VEC> struct Loader {
+    static constexpr int XV = CH * TT / LOADERS, XPR = CH / XV; // channels, threads per token
+    static constexpr int BV = 4, BPR = 16 * S / BV, BTOK = LOADERS / BPR, BK = TT / BTOK;
+    static_assert(XPR * TT == LOADERS && BK * BTOK == TT && BK > 0, "every thread loads as much");
+    Sources s;
+    int xt, xc, bt, bn, nx, nb; // token, channel, token, state; channels and states there are
+    int col, state;             // the first column of x's and of B's rows
+    bool gate;
+    long t0;
+    int len;
+    Cells<XV, T, VEC> rx, rd, rz;
+    Cells<BV, T, VEC> rb[BK], rc[BK];
+
+    __device__ __forceinline__ Loader(const Sources &s, int id, int c0, int channels, int b0, int states)
+        : s(s), xt(id / XPR), xc(id % XPR * XV), bt(id / BPR), bn(id % BPR * BV), nx(channels - xc), nb(states - bn),
+          col(c0 + (nx > 0 ? xc : 0)), state(b0 + (nb > 0 ? bn : 0)), gate(s.z)
+    {
+    }
+    __device__ __forceinline__ void piece(int first, int tokens)
+    {
+        t0 = first;
+        len = tokens;
+    }
+    // Row `row` of the stage's, at base plus a lane's own columns: the base is the same
+    // for all lanes, and what differs fits 32 bits (64 rows of at most 2^22 elements).
+    template <typename Cell>
+    __device__ __forceinline__ void row(Cell &r, const void *p, long stride, int from, int at, int col, int n)
+    {
+        const T *const base = static_cast<const T *>(p) + (t0 + from) * stride;
+        r.load(base + static_cast<unsigned>(min(at, len - 1 - from) * static_cast<int>(stride) + col), n);
+    }
+    // Z, C: whether those are ever wanted.  Behind the piece's end: its last row.
+    template <bool Z, bool C> __device__ __forceinline__ void read(int from)
+    {
+        from = min(from, (len - 1) / TT * TT);
+        row(rx, s.x, s.xs, from, xt, col, nx);
+        row(rd, s.dt, s.dts, from, xt, col, nx);
+        if constexpr (Z)
+            row(rz, gate ? s.z : s.x, gate ? s.zs : s.xs, from, xt, col, nx);
+#pragma unroll
+        for (int k = 0; k < BK; ++k) {
+            row(rb[k], s.b, s.bs, from, bt + k * BTOK, state, nb);
+            if constexpr (C)
+                row(rc[k], s.c, s.cs, from, bt + k * BTOK, state, nb);
+        }
+    }
+    template <bool Z, bool C> __device__ __forceinline__ void put(Stage<S, TT> &st, int from)
+    {
+        const int n = from + xt < len ? nx : 0;
+        rx.keep(n);
+        rd.keep(n);
+        if constexpr (Z)
+            rz.keep(gate ? n : 0);
+#pragma unroll
+        for (int i = 0; i < XV; ++i) {
+            st.x[xc + i][xt] = to_f(rx.v[i]);
+            st.dt[xc + i][xt] = to_f(rd.v[i]);
+            if constexpr (Z)
+                st.z[xc + i][xt] = to_f(rz.v[i]);
+        }
+#pragma unroll
+        for (int k = 0; k < BK; ++k) {
+            const int m = from + bt + k * BTOK < len ? nb : 0;
+            rb[k].keep(m);
+            if constexpr (C)
+                rc[k].keep(m);
+#pragma unroll
+            for (int i = 0; i < BV; ++i) {
+                st.b[bn + i][bt + k * BTOK] = to_f(rb[k].v[i]);
+                if constexpr (C)
+                    st.c[bn + i][bt + k * BTOK] = to_f(rc[k].v[i]);
+            }
+        }
+    }
+};
+
+// What lane j of a row forms of its tokens at, at + 16, ... of a stage: x, delta, the
+// gate's silu (1 without one).  Straight code for all blocks of the stage, whose chains
+// of dependent operations then overlap; tokens behind the `live` ones have delta 0 and
+// change nothing.
+template <int NB> struct Own {
+    float x[NB], delta[NB], z[NB];
+    template <bool Z, typename St>
+    __device__ __forceinline__ void form(const St &st, int row, int j, int live, float bias, int softplus_on, float no_gate)
+    {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int at = i * TB + j;
+            float e, raw = st.dt[row][at] + bias, soft = softplus(raw, e);
+            asm("" : "+v"(soft)); // a selection, not a branch
+            x[i] = st.x[row][at];
+            delta[i] = at < live ? softplus_on ? soft : raw : 0.f;
+            z[i] = 1.f;
+            if constexpr (Z) {
+                const float v = st.z[row][at]; // 0 without a gate
+                z[i] = fmaf(v, sigmoid(v), no_gate);
+            }
+        }
+    }
+};
+
+// The workgroup's channels: tile `tile` of sixteen, within one group.
+struct Tile {
+    int g, c0, nc; // group, first channel, channels there are
+    __device__ __forceinline__ Tile(const SsmArgs &a, int tile, int width)
+    {
+        const int per = (a.CG + width - 1) / width;
+        g = tile / per;
+        c0 = g * a.CG + tile % per * width;
+        nc = min(width, (g + 1) * a.CG - c0);
+    }
+};
 
 } // namespace dl::ssm

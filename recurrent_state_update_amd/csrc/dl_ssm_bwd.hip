@@ -9,19 +9,19 @@ using namespace ssm;
 namespace {
 
 constexpr int NT = 256, WAVES = 4;
-constexpr int CH = kSsmGradTile; // channels per workgroup
-constexpr int R = CH / (WAVES * 4); // channels of a row of lanes, one after the other
+constexpr int GC = kSsmGradTile; // channels per workgroup
+constexpr int R = GC / (WAVES * 4); // channels of a row of lanes, one after the other
 constexpr int LD = TB + 1, BLD = TB + 4;
-static_assert(CH * TB == NT * 4, "four channels of a token per thread");
+static_assert(GC * TB == NT * 4, "four channels of a token per thread");
 
-template <int S> struct Stage {
-    float x[CH][LD], dt[CH][LD], z[CH][LD], dy[CH][LD];
+template <int S> struct GradStage {
+    float x[GC][LD], dt[GC][LD], z[GC][LD], dy[GC][LD];
     alignas(16) float b[16 * S][BLD], c[16 * S][BLD];
 };
 // A lane puts dx, ddt and dz where x, dt and z were, which nothing else reads:
 // three stages, so that one can be stored while the next but one is put in.
 template <int S> struct Shared {
-    Stage<S> in[3];
+    GradStage<S> in[3];
     alignas(16) float db[2][WAVES][16 * S][TB], dc[2][WAVES][16 * S][TB];
 };
 
@@ -95,14 +95,16 @@ template <int T0> __device__ __forceinline__ void fma_bcast_sum(float &even, flo
 // it adds up of dB and dC over channels stays in registers meanwhile, B and C too.
 template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ? 2 : 1) void ssm_bwd_kernel(SsmArgs a)
 {
-    constexpr int XV = 4, XPR = CH / XV;
+    constexpr int XV = 4, XPR = GC / XV;
     constexpr int BN = 16 * S * TB / NT; // states of a token per thread
     __shared__ Shared<S> sh;
 
-    const long work = xcd_order(blockIdx.x, gridDim.x);
-    const int slot = work / a.tiles, tile = work % a.tiles;
-    const int per = (a.CG + CH - 1) / CH, g = tile / per, c0 = g * a.CG + tile % per * CH;
-    const int nc = min(CH, (g + 1) * a.CG - c0);
+    const Work work(blockIdx.x, a.tiles);
+    if (work.tile < 0)
+        return;
+    const int slot = work.slot, of_group = work.tile % ((a.CG + GC - 1) / GC);
+    const Tile tile(a, work.tile, GC);
+    const int g = tile.g, c0 = tile.c0, nc = tile.nc;
     const Sequences seqs{a.cu, a.T, a.N};
     const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, j = lane % 16, row = lane / 16;
     const int xt = tid / XPR, xc = tid % XPR * XV, bt = tid / 16, bn = tid % 16 * BN;
@@ -183,7 +185,7 @@ template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ?
             for (int i = 0; i < R; ++i)
                 ahead[s][i] = from[static_cast<long>(c0 + min(in_tile(i), nc - 1)) * a.S + min(j + 16 * s, a.S - 1)];
     };
-    const auto put = [&](Stage<S> &st, int t0) {
+    const auto put = [&](GradStage<S> &st, int t0) {
         const int n = t0 + xt < len ? nc - xc : 0, m = t0 + bt < len ? a.S - bn : 0;
         rx.keep(n);
         rd.keep(n);
@@ -223,7 +225,7 @@ template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ?
     }
     __syncthreads();
     for (int k = 0; k < blocks; ++k) {
-        Stage<S> &st = sh.in[k % 3];
+        GradStage<S> &st = sh.in[k % 3];
         const int t0 = (blocks - 1 - k) * TB;
         if (k + 1 < blocks)
             read(t0 - TB);
@@ -330,7 +332,7 @@ template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ?
         if (t0 + xt < len) {
             const long to = static_cast<long>(p.t0 + t0 + xt) * a.C + c0 + xc;
             Cells<XV, T, VEC> v;
-            const auto out = [&](void *dst, const float (&src)[CH][LD]) {
+            const auto out = [&](void *dst, const float (&src)[GC][LD]) {
 #pragma unroll
                 for (int i = 0; i < XV; ++i)
                     v.v[i] = static_cast<T>(src[xc + i][xt]);
@@ -343,7 +345,7 @@ template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ?
         }
         if (t0 + bt < len) {
             // [tile of the group][token][group][B's states, C's states]
-            float *to = a.part_bc + ((static_cast<long>(tile % per) * a.T + p.t0 + t0 + bt) * a.G + g) * 2 * a.S;
+            float *to = a.part_bc + ((static_cast<long>(of_group) * a.T + p.t0 + t0 + bt) * a.G + g) * 2 * a.S;
 #pragma unroll
             for (int i = 0; i < BN; ++i) {
                 const int n = bn + i;
@@ -404,7 +406,7 @@ template <typename T, int S, bool VEC> void launch(const SsmArgs &a, dim3 grid, 
 }
 template <typename T> hipError_t bwd_t(const SsmArgs &a, hipStream_t st)
 {
-    const dim3 grid(static_cast<unsigned>(static_cast<long>(a.slots) * a.tiles));
+    const dim3 grid(static_cast<unsigned>(work_groups(a)));
     const bool vec = a.vec_x && a.vec_b;
     if (a.S <= 16)
         vec ? launch<T, 1, true>(a, grid, st) : launch<T, 1, false>(a, grid, st);
@@ -416,7 +418,7 @@ template <typename T> hipError_t bwd_t(const SsmArgs &a, hipStream_t st)
         return e;
     const long n = static_cast<long>(a.T) * 2 * a.G * a.S;
     hipLaunchKernelGGL((ssm_bc_kernel<T>), dim3(static_cast<unsigned>((n + NT - 1) / NT)), dim3(NT), 0, st, a,
-                       (a.CG + CH - 1) / CH);
+                       (a.CG + GC - 1) / GC);
     return hipGetLastError();
 }
 
@@ -426,7 +428,7 @@ hipError_t launch_ssm_backward(int dtype, const SsmArgs &ahead, const SsmArgs &a
 {
     hipError_t e = hipSuccess;
     if (a.seg)
-        e = launch_ssm_ahead_of_adjoint(dtype, ahead, st);
+        e = launch_ssm_ahead(dtype, true, ahead, st);
     if (e == hipSuccess)
         e = dtype == F32 ? bwd_t<float>(a, st) : bwd_t<__bf16>(a, st);
     if (e == hipSuccess)

@@ -14,7 +14,7 @@ import torch
 
 from . import (_check, _dtype_id, _lib, dl_conv_desc, dl_short_conv_workspace_bytes, dl_ssm_backward_workspace_bytes,
                dl_ssm_desc, dl_ssm_saved_bytes, dl_ssm_workspace_bytes)
-from .sequence import _bytes, _count, _current, _gpu, _no_grad, _on, _p, _plain, _rows, _tensor, _wants_grad
+from .sequence import _MOST_STRIDE, _bytes, _count, _current, _gpu, _no_grad, _on, _p, _plain, _rows, _tensor, _wants_grad
 
 _MOST_STATES = 64
 
@@ -52,7 +52,7 @@ def _channel_rows(t, lead):
         return None, 0
     if t.is_contiguous():
         return t, t.shape[-1]
-    wide, stride = _rows(t.unsqueeze(-2), lead)
+    wide, stride = _rows(t.unsqueeze(-2), lead, _MOST_STRIDE)
     return wide.squeeze(-2), stride
 
 
@@ -235,7 +235,7 @@ class _Ssm:
         and their descriptor."""
         n = len(self.lead)
         (x, xs), (dt, dts), (z, zs) = (_channel_rows(t, n) for t in (x, dt, z))
-        (B, bs), (C, cs) = (_rows(t, n) if self.grouped else _channel_rows(t, n) for t in (B, C))
+        (B, bs), (C, cs) = (_rows(t, n, _MOST_STRIDE) if self.grouped else _channel_rows(t, n) for t in (B, C))
         A, D, dt_bias = _whole(A), _whole(D), _whole(dt_bias)
         return (x, dt, A, B, C, D, z, dt_bias, cu_seqlens), dl_ssm_desc(
             self.dti, self.T, N, self.C, self.S, self.G, self.softplus, xs, dts, zs, bs, cs, _p(cu_seqlens),
