@@ -396,7 +396,7 @@ typedef struct {
  * first; NULL: zero).  y [tokens, channels] contiguous; final_state (NULL: not
  * wanted) as initial, for what follows.  Nothing may overlap what is written.
  * Sizes: 2 <= taps <= 4, channels <= 2^20, tokens and seqs <= 2^30,
- * (tokens + seqs) * channels < 2^34. */
+ * (tokens + seqs) * channels < 2^34, x_stride <= 2^22. */
 dl_status dl_short_conv(const dl_conv_desc *d, const void *initial, void *final_state, void *y, void *stream);
 /* Its gradients from dy [tokens, channels] and d_final (as final_state; either
  * NULL: zero): dx (contiguous), dweight, dbias (NULL: not wanted; else the

@@ -118,7 +118,7 @@ template <typename T, int W, int V, bool VEC> struct Lane {
         sums(s);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float sig = 1.f / (1.f + expf(-s[i]));
+            const float sig = sigmoid(s[i]);
             ds[i] = a.silu ? dy[i] * sig * fmaf(s[i], 1.f - sig, 1.f) : dy[i];
         }
     }
@@ -154,24 +154,29 @@ template <typename T, int W, int V, bool VEC> __global__ __launch_bounds__(NT) v
     if (t0 >= t1)
         return;
     Lane<T, W, V, VEC> l(a, c);
+    // rows as offsets from the run's first (of at most 64 rows): the last one again behind it
+    const T *const x = static_cast<const T *>(a.x) + t0 * a.xs + c;
+    T *const y = static_cast<T *>(a.y) + static_cast<long>(t0) * a.C + c;
+    const unsigned xs = a.xs, last = (t1 - 1 - t0) * xs;
+    unsigned from = 0;
     Cells<V, T, VEC> next[U];
-    const auto read = [&](int t) {
+    const auto read = [&] {
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-            next[i].load(static_cast<const T *>(a.x) + min(t + i, t1 - 1) * a.xs + c, l.m);
+        for (int i = 0; i < U; ++i) {
+            next[i].load(x + min(from, last), l.m);
+            from += xs;
+        }
     };
-    read(t0);
+    read();
     l.begin(t0);
     for (int t = t0; t < t1; t += U) {
         Cells<V, T, VEC> now[U];
 #pragma unroll
         for (int i = 0; i < U; ++i)
             now[i] = next[i];
-        read(t + U);
+        read();
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            if (t + i >= t1)
-                break;
             const bool live = l.enter(t + i);
             now[i].get(l.x[W - 1]);
             float s[V];
@@ -179,12 +184,13 @@ template <typename T, int W, int V, bool VEC> __global__ __launch_bounds__(NT) v
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 if (a.silu)
-                    s[e] = s[e] / (1.f + expf(-s[e]));
+                    s[e] *= sigmoid(s[e]);
                 s[e] = live ? s[e] : 0.f;
             }
-            Cells<V, T, VEC> y;
-            y.put(s);
-            y.store(static_cast<T *>(a.y) + static_cast<long>(t + i) * a.C + c, l.m);
+            Cells<V, T, VEC> out;
+            out.put(s);
+            if (t + i < t1)
+                out.store(y + static_cast<unsigned>(t + i - t0) * static_cast<unsigned>(a.C), l.m);
             l.leave();
         }
     }
@@ -264,18 +270,25 @@ template <typename T, int W, int V, bool VEC> __global__ __launch_bounds__(NT) v
         r.store(static_cast<T *>(a.dx) + static_cast<long>(t) * a.C + c, l.m);
     };
     if (t0 < t1) {
-        Cells<V, T, VEC> nx, ny;
-        const auto read = [&](int t) {
-            t = min(t, a.T - 1);
-            nx.load(static_cast<const T *>(a.x) + t * a.xs + c, l.m);
-            if (a.dy)
-                ny.load(static_cast<const T *>(a.dy) + static_cast<long>(t) * a.C + c, l.m);
+        constexpr int U = 4; // tokens loaded ahead
+        const int stop = min(t1 + W - 1, a.T);
+        const T *const x = static_cast<const T *>(a.x) + t0 * a.xs + c,
+                *const dy = static_cast<const T *>(a.dy ? a.dy : a.x) + t0 * (a.dy ? a.C : a.xs) + c;
+        const unsigned xs = a.xs, ys = a.dy ? a.C : a.xs, xlast = (stop - 1 - t0) * xs, ylast = (stop - 1 - t0) * ys;
+        unsigned xfrom = 0, yfrom = 0;
+        Cells<V, T, VEC> nx[U], ny[U];
+        const auto read = [&] {
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                nx[i].load(x + min(xfrom, xlast), l.m);
+                ny[i].load(dy + min(yfrom, ylast), l.m);
+                xfrom += xs;
+                yfrom += ys;
+            }
         };
-        read(t0);
-        l.begin(t0);
-        int t = t0;
-        for (; t < t1 + W - 1; ++t) {
-            if (t == l.end) { // behind a sequence's last token: what is gathered is whole
+        // Token t; whether there are more of use.
+        const auto token = [&](int t, const Cells<V, T, VEC> &cx, Cells<V, T, VEC> &cy) {
+            if (t == l.end) // behind a sequence's last token: what is gathered is whole
 #pragma unroll
                 for (int k = 1; k < W; ++k) {
                     done(g[k], t - k);
@@ -283,40 +296,34 @@ template <typename T, int W, int V, bool VEC> __global__ __launch_bounds__(NT) v
                     for (int i = 0; i < V; ++i)
                         g[k][i] = 0.f;
                 }
-            }
-            if (t >= a.T || (t >= t1 && t >= l.end))
-                break;
+            if (t >= stop || (t >= t1 && t >= l.end))
+                return false;
             const bool live = l.enter(t);
-            float dy[V], ds[V];
-            nx.get(l.x[W - 1]);
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                dy[i] = 0.f;
-            if (a.dy)
-                ny.get(dy);
-            read(t + 1);
-            if (!live) { // of no sequence
-                if (t < t1) {
-                    Cells<V, T, VEC> zero;
-                    zero.zero();
-                    zero.store(static_cast<T *>(a.dx) + static_cast<long>(t) * a.C + c, l.m);
-                }
-                continue;
-            }
-            l.slope(ds, dy);
+            float dyv[V], ds[V];
+            cx.get(l.x[W - 1]);
+            cy.keep(a.dy && live ? l.m : 0);
+            cy.get(dyv);
+            l.slope(ds, dyv);
+            const bool own = live && t < t1;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
+                ds[i] = live ? ds[i] : 0.f; // (of no sequence)
 #pragma unroll
                 for (int k = 0; k < W; ++k)
                     g[k][i] = fmaf(l.w[W - 1 - k][i], ds[i], g[k][i]);
-                if (t < t1) {
-                    db[i] += ds[i];
+                const float mine = own ? ds[i] : 0.f;
+                db[i] += mine;
 #pragma unroll
-                    for (int j = 0; j < W; ++j)
-                        dw[j][i] = fmaf(ds[i], l.x[j][i], dw[j][i]);
-                }
+                for (int j = 0; j < W; ++j)
+                    dw[j][i] = own ? fmaf(mine, l.x[j][i], dw[j][i]) : dw[j][i];
             }
-            done(g[W - 1], t - (W - 1));
+            if (live) {
+                done(g[W - 1], t - (W - 1));
+            } else if (t < t1) {
+                Cells<V, T, VEC> zero;
+                zero.zero();
+                zero.store(static_cast<T *>(a.dx) + static_cast<long>(t) * a.C + c, l.m);
+            }
 #pragma unroll
             for (int i = 0; i < V; ++i) {
 #pragma unroll
@@ -325,6 +332,22 @@ template <typename T, int W, int V, bool VEC> __global__ __launch_bounds__(NT) v
                 g[0][i] = 0.f;
             }
             l.leave();
+            return true;
+        };
+        read();
+        l.begin(t0);
+        bool more = true;
+        for (int t = t0; more; t += U) {
+            Cells<V, T, VEC> cx[U], cy[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                cx[i] = nx[i];
+                cy[i] = ny[i];
+            }
+            read();
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                more = more && token(t + i, cx[i], cy[i]);
         }
     }
 #pragma unroll
@@ -366,7 +389,7 @@ template <typename T, int W, int V, bool VEC> __global__ __launch_bounds__(NT) v
     if (a.silu)
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            s[i] = s[i] / (1.f + expf(-s[i]));
+            s[i] *= sigmoid(s[i]);
     Cells<V, T, VEC> y;
     y.put(s);
     y.store(static_cast<T *>(a.y) + static_cast<long>(t) * a.C + c, l.m);

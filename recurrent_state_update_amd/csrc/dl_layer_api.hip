@@ -67,6 +67,8 @@ dl_status conv_inputs(const dl_conv_desc *d, bool step, dl::ConvArgs &a, Span (&
         return DL_E_INVALID;
     if (!step && !d->cu_seqlens && d->tokens % d->seqs != 0)
         return DL_E_INVALID;
+    if (xs > kMostStride) // a run's rows are addressed in 32 bits
+        return DL_E_SHAPE;
     const size_t es = elem(d->dtype);
     if (!aligned(d->x, es) || !aligned(d->weight, 4) || !aligned(d->bias, 4) || !aligned(d->cu_seqlens, 4))
         return DL_E_ALIGN;
@@ -120,7 +122,7 @@ int ssm_segment(const dl_ssm_desc *d, bool backward)
 {
     const long tiles = tiles_of(d, backward ? dl::kSsmGradTile : dl::kSsmTile), wgs = tiles * d->seqs;
     const long want = backward ? 512 : 256, each = d->tokens / d->seqs;
-    if (wgs * 2 > want || each < 256)
+    if (wgs * 2 > want || each < (backward ? 128 : 256))
         return 0;
     long n = want / wgs;
     if (n > each / 64)

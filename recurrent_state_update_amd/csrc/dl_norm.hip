@@ -583,16 +583,23 @@ __global__ __launch_bounds__(NT) void residual_norm_fp8_kernel(NormFp8Args a)
     }
 }
 
+template <typename T, int NT, int VEC, int E, bool GROUPS, bool ONCE> hipError_t norm_fp8_o(const NormFp8Args &a, hipStream_t st)
+{
+    hipLaunchKernelGGL((residual_norm_fp8_kernel<T, NT, VEC, E, GROUPS, ONCE>),
+                       dim3(static_cast<unsigned>(a.rows < kForwardBlocks ? a.rows : kForwardBlocks)), dim3(NT), 0, st, a);
+    return hipGetLastError();
+}
 template <typename T, int NT, int VEC, int E> hipError_t norm_fp8_k(const NormFp8Args &a, hipStream_t st)
 {
-    const dim3 grid(static_cast<unsigned>(a.rows < kForwardBlocks ? a.rows : kForwardBlocks));
-    if constexpr (VEC > 1)
-        if (a.group != a.D) {
-            hipLaunchKernelGGL((residual_norm_fp8_kernel<T, NT, VEC, E, true, false>), grid, dim3(NT), 0, st, a);
-            return hipGetLastError();
-        }
-    hipLaunchKernelGGL((residual_norm_fp8_kernel<T, NT, VEC, E, false, false>), grid, dim3(NT), 0, st, a);
-    return hipGetLastError();
+    if constexpr (VEC > 1) {
+        // past the caches where a pass moves more than the last-level one holds, as residual_norm_t
+        const bool once = a.rows * a.D * static_cast<long>(a.y ? 9 + sizeof(T) : 5) > (256L << 20);
+        if (a.group != a.D)
+            return once ? norm_fp8_o<T, NT, VEC, E, true, true>(a, st) : norm_fp8_o<T, NT, VEC, E, true, false>(a, st);
+        if (once)
+            return norm_fp8_o<T, NT, VEC, E, false, true>(a, st);
+    }
+    return norm_fp8_o<T, NT, VEC, E, false, false>(a, st);
 }
 
 template <typename T, int VEC> hipError_t norm_fp8_e(const NormFp8Args &a, hipStream_t st)

@@ -37,7 +37,6 @@ namespace dl::ssm {
 
 constexpr int TB = kSsmBlock; // tokens per block: one per lane of a row
 static_assert(TB == 16, "a row of lanes");
-constexpr float kLog2e = 1.44269504088896340736f;
 
 using f32x4 = float __attribute__((ext_vector_type(4)));
 using f32x2 = float __attribute__((ext_vector_type(2)));
@@ -140,10 +139,6 @@ __device__ __forceinline__ float softplus(float r, float &e)
 __device__ __forceinline__ float softplus_slope(float r, float e)
 {
     return (r < 0.f ? e : 1.f) * __builtin_amdgcn_rcpf(1.f + e);
-}
-__device__ __forceinline__ float sigmoid(float z)
-{
-    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-z * kLog2e));
 }
 // A as the exponent of 2, for the decay of a token.  -inf (a state that forgets
 // all) is kept finite: a token that is not there has delta = 0, and its decay

@@ -69,12 +69,24 @@ template <typename T, int S, bool VEC, bool SAVE> __global__ __launch_bounds__(N
         rate[s] = has[s] ? finite_rate(a.A[of_c + 16 * s] * kLog2e) : 0.f;
         h[s] = a.init && has[s] ? a.init[p.n * states + of_c + 16 * s] : 0.f;
     }
-    for (int i = 0; i < p.index; ++i) { // the segments ahead
-        const float sum = a.seg_d[static_cast<long>(p.base + i) * a.C + c];
+    // The segments ahead, a few of them loaded at a time.
+    constexpr int JOIN = 8;
+    for (int i0 = 0; i0 < p.index; i0 += JOIN) {
+        float sum[JOIN], add[JOIN][S];
 #pragma unroll
-        for (int s = 0; s < S; ++s)
-            if (has[s])
-                h[s] = fmaf(__builtin_amdgcn_exp2f(sum * rate[s]), h[s], a.seg_h[(p.base + i) * states + of_c + 16 * s]);
+        for (int i = 0; i < JOIN; ++i) {
+            const long at = static_cast<long>(p.base + min(i0 + i, p.index - 1)) * a.C + c;
+            sum[i] = a.seg_d[at];
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                add[i][s] = a.seg_h[at * a.S + min(j + 16 * s, a.S - 1)];
+        }
+#pragma unroll
+        for (int i = 0; i < JOIN; ++i)
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                if (i0 + i < p.index && has[s])
+                    h[s] = fmaf(__builtin_amdgcn_exp2f(sum[i] * rate[s]), h[s], add[i][s]);
     }
     if (set == 0)
 #pragma unroll

@@ -146,18 +146,28 @@ template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ?
                 G[i][s] = a.dfin[p.n * states + at];
         }
     }
-    if (len > 0 && a.seg) { // the segments behind
+    if (len > 0 && a.seg) { // the segments behind, a few of them loaded at a time
+        constexpr int JOIN = 4;
         const int count = (p.end - p.start + a.seg - 1) / a.seg;
-        for (int k = count - 1; k > p.index; --k)
+        for (int k0 = count - 1; k0 > p.index; k0 -= JOIN)
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const int c = c0 + min(in_tile(i), nc - 1);
-                const float sum = a.seg_d[static_cast<long>(p.base + k) * a.C + c];
+                float sum[JOIN], add[JOIN][S];
 #pragma unroll
-                for (int s = 0; s < S; ++s)
-                    if (in_tile(i) < nc && j + 16 * s < a.S)
-                        G[i][s] = fmaf(__builtin_amdgcn_exp2f(sum * rate[i][s]), G[i][s],
-                                       a.seg_h[(p.base + k) * states + static_cast<long>(c) * a.S + j + 16 * s]);
+                for (int k = 0; k < JOIN; ++k) {
+                    const long at = static_cast<long>(p.base + max(k0 - k, p.index + 1)) * a.C + c;
+                    sum[k] = a.seg_d[at];
+#pragma unroll
+                    for (int s = 0; s < S; ++s)
+                        add[k][s] = a.seg_h[at * a.S + min(j + 16 * s, a.S - 1)];
+                }
+#pragma unroll
+                for (int k = 0; k < JOIN; ++k)
+#pragma unroll
+                    for (int s = 0; s < S; ++s)
+                        if (k0 - k > p.index && in_tile(i) < nc && j + 16 * s < a.S)
+                            G[i][s] = fmaf(__builtin_amdgcn_exp2f(sum[k] * rate[i][s]), G[i][s], add[k][s]);
             }
     }
 

@@ -59,4 +59,13 @@ template <int G> __device__ __forceinline__ float group_sum(float x)
     return x;
 }
 
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// 1 / (1 + e^-z), from the exponential and the reciprocal of the hardware (each good to
+// two roundings; the exponent's own rounding is |z| 2^-24 of the exponential).
+__device__ __forceinline__ float sigmoid(float z)
+{
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-z * kLog2e));
+}
+
 } // namespace dl
