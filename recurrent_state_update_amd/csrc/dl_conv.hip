@@ -286,6 +286,42 @@ template <typename T, int W, int V, bool VEC> __global__ __launch_bounds__(NT) v
                 yfrom += ys;
             }
         };
+        // Tokens t ... t + U - 1 of one sequence, and of this run: nothing to look at but
+        // where the run or the sequence begins.
+        const auto inner = [&](int t, const Cells<V, T, VEC> (&cx)[U], const Cells<V, T, VEC> (&cy)[U]) {
+            const int first = max(t0, l.start);
+            T *const to = static_cast<T *>(a.dx) + static_cast<long>(t) * a.C + c;
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                float dyv[V], ds[V];
+                cx[i].get(l.x[W - 1]);
+                cy[i].get(dyv);
+                l.slope(ds, dyv);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+#pragma unroll
+                    for (int k = 0; k < W; ++k)
+                        g[k][e] = fmaf(l.w[W - 1 - k][e], ds[e], g[k][e]);
+                    db[e] += ds[e];
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        dw[j][e] = fmaf(ds[e], l.x[j][e], dw[j][e]);
+                }
+                if (t + i - (W - 1) >= first) {
+                    Cells<V, T, VEC> r;
+                    r.put(g[W - 1]);
+                    r.store(to + (i - (W - 1)) * a.C, l.m);
+                }
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+#pragma unroll
+                    for (int k = W - 1; k > 0; --k)
+                        g[k][e] = g[k - 1][e];
+                    g[0][e] = 0.f;
+                }
+                l.leave();
+            }
+        };
         // Token t; whether there are more of use.
         const auto token = [&](int t, const Cells<V, T, VEC> &cx, Cells<V, T, VEC> &cy) {
             if (t == l.end) // behind a sequence's last token: what is gathered is whole
@@ -345,9 +381,13 @@ template <typename T, int W, int V, bool VEC> __global__ __launch_bounds__(NT) v
                 cy[i] = ny[i];
             }
             read();
+            // (the sequence of the token before: its window is the one at hand)
+            if (a.dy && t > l.start && t + U <= min(l.end, t1))
+                inner(t, cx, cy);
+            else
 #pragma unroll
-            for (int i = 0; i < U; ++i)
-                more = more && token(t + i, cx[i], cy[i]);
+                for (int i = 0; i < U; ++i)
+                    more = more && token(t + i, cx[i], cy[i]);
         }
     }
 #pragma unroll

@@ -42,12 +42,23 @@ dl_status check_conv(const dl_conv_desc *d)
 }
 
 // Tokens per run: long ones re-read less at their ends (W - 1 tokens of each) and
-// leave fewer partial sums, and there have to be enough to fill the GPU.
+// leave fewer partial sums, short ones give more lanes.  us by the run's length, bf16,
+// four taps, tokens x channels:
+//                       4     8    16    32    64   128
+//   forward 2048 x 2048 9.4   8.1  9.5  14.9  23.3
+//          2756 x 12288 49.9  34.9 31.0 30.8  35.2
+//          8192 x 4096  48.2  34.3 30.3 28.9  30.7
+//         16384 x 4096  89.6  60.1 52.0 55.8  50.5
+//   training 2048 x 2048 44.1 32.8 29.7 33.9  41.6  60.9   (forward by the rule)
+//          2756 x 12288  254  171  128  111   108   98.5
+//          8192 x 4096   256  165  118  99.8  84.8  93.1
+//         16384 x 4096   465  326  234  193   170   155
 int conv_run(const dl_conv_desc *d, bool backward)
 {
-    const long groups = (d->channels + dl::kConvChannels - 1) / dl::kConvChannels;
-    int run = backward ? 8 : 4;
-    while (run < (backward ? 128 : 64) && d->tokens / (2 * run) * groups >= 256L * 256 * (backward ? 1 : 2))
+    const long groups = (d->channels + dl::kConvChannels - 1) / dl::kConvChannels, lanes = backward ? 1 << 16 : 1 << 17;
+    int run = backward ? 8 : 4, most = d->tokens * groups > 1L << 23 ? 64 : 32;
+    most *= backward ? 2 : 1;
+    while (run < most && d->tokens / (2 * run) * groups >= lanes)
         run *= 2;
     return run;
 }
