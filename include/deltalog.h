@@ -428,8 +428,9 @@ typedef struct {
 } dl_ssm_desc;
 
 /* Device bytes of the scan's workspace, of the `saved` buffer that a backward pass
- * needs (the state ahead of every 16 tokens), and of the backward pass's
- * workspace, each 256-byte aligned; 0 for sizes that are not supported: 1 <=
+ * needs (the state ahead of every 16 tokens; with z also y ahead of the gate, fp32),
+ * and of the backward pass's workspace, each 256-byte aligned (of d only the sizes,
+ * dtype and whether z is NULL are read); 0 for sizes that are not supported: 1 <=
  * states <= 64, channels a multiple of groups, channels <= 2^20, tokens and seqs
  * <= 2^30, (seqs + tokens/64) * channels/16 < 2^23 (channels rounded up to
  * sixteens per group, and their number to a multiple of eight), tokens * groups *

@@ -229,6 +229,7 @@ struct SsmArgs {
     // delta; backward: the gradient of its start state, from zero behind it
     float *seg_h, *seg_d;
     float *saved; // [ssm_slots(T, N, kSsmBlock)][C][S] the state ahead of every block, or NULL
+    float *plain; // [T][C] y ahead of the gate (saved with it, where there is one)
     // single tokens
     float *state;    // [n_rows][C][S]
     const int *rows; // [T], or NULL: row t

@@ -144,7 +144,7 @@ int ssm_segment(const dl_ssm_desc *d, bool backward)
 
 struct SsmSizes {
     int seg, bseg, slots, bslots;
-    size_t states, sums, saved, bstates, bsums, bc;
+    size_t states, sums, ahead, plain, bstates, bsums, bc;
     explicit SsmSizes(const dl_ssm_desc *d)
         : seg(ssm_segment(d, false)), bseg(ssm_segment(d, true)),
           slots(seg ? static_cast<int>(dl::ssm_slots(d->tokens, d->seqs, seg)) : d->seqs),
@@ -153,12 +153,15 @@ struct SsmSizes {
         const size_t C = d->channels, state = C * d->states * 4;
         states = seg ? up256(slots * state) : 0;
         sums = seg ? up256(slots * C * 4) : 0;
-        saved = up256(dl::ssm_slots(d->tokens, d->seqs, dl::kSsmBlock) * state);
+        ahead = up256(dl::ssm_slots(d->tokens, d->seqs, dl::kSsmBlock) * state);
+        plain = d->z ? up256(d->tokens * C * 4) : 0;
         bstates = up256(bslots * state);
         bsums = up256(bslots * C * 4);
         bc = up256(static_cast<size_t>(tiles_of(d, dl::kSsmGradTile) / d->groups) * d->tokens * d->groups * 2 * d->states * 4);
     }
     size_t forward() const { return states + sums + 256; } // never 0
+    // the state ahead of every block, and y ahead of the gate
+    size_t saved() const { return ahead + plain; }
     // dB and dC of every tile; dA, dD and dt_bias's gradient of every piece; the
     // segments' G and sums of delta
     size_t backward() const { return bc + bstates + 2 * bsums + (bseg ? bstates + bsums : 0); }
@@ -335,7 +338,7 @@ dl_status dl_short_conv_step(const dl_conv_desc *d, void *state, const int *stat
 
 size_t dl_ssm_workspace_bytes(const dl_ssm_desc *d) { return check_ssm(d) == DL_OK ? SsmSizes(d).forward() : 0; }
 
-size_t dl_ssm_saved_bytes(const dl_ssm_desc *d) { return check_ssm(d) == DL_OK ? SsmSizes(d).saved : 0; }
+size_t dl_ssm_saved_bytes(const dl_ssm_desc *d) { return check_ssm(d) == DL_OK ? SsmSizes(d).saved() : 0; }
 
 size_t dl_ssm_backward_workspace_bytes(const dl_ssm_desc *d)
 {
@@ -358,7 +361,7 @@ dl_status dl_ssm_scan(const dl_ssm_desc *d, const float *initial, float *final_s
         return DL_E_ALIGN;
     const SsmSizes z(d);
     const size_t states = d->seqs * C * d->states * 4;
-    const Span w[4] = {{y, d->tokens * C * es}, {final_state, states}, {saved, z.saved}, {workspace, z.forward()}};
+    const Span w[4] = {{y, d->tokens * C * es}, {final_state, states}, {saved, z.saved()}, {workspace, z.forward()}};
     const Span r[10] = {in[0], in[1], in[2], in[3], in[4], in[5], in[6], in[7], in[8], {initial, states}};
     if (clash(w, r))
         return DL_E_INVALID;
@@ -367,6 +370,7 @@ dl_status dl_ssm_scan(const dl_ssm_desc *d, const float *initial, float *final_s
     a.y = y;
     a.vec_x = a.vec_x && aligned(y, 4 * es) && d->channels % 4 == 0;
     a.saved = static_cast<float *>(saved);
+    a.plain = saved ? reinterpret_cast<float *>(static_cast<char *>(saved) + z.ahead) : nullptr;
     a.seg = z.seg;
     a.slots = z.slots;
     a.tiles = tiles_of(d, dl::kSsmTile);
@@ -400,11 +404,12 @@ dl_status dl_ssm_scan_backward(const dl_ssm_desc *d, const void *saved, const vo
     const size_t states = d->seqs * C * d->states * 4, bc = T * d->groups * d->states * es;
     const Span w[10] = {{dx, T * C * es}, {ddt, T * C * es}, {dz, T * C * es}, {db, bc}, {dc, bc}, {da, in[5].bytes},
                         {dd, C * 4}, {ddt_bias, C * 4}, {d_initial, states}, {workspace, z.backward()}};
-    const Span r[12] = {in[0], in[1], in[2], in[3], in[4], in[5], in[6], in[7], in[8], {saved, z.saved},
+    const Span r[12] = {in[0], in[1], in[2], in[3], in[4], in[5], in[6], in[7], in[8], {saved, z.saved()},
                         {dy, T * C * es}, {d_final, states}};
     if (clash(w, r))
         return DL_E_INVALID;
     a.saved = static_cast<float *>(const_cast<void *>(saved));
+    a.plain = reinterpret_cast<float *>(static_cast<char *>(const_cast<void *>(saved)) + z.ahead);
     a.dy = dy;
     a.dfin = d_final;
     a.dx = dx;

@@ -203,11 +203,12 @@ static_assert(CH == 16, "four waves of four rows");
 
 template <int S, int TT> struct Stage {
     static constexpr int XLD = TT + 2, BLD = TT + 4;
-    float x[CH][XLD], dt[CH][XLD], z[CH][XLD];
+    float x[CH][XLD], dt[CH][XLD];
     alignas(16) float b[16 * S][BLD], c[16 * S][BLD];
 };
 
-// What of it a kernel reads: the adjoint's has dy and C in the place of x and B.
+// What it is read from: the adjoint's has dy, times the gate's silu, and C in the
+// place of x and B.
 struct Sources {
     const void *x, *dt, *z, *b, *c; // z: NULL without a gate
     long xs, dts, zs, bs, cs;
@@ -263,7 +264,8 @@ template <typename T, int S, int TT, bool VEC> struct Loader {
                 row(rc[k], s.c, s.cs, from, bt + k * BTOK, state, nb);
         }
     }
-    template <bool Z, bool C> __device__ __forceinline__ void put(Stage<S, TT> &st, int from)
+    // GATED: x times the gate's silu
+    template <bool GATED, bool Z, bool C> __device__ __forceinline__ void put(Stage<S, TT> &st, int from)
     {
         const int n = from + xt < len ? nx : 0;
         rx.keep(n);
@@ -272,10 +274,13 @@ template <typename T, int S, int TT, bool VEC> struct Loader {
             rz.keep(gate ? n : 0);
 #pragma unroll
         for (int i = 0; i < XV; ++i) {
-            st.x[xc + i][xt] = to_f(rx.v[i]);
+            float x = to_f(rx.v[i]);
+            if constexpr (GATED) {
+                const float z = to_f(rz.v[i]);
+                x *= fmaf(z, sigmoid(z), gate ? 0.f : 1.f);
+            }
+            st.x[xc + i][xt] = x;
             st.dt[xc + i][xt] = to_f(rd.v[i]);
-            if constexpr (Z)
-                st.z[xc + i][xt] = to_f(rz.v[i]);
         }
 #pragma unroll
         for (int k = 0; k < BK; ++k) {
@@ -293,14 +298,13 @@ template <typename T, int S, int TT, bool VEC> struct Loader {
     }
 };
 
-// What lane j of a row forms of its tokens at, at + 16, ... of a stage: x, delta, the
-// gate's silu (1 without one).  Straight code for all blocks of the stage, whose chains
-// of dependent operations then overlap; tokens behind the `live` ones have delta 0 and
-// change nothing.
+// What lane j of a row forms of its tokens at, at + 16, ... of a stage: x and delta.
+// Straight code for all blocks of the stage, whose chains of dependent operations then
+// overlap; tokens behind the `live` ones have delta 0 and change nothing.
 template <int NB> struct Own {
-    float x[NB], delta[NB], z[NB];
-    template <bool Z, typename St>
-    __device__ __forceinline__ void form(const St &st, int row, int j, int live, float bias, int softplus_on, float no_gate)
+    float x[NB], delta[NB];
+    template <typename St>
+    __device__ __forceinline__ void form(const St &st, int row, int j, int live, float bias, int softplus_on)
     {
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
@@ -309,11 +313,6 @@ template <int NB> struct Own {
             asm("" : "+v"(soft)); // a selection, not a branch
             x[i] = st.x[row][at];
             delta[i] = at < live ? softplus_on ? soft : raw : 0.f;
-            z[i] = 1.f;
-            if constexpr (Z) {
-                const float v = st.z[row][at]; // 0 without a gate
-                z[i] = fmaf(v, sigmoid(v), no_gate);
-            }
         }
     }
 };

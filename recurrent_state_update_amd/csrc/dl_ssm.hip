@@ -61,7 +61,7 @@ template <typename T, int S, bool VEC, bool SAVE> __global__ __launch_bounds__(N
 
     const int c = tile.c0 + min(row, tile.nc - 1); // this row's channel
     const long of_c = static_cast<long>(c) * a.S + j, states = static_cast<long>(a.C) * a.S;
-    float rate[S], h[S], bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = a.D ? a.D[c] : 0.f;
+    float rate[S], h[S], bias = a.dt_bias ? a.dt_bias[c] : 0.f;
     bool has[S];
 #pragma unroll
     for (int s = 0; s < S; ++s) {
@@ -92,13 +92,20 @@ template <typename T, int S, bool VEC, bool SAVE> __global__ __launch_bounds__(N
 #pragma unroll
         for (int s = 0; s < S; ++s)
             sh.h[s][tid] = h[s];
+    float skip[Load::XV]; // D, of the channels that this thread loads and stores
+#pragma unroll
+    for (int i = 0; i < Load::XV; ++i)
+        skip[i] = a.D && i < load.nx ? a.D[load.col + i] : 0.f;
     const float no_gate = a.z ? 0.f : 1.f;
     // What was loaded above is here before the loop: its first use would wait for the
     // loop's own loads, too.
-    asm volatile("" : "+v"(bias), "+v"(skip));
+    asm volatile("" : "+v"(bias));
 #pragma unroll
     for (int s = 0; s < S; ++s)
         asm volatile("" : "+v"(rate[s]));
+#pragma unroll
+    for (int i = 0; i < Load::XV; ++i)
+        asm volatile("" : "+v"(skip[i]));
 
     const int stages = (p.len + TT - 1) / TT;
     // What needs no state: of the stage's own tokens, and the decays and inputs.
@@ -106,7 +113,7 @@ template <typename T, int S, bool VEC, bool SAVE> __global__ __launch_bounds__(N
     float d[NB][S][TB], v[NB][S][TB];
     const auto ahead = [&](int k) {
         const typename Shared<S>::In &st = sh.in[k % 3];
-        own.template form<true>(st, row, j, p.len - k * TT, bias, a.softplus, no_gate);
+        own.form(st, row, j, p.len - k * TT, bias, a.softplus);
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             const float u = own.delta[i] * own.x[i];
@@ -164,16 +171,25 @@ template <typename T, int S, bool VEC, bool SAVE> __global__ __launch_bounds__(N
                     y[t] = s ? fmaf(w, v[i][s][t], y[t]) : w * v[i][s][t];
                 }
             });
-            sh.y[k % 2][row][i * TB + j] = fmaf(skip, own.x[i], row_sums(y, j)) * own.z[i];
+            sh.y[k % 2][row][i * TB + j] = row_sums(y, j);
         }
     };
+    // y of the stage, by the threads that loaded its x and z.
+    Cells<Load::XV, T, VEC> kx, kz;
     const auto store = [&](int k) {
         if (k * TT + load.xt < p.len) {
             Cells<Load::XV, T, VEC> out;
+            Cells<Load::XV, float, VEC> plain;
 #pragma unroll
-            for (int i = 0; i < Load::XV; ++i)
-                out.v[i] = static_cast<T>(sh.y[k % 2][load.xc + i][load.xt]);
-            out.store(static_cast<T *>(a.y) + static_cast<long>(p.t0 + k * TT + load.xt) * a.C + tile.c0 + load.xc, load.nx);
+            for (int i = 0; i < Load::XV; ++i) {
+                const float z = to_f(kz.v[i]), y = fmaf(skip[i], to_f(kx.v[i]), sh.y[k % 2][load.xc + i][load.xt]);
+                plain.v[i] = y;
+                out.v[i] = static_cast<T>(y * fmaf(z, sigmoid(z), no_gate));
+            }
+            const long at = static_cast<long>(p.t0 + k * TT + load.xt) * a.C + tile.c0 + load.xc;
+            out.store(static_cast<T *>(a.y) + at, load.nx);
+            if (SAVE && a.z)
+                plain.store(a.plain + at, load.nx);
         }
     };
     // Slot t, which ends at a barrier: chain(t) by one set, ahead(t + 1) by the other.
@@ -181,7 +197,7 @@ template <typename T, int S, bool VEC, bool SAVE> __global__ __launch_bounds__(N
     // have every load waited for at once.)
     if (stages > 0) {
         load.template read<true, true>(set * TT);
-        load.template put<true, true>(sh.in[set], set * TT);
+        load.template put<false, true, true>(sh.in[set], set * TT);
     }
     __syncthreads();
     int slots = stages + 1; // from -1 on
@@ -192,9 +208,11 @@ template <typename T, int S, bool VEC, bool SAVE> __global__ __launch_bounds__(N
     for (int k = set; k < stages; k += 2) {
         ahead(k);
         __syncthreads();
+        kx = load.rx;
+        kz = load.rz;
         load.template read<true, true>((k + 2) * TT);
         chain(k);
-        load.template put<true, true>(sh.in[(k + 2) % 3], (k + 2) * TT);
+        load.template put<false, true, true>(sh.in[(k + 2) % 3], (k + 2) * TT);
         __syncthreads();
         slots -= 2;
         store(k);

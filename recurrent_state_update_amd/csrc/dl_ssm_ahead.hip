@@ -44,7 +44,6 @@ template <typename T, int S, bool ADJOINT, bool VEC> __global__ __launch_bounds_
                                  : Sources{a.x, a.dt, nullptr, a.b, nullptr, a.xs, a.dts, 0, a.bs, 0};
     Loader<T, S, TT, VEC> load(from, tid, tile.c0, tile.nc, tile.g * a.S, a.S);
     load.piece(p.t0, p.len);
-    const float no_gate = a.z ? 0.f : 1.f;
     // What was loaded above is here before the loop: its first use would wait for the
     // loop's own loads, too.
     asm volatile("" : "+v"(bias));
@@ -55,18 +54,18 @@ template <typename T, int S, bool ADJOINT, bool VEC> __global__ __launch_bounds_
     const int stages = (p.len + TT - 1) / TT;
     const auto at_stage = [&](int k) { return (ADJOINT ? stages - 1 - k : k) * TT; };
     load.template read<ADJOINT, false>(at_stage(0));
-    load.template put<ADJOINT, false>(in[0], at_stage(0));
+    load.template put<ADJOINT, ADJOINT, false>(in[0], at_stage(0));
     __syncthreads();
     for (int k = 0; k < stages; ++k) {
         const Stage<S, TT> &st = in[k % 2];
         const int t0 = at_stage(k), next = at_stage(min(k + 1, stages - 1));
         load.template read<ADJOINT, false>(next);
         Own<NB> own;
-        own.template form<ADJOINT>(st, row, j, p.len - t0, bias, a.softplus, no_gate);
+        own.form(st, row, j, p.len - t0, bias, a.softplus);
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             const int i = ADJOINT ? NB - 1 - n : n;
-            const float u = ADJOINT ? own.x[i] * own.z[i] : own.x[i] * own.delta[i];
+            const float u = ADJOINT ? own.x[i] : own.x[i] * own.delta[i];
             float d[S][TB], v[S][TB];
             for_tokens([&](auto J) {
                 constexpr int t = decltype(J)::value;
@@ -88,7 +87,7 @@ template <typename T, int S, bool ADJOINT, bool VEC> __global__ __launch_bounds_
                 for_tokens(token);
             sum += own.delta[i];
         }
-        load.template put<ADJOINT, false>(in[(k + 1) % 2], next);
+        load.template put<ADJOINT, ADJOINT, false>(in[(k + 1) % 2], next);
         __syncthreads();
     }
     const long at = static_cast<long>(slot) * a.C + c;

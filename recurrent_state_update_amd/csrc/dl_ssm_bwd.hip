@@ -14,12 +14,13 @@ constexpr int R = GC / (WAVES * 4); // channels of a row of lanes, one after the
 constexpr int LD = TB + 1, BLD = TB + 4;
 static_assert(GC * TB == NT * 4, "four channels of a token per thread");
 
+// dy: times the gate's silu; slope: delta's, by dt.
 template <int S> struct GradStage {
-    float x[GC][LD], dt[GC][LD], z[GC][LD], dy[GC][LD];
+    float x[GC][LD], delta[GC][LD], slope[GC][LD], dy[GC][LD];
     alignas(16) float b[16 * S][BLD], c[16 * S][BLD];
 };
-// A lane puts dx, ddt and dz where x, dt and z were, which nothing else reads:
-// three stages, so that one can be stored while the next but one is put in.
+// A lane puts dx and ddt where x and slope were, which nothing else reads: three
+// stages, so that one can be stored while the next but one is put in.
 template <int S> struct Shared {
     GradStage<S> in[3];
     alignas(16) float db[2][WAVES][16 * S][TB], dc[2][WAVES][16 * S][TB];
@@ -88,6 +89,10 @@ template <int T0> __device__ __forceinline__ void fma_bcast_sum(float &even, flo
           "n"(T0 + 1), "n"(T0 + 2), "n"(T0 + 3), "n"(T0 + 4), "n"(T0 + 5), "n"(T0 + 6), "n"(T0 + 7));
 }
 
+// Where token t of state n is in a row of db or dc: its fours in another order for
+// every other state, so that states in step do not meet in the same banks.
+__device__ __forceinline__ int swizzle(int n, int t) { return t ^ (n / 2 % 4 * 4); }
+
 // One workgroup per tile of 64 channels and piece of a sequence: blocks of
 // sixteen tokens from its end.  Per block the states are formed anew from the
 // saved one ahead of it, sixteen in registers with their decays; then the adjoint
@@ -128,12 +133,11 @@ template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ?
 
     // this row's channels are ch(0) ... ch(R - 1)
     const auto in_tile = [&](int i) { return wave * 4 * R + i * 4 + row; };
-    float rate[R][S], G[R][S], dA[R][S], skip[R], bias[R], dD[R], dbias[R];
+    float rate[R][S], G[R][S], dA[R][S], skip[R], dD[R], dbias[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int c = c0 + min(in_tile(i), nc - 1);
         skip[i] = a.D ? a.D[c] : 0.f;
-        bias[i] = a.dt_bias ? a.dt_bias[c] : 0.f;
         dD[i] = dbias[i] = 0.f;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
@@ -174,7 +178,12 @@ template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ?
     // Loads beyond the channels, states or tokens there are go to the first or last that
     // is, and are dropped.  The state ahead of a block is loaded with the rest.
     Cells<XV, T, VEC> rx, rd, rz, ry;
+    Cells<XV, float, VEC> rp;
     Cells<BN, T, VEC> rb, rc;
+    float bias[XV];
+#pragma unroll
+    for (int i = 0; i < XV; ++i)
+        bias[i] = a.dt_bias && i < nc - xc ? a.dt_bias[c0 + xc + i] : 0.f;
     float ahead[S][R];
     const int col = c0 + (xc < nc ? xc : 0), bcol = g * a.S + (bn < a.S ? bn : 0);
     const float *const saved = a.saved + (p.none() ? 0 : p.start / TB + p.n + (p.t0 - p.start) / TB) * states;
@@ -183,8 +192,8 @@ template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ?
         rx.load(static_cast<const T *>(a.x) + t * a.xs + col, nc - xc);
         rd.load(static_cast<const T *>(a.dt) + t * a.dts + col, nc - xc);
         ry.load(static_cast<const T *>(a.dy) + t * a.C + col, nc - xc);
-        if (gate)
-            rz.load(static_cast<const T *>(a.z) + t * a.zs + col, nc - xc);
+        rz.load(gate ? static_cast<const T *>(a.z) + t * a.zs + col : static_cast<const T *>(a.x) + t * a.xs + col, nc - xc);
+        rp.load((gate ? a.plain + t * a.C : a.saved) + col, nc - xc);
         const long u = p.t0 + min(t0 + bt, len - 1);
         rb.load(static_cast<const T *>(a.b) + u * a.bs + bcol, a.S - bn);
         rc.load(static_cast<const T *>(a.c) + u * a.cs + bcol, a.S - bn);
@@ -200,18 +209,24 @@ template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ?
         rx.keep(n);
         rd.keep(n);
         ry.keep(n);
-        if (gate)
-            rz.keep(n);
+        rz.keep(gate ? n : 0);
         rb.keep(m);
         rc.keep(m);
+        Cells<XV, T, VEC> dz;
 #pragma unroll
         for (int i = 0; i < XV; ++i) {
+            float e, raw = to_f(rd.v[i]) + bias[i], soft = softplus(raw, e), slope = softplus_slope(raw, e);
+            asm("" : "+v"(soft), "+v"(slope)); // selections, not branches
+            const bool there = i < n;
             st.x[xc + i][xt] = to_f(rx.v[i]);
-            st.dt[xc + i][xt] = to_f(rd.v[i]);
-            st.dy[xc + i][xt] = to_f(ry.v[i]);
-            if (gate)
-                st.z[xc + i][xt] = to_f(rz.v[i]);
+            st.delta[xc + i][xt] = there ? a.softplus ? soft : raw : 0.f;
+            st.slope[xc + i][xt] = there ? a.softplus ? slope : 1.f : 0.f;
+            const float z = to_f(rz.v[i]), sg = sigmoid(z), dy = to_f(ry.v[i]);
+            st.dy[xc + i][xt] = dy * fmaf(z, sg, gate ? 0.f : 1.f);
+            dz.v[i] = static_cast<T>(dy * rp.v[i] * sg * fmaf(z, 1.f - sg, 1.f));
         }
+        if (gate && t0 + xt < len)
+            dz.store(static_cast<T *>(a.dz) + static_cast<long>(p.t0 + t0 + xt) * a.C + c0 + xc, nc - xc);
 #pragma unroll
         for (int i = 0; i < BN; ++i) {
             st.b[bn + i][bt] = to_f(rb.v[i]);
@@ -239,11 +254,10 @@ template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ?
         const int t0 = (blocks - 1 - k) * TB;
         if (k + 1 < blocks)
             read(t0 - TB);
-        const bool live = t0 + j < len;
-        float sy[R], sq[R], sr[R];
+        float sq[R], sr[R];
 #pragma unroll
         for (int i = 0; i < R; ++i)
-            sy[i] = sq[i] = sr[i] = 0.f;
+            sq[i] = sr[i] = 0.f;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             float B[TB], C[TB], dB[TB], dC[TB];
@@ -261,30 +275,19 @@ template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ?
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const int c = in_tile(i);
-                float delta = st.dt[c][j] + bias[i], e;
-                delta = a.softplus ? softplus(delta, e) : delta;
-                delta = live ? delta : 0.f;
-                float dy = st.dy[c][j];
-                if (gate) {
-                    const float z = st.z[c][j];
-                    dy *= z * sigmoid(z);
-                }
-                float u = delta * st.x[c][j];
+                float delta = st.delta[c][j], dy = st.dy[c][j], u = delta * st.x[c][j];
                 in_order({&delta, &u, &dy, &start[s][i]});
                 // forward over the block
-                float d[TB], h[TB + 1], y[TB], f = G[i][s];
+                float d[TB], h[TB + 1], f = G[i][s];
                 h[0] = start[s][i];
                 for_tokens([&](auto J) {
                     constexpr int t = decltype(J)::value;
                     d[t] = __builtin_amdgcn_exp2f(row_bcast<t>(delta) * rate[i][s]);
                     h[t + 1] = fmaf(d[t], h[t], row_bcast<t>(u) * B[t]);
-                    y[t] = C[t] * h[t + 1];
                 });
                 fma_bcast<0>(dC, dy, h + 1);
                 fma_bcast<8>(dC + 8, dy, h + 9);
-                if (gate)
-                    sy[i] += row_sums(y, j);
-                in_order({&sy[i], &f});
+                in_order({&f});
                 // and back
                 float q[TB], r[TB], F[TB], moved[TB], odd = 0.f;
                 const auto back = [&](auto J) {
@@ -309,28 +312,16 @@ template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ?
             }
             rows_sum(dB);
             rows_sum(dC);
-            *reinterpret_cast<f32x4 *>(&sh.db[k % 2][wave][j + 16 * s][4 * row]) = f32x4{dB[0], dB[1], dB[2], dB[3]};
-            *reinterpret_cast<f32x4 *>(&sh.dc[k % 2][wave][j + 16 * s][4 * row]) = f32x4{dC[0], dC[1], dC[2], dC[3]};
+            *reinterpret_cast<f32x4 *>(&sh.db[k % 2][wave][j + 16 * s][swizzle(j, 4 * row)]) = f32x4{dB[0], dB[1], dB[2], dB[3]};
+            *reinterpret_cast<f32x4 *>(&sh.dc[k % 2][wave][j + 16 * s][swizzle(j, 4 * row)]) = f32x4{dC[0], dC[1], dC[2], dC[3]};
         }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int c = in_tile(i);
-            const float raw = st.dt[c][j] + bias[i], x = st.x[c][j];
-            float delta = raw, slope = 1.f, e;
-            if (a.softplus) {
-                delta = softplus(raw, e);
-                slope = softplus_slope(raw, e);
-            }
-            delta = live ? delta : 0.f;
-            float dy = st.dy[c][j];
-            if (gate) {
-                const float z = st.z[c][j], sg = sigmoid(z);
-                st.z[c][j] = dy * fmaf(skip[i], x, sy[i]) * sg * fmaf(z, 1.f - sg, 1.f);
-                dy *= z * sg;
-            }
-            const float dt = live ? fmaf(x, sq[i], sr[i] * (1.f / kLog2e)) * slope : 0.f;
-            st.x[c][j] = fmaf(delta, sq[i], skip[i] * dy);
-            st.dt[c][j] = dt;
+            const float x = st.x[c][j], dy = st.dy[c][j];
+            const float dt = fmaf(x, sq[i], sr[i] * (1.f / kLog2e)) * st.slope[c][j];
+            st.x[c][j] = fmaf(st.delta[c][j], sq[i], skip[i] * dy);
+            st.slope[c][j] = dt;
             dD[i] = fmaf(dy, x, dD[i]);
             dbias[i] += dt;
         }
@@ -349,9 +340,7 @@ template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ?
                 v.store(static_cast<T *>(dst) + to, nc - xc);
             };
             out(a.dx, st.x);
-            out(a.ddt, st.dt);
-            if (gate)
-                out(a.dz, st.z);
+            out(a.ddt, st.slope);
         }
         if (t0 + bt < len) {
             // [tile of the group][token][group][B's states, C's states]
@@ -362,8 +351,8 @@ template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ?
                 float x = 0.f, y = 0.f;
 #pragma unroll
                 for (int w = 0; w < WAVES; ++w) {
-                    x += sh.db[k % 2][w][n][bt];
-                    y += sh.dc[k % 2][w][n][bt];
+                    x += sh.db[k % 2][w][n][swizzle(n, bt)];
+                    y += sh.dc[k % 2][w][n][swizzle(n, bt)];
                 }
                 if (n < a.S) {
                     to[n] = x;

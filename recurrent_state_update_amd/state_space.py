@@ -304,7 +304,7 @@ def ssm_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = True
     Returns y, shaped as x in its dtype, and the end states, fp32.  Rows of no
     sequence hold zeros, in y and in the gradients.  Differentiable by all of
     them.  A forward pass that will be differentiated keeps the state of every 16th
-    token until its backward pass."""
+    token, and with z an fp32 [T,C], until its backward pass."""
     _plain("ssm_scan", x, dt, A, B, C, D, z, dt_bias, initial_state)
     dev = _gpu(x, "x")
     s = _Ssm(x, dt, A, B, C, D, z, dt_bias, softplus)
