@@ -239,8 +239,8 @@ struct SsmArgs {
     const float *dfin; // [N][C][S], or NULL (zero)
     void *dx, *ddt, *dz, *db, *dc;
     float *d_A, *d_D, *d_bias, *dinit;
-    float *part_bc;                       // [tiles of a group][T][G][2][S]
-    float *part_a, *part_d, *part_bias;   // [slots][C][S], [slots][C], [slots][C]
+    float *part_bc; // [tiles of a group][T][G][2][S]
+    float *part_a;  // [slots][C S + C + C]: sums for A, D and dt_bias
 };
 hipError_t launch_ssm_scan(int dtype, const SsmArgs &a, hipStream_t st);
 // What segments add to the state behind them, or the gradient ahead of them.

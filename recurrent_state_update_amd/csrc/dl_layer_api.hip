@@ -144,7 +144,7 @@ int ssm_segment(const dl_ssm_desc *d, bool backward)
 
 struct SsmSizes {
     int seg, bseg, slots, bslots;
-    size_t states, sums, ahead, plain, bstates, bsums, bc;
+    size_t states, sums, ahead, plain, bstates, bsums, part, bc;
     explicit SsmSizes(const dl_ssm_desc *d)
         : seg(ssm_segment(d, false)), bseg(ssm_segment(d, true)),
           slots(seg ? static_cast<int>(dl::ssm_slots(d->tokens, d->seqs, seg)) : d->seqs),
@@ -155,8 +155,9 @@ struct SsmSizes {
         sums = seg ? up256(slots * C * 4) : 0;
         ahead = up256(dl::ssm_slots(d->tokens, d->seqs, dl::kSsmBlock) * state);
         plain = d->z ? up256(d->tokens * C * 4) : 0;
-        bstates = up256(bslots * state);
-        bsums = up256(bslots * C * 4);
+        bstates = bseg ? up256(bslots * state) : 0;
+        bsums = bseg ? up256(bslots * C * 4) : 0;
+        part = up256(bslots * (state + 2 * C * 4));
         bc = up256(static_cast<size_t>(tiles_of(d, dl::kSsmGradTile) / d->groups) * d->tokens * d->groups * 2 * d->states * 4);
     }
     size_t forward() const { return states + sums + 256; } // never 0
@@ -164,7 +165,7 @@ struct SsmSizes {
     size_t saved() const { return ahead + plain; }
     // dB and dC of every tile; dA, dD and dt_bias's gradient of every piece; the
     // segments' G and sums of delta
-    size_t backward() const { return bc + bstates + 2 * bsums + (bseg ? bstates + bsums : 0); }
+    size_t backward() const { return bc + part + bstates + bsums; }
 };
 
 dl_status ssm_inputs(const dl_ssm_desc *d, bool step, dl::SsmArgs &a, Span (&r)[9])
@@ -429,13 +430,8 @@ dl_status dl_ssm_scan_backward(const dl_ssm_desc *d, const void *saved, const vo
     char *p = static_cast<char *>(workspace);
     a.part_bc = reinterpret_cast<float *>(p);
     a.part_a = reinterpret_cast<float *>(p += z.bc);
-    a.part_d = dd ? reinterpret_cast<float *>(p += z.bstates) : (p += z.bstates, nullptr);
-    a.part_bias = ddt_bias ? reinterpret_cast<float *>(p += z.bsums) : (p += z.bsums, nullptr);
-    p += z.bsums;
-    if (z.bseg) {
-        a.seg_h = reinterpret_cast<float *>(p);
-        a.seg_d = reinterpret_cast<float *>(p + z.bstates);
-    }
+    a.seg_h = reinterpret_cast<float *>(p += z.part);
+    a.seg_d = reinterpret_cast<float *>(p + z.bstates);
     dl::SsmArgs ahead = a;
     ahead.tiles = tiles_of(d, dl::kSsmTile);
     return status(dl::launch_ssm_backward(d->dtype, ahead, a, static_cast<hipStream_t>(stream)));

@@ -361,6 +361,7 @@ template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ?
             }
         }
     }
+    float *const sums = a.part_a + slot * (states + 2 * a.C);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const long c = c0 + in_tile(i);
@@ -368,33 +369,69 @@ template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ?
 #pragma unroll
         for (int s = 0; s < S; ++s)
             if (there && j + 16 * s < a.S) {
-                a.part_a[slot * states + c * a.S + j + 16 * s] = dA[i][s];
+                sums[c * a.S + j + 16 * s] = dA[i][s];
                 if (!p.none() && p.index == 0 && a.dinit)
                     a.dinit[p.n * states + c * a.S + j + 16 * s] = G[i][s];
             }
         const float x = row_sum(dD[i]), y = row_sum(dbias[i]);
         if (there && j == 0) {
-            if (a.part_d)
-                a.part_d[static_cast<long>(slot) * a.C + c] = x;
-            if (a.part_bias)
-                a.part_bias[static_cast<long>(slot) * a.C + c] = y;
+            sums[states + c] = x;
+            sums[states + a.C + c] = y;
         }
     }
 }
 
-// dB and dC from the tiles' sums, zero for tokens of no sequence.  In 64 bits:
-// up to hundreds are added, and the time is the loads'.
-template <typename T> __global__ __launch_bounds__(NT) void ssm_bc_kernel(SsmArgs a, int tiles)
+// What is summed over workgroups, in 64 bits and in a fixed order (up to hundreds are
+// added, and the time is the loads').  The first `first` workgroups: dA, dD and
+// dt_bias's gradient, columns of [slots][C S + 2 C], sixteen columns a workgroup and
+// every sixteenth row a thread.  The others: dB and dC from the tiles' sums, zero for
+// tokens of no sequence.
+template <typename T> __global__ __launch_bounds__(NT) void ssm_sums_kernel(SsmArgs a, int first, int tiles)
 {
-    const long width = 2L * a.G * a.S, i = static_cast<long>(blockIdx.x) * NT + threadIdx.x;
-    if (i >= a.T * width)
+    constexpr int U = 8; // loads at a time
+    if (static_cast<int>(blockIdx.x) < first) {
+        __shared__ double part[16][17];
+        const int c = threadIdx.x % 16, s = threadIdx.x / 16;
+        const long CS = static_cast<long>(a.C) * a.S, n = CS + 2 * a.C, col = blockIdx.x * 16L + c;
+        double x = 0.;
+        if (col < n)
+            for (int r0 = s; r0 < a.slots; r0 += 16 * U) {
+                float v[U];
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+                    v[i] = a.part_a[min(r0 + 16 * i, a.slots - 1) * n + col];
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+                    x += r0 + 16 * i < a.slots ? v[i] : 0.f;
+            }
+        part[s][c] = x;
+        __syncthreads();
+        if (s > 0 || col >= n)
+            return;
+        for (int t = 1; t < 16; ++t)
+            x += part[t][c];
+        float *const out = col < CS ? a.d_A + col : col < CS + a.C ? a.d_D ? a.d_D + (col - CS) : nullptr
+                                                  : a.d_bias ? a.d_bias + (col - CS - a.C) : nullptr;
+        if (out)
+            *out = static_cast<float>(x);
+        return;
+    }
+    const long width = 2L * a.G * a.S, all = a.T * width, i = static_cast<long>(blockIdx.x - first) * NT + threadIdx.x;
+    if (i >= all)
         return;
     const int t = i / width, k = i % width, g = k / (2 * a.S), n = k % (2 * a.S);
     const Sequences seqs{a.cu, a.T, a.N};
     double x = 0.;
     if (t >= seqs.at(0) && t < seqs.at(a.N))
-        for (int p = 0; p < tiles; ++p)
-            x += a.part_bc[p * (a.T * width) + i];
+        for (int p0 = 0; p0 < tiles; p0 += U) {
+            float v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                v[u] = a.part_bc[min(p0 + u, tiles - 1) * all + i];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                x += p0 + u < tiles ? v[u] : 0.f;
+        }
     T *const out = static_cast<T *>(n < a.S ? a.db : a.dc);
     out[(static_cast<long>(t) * a.G + g) * a.S + (n < a.S ? n : n - a.S)] = static_cast<T>(static_cast<float>(x));
 }
@@ -413,11 +450,12 @@ template <typename T> hipError_t bwd_t(const SsmArgs &a, hipStream_t st)
         vec ? launch<T, 2, true>(a, grid, st) : launch<T, 2, false>(a, grid, st);
     else
         vec ? launch<T, 4, true>(a, grid, st) : launch<T, 4, false>(a, grid, st);
-    if (hipError_t e = hipGetLastError(); e != hipSuccess || a.T == 0)
+    if (hipError_t e = hipGetLastError(); e != hipSuccess)
         return e;
-    const long n = static_cast<long>(a.T) * 2 * a.G * a.S;
-    hipLaunchKernelGGL((ssm_bc_kernel<T>), dim3(static_cast<unsigned>((n + NT - 1) / NT)), dim3(NT), 0, st, a,
-                       (a.CG + GC - 1) / GC);
+    const long columns = static_cast<long>(a.C) * (a.S + 2), bc = static_cast<long>(a.T) * 2 * a.G * a.S;
+    const int first = static_cast<int>((columns + 15) / 16);
+    hipLaunchKernelGGL((ssm_sums_kernel<T>), dim3(static_cast<unsigned>(first + (bc + NT - 1) / NT)), dim3(NT), 0, st, a,
+                       first, (a.CG + GC - 1) / GC);
     return hipGetLastError();
 }
 
@@ -430,12 +468,6 @@ hipError_t launch_ssm_backward(int dtype, const SsmArgs &ahead, const SsmArgs &a
         e = launch_ssm_ahead(dtype, true, ahead, st);
     if (e == hipSuccess)
         e = dtype == F32 ? bwd_t<float>(a, st) : bwd_t<__bf16>(a, st);
-    if (e == hipSuccess)
-        e = column_sum(a.part_a, a.slots, a.C * a.S, a.d_A, nullptr, st);
-    if (e == hipSuccess && a.part_d)
-        e = column_sum(a.part_d, a.slots, a.C, a.d_D, nullptr, st);
-    if (e == hipSuccess && a.part_bias)
-        e = column_sum(a.part_bias, a.slots, a.C, a.d_bias, nullptr, st);
     return e;
 }
 
