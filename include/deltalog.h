@@ -396,7 +396,7 @@ typedef struct {
  * first; NULL: zero).  y [tokens, channels] contiguous; final_state (NULL: not
  * wanted) as initial, for what follows.  Nothing may overlap what is written.
  * Sizes: 2 <= taps <= 4, channels <= 2^20, tokens and seqs <= 2^30,
- * (tokens + seqs) * channels < 2^34, x_stride <= 2^22. */
+ * (tokens + seqs) * ceil(channels / 1024) < 2^24, x_stride <= 2^22. */
 dl_status dl_short_conv(const dl_conv_desc *d, const void *initial, void *final_state, void *y, void *stream);
 /* Its gradients from dy [tokens, channels] and d_final (as final_state; either
  * NULL: zero): dx (contiguous), dweight, dbias (NULL: not wanted; else the
@@ -433,8 +433,8 @@ typedef struct {
  * dtype and whether z is NULL are read); 0 for sizes that are not supported: 1 <=
  * states <= 64, channels a multiple of groups, channels <= 2^20, tokens and seqs
  * <= 2^30, (seqs + tokens/64) * channels/16 < 2^23 (channels rounded up to
- * sixteens per group, and their number to a multiple of eight), tokens * groups *
- * states < 2^31, strides <= 2^22. */
+ * sixteens per group, and their number to a multiple of eight), 2 tokens * groups *
+ * states + 16 channels * (states + 2) < 2^32 - 2^13, strides <= 2^22. */
 size_t dl_ssm_workspace_bytes(const dl_ssm_desc *d);
 size_t dl_ssm_saved_bytes(const dl_ssm_desc *d);
 size_t dl_ssm_backward_workspace_bytes(const dl_ssm_desc *d);
@@ -452,7 +452,7 @@ dl_status dl_ssm_scan_backward(const dl_ssm_desc *d, const void *saved, const vo
                                void *dx, void *ddt, void *dz, void *db, void *dc, float *da, float *dd,
                                float *ddt_bias, float *d_initial, void *workspace, void *stream);
 /* One token of each of `tokens` requests, rows of `state` [n_state_rows, channels,
- * states] fp32 as for dl_short_conv_step; tokens * channels < 2^28. */
+ * states] fp32 as for dl_short_conv_step; tokens * ceil(channels / 16) < 2^24. */
 dl_status dl_ssm_step(const dl_ssm_desc *d, float *state, const int *state_rows, int n_state_rows, void *y,
                       void *stream);
 

@@ -405,9 +405,9 @@ template <typename T, int W, int V, bool VEC> __global__ __launch_bounds__(NT) v
 // One token each: state row r = [W - 1][C] moves up by one and takes x.
 template <typename T, int W, int V, bool VEC> __global__ __launch_bounds__(NT) void conv_step_kernel(ConvArgs a)
 {
-    const long unit = static_cast<long>(blockIdx.x) * NT + threadIdx.x;
-    const int groups = (a.C + V - 1) / V, t = unit / groups, c = unit % groups * V;
-    if (t >= a.T)
+    // workgroups of a row: `wide`
+    const int wide = ((a.C + V - 1) / V + NT - 1) / NT, t = blockIdx.x / wide, c = (blockIdx.x % wide * NT + threadIdx.x) * V;
+    if (c >= a.C)
         return;
     Lane<T, W, V, VEC> l(a, c);
     const int r = a.rows ? a.rows[t] : t;
@@ -444,10 +444,11 @@ enum Kind { FORWARD, BACKWARD, STEP };
 template <typename T, int W, int V, bool VEC> hipError_t conv_v(Kind kind, const ConvArgs &a, hipStream_t st)
 {
     const long groups = (a.C + V - 1) / V;
-    const long units = groups * (kind == STEP ? a.T : a.runs + ((kind == FORWARD ? a.fin : a.dinit) ? a.N : 0));
-    if (units == 0)
+    const long units = groups * (a.runs + ((kind == FORWARD ? a.fin : a.dinit) ? a.N : 0));
+    const long blocks = kind == STEP ? a.T * ((groups + NT - 1) / NT) : (units + NT - 1) / NT;
+    if (blocks == 0)
         return hipSuccess;
-    const dim3 grid(static_cast<unsigned>((units + NT - 1) / NT));
+    const dim3 grid(static_cast<unsigned>(blocks));
     if (kind == FORWARD)
         hipLaunchKernelGGL((conv_kernel<T, W, V, VEC>), grid, dim3(NT), 0, st, a);
     else if (kind == BACKWARD)

@@ -36,7 +36,8 @@ dl_status check_conv(const dl_conv_desc *d)
     if (d->taps < 2 || d->taps > 4 || d->channels > kMostChannels || d->tokens > (1 << 30) || d->seqs > (1 << 30))
         return DL_E_SHAPE;
     const long long groups = (d->channels + dl::kConvChannels - 1) / dl::kConvChannels;
-    if ((static_cast<long long>(d->tokens) + d->seqs) * groups > (kMostBlocks - 1) * 256)
+    // (a step's rows are whole workgroups)
+    if ((static_cast<long long>(d->tokens) + d->seqs) * ((groups + 255) / 256) >= kMostBlocks)
         return DL_E_SHAPE;
     return DL_OK;
 }
@@ -113,10 +114,10 @@ dl_status check_ssm(const dl_ssm_desc *d)
         return DL_E_SHAPE;
     const long long tiles = static_cast<long long>(d->groups) *
                             ((d->channels / d->groups + dl::kSsmTile - 1) / dl::kSsmTile);
-    // a workgroup per sequence (or segment, not shorter than 64 tokens) and tile; a
-    // thread per element of dB and dC
+    // a workgroup per sequence (or segment, not shorter than 64 tokens) and tile; in one
+    // launch a thread per element of dB and dC and sixteen per one of dA, dD, ddt_bias
     if ((static_cast<long long>(d->seqs) + d->tokens / 64) * ((tiles + 7) / 8 * 8) * 2 >= kMostBlocks ||
-        2LL * d->tokens * d->groups * d->states >= kMostBlocks * 256)
+        2LL * d->tokens * d->groups * d->states + 16LL * d->channels * (d->states + 2) >= kMostBlocks * 256 - 4096)
         return DL_E_SHAPE;
     return DL_OK;
 }
@@ -444,7 +445,8 @@ dl_status dl_ssm_step(const dl_ssm_desc *d, float *state, const int *state_rows,
     const dl_status st = ssm_inputs(d, true, a, in);
     if (st != DL_OK)
         return st;
-    if (static_cast<long long>(d->tokens) * d->channels >= 1LL << 28) // up to sixteen lanes each
+    // up to sixteen lanes a channel, whole workgroups a row
+    if (static_cast<long long>(d->tokens) * ((16LL * d->channels + 255) / 256) >= kMostBlocks)
         return DL_E_SHAPE;
     if (d->tokens == 0)
         return DL_OK;

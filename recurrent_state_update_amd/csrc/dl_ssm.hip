@@ -255,11 +255,12 @@ constexpr int STEP = 256;
 // are whole vectors.
 template <typename T, int L, bool VEC> __global__ __launch_bounds__(STEP) void ssm_step_kernel(SsmArgs a)
 {
-    const long unit = (static_cast<long>(blockIdx.x) * STEP + threadIdx.x) / L; // row and channel
+    // workgroups of a row: `wide`
+    const int wide = (a.C * L + STEP - 1) / STEP, t = blockIdx.x / wide, c = (blockIdx.x % wide * STEP + threadIdx.x) / L;
     const int n0 = threadIdx.x % L * 4;
-    if (unit >= static_cast<long>(a.T) * a.C) // whole groups of lanes
+    if (c >= a.C) // whole groups of lanes
         return;
-    const int t = unit / a.C, c = unit % a.C, g = c / a.CG, m = a.S - n0; // states of this lane, if positive
+    const int g = a.G == 1 ? 0 : c / a.CG, m = a.S - n0; // states of this lane, if positive
     const int r = a.rows ? a.rows[t] : t;
     float *const state = a.state + (static_cast<long>(r) * a.C + c) * a.S + n0;
     const bool known = r >= 0 && r < a.n_rows;
@@ -301,8 +302,7 @@ template <typename T, int L, bool VEC> __global__ __launch_bounds__(STEP) void s
 
 template <typename T, int L> hipError_t step_l(const SsmArgs &a, hipStream_t st)
 {
-    const long lanes = static_cast<long>(a.T) * a.C * L;
-    const dim3 grid(static_cast<unsigned>((lanes + STEP - 1) / STEP));
+    const dim3 grid(static_cast<unsigned>(static_cast<long>(a.T) * ((a.C * L + STEP - 1) / STEP)));
     if (a.vec_s && a.vec_b)
         hipLaunchKernelGGL((ssm_step_kernel<T, L, true>), grid, dim3(STEP), 0, st, a);
     else
