@@ -2,7 +2,7 @@
 
     python bench_decoder.py [--op gdn] [--layers 8] [--B 64] [--H 32] [--d 128]
                             [--M 8] [--hidden 2048] [--ffn 4096] [--cycles 8]
-                            [--gated] [--fused] [--prompt T]
+                            [--gated] [--fused] [--conv TAPS] [--prompt T]
 
 The pages find that the state-update kernel's speedup shrinks end to end,
 since the rest of a decode step is unchanged ([sum] "Results" and
@@ -28,7 +28,9 @@ which runs in libdeltalog.
 --gated puts a per-head norm with an output gate behind the step, as GDN and
 KDA layers have it: o <- rms(o) g silu(h @ W_g).  --fused runs the residual
 adds and norms (and that gated norm) as the library's fused operators instead
-of torch's elementwise ones.  --prompt T first runs a prompt of T tokens per
+of torch's elementwise ones.  --conv TAPS puts the short causal convolution of
+such layers, with its SiLU, on q, k and v behind the projection (the library's
+short_conv, and short_conv_step on a state per layer).  --prompt T first runs a prompt of T tokens per
 request through all layers as whole sequences (the library's scan, from the
 initial states), times it, and decodes from the states it leaves.
 
@@ -82,13 +84,17 @@ class SyntheticDecoder:
                 # library GEMM picks a better kernel at decode batch sizes)
                 lay = {k: torch.from_numpy(p[k]).cuda().to(wdtype).t().contiguous()
                        for k in ("W_in", "W_o", "W_gu", "W_dn", "W_g") if k in p}
+                if ds.taps:
+                    lay["conv"] = torch.from_numpy(p["conv"]).cuda()
                 lay["g"] = torch.from_numpy(p["g"]).cuda() if ds.gated else None
                 lay["u"] = None if p["u"] is None else torch.from_numpy(p["u"]).cuda()
                 lay["X0"] = p["X0"]
             else:
                 src = weights_from.layers[l]
-                lay = {k: src[k] for k in ("W_in", "W_o", "W_gu", "W_dn", "W_g", "g", "u", "X0") if k in src}
+                lay = {k: src[k] for k in ("W_in", "W_o", "W_gu", "W_dn", "W_g", "conv", "g", "u", "X0") if k in src}
             lay["base"] = torch.from_numpy(lay["X0"]).cuda()
+            if ds.taps:  # the last inputs of every request's convolution
+                lay["seen"] = torch.zeros(ds.B, ds.taps - 1, lay["conv"].shape[0], dtype=wdtype, device="cuda")
             if path == "deltalog":
                 lay["st"] = rsu.DeltaLogState(ds.op, ds.B, ds.H, ds.dk, ds.dv, ds.M, dtype=wdtype,
                                               base=lay["base"], u=lay["u"])
@@ -104,16 +110,31 @@ class SyntheticDecoder:
         import torch.nn.functional as F
         return self.project(F.rms_norm(x, (self.ds.hidden,), eps=EPS).to(self.wd), lay)
 
-    def project(self, h, lay):
+    def mix(self, x, lay, tokens):
+        """The short convolution of q, k and v, rows x [n, H(2 d_k + d_v)]: the
+        next token of each request, or all of a prompt's from its start.  Leaves
+        the layer's last inputs."""
+        import torch
+        if not tokens:
+            return self.rsu.short_conv_step(x, lay["seen"], lay["conv"])
+        with torch.no_grad():
+            y, end = self.rsu.short_conv(x.unflatten(0, (-1, tokens)), lay["conv"])
+        lay["seen"].copy_(end)
+        return y.flatten(0, 1)
+
+    def project(self, h, lay, tokens=0):
         """Projection and per-head prep of one layer: q, k, v in the input
         dtype, beta and ld in fp32, shaped as the decode step takes them, for
-        rows h [n, hidden] (a request's tokens, or one of each request)."""
+        rows h [n, hidden] (a prompt's `tokens` of each request, or the next of each)."""
         import torch
         import torch.nn.functional as F
         ds = self.ds
         n, H = h.shape[0], ds.H
-        p = F.linear(h, lay["W_in"]).float()
-        q, k, v, zb, zd = torch.split(p, ds.proj_split, dim=1)
+        p = F.linear(h, lay["W_in"])
+        if ds.taps:
+            qkv, rest = p.split([lay["conv"].shape[0], p.shape[1] - lay["conv"].shape[0]], dim=1)
+            p = torch.cat([self.mix(qkv, lay, tokens), rest], dim=1)
+        q, k, v, zb, zd = torch.split(p.float(), ds.proj_split, dim=1)
         q = q.reshape(n, H, ds.dk)
         k = k.reshape(n, H, ds.dk)
         if ds.op != "rwkv6":
@@ -164,16 +185,17 @@ class SyntheticDecoder:
                 o = F.rms_norm(o.float(), (ds.dv,), eps=EPS) * lay["g"] * F.silu(gate.float())
         return o.reshape(-1, ds.H * ds.dv).to(self.wd)
 
-    def rows(self, x, recurrence):
-        """Rows x [n, hidden] fp32 through all layers; recurrence(lay, q, k, v,
-        beta, ld) gives their o.  Returns the last layer's output and its rms
-        (both fp32)."""
+    def rows(self, x, recurrence, tokens=0):
+        """Rows x [n, hidden] fp32 (a prompt's `tokens` of each request, or the
+        next of each) through all layers; recurrence(lay, q, k, v, beta, ld)
+        gives their o.  Returns the last layer's output and its rms (both
+        fp32)."""
         import torch
         import torch.nn.functional as F
         ds = self.ds
         x, h = self.add_norm(x)
         for i, lay in enumerate(self.layers):
-            o = recurrence(lay, *self.project(h, lay))
+            o = recurrence(lay, *self.project(h, lay, tokens))
             x, h = self.add_norm(x, F.linear(self.output(o, h, lay), lay["W_o"]))
             g, u = F.linear(h, lay["W_gu"]).float().split(ds.ffn, dim=1)
             last = i + 1 == len(self.layers)
@@ -190,7 +212,7 @@ class SyntheticDecoder:
         leaving every layer's states.  Returns what `token` returns for each
         request's last token."""
         B, T, hidden = X.shape
-        out, h = self.rows(X.reshape(B * T, hidden), lambda lay, *a: self.sequence_step(lay, *a, B, T))
+        out, h = self.rows(X.reshape(B * T, hidden), lambda lay, *a: self.sequence_step(lay, *a, B, T), T)
         return out.unflatten(0, (B, T))[:, -1], h.unflatten(0, (B, T))[:, -1]
 
     def token(self, x):
@@ -302,6 +324,8 @@ def main():
     ap.add_argument("--cycles", type=int, default=8, help="timed graph replays (M tokens each)")
     ap.add_argument("--gated", action="store_true", help="a gated per-head norm behind the step")
     ap.add_argument("--fused", action="store_true", help="residual adds and norms as the library's operators")
+    ap.add_argument("--conv", type=int, default=0, choices=[0, 2, 3, 4], metavar="TAPS",
+                    help="taps of a short causal convolution of q, k and v")
     ap.add_argument("--prompt", type=int, default=0, help="tokens per request run as whole sequences first")
     args = ap.parse_args()
 
@@ -309,7 +333,7 @@ def main():
     assert torch.cuda.is_available(), "bench_decoder.py needs a GPU"
     torch.cuda.set_device(0)
     ds = synth.DecoderShape(args.op, args.layers, args.B, args.H, args.d, args.d, args.M,
-                            args.hidden, args.ffn, gated=args.gated)
+                            args.hidden, args.ffn, gated=args.gated, taps=args.conv)
     wd = torch.bfloat16
     t0 = time.time()
     dl = SyntheticDecoder(ds, "deltalog", wd, fused=args.fused)
@@ -367,6 +391,8 @@ def main():
     }
     if args.gated or args.fused:
         out["config"].update(gated=args.gated, fused=args.fused)
+    if args.conv:
+        out["config"].update(conv_taps=args.conv)
     if prompt:
         out["prompt"] = prompt
     dl.close()

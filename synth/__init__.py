@@ -174,6 +174,7 @@ class DecoderShape:
     ffn: int
     seed: int = 0
     gated: bool = False   # a per-head norm with an output gate behind the step
+    taps: int = 0         # of a short causal convolution of q, k and v (0: none)
 
     def describe(self) -> str:
         return (f"{self.op} L={self.L} B={self.B} H={self.H} dk={self.dk} dv={self.dv} "
@@ -199,8 +200,9 @@ def decoder_layer(ds: DecoderShape, layer: int) -> dict:
     [hidden, sum(proj_split)], W_o [H*dv, hidden], W_gu [hidden, 2*ffn] (gate
     then up), W_dn [ffn, hidden]; RWKV6's u [H, dk] ~ N(0, 0.1) (else None);
     and the layer's initial state [B, H, dk, dv] ~ N(0, 0.1); gated shapes
-    then W_g [hidden, H*dv] and the norm's gain g [dv] ~ N(1, 0.1).  Draw order
-    as listed, from stream layer+1."""
+    then W_g [hidden, H*dv] and the norm's gain g [dv] ~ N(1, 0.1); shapes with
+    taps then conv [H*(2 dk + dv), taps] ~ N(0, 1/taps).  Draw order as listed,
+    from stream layer+1."""
     rng = _drng(ds, layer + 1)
     n_in = sum(ds.proj_split)
     out = {}
@@ -212,6 +214,8 @@ def decoder_layer(ds: DecoderShape, layer: int) -> dict:
     if ds.gated:
         out["W_g"] = _normal(rng, (ds.hidden, ds.H * ds.dv), 0.0, 1.0 / np.sqrt(ds.hidden))
         out["g"] = _normal(rng, (ds.dv,), 1.0, 0.1)
+    if ds.taps:
+        out["conv"] = _normal(rng, (sum(ds.proj_split[:3]), ds.taps), 0.0, 1.0 / np.sqrt(ds.taps))
     return out
 
 
