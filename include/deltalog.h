@@ -432,9 +432,9 @@ typedef struct {
  * and of the backward pass's workspace, each 256-byte aligned (of d only the sizes,
  * dtype and whether z is NULL are read); 0 for sizes that are not supported: 1 <=
  * states <= 64, channels a multiple of groups, channels <= 2^20, tokens and seqs
- * <= 2^30, (seqs + tokens/64) * channels/16 < 2^23 (channels rounded up to
- * sixteens per group, and their number to a multiple of eight), 2 tokens * groups *
- * states + 16 channels * (states + 2) < 2^32 - 2^13, strides <= 2^22. */
+ * <= 2^30, seqs * channels/16 < 2^22 (channels rounded up to sixteens per
+ * group, and their number to a multiple of eight), 2 tokens * groups * states +
+ * 16 channels * (states + 2) < 2^32 - 2^13, strides <= 2^22. */
 size_t dl_ssm_workspace_bytes(const dl_ssm_desc *d);
 size_t dl_ssm_saved_bytes(const dl_ssm_desc *d);
 size_t dl_ssm_backward_workspace_bytes(const dl_ssm_desc *d);

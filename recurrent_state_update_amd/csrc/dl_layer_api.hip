@@ -114,9 +114,10 @@ dl_status check_ssm(const dl_ssm_desc *d)
         return DL_E_SHAPE;
     const long long tiles = static_cast<long long>(d->groups) *
                             ((d->channels / d->groups + dl::kSsmTile - 1) / dl::kSsmTile);
-    // a workgroup per sequence (or segment, not shorter than 64 tokens) and tile; in one
-    // launch a thread per element of dB and dC and sixteen per one of dA, dD, ddt_bias
-    if ((static_cast<long long>(d->seqs) + d->tokens / 64) * ((tiles + 7) / 8 * 8) * 2 >= kMostBlocks ||
+    // a workgroup (of 512) per sequence and tile, of which cuts add no more than a few
+    // hundred; in one launch a thread per element of dB and dC and sixteen per one of
+    // dA, dD and ddt_bias
+    if (d->seqs * ((tiles + 7) / 8 * 8) >= kMostBlocks / 4 ||
         2LL * d->tokens * d->groups * d->states + 16LL * d->channels * (d->states + 2) >= kMostBlocks * 256 - 4096)
         return DL_E_SHAPE;
     return DL_OK;
