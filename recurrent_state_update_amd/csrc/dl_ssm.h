@@ -147,6 +147,14 @@ __device__ __forceinline__ float finite_rate(float a)
 {
     return a < -1e37f ? -1e37f : a;
 }
+// The state (the adjoint's G) on the other side of a segment whose decays' exponents add
+// up to `by`, which adds `add`.  In two halves: where states grow, the whole factor can
+// be out of range though a small state's product is not; and a state of zero stays so.
+__device__ __forceinline__ float across(float h, float by, float add)
+{
+    const float half = __builtin_amdgcn_exp2f(0.5f * by);
+    return h == 0.f ? add : fmaf(half * h, half, add);
+}
 
 // What a workgroup works on: tokens [t0, t0 + len) of sequence n, its segment
 // `index` of those whose first has slot `base`; last: the sequence ends with it.

@@ -86,7 +86,7 @@ template <typename T, int S, bool VEC, bool SAVE> __global__ __launch_bounds__(N
 #pragma unroll
             for (int s = 0; s < S; ++s)
                 if (i0 + i < p.index && has[s])
-                    h[s] = fmaf(__builtin_amdgcn_exp2f(sum[i] * rate[s]), h[s], add[i][s]);
+                    h[s] = across(h[s], sum[i] * rate[s], add[i][s]);
     }
     if (set == 0)
 #pragma unroll

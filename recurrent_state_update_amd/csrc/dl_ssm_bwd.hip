@@ -171,7 +171,7 @@ template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ?
 #pragma unroll
                     for (int s = 0; s < S; ++s)
                         if (k0 - k > p.index && in_tile(i) < nc && j + 16 * s < a.S)
-                            G[i][s] = fmaf(__builtin_amdgcn_exp2f(sum[k] * rate[i][s]), G[i][s], add[k][s]);
+                            G[i][s] = across(G[i][s], sum[k] * rate[i][s], add[k][s]);
             }
     }
 
