@@ -479,9 +479,9 @@ hipError_t launch_short_conv_backward(int dtype, const ConvArgs &a, hipStream_t 
 {
     hipError_t e = conv(BACKWARD, dtype, a, st);
     if (e == hipSuccess && a.d_weight)
-        e = column_sum(a.part_w, a.runs, a.C * a.W, a.d_weight, nullptr, st);
-    if (e == hipSuccess && a.d_bias)
-        e = column_sum(a.part_b, a.runs, a.C, a.d_bias, nullptr, st);
+        e = column_sum(a.part_w, a.runs, a.C * a.W, a.d_weight, a.C, a.d_bias, st);
+    else if (e == hipSuccess && a.d_bias)
+        e = column_sum(a.part_b, a.runs, a.C, a.d_bias, 0, nullptr, st);
     return e;
 }
 

@@ -165,8 +165,8 @@ hipError_t launch_scan_kda(int dtype, bool backward, const ScanArgs &a, hipStrea
 hipError_t launch_scan_rwkv6(int dtype, bool backward, const ScanArgs &a, hipStream_t st);
 
 // out0[j] = the sum over the rows of partial [blocks][n], in 64 bits and in a fixed
-// order; with out1 the same of a second such array right behind the first (dl_norm.hip).
-hipError_t column_sum(const float *partial, int blocks, int n, float *out0, float *out1, hipStream_t st);
+// order; with out1 the same of a second array [blocks][n1] right behind (dl_norm.hip).
+hipError_t column_sum(const float *partial, int blocks, int n, float *out0, int n1, float *out1, hipStream_t st);
 
 struct GatedNormArgs {
     long units; // rows x H
@@ -269,7 +269,7 @@ struct ConvArgs {
     const void *dy, *dfin;
     void *dx, *dinit;
     float *d_weight, *d_bias;
-    float *part_w, *part_b; // [runs][C][W], [runs][C]
+    float *part_w, *part_b; // [runs][C][W] and, behind it, [runs][C]; each NULL if not wanted
 };
 hipError_t launch_short_conv(int dtype, const ConvArgs &a, hipStream_t st);
 hipError_t launch_short_conv_backward(int dtype, const ConvArgs &a, hipStream_t st);

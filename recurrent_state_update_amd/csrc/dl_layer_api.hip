@@ -266,8 +266,7 @@ size_t dl_short_conv_workspace_bytes(const dl_conv_desc *d)
 {
     if (check_conv(d) != DL_OK)
         return 0;
-    const size_t rows = static_cast<size_t>(conv_runs(d, true)) * d->channels * 4;
-    return up256(rows * d->taps) + up256(rows) + 256; // never 0
+    return static_cast<size_t>(conv_runs(d, true)) * d->channels * (d->taps + 1) * 4 + 256; // never 0
 }
 
 dl_status dl_short_conv_backward(const dl_conv_desc *d, const void *initial, const void *dy, const void *d_final,
@@ -307,8 +306,7 @@ dl_status dl_short_conv_backward(const dl_conv_desc *d, const void *initial, con
     if (dweight)
         a.part_w = static_cast<float *>(workspace);
     if (dbias)
-        a.part_b = reinterpret_cast<float *>(static_cast<char *>(workspace) +
-                                             up256(static_cast<size_t>(a.runs) * d->channels * d->taps * 4));
+        a.part_b = static_cast<float *>(workspace) + static_cast<size_t>(a.runs) * d->channels * d->taps;
     return status(dl::launch_short_conv_backward(d->dtype, a, static_cast<hipStream_t>(stream)));
 }
 

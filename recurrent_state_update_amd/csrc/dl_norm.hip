@@ -139,12 +139,16 @@ __global__ __launch_bounds__(256) void gated_norm_bwd_kernel(GatedNormArgs a)
 // take every 16th row, eight loads at a time.  In 64 bits: up to 1024 rows are
 // summed, and the time is the loads'.
 __global__ __launch_bounds__(256) void column_sum_kernel(const float *partial, int blocks, int n, float *out0,
-                                                         float *out1)
+                                                         int n1, float *out1)
 {
     __shared__ double part[16][17];
     const int c = threadIdx.x % 16, s = threadIdx.x / 16, j = blockIdx.x * 16 + c;
-    partial += static_cast<long>(blockIdx.y) * blocks * n;
-    float *out = blockIdx.y ? out1 : out0;
+    float *out = out0;
+    if (blockIdx.y) {
+        partial += static_cast<long>(blocks) * n;
+        n = n1;
+        out = out1;
+    }
     double x = 0.;
     if (j < n) {
         int b = s;
@@ -171,10 +175,11 @@ __global__ __launch_bounds__(256) void column_sum_kernel(const float *partial, i
 
 } // namespace
 
-hipError_t column_sum(const float *partial, int blocks, int n, float *out0, float *out1, hipStream_t st)
+hipError_t column_sum(const float *partial, int blocks, int n, float *out0, int n1, float *out1, hipStream_t st)
 {
-    hipLaunchKernelGGL(column_sum_kernel, dim3((n + 15) / 16, out1 ? 2 : 1), dim3(256), 0, st, partial, blocks, n, out0,
-                       out1);
+    const int most = out1 && n1 > n ? n1 : n;
+    hipLaunchKernelGGL(column_sum_kernel, dim3((most + 15) / 16, out1 ? 2 : 1), dim3(256), 0, st, partial, blocks, n,
+                       out0, n1, out1);
     return hipGetLastError();
 }
 
@@ -200,7 +205,7 @@ hipError_t gated_norm_t(bool aligned, bool backward, const GatedNormArgs &a, hip
         hipLaunchKernelGGL((gated_norm_bwd_kernel<TO, T, D, false>), dim3(a.blocks), dim3(256), 0, st, a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess || !a.d_weight)
         return e;
-    return column_sum(a.partial, a.blocks, D, a.d_weight, nullptr, st);
+    return column_sum(a.partial, a.blocks, D, a.d_weight, 0, nullptr, st);
 }
 
 template <typename TO, typename T>
@@ -424,7 +429,8 @@ hipError_t residual_norm_k(bool backward, const ResidualNormArgs &a, hipStream_t
     hipLaunchKernelGGL((residual_norm_bwd_kernel<T, NT, VEC, E, ONCE>), dim3(a.blocks), dim3(NT), 0, st, a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && (a.d_scale || a.d_weight))
-        e = column_sum(a.partial, a.blocks, a.D, a.d_scale ? a.d_scale : a.d_weight, a.d_scale ? a.d_weight : nullptr, st);
+        e = column_sum(a.partial, a.blocks, a.D, a.d_scale ? a.d_scale : a.d_weight, a.D, a.d_scale ? a.d_weight : nullptr,
+                       st);
     return e;
 }
 
