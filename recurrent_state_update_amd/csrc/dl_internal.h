@@ -223,7 +223,7 @@ struct SsmArgs {
     const float *init; // [N][C][S], or NULL (zero)
     float *fin;        // [N][C][S], or NULL
     void *y;           // [T][C]
-    int seg;           // tokens per segment (a multiple of every stage's), or 0: sequences uncut
+    int seg;           // tokens per segment (a multiple of kSsmBlock), or 0: sequences uncut
     int slots, tiles;  // pieces (N, or segments' slots), channel tiles
     // [slots][C][S] a segment's end state from zero and [slots][C] its sum of
     // delta; backward: the gradient of its start state, from zero behind it

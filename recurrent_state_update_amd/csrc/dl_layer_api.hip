@@ -115,7 +115,7 @@ dl_status check_ssm(const dl_ssm_desc *d)
     const long long tiles = static_cast<long long>(d->groups) *
                             ((d->channels / d->groups + dl::kSsmTile - 1) / dl::kSsmTile);
     // a workgroup (of 512) per sequence and tile, of which cuts add no more than a few
-    // hundred; in one launch a thread per element of dB and dC and sixteen per one of
+    // thousand; in one launch a thread per element of dB and dC and sixteen per one of
     // dA, dD and ddt_bias
     if (d->seqs * ((tiles + 7) / 8 * 8) >= kMostBlocks / 4 ||
         2LL * d->tokens * d->groups * d->states + 16LL * d->channels * (d->states + 2) >= kMostBlocks * 256 - 4096)
@@ -131,24 +131,60 @@ int tiles_of(const dl_ssm_desc *d, int tile)
 // Tokens per segment, or 0: sequences uncut.  Cut, every token is gone over twice
 // (once for what its segment adds to the state), which pays where uncut ones leave
 // most of the GPU idle.
-int ssm_segment(const dl_ssm_desc *d, bool backward)
+//
+// Forward: where the sequences' mean length says so.  us, 16 states, bf16, by segment
+// (uncut first):
+//                     uncut   64   128   256   512  1024
+//   512 x 64 channels  15.4  10.6  12.9  18.0
+//   1024 x 512         26.1  18.0  13.8  18.4  28.2
+//   1024 x 2048        27.2  59.8  40.1  31.4  29.4
+//   4096 x 512         97               32.8  29.8
+//   4096 x 2048       101                      95    89
+//   2 x 2048 x 2048    52.4       159   114    90    78.3
+//   16384 x 256       375     best 55
+int ssm_forward_segment(const dl_ssm_desc *d)
 {
-    const long tiles = tiles_of(d, backward ? dl::kSsmGradTile : dl::kSsmTile), wgs = tiles * d->seqs;
-    const long want = backward ? 512 : 256, each = d->tokens / d->seqs;
-    if (wgs * 2 > want || each < (backward ? 128 : 256))
+    const long want = 256, wgs = static_cast<long>(tiles_of(d, dl::kSsmTile)) * d->seqs, each = d->tokens / d->seqs;
+    if (wgs * 2 > want || each < 256)
         return 0;
-    long n = want / wgs;
-    if (n > each / 64)
-        n = each / 64;
-    const long seg = ((each + n - 1) / n + 63) / 64 * 64;
-    return static_cast<int>(seg);
+    const long n = want / wgs < each / 64 ? want / wgs : each / 64;
+    return static_cast<int>(((each + n - 1) / n + 63) / 64 * 64);
+}
+
+// Backward: a wave has four times the channels and eight times the work of a token, so
+// that one long sequence among short ones is what a batch waits for.  As many tokens as
+// fill the GPU if all are as long, whatever their lengths are (they are known on the
+// device only: where none is longer the cut costs 5 to 15 us, where one is it gains most
+// of the time), and not less than about sqrt(1.5 T), where a sequence's joins begin to
+// cost more than its segments.  us of both passes:
+//                           uncut    32    64    96   128   256   512
+//   128 x 64 channels        45.8  27.9  35.7
+//   512 x 64                  144  37.5  41.4  50.5  56.6  90.6
+//   512 x 1024, 64 states     481   108   125   148   169   287
+//   3 x 200 x 512, 64 states  206  85.8   106   132   157
+//   4096 x 512               1067   162   107   110   107   131   189
+//   1024 x 2048               301   120  95.2   105  99.8   126   189
+//   2 x 2048 x 2048           583               255   227   219   302
+//   40 x 100 + 2000, x 2048   800               473   423   423   478
+//   255 x 17 + 4096, x 512   1330         420   423   420   428   487
+//   16 x 64 x 512            35.9  45.3  41.4  41.3  40.9  40.5  40.8
+//   16 x 300 x 2048           237               311   303   299   252
+int ssm_backward_segment(const dl_ssm_desc *d)
+{
+    const long want = 512, T = d->tokens, tiles = tiles_of(d, dl::kSsmGradTile);
+    const long full = (T * tiles + want - 1) / want;
+    long seg = (full + 31) / 32 * 32;
+    seg = seg < 32 ? 32 : seg;
+    while (2 * seg * seg < 3 * T)
+        seg += 32;
+    return T < 128 || 2 * seg > T ? 0 : static_cast<int>(seg);
 }
 
 struct SsmSizes {
     int seg, bseg, slots, bslots;
     size_t states, sums, ahead, plain, bstates, bsums, part, bc;
     explicit SsmSizes(const dl_ssm_desc *d)
-        : seg(ssm_segment(d, false)), bseg(ssm_segment(d, true)),
+        : seg(ssm_forward_segment(d)), bseg(ssm_backward_segment(d)),
           slots(seg ? static_cast<int>(dl::ssm_slots(d->tokens, d->seqs, seg)) : d->seqs),
           bslots(bseg ? static_cast<int>(dl::ssm_slots(d->tokens, d->seqs, bseg)) : d->seqs)
     {
@@ -266,7 +302,7 @@ size_t dl_short_conv_workspace_bytes(const dl_conv_desc *d)
 {
     if (check_conv(d) != DL_OK)
         return 0;
-    return static_cast<size_t>(conv_runs(d, true)) * d->channels * (d->taps + 1) * 4 + 256; // never 0
+    return up256(static_cast<size_t>(conv_runs(d, true)) * d->channels * (d->taps + 1) * 4) + 256; // never 0
 }
 
 dl_status dl_short_conv_backward(const dl_conv_desc *d, const void *initial, const void *dy, const void *d_final,

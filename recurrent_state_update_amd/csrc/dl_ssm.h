@@ -173,9 +173,9 @@ struct Piece {
         len = end - start;
         last = true;
         if (seg) {
-            const int off = index * seg; // index <= slots <= T / seg + N: checked on the host to fit
-            t0 = start + off;
-            len = len - off;
+            const long off = static_cast<long>(index) * seg; // (offsets out of order can give any index)
+            t0 = start + static_cast<int>(off);
+            len = off < len ? len - static_cast<int>(off) : 0;
             last = len <= seg;
             len = len > seg ? seg : len;
         }

@@ -123,7 +123,7 @@ int main()
                                                        nullptr, fake(23), nullptr) == DL_OK);
                             const dl::SsmArgs b = dl::g_ssm, h = dl::g_ahead;
                             CHECK(b.saved == f.saved && b.plain == f.plain && h.seg == b.seg && h.slots == b.slots && h.tiles == f.tiles);
-                            CHECK(b.tiles * 64L >= C && b.seg % 64 == 0 && b.slots * ((b.tiles + 7L) / 8 * 8) < (1L << 24));
+                            CHECK(b.tiles * 64L >= C && b.seg % 16 == 0 && b.slots * ((b.tiles + 7L) / 8 * 8) < (1L << 24));
                             CHECK(b.slots * ((h.tiles + 7L) / 8 * 8) < (1L << 24));
                             if (b.seg)
                                 CHECK(b.slots >= T / b.seg + N && long(b.slots) * b.seg < INT_MAX);

@@ -490,3 +490,14 @@ def test_step_cache_beyond_32_bits():
     want = rsu.ssm_step(v["x"], v["dt"], small, *args)
     assert torch.equal(y, want) and torch.equal(cache[S - 1], small[0]) and torch.equal(cache[0], small[1])
     assert not cache[1:S - 1].any()
+
+
+@needs_gpu
+@pytest.mark.parametrize("lens,C,N", [([128], 16, 16), ([64, 64], 20, 33), ([1] * 40 + [300] + [2] * 20, 70, 16),
+                                      ([5, 0, 0, 590, 0], 130, 24)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_one_long_sequence_among_short_ones(lens, C, N, dtype):
+    """Cut by all tokens, not by each sequence's: pieces that do not exist, empty ones."""
+    x, cu, dy, dend = inputs(lens, C, N, 1, dtype, first=1, tail=40, seed=6)
+    poison()
+    compare(x, cu, dy, dend, run(x, cu, dy, dend), max(lens))
