@@ -228,7 +228,7 @@ struct Sources {
 // for it early; what is not there is dropped when put.
 template <typename T, int S, int TT, bool VEC> struct Loader {
     static constexpr int XV = CH * TT / LOADERS, XPR = CH / XV; // channels, threads per token
-    static constexpr int BV = 4, BPR = 16 * S / BV, BTOK = LOADERS / BPR, BK = TT / BTOK;
+    static constexpr int BV = 16 * S * TT / LOADERS < 4 ? 16 * S * TT / LOADERS : 4, BPR = 16 * S / BV, BTOK = LOADERS / BPR, BK = TT / BTOK;
     static_assert(XPR * TT == LOADERS && BK * BTOK == TT && BK > 0, "every thread loads as much");
     Sources s;
     int xt, xc, bt, bn, nx, nb; // token, channel, token, state; channels and states there are

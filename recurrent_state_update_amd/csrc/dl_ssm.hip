@@ -12,11 +12,25 @@ namespace {
 
 constexpr int NT = 2 * LOADERS;
 
-// Tokens per stage: its decays and inputs are 64 registers each.
-constexpr int stage_tokens(int S) { return 64 / S; }
+// Tokens per stage (TT, times S): the decays and inputs of 64 are 64 registers each, of
+// which a SIMD holds the waves of one workgroup; of 32 those of two.  Where there is a
+// workgroup per CU at the most, the fewest barriers; where there are more, two at a time,
+// which hide each other's; and 16 for short sequences, whose stages are not full.  us,
+// bf16, 16 states, sequences x tokens x channels (4096 and 2 x 2048 x 2048: 256
+// workgroups, one per CU):
+//                          16     32     64
+//   1024 x 8 x 512         161           576
+//   256 x 32 x 512        52.7           149
+//   16 x 128 x 2048       33.2   35.1   53.7
+//   8 x 256 x 2048        31.4   30.5   40.0
+//   8 x 1024 x 2048        111   99.9    110
+//   4 x 2048 x 4096        198    177    189
+//   2 x 2048 x 2048       73.9   62.9   51.8
+//   4096 x 4096            143    119   95.8
+constexpr int CUS = 256, SHORT = 128;
 
-template <int S> struct Shared {
-    using In = Stage<S, stage_tokens(S)>;
+template <int S, int TT> struct Shared {
+    using In = Stage<S, TT>;
     In in[3];
     float y[2][CH][In::XLD];
     float h[S][LOADERS];
@@ -28,11 +42,11 @@ template <int S> struct Shared {
 // whose latency is twice its issue), forms y and loads, the other forms the decays and
 // inputs of the next, which need no state.  So a sequence of a few thousand channels,
 // one wave of states per SIMD, has two to issue from.
-template <typename T, int S, bool VEC, bool SAVE> __global__ __launch_bounds__(NT, 2) void ssm_kernel(SsmArgs a)
+template <typename T, int S, int TT, bool VEC, bool SAVE> __global__ __launch_bounds__(NT, 2) void ssm_kernel(SsmArgs a)
 {
-    constexpr int TT = stage_tokens(S), NB = TT / TB;
+    constexpr int NB = TT / TB;
     using Load = Loader<T, S, TT, VEC>;
-    __shared__ Shared<S> sh;
+    __shared__ Shared<S, TT> sh;
 
     const Work work(blockIdx.x, a.tiles);
     if (work.tile < 0)
@@ -112,7 +126,7 @@ template <typename T, int S, bool VEC, bool SAVE> __global__ __launch_bounds__(N
     Own<NB> own;
     float d[NB][S][TB], v[NB][S][TB];
     const auto ahead = [&](int k) {
-        const typename Shared<S>::In &st = sh.in[k % 3];
+        const typename Shared<S, TT>::In &st = sh.in[k % 3];
         own.form(st, row, j, p.len - k * TT, bias, a.softplus);
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
@@ -135,7 +149,7 @@ template <typename T, int S, bool VEC, bool SAVE> __global__ __launch_bounds__(N
     };
     // The states through the stage, and its y.
     const auto chain = [&](int k) {
-        const typename Shared<S>::In &st = sh.in[k % 3];
+        const typename Shared<S, TT>::In &st = sh.in[k % 3];
 #pragma unroll
         for (int s = 0; s < S; ++s)
             h[s] = sh.h[s][tid];
@@ -228,18 +242,27 @@ template <typename T, int S, bool VEC, bool SAVE> __global__ __launch_bounds__(N
                 a.fin[p.n * states + of_c + 16 * s] = sh.h[s][tid];
 }
 
-template <typename T, int S, bool VEC> hipError_t scan_v(const SsmArgs &a, hipStream_t st)
+template <typename T, int S, int TT, bool VEC> hipError_t scan_v(const SsmArgs &a, hipStream_t st)
 {
     const dim3 grid(static_cast<unsigned>(work_groups(a)));
     if (a.saved)
-        hipLaunchKernelGGL((ssm_kernel<T, S, VEC, true>), grid, dim3(NT), 0, st, a);
+        hipLaunchKernelGGL((ssm_kernel<T, S, TT, VEC, true>), grid, dim3(NT), 0, st, a);
     else
-        hipLaunchKernelGGL((ssm_kernel<T, S, VEC, false>), grid, dim3(NT), 0, st, a);
+        hipLaunchKernelGGL((ssm_kernel<T, S, TT, VEC, false>), grid, dim3(NT), 0, st, a);
     return hipGetLastError();
+}
+template <typename T, int S, int TT> hipError_t scan_l(const SsmArgs &a, hipStream_t st)
+{
+    return a.vec_x && a.vec_b ? scan_v<T, S, TT, true>(a, st) : scan_v<T, S, TT, false>(a, st);
 }
 template <typename T, int S> hipError_t scan_s(const SsmArgs &a, hipStream_t st)
 {
-    return a.vec_x && a.vec_b ? scan_v<T, S, true>(a, st) : scan_v<T, S, false>(a, st);
+    if (a.T <= static_cast<long>(SHORT) * a.N)
+        return scan_l<T, S, TB>(a, st);
+    const long pieces = a.seg ? a.T / a.seg : a.N;
+    if (pieces * a.tiles > CUS)
+        return scan_l<T, S, S == 1 ? 32 : TB>(a, st);
+    return scan_l<T, S, 64 / S>(a, st);
 }
 template <typename T> hipError_t scan_t(const SsmArgs &a, hipStream_t st)
 {

@@ -501,3 +501,27 @@ def test_one_long_sequence_among_short_ones(lens, C, N, dtype):
     x, cu, dy, dend = inputs(lens, C, N, 1, dtype, first=1, tail=40, seed=6)
     poison()
     compare(x, cu, dy, dend, run(x, cu, dy, dend), max(lens))
+
+
+@needs_gpu
+@pytest.mark.parametrize("N,C", [(16, 4112), (20, 4100), (40, 4097)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_channels(N, C, dtype):
+    """More workgroups than CUs, of sequences that are not short."""
+    x, cu, dy, dend = inputs([150, 131], C, N, 1, dtype, seed=9)
+    poison()
+    compare(x, cu, dy, dend, run(x, cu, dy, dend), 150)
+
+
+@needs_gpu
+@pytest.mark.parametrize("N", [8, 24, 64])
+def test_any_company(N):
+    """A sequence's results are the same bits alone and among others, short and long,
+    whatever stages those take (it is not cut in either)."""
+    x, cu, _, _ = inputs([150, 1, 7] + [2] * 30 + [90] * 20, 4112, N, 1, "bf16", seed=4)
+    both = run(x, cu)
+    for k, n in enumerate([150, 1, 7]):
+        b = cu[k]
+        one = {m: t[b:b + n] if m in ("x", "dt", "B", "C", "z") else t[k:k + 1] if m == "initial" else t for m, t in x.items()}
+        alone = run(one, [0, n])
+        assert torch.equal(alone["y"], both["y"][b:b + n]) and torch.equal(alone["end"][0], both["end"][k])
