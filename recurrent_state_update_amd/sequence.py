@@ -493,8 +493,8 @@ def residual_norm_fp8(x, y=None, scale=None, weight=None, eps: float = 1e-6, gro
         xs, y = (None if t is None else _state(t) if group else t.contiguous() for t in (x, y))
         scale, weight = (None if t is None else t.contiguous() for t in (scale, weight))
         x_out = None if y is None else torch.empty_like(xs)
-        h = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-        h_scale = torch.empty((*lead, D // 128) if group else lead, dtype=torch.float32, device=x.device)
+        h = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
+        h_scale = x.new_empty((*lead, D // 128) if group else lead)
         _check(_lib.dl_residual_norm_quant(rows, D, DTYPES[dtype], xs.data_ptr(), _p(y), _p(scale), _p(weight), float(eps),
                                          _p(x_out), group or 0, h.data_ptr(), h_scale.data_ptr(), _current(x.device)),
                "dl_residual_norm_quant")

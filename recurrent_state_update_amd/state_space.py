@@ -14,7 +14,7 @@ import torch
 
 from . import (_check, _dtype_id, _lib, dl_conv_desc, dl_short_conv_workspace_bytes, dl_ssm_backward_workspace_bytes,
                dl_ssm_desc, dl_ssm_saved_bytes, dl_ssm_workspace_bytes)
-from .sequence import _MOST_STRIDE, _bytes, _count, _current, _gpu, _no_grad, _on, _p, _plain, _rows, _tensor, _wants_grad
+from .sequence import _MOST_STRIDE, _count, _current, _gpu, _no_grad, _on, _p, _plain, _rows, _tensor, _wants_grad
 
 _MOST_STATES = 64
 
@@ -61,7 +61,13 @@ def _whole(t):
 
 
 def _like(t):
-    return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    """A contiguous tensor of t's shape and type (half the host's time of torch.empty)."""
+    return None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def _scratch(n, t):
+    """n bytes beside t, an fp32 tensor."""
+    return t.new_empty(n + 3 >> 2)
 
 
 def _in_place(state, name, dtype, tail, device):
@@ -112,9 +118,8 @@ class _Conv:
             self.dti, self.T, N, self.C, self.W, self.silu, stride, _p(cu_seqlens), x.data_ptr(), weight.data_ptr(),
             _p(bias))
 
-    def forward(self, desc, N, initial):
-        y = torch.empty((*self.lead, self.C), dtype=self.dtype, device=self.device)
-        end = torch.empty((N, self.W - 1, self.C), dtype=self.dtype, device=self.device)
+    def forward(self, desc, x, N, initial):
+        y, end = _like(x), x.new_empty((N, self.W - 1, self.C))
         _check(_lib.dl_short_conv(desc, _p(initial), end.data_ptr(), y.data_ptr(), _current(self.device)),
                "dl_short_conv")
         return y, end
@@ -124,7 +129,7 @@ class _ConvFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, s, N, cu_seqlens, x, weight, bias, initial):
         tensors, desc = s.describe(N, x, weight, bias, cu_seqlens)
-        out = s.forward(desc, N, initial)
+        out = s.forward(desc, x, N, initial)
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(*tensors, initial)
         ctx.conv, ctx.N = s, N
@@ -139,11 +144,11 @@ class _ConvFn(torch.autograd.Function):
             # (a tensor's layout may be another than when it was saved)
             (x, weight, bias, cu_seqlens), desc = s.describe(ctx.N, x, weight, bias, cu_seqlens)
             initial, dy, d_end = _whole(initial), _whole(dy), _whole(d_end)
-            dx = torch.empty((*s.lead, s.C), dtype=s.dtype, device=s.device)
+            dx = _like(x)
             dw = _like(weight) if ctx.needs_input_grad[4] else None
             db = _like(bias) if ctx.needs_input_grad[5] else None
             d0 = _like(initial) if ctx.needs_input_grad[6] else None
-            ws = _bytes(dl_short_conv_workspace_bytes(desc), s.device) if dw is not None or db is not None else None
+            ws = None if dw is None and db is None else _scratch(dl_short_conv_workspace_bytes(desc), weight)
             _check(_lib.dl_short_conv_backward(desc, _p(initial), _p(dy), _p(d_end), dx.data_ptr(), _p(dw), _p(db),
                                                _p(d0), _p(ws), _current(s.device)), "dl_short_conv_backward")
         return None, None, None, dx, dw, db, d0
@@ -174,7 +179,7 @@ def short_conv(x, weight, bias=None, initial_state=None, cu_seqlens=None, silu: 
         if _wants_grad(x, weight, bias, initial):
             return _ConvFn.apply(s, N, cu, x, weight, bias, initial)
         tensors, desc = s.describe(N, x, weight, bias, cu)
-        return s.forward(desc, N, initial)
+        return s.forward(desc, x, N, initial)
 
 
 def short_conv_step(x, state, weight, bias=None, rows=None, silu: bool = True, stream=None):
@@ -194,7 +199,7 @@ def short_conv_step(x, state, weight, bias=None, rows=None, silu: bool = True, s
     _no_grad("short_conv_step", x, state, weight, bias)
     with _on(dev, stream):
         tensors, desc = s.describe(1, x, weight, bias, None)
-        y = torch.empty((s.T, s.C), dtype=x.dtype, device=dev)
+        y = _like(x)
         _check(_lib.dl_short_conv_step(desc, state.data_ptr(), _p(rows), state.shape[0], y.data_ptr(), _current(dev)),
                "dl_short_conv_step")
         _changed(state)
@@ -241,14 +246,12 @@ class _Ssm:
             self.dti, self.T, N, self.C, self.S, self.G, self.softplus, xs, dts, zs, bs, cs, _p(cu_seqlens),
             x.data_ptr(), dt.data_ptr(), _p(z), B.data_ptr(), C.data_ptr(), A.data_ptr(), _p(D), _p(dt_bias))
 
-    def forward(self, desc, N, initial, saved=None):
+    def forward(self, desc, x, A, N, initial, saved=None):
         n = dl_ssm_workspace_bytes(desc)
         if n == 0:
             raise ValueError(f"unsupported scan shape tokens={self.T} sequences={N} channels={self.C} states={self.S} "
                              f"groups={self.G}")
-        y = torch.empty((*self.lead, self.C), dtype=self.dtype, device=self.device)
-        end = torch.empty((N, self.C, self.S), dtype=torch.float32, device=self.device)
-        ws = _bytes(n, self.device)
+        y, end, ws = _like(x), A.new_empty((N, self.C, self.S)), _scratch(n, A)
         _check(_lib.dl_ssm_scan(desc, _p(initial), end.data_ptr(), y.data_ptr(), _p(saved), ws.data_ptr(),
                                 _current(self.device)), "dl_ssm_scan")
         return y, end
@@ -258,8 +261,8 @@ class _SsmFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, s, N, cu_seqlens, x, dt, A, B, C, D, z, dt_bias, initial):
         tensors, desc = s.describe(N, x, dt, A, B, C, D, z, dt_bias, cu_seqlens)
-        saved = _bytes(dl_ssm_saved_bytes(desc), s.device)
-        out = s.forward(desc, N, initial, saved)
+        saved = _scratch(dl_ssm_saved_bytes(desc), A)
+        out = s.forward(desc, x, A, N, initial, saved)
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(*tensors, saved)
         ctx.ssm, ctx.N = s, N
@@ -278,8 +281,8 @@ class _SsmFn(torch.autograd.Function):
             dz = _like(z)
             dD = _like(D) if ctx.needs_input_grad[8] else None
             dbias = _like(dt_bias) if ctx.needs_input_grad[10] else None
-            d0 = torch.empty((N, s.C, s.S), dtype=torch.float32, device=s.device) if ctx.needs_input_grad[11] else None
-            ws = _bytes(dl_ssm_backward_workspace_bytes(desc), s.device)
+            d0 = A.new_empty((N, s.C, s.S)) if ctx.needs_input_grad[11] else None
+            ws = _scratch(dl_ssm_backward_workspace_bytes(desc), A)
             _check(_lib.dl_ssm_scan_backward(desc, saved.data_ptr(), dy.data_ptr(), _p(d_end), dx.data_ptr(),
                                              ddt.data_ptr(), _p(dz), dB.data_ptr(), dC.data_ptr(), dA.data_ptr(),
                                              _p(dD), _p(dbias), _p(d0), ws.data_ptr(), _current(s.device)),
@@ -316,7 +319,7 @@ def ssm_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = True
         if _wants_grad(x, dt, A, B, C, D, z, dt_bias, initial):
             return _SsmFn.apply(s, N, cu, x, dt, A, B, C, D, z, dt_bias, initial)
         tensors, desc = s.describe(N, x, dt, A, B, C, D, z, dt_bias, cu)
-        return s.forward(desc, N, initial)
+        return s.forward(desc, x, A, N, initial)
 
 
 def ssm_step(x, dt, state, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = True, rows=None, stream=None):
@@ -336,7 +339,7 @@ def ssm_step(x, dt, state, A, B, C, D=None, z=None, dt_bias=None, softplus: bool
     _no_grad("ssm_step", x, dt, state, A, B, C, D, z, dt_bias)
     with _on(dev, stream):
         tensors, desc = s.describe(1, x, dt, A, B, C, D, z, dt_bias, None)
-        y = torch.empty((s.T, s.C), dtype=x.dtype, device=dev)
+        y = _like(x)
         _check(_lib.dl_ssm_step(desc, state.data_ptr(), _p(rows), state.shape[0], y.data_ptr(), _current(dev)),
                "dl_ssm_step")
         _changed(state)
