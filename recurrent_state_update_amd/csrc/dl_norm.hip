@@ -135,7 +135,7 @@ __global__ __launch_bounds__(256) void gated_norm_bwd_kernel(GatedNormArgs a)
 }
 
 // out[j] = the sum over the blocks' rows of partial [blocks][n] (blockIdx.y:
-// the second such pair).  A workgroup takes 16 columns; 16 threads per column
+// the second array, of n1 columns).  A workgroup takes 16 columns; 16 threads per column
 // take every 16th row, eight loads at a time.  In 64 bits: up to 1024 rows are
 // summed, and the time is the loads'.
 __global__ __launch_bounds__(256) void column_sum_kernel(const float *partial, int blocks, int n, float *out0,
@@ -488,12 +488,19 @@ constexpr float kE4m3Most = 448.f;
 // the largest is 448 whatever the rounding.  m is 1e-30 at the least, so that a
 // group of zeros has a scale, too; a row that holds a NaN or an infinity has a
 // scale of NaN.
+//
+// Bound by HBM.  A thread keeps its columns' scale and weight in registers for all of
+// its workgroup's rows: read again for every row they come from the caches, but behind
+// the next row's loads, for which a wave then waits (16384 x 2048, bf16, 370 MB: 103 ->
+// 66 us).
 template <typename T, int NT, int VEC, int E, bool GROUPS, bool ONCE>
 __global__ __launch_bounds__(NT) void residual_norm_fp8_kernel(NormFp8Args a)
 {
     using L = Cols<NT, VEC, E>;
+    using Raw = T __attribute__((ext_vector_type(VEC)));
     __shared__ float part[2 * (NT / 64)];
-    float xn[L::K][VEC], yn[L::K][VEC];
+    float xn[L::K][VEC], s[L::K][VEC], w[L::K][VEC];
+    Raw yn[L::K];
     const auto read = [&](long row) {
 #pragma unroll
         for (int k = 0; k < L::K; ++k) {
@@ -501,16 +508,22 @@ __global__ __launch_bounds__(NT) void residual_norm_fp8_kernel(NormFp8Args a)
             if (c >= a.D)
                 continue;
             load<VEC, true, ONCE>(xn[k], a.x + row * a.D + c);
-            if (a.y)
-                load<VEC, true, ONCE>(yn[k], static_cast<const T *>(a.y) + row * a.D + c);
+            if (a.y) {
+                const Raw *const y = reinterpret_cast<const Raw *>(static_cast<const T *>(a.y) + row * a.D + c);
+                yn[k] = ONCE ? __builtin_nontemporal_load(y) : *y;
+            }
         }
     };
-    constexpr bool AHEAD = E <= 2; // else the registers do not hold two rows
-    if (AHEAD)
-        read(blockIdx.x);
+    read(blockIdx.x);
+#pragma unroll
+    for (int k = 0; k < L::K; ++k)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int c = L::col(k) < a.D ? L::col(k) + i : 0;
+            s[k][i] = a.scale ? a.scale[c] : 1.f;
+            w[k][i] = a.weight ? a.weight[c] : 1.f;
+        }
     for (long row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        if (!AHEAD)
-            read(row);
         const long at = row * a.D;
         float x[L::K][VEC], m[GROUPS ? L::K : 1], ss = 0.f;
         m[0] = 0.f;
@@ -524,21 +537,21 @@ __global__ __launch_bounds__(NT) void residual_norm_fp8_kernel(NormFp8Args a)
             float &most = m[GROUPS ? k : 0];
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
+#pragma clang fp contract(off) // x' bit for bit residual_norm's
                 x[k][i] = xn[k][i];
                 if (a.y)
-                    x[k][i] += a.scale ? yn[k][i] * a.scale[c + i] : yn[k][i];
+                    x[k][i] += to_f(yn[k][i]) * s[k][i];
                 ss = fmaf(x[k][i], x[k][i], ss);
             }
             if (a.y)
                 store<VEC, true>(a.x_out + at + c, x[k]);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                if (a.weight)
-                    x[k][i] *= a.weight[c + i];
+                x[k][i] *= w[k][i];
                 most = fmaxf(most, fabsf(x[k][i]));
             }
         }
-        if (AHEAD && row + gridDim.x < a.rows)
+        if (row + gridDim.x < a.rows)
             read(row + gridDim.x);
         ss = group_sum<64>(ss);
         if constexpr (!GROUPS)
@@ -591,8 +604,9 @@ __global__ __launch_bounds__(NT) void residual_norm_fp8_kernel(NormFp8Args a)
 
 template <typename T, int NT, int VEC, int E, bool GROUPS, bool ONCE> hipError_t norm_fp8_o(const NormFp8Args &a, hipStream_t st)
 {
+    constexpr long blocks = kForwardBlocks * 256 / NT; // every wave slot
     hipLaunchKernelGGL((residual_norm_fp8_kernel<T, NT, VEC, E, GROUPS, ONCE>),
-                       dim3(static_cast<unsigned>(a.rows < kForwardBlocks ? a.rows : kForwardBlocks)), dim3(NT), 0, st, a);
+                       dim3(static_cast<unsigned>(a.rows < blocks ? a.rows : blocks)), dim3(NT), 0, st, a);
     return hipGetLastError();
 }
 template <typename T, int NT, int VEC, int E> hipError_t norm_fp8_k(const NormFp8Args &a, hipStream_t st)
@@ -610,16 +624,16 @@ template <typename T, int NT, int VEC, int E> hipError_t norm_fp8_k(const NormFp
 
 template <typename T, int VEC> hipError_t norm_fp8_e(const NormFp8Args &a, hipStream_t st)
 {
-    // as residual_norm_e
+    // eight columns per thread, sixteen in the widest rows
     if (a.D <= 512)
         return norm_fp8_k<T, 64, VEC, 1>(a, st);
     if (a.D <= 2048)
         return norm_fp8_k<T, 256, VEC, 1>(a, st);
     if (a.D <= 4096)
-        return norm_fp8_k<T, 256, VEC, 2>(a, st);
+        return norm_fp8_k<T, 512, VEC, 1>(a, st);
     if (a.D <= 8192)
-        return norm_fp8_k<T, 256, VEC, 4>(a, st);
-    return norm_fp8_k<T, 256, VEC, 8>(a, st);
+        return norm_fp8_k<T, 1024, VEC, 1>(a, st);
+    return norm_fp8_k<T, 1024, VEC, 2>(a, st);
 }
 
 } // namespace
