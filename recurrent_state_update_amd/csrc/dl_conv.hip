@@ -7,7 +7,10 @@
 // A few operations per byte, bound by HBM: a lane walks down a run of tokens with
 // a few channels (one vector load and store a token), the last W - 1 inputs and
 // the weights in registers, and re-reads the W - 1 tokens ahead of its run
-// (backward: behind it).
+// (backward: behind it).  8192 tokens x 4096 channels, four taps, bf16: forward 28.8
+// us, 134 MB at 4.7 TB/s, which is a large copy's rate; backward 49.6 us, 201 MB at
+// 4.1 (its 32 instructions an element keep the vector units 78% busy); 2756 x 12288,
+// six prompts in slices of wider rows, 34.4 us, 4.0 TB/s.
 #include "dl_vec.h"
 
 #include "dl_internal.h"
@@ -402,7 +405,9 @@ template <typename T, int W, int V, bool VEC> __global__ __launch_bounds__(NT) v
         }
 }
 
-// One token each: state row r = [W - 1][C] moves up by one and takes x.
+// One token each: state row r = [W - 1][C] moves up by one and takes x.  64 x 12288,
+// four taps, bf16: 5.7 us for 13 MB, most of it the latency of two loads in a row (the
+// state's row, then what is in it) and the launch.
 template <typename T, int W, int V, bool VEC> __global__ __launch_bounds__(NT) void conv_step_kernel(ConvArgs a)
 {
     // workgroups of a row: `wide`

@@ -612,7 +612,9 @@ template <typename T, int NT, int VEC, int E, bool GROUPS, bool ONCE> hipError_t
 template <typename T, int NT, int VEC, int E> hipError_t norm_fp8_k(const NormFp8Args &a, hipStream_t st)
 {
     if constexpr (VEC > 1) {
-        // past the caches where a pass moves more than the last-level one holds, as residual_norm_t
+        // past the caches where a pass moves more than the last-level one holds, as
+        // residual_norm_t.  us (plain, past the caches) of D = 2048, bf16: 16384 rows 75.5,
+        // 65.8; 12000 49.5, 49.2; 8192 31.6, 35.8; 4096 18.7, 22.4.
         const bool once = a.rows * a.D * static_cast<long>(a.y ? 9 + sizeof(T) : 5) > (256L << 20);
         if (a.group != a.D)
             return once ? norm_fp8_o<T, NT, VEC, E, true, true>(a, st) : norm_fp8_o<T, NT, VEC, E, true, false>(a, st);
@@ -624,7 +626,8 @@ template <typename T, int NT, int VEC, int E> hipError_t norm_fp8_k(const NormFp
 
 template <typename T, int VEC> hipError_t norm_fp8_e(const NormFp8Args &a, hipStream_t st)
 {
-    // eight columns per thread, sixteen in the widest rows
+    // eight columns per thread, sixteen in the widest rows (the registers hold their scale
+    // and weight); few threads in short rows, whose waves then have rows of their own
     if (a.D <= 512)
         return norm_fp8_k<T, 64, VEC, 1>(a, st);
     if (a.D <= 2048)

@@ -98,6 +98,10 @@ __device__ __forceinline__ int swizzle(int n, int t) { return t ^ (n / 2 % 4 * 4
 // saved one ahead of it, sixteen in registers with their decays; then the adjoint
 // goes back over them.  A wave takes four channels at a time, four times: what
 // it adds up of dB and dC over channels stays in registers meanwhile, B and C too.
+//
+// Bound by the vector units, 84% busy at two waves per SIMD: 2 x 2048 x 2048, 16 states,
+// bf16: 121 us (218 MB; at a copy's rate 46).  64 channels: fewer leave more sums of dB
+// and dC to memory (a tile's are 256 bytes a token), more do not fill the GPU.
 template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ? 2 : 1) void ssm_bwd_kernel(SsmArgs a)
 {
     constexpr int XV = 4, XPR = GC / XV;
@@ -385,7 +389,7 @@ template <typename T, int S, bool VEC> __global__ __launch_bounds__(NT, S == 1 ?
 // added, and the time is the loads').  The first `first` workgroups: dA, dD and
 // dt_bias's gradient, columns of [slots][C S + 2 C], sixteen columns a workgroup and
 // every sixteenth row a thread.  The others: dB and dC from the tiles' sums, zero for
-// tokens of no sequence.
+// tokens of no sequence.  7.0 us of 22 MB for 2 x 2048 x 2048.
 template <typename T> __global__ __launch_bounds__(NT) void ssm_sums_kernel(SsmArgs a, int first, int tiles)
 {
     constexpr int U = 8; // loads at a time

@@ -1,10 +1,11 @@
 """The sequence operators beside the decode step, on torch tensors: `scan` (the
 recurrence over whole sequences: prefill and training), `gated_norm` and
-`residual_norm` (the norms behind and before a recurrent block).
+`residual_norm` (the norms behind and before a recurrent block), and
+`residual_norm_fp8` (the latter with its output in 8 bits, for inference).
 
 Argument checks, output and workspace allocation and autograd nodes only: the
 arithmetic is in libdeltalog (dl_scan, dl_gated_norm, dl_residual_norm and
-their backward passes).  All three are differentiable once (in reverse;
+their backward passes).  The first three are differentiable once (in reverse;
 forward-mode derivatives and tracing are refused), asynchronous on the current
 stream (or ``stream``, on which their outputs are then allocated too; the
 inputs have to be ready there, as for torch's own operators) and capturable
