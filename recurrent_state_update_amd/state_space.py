@@ -30,7 +30,7 @@ def _shape(x):
 
 
 def _sequences(lead, cu_seqlens, device):
-    """How many sequences there are, and their offsets."""
+    """How many sequences there are."""
     if cu_seqlens is None:
         N = lead[0] if len(lead) == 2 else 1
     else:
@@ -39,10 +39,10 @@ def _sequences(lead, cu_seqlens, device):
         if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens: want a 1-D int32 GPU tensor of at least two offsets")
         _tensor(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, device)
-        cu_seqlens, N = cu_seqlens.contiguous(), cu_seqlens.numel() - 1
+        N = cu_seqlens.numel() - 1
     if N < 1:
         raise ValueError("want at least one sequence")
-    return N, cu_seqlens
+    return N
 
 
 def _channel_rows(t, lead):
@@ -83,9 +83,8 @@ def _state_rows(rows, T, state, device):
     if rows is None:
         if state.shape[0] < T:
             raise ValueError(f"state: {state.shape[0]} rows for {T} tokens: name their rows")
-        return None
-    _tensor(rows, "rows", torch.int32, (T,), device)
-    return rows.contiguous()
+    else:
+        _tensor(rows, "rows", torch.int32, (T,), device)
 
 
 def _changed(state):
@@ -113,7 +112,7 @@ class _Conv:
         """These tensors, copied where the library cannot read them as they are,
         and their descriptor."""
         x, stride = _channel_rows(x, len(self.lead))
-        weight, bias = _whole(weight), _whole(bias)
+        weight, bias, cu_seqlens = _whole(weight), _whole(bias), _whole(cu_seqlens)
         return (x, weight, bias, cu_seqlens), dl_conv_desc(
             self.dti, self.T, N, self.C, self.W, self.silu, stride, _p(cu_seqlens), x.data_ptr(), weight.data_ptr(),
             _p(bias))
@@ -171,14 +170,14 @@ def short_conv(x, weight, bias=None, initial_state=None, cu_seqlens=None, silu: 
     _plain("short_conv", x, weight, bias, initial_state)
     dev = _gpu(x, "x")
     s = _Conv(x, weight, bias, silu)
-    N, cu = _sequences(s.lead, cu_seqlens, dev)
+    N = _sequences(s.lead, cu_seqlens, dev)
     if initial_state is not None:
         _tensor(initial_state, "initial_state", x.dtype, (N, s.W - 1, s.C), dev)
     with _on(dev, stream):
         initial = _whole(initial_state)
         if _wants_grad(x, weight, bias, initial):
-            return _ConvFn.apply(s, N, cu, x, weight, bias, initial)
-        tensors, desc = s.describe(N, x, weight, bias, cu)
+            return _ConvFn.apply(s, N, cu_seqlens, x, weight, bias, initial)
+        tensors, desc = s.describe(N, x, weight, bias, cu_seqlens)
         return s.forward(desc, x, N, initial)
 
 
@@ -195,11 +194,11 @@ def short_conv_step(x, state, weight, bias=None, rows=None, silu: bool = True, s
         raise ValueError(f"x: want [B,C], got {tuple(x.shape)}")
     s = _Conv(x, weight, bias, silu)
     _in_place(state, "state", x.dtype, (s.W - 1, s.C), dev)
-    rows = _state_rows(rows, s.T, state, dev)
+    _state_rows(rows, s.T, state, dev)
     _no_grad("short_conv_step", x, state, weight, bias)
     with _on(dev, stream):
         tensors, desc = s.describe(1, x, weight, bias, None)
-        y = _like(x)
+        y, rows = _like(x), _whole(rows)
         _check(_lib.dl_short_conv_step(desc, state.data_ptr(), _p(rows), state.shape[0], y.data_ptr(), _current(dev)),
                "dl_short_conv_step")
         _changed(state)
@@ -241,7 +240,7 @@ class _Ssm:
         n = len(self.lead)
         (x, xs), (dt, dts), (z, zs) = (_channel_rows(t, n) for t in (x, dt, z))
         (B, bs), (C, cs) = (_rows(t, n, _MOST_STRIDE) if self.grouped else _channel_rows(t, n) for t in (B, C))
-        A, D, dt_bias = _whole(A), _whole(D), _whole(dt_bias)
+        A, D, dt_bias, cu_seqlens = _whole(A), _whole(D), _whole(dt_bias), _whole(cu_seqlens)
         return (x, dt, A, B, C, D, z, dt_bias, cu_seqlens), dl_ssm_desc(
             self.dti, self.T, N, self.C, self.S, self.G, self.softplus, xs, dts, zs, bs, cs, _p(cu_seqlens),
             x.data_ptr(), dt.data_ptr(), _p(z), B.data_ptr(), C.data_ptr(), A.data_ptr(), _p(D), _p(dt_bias))
@@ -311,14 +310,14 @@ def ssm_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = True
     _plain("ssm_scan", x, dt, A, B, C, D, z, dt_bias, initial_state)
     dev = _gpu(x, "x")
     s = _Ssm(x, dt, A, B, C, D, z, dt_bias, softplus)
-    N, cu = _sequences(s.lead, cu_seqlens, dev)
+    N = _sequences(s.lead, cu_seqlens, dev)
     if initial_state is not None:
         _tensor(initial_state, "initial_state", torch.float32, (N, s.C, s.S), dev)
     with _on(dev, stream):
         initial = _whole(initial_state)
         if _wants_grad(x, dt, A, B, C, D, z, dt_bias, initial):
-            return _SsmFn.apply(s, N, cu, x, dt, A, B, C, D, z, dt_bias, initial)
-        tensors, desc = s.describe(N, x, dt, A, B, C, D, z, dt_bias, cu)
+            return _SsmFn.apply(s, N, cu_seqlens, x, dt, A, B, C, D, z, dt_bias, initial)
+        tensors, desc = s.describe(N, x, dt, A, B, C, D, z, dt_bias, cu_seqlens)
         return s.forward(desc, x, A, N, initial)
 
 
@@ -335,11 +334,11 @@ def ssm_step(x, dt, state, A, B, C, D=None, z=None, dt_bias=None, softplus: bool
         raise ValueError(f"x: want [B,C], got {tuple(x.shape)}")
     s = _Ssm(x, dt, A, B, C, D, z, dt_bias, softplus)
     _in_place(state, "state", torch.float32, (s.C, s.S), dev)
-    rows = _state_rows(rows, s.T, state, dev)
+    _state_rows(rows, s.T, state, dev)
     _no_grad("ssm_step", x, dt, state, A, B, C, D, z, dt_bias)
     with _on(dev, stream):
         tensors, desc = s.describe(1, x, dt, A, B, C, D, z, dt_bias, None)
-        y = _like(x)
+        y, rows = _like(x), _whole(rows)
         _check(_lib.dl_ssm_step(desc, state.data_ptr(), _p(rows), state.shape[0], y.data_ptr(), _current(dev)),
                "dl_ssm_step")
         _changed(state)

@@ -234,3 +234,33 @@ def test_small_states_that_grow():
     refs = [ssm_ref(*x.values(), cu, False, size=s) for s in (False, True)]
     # 128 steps at 4 roundings, their exponents' 128 at 22, the sum of 4 and D's
     check(got, {n: refs[0][n] for n in got}, refs[1], 4 * 128 + 22 * 128 + 8)
+
+
+@needs_gpu
+def test_copies_are_made_on_the_stream_named():
+    """Offsets and rows that have to be copied, on a stream other than the current one,
+    which is busy: the copies wait for nothing there."""
+    import recurrent_state_update_amd as rsu
+    x, _, _, _ = inputs([30, 34], 20, 16, dtype="bf16")
+    v = {n: t.cuda() for n, t in x.items()}
+    off = torch.tensor([[0, 9], [30, 9], [64, 9]], dtype=torch.int32, device="cuda")[:, 0]
+    rows = torch.tensor([[k, 9] for k in range(64)], dtype=torch.int32, device="cuda").flip(0)[:, 0]
+    w = torch.randn(20, 4, device="cuda")
+    cache = torch.randn(64, 3, 20, device="cuda").bfloat16(), torch.randn(64, 20, 16, device="cuda")
+
+    def go(stream, off, rows):
+        with torch.no_grad():
+            a, b = (t.clone() for t in cache)
+            torch.cuda.synchronize()
+            if stream:
+                torch.cuda._sleep(50_000_000)
+            outs = [*rsu.short_conv(v["x"], w, cu_seqlens=off, stream=stream),
+                    *rsu.ssm_scan(*(v[n] for n in NAMES[:-1]), cu_seqlens=off, stream=stream),
+                    rsu.short_conv_step(v["x"], a, w, rows=rows, stream=stream),
+                    rsu.ssm_step(v["x"], v["dt"], b, *(v[n] for n in NAMES[2:-1]), rows=rows, stream=stream), a, b]
+            torch.cuda.synchronize()
+        return outs
+    want = go(None, off.contiguous(), rows.contiguous())
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    assert all(torch.equal(p, q) for p, q in zip(go(s, off, rows), want))

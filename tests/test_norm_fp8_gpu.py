@@ -63,6 +63,15 @@ def test_against_64_bits(lead, D, group, dtype, form):
 
 
 @needs_gpu
+@pytest.mark.parametrize("rows,D,group", [(8300, 130, None), (8300, 256, 128), (2200, 641, None), (2200, 640, 128),
+                                          (1100, 2176, 128), (1100, 2051, None), (600, 4224, 128), (600, 8200, None)])
+def test_many_rows(rows, D, group):
+    """More rows than workgroups: each takes several."""
+    v = inputs((rows,), D, "bf16", seed=D)
+    verify(v, gpu(v, group), group)
+
+
+@needs_gpu
 def test_agrees_with_residual_norm():
     """x' is bit for bit residual_norm's, and h its h to e4m3's rounding."""
     import recurrent_state_update_amd as rsu
