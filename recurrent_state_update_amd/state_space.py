@@ -23,10 +23,10 @@ def _shape(x):
     """The leading dimensions of x [T,C] or [N,T,C], its channels and rows."""
     if x.dim() not in (2, 3):
         raise ValueError(f"x: want [T,C] or [N,T,C], got {tuple(x.shape)}")
-    lead, C = tuple(x.shape[:-1]), x.shape[-1]
+    *lead, C = x.shape
     if C < 1:
         raise ValueError("x: want at least one channel")
-    return lead, C, _count(x.numel() // C)
+    return tuple(lead), C, _count(x.numel() // C)
 
 
 def _sequences(lead, cu_seqlens, device):
@@ -211,36 +211,43 @@ class _Ssm:
     """The checked arguments of one selective scan."""
 
     def __init__(self, x, dt, A, B, C, D, z, dt_bias, softplus):
-        self.device, self.dtype = x.device, x.dtype
-        self.lead, self.C, self.T = _shape(x)
-        dev, ch = self.device, self.C
-        self.dti = _dtype_id(x.dtype)
-        _tensor(dt, "dt", x.dtype, x.shape, dev)
+        dev, dtype, shape = x.device, x.dtype, x.shape
+        self.device, self.dtype = dev, dtype
+        lead, ch, self.T = _shape(x)
+        self.lead, self.C = lead, ch
+        self.dti = _dtype_id(dtype)
+        _tensor(dt, "dt", dtype, shape, dev)
         if z is not None:
-            _tensor(z, "z", x.dtype, x.shape, dev)
+            _tensor(z, "z", dtype, shape, dev)
         if not isinstance(A, torch.Tensor) or A.dim() != 2 or not 1 <= A.shape[1] <= _MOST_STATES:
             raise ValueError(f"A: want fp32 [C,N] with 1 to {_MOST_STATES} states")
         self.S = A.shape[1]
         _tensor(A, "A", torch.float32, (ch, self.S), dev)
-        self.grouped = isinstance(B, torch.Tensor) and B.dim() == len(self.lead) + 2
+        self.grouped = isinstance(B, torch.Tensor) and B.dim() == len(lead) + 2
         self.G = B.shape[-2] if self.grouped else 1
-        self.bc = (*self.lead, self.G, self.S) if self.grouped else (*self.lead, self.S)
-        _tensor(B, "B", x.dtype, self.bc, dev)
-        _tensor(C, "C", x.dtype, self.bc, dev)
+        bc = (*lead, self.G, self.S) if self.grouped else (*lead, self.S)
+        _tensor(B, "B", dtype, bc, dev)
+        _tensor(C, "C", dtype, bc, dev)
         if self.G < 1 or ch % self.G != 0:
             raise ValueError(f"B: {self.G} groups for {ch} channels")
-        for t, name in ((D, "D"), (dt_bias, "dt_bias")):
-            if t is not None:
-                _tensor(t, name, torch.float32, (ch,), dev)
+        if D is not None:
+            _tensor(D, "D", torch.float32, (ch,), dev)
+        if dt_bias is not None:
+            _tensor(dt_bias, "dt_bias", torch.float32, (ch,), dev)
         self.softplus = int(bool(softplus))
 
     def describe(self, N, x, dt, A, B, C, D, z, dt_bias, cu_seqlens):
         """These tensors, copied where the library cannot read them as they are,
         and their descriptor."""
         n = len(self.lead)
-        (x, xs), (dt, dts), (z, zs) = (_channel_rows(t, n) for t in (x, dt, z))
-        (B, bs), (C, cs) = (_rows(t, n, _MOST_STRIDE) if self.grouped else _channel_rows(t, n) for t in (B, C))
-        A, D, dt_bias, cu_seqlens = _whole(A), _whole(D), _whole(dt_bias), _whole(cu_seqlens)
+        x, xs = _channel_rows(x, n)
+        dt, dts = _channel_rows(dt, n)
+        z, zs = _channel_rows(z, n)
+        if self.grouped:
+            (B, bs), (C, cs) = _rows(B, n, _MOST_STRIDE), _rows(C, n, _MOST_STRIDE)
+        else:
+            (B, bs), (C, cs) = _channel_rows(B, n), _channel_rows(C, n)
+        A, D, dt_bias, cu_seqlens = A.contiguous(), _whole(D), _whole(dt_bias), _whole(cu_seqlens)
         return (x, dt, A, B, C, D, z, dt_bias, cu_seqlens), dl_ssm_desc(
             self.dti, self.T, N, self.C, self.S, self.G, self.softplus, xs, dts, zs, bs, cs, _p(cu_seqlens),
             x.data_ptr(), dt.data_ptr(), _p(z), B.data_ptr(), C.data_ptr(), A.data_ptr(), _p(D), _p(dt_bias))
