@@ -101,11 +101,11 @@ def _none(t, name, why):
         raise ValueError(f"{name}: {why} takes none")
 
 
-def _count(rows):
-    """The library counts rows in an int."""
-    if rows >= 1 << 31:
-        raise ValueError(f"{rows} rows: want fewer than 2^31")
-    return rows
+def _count(n, what="rows"):
+    """The library counts in ints, and ctypes would pass a number's lowest bits."""
+    if n >= 1 << 31:
+        raise ValueError(f"{n} {what}: want fewer than 2^31")
+    return n
 
 
 def _state(t):

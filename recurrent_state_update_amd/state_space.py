@@ -26,7 +26,7 @@ def _shape(x):
     *lead, C = x.shape
     if C < 1:
         raise ValueError("x: want at least one channel")
-    return tuple(lead), C, _count(x.numel() // C)
+    return tuple(lead), _count(C, "channels"), _count(x.numel() // C)
 
 
 def _sequences(lead, cu_seqlens, device):
@@ -42,7 +42,7 @@ def _sequences(lead, cu_seqlens, device):
         N = cu_seqlens.numel() - 1
     if N < 1:
         raise ValueError("want at least one sequence")
-    return N
+    return _count(N, "sequences")
 
 
 def _channel_rows(t, lead):
@@ -74,7 +74,7 @@ def _in_place(state, name, dtype, tail, device):
     """A cache of states [rows,*tail] that a step moves on."""
     if not isinstance(state, torch.Tensor) or state.dim() != 1 + len(tail):
         raise ValueError(f"{name}: want a GPU tensor [rows,{','.join(map(str, tail))}]")
-    _tensor(state, name, dtype, (state.shape[0], *tail), device)
+    _tensor(state, name, dtype, (_count(state.shape[0], "rows of states"), *tail), device)
     if not state.is_contiguous():
         raise ValueError(f"{name}: want a contiguous tensor, since it is updated in place")
 
