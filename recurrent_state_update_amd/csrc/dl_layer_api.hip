@@ -361,7 +361,7 @@ dl_status dl_short_conv_step(const dl_conv_desc *d, void *state, const int *stat
     const size_t es = elem(d->dtype), row = static_cast<size_t>(d->channels) * es;
     if (!aligned(state, es) || !aligned(y, es) || !aligned(state_rows, 4))
         return DL_E_ALIGN;
-    const Span w[2] = {{y, d->tokens * row}, {state, n_state_rows * (d->taps - 1) * row}};
+    const Span w[2] = {{y, d->tokens * row}, {state, static_cast<size_t>(n_state_rows) * (d->taps - 1) * row}};
     const Span r[4] = {in[0], in[1], in[2], {state_rows, static_cast<size_t>(d->tokens) * 4}};
     if (clash(w, r))
         return DL_E_INVALID;
