@@ -482,13 +482,14 @@ template <int G> __device__ __forceinline__ float group_max(float x)
 }
 
 constexpr float kE4m3Most = 448.f;
+constexpr float kSmallest = 0x1p-126f; // normal number
 
 // As residual_norm_kernel, with h = rms(x') w as e4m3 values times a scale, of a
 // row or (GROUPS) of 128 columns.  With m = max |x' w| and r the row's 1 / rms, the
 // scale is r m / 448 and the value x' w (448 / m): one pass, since r cancels, and
-// the largest is 448 whatever the rounding.  m is 1e-30 at the least, so that a
-// group of zeros has a scale, too; a row that holds a NaN or an infinity has a
-// scale of NaN.
+// the largest is 448 whatever the rounding.  m is 1e-30 at the least, and the scale of
+// what is all zeros the smallest normal number at the least: it has one, too, that can be
+// divided by.  A row that holds a NaN has scales of NaN, one with an infinity where that is.
 //
 // Bound by HBM.  A thread keeps its columns' scale and weight in registers for all of
 // its workgroup's rows: read again for every row they come from the caches, but behind
@@ -581,7 +582,11 @@ __global__ __launch_bounds__(NT) void residual_norm_fp8_kernel(NormFp8Args a)
             const int c = L::col(k);
             if (c >= a.D)
                 continue;
-            const float most = fmaxf(m[GROUPS ? k : 0], 1e-30f), scale = r * (most / kE4m3Most);
+            const float most = fmaxf(m[GROUPS ? k : 0], 1e-30f);
+            float scale = r * (most / kE4m3Most);
+            // where all are zero r can take it to zero (a row's rms beyond 3e12)
+            if (m[GROUPS ? k : 0] == 0.f && scale < kSmallest)
+                scale = kSmallest;
             // 0 r: NaN where the row's norm is none
             const float by = kE4m3Most / most + 0.f * r;
             if constexpr (VEC == 4) {
