@@ -67,7 +67,7 @@ template <int T0> __device__ __forceinline__ void fma_bcast(float *acc, float x,
         "v_fmac_f32_dpp %6, %8, %15 row_newbcast:%c23 row_mask:0xf bank_mask:0xf\n"
         "v_fmac_f32_dpp %7, %8, %16 row_newbcast:%c24 row_mask:0xf bank_mask:0xf\n"
         "s_nop 1"
-        : "+v"(acc[0]), "+v"(acc[1]), "+v"(acc[2]), "+v"(acc[3]), "+v"(acc[4]), "+v"(acc[5]), "+v"(acc[6]), "+v"(acc[7])
+        : "+&v"(acc[0]), "+&v"(acc[1]), "+&v"(acc[2]), "+&v"(acc[3]), "+&v"(acc[4]), "+&v"(acc[5]), "+&v"(acc[6]), "+&v"(acc[7])
         : "v"(x), "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(v[4]), "v"(v[5]), "v"(v[6]), "v"(v[7]), "n"(T0),
           "n"(T0 + 1), "n"(T0 + 2), "n"(T0 + 3), "n"(T0 + 4), "n"(T0 + 5), "n"(T0 + 6), "n"(T0 + 7));
 }
@@ -84,7 +84,7 @@ template <int T0> __device__ __forceinline__ void fma_bcast_sum(float &even, flo
         "v_fmac_f32_dpp %0, %2, %9 row_newbcast:%c17 row_mask:0xf bank_mask:0xf\n"
         "v_fmac_f32_dpp %1, %2, %10 row_newbcast:%c18 row_mask:0xf bank_mask:0xf\n"
         "s_nop 1"
-        : "+v"(even), "+v"(odd)
+        : "+&v"(even), "+&v"(odd)
         : "v"(x), "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(v[4]), "v"(v[5]), "v"(v[6]), "v"(v[7]), "n"(T0),
           "n"(T0 + 1), "n"(T0 + 2), "n"(T0 + 3), "n"(T0 + 4), "n"(T0 + 5), "n"(T0 + 6), "n"(T0 + 7));
 }
