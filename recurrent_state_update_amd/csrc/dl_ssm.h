@@ -121,16 +121,16 @@ __device__ __forceinline__ float row_sum(float x)
 
 // softplus(r) = max(r, 0) + log1p(e), e = e^{-|r|}: the logarithm as
 // 2 artanh(s), s = e / (2 + e) <= 1/3, so that small results keep all their bits.
-// artanh(s) / s is a polynomial in s^2, the best of degree 4 on [0, 1/9] (off by
-// 2^-27.9 at the most).
+// artanh(s) / s is a polynomial in s^2, the best of degree 4 on [0, 1/9] with a constant
+// term of 1 (off by 2^-27.7 at the most).
 __device__ __forceinline__ float softplus(float r, float &e)
 {
     e = __builtin_amdgcn_exp2f(-fabsf(r) * kLog2e);
     const float s = e * __builtin_amdgcn_rcpf(2.f + e), w = s * s;
-    float p = 0.140891671f;
-    p = fmaf(p, w, 0.139803007f);
-    p = fmaf(p, w, 0.200124547f);
-    p = fmaf(p, w, 0.333331585f);
+    float p = 0.140032008f;
+    p = fmaf(p, w, 0.140015468f);
+    p = fmaf(p, w, 0.200107172f);
+    p = fmaf(p, w, 0.333332092f);
     p = fmaf(p, w, 1.f);
     // (r > 0 ? r : 0 would lose a NaN)
     return fmaf(2.f * s, p, r < 0.f ? 0.f : r);
