@@ -8,9 +8,11 @@
 // a few channels (one vector load and store a token), the last W - 1 inputs and
 // the weights in registers, and re-reads the W - 1 tokens ahead of its run
 // (backward: behind it).  8192 tokens x 4096 channels, four taps, bf16: forward 28.8
-// us, 134 MB at 4.7 TB/s, which is a large copy's rate; backward 49.6 us, 201 MB at
-// 4.1 (its 32 instructions an element keep the vector units 78% busy); 2756 x 12288,
-// six prompts in slices of wider rows, 34.4 us, 4.0 TB/s.
+// us, 134 MB at 4.7 TB/s (a copy of as much from memory: 5.1); backward 49.8 us, 201 MB at
+// 4.0 (its 32 instructions an element keep the vector units 78% busy); 2756 x 12288,
+// six prompts in slices of wider rows, 34.6 us, 4.0 TB/s.  fp32, 8192 x 4096: 48.9 and
+// 81.9 us, 5.5 and 4.9 TB/s.  Rows that are not whole vectors take four-byte accesses:
+// 777 x 1531, three taps, fp32: 11.0 and 18.6 us for 9.5 and 14.3 MB.
 #include "dl_vec.h"
 
 #include "dl_internal.h"

@@ -132,7 +132,9 @@ int tiles_of(const dl_ssm_desc *d, int tile)
 // (once for what its segment adds to the state), which pays where uncut ones leave
 // most of the GPU idle.
 //
-// Forward: where the sequences' mean length says so.  us, 16 states, bf16, by segment
+// Forward: where the sequences' mean length says so, which one long sequence among short
+// ones does not reach: 4096 tokens of 512 channels take 33 us alone, among fifteen
+// sequences of 17 tokens 113, among 255 of them 182.  us, 16 states, bf16, by segment
 // (uncut first):
 //                     uncut   64   128   256   512  1024
 //   512 x 64 channels  15.4  10.6  12.9  18.0

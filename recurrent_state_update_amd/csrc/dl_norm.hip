@@ -137,8 +137,8 @@ __global__ __launch_bounds__(256) void gated_norm_bwd_kernel(GatedNormArgs a)
 // out[j] = the sum over the blocks' rows of partial [blocks][n] (blockIdx.y:
 // the second array, of n1 columns).  A workgroup takes 16 columns; 16 threads per column
 // take every 16th row, eight loads at a time.  In 64 bits: the norms have up to 1024
-// rows, the convolution one for every run of tokens (16384 for 2^20 tokens of 16
-// channels), and the time is the loads'.
+// rows, the convolution one for every run of tokens, and the time is the loads', of few
+// columns and many rows their latency (128 rows x 20480 columns 4.4 us, 16384 x 80 48).
 __global__ __launch_bounds__(256) void column_sum_kernel(const float *partial, int blocks, int n, float *out0,
                                                          int n1, float *out1)
 {

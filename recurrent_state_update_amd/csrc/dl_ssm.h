@@ -18,13 +18,14 @@
 // A diagonal recurrence shares nothing between channels that a matrix
 // instruction could use: each (token, channel, state) takes an exponential (two
 // issue slots on gfx950) and four to fourteen other operations, and the vector
-// units are the bound, ahead of memory.  So the layout spends no instruction on
+// units are the bound, ahead of memory.  So the layout spends few instructions on
 // moving data: the sixteen lanes of a row hold sixteen states of one channel
 // (states n, n + 16, ... where there are more), and lane j of the row loads what
 // belongs to token j of a block of sixteen (x, delta, the gate: formed once per
 // token and channel).  The recurrence reads them as row broadcasts, which are a
-// modifier of the multiplication that uses them, and sums over a row end with
-// token j's in lane j.
+// modifier of the multiplication that uses them (backward, dy's are instructions of
+// their own: 64 of the 1536 vector instructions of a block of tokens), and sums over a
+// row end with token j's in lane j.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -44,9 +44,11 @@ template <int S, int TT> struct Shared {
 // one wave of states per SIMD, has two to issue from.
 //
 // Bound by the vector units: 4096 tokens x 4096 channels, 16 states, bf16: 102 us, of
-// which they are busy 85% (an exponential, three products and sums and a sixteenth of
-// the sums over states for each state and token); its 134 MB at a copy's rate would take
-// 29.  With the states of every block saved, 2 x 2048 x 2048: 63 us.
+// which they are busy 85%.  Of a stage's 714 issue slots per wave 516 are an exponential
+// (two), the products for its exponent, the input and C, the recurrence and a sixteenth
+// of the sums over states for each state and token; the others load, convert and store,
+// and form softplus and gate.  A copy of its 134 MB takes 26.  With the states of every
+// block saved, 2 x 2048 x 2048: 63 us.
 template <typename T, int S, int TT, bool VEC, bool SAVE> __global__ __launch_bounds__(NT, 2) void ssm_kernel(SsmArgs a)
 {
     constexpr int NB = TT / TB;
@@ -281,7 +283,7 @@ constexpr int STEP = 256;
 // Four states per lane, L = 1 ... 16 lanes (a power of two) per channel; the
 // state's 8 bytes per element are all of the traffic that counts.  VEC: its rows
 // are whole vectors.  64 requests x 4096 channels x 16 states: 9.0 us for 36 MB, 4.0
-// TB/s (a copy of as much takes 7.7).
+// TB/s (a copy of as much takes 7.6 from memory, 4.9 from the caches).
 template <typename T, int L, bool VEC> __global__ __launch_bounds__(STEP) void ssm_step_kernel(SsmArgs a)
 {
     // workgroups of a row: `wide`
